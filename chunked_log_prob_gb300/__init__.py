@@ -29,3 +29,17 @@ from ._binding import (  # noqa: F401
     make_shape,
     status_string,
 )
+from ._norm_ckpt import (  # noqa: F401
+    Checkpoint8,
+    NormBackward,
+    NormForward,
+    alloc_ckpt,
+    grpo_ckpt_pack,
+    grpo_ckpt_size,
+    grpo_ckpt_unpack,
+    grpo_ckpt_wgrad,
+    grpo_ckpt_wgrad_workspace_size,
+    grpo_norm_bwd,
+    grpo_norm_fwd,
+    grpo_norm_workspace_size,
+)

@@ -52,6 +52,16 @@ class GrpoPlanInfo(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_uint64)]
 
 
+class GrpoNormDesc(ctypes.Structure):
+    _fields_ = [("n_tokens", ctypes.c_int64), ("hidden", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32),
+                ("kind", ctypes.c_int32), ("eps", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("x_stride", ctypes.c_int64), ("residual_stride", ctypes.c_int64),
+                ("y_stride", ctypes.c_int64), ("z_stride", ctypes.c_int64),
+                ("dy_stride", ctypes.c_int64), ("dres_stride", ctypes.c_int64),
+                ("dx_stride", ctypes.c_int64)]
+
+
 class GrpoError(RuntimeError):
     def __init__(self, code: int, where: str):
         self.code = code
@@ -91,6 +101,21 @@ def _load():
     lib.grpo_launch_timing_enable.restype = ctypes.c_int
     lib.grpo_launch_timing_read.argtypes = [P(GrpoKernelTime), ctypes.c_int, P(ctypes.c_int)]
     lib.grpo_launch_timing_read.restype = ctypes.c_int
+    i32, i64 = ctypes.c_int32, ctypes.c_int64
+    desc = P(GrpoNormDesc)
+    for name, args in {
+        "grpo_norm_fwd": [vp] * 10 + [desc, vp],
+        "grpo_norm_workspace_size": [desc, P(sz)],
+        "grpo_norm_bwd": [vp] * 13 + [desc, vp, sz, vp],
+        "grpo_ckpt_size": [i64, i32, P(sz)],
+        "grpo_ckpt_layout": [i64, i32, P(i64), P(i64), P(i64)],
+        "grpo_ckpt_pack": [vp, vp, vp, i64, i32, i32, i64, vp],
+        "grpo_ckpt_unpack": [vp, vp, i64, i32, i32, i64, vp],
+        "grpo_ckpt_wgrad_workspace_size": [i64, i32, i32, P(sz)],
+        "grpo_ckpt_wgrad": [vp, vp, vp, vp, i64, i32, i32, i64, vp, sz, vp],
+    }.items():
+        fn = getattr(lib, name)
+        fn.argtypes, fn.restype = args, ctypes.c_int
     lib.grpo_status_string.argtypes = [ctypes.c_int]
     lib.grpo_status_string.restype = ctypes.c_char_p
     return lib
@@ -101,7 +126,10 @@ lib = _load()
 EXPORTED = ("grpo_default_params", "grpo_workspace_size", "grpo_logp_fwd",
             "grpo_loss_fwd_bwd", "grpo_get_plan", "grpo_read_device_status",
             "grpo_logp_fwd_noalloc", "grpo_selftest_bounded_wait", "grpo_launch_timing_enable",
-            "grpo_launch_timing_read", "grpo_status_string")
+            "grpo_launch_timing_read", "grpo_status_string",
+            "grpo_norm_fwd", "grpo_norm_workspace_size", "grpo_norm_bwd", "grpo_ckpt_size",
+            "grpo_ckpt_layout", "grpo_ckpt_pack", "grpo_ckpt_unpack",
+            "grpo_ckpt_wgrad_workspace_size", "grpo_ckpt_wgrad")
 
 FLAG_STORED_LOGITS = 1
 FLAG_SINGLE_CTA = 2

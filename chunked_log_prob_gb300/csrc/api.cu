@@ -53,14 +53,6 @@ static_assert(kOffPartials + kMaxFinalizeBlocks * sizeof(double) <= kHeaderBytes
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-// An NVTX range around one ABI call (host side: it brackets the enqueueing of
-// the call's launches), so that profilers can attribute the kernels to it.
-struct NvtxRange {
-  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-  NvtxRange(const NvtxRange&) = delete;
-  NvtxRange& operator=(const NvtxRange&) = delete;
-};
 long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
 
 // D columns per dH unit, in units of 256: the pair kernel covers 512 (two
@@ -1641,6 +1633,11 @@ thread_local TimingState t_timing;
 
 bool launch_timing_on() { return t_timing.on; }
 
+int setup_device(int* sms) { return device_setup(sms); }
+
+CallRange::CallRange(const char* name) { nvtxRangePushA(name); }
+CallRange::~CallRange() { nvtxRangePop(); }
+
 void LaunchTimer::begin(const char* name, cudaStream_t stream) {
   TimingState& st = t_timing;
   if (st.pending.size() >= kMaxTimedLaunches) return;
@@ -1721,7 +1718,7 @@ int grpo_workspace_size(const grpo_shape* shape, const grpo_params* params, size
 int grpo_logp_fwd(const void* hidden, const void* W, const int32_t* ids, float* logp,
                   float* lse_or_null, const grpo_shape* shape, const grpo_params* params,
                   void* workspace, size_t workspace_bytes, void* stream) {
-  const NvtxRange range("grpo_logp_fwd");
+  const CallRange range("grpo_logp_fwd");
   int r = check_shape(shape, false);
   if (r != GRPO_OK) return r;
   if ((r = check_params(params)) != GRPO_OK) return r;
@@ -1767,7 +1764,7 @@ int grpo_loss_fwd_bwd(const void* hidden, const void* W, const int32_t* ids,
                       const float* adv, float* loss, float* logp_or_null, void* dH,
                       float* dW_or_null, const grpo_shape* shape, const grpo_params* params,
                       void* workspace, size_t workspace_bytes, void* stream) {
-  const NvtxRange range("grpo_loss_fwd_bwd");
+  const CallRange range("grpo_loss_fwd_bwd");
   int r = check_shape(shape, true);
   if (r != GRPO_OK) return r;
   if ((r = check_params(params)) != GRPO_OK) return r;
@@ -2051,7 +2048,7 @@ int noalloc_scratch(void** out) {
 extern "C" int grpo_logp_fwd_noalloc(const void* hidden, const void* W, const int32_t* ids,
                                      float* logp, float* lse_or_null, const grpo_shape* shape,
                                      void* stream) {
-  const NvtxRange range("grpo_logp_fwd_noalloc");
+  const CallRange range("grpo_logp_fwd_noalloc");
   int r = check_shape(shape, false);
   if (r != GRPO_OK) return r;
   if (shape->n_tokens > GRPO_NOALLOC_MAX_TOKENS) return GRPO_ERR_UNSUPPORTED_SHAPE;

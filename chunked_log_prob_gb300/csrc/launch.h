@@ -88,6 +88,20 @@ struct FinishArgs {
   float* loss_out;
 };
 
+// Checks the current device once, opts its kernels in to their shared memory
+// and gives its SM count; GRPO_OK or a negative status. Defined in api.cu.
+int setup_device(int* sms);
+
+// An NVTX range around one ABI call (host side: it brackets the enqueueing of
+// the call's launches), so that profilers can attribute the kernels to it.
+class CallRange {
+ public:
+  explicit CallRange(const char* name);
+  ~CallRange();
+  CallRange(const CallRange&) = delete;
+  CallRange& operator=(const CallRange&) = delete;
+};
+
 constexpr int kGformThreads = 256;
 constexpr int kFinalizeThreads = 256;
 constexpr int kMaxFinalizeBlocks = 1024;

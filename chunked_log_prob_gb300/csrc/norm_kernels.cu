@@ -1,0 +1,695 @@
+// Layer norm and RMS norm, forward and backward, with the residual add, the
+// row mask and the 8-bit checkpoint of the normed stream fused in.
+//
+//   z = round(x + r);  mu = mean z (layer), 0 (rms);
+//   rstd = (mean (z - mu)^2 + eps)^-1/2;  y = (z - mu) rstd w + b
+//   h = (z - mu) rstd, u = dy w:
+//   dx = rstd (u - mean u - h mean(u h)) + dres   (rms: without mean u)
+//   dw = sum_t dy h, db = sum_t dy
+//
+// Memory bound: about 10 operations per value against 4 to 9 bytes. A row is
+// read once and held in registers (up to 8192 columns); statistics are fp32.
+#include <algorithm>
+#include <atomic>
+
+#include "launch.h"
+#include "norm.h"
+#include "row_ops.cuh"
+
+namespace grpo {
+
+namespace {
+
+constexpr int kRowThreads = 256;  // threads of a CTA whose rows are short
+
+__device__ __forceinline__ bool row_live(const uint8_t* mask, long long row, long long n) {
+  return row < n && (mask == nullptr || mask[row] != 0);
+}
+
+// Mean and centred sum of squares of a row. Layer norm: each warp centres its
+// values on their own mean, then the warps' sums are joined exactly as if one
+// had centred on the row's (no difference of large squares). `cnt`: valid
+// values of this warp, shared by all warps in cnt_sh.
+template <int CH, bool VEC>
+__device__ __forceinline__ float2 row_moments(const float (&v)[CH][8], int kind, int t, int tpr,
+                                              int d, int bar, float2* sh, const float* cnt_sh,
+                                              int& phase) {
+  float s = 0.f;
+  if (kind == GRPO_NORM_RMS) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += v[c][j] * v[c][j];
+    return make_float2(0.f, row_sum2(make_float2(s, 0.f), t, tpr, bar, sh, phase).x);
+  }
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s += v[c][j];
+  s = warp_sum(s);
+  const int warp = t >> 5, lane = t & 31;
+  const float cnt = cnt_sh[warp];
+  const float mw = cnt > 0.f ? s / cnt : 0.f;
+  float m2 = 0.f;
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float e = v[c][j] - mw;
+      if (chunk_col<VEC>(c, j, t, tpr) < d) m2 += e * e;
+    }
+  m2 = warp_sum(m2);
+  if (tpr == 32) return make_float2(mw, m2);
+  float2* p = sh + phase * 32;
+  phase ^= 1;
+  if (lane == 0) p[warp] = make_float2(s, m2);
+  named_barrier(bar, tpr);
+  const bool in = lane < (tpr >> 5);
+  const float2 o = in ? p[lane] : make_float2(0.f, 0.f);
+  const float n = in ? cnt_sh[lane] : 0.f;
+  const float mean = warp_sum(o.x) / static_cast<float>(d);
+  const float e = n > 0.f ? o.x / n - mean : 0.f;
+  return make_float2(mean, warp_sum(o.y + n * e * e));
+}
+
+// Valid columns of each warp of a row into cnt_sh; followed by a barrier.
+template <int CH, bool VEC>
+__device__ __forceinline__ void count_columns(int t, int tpr, int d, float* cnt_sh) {
+  float n = 0.f;
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) n += chunk_col<VEC>(c, j, t, tpr) < d ? 1.f : 0.f;
+  n = warp_sum(n);
+  if ((t & 31) == 0) cnt_sh[t >> 5] = n;
+}
+
+// blockDim = (tpr, rows of the CTA). The next row's loads are issued before
+// this row's sums, so that they are in flight during its barrier and stores.
+template <typename T, bool VEC, int CH>
+__global__ void __launch_bounds__(512) norm_fwd_kernel(const NormFwdArgs a) {
+  __shared__ float2 red[8][2 * 32];
+  __shared__ float cnt_all[8][32];
+  const int t = threadIdx.x, tpr = blockDim.x, g = threadIdx.y, d = a.d;
+  int phase = 0;
+  float w[CH][8], b[CH][8];
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int col = chunk_col<VEC>(c, j, t, tpr);
+      w[c][j] = a.weight != nullptr && col < d ? load_param(a.weight, a.wtype, col) : 1.f;
+      b[c][j] = a.bias != nullptr && col < d ? load_param(a.bias, a.wtype, col) : 0.f;
+    }
+  count_columns<CH, VEC>(t, tpr, d, cnt_all[g]);
+  __syncthreads();
+
+  const T* x = static_cast<const T*>(a.x);
+  const T* res = static_cast<const T*>(a.res);
+  T* y = static_cast<T*>(a.y);
+  T* z = static_cast<T*>(a.z);
+  const long long step = static_cast<long long>(gridDim.x) * blockDim.y;
+  long long row = static_cast<long long>(blockIdx.x) * blockDim.y + g;
+  bool live = row_live(a.mask, row, a.n);
+  bool live1 = row_live(a.mask, row + step, a.n);
+  Raw8<T> rx[CH], rr[CH];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    if (live) rx[c] = load_chunk<T, VEC>(x + row * a.ldx, c, t, tpr, d);
+    if (live && res != nullptr) rr[c] = load_chunk<T, VEC>(res + row * a.ldr, c, t, tpr, d);
+  }
+  for (; row < a.n; row += step) {
+    const bool live2 = row_live(a.mask, row + 2 * step, a.n);
+    const long long next = row + step;
+    float v[CH][8];
+    if (live) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        widen(rx[c], v[c]);
+        if (res != nullptr) {
+          float r[8];
+          widen(rr[c], r);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[c][j] += r[j];
+          // The stream holds z rounded; the norm is taken of what it holds.
+          const Raw8<T> o = narrow<T>(v[c]);
+          if (z != nullptr) store_chunk<T, VEC>(z + row * a.ldz, o, c, t, tpr, d);
+          widen(o, v[c]);
+        }
+      }
+    }
+    if (live1) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        rx[c] = load_chunk<T, VEC>(x + next * a.ldx, c, t, tpr, d);
+        if (res != nullptr) rr[c] = load_chunk<T, VEC>(res + next * a.ldr, c, t, tpr, d);
+      }
+    }
+    float mean = 0.f, rstd = 0.f;
+    if (live) {
+      const float2 m = row_moments<CH, VEC>(v, a.kind, t, tpr, d, g + 1, red[g], cnt_all[g], phase);
+      mean = m.x;
+      rstd = 1.f / sqrtf(m.y / static_cast<float>(d) + a.eps);
+    } else {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[c][j] = 0.f;
+        if (z != nullptr && res != nullptr)
+          store_chunk<T, VEC>(z + row * a.ldz, narrow<T>(v[c]), c, t, tpr, d);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      if (a.ck.q != nullptr)
+        ckpt_store_chunk<T, VEC>(v[c], a.ck.q + row * a.ck.ldq, a.ck.ex + row * a.ck.lde, c, t, tpr,
+                                 d);
+      if (live) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[c][j] = (v[c][j] - mean) * rstd * w[c][j] + b[c][j];
+      }
+      store_chunk<T, VEC>(y + row * a.ldy, narrow<T>(v[c]), c, t, tpr, d);
+    }
+    if (t == 0) {
+      if (a.mean != nullptr) a.mean[row] = mean;
+      if (a.rstd != nullptr) a.rstd[row] = rstd;
+    }
+    live = live1;
+    live1 = live2;
+  }
+}
+
+// Rows beyond kNormRegisterRow columns: the CTA walks over the row three times
+// (sum, centred squares, output); the second and third walk find it in L2. A
+// thread rereads only what it stored itself, so outputs may lie on the inputs.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(512) norm_fwd_long_kernel(const NormFwdArgs a) {
+  __shared__ float2 red[2 * 32];
+  const int t = threadIdx.x, tpr = blockDim.x, d = a.d;
+  const int chunks = (d + 8 * tpr - 1) / (8 * tpr);
+  int phase = 0;
+  for (long long row = blockIdx.x; row < a.n; row += gridDim.x) {
+    const bool live = row_live(a.mask, row, a.n);
+    const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+    const T* res = a.res != nullptr ? static_cast<const T*>(a.res) + row * a.ldr : nullptr;
+    T* z = a.z != nullptr && res != nullptr ? static_cast<T*>(a.z) + row * a.ldz : nullptr;
+    T* y = static_cast<T*>(a.y) + row * a.ldy;
+    const auto stream = [&](int c, float(&v)[8]) {
+      if (!live) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.f;
+        return;
+      }
+      widen(load_chunk<T, VEC>(x, c, t, tpr, d), v);
+      if (res != nullptr) {
+        float r[8];
+        widen(load_chunk<T, VEC>(res, c, t, tpr, d), r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += r[j];
+        widen(narrow<T>(v), v);
+      }
+    };
+    float mean = 0.f, rstd = 0.f;
+    if (live) {
+      float v[8];
+      if (a.kind != GRPO_NORM_RMS) {
+        float s = 0.f;
+        for (int c = 0; c < chunks; ++c) {
+          stream(c, v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) s += v[j];
+        }
+        mean = row_sum2(make_float2(s, 0.f), t, tpr, 1, red, phase).x / static_cast<float>(d);
+      }
+      float m2 = 0.f;
+      for (int c = 0; c < chunks; ++c) {
+        stream(c, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float e = v[j] - mean;
+          if (chunk_col<VEC>(c, j, t, tpr) < d) m2 += e * e;
+        }
+      }
+      m2 = row_sum2(make_float2(m2, 0.f), t, tpr, 1, red, phase).x;
+      rstd = 1.f / sqrtf(m2 / static_cast<float>(d) + a.eps);
+    }
+    for (int c = 0; c < chunks; ++c) {
+      float v[8];
+      stream(c, v);
+      if (z != nullptr) store_chunk<T, VEC>(z, narrow<T>(v), c, t, tpr, d);
+      if (a.ck.q != nullptr)
+        ckpt_store_chunk<T, VEC>(v, a.ck.q + row * a.ck.ldq, a.ck.ex + row * a.ck.lde, c, t, tpr,
+                                 d);
+      if (live) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int col = chunk_col<VEC>(c, j, t, tpr);
+          if (col >= d) continue;
+          const float w = a.weight != nullptr ? load_param(a.weight, a.wtype, col) : 1.f;
+          const float b = a.bias != nullptr ? load_param(a.bias, a.wtype, col) : 0.f;
+          v[j] = (v[j] - mean) * rstd * w + b;
+        }
+      }
+      store_chunk<T, VEC>(y, narrow<T>(v), c, t, tpr, d);
+    }
+    if (t == 0) {
+      if (a.mean != nullptr) a.mean[row] = mean;
+      if (a.rstd != nullptr) a.rstd[row] = rstd;
+    }
+  }
+}
+
+// One chunk of the stream for the backward pass, as loaded.
+template <typename T, bool VEC, bool CK>
+struct RawStream {
+  Raw8<T> r;
+  __device__ __forceinline__ void load(const NormBwdArgs& a, long long row, int c, int t, int tpr) {
+    r = load_chunk<T, VEC>(static_cast<const T*>(a.x) + row * a.ldx, c, t, tpr, a.d);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const { widen(r, v); }
+};
+template <typename T, bool VEC>
+struct RawStream<T, VEC, true> {
+  RawCkpt<VEC> r;
+  __device__ __forceinline__ void load(const NormBwdArgs& a, long long row, int c, int t, int tpr) {
+    r = ckpt_load_chunk<VEC>(a.ck.q + row * a.ck.ldq, a.ck.ex + row * a.ck.lde, c, t, tpr, a.d);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const { ckpt_widen<VEC>(r, v); }
+};
+
+// dx, and this CTA's sums over its rows for dw (and db), which each thread
+// keeps in registers for its own columns: the rows' order is fixed by the grid,
+// so the sums are the same on every run.
+template <typename T, bool VEC, int CH, bool CK, bool DB>
+__global__ void __launch_bounds__(512) norm_bwd_kernel(const NormBwdArgs a) {
+  __shared__ float2 red[8][2 * 32];
+  extern __shared__ float col_sums[];  // [d], [d] when the CTA has several rows in flight
+  const int t = threadIdx.x, tpr = blockDim.x, g = threadIdx.y, d = a.d;
+  int phase = 0;
+  float w[CH][8], dw[CH][8], db[DB ? CH : 1][8];
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int col = chunk_col<VEC>(c, j, t, tpr);
+      w[c][j] = a.weight != nullptr && col < d ? load_param(a.weight, a.wtype, col) : 1.f;
+      dw[c][j] = 0.f;
+      if (DB) db[DB ? c : 0][j] = 0.f;
+    }
+  const T* dy = static_cast<const T*>(a.dy);
+  const T* dres = static_cast<const T*>(a.dres);
+  T* dx = static_cast<T*>(a.dx);
+  const long long step = static_cast<long long>(gridDim.x) * blockDim.y;
+  long long row = static_cast<long long>(blockIdx.x) * blockDim.y + g;
+  bool live = row_live(a.mask, row, a.n);
+  bool live1 = row_live(a.mask, row + step, a.n);
+  const float inv_d = 1.f / static_cast<float>(d);
+  Raw8<T> ry[CH], rr[CH];
+  RawStream<T, VEC, CK> rx[CH];
+  float mean = 0.f, rstd = 0.f;
+  const auto fetch = [&](long long r) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      ry[c] = load_chunk<T, VEC>(dy + r * a.lddy, c, t, tpr, d);
+      rx[c].load(a, r, c, t, tpr);
+      if (dres != nullptr) rr[c] = load_chunk<T, VEC>(dres + r * a.lddres, c, t, tpr, d);
+    }
+    rstd = a.rstd[r];
+    mean = a.kind != GRPO_NORM_RMS ? a.mean[r] : 0.f;
+  };
+  if (live) fetch(row);
+  for (; row < a.n; row += step) {
+    const bool live2 = row_live(a.mask, row + 2 * step, a.n);
+    if (!live) {
+      const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+        store_chunk<T, VEC>(dx + row * a.lddx, narrow<T>(zero), c, t, tpr, d);
+      if (live1) fetch(row + step);
+    } else {
+      float u[CH][8], h[CH][8];
+      Raw8<T> cur_res[CH];
+      float2 s = make_float2(0.f, 0.f);
+      const float rs = rstd;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        widen(ry[c], u[c]);
+        rx[c].get(h[c]);
+        if (dres != nullptr) cur_res[c] = rr[c];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          h[c][j] = (h[c][j] - mean) * rs;
+          dw[c][j] += u[c][j] * h[c][j];
+          if (DB) db[DB ? c : 0][j] += u[c][j];
+          u[c][j] *= w[c][j];
+          s.x += u[c][j];
+          s.y += u[c][j] * h[c][j];
+        }
+      }
+      if (live1) fetch(row + step);
+      s = row_sum2(s, t, tpr, g + 1, red[g], phase);
+      const float c1 = a.kind != GRPO_NORM_RMS ? s.x * inv_d : 0.f;
+      const float c2 = s.y * inv_d;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[c][j] = rs * (u[c][j] - c1 - h[c][j] * c2);
+        if (dres != nullptr) {
+          float r[8];
+          widen(cur_res[c], r);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) u[c][j] += r[j];
+        }
+        store_chunk<T, VEC>(dx + row * a.lddx, narrow<T>(u[c]), c, t, tpr, d);
+      }
+    }
+    live = live1;
+    live1 = live2;
+  }
+  if (a.dweight == nullptr && !DB) return;
+  // The CTA's rows in flight, added in their order.
+  if (blockDim.y > 1) {
+    float* sw = col_sums;
+    float* sb = col_sums + d;
+    for (int k = 0; k < static_cast<int>(blockDim.y); ++k) {
+      if (g == k) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int col = chunk_col<VEC>(c, j, t, tpr);
+            if (col < d) {
+              sw[col] = k == 0 ? dw[c][j] : sw[col] + dw[c][j];
+              if (DB) sb[col] = k == 0 ? db[DB ? c : 0][j] : sb[col] + db[DB ? c : 0][j];
+            }
+          }
+      }
+      __syncthreads();
+    }
+    float* pw = a.partials + static_cast<long long>(blockIdx.x) * d;
+    float* pb = pw + static_cast<long long>(gridDim.x) * d;
+    for (int col = g * tpr + t; col < d; col += tpr * blockDim.y) {
+      pw[col] = sw[col];
+      if (DB) pb[col] = sb[col];
+    }
+  } else {
+    float* pw = a.partials + static_cast<long long>(blockIdx.x) * d;
+    float* pb = pw + static_cast<long long>(gridDim.x) * d;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int col = chunk_col<VEC>(c, j, t, tpr);
+        if (col < d) {
+          pw[col] = dw[c][j];
+          if (DB) pb[col] = db[DB ? c : 0][j];
+        }
+      }
+  }
+}
+
+// Rows beyond kNormRegisterRow columns: dx in two walks over the row.
+template <typename T, bool VEC, bool CK>
+__global__ void __launch_bounds__(512) norm_bwd_long_kernel(const NormBwdArgs a) {
+  __shared__ float2 red[2 * 32];
+  const int t = threadIdx.x, tpr = blockDim.x, d = a.d;
+  const int chunks = (d + 8 * tpr - 1) / (8 * tpr);
+  int phase = 0;
+  for (long long row = blockIdx.x; row < a.n; row += gridDim.x) {
+    T* dx = static_cast<T*>(a.dx) + row * a.lddx;
+    const T* dy = static_cast<const T*>(a.dy) + row * a.lddy;
+    const bool live = row_live(a.mask, row, a.n);
+    float u[8], h[8];
+    float2 s = make_float2(0.f, 0.f);
+    const float rs = live ? a.rstd[row] : 0.f;
+    const float mean = live && a.kind != GRPO_NORM_RMS ? a.mean[row] : 0.f;
+    const auto terms = [&](int c) {
+      RawStream<T, VEC, CK> rx;
+      rx.load(a, row, c, t, tpr);
+      rx.get(h);
+      widen(load_chunk<T, VEC>(dy, c, t, tpr, d), u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int col = chunk_col<VEC>(c, j, t, tpr);
+        h[j] = (h[j] - mean) * rs;
+        if (col < d && a.weight != nullptr) u[j] *= load_param(a.weight, a.wtype, col);
+      }
+    };
+    if (live) {
+      for (int c = 0; c < chunks; ++c) {
+        terms(c);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          s.x += u[j];
+          s.y += u[j] * h[j];
+        }
+      }
+      s = row_sum2(s, t, tpr, 1, red, phase);
+    }
+    const float c1 = a.kind != GRPO_NORM_RMS ? s.x / static_cast<float>(d) : 0.f;
+    const float c2 = s.y / static_cast<float>(d);
+    for (int c = 0; c < chunks; ++c) {
+      if (live) {
+        terms(c);
+        float r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (a.dres != nullptr)
+          widen(load_chunk<T, VEC>(static_cast<const T*>(a.dres) + row * a.lddres, c, t, tpr, d), r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] = rs * (u[j] - c1 - h[j] * c2) + r[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] = 0.f;
+      }
+      store_chunk<T, VEC>(dx, narrow<T>(u), c, t, tpr, d);
+    }
+  }
+}
+
+// The weight gradients of such rows, before dx is written (dx may lie on dy):
+// a CTA takes 8 x 32 columns (VEC) or 32 x 8 and every gridDim.y-th group of 8
+// rows, one row to each of its 8 warps.
+template <typename T, bool VEC, bool CK>
+__global__ void __launch_bounds__(256) norm_bwd_cols_kernel(const NormBwdArgs a) {
+  __shared__ float sh[2][8][256];
+  const int t = threadIdx.x, g = threadIdx.y, d = a.d;
+  const int first = blockIdx.x * 256;  // columns [first, first + 256)
+  float dw[8], db[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) dw[j] = db[j] = 0.f;
+  const int dd = min(d - first, 256);
+  const T* dy = static_cast<const T*>(a.dy) + first;
+  NormBwdArgs s = a;  // the same rows, from this column on
+  s.d = dd;
+  if (CK) {
+    s.ck.q += first;
+    s.ck.ex += first / kCkptBlock;
+  } else {
+    s.x = static_cast<const T*>(a.x) + first;
+  }
+  for (long long row = static_cast<long long>(blockIdx.y) * 8 + g; row < a.n;
+       row += static_cast<long long>(gridDim.y) * 8) {
+    if (!row_live(a.mask, row, a.n)) continue;
+    float u[8], h[8];
+    widen(load_chunk<T, VEC>(dy + row * a.lddy, 0, t, 32, dd), u);
+    RawStream<T, VEC, CK> rx;
+    rx.load(s, row, 0, t, 32);
+    rx.get(h);
+    const float rs = a.rstd[row];
+    const float mean = a.kind != GRPO_NORM_RMS ? a.mean[row] : 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      dw[j] += u[j] * ((h[j] - mean) * rs);
+      db[j] += u[j];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int col = chunk_col<VEC>(0, j, t, 32);
+    sh[0][g][col] = dw[j];
+    sh[1][g][col] = db[j];
+  }
+  __syncthreads();
+  const int col = g * 32 + t;
+  if (col >= dd) return;
+  float w = 0.f, b = 0.f;
+  for (int k = 0; k < 8; ++k) {
+    w += sh[0][k][col];
+    b += sh[1][k][col];
+  }
+  a.partials[static_cast<long long>(blockIdx.y) * d + first + col] = w;
+  if (a.dbias != nullptr)
+    a.partials[static_cast<long long>(gridDim.y + blockIdx.y) * d + first + col] = b;
+}
+
+// dw and db from the CTAs' partial sums: 32 columns a CTA, the partial rows
+// dealt to its 8 warps, whose sums are added in warp order.
+__global__ void __launch_bounds__(256) norm_bwd_finish_kernel(const float* __restrict__ partials,
+                                                              int rows, int d, float* dweight,
+                                                              float* dbias, const float* add_dw,
+                                                              const float* add_db) {
+  __shared__ float sh[8][33];
+  const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + lane;
+  const bool bias = blockIdx.y == 1;
+  const float* p = partials + (bias ? static_cast<long long>(rows) * d : 0);
+  float s = 0.f;
+  if (col < d) {
+#pragma unroll 8
+    for (int r = g; r < rows; r += 8) s += p[static_cast<long long>(r) * d + col];
+  }
+  sh[g][lane] = s;
+  __syncthreads();
+  if (g != 0 || col >= d) return;
+  for (int k = 1; k < 8; ++k) s += sh[k][lane];
+  const float* add = bias ? add_db : add_dw;
+  float* out = bias ? dbias : dweight;
+  if (out != nullptr) out[col] = add != nullptr ? add[col] + s : s;
+}
+
+// Threads of a row and rows of a CTA for D columns held in registers: 16
+// values a thread (8 up to 256 columns).
+struct RowShape {
+  int tpr, rows, ch;
+};
+RowShape row_shape(int d) {
+  RowShape s;
+  s.ch = d <= 256 ? 1 : 2;
+  const int per = 8 * s.ch;
+  s.tpr = (d + per * 32 - 1) / (per * 32) * 32;
+  s.rows = s.tpr >= kRowThreads ? 1 : kRowThreads / s.tpr;
+  return s;
+}
+
+// CTAs of `threads` threads resident on the device, looked up once per kernel.
+template <auto Kernel>
+int resident(int threads, size_t smem, int sms) {
+  static std::atomic<int> known[33];
+  std::atomic<int>& k = known[threads / 32];
+  int n = k.load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, Kernel, threads, smem) != cudaSuccess ||
+        n < 1)
+      n = 1;
+    k.store(n, std::memory_order_relaxed);
+  }
+  return n * sms;
+}
+
+template <typename T, bool VEC, int CH>
+cudaError_t fwd(const NormFwdArgs& a, const RowShape& s, int sms, cudaStream_t st) {
+  constexpr auto kernel = norm_fwd_kernel<T, VEC, CH>;
+  const long long units = (a.n + s.rows - 1) / s.rows;
+  const int grid = static_cast<int>(
+      std::min<long long>(units, resident<kernel>(s.tpr * s.rows, 0, sms)));
+  LaunchTimer timer("norm_fwd_kernel", st);
+  kernel<<<grid, dim3(s.tpr, s.rows), 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T, bool VEC>
+cudaError_t fwd_any(const NormFwdArgs& a, int sms, cudaStream_t st) {
+  if (a.d > kNormRegisterRow) {
+    const int grid = static_cast<int>(std::min<long long>(a.n, 3LL * sms));
+    LaunchTimer timer("norm_fwd_long_kernel", st);
+    norm_fwd_long_kernel<T, VEC><<<grid, 512, 0, st>>>(a);
+    return cudaGetLastError();
+  }
+  const RowShape s = row_shape(a.d);
+  return s.ch == 1 ? fwd<T, VEC, 1>(a, s, sms, st) : fwd<T, VEC, 2>(a, s, sms, st);
+}
+
+cudaError_t finish(const NormBwdArgs& a, int rows, cudaStream_t st) {
+  if (a.dweight == nullptr && a.dbias == nullptr) return cudaSuccess;
+  const dim3 grid((a.d + 31) / 32, a.dbias != nullptr ? 2 : 1);
+  LaunchTimer timer("norm_bwd_finish_kernel", st);
+  norm_bwd_finish_kernel<<<grid, 256, 0, st>>>(a.partials, rows, a.d, a.dweight, a.dbias,
+                                               a.add_dweight, a.add_dbias);
+  return cudaGetLastError();
+}
+
+template <typename T, bool VEC, int CH, bool CK, bool DB>
+cudaError_t bwd(const NormBwdArgs& a, const RowShape& s, int sms, cudaStream_t st) {
+  constexpr auto kernel = norm_bwd_kernel<T, VEC, CH, CK, DB>;
+  const long long units = (a.n + s.rows - 1) / s.rows;
+  const size_t smem = s.rows > 1 ? static_cast<size_t>(a.d) * (DB ? 8 : 4) : 0;
+  // Occupancy is asked for the largest such buffer (rows > 1: at most 2048 columns).
+  const int grid = static_cast<int>(std::min<long long>(
+      std::min<long long>(units, kNormMaxPartials),
+      resident<kernel>(s.tpr * s.rows, s.rows > 1 ? 2048 * 8 : 0, sms)));
+  {
+    LaunchTimer timer("norm_bwd_kernel", st);
+    kernel<<<grid, dim3(s.tpr, s.rows), smem, st>>>(a);
+  }
+  const cudaError_t e = cudaGetLastError();
+  return e != cudaSuccess ? e : finish(a, grid, st);
+}
+
+template <typename T, bool VEC, bool CK>
+cudaError_t bwd_any(const NormBwdArgs& a, int sms, cudaStream_t st) {
+  if (a.d > kNormRegisterRow) {
+    const int slabs = (a.d + 255) / 256;
+    const int groups = norm_bwd_partials(a.n, a.d);
+    if (a.dweight != nullptr || a.dbias != nullptr) {
+      LaunchTimer timer("norm_bwd_cols_kernel", st);
+      norm_bwd_cols_kernel<T, VEC, CK><<<dim3(slabs, groups), dim3(32, 8), 0, st>>>(a);
+    }
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    {
+      LaunchTimer timer("norm_bwd_long_kernel", st);
+      const int grid = static_cast<int>(std::min<long long>(a.n, 3LL * sms));
+      norm_bwd_long_kernel<T, VEC, CK><<<grid, 512, 0, st>>>(a);
+    }
+    e = cudaGetLastError();
+    return e != cudaSuccess ? e : finish(a, groups, st);
+  }
+  const RowShape s = row_shape(a.d);
+  if (a.dbias != nullptr)
+    return s.ch == 1 ? bwd<T, VEC, 1, CK, true>(a, s, sms, st)
+                     : bwd<T, VEC, 2, CK, true>(a, s, sms, st);
+  return s.ch == 1 ? bwd<T, VEC, 1, CK, false>(a, s, sms, st)
+                   : bwd<T, VEC, 2, CK, false>(a, s, sms, st);
+}
+
+template <typename T>
+cudaError_t bwd_typed(const NormBwdArgs& a, bool vec, int sms, cudaStream_t st) {
+  if (a.x != nullptr)
+    return vec ? bwd_any<T, true, false>(a, sms, st) : bwd_any<T, false, false>(a, sms, st);
+  return vec ? bwd_any<T, true, true>(a, sms, st) : bwd_any<T, false, true>(a, sms, st);
+}
+
+}  // namespace
+
+int norm_bwd_partials(long long n, int d) {
+  if (d > kNormRegisterRow) {
+    // Row groups of norm_bwd_cols_kernel: 8 CTAs an SM.
+    return static_cast<int>(std::min<long long>(std::max(1, 8 * 152 / ((d + 255) / 256)),
+                                                std::max<long long>(1, (n + 7) / 8)));
+  }
+  const int rows = row_shape(d).rows;
+  return static_cast<int>(
+      std::min<long long>(kNormMaxPartials, std::max<long long>(1, (n + rows - 1) / rows)));
+}
+
+cudaError_t launch_norm_fwd(const NormFwdArgs& a, int dtype, bool vec, int sms, cudaStream_t st) {
+  switch (dtype) {
+    case GRPO_DTYPE_BF16:
+      return vec ? fwd_any<__nv_bfloat16, true>(a, sms, st)
+                 : fwd_any<__nv_bfloat16, false>(a, sms, st);
+    case GRPO_DTYPE_FP16:
+      return vec ? fwd_any<__half, true>(a, sms, st) : fwd_any<__half, false>(a, sms, st);
+    default:
+      return vec ? fwd_any<float, true>(a, sms, st) : fwd_any<float, false>(a, sms, st);
+  }
+}
+
+cudaError_t launch_norm_bwd(const NormBwdArgs& a, int dtype, bool vec, int sms, cudaStream_t st) {
+  if (a.n == 0) return finish(a, 0, st);
+  switch (dtype) {
+    case GRPO_DTYPE_BF16: return bwd_typed<__nv_bfloat16>(a, vec, sms, st);
+    case GRPO_DTYPE_FP16: return bwd_typed<__half>(a, vec, sms, st);
+    default: return bwd_typed<float>(a, vec, sms, st);
+  }
+}
+
+}  // namespace grpo

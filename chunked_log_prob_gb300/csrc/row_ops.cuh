@@ -1,0 +1,335 @@
+// Row-wise building blocks shared by the norm and the activation checkpoint
+// kernels: a thread's share of a row, loads and stores of 8 values at a time,
+// sums over the threads of a row, and the 8-bit checkpoint format.
+//
+// A row of D values is spread over `tpr` threads (a multiple of 32); thread t
+// holds chunks of 8 values. Where every row starts on 16 bytes and D % 8 == 0
+// (VEC), chunk c of thread t is the 8 consecutive columns from (c tpr + t) 8.
+// Otherwise its value j is column (8 c + j) tpr + t, loaded one by one: any D,
+// stride and alignment. In both, the 32 columns of a checkpoint block are held
+// by one warp: by 4 neighbouring lanes (VEC), or one column to a lane.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cfloat>
+#include <cstdint>
+
+#include "ptx.cuh"
+
+namespace grpo {
+
+constexpr int kCkptBlock = 32;     // columns that share a power of two
+constexpr int kCkptMinExp = -117;  // 2^-117 2^-9 is a normal bf16: every value
+                                   // of the format expands to bf16 exactly
+constexpr int kCkptBias = 127;
+
+template <typename T>
+struct alignas(16) Raw8 {
+  T e[8];
+};
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T v) {
+  return static_cast<float>(v);
+}
+
+// Two values rounded to T, to nearest even.
+__device__ __forceinline__ void from_f32x2(float a, float b, __nv_bfloat16* o) {
+  *reinterpret_cast<__nv_bfloat162*>(o) = __floats2bfloat162_rn(a, b);
+}
+__device__ __forceinline__ void from_f32x2(float a, float b, __half* o) {
+  *reinterpret_cast<__half2*>(o) = __floats2half2_rn(a, b);
+}
+__device__ __forceinline__ void from_f32x2(float a, float b, float* o) {
+  o[0] = a;
+  o[1] = b;
+}
+
+template <bool VEC>
+__device__ __forceinline__ int chunk_col(int c, int j, int t, int tpr) {
+  return VEC ? (c * tpr + t) * 8 + j : (c * 8 + j) * tpr + t;
+}
+
+// Chunk c of this thread's share of a row; zeros past column d.
+template <typename T, bool VEC>
+__device__ __forceinline__ Raw8<T> load_chunk(const T* row, int c, int t, int tpr, int d) {
+  Raw8<T> r;
+  if (VEC) {
+    const int col = chunk_col<true>(c, 0, t, tpr);
+    uint4* w = reinterpret_cast<uint4*>(&r);
+    if (col < d) {
+      const uint4* p = reinterpret_cast<const uint4*>(row + col);
+#pragma unroll
+      for (int i = 0; i < static_cast<int>(sizeof(r) / 16); ++i) w[i] = p[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < static_cast<int>(sizeof(r) / 16); ++i) w[i] = make_uint4(0, 0, 0, 0);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int col = chunk_col<false>(c, j, t, tpr);
+      r.e[j] = col < d ? row[col] : T(0.f);
+    }
+  }
+  return r;
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_chunk(T* row, const Raw8<T>& r, int c, int t, int tpr,
+                                            int d) {
+  if (VEC) {
+    const int col = chunk_col<true>(c, 0, t, tpr);
+    if (col < d) {
+      uint4* p = reinterpret_cast<uint4*>(row + col);
+      const uint4* w = reinterpret_cast<const uint4*>(&r);
+#pragma unroll
+      for (int i = 0; i < static_cast<int>(sizeof(r) / 16); ++i) p[i] = w[i];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int col = chunk_col<false>(c, j, t, tpr);
+      if (col < d) row[col] = r.e[j];
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void widen(const Raw8<T>& r, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = to_f32(r.e[j]);
+}
+
+template <typename T>
+__device__ __forceinline__ Raw8<T> narrow(const float (&v)[8]) {
+  Raw8<T> r;
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) from_f32x2(v[j], v[j + 1], &r.e[j]);
+  return r;
+}
+
+// A weight or bias of either type; `type` is a grpo_dtype.
+__device__ __forceinline__ float load_param(const void* p, int type, int col) {
+  if (type == GRPO_DTYPE_FP32) return static_cast<const float*>(p)[col];
+  if (type == GRPO_DTYPE_BF16) return to_f32(static_cast<const __nv_bfloat16*>(p)[col]);
+  return to_f32(static_cast<const __half*>(p)[col]);
+}
+
+// Sum of a pair over the `tpr` threads of a row, given to all of them, in a
+// fixed order. tpr == 32: shuffles alone. Otherwise one named barrier (`bar`,
+// 1-15) of the row's threads; `sh` holds 2 x 32 pairs, used in turn (`phase`).
+__device__ __forceinline__ float2 warp_sum2(float2 v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+  }
+  return v;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+__device__ __forceinline__ float2 row_sum2(float2 v, int t, int tpr, int bar, float2* sh,
+                                           int& phase) {
+  v = warp_sum2(v);
+  if (tpr == 32) return v;
+  float2* s = sh + phase * 32;
+  phase ^= 1;
+  if ((t & 31) == 0) s[t >> 5] = v;
+  named_barrier(bar, tpr);
+  const int lane = t & 31;
+  return warp_sum2(lane < (tpr >> 5) ? s[lane] : make_float2(0.f, 0.f));
+}
+
+// ---------------------------------------------------- 8-bit checkpoints ----
+// Blocks of 32 columns of a row share 2^k; a value is q 2^k with q = e4m3 of
+// x / 2^k, rounded to nearest even (half a step: 2^-4 relative for |q| >=
+// 2^-6, 2^-10 2^k below). With a = max |x| over the block's finite values,
+// a = m 2^e, 1 <= m < 2: k = e - 8 if m <= 1.75 (a / 2^k <= 448, e4m3's
+// largest), else e - 7. A power of two makes x / 2^k and q 2^k exact.
+// Infinities and NaN are kept as NaN. Where m > 1.75 at the type's largest
+// exponent, rounding up to 256 2^k would leave the type: held to 240 there.
+
+template <typename T>
+struct CkptTop;  // the k at which 256 2^k is beyond the type's largest value
+template <>
+struct CkptTop<__nv_bfloat16> {
+  static constexpr int k = 120;
+};
+template <>
+struct CkptTop<__half> {
+  static constexpr int k = 8;
+};
+template <>
+struct CkptTop<float> {
+  static constexpr int k = 120;
+};
+
+// k of a block whose largest finite magnitude is `a` (a >= 0, finite).
+__device__ __forceinline__ int ckpt_exponent(float a) {
+  const uint32_t u = __float_as_uint(a);
+  const int k = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return max(k, kCkptMinExp);
+}
+
+// 2^k for k in [-126, 127].
+__device__ __forceinline__ float pow2(int k) {
+  return __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+}
+
+// |v| maxima that keep a NaN.
+__device__ __forceinline__ float max_abs_nan(float m, float v) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+  return r;
+}
+
+// Two e4m3 (low byte first), to nearest even; NaN stays NaN.
+__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Two e4m3 (low byte first) widened.
+__device__ __forceinline__ float2 unpack_e4m3x2(uint32_t w) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(w)));
+  float2 f;
+  unpack_f16x2(h, f.x, f.y);
+  return f;
+}
+
+// One value for the checkpoint, with everything that can be special about it.
+template <typename T>
+__device__ __forceinline__ float ckpt_scaled(float v, float inv, int k) {
+  if (!(fabsf(v) <= FLT_MAX)) return __uint_as_float(0x7fc00000u);
+  v *= inv;
+  if (k >= CkptTop<T>::k) v = fminf(fmaxf(v, -240.f), 240.f);
+  return v;
+}
+
+// Writes chunk c of a row to its checkpoint. Every lane of the warp calls this
+// (values past column d are 0). q: the row's bytes; ex: its exponents.
+template <typename T, bool VEC>
+__device__ __forceinline__ void ckpt_store_chunk(const float (&v)[8], uint8_t* q, uint8_t* ex,
+                                                 int c, int t, int tpr, int d) {
+  if (VEC) {
+    const int col = chunk_col<true>(c, 0, t, tpr);
+    float a = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a = max_abs_nan(a, v[j]);
+    a = max_abs_nan(a, __shfl_xor_sync(0xffffffffu, a, 1));
+    a = max_abs_nan(a, __shfl_xor_sync(0xffffffffu, a, 2));
+    uint2 w;
+    int k;
+    // No value of the warp's blocks is special (the usual case): scale and
+    // round. The branch keeps some ten instructions per value out of the path.
+    const bool plain = a <= FLT_MAX && ckpt_exponent(a) < CkptTop<T>::k;
+    if (__all_sync(0xffffffffu, plain)) {
+      k = ckpt_exponent(a);
+      const float inv = pow2(-k);
+      w.x = pack_e4m3x2(v[0] * inv, v[1] * inv) | pack_e4m3x2(v[2] * inv, v[3] * inv) << 16;
+      w.y = pack_e4m3x2(v[4] * inv, v[5] * inv) | pack_e4m3x2(v[6] * inv, v[7] * inv) << 16;
+    } else {
+      a = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float m = fabsf(v[j]);
+        if (m <= FLT_MAX) a = fmaxf(a, m);
+      }
+      a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+      a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+      k = ckpt_exponent(a);
+      const float inv = pow2(-k);
+      uint32_t h[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        h[j] = pack_e4m3x2(ckpt_scaled<T>(v[2 * j], inv, k), ckpt_scaled<T>(v[2 * j + 1], inv, k));
+      w.x = h[0] | h[1] << 16;
+      w.y = h[2] | h[3] << 16;
+    }
+    if (col < d) {
+      *reinterpret_cast<uint2*>(q + col) = w;
+      if ((t & 3) == 0) ex[col / kCkptBlock] = static_cast<uint8_t>(k + kCkptBias);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int col = chunk_col<false>(c, j, t, tpr);
+      const uint32_t u = __float_as_uint(v[j]) & 0x7fffffffu;
+      const uint32_t a = __reduce_max_sync(0xffffffffu, u < 0x7f800000u ? u : 0u);
+      const int k = ckpt_exponent(__uint_as_float(a));
+      const float s = ckpt_scaled<T>(v[j], pow2(-k), k);
+      if (col < d) {
+        q[col] = static_cast<uint8_t>(pack_e4m3x2(s, 0.f) & 0xffu);
+        if ((t & 31) == 0) ex[col / kCkptBlock] = static_cast<uint8_t>(k + kCkptBias);
+      }
+    }
+  }
+}
+
+// A chunk of a checkpoint row as loaded: its bytes and its exponents.
+template <bool VEC>
+struct RawCkpt {
+  uint2 w;
+  uint8_t ex[VEC ? 1 : 8];
+};
+
+template <bool VEC>
+__device__ __forceinline__ RawCkpt<VEC> ckpt_load_chunk(const uint8_t* q, const uint8_t* ex, int c,
+                                                        int t, int tpr, int d) {
+  RawCkpt<VEC> r;
+  if (VEC) {
+    const int col = chunk_col<true>(c, 0, t, tpr);
+    r.w = make_uint2(0, 0);
+    r.ex[0] = kCkptBias;
+    if (col < d) {
+      r.w = *reinterpret_cast<const uint2*>(q + col);
+      r.ex[0] = ex[col / kCkptBlock];
+    }
+  } else {
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int col = chunk_col<false>(c, j, t, tpr);
+      r.ex[VEC ? 0 : j] = kCkptBias;
+      if (col < d) {
+        w[j >> 2] |= static_cast<uint32_t>(q[col]) << (8 * (j & 3));
+        r.ex[VEC ? 0 : j] = ex[col / kCkptBlock];
+      }
+    }
+    r.w = make_uint2(w[0], w[1]);
+  }
+  return r;
+}
+
+// The stored exponent byte as the factor 2^k. Bytes outside what packing
+// writes (10 to 247) are held to [1, 254], where the factor is a normal fp32.
+__device__ __forceinline__ float ckpt_factor(uint32_t byte) {
+  return __uint_as_float(min(max(byte, 1u), 254u) << 23);
+}
+
+template <bool VEC>
+__device__ __forceinline__ void ckpt_widen(const RawCkpt<VEC>& r, float (&v)[8]) {
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    const uint32_t w = (h < 2 ? r.w.x : r.w.y) >> (16 * (h & 1));
+    const float2 f = unpack_e4m3x2(w & 0xffffu);
+    v[2 * h] = f.x * ckpt_factor(r.ex[VEC ? 0 : 2 * h]);
+    v[2 * h + 1] = f.y * ckpt_factor(r.ex[VEC ? 0 : 2 * h + 1]);
+  }
+}
+
+}  // namespace grpo

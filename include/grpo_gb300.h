@@ -366,6 +366,118 @@ typedef struct grpo_kernel_time {
 int grpo_launch_timing_enable(int on);
 int grpo_launch_timing_read(grpo_kernel_time* out, int capacity, int* count);
 
+/* ---------------------------------------------------------------------------
+ * What stands before the head in a training step: the decoder's final norm
+ * (and any other norm on the residual stream), and activations kept for the
+ * backward pass in 8 bits. grpo_loss_fwd_bwd's dH is grpo_norm_bwd's dy.
+ *
+ * Tensors are [n_tokens][hidden] with their own row strides, in elements; any
+ * hidden size, stride and alignment (of the element's size) is taken, rows on
+ * 16 bytes with hidden % 8 == 0 are the fast form. `mask` (uint8 [n_tokens] or
+ * NULL): a row with mask 0 is never read, each of its output rows is exact
+ * zeros and it adds nothing to any gradient. n_tokens = 0 is allowed.
+ * Outputs may lie on inputs of the same type and stride (y on x, z on
+ * residual, dx on dy, dres or x); other overlaps are not. Calls are
+ * asynchronous on `stream`, allocate nothing, and can be captured in a graph.
+ * ------------------------------------------------------------------------- */
+#define GRPO_DTYPE_BF16 0
+#define GRPO_DTYPE_FP16 1
+#define GRPO_DTYPE_FP32 2
+
+#define GRPO_NORM_LAYER 0
+#define GRPO_NORM_RMS 1
+
+typedef struct grpo_norm_desc {
+  int64_t n_tokens;
+  int32_t hidden;
+  int32_t dtype;           /* GRPO_DTYPE_* of x, residual, y, z, dy, dres, dx  */
+  int32_t weight_dtype;    /* of weight and bias: dtype, or GRPO_DTYPE_FP32    */
+  int32_t kind;            /* GRPO_NORM_LAYER or GRPO_NORM_RMS                 */
+  float eps;               /* added to the variance (mean square); >= 0        */
+  int32_t reserved;        /* must be 0                                        */
+  /* Elements from one row to the next; 0 = hidden. */
+  int64_t x_stride, residual_stride, y_stride, z_stride;
+  int64_t dy_stride, dres_stride, dx_stride;
+} grpo_norm_desc;
+
+/* z = x + residual, rounded to dtype (z = x without a residual);
+ * layer: y = (z - mean z) rstd weight + bias, rstd = (var z + eps)^-1/2;
+ * rms:   y = z rstd weight + bias,            rstd = (mean z^2 + eps)^-1/2.
+ *   weight_or_null, bias_or_null: [hidden]; NULL = ones, zeros
+ *   z_or_null: required with a residual unless nothing later needs the stream
+ *   mean_or_null, rstd_or_null: fp32 [n_tokens], what grpo_norm_bwd needs
+ *     (mean: layer only)
+ *   ckpt_or_null: checkpoint of z (grpo_ckpt_size bytes, 256-byte aligned)
+ * Statistics are fp32, of the rounded z. One kernel, no workspace. */
+int grpo_norm_fwd(const void* x, const void* residual_or_null, const void* weight_or_null,
+                  const void* bias_or_null, const uint8_t* mask_or_null, void* y,
+                  void* z_or_null, float* mean_or_null, float* rstd_or_null,
+                  void* ckpt_or_null, const grpo_norm_desc* desc, void* stream);
+
+/* Bytes of workspace that grpo_norm_bwd needs (partial weight gradients: at
+ * most 608 rows of `hidden` fp32, two of each with a bias). Host only. */
+int grpo_norm_workspace_size(const grpo_norm_desc* desc, size_t* bytes);
+
+/* h = (z - mean) rstd, u = dy weight (rms: mean 0, and no mean(u) term):
+ *   dx      = rstd (u - mean(u) - h mean(u h)) + dres
+ *   dweight = add_dweight + sum_t dy h,  dbias = add_dbias + sum_t dy
+ * z comes from x, or from its checkpoint (exactly one is given). x + residual
+ * share the gradient dx; dres is the gradient that reaches z past the norm.
+ *   mean (layer only), rstd: fp32 [n_tokens] of the forward pass
+ *   dweight_or_null, dbias_or_null: fp32 [hidden], overwritten
+ *   add_dweight_or_null, add_dbias_or_null: fp32 [hidden], may be the outputs
+ * Sums are fp32 in an order fixed by the sizes: results repeat bit for bit. */
+int grpo_norm_bwd(const void* dy, const void* x_or_null, const void* ckpt_or_null,
+                  const void* weight_or_null, const float* mean_or_null, const float* rstd,
+                  const uint8_t* mask_or_null, const void* dres_or_null, void* dx,
+                  float* dweight_or_null, float* dbias_or_null,
+                  const float* add_dweight_or_null, const float* add_dbias_or_null,
+                  const grpo_norm_desc* desc, void* workspace, size_t workspace_bytes,
+                  void* stream);
+
+/* Activation checkpoints in 8 bits. Of each row, every 32 columns share a
+ * power of two 2^k, and a value x is kept as the e4m3 (round to nearest even)
+ * of x / 2^k. With a = max |x| over the block's finite values, a = m 2^e,
+ * 1 <= m < 2: k = e - 8 if m <= 1.75, else e - 7, and at least -117. A value is
+ * off by at most 2^-4 of itself, or 2^-10 2^k (|x| below 2^-6 2^k). Scaling and
+ * expanding are exact, and every q 2^k is a normal bf16. Infinities and NaN are
+ * kept as NaN; a value that would round beyond the type's largest is held to
+ * 240 2^k.
+ *
+ * Buffer of a checkpoint: n_tokens rows of q, hidden rounded up to 16 bytes
+ * each; from the next multiple of 256 on, rows of exponents, one byte k + 127
+ * per 32 columns, rounded up to 4 bytes each. Padding bytes are not written.
+ * hidden: 1 to 2^27. 1.03 bytes a value. */
+int grpo_ckpt_size(int64_t n_tokens, int32_t hidden, size_t* bytes);
+
+/* Where the exponents begin, and the bytes from row to row (host only). */
+int grpo_ckpt_layout(int64_t n_tokens, int32_t hidden, int64_t* q_stride,
+                     int64_t* exponent_offset, int64_t* exponent_stride);
+
+/* x [n_tokens][hidden] of `dtype`, rows x_stride elements apart (0 = hidden),
+ * to its checkpoint and back. Unpacking rounds q 2^k once to `dtype`. */
+int grpo_ckpt_pack(const void* x, const uint8_t* mask_or_null, void* ckpt, int64_t n_tokens,
+                   int32_t hidden, int32_t dtype, int64_t x_stride, void* stream);
+int grpo_ckpt_unpack(const void* ckpt, void* x, int64_t n_tokens, int32_t hidden, int32_t dtype,
+                     int64_t x_stride, void* stream);
+
+/* Weight gradient of a linear layer whose input was kept as a checkpoint:
+ *   dW[o][i] = add[o][i] + sum_t dY[t][o] X[t][i],  X = q 2^k
+ *   dY: bf16 [n_tokens][out_features], rows dy_stride elements apart (0 =
+ *     out_features); the checkpoint is of [n_tokens][in_features]
+ *   dW: fp32 [out_features][in_features], packed, overwritten
+ *   add_or_null: fp32, like dW, may be dW itself; NULL = 0
+ * out_features, in_features and dy_stride are multiples of 8; dY, dW and add
+ * start on 16 bytes. X is exact in bf16, products are exact, sums are fp32 in
+ * an order fixed by the sizes. Masked tokens: pack with the mask and let dY be
+ * 0 there. The first bytes of the workspace (grpo_ckpt_wgrad_workspace_size,
+ * 256-byte aligned) are a status word for grpo_read_device_status. */
+int grpo_ckpt_wgrad_workspace_size(int64_t n_tokens, int32_t out_features, int32_t in_features,
+                                   size_t* bytes);
+int grpo_ckpt_wgrad(const void* dy, const void* ckpt, const float* add_or_null, float* dW,
+                    int64_t n_tokens, int32_t out_features, int32_t in_features,
+                    int64_t dy_stride, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static text for a status code. */
 const char* grpo_status_string(int status);
 
