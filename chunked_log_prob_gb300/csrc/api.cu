@@ -693,7 +693,7 @@ int device_setup(int* sms) {
     } else if (major != 10 || minor != 3) {
       d.status = GRPO_ERR_UNSUPPORTED_DEVICE;
     } else if (prepare_fwd_gemm() != cudaSuccess || prepare_bwd_gemms() != cudaSuccess ||
-               prepare_fwds_gemm() != cudaSuccess) {
+               prepare_fwds_gemm() != cudaSuccess || prepare_ckpt_wgrad() != cudaSuccess) {
       d.status = GRPO_ERR_CUDA;
     }
     if (d.status == GRPO_OK) {
@@ -732,14 +732,8 @@ bool encode_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t oute
                uint64_t pitch_elems, uint32_t box_inner, uint32_t box_outer,
                CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                uint64_t elem_bytes = 2) {
-  cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {pitch_elems * elem_bytes};
-  cuuint32_t box[2] = {box_inner, box_outer};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = g_encode(map, type, 2, const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
+  return encode_map_2d(map, base, inner, outer, pitch_elems * elem_bytes, box_inner, box_outer,
+                       type, true);
 }
 
 struct Ws {
@@ -1634,6 +1628,20 @@ thread_local TimingState t_timing;
 bool launch_timing_on() { return t_timing.on; }
 
 int setup_device(int* sms) { return device_setup(sms); }
+
+bool encode_map_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
+                   uint64_t pitch, uint32_t box_inner, uint32_t box_outer,
+                   CUtensorMapDataType type, bool swizzle) {
+  cuuint64_t dims[2] = {inner, outer};
+  cuuint64_t strides[1] = {pitch};
+  cuuint32_t box[2] = {box_inner, box_outer};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = g_encode(map, type, 2, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
 
 CallRange::CallRange(const char* name) { nvtxRangePushA(name); }
 CallRange::~CallRange() { nvtxRangePop(); }

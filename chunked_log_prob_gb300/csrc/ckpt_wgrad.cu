@@ -1,5 +1,22 @@
 // Weight gradient of a linear layer from the 8-bit checkpoint of its input:
-//   dW[o][i] = add[o][i] + sum_t dY[t][o] X[t][i],  X = q 2^k exactly.
+//   dW[o][i] = add[o][i] + sum_t dY[t][o] X[t][i],  X = q 2^k.
+//
+// A tcgen05 GEMM over the tokens, both operands MN-major (a token's row holds
+// 64 outputs or inputs in 128 bytes). X never exists in memory: its e4m3 tiles
+// arrive by TMA, eight converter warps widen them on chip to bf16 - exactly,
+// since 2^k is a power of two and e4m3 has 4 significant bits - into the
+// 128-byte-swizzled layout that a bf16 TMA load would have left, and the tensor
+// cores read them from there. Against expanding X first (16384 x 4096: 69 MB
+// read, 134 MB written, 134 MB read again) the operand costs 1.03 bytes a value.
+//
+// A CTA pair computes 256 outputs x 256 inputs. The tensor core's fp32 sums cut
+// off instead of rounding, which bends a long sum towards zero in proportion to
+// its length (measured against fp64: 3.1e-6 at 5541 tokens, 1.1e-5 at 16384), so
+// TMEM holds the sum of kSegment stages at a time (two buffers in turn), and the
+// epilogue warps add each to the tile's running sum in their registers, rounded.
+#include <algorithm>
+#include <cstring>
+
 #include "launch.h"
 #include "norm.h"
 #include "row_ops.cuh"
@@ -7,68 +24,545 @@
 namespace grpo {
 namespace {
 
-constexpr int kTile = 64;   // outputs x inputs of a CTA
-constexpr int kDepth = 32;  // tokens staged at a time
+constexpr int kTileM = 256;        // outputs of a pair's tile, 128 per CTA
+constexpr int kTileN = 256;        // inputs of a pair's tile
+constexpr int kTok = 64;           // tokens of a stage
+constexpr int kStages = 5;         // operand ring: dY tile and widened X tile
+constexpr int kRaw = 4;            // ring of e4m3 tiles
+constexpr int kBoxBytes = kTok * 128;      // 64 tokens x 64 bf16 columns
+constexpr int kOperand = 2 * kBoxBytes;    // a CTA's 128 outputs, or 128 inputs
+constexpr int kRawBytes = kTok * 128;      // 64 tokens x 128 e4m3
+constexpr int kStoreBuf = 32 * 128;        // 32 x 32 fp32 on its way out
+constexpr int kSegment = 16;       // stages summed in TMEM: 1024 tokens
+// Warps: 0 TMA, 1 MMA, 2-3 idle, then two warpgroups of each of these.
+constexpr int kEpilogueWarps = 8, kConvertWarps = 8;
+constexpr int kFirstEpilogue = 4, kFirstConvert = kFirstEpilogue + kEpilogueWarps;
+constexpr int kThreads = 32 * (kFirstConvert + kConvertWarps);
+// Registers of a thread: 96 at launch (640 x 96 = 61440), moved to the epilogue,
+// whose threads hold 128 sums: 128 x 32 + 256 x 168 + 256 x 56 = 61440.
+constexpr int kLaunchRegs = 96, kControlRegs = 32, kEpilogueRegs = 168, kConvertRegs = 56;
+static_assert(128 * kControlRegs + 32 * kEpilogueWarps * kEpilogueRegs +
+                      32 * kConvertWarps * kConvertRegs <=
+                  kThreads * kLaunchRegs,
+              "registers of a CTA");
+constexpr int kSmem = 1024 + kStages * 2 * kOperand + kRaw * kRawBytes +
+                      kEpilogueWarps * kStoreBuf;
+constexpr uint32_t kTmemCols = 512;
+static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+constexpr int kGroupM = 8;         // tiles are walked 8 row tiles at a time
+constexpr int kSlotFloats = kTileM * kTileN;
+constexpr int kRefPairs = 76;      // GB300's SM pairs
 
-// 256 threads, 4 x 4 sums each, fp32.
-__global__ void __launch_bounds__(256) ckpt_wgrad_kernel(const WgradArgs a) {
-  __shared__ float sy[kDepth][kTile + 1], sx[kDepth][kTile + 1];
-  const int o0 = blockIdx.y * kTile, i0 = blockIdx.x * kTile;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const __nv_bfloat16* dy = static_cast<const __nv_bfloat16*>(a.dy);
-  float acc[4][4] = {};
-  for (long long t0 = 0; t0 < a.n; t0 += kDepth) {
-    for (int e = threadIdx.x; e < kDepth * kTile; e += 256) {
-      const int r = e / kTile, c = e % kTile;
-      const long long t = t0 + r;
-      sy[r][c] = t < a.n && o0 + c < a.out ? to_f32(dy[t * a.lddy + o0 + c]) : 0.f;
-      float v = 0.f;
-      if (t < a.n && i0 + c < a.in)
-        v = unpack_e4m3x2(a.ck.q[t * a.ck.ldq + i0 + c]).x *
-            ckpt_factor(a.ck.ex[t * a.ck.lde + (i0 + c) / kCkptBlock]);
-      sx[r][c] = v;
-    }
-    __syncthreads();
-#pragma unroll 4
-    for (int r = 0; r < kDepth; ++r) {
-      float y[4], x[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        y[k] = sy[r][ty + 16 * k];
-        x[k] = sx[r][tx + 16 * k];
+// The work of a launch, in stages of kTok tokens. Tiles are dealt whole, one to
+// a pair and round, except the last round's `cut` tiles when they fill it
+// badly: their stages are dealt evenly, `per_pair` in a row to each pair, and
+// a second kernel adds the pieces of a tile in the order of its tokens.
+struct WgradPlan {
+  int n_m, n_n, kt;
+  int whole;     // tiles dealt whole
+  int cut;       // tiles dealt in pieces
+  int per_pair;  // stages of a pair's part of them
+};
+
+struct Item {
+  int tile, kb, ke;
+  int slot;  // partial tile to write, -1: the tile itself
+};
+
+struct WorkList {
+  int i = 0;
+  long long pos = -1, end = 0;
+  __device__ __forceinline__ bool next(const WgradPlan& p, int pair, int pairs, Item& it) {
+    if (pos < 0) {
+      it.tile = pair + i++ * pairs;
+      if (it.tile < p.whole) {
+        it.kb = 0;
+        it.ke = p.kt;
+        it.slot = -1;
+        return true;
       }
-#pragma unroll
-      for (int p = 0; p < 4; ++p)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) acc[p][k] += y[p] * x[k];
+      const long long all = static_cast<long long>(p.cut) * p.kt;
+      pos = min(static_cast<long long>(pair) * p.per_pair, all);
+      end = min(pos + p.per_pair, all);
+      i = 0;
     }
-    __syncthreads();
+    if (pos >= end) return false;
+    const int t = static_cast<int>(pos / p.kt);
+    it.tile = p.whole + t;
+    it.kb = static_cast<int>(pos - static_cast<long long>(t) * p.kt);
+    it.ke = static_cast<int>(min(static_cast<long long>(p.kt), it.kb + (end - pos)));
+    it.slot = it.ke - it.kb == p.kt ? -1 : 2 * pair + i;
+    ++i;
+    pos += it.ke - it.kb;
+    return true;
+  }
+};
+
+// Row and column of a tile: column by column within kGroupM row tiles, so that
+// the tiles of a round share both operands in L2.
+__device__ __forceinline__ void tile_place(const WgradPlan& p, int tile, int& m, int& n) {
+  const int per_group = kGroupM * p.n_n;
+  const int g = tile / per_group, r = tile - g * per_group;
+  const int rows = min(kGroupM, p.n_m - g * kGroupM);
+  n = r / rows;
+  m = g * kGroupM + (r - n * rows);
+}
+
+// Inputs of a tile: 256, or 128 where no more are left.
+__device__ __forceinline__ int tile_cols(int in, int n) {
+  return in - n * kTileN <= kTileN / 2 ? kTileN / 2 : kTileN;
+}
+
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity))
+    if (clock64() - t0 > kWaitLimitCycles) return;
+}
+
+template <int N>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    ckpt_wgrad_kernel(const __grid_constant__ CUtensorMap map_dy,
+                      const __grid_constant__ CUtensorMap map_q,
+                      const __grid_constant__ CUtensorMap map_dw, const WgradArgs args,
+                      const WgradPlan plan) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full_bar[kStages];   // leader: both CTAs' dY tiles landed
+  __shared__ __align__(8) uint64_t cvt_bar[kStages];    // leader: both CTAs' X tiles widened
+  __shared__ __align__(8) uint64_t empty_bar[kStages];  // the stage's MMAs are done
+  __shared__ __align__(8) uint64_t raw_full[kRaw];      // this CTA's e4m3 tile landed
+  __shared__ __align__(8) uint64_t raw_empty[kRaw];     // its converter warps have read it
+  __shared__ __align__(8) uint64_t tfull_bar[2], tempty_bar[2];
+  __shared__ __align__(8) uint64_t drain_bar;
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int abort_sh;
+
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* const ring = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+  uint8_t* const raw = ring + kStages * 2 * kOperand;
+  uint8_t* const out = raw + kRaw * kRawBytes;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = static_cast<int>(blockIdx.x) / 2, pairs = static_cast<int>(gridDim.x) / 2;
+  volatile int* abort_flag = &abort_sh;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full_bar[s], 2);
+      mbar_init(&cvt_bar[s], 2 * kConvertWarps);
+      mbar_init(&empty_bar[s], 1);
+    }
+    for (int s = 0; s < kRaw; ++s) {
+      mbar_init(&raw_full[s], 1);
+      mbar_init(&raw_empty[s], kConvertWarps);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull_bar[b], 1);
+      mbar_init(&tempty_bar[b], 2 * kEpilogueWarps);  // both CTAs' epilogue warps
+    }
+    mbar_init(&drain_bar, 1);
+    abort_sh = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&map_dy);
+    tma_prefetch_desc(&map_q);
+    tma_prefetch_desc(&map_dw);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(&tmem_base_sh, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = tmem_base_sh;
+
+  WorkList work;
+  Item it;
+  bool ok = true;
+
+  if (warp < kFirstEpilogue) give_registers<kControlRegs>();
+  if (warp == 0) {
+    // ------------------------------------------------------ TMA producer --
+    if (lane == 0) {
+      uint32_t n = 0;  // stages issued
+      while (ok && work.next(plan, pair, pairs, it)) {
+        int tm, tn;
+        tile_place(plan, it.tile, tm, tn);
+        const int o0 = tm * kTileM + static_cast<int>(rank) * (kTileM / 2);
+        const int i0 = tn * kTileN + static_cast<int>(rank) * (tile_cols(args.in, tn) / 2);
+        for (int k = it.kb; k < it.ke; ++k, ++n) {
+          const uint32_t s = n % kStages, r = n % kRaw;
+          if (!mbar_wait(&empty_bar[s], ((n / kStages) & 1u) ^ 1u, abort_flag, args.status) ||
+              !mbar_wait(&raw_empty[r], ((n / kRaw) & 1u) ^ 1u, abort_flag, args.status)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&raw_full[r], kRawBytes);
+          tma_load_2d(raw + r * kRawBytes, &map_q, &raw_full[r], i0, k * kTok);
+          const uint32_t lead = mapa_shared(smem_u32(&full_bar[s]), 0);
+          mbar_arrive_expect_tx_cluster(lead, kOperand);
+          uint8_t* a = ring + s * 2 * kOperand;
+          tma_load_2d_pair_nohint(a, &map_dy, lead, o0, k * kTok);
+          tma_load_2d_pair_nohint(a + kBoxBytes, &map_dy, lead, o0 + 64, k * kTok);
+        }
+      }
+      if (!ok) {
+        // Let the copies in flight land before the CTA exits (the peer passes
+        // the closing cluster barrier only after this).
+        for (uint32_t j = n >= kRaw ? n - kRaw : 0; j < n; ++j)
+          drain(&raw_full[j % kRaw], (j / kRaw) & 1u);
+        if (rank == 0)
+          for (uint32_t j = n >= kStages ? n - kStages : 0; j < n; ++j)
+            drain(&full_bar[j % kStages], (j / kStages) & 1u);
+      }
+    }
+  } else if (warp == 1) {
+    // -------------------------------------------------------- MMA issuer --
+    if (lane == 0 && rank == 0) {
+      uint32_t n = 0, seg = 0;  // stages, segments issued
+      while (ok && work.next(plan, pair, pairs, it)) {
+        int tm, tn;
+        tile_place(plan, it.tile, tm, tn);
+        const uint32_t idesc = idesc_bf16(kTileM, tile_cols(args.in, tn), true, true);
+        for (int k = it.kb; k < it.ke; ++k, ++n) {
+          const bool first = (k - it.kb) % kSegment == 0;
+          const uint32_t buf = seg & 1u;
+          if (first &&
+              !mbar_wait(&tempty_bar[buf], ((seg >> 1) & 1u) ^ 1u, abort_flag, args.status)) {
+            ok = false;
+            break;
+          }
+          const uint32_t d = tmem_base + buf * kTileN;
+          const uint32_t s = n % kStages, parity = (n / kStages) & 1u;
+          if (!mbar_wait(&full_bar[s], parity, abort_flag, args.status) ||
+              !mbar_wait(&cvt_bar[s], parity, abort_flag, args.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a = smem_u32(ring + s * 2 * kOperand), b = a + kOperand;
+#pragma unroll
+          for (int kk = 0; kk < kTok / 16; ++kk)
+            // 64-wide blocks of outputs or inputs 8 KB apart, 8 tokens 1 KB.
+            tc_mma_bf16_pair(d, sdesc_sw128(a + kk * 2048, kBoxBytes, 1024),
+                             sdesc_sw128(b + kk * 2048, kBoxBytes, 1024), idesc,
+                             first && kk == 0 ? 0u : 1u);
+          tc_commit_pair_multicast(&empty_bar[s], 0x3);
+          if ((k - it.kb) % kSegment == kSegment - 1 || k == it.ke - 1) {
+            tc_commit_pair_multicast(&tfull_bar[buf], 0x3);
+            ++seg;
+          }
+        }
+      }
+      tc_commit_pair(&drain_bar);
+      drain(&drain_bar, 0);
+    }
+  } else if (warp >= kFirstConvert) {
+    // -------------------------------------------------------- converters --
+    give_registers<kConvertRegs>();
+    // A thread widens 16 columns of two tokens of each stage. The exponents of
+    // the next kAhead stages are loaded a group ahead.
+    constexpr int kAhead = 4;
+    const int ct = static_cast<int>(threadIdx.x) - 32 * kFirstConvert;
+    const int c = ct & 7, r0 = ct >> 3;
+    const uint32_t cvt0 = mapa_shared(smem_u32(&cvt_bar[0]), 0);
+    uint32_t n = 0;
+    while (ok && work.next(plan, pair, pairs, it)) {
+      int tm, tn;
+      tile_place(plan, it.tile, tm, tn);
+      const int col = tn * kTileN + static_cast<int>(rank) * (tile_cols(args.in, tn) / 2) + 16 * c;
+      const uint8_t* ex = args.ck.ex + col / kCkptBlock;
+      const auto exponent = [&](int k, int h) -> uint32_t {
+        const long long t = static_cast<long long>(k) * kTok + r0 + 32 * h;
+        return k < it.ke && col < args.in && t < args.n ? __ldg(ex + t * args.ck.lde) : kCkptBias;
+      };
+      uint32_t cur[kAhead][2], nxt[kAhead][2];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) cur[j][h] = exponent(it.kb + j, h);
+      for (int k0 = it.kb; k0 < it.ke && ok; k0 += kAhead) {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) nxt[j][h] = exponent(k0 + kAhead + j, h);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          if (k0 + j >= it.ke || !ok) break;
+          const uint32_t s = n % kStages, r = n % kRaw;
+          if (!mbar_wait(&raw_full[r], (n / kRaw) & 1u, abort_flag, args.status) ||
+              !mbar_wait(&empty_bar[s], ((n / kStages) & 1u) ^ 1u, abort_flag, args.status)) {
+            ok = false;
+            break;
+          }
+          uint8_t* b = ring + s * 2 * kOperand + kOperand + (c >> 2) * kBoxBytes;
+          uint4 w[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            w[h] = *reinterpret_cast<const uint4*>(raw + r * kRawBytes + (r0 + 32 * h) * 128 + c * 16);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float f = ckpt_factor(cur[j][h]);
+            const uint32_t in[4] = {w[h].x, w[h].y, w[h].z, w[h].w};
+            uint32_t o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float2 v = unpack_e4m3x2(in[e >> 1] >> (16 * (e & 1)));
+              o[e] = pack_bf16x2(v.x * f, v.y * f);
+            }
+            // The token's 16-byte pieces 2 (c & 3) and the next, at their
+            // swizzled place; lanes of the second box store them the other way
+            // round, so that 8 lanes meet 8 different banks.
+            const int row = r0 + 32 * h;
+            uint4* dst = reinterpret_cast<uint4*>(b + row * 128);
+            const int p = 2 * (c & 3), flip = c >> 2;
+            const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]);
+            const uint4 hi = make_uint4(o[4], o[5], o[6], o[7]);
+            dst[(p + flip) ^ (row & 7)] = flip ? hi : lo;
+            dst[(p + 1 - flip) ^ (row & 7)] = flip ? lo : hi;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&raw_empty[r]);
+            mbar_arrive_cluster(cvt0 + s * 8u);
+          }
+          ++n;
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) cur[j][h] = nxt[j][h];
+      }
+    }
+  } else if (warp >= kFirstEpilogue) {
+    // ---------------------------------------------------------- epilogue --
+    // A thread holds one output's sums over half of the tile's inputs.
+    take_registers<kEpilogueRegs>();
+    const int q = warp & 3;  // TMEM lane quarter of this warp
+    const int half = (warp - kFirstEpilogue) >> 2;
+    const uint32_t tempty0 = mapa_shared(smem_u32(&tempty_bar[0]), 0);
+    uint8_t* const stage = out + (warp - kFirstEpilogue) * kStoreBuf;
+    const uint32_t t0 =
+        tmem_base + (static_cast<uint32_t>(q * 32) << 16) + half * (kTileN / 2);
+    uint32_t seg = 0;
+    while (ok && work.next(plan, pair, pairs, it)) {
+      int tm, tn;
+      tile_place(plan, it.tile, tm, tn);
+      float sum[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) sum[c][j] = 0.f;
+      for (int k = it.kb; k < it.ke; k += kSegment, ++seg) {
+        const uint32_t buf = seg & 1u;
+        if (!mbar_wait(&tfull_bar[buf], (seg >> 1) & 1u, abort_flag, args.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float v[16];
+            tmem_ld16(t0 + buf * kTileN + c * 32 + h * 16, v);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sum[c][16 * h + j] += v[j];
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(tempty0 + buf * 8u);
+      }
+      if (!ok) break;
+      const int lrow = static_cast<int>(rank) * 128 + q * 32 + lane;  // row of the tile
+      const int row0 = tm * kTileM + static_cast<int>(rank) * 128 + q * 32;
+      const int row = row0 + lane;
+      if (row0 >= args.out) continue;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int cb = half * 4 + c;
+        const int i0 = tn * kTileN + cb * 32;
+        if (i0 >= args.in) break;
+        if (it.slot >= 0) {
+          float* p = args.partials + static_cast<long long>(it.slot) * kSlotFloats +
+                     (cb * 8 * kTileM + lrow) * 4;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            st_global_v4(p + j * kTileM * 4, __float_as_uint(sum[c][4 * j]),
+                         __float_as_uint(sum[c][4 * j + 1]), __float_as_uint(sum[c][4 * j + 2]),
+                         __float_as_uint(sum[c][4 * j + 3]));
+          continue;
+        }
+        if (args.add != nullptr && row < args.out) {
+          const float* a = args.add + row * args.ldadd + i0;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (i0 + 4 * j >= args.in) break;
+            const float4 x = *reinterpret_cast<const float4*>(a + 4 * j);
+            sum[c][4 * j] += x.x;
+            sum[c][4 * j + 1] += x.y;
+            sum[c][4 * j + 2] += x.z;
+            sum[c][4 * j + 3] += x.w;
+          }
+        }
+        if (lane == 0) bulk_wait_group_read<0>();  // the last box has been read
+        __syncwarp();
+        uint4* srow = reinterpret_cast<uint4*>(stage + lane * 128);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          srow[j ^ (lane & 7)] =
+              make_uint4(__float_as_uint(sum[c][4 * j]), __float_as_uint(sum[c][4 * j + 1]),
+                         __float_as_uint(sum[c][4 * j + 2]), __float_as_uint(sum[c][4 * j + 3]));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(&map_dw, stage, i0, row0);
+          bulk_commit_group();
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_group<0>();
+  }
+
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem_base, kTmemCols);
+}
+
+// dW of the cut tiles: each tile's pieces added in the order of their tokens,
+// then `add`. Grid: cut tiles x 16 column chunks; a thread per row of the tile.
+__global__ void __launch_bounds__(kTileM) ckpt_wgrad_join_kernel(const WgradArgs args,
+                                                                 const WgradPlan plan) {
+  const int t = static_cast<int>(blockIdx.x);
+  const long long first = static_cast<long long>(t) * plan.kt;
+  const int qa = static_cast<int>(first / plan.per_pair);
+  const int qb = static_cast<int>((first + plan.kt - 1) / plan.per_pair);
+  if (qa == qb) return;  // one piece covered the tile
+  int tm, tn;
+  tile_place(plan, plan.whole + t, tm, tn);
+  const int lrow = static_cast<int>(threadIdx.x);
+  const int row = tm * kTileM + lrow;
+  const int c0 = static_cast<int>(blockIdx.y) * 16;  // column of the tile
+  const int i0 = tn * kTileN + c0;
+  if (row >= args.out || i0 >= args.in) return;
+  float4 v[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int q = qa; q <= qb; ++q) {
+    // A pair's second piece begins with its tile; its first one does not, or
+    // is the first of the pair's part.
+    const int slot = 2 * q + (static_cast<long long>(q) * plan.per_pair < first ? 1 : 0);
+    const float* p = args.partials + static_cast<long long>(slot) * kSlotFloats +
+                     (c0 / 4 * kTileM + lrow) * 4;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 x = *reinterpret_cast<const float4*>(p + j * kTileM * 4);
+      v[j].x += x.x;
+      v[j].y += x.y;
+      v[j].z += x.z;
+      v[j].w += x.w;
+    }
   }
 #pragma unroll
-  for (int p = 0; p < 4; ++p)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int o = o0 + ty + 16 * p, i = i0 + tx + 16 * k;
-      if (o >= a.out || i >= a.in) continue;
-      const float add = a.add != nullptr ? a.add[o * a.ldadd + i] : 0.f;
-      a.dw[o * a.lddw + i] = add + acc[p][k];
+  for (int j = 0; j < 4; ++j) {
+    if (i0 + 4 * j >= args.in) break;
+    if (args.add != nullptr) {
+      const float4 x = *reinterpret_cast<const float4*>(args.add + row * args.ldadd + i0 + 4 * j);
+      v[j].x += x.x;
+      v[j].y += x.y;
+      v[j].z += x.z;
+      v[j].w += x.w;
     }
+    *reinterpret_cast<float4*>(args.dw + row * args.lddw + i0 + 4 * j) = v[j];
+  }
+}
+
+// A launch on `pairs` SM pairs.
+WgradPlan make_plan(long long n, int out, int in, int pairs) {
+  WgradPlan p;
+  p.n_m = (out + kTileM - 1) / kTileM;
+  p.n_n = (in + kTileN - 1) / kTileN;
+  p.kt = static_cast<int>((n + kTok - 1) / kTok);
+  const int tiles = p.n_m * p.n_n;
+  p.cut = tiles % pairs;
+  // Cut the last round's tiles when that saves at least kMinSaved stages of
+  // its length, in pieces of at least kMinPiece.
+  constexpr int kMinSaved = 24, kMinPiece = 8;
+  p.per_pair = 0;
+  if (p.cut > 0) {
+    const long long stages = static_cast<long long>(p.cut) * p.kt;
+    p.per_pair = static_cast<int>(std::max<long long>(kMinPiece, (stages + pairs - 1) / pairs));
+    if (p.kt - p.per_pair < kMinSaved) p.cut = 0;
+  }
+  if (p.cut == 0) p.per_pair = 0;
+  p.whole = tiles - p.cut;
+  return p;
 }
 
 }  // namespace
 
-cudaError_t launch_ckpt_wgrad(const WgradArgs& a, int sms, cudaStream_t st) {
-  (void)sms;
-  LaunchTimer timer("ckpt_wgrad_kernel", st);
-  ckpt_wgrad_kernel<<<dim3((a.in + kTile - 1) / kTile, (a.out + kTile - 1) / kTile), 256, 0, st>>>(a);
-  return cudaGetLastError();
+size_t ckpt_wgrad_workspace(long long n, int out, int in) {
+  const WgradPlan p = make_plan(n, out, in, kRefPairs);
+  return 256 + (p.cut > 0 ? static_cast<size_t>(2) * kRefPairs * kSlotFloats * sizeof(float) : 0);
 }
 
-size_t ckpt_wgrad_workspace(long long n, int out, int in) {
-  (void)n;
-  (void)out;
-  (void)in;
-  return 256;
+cudaError_t prepare_ckpt_wgrad() {
+  return cudaFuncSetAttribute(ckpt_wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              kSmem);
+}
+
+cudaError_t launch_ckpt_wgrad(const WgradArgs& a, int sms, cudaStream_t st) {
+  const int pairs = std::min(sms / 2, kRefPairs);
+  if (pairs < kRefPairs) return cudaErrorNotSupported;  // the workspace's plan is for 76 pairs
+  CUtensorMap map_dy, map_q, map_dw;
+  if (!encode_map_2d(&map_dy, a.dy, a.out, a.n, a.lddy * 2, 64, kTok,
+                     CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, true) ||
+      !encode_map_2d(&map_q, a.ck.q, a.in, a.n, a.ck.ldq, 128, kTok, CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                     false) ||
+      !encode_map_2d(&map_dw, a.dw, a.in, a.out, a.lddw * 4, 32, 32,
+                     CU_TENSOR_MAP_DATA_TYPE_FLOAT32, true))
+    return cudaErrorInvalidValue;
+  const WgradPlan plan = make_plan(a.n, a.out, a.in, pairs);
+  const long long stages = static_cast<long long>(plan.cut) * plan.kt;
+  const int busy = std::max(
+      std::min(plan.whole, pairs),
+      plan.per_pair > 0 ? static_cast<int>((stages + plan.per_pair - 1) / plan.per_pair) : 0);
+  cudaLaunchConfig_t cfg = {};
+  // Whole tiles are dealt to `pairs` pairs: fewer only when one round holds all.
+  cfg.gridDim = dim3(2 * (plan.whole > pairs ? pairs : busy));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e;
+  {
+    LaunchTimer timer("ckpt_wgrad_kernel", st);
+    e = cudaLaunchKernelEx(&cfg, ckpt_wgrad_kernel, map_dy, map_q, map_dw, a, plan);
+  }
+  if (e != cudaSuccess || plan.cut == 0) return e;
+  LaunchTimer timer("ckpt_wgrad_join_kernel", st);
+  ckpt_wgrad_join_kernel<<<dim3(plan.cut, kTileN / 16), kTileM, 0, st>>>(a, plan);
+  return cudaGetLastError();
 }
 
 }  // namespace grpo

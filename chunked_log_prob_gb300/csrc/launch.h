@@ -92,6 +92,13 @@ struct FinishArgs {
 // and gives its SM count; GRPO_OK or a negative status. Defined in api.cu.
 int setup_device(int* sms);
 
+// 2-D tensor map: `inner` contiguous elements per row, `outer` rows `pitch`
+// bytes apart, boxes {box_inner, box_outer}, with the 128-byte swizzle or
+// none; out-of-range elements read as zero. After setup_device.
+bool encode_map_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
+                   uint64_t pitch, uint32_t box_inner, uint32_t box_outer,
+                   CUtensorMapDataType type, bool swizzle);
+
 // An NVTX range around one ABI call (host side: it brackets the enqueueing of
 // the call's launches), so that profilers can attribute the kernels to it.
 class CallRange {
@@ -171,6 +178,7 @@ cudaError_t prepare_gemm_variant() {
 // ctas selects the single-CTA (1) or CTA-pair (2) variant.
 cudaError_t prepare_fwd_gemm();   // opt-in to the large dynamic smem
 cudaError_t prepare_bwd_gemms();
+cudaError_t prepare_ckpt_wgrad();
 cudaError_t launch_fwd_gemm(int ctas, const CUtensorMap& map_a, const CUtensorMap& map_b,
                             const CUtensorMap& map_h16,
                             const TileArgs& args, int grid, cudaStream_t stream,
