@@ -12,7 +12,7 @@ namespace grpo {
 CkptLayout ckpt_layout(long long n, int hidden) {
   CkptLayout l;
   l.ldq = (hidden + 15LL) / 16 * 16;
-  l.lde = ((hidden + kCkptBlock - 1LL) / kCkptBlock + 3) / 4 * 4;
+  l.lde = ((hidden + kCkptBlock - 1LL) / kCkptBlock + 15) / 16 * 16;
   l.off_ex = (static_cast<size_t>(n) * l.ldq + 255) / 256 * 256;
   l.total = l.off_ex + (static_cast<size_t>(n) * l.lde + 255) / 256 * 256;
   return l;

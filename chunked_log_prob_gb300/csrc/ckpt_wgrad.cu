@@ -27,15 +27,19 @@ namespace {
 constexpr int kTileM = 256;        // outputs of a pair's tile, 128 per CTA
 constexpr int kTileN = 256;        // inputs of a pair's tile
 constexpr int kTok = 64;           // tokens of a stage
-constexpr int kStages = 5;         // operand ring: dY tile and widened X tile
-constexpr int kRaw = 4;            // ring of e4m3 tiles
+constexpr int kStages = 4;         // operand ring: dY tile and widened X tile
+constexpr int kRaw = 6;            // ring of e4m3 tiles with their exponents
 constexpr int kBoxBytes = kTok * 128;      // 64 tokens x 64 bf16 columns
 constexpr int kOperand = 2 * kBoxBytes;    // a CTA's 128 outputs, or 128 inputs
-constexpr int kRawBytes = kTok * 128;      // 64 tokens x 128 e4m3
+constexpr int kRawQ = kTok * 128;          // 64 tokens x 128 e4m3
+constexpr int kRawBytes = kRawQ + kTok * 16;  // and 16 exponents, ours among them
 constexpr int kStoreBuf = 32 * 128;        // 32 x 32 fp32 on its way out
 constexpr int kSegment = 16;       // stages summed in TMEM: 1024 tokens
-// Warps: 0 TMA, 1 MMA, 2-3 idle, then two warpgroups of each of these.
+// Warps: 0 dY by TMA, 1 MMA, 2 the checkpoint by TMA, 3 idle, then two
+// warpgroups of each of these. The converters' warpgroups take turns with the
+// stages, so that one's waits and fences lie beside the other's work.
 constexpr int kEpilogueWarps = 8, kConvertWarps = 8;
+constexpr int kConvertGroup = 4;  // warps that share a stage
 constexpr int kFirstEpilogue = 4, kFirstConvert = kFirstEpilogue + kEpilogueWarps;
 constexpr int kThreads = 32 * (kFirstConvert + kConvertWarps);
 // Registers of a thread: 96 at launch (640 x 96 = 61440), moved to the epilogue,
@@ -128,9 +132,41 @@ __device__ __forceinline__ void give_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// 16 e4m3 of a block with the exponent byte `e` to 16 bf16, exactly. Where 2^k
+// is an fp16 (k in [-24, 15]: the usual activations), a value costs one mixed
+// multiply-add of two fp16 into fp32 (two operations fewer a pair).
+__device__ __forceinline__ void widen16(const uint4& w, uint32_t e, uint32_t (&o)[8]) {
+  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+  const float f = ckpt_factor(e);
+  if (e - 103u <= 39u || (w.x | w.y | w.z | w.w) == 0u) {
+    uint16_t f16;
+    asm("cvt.rn.f16.f32 %0, %1;" : "=h"(f16) : "f"(f));
+    if (e - 103u > 39u) f16 = 0;  // all values are 0
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float lo, hi;
+      asm("{\n\t.reg .b32 t;\n\t.reg .b16 l, h;\n\t"
+          "cvt.rn.f16x2.e4m3x2 t, %2;\n\t"
+          "mov.b32 {l, h}, t;\n\t"
+          "fma.rn.f32.f16 %0, l, %3, %4;\n\t"
+          "fma.rn.f32.f16 %1, h, %3, %4;\n\t}"
+          : "=f"(lo), "=f"(hi)
+          : "h"(static_cast<uint16_t>(in[j >> 1] >> (16 * (j & 1)))), "h"(f16), "f"(0.f));
+      o[j] = pack_bf16x2(lo, hi);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float2 v = unpack_e4m3x2(in[j >> 1] >> (16 * (j & 1)));
+      o[j] = pack_bf16x2(v.x * f, v.y * f);
+    }
+  }
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
     ckpt_wgrad_kernel(const __grid_constant__ CUtensorMap map_dy,
                       const __grid_constant__ CUtensorMap map_q,
+                      const __grid_constant__ CUtensorMap map_ex,
                       const __grid_constant__ CUtensorMap map_dw, const WgradArgs args,
                       const WgradPlan plan) {
   extern __shared__ uint8_t smem_raw[];
@@ -157,12 +193,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full_bar[s], 2);
-      mbar_init(&cvt_bar[s], 2 * kConvertWarps);
+      mbar_init(&cvt_bar[s], 2 * kConvertGroup);
       mbar_init(&empty_bar[s], 1);
     }
     for (int s = 0; s < kRaw; ++s) {
       mbar_init(&raw_full[s], 1);
-      mbar_init(&raw_empty[s], kConvertWarps);
+      mbar_init(&raw_empty[s], kConvertGroup);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull_bar[b], 1);
@@ -175,6 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&map_dy);
     tma_prefetch_desc(&map_q);
+    tma_prefetch_desc(&map_ex);
     tma_prefetch_desc(&map_dw);
   }
   if (warp == 1) {
@@ -192,23 +229,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < kFirstEpilogue) give_registers<kControlRegs>();
   if (warp == 0) {
-    // ------------------------------------------------------ TMA producer --
+    // ---------------------------------------------------- dY's tiles by TMA --
     if (lane == 0) {
       uint32_t n = 0;  // stages issued
       while (ok && work.next(plan, pair, pairs, it)) {
         int tm, tn;
         tile_place(plan, it.tile, tm, tn);
         const int o0 = tm * kTileM + static_cast<int>(rank) * (kTileM / 2);
-        const int i0 = tn * kTileN + static_cast<int>(rank) * (tile_cols(args.in, tn) / 2);
         for (int k = it.kb; k < it.ke; ++k, ++n) {
-          const uint32_t s = n % kStages, r = n % kRaw;
-          if (!mbar_wait(&empty_bar[s], ((n / kStages) & 1u) ^ 1u, abort_flag, args.status) ||
-              !mbar_wait(&raw_empty[r], ((n / kRaw) & 1u) ^ 1u, abort_flag, args.status)) {
+          const uint32_t s = n % kStages;
+          if (!mbar_wait(&empty_bar[s], ((n / kStages) & 1u) ^ 1u, abort_flag, args.status)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&raw_full[r], kRawBytes);
-          tma_load_2d(raw + r * kRawBytes, &map_q, &raw_full[r], i0, k * kTok);
           const uint32_t lead = mapa_shared(smem_u32(&full_bar[s]), 0);
           mbar_arrive_expect_tx_cluster(lead, kOperand);
           uint8_t* a = ring + s * 2 * kOperand;
@@ -216,15 +249,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_2d_pair_nohint(a + kBoxBytes, &map_dy, lead, o0 + 64, k * kTok);
         }
       }
-      if (!ok) {
-        // Let the copies in flight land before the CTA exits (the peer passes
-        // the closing cluster barrier only after this).
+      // After a timeout: let the copies in flight land before the CTA exits
+      // (the peer passes the closing cluster barrier only after this).
+      if (!ok && rank == 0)
+        for (uint32_t j = n >= kStages ? n - kStages : 0; j < n; ++j)
+          drain(&full_bar[j % kStages], (j / kStages) & 1u);
+    }
+  } else if (warp == 2) {
+    // ---------------------------------------------- checkpoint tiles by TMA --
+    if (lane == 0) {
+      uint32_t n = 0;
+      while (ok && work.next(plan, pair, pairs, it)) {
+        int tm, tn;
+        tile_place(plan, it.tile, tm, tn);
+        const int i0 = tn * kTileN + static_cast<int>(rank) * (tile_cols(args.in, tn) / 2);
+        // Exponents come 16 at a time (a TMA copy starts on 16 bytes).
+        const int x0 = (i0 / kCkptBlock) & ~15;
+        for (int k = it.kb; k < it.ke; ++k, ++n) {
+          const uint32_t r = n % kRaw;
+          if (!mbar_wait(&raw_empty[r], ((n / kRaw) & 1u) ^ 1u, abort_flag, args.status)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&raw_full[r], kRawBytes);
+          tma_load_2d(raw + r * kRawBytes, &map_q, &raw_full[r], i0, k * kTok);
+          tma_load_2d(raw + r * kRawBytes + kRawQ, &map_ex, &raw_full[r], x0, k * kTok);
+        }
+      }
+      if (!ok)
         for (uint32_t j = n >= kRaw ? n - kRaw : 0; j < n; ++j)
           drain(&raw_full[j % kRaw], (j / kRaw) & 1u);
-        if (rank == 0)
-          for (uint32_t j = n >= kStages ? n - kStages : 0; j < n; ++j)
-            drain(&full_bar[j % kStages], (j / kStages) & 1u);
-      }
     }
   } else if (warp == 1) {
     // -------------------------------------------------------- MMA issuer --
@@ -270,79 +324,50 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= kFirstConvert) {
     // -------------------------------------------------------- converters --
     give_registers<kConvertRegs>();
-    // A thread widens 16 columns of two tokens of each stage. The exponents of
-    // the next kAhead stages are loaded a group ahead.
-    constexpr int kAhead = 4;
-    const int ct = static_cast<int>(threadIdx.x) - 32 * kFirstConvert;
+    // A thread widens 16 columns of four tokens of every second stage.
+    const int ct = (static_cast<int>(threadIdx.x) - 32 * kFirstConvert) & 127;
+    const uint32_t group = (warp - kFirstConvert) / kConvertGroup;
     const int c = ct & 7, r0 = ct >> 3;
     const uint32_t cvt0 = mapa_shared(smem_u32(&cvt_bar[0]), 0);
     uint32_t n = 0;
     while (ok && work.next(plan, pair, pairs, it)) {
       int tm, tn;
       tile_place(plan, it.tile, tm, tn);
-      const int col = tn * kTileN + static_cast<int>(rank) * (tile_cols(args.in, tn) / 2) + 16 * c;
-      const uint8_t* ex = args.ck.ex + col / kCkptBlock;
-      const auto exponent = [&](int k, int h) -> uint32_t {
-        const long long t = static_cast<long long>(k) * kTok + r0 + 32 * h;
-        return k < it.ke && col < args.in && t < args.n ? __ldg(ex + t * args.ck.lde) : kCkptBias;
-      };
-      uint32_t cur[kAhead][2], nxt[kAhead][2];
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) cur[j][h] = exponent(it.kb + j, h);
-      for (int k0 = it.kb; k0 < it.ke && ok; k0 += kAhead) {
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) nxt[j][h] = exponent(k0 + kAhead + j, h);
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-          if (k0 + j >= it.ke || !ok) break;
-          const uint32_t s = n % kStages, r = n % kRaw;
-          if (!mbar_wait(&raw_full[r], (n / kRaw) & 1u, abort_flag, args.status) ||
-              !mbar_wait(&empty_bar[s], ((n / kStages) & 1u) ^ 1u, abort_flag, args.status)) {
-            ok = false;
-            break;
-          }
-          uint8_t* b = ring + s * 2 * kOperand + kOperand + (c >> 2) * kBoxBytes;
-          uint4 w[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            w[h] = *reinterpret_cast<const uint4*>(raw + r * kRawBytes + (r0 + 32 * h) * 128 + c * 16);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float f = ckpt_factor(cur[j][h]);
-            const uint32_t in[4] = {w[h].x, w[h].y, w[h].z, w[h].w};
-            uint32_t o[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float2 v = unpack_e4m3x2(in[e >> 1] >> (16 * (e & 1)));
-              o[e] = pack_bf16x2(v.x * f, v.y * f);
-            }
-            // The token's 16-byte pieces 2 (c & 3) and the next, at their
-            // swizzled place; lanes of the second box store them the other way
-            // round, so that 8 lanes meet 8 different banks.
-            const int row = r0 + 32 * h;
-            uint4* dst = reinterpret_cast<uint4*>(b + row * 128);
-            const int p = 2 * (c & 3), flip = c >> 2;
-            const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]);
-            const uint4 hi = make_uint4(o[4], o[5], o[6], o[7]);
-            dst[(p + flip) ^ (row & 7)] = flip ? hi : lo;
-            dst[(p + 1 - flip) ^ (row & 7)] = flip ? lo : hi;
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&raw_empty[r]);
-            mbar_arrive_cluster(cvt0 + s * 8u);
-          }
-          ++n;
+      const int i0 = tn * kTileN + static_cast<int>(rank) * (tile_cols(args.in, tn) / 2);
+      const int x = ((i0 / kCkptBlock) & 15) + (c >> 1);  // our exponent of the 16
+      for (int k = it.kb; k < it.ke; ++k, ++n) {
+        if ((n & 1u) != group) continue;
+        const uint32_t s = n % kStages, r = n % kRaw;
+        if (!mbar_wait(&raw_full[r], (n / kRaw) & 1u, abort_flag, args.status) ||
+            !mbar_wait(&empty_bar[s], ((n / kStages) & 1u) ^ 1u, abort_flag, args.status)) {
+          ok = false;
+          break;
         }
+        const uint8_t* src = raw + r * kRawBytes;
+        uint8_t* b = ring + s * 2 * kOperand + kOperand + (c >> 2) * kBoxBytes;
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) cur[j][h] = nxt[j][h];
+        for (int h = 0; h < 4; ++h) {
+          const int row = r0 + 16 * h;
+          const uint4 w = *reinterpret_cast<const uint4*>(src + row * 128 + c * 16);
+          const uint32_t e = src[kRawQ + row * 16 + x];
+          uint32_t o[8];
+          widen16(w, e, o);
+          // The token's 16-byte pieces 2 (c & 3) and the next, at their
+          // swizzled place; lanes of the second box store them the other way
+          // round, so that 8 lanes meet 8 different banks.
+          uint4* dst = reinterpret_cast<uint4*>(b + row * 128);
+          const int p = 2 * (c & 3), flip = c >> 2;
+          const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]);
+          const uint4 hi = make_uint4(o[4], o[5], o[6], o[7]);
+          dst[(p + flip) ^ (row & 7)] = flip ? hi : lo;
+          dst[(p + 1 - flip) ^ (row & 7)] = flip ? lo : hi;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&raw_empty[r]);
+          mbar_arrive_cluster(cvt0 + s * 8u);
+        }
       }
     }
   } else if (warp >= kFirstEpilogue) {
@@ -528,11 +553,13 @@ cudaError_t prepare_ckpt_wgrad() {
 cudaError_t launch_ckpt_wgrad(const WgradArgs& a, int sms, cudaStream_t st) {
   const int pairs = std::min(sms / 2, kRefPairs);
   if (pairs < kRefPairs) return cudaErrorNotSupported;  // the workspace's plan is for 76 pairs
-  CUtensorMap map_dy, map_q, map_dw;
+  CUtensorMap map_dy, map_q, map_ex, map_dw;
   if (!encode_map_2d(&map_dy, a.dy, a.out, a.n, a.lddy * 2, 64, kTok,
                      CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, true) ||
       !encode_map_2d(&map_q, a.ck.q, a.in, a.n, a.ck.ldq, 128, kTok, CU_TENSOR_MAP_DATA_TYPE_UINT8,
                      false) ||
+      !encode_map_2d(&map_ex, a.ck.ex, a.ck.lde, a.n, a.ck.lde, 16, kTok,
+                     CU_TENSOR_MAP_DATA_TYPE_UINT8, false) ||
       !encode_map_2d(&map_dw, a.dw, a.in, a.out, a.lddw * 4, 32, 32,
                      CU_TENSOR_MAP_DATA_TYPE_FLOAT32, true))
     return cudaErrorInvalidValue;
@@ -557,7 +584,7 @@ cudaError_t launch_ckpt_wgrad(const WgradArgs& a, int sms, cudaStream_t st) {
   cudaError_t e;
   {
     LaunchTimer timer("ckpt_wgrad_kernel", st);
-    e = cudaLaunchKernelEx(&cfg, ckpt_wgrad_kernel, map_dy, map_q, map_dw, a, plan);
+    e = cudaLaunchKernelEx(&cfg, ckpt_wgrad_kernel, map_dy, map_q, map_ex, map_dw, a, plan);
   }
   if (e != cudaSuccess || plan.cut == 0) return e;
   LaunchTimer timer("ckpt_wgrad_join_kernel", st);

@@ -20,7 +20,7 @@ struct CkptLayout {
   long long ldq, lde;
   size_t off_ex, total;
 };
-// ldq: D up to 16 (a TMA row stride); lde: a byte per 32 columns, up to 4.
+// ldq: D up to 16; lde: a byte per 32 columns, up to 16 (TMA row strides).
 CkptLayout ckpt_layout(long long n, int hidden);
 CkptView ckpt_view(const void* buf, long long n, int hidden);
 

@@ -536,6 +536,24 @@ def test_wgrad_in_place_and_repeatable(clp):
         assert torch.equal(acc, want)
 
 
+def test_wgrad_exponents_of_every_size(clp):
+    # Blocks from 2^-100 to 2^100: each of them is widened exactly, whichever
+    # way its exponent takes on chip, with blocks of zeros among them.
+    g = torch.Generator().manual_seed(3)
+    n, out, d = 130, 24, 1024
+    size = torch.randint(-100, 101, (n, d // 32), generator=g).double()
+    size[5], size[:, 7] = -130, -140  # below the smallest exponent: zeros
+    x = (torch.randn(n, d, generator=g).double() * torch.exp2(size).repeat_interleave(32, 1)).bfloat16()
+    dy = torch.zeros(n, out, dtype=torch.bfloat16)
+    dy[torch.arange(n), torch.arange(n) % out] = 1.0  # few terms in each sum
+    c = clp.grpo_ckpt_pack(x.to(DEV))
+    got = clp.grpo_ckpt_wgrad(dy.to(DEV), c)
+    q, ex = o.ckpt_pack(f64(x), float(torch.finfo(torch.bfloat16).max))
+    x64 = o.ckpt_expand(q, ex)
+    mag = np.abs(f64(dy)).T @ np.abs(x64)
+    check("dW", got, f64(dy).T @ x64, 8 * 2 * E * mag)  # 6 terms
+
+
 def test_wgrad_nan_reaches_only_its_columns(clp):
     x = rand(torch.Generator().manual_seed(0), 100, 64, torch.bfloat16).to(DEV)
     x[50, 9] = float("nan")
