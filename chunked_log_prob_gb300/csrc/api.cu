@@ -733,7 +733,7 @@ bool encode_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t oute
                CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                uint64_t elem_bytes = 2) {
   return encode_map_2d(map, base, inner, outer, pitch_elems * elem_bytes, box_inner, box_outer,
-                       type, true);
+                       type, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 struct Ws {
@@ -1631,15 +1631,13 @@ int setup_device(int* sms) { return device_setup(sms); }
 
 bool encode_map_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
                    uint64_t pitch, uint32_t box_inner, uint32_t box_outer,
-                   CUtensorMapDataType type, bool swizzle) {
+                   CUtensorMapDataType type, CUtensorMapSwizzle swizzle) {
   cuuint64_t dims[2] = {inner, outer};
   cuuint64_t strides[1] = {pitch};
   cuuint32_t box[2] = {box_inner, box_outer};
   cuuint32_t estr[2] = {1, 1};
   CUresult r = g_encode(map, type, 2, const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 

@@ -27,13 +27,16 @@ namespace {
 constexpr int kTileM = 256;        // outputs of a pair's tile, 128 per CTA
 constexpr int kTileN = 256;        // inputs of a pair's tile
 constexpr int kTok = 64;           // tokens of a stage
-constexpr int kStages = 4;         // operand ring: dY tile and widened X tile
-constexpr int kRaw = 6;            // ring of e4m3 tiles with their exponents
+// Rings: a slot's way round (barrier to barrier, TMA or widening, the MMAs)
+// takes several stages' MMA time, so each of them is as deep as memory allows.
+constexpr int kDy = 6;             // dY tiles
+constexpr int kX = 4;              // widened X tiles
+constexpr int kRaw = 5;            // e4m3 tiles with their exponents
 constexpr int kBoxBytes = kTok * 128;      // 64 tokens x 64 bf16 columns
 constexpr int kOperand = 2 * kBoxBytes;    // a CTA's 128 outputs, or 128 inputs
 constexpr int kRawQ = kTok * 128;          // 64 tokens x 128 e4m3
 constexpr int kRawBytes = kRawQ + kTok * 16;  // and 16 exponents, ours among them
-constexpr int kStoreBuf = 32 * 128;        // 32 x 32 fp32 on its way out
+constexpr int kStoreBuf = 32 * 64;         // 32 x 16 fp32 on its way out
 constexpr int kSegment = 16;       // stages summed in TMEM: 1024 tokens
 // Warps: 0 dY by TMA, 1 MMA, 2 the checkpoint by TMA, 3 idle, then two
 // warpgroups of each of these. The converters' warpgroups take turns with the
@@ -43,13 +46,13 @@ constexpr int kConvertGroup = 4;  // warps that share a stage
 constexpr int kFirstEpilogue = 4, kFirstConvert = kFirstEpilogue + kEpilogueWarps;
 constexpr int kThreads = 32 * (kFirstConvert + kConvertWarps);
 // Registers of a thread: 96 at launch (640 x 96 = 61440), moved to the epilogue,
-// whose threads hold 128 sums: 128 x 32 + 256 x 168 + 256 x 56 = 61440.
-constexpr int kLaunchRegs = 96, kControlRegs = 32, kEpilogueRegs = 168, kConvertRegs = 56;
+// whose threads hold 128 sums: 128 x 32 + 256 x 160 + 256 x 64 = 61440.
+constexpr int kLaunchRegs = 96, kControlRegs = 32, kEpilogueRegs = 160, kConvertRegs = 64;
 static_assert(128 * kControlRegs + 32 * kEpilogueWarps * kEpilogueRegs +
                       32 * kConvertWarps * kConvertRegs <=
                   kThreads * kLaunchRegs,
               "registers of a CTA");
-constexpr int kSmem = 1024 + kStages * 2 * kOperand + kRaw * kRawBytes +
+constexpr int kSmem = 1024 + (kDy + kX) * kOperand + kRaw * kRawBytes +
                       kEpilogueWarps * kStoreBuf;
 constexpr uint32_t kTmemCols = 512;
 static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
@@ -123,6 +126,20 @@ __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
     if (clock64() - t0 > kWaitLimitCycles) return;
 }
 
+// True in one lane of the (whole) warp. The compiler then knows that one thread
+// runs what follows and feeds tcgen05 and TMA their uniform operands directly;
+// behind `lane == 0` it cannot, and a stage took its issuing thread twice as
+// long as the tensor core (16384 x 4096 x 4096: 518 us against 407).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\t"
+      "elect.sync _|P, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, P;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 template <int N>
 __device__ __forceinline__ void take_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -170,11 +187,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap map_dw, const WgradArgs args,
                       const WgradPlan plan) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full_bar[kStages];   // leader: both CTAs' dY tiles landed
-  __shared__ __align__(8) uint64_t cvt_bar[kStages];    // leader: both CTAs' X tiles widened
-  __shared__ __align__(8) uint64_t empty_bar[kStages];  // the stage's MMAs are done
-  __shared__ __align__(8) uint64_t raw_full[kRaw];      // this CTA's e4m3 tile landed
-  __shared__ __align__(8) uint64_t raw_empty[kRaw];     // its converter warps have read it
+  // By stage, in turns of kDy. The X ring is shorter: a converter waits for the
+  // MMAs of the stage kX before its own, whose barrier cannot go round again
+  // before that stage's X tile is there.
+  __shared__ __align__(8) uint64_t full_bar[kDy];  // leader: both CTAs' dY and X tiles are there
+  __shared__ __align__(8) uint64_t done_bar[kDy];  // the stage's MMAs are done
+  __shared__ __align__(8) uint64_t raw_full[kRaw];   // this CTA's e4m3 tile landed
+  __shared__ __align__(8) uint64_t raw_empty[kRaw];  // its converter warps have read it
   __shared__ __align__(8) uint64_t tfull_bar[2], tempty_bar[2];
   __shared__ __align__(8) uint64_t drain_bar;
   __shared__ uint32_t tmem_base_sh;
@@ -182,7 +201,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* const ring = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
-  uint8_t* const raw = ring + kStages * 2 * kOperand;
+  uint8_t* const xring = ring + kDy * kOperand;
+  uint8_t* const raw = xring + kX * kOperand;
   uint8_t* const out = raw + kRaw * kRawBytes;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -191,10 +211,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = &abort_sh;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full_bar[s], 2);
-      mbar_init(&cvt_bar[s], 2 * kConvertGroup);
-      mbar_init(&empty_bar[s], 1);
+    for (int s = 0; s < kDy; ++s) {
+      mbar_init(&full_bar[s], 2 + 2 * kConvertGroup);  // dY's TMA threads, converter warps
+      mbar_init(&done_bar[s], 1);
     }
     for (int s = 0; s < kRaw; ++s) {
       mbar_init(&raw_full[s], 1);
@@ -230,34 +249,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < kFirstEpilogue) give_registers<kControlRegs>();
   if (warp == 0) {
     // ---------------------------------------------------- dY's tiles by TMA --
-    if (lane == 0) {
+    if (elect_one()) {
       uint32_t n = 0;  // stages issued
       while (ok && work.next(plan, pair, pairs, it)) {
         int tm, tn;
         tile_place(plan, it.tile, tm, tn);
         const int o0 = tm * kTileM + static_cast<int>(rank) * (kTileM / 2);
         for (int k = it.kb; k < it.ke; ++k, ++n) {
-          const uint32_t s = n % kStages;
-          if (!mbar_wait(&empty_bar[s], ((n / kStages) & 1u) ^ 1u, abort_flag, args.status)) {
+          const uint32_t s = n % kDy;
+          if (!mbar_wait(&done_bar[s], ((n / kDy) & 1u) ^ 1u, abort_flag, args.status)) {
             ok = false;
             break;
           }
           const uint32_t lead = mapa_shared(smem_u32(&full_bar[s]), 0);
           mbar_arrive_expect_tx_cluster(lead, kOperand);
-          uint8_t* a = ring + s * 2 * kOperand;
+          uint8_t* a = ring + s * kOperand;
           tma_load_2d_pair_nohint(a, &map_dy, lead, o0, k * kTok);
           tma_load_2d_pair_nohint(a + kBoxBytes, &map_dy, lead, o0 + 64, k * kTok);
         }
       }
-      // After a timeout: let the copies in flight land before the CTA exits
-      // (the peer passes the closing cluster barrier only after this).
+      // After a timeout: let the copies in flight land before the CTA exits (the
+      // peer passes the closing cluster barrier only after this). Their barriers
+      // also wait for converters that may have given up: the drain ends by its
+      // own limit then, long after any copy.
       if (!ok && rank == 0)
-        for (uint32_t j = n >= kStages ? n - kStages : 0; j < n; ++j)
-          drain(&full_bar[j % kStages], (j / kStages) & 1u);
+        for (uint32_t j = n >= kDy ? n - kDy : 0; j < n; ++j)
+          drain(&full_bar[j % kDy], (j / kDy) & 1u);
     }
   } else if (warp == 2) {
     // ---------------------------------------------- checkpoint tiles by TMA --
-    if (lane == 0) {
+    if (elect_one()) {
       uint32_t n = 0;
       while (ok && work.next(plan, pair, pairs, it)) {
         int tm, tn;
@@ -282,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // -------------------------------------------------------- MMA issuer --
-    if (lane == 0 && rank == 0) {
+    if (rank == 0 && elect_one()) {
       uint32_t n = 0, seg = 0;  // stages, segments issued
       while (ok && work.next(plan, pair, pairs, it)) {
         int tm, tn;
@@ -297,21 +318,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           const uint32_t d = tmem_base + buf * kTileN;
-          const uint32_t s = n % kStages, parity = (n / kStages) & 1u;
-          if (!mbar_wait(&full_bar[s], parity, abort_flag, args.status) ||
-              !mbar_wait(&cvt_bar[s], parity, abort_flag, args.status)) {
+          const uint32_t sa = n % kDy;
+          if (!mbar_wait(&full_bar[sa], (n / kDy) & 1u, abort_flag, args.status)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a = smem_u32(ring + s * 2 * kOperand), b = a + kOperand;
+          const uint32_t a = smem_u32(ring + sa * kOperand);
+          const uint32_t b = smem_u32(xring + n % kX * kOperand);
 #pragma unroll
           for (int kk = 0; kk < kTok / 16; ++kk)
             // 64-wide blocks of outputs or inputs 8 KB apart, 8 tokens 1 KB.
             tc_mma_bf16_pair(d, sdesc_sw128(a + kk * 2048, kBoxBytes, 1024),
                              sdesc_sw128(b + kk * 2048, kBoxBytes, 1024), idesc,
                              first && kk == 0 ? 0u : 1u);
-          tc_commit_pair_multicast(&empty_bar[s], 0x3);
+          tc_commit_pair_multicast(&done_bar[sa], 0x3);
           if ((k - it.kb) % kSegment == kSegment - 1 || k == it.ke - 1) {
             tc_commit_pair_multicast(&tfull_bar[buf], 0x3);
             ++seg;
@@ -328,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ct = (static_cast<int>(threadIdx.x) - 32 * kFirstConvert) & 127;
     const uint32_t group = (warp - kFirstConvert) / kConvertGroup;
     const int c = ct & 7, r0 = ct >> 3;
-    const uint32_t cvt0 = mapa_shared(smem_u32(&cvt_bar[0]), 0);
+    const uint32_t full0 = mapa_shared(smem_u32(&full_bar[0]), 0);
     uint32_t n = 0;
     while (ok && work.next(plan, pair, pairs, it)) {
       int tm, tn;
@@ -337,28 +358,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int x = ((i0 / kCkptBlock) & 15) + (c >> 1);  // our exponent of the 16
       for (int k = it.kb; k < it.ke; ++k, ++n) {
         if ((n & 1u) != group) continue;
-        const uint32_t s = n % kStages, r = n % kRaw;
-        if (!mbar_wait(&raw_full[r], (n / kRaw) & 1u, abort_flag, args.status) ||
-            !mbar_wait(&empty_bar[s], ((n / kStages) & 1u) ^ 1u, abort_flag, args.status)) {
+        const uint32_t r = n % kRaw;
+        if (!mbar_wait(&raw_full[r], (n / kRaw) & 1u, abort_flag, args.status)) {
           ok = false;
           break;
         }
         const uint8_t* src = raw + r * kRawBytes;
-        uint8_t* b = ring + s * 2 * kOperand + kOperand + (c >> 2) * kBoxBytes;
+        uint32_t o[4][8];
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
           const int row = r0 + 16 * h;
-          const uint4 w = *reinterpret_cast<const uint4*>(src + row * 128 + c * 16);
-          const uint32_t e = src[kRawQ + row * 16 + x];
-          uint32_t o[8];
-          widen16(w, e, o);
+          widen16(*reinterpret_cast<const uint4*>(src + row * 128 + c * 16),
+                  src[kRawQ + row * 16 + x], o[h]);
+        }
+        // Widened before the slot is waited for: only the stores, the fence and
+        // the barriers lie on the slot's way round.
+        if (n >= kX && !mbar_wait(&done_bar[(n - kX) % kDy], ((n - kX) / kDy) & 1u, abort_flag,
+                                  args.status)) {
+          ok = false;
+          break;
+        }
+        uint8_t* b = xring + n % kX * kOperand + (c >> 2) * kBoxBytes;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
           // The token's 16-byte pieces 2 (c & 3) and the next, at their
           // swizzled place; lanes of the second box store them the other way
           // round, so that 8 lanes meet 8 different banks.
+          const int row = r0 + 16 * h;
           uint4* dst = reinterpret_cast<uint4*>(b + row * 128);
           const int p = 2 * (c & 3), flip = c >> 2;
-          const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]);
-          const uint4 hi = make_uint4(o[4], o[5], o[6], o[7]);
+          const uint4 lo = make_uint4(o[h][0], o[h][1], o[h][2], o[h][3]);
+          const uint4 hi = make_uint4(o[h][4], o[h][5], o[h][6], o[h][7]);
           dst[(p + flip) ^ (row & 7)] = flip ? hi : lo;
           dst[(p + 1 - flip) ^ (row & 7)] = flip ? lo : hi;
         }
@@ -366,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&raw_empty[r]);
-          mbar_arrive_cluster(cvt0 + s * 8u);
+          mbar_arrive_cluster(full0 + n % kDy * 8u);
         }
       }
     }
@@ -399,11 +429,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float v[16];
-            tmem_ld16(t0 + buf * kTileN + c * 32 + h * 16, v);
+          for (int h = 0; h < 4; ++h) {
+            float v[8];
+            tmem_ld8(t0 + buf * kTileN + c * 32 + h * 8, v);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) sum[c][16 * h + j] += v[j];
+            for (int j = 0; j < 8; ++j) sum[c][8 * h + j] += v[j];
           }
         }
         tc_fence_before();
@@ -442,19 +472,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             sum[c][4 * j + 3] += x.w;
           }
         }
-        if (lane == 0) bulk_wait_group_read<0>();  // the last box has been read
-        __syncwarp();
-        uint4* srow = reinterpret_cast<uint4*>(stage + lane * 128);
+        // Two boxes of 16 inputs, through the 64-byte swizzle.
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          srow[j ^ (lane & 7)] =
-              make_uint4(__float_as_uint(sum[c][4 * j]), __float_as_uint(sum[c][4 * j + 1]),
-                         __float_as_uint(sum[c][4 * j + 2]), __float_as_uint(sum[c][4 * j + 3]));
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_2d(&map_dw, stage, i0, row0);
-          bulk_commit_group();
+        for (int h = 0; h < 2; ++h) {
+          if (i0 + 16 * h >= args.in) break;
+          if (lane == 0) bulk_wait_group_read<0>();  // the last box has been read
+          __syncwarp();
+          uint4* srow = reinterpret_cast<uint4*>(stage + lane * 64);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float* v = &sum[c][16 * h + 4 * j];
+            srow[j ^ ((lane >> 1) & 3)] =
+                make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                           __float_as_uint(v[3]));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&map_dw, stage, i0 + 16 * h, row0);
+            bulk_commit_group();
+          }
         }
       }
     }
@@ -555,13 +592,13 @@ cudaError_t launch_ckpt_wgrad(const WgradArgs& a, int sms, cudaStream_t st) {
   if (pairs < kRefPairs) return cudaErrorNotSupported;  // the workspace's plan is for 76 pairs
   CUtensorMap map_dy, map_q, map_ex, map_dw;
   if (!encode_map_2d(&map_dy, a.dy, a.out, a.n, a.lddy * 2, 64, kTok,
-                     CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, true) ||
+                     CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_map_2d(&map_q, a.ck.q, a.in, a.n, a.ck.ldq, 128, kTok, CU_TENSOR_MAP_DATA_TYPE_UINT8,
-                     false) ||
+                     CU_TENSOR_MAP_SWIZZLE_NONE) ||
       !encode_map_2d(&map_ex, a.ck.ex, a.ck.lde, a.n, a.ck.lde, 16, kTok,
-                     CU_TENSOR_MAP_DATA_TYPE_UINT8, false) ||
-      !encode_map_2d(&map_dw, a.dw, a.in, a.out, a.lddw * 4, 32, 32,
-                     CU_TENSOR_MAP_DATA_TYPE_FLOAT32, true))
+                     CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !encode_map_2d(&map_dw, a.dw, a.in, a.out, a.lddw * 4, 16, 32,
+                     CU_TENSOR_MAP_DATA_TYPE_FLOAT32, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
   const WgradPlan plan = make_plan(a.n, a.out, a.in, pairs);
   const long long stages = static_cast<long long>(plan.cut) * plan.kt;

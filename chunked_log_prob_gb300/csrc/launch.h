@@ -93,11 +93,11 @@ struct FinishArgs {
 int setup_device(int* sms);
 
 // 2-D tensor map: `inner` contiguous elements per row, `outer` rows `pitch`
-// bytes apart, boxes {box_inner, box_outer}, with the 128-byte swizzle or
-// none; out-of-range elements read as zero. After setup_device.
+// bytes apart, boxes {box_inner, box_outer}; out-of-range elements read as
+// zero. After setup_device.
 bool encode_map_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
                    uint64_t pitch, uint32_t box_inner, uint32_t box_outer,
-                   CUtensorMapDataType type, bool swizzle);
+                   CUtensorMapDataType type, CUtensorMapSwizzle swizzle);
 
 // An NVTX range around one ABI call (host side: it brackets the enqueueing of
 // the call's launches), so that profilers can attribute the kernels to it.
