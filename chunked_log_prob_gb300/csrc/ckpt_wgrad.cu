@@ -149,33 +149,47 @@ __device__ __forceinline__ void give_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// 16 e4m3 of a block with the exponent byte `e` to 16 bf16, exactly. Where 2^k
-// is an fp16 (k in [-24, 15]: the usual activations), a value costs one mixed
-// multiply-add of two fp16 into fp32 (two operations fewer a pair).
-__device__ __forceinline__ void widen16(const uint4& w, uint32_t e, uint32_t (&o)[8]) {
-  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-  const float f = ckpt_factor(e);
-  if (e - 103u <= 39u || (w.x | w.y | w.z | w.w) == 0u) {
-    uint16_t f16;
-    asm("cvt.rn.f16.f32 %0, %1;" : "=h"(f16) : "f"(f));
-    if (e - 103u > 39u) f16 = 0;  // all values are 0
+// Four times 16 e4m3 of one block each, with their exponent bytes, to bf16,
+// exactly. Where every 2^k is an fp16 (k in [-24, 15], or all values 0: the
+// usual activations), a value costs one mixed multiply-add of two fp16 into
+// fp32. One branch for all 64 values leaves them to be interleaved.
+__device__ __forceinline__ void widen64(const uint4 (&w)[4], const uint32_t (&e)[4],
+                                        uint32_t (&o)[4][8]) {
+  bool small = true;
+  uint16_t f16[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float lo, hi;
-      asm("{\n\t.reg .b32 t;\n\t.reg .b16 l, h;\n\t"
-          "cvt.rn.f16x2.e4m3x2 t, %2;\n\t"
-          "mov.b32 {l, h}, t;\n\t"
-          "fma.rn.f32.f16 %0, l, %3, %4;\n\t"
-          "fma.rn.f32.f16 %1, h, %3, %4;\n\t}"
-          : "=f"(lo), "=f"(hi)
-          : "h"(static_cast<uint16_t>(in[j >> 1] >> (16 * (j & 1)))), "h"(f16), "f"(0.f));
-      o[j] = pack_bf16x2(lo, hi);
+  for (int h = 0; h < 4; ++h) {
+    const bool in = e[h] - 103u <= 39u;
+    small = small && (in || (w[h].x | w[h].y | w[h].z | w[h].w) == 0u);
+    asm("cvt.rn.f16.f32 %0, %1;" : "=h"(f16[h]) : "f"(in ? ckpt_factor(e[h]) : 0.f));
+  }
+  if (small) {
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      const uint32_t in[4] = {w[h].x, w[h].y, w[h].z, w[h].w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float lo, hi;
+        asm("{\n\t.reg .b32 t;\n\t.reg .b16 l, h;\n\t"
+            "cvt.rn.f16x2.e4m3x2 t, %2;\n\t"
+            "mov.b32 {l, h}, t;\n\t"
+            "fma.rn.f32.f16 %0, l, %3, %4;\n\t"
+            "fma.rn.f32.f16 %1, h, %3, %4;\n\t}"
+            : "=f"(lo), "=f"(hi)
+            : "h"(static_cast<uint16_t>(in[j >> 1] >> (16 * (j & 1)))), "h"(f16[h]), "f"(0.f));
+        o[h][j] = pack_bf16x2(lo, hi);
+      }
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 v = unpack_e4m3x2(in[j >> 1] >> (16 * (j & 1)));
-      o[j] = pack_bf16x2(v.x * f, v.y * f);
+    for (int h = 0; h < 4; ++h) {
+      const uint32_t in[4] = {w[h].x, w[h].y, w[h].z, w[h].w};
+      const float f = ckpt_factor(e[h]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float2 v = unpack_e4m3x2(in[j >> 1] >> (16 * (j & 1)));
+        o[h][j] = pack_bf16x2(v.x * f, v.y * f);
+      }
     }
   }
 }
@@ -364,13 +378,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         const uint8_t* src = raw + r * kRawBytes;
-        uint32_t o[4][8];
+        uint4 w[4];
+        uint32_t e[4], o[4][8];
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
           const int row = r0 + 16 * h;
-          widen16(*reinterpret_cast<const uint4*>(src + row * 128 + c * 16),
-                  src[kRawQ + row * 16 + x], o[h]);
+          w[h] = *reinterpret_cast<const uint4*>(src + row * 128 + c * 16);
+          e[h] = src[kRawQ + row * 16 + x];
         }
+        widen64(w, e, o);
         // Widened before the slot is waited for: only the stores, the fence and
         // the barriers lie on the slot's way round.
         if (n >= kX && !mbar_wait(&done_bar[(n - kX) % kDy], ((n - kX) / kDy) & 1u, abort_flag,
