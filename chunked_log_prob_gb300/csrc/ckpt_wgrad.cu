@@ -3,7 +3,7 @@
 //
 // A tcgen05 GEMM over the tokens, both operands MN-major (a token's row holds
 // 64 outputs or inputs in 128 bytes). X never exists in memory: its e4m3 tiles
-// arrive by TMA, eight converter warps widen them on chip to bf16 - exactly,
+// arrive by TMA, converter warps widen them on chip to bf16 - exactly,
 // since 2^k is a power of two and e4m3 has 4 significant bits - into the
 // 128-byte-swizzled layout that a bf16 TMA load would have left, and the tensor
 // cores read them from there. Against expanding X first (16384 x 4096: 69 MB
@@ -39,15 +39,17 @@ constexpr int kRawBytes = kRawQ + kTok * 16;  // and 16 exponents, ours among th
 constexpr int kStoreBuf = 32 * 64;         // 32 x 16 fp32 on its way out
 constexpr int kSegment = 16;       // stages summed in TMEM: 1024 tokens
 // Warps: 0 dY by TMA, 1 MMA, 2 the checkpoint by TMA, 3 idle, then two
-// warpgroups of each of these. The converters' warpgroups take turns with the
-// stages, so that one's waits and fences lie beside the other's work.
-constexpr int kEpilogueWarps = 8, kConvertWarps = 8;
-constexpr int kConvertGroup = 4;  // warps that share a stage
+// warpgroups that hold the sums and four that widen. The latter work in two
+// halves that take turns with the stages: widening is short dependent chains
+// between barriers, so it wants many warps (16384 x 4096 x 4096: 397 us with
+// eight of them, 372 with sixteen).
+constexpr int kEpilogueWarps = 8, kConvertWarps = 16;
+constexpr int kConvertGroup = 8;  // warps that share a stage
 constexpr int kFirstEpilogue = 4, kFirstConvert = kFirstEpilogue + kEpilogueWarps;
 constexpr int kThreads = 32 * (kFirstConvert + kConvertWarps);
-// Registers of a thread: 96 at launch (640 x 96 = 61440), moved to the epilogue,
-// whose threads hold 128 sums: 128 x 32 + 256 x 160 + 256 x 64 = 61440.
-constexpr int kLaunchRegs = 96, kControlRegs = 32, kEpilogueRegs = 160, kConvertRegs = 64;
+// Registers of a thread: 72 at launch (896 x 72 = 64512), moved to the epilogue,
+// whose threads hold 128 sums: 128 x 24 + 256 x 144 + 512 x 48 = 64512.
+constexpr int kLaunchRegs = 72, kControlRegs = 24, kEpilogueRegs = 144, kConvertRegs = 48;
 static_assert(128 * kControlRegs + 32 * kEpilogueWarps * kEpilogueRegs +
                       32 * kConvertWarps * kConvertRegs <=
                   kThreads * kLaunchRegs,
@@ -149,23 +151,28 @@ __device__ __forceinline__ void give_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// Four times 16 e4m3 of one block each, with their exponent bytes, to bf16,
-// exactly. Where every 2^k is an fp16 (k in [-24, 15], or all values 0: the
-// usual activations), a value costs one mixed multiply-add of two fp16 into
-// fp32. One branch for all 64 values leaves them to be interleaved.
-__device__ __forceinline__ void widen64(const uint4 (&w)[4], const uint32_t (&e)[4],
-                                        uint32_t (&o)[4][8]) {
-  bool small = true;
-  uint16_t f16[4];
+// Twice 16 e4m3 of one block each, with their exponent bytes, to bf16, exactly.
+// Where both 2^k are fp16 (k in [-24, 15], or all values 0: the usual
+// activations), a value costs one mixed multiply-add of two fp16 into fp32.
+__device__ __forceinline__ void widen32(const uint4 (&w)[2], const uint32_t (&e)[2],
+                                        uint32_t (&o)[2][8]) {
+  uint16_t f16[2];
+  bool small = e[0] - 103u <= 39u && e[1] - 103u <= 39u;
 #pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    const bool in = e[h] - 103u <= 39u;
-    small = small && (in || (w[h].x | w[h].y | w[h].z | w[h].w) == 0u);
-    asm("cvt.rn.f16.f32 %0, %1;" : "=h"(f16[h]) : "f"(in ? ckpt_factor(e[h]) : 0.f));
+  for (int h = 0; h < 2; ++h)
+    asm("cvt.rn.f16.f32 %0, %1;" : "=h"(f16[h]) : "f"(__uint_as_float(e[h] << 23)));
+  if (!small) {
+    small = true;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (e[h] - 103u <= 39u) continue;
+      f16[h] = 0;
+      small = small && (w[h].x | w[h].y | w[h].z | w[h].w) == 0u;
+    }
   }
   if (small) {
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
+    for (int h = 0; h < 2; ++h) {
       const uint32_t in[4] = {w[h].x, w[h].y, w[h].z, w[h].w};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -182,7 +189,7 @@ __device__ __forceinline__ void widen64(const uint4 (&w)[4], const uint32_t (&e)
     }
   } else {
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
+    for (int h = 0; h < 2; ++h) {
       const uint32_t in[4] = {w[h].x, w[h].y, w[h].z, w[h].w};
       const float f = ckpt_factor(e[h]);
 #pragma unroll
@@ -359,62 +366,74 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= kFirstConvert) {
     // -------------------------------------------------------- converters --
     give_registers<kConvertRegs>();
-    // A thread widens 16 columns of four tokens of every second stage.
-    const int ct = (static_cast<int>(threadIdx.x) - 32 * kFirstConvert) & 127;
-    const uint32_t group = (warp - kFirstConvert) / kConvertGroup;
-    const int c = ct & 7, r0 = ct >> 3;
+    // A thread widens 16 columns of two tokens, 32 apart, of every second stage:
+    // piece c of the 64 columns of one box. Eight lanes that load or store at
+    // once take 4 pieces of the rows rho and rho ^ 5 of 8: the 128-byte swizzle
+    // (raw tile: piece c at c ^ row; X tile: pieces 2c and 2c + 1 at theirs ^
+    // row) puts them in eight different banks both times.
+    const int wid = warp - kFirstConvert;
+    const uint32_t group = wid / kConvertGroup;
+    const int box = wid & 1;
+    const int c = lane & 3;
+    const int row = ((wid & (kConvertGroup - 1)) >> 1) * 8 +
+                    ((lane >> 3) ^ (((lane >> 2) & 1) * 5));
+    const uint32_t src0 = smem_u32(raw) + row * 128 + (((box * 4 + c) ^ (row & 7)) << 4);
+    const uint32_t exp0 = smem_u32(raw) + kRawQ + row * 16 + box * 2 + (c >> 1);
+    const uint32_t dst0 =
+        smem_u32(xring) + box * kBoxBytes + row * 128 + (((2 * c) ^ (row & 7)) << 4);
     const uint32_t full0 = mapa_shared(smem_u32(&full_bar[0]), 0);
-    uint32_t n = 0;
+    // Ring positions of stage n, and of stage n - kX in the ring of done_bar.
+    uint32_t n = 0, r = group, r_par = 0, f = group;
+    uint32_t d = 2 * kDy - kX + group, d_par = 1;
+    while (d >= kDy) d -= kDy;
     while (ok && work.next(plan, pair, pairs, it)) {
       int tm, tn;
       tile_place(plan, it.tile, tm, tn);
       const int i0 = tn * kTileN + static_cast<int>(rank) * (tile_cols(args.in, tn) / 2);
-      const int x = ((i0 / kCkptBlock) & 15) + (c >> 1);  // our exponent of the 16
-      for (int k = it.kb; k < it.ke; ++k, ++n) {
-        if ((n & 1u) != group) continue;
-        const uint32_t r = n % kRaw;
-        if (!mbar_wait(&raw_full[r], (n / kRaw) & 1u, abort_flag, args.status)) {
+      const uint32_t ex = exp0 + ((i0 / kCkptBlock) & 15);  // our exponent of the 16
+      const uint32_t n_end = n + (it.ke - it.kb);
+      for (uint32_t m = n + ((n ^ group) & 1u); m < n_end; m += 2) {
+        if (!mbar_wait(&raw_full[r], r_par, abort_flag, args.status)) {
           ok = false;
           break;
         }
-        const uint8_t* src = raw + r * kRawBytes;
-        uint4 w[4];
-        uint32_t e[4], o[4][8];
+        uint4 w[2];
+        uint32_t e[2], o[2][8];
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const int row = r0 + 16 * h;
-          w[h] = *reinterpret_cast<const uint4*>(src + row * 128 + c * 16);
-          e[h] = src[kRawQ + row * 16 + x];
+        for (int h = 0; h < 2; ++h) {
+          w[h] = lds_v4(src0 + r * kRawBytes + h * 32 * 128);
+          e[h] = lds_u8(ex + r * kRawBytes + h * 32 * 16);
         }
-        widen64(w, e, o);
+        widen32(w, e, o);
         // Widened before the slot is waited for: only the stores, the fence and
         // the barriers lie on the slot's way round.
-        if (n >= kX && !mbar_wait(&done_bar[(n - kX) % kDy], ((n - kX) / kDy) & 1u, abort_flag,
-                                  args.status)) {
+        if (m >= kX && !mbar_wait(&done_bar[d], d_par, abort_flag, args.status)) {
           ok = false;
           break;
         }
-        uint8_t* b = xring + n % kX * kOperand + (c >> 2) * kBoxBytes;
+        const uint32_t dst = dst0 + (m % kX) * kOperand;
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          // The token's 16-byte pieces 2 (c & 3) and the next, at their
-          // swizzled place; lanes of the second box store them the other way
-          // round, so that 8 lanes meet 8 different banks.
-          const int row = r0 + 16 * h;
-          uint4* dst = reinterpret_cast<uint4*>(b + row * 128);
-          const int p = 2 * (c & 3), flip = c >> 2;
-          const uint4 lo = make_uint4(o[h][0], o[h][1], o[h][2], o[h][3]);
-          const uint4 hi = make_uint4(o[h][4], o[h][5], o[h][6], o[h][7]);
-          dst[(p + flip) ^ (row & 7)] = flip ? hi : lo;
-          dst[(p + 1 - flip) ^ (row & 7)] = flip ? lo : hi;
+        for (int h = 0; h < 2; ++h) {
+          sts_v4(dst + h * 32 * 128, o[h][0], o[h][1], o[h][2], o[h][3]);
+          sts_v4((dst + h * 32 * 128) ^ 16u, o[h][4], o[h][5], o[h][6], o[h][7]);
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&raw_empty[r]);
-          mbar_arrive_cluster(full0 + n % kDy * 8u);
+          mbar_arrive_cluster(full0 + f * 8u);
+        }
+        if ((r += 2) >= kRaw) {
+          r -= kRaw;
+          r_par ^= 1u;
+        }
+        if ((f += 2) >= kDy) f -= kDy;
+        if ((d += 2) >= kDy) {
+          d -= kDy;
+          d_par ^= 1u;
         }
       }
+      n = n_end;
     }
   } else if (warp >= kFirstEpilogue) {
     // ---------------------------------------------------------- epilogue --
@@ -514,6 +533,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) bulk_wait_group<0>();
   }
 
+  // The closing barrier is one of whole warps: the lanes that had no part in an
+  // elected lane's loop wait for it here.
+  __syncwarp();
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
@@ -610,7 +632,7 @@ cudaError_t launch_ckpt_wgrad(const WgradArgs& a, int sms, cudaStream_t st) {
   if (!encode_map_2d(&map_dy, a.dy, a.out, a.n, a.lddy * 2, 64, kTok,
                      CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_map_2d(&map_q, a.ck.q, a.in, a.n, a.ck.ldq, 128, kTok, CU_TENSOR_MAP_DATA_TYPE_UINT8,
-                     CU_TENSOR_MAP_SWIZZLE_NONE) ||
+                     CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_map_2d(&map_ex, a.ck.ex, a.ck.lde, a.n, a.ck.lde, 16, kTok,
                      CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE) ||
       !encode_map_2d(&map_dw, a.dw, a.in, a.out, a.lddw * 4, 16, 32,
