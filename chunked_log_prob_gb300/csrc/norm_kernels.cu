@@ -179,6 +179,140 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormFwdArgs a) {
   }
 }
 
+// The aligned form. Each row of the CTA (threadIdx.y) has a ring of `slots`
+// rows in shared memory, filled by bulk copies; a slot is filled again as soon
+// as the row's sum has been taken, when every thread holds its values.
+struct Ring {
+  int slots;          // rows in flight for each row of the CTA
+  uint32_t row_bytes;  // of a slot
+};
+
+// Shared memory: barriers, then the parameters as fp32, then the rings.
+constexpr uint32_t kRingBars = 8 * 8 * sizeof(uint64_t);  // 8 rows x 8 slots at most
+constexpr int kMaxSlots = 8;
+
+// After a timeout: lets the copies still in flight land (within the same limit).
+__device__ __forceinline__ void land(uint64_t* bars, int slots, uint32_t parity, uint32_t pending) {
+  for (int s = 0; s < slots; ++s)
+    if ((pending >> s) & 1u) row_wait(&bars[s], (parity >> s) & 1u);
+}
+
+template <typename T, int CH>
+__global__ void __launch_bounds__(512) norm_fwd_ring_kernel(const NormFwdArgs a, const Ring ring) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float2 red[8][2 * 32];
+  __shared__ float cnt_all[8][32];
+  const int t = threadIdx.x, tpr = blockDim.x, g = threadIdx.y, d = a.d;
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(smem) + g * kMaxSlots;
+  float* const sw = reinterpret_cast<float*>(smem + kRingBars);
+  float* const sb = sw + (a.weight != nullptr ? d : 0);
+  const uint32_t rows0 = smem_u32(sb + (a.bias != nullptr ? d : 0)) +
+                         g * ring.slots * ring.row_bytes;
+  const uint32_t x_bytes = d * sizeof(T);
+  const T* x = static_cast<const T*>(a.x);
+  const T* res = static_cast<const T*>(a.res);
+  T* y = static_cast<T*>(a.y);
+  T* z = static_cast<T*>(a.z);
+  const long long step = static_cast<long long>(gridDim.x) * blockDim.y;
+  long long row = static_cast<long long>(blockIdx.x) * blockDim.y + g;
+  uint32_t pending = 0;  // thread 0: slots whose copies have not been waited for
+  const auto issue = [&](long long r, int slot) {
+    if (!row_live(a.mask, r, a.n)) return;
+    pending |= 1u << slot;
+    const uint32_t dst = rows0 + slot * ring.row_bytes;
+    mbar_arrive_expect_tx(&bars[slot], res != nullptr ? 2 * x_bytes : x_bytes);
+    bulk_load(dst, x + r * a.ldx, x_bytes, &bars[slot]);
+    if (res != nullptr) bulk_load(dst + x_bytes, res + r * a.ldr, x_bytes, &bars[slot]);
+  };
+  if (t == 0) {
+    for (int s = 0; s < ring.slots; ++s) mbar_init(&bars[s], 1);
+    fence_mbar_init();
+    for (int s = 0; s < ring.slots; ++s) issue(row + s * step, s);
+  }
+  if (a.weight != nullptr)
+    stage_param(sw, a.weight, a.wtype, 1.f, d, g * tpr + t, tpr * blockDim.y);
+  if (a.bias != nullptr) stage_param(sb, a.bias, a.wtype, 0.f, d, g * tpr + t, tpr * blockDim.y);
+  count_columns<CH, true>(t, tpr, d, cnt_all[g]);
+  __syncthreads();
+
+  int phase = 0, slot = 0;
+  uint32_t parity = 0;  // a bit per slot
+  bool ok = true;
+  bool live = row_live(a.mask, row, a.n);
+  for (; row < a.n; row += step) {
+    const bool live1 = row_live(a.mask, row + step, a.n);
+    float v[CH][8];
+    float mean = 0.f, rstd = 0.f;
+    if (live) {
+      ok = ok && row_wait(&bars[slot], (parity >> slot) & 1u);
+      if (ok) {
+        parity ^= 1u << slot;
+        pending &= ~(1u << slot);
+      }
+      const uint32_t src = rows0 + slot * ring.row_bytes;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        widen(lds_chunk<T>(src, c, t, tpr, d), v[c]);
+        if (res != nullptr) {
+          float r[8];
+          widen(lds_chunk<T>(src + x_bytes, c, t, tpr, d), r);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[c][j] += r[j];
+          // The stream holds z rounded; the norm is taken of what it holds.
+          const Raw8<T> o = narrow<T>(v[c]);
+          if (z != nullptr) store_chunk<T, true>(z + row * a.ldz, o, c, t, tpr, d);
+          widen(o, v[c]);
+        }
+      }
+      const float2 m =
+          row_moments<CH, true>(v, a.kind, t, tpr, d, g + 1, red[g], cnt_all[g], phase);
+      mean = m.x;
+      rstd = 1.f / sqrtf(m.y / static_cast<float>(d) + a.eps);
+      if (!ok) rstd = __uint_as_float(0x7fc00000u);
+    } else {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[c][j] = 0.f;
+        if (z != nullptr && res != nullptr)
+          store_chunk<T, true>(z + row * a.ldz, narrow<T>(v[c]), c, t, tpr, d);
+      }
+    }
+    // Every thread has its values (the sum's barrier, or the warp's).
+    __syncwarp();
+    if (t == 0 && ok) issue(row + ring.slots * step, slot);
+    if (++slot == ring.slots) slot = 0;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      if (a.ck.q != nullptr)
+        ckpt_store_chunk<T, true>(v[c], a.ck.q + row * a.ck.ldq, a.ck.ex + row * a.ck.lde, c, t,
+                                  tpr, d);
+      if (live) {
+        float w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[c][j] = (v[c][j] - mean) * rstd;
+        if (a.weight != nullptr) {
+          read_param(sw, c, t, tpr, d, w);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[c][j] *= w[j];
+        }
+        if (a.bias != nullptr) {
+          read_param(sb, c, t, tpr, d, w);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[c][j] += w[j];
+        }
+      }
+      store_chunk<T, true>(y + row * a.ldy, narrow<T>(v[c]), c, t, tpr, d);
+    }
+    if (t == 0) {
+      if (a.mean != nullptr) a.mean[row] = mean;
+      if (a.rstd != nullptr) a.rstd[row] = rstd;
+    }
+    live = live1;
+  }
+  land(bars, ring.slots, parity, pending);
+}
+
 // Rows beyond kNormRegisterRow columns: the CTA walks over the row three times
 // (sum, centred squares, output); the second and third walk find it in L2. A
 // thread rereads only what it stored itself, so outputs may lie on the inputs.
@@ -408,6 +542,190 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormBwdArgs a) {
   }
 }
 
+// The aligned form of norm_bwd_kernel, its rows in flight as in
+// norm_fwd_ring_kernel. A slot holds dy, then x (or its bytes and exponents),
+// then dres.
+template <typename T, int CH, bool CK, bool DB>
+__global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const NormBwdArgs a, const Ring ring) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float2 red[8][2 * 32];
+  const int t = threadIdx.x, tpr = blockDim.x, g = threadIdx.y, d = a.d;
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(smem) + g * kMaxSlots;
+  float* const sw = reinterpret_cast<float*>(smem + kRingBars);
+  uint8_t* const ring0 = reinterpret_cast<uint8_t*>(sw + (a.weight != nullptr ? d : 0));
+  const uint32_t rows0 = smem_u32(ring0) + g * ring.slots * ring.row_bytes;
+  const uint32_t t_bytes = d * sizeof(T);
+  const uint32_t x_bytes =
+      CK ? static_cast<uint32_t>(a.ck.ldq + a.ck.lde) : t_bytes;  // rows of 16 bytes
+  const T* dy = static_cast<const T*>(a.dy);
+  const T* dres = static_cast<const T*>(a.dres);
+  T* dx = static_cast<T*>(a.dx);
+  const long long step = static_cast<long long>(gridDim.x) * blockDim.y;
+  long long row = static_cast<long long>(blockIdx.x) * blockDim.y + g;
+  uint32_t pending = 0;  // thread 0: slots whose copies have not been waited for
+  const auto issue = [&](long long r, int slot) {
+    if (!row_live(a.mask, r, a.n)) return;
+    pending |= 1u << slot;
+    const uint32_t dst = rows0 + slot * ring.row_bytes;
+    mbar_arrive_expect_tx(&bars[slot], t_bytes + x_bytes + (dres != nullptr ? t_bytes : 0));
+    bulk_load(dst, dy + r * a.lddy, t_bytes, &bars[slot]);
+    if (CK) {
+      bulk_load(dst + t_bytes, a.ck.q + r * a.ck.ldq, static_cast<uint32_t>(a.ck.ldq), &bars[slot]);
+      bulk_load(dst + t_bytes + static_cast<uint32_t>(a.ck.ldq), a.ck.ex + r * a.ck.lde,
+                static_cast<uint32_t>(a.ck.lde), &bars[slot]);
+    } else {
+      bulk_load(dst + t_bytes, static_cast<const T*>(a.x) + r * a.ldx, t_bytes, &bars[slot]);
+    }
+    if (dres != nullptr) bulk_load(dst + t_bytes + x_bytes, dres + r * a.lddres, t_bytes, &bars[slot]);
+  };
+  if (t == 0) {
+    for (int s = 0; s < ring.slots; ++s) mbar_init(&bars[s], 1);
+    fence_mbar_init();
+    for (int s = 0; s < ring.slots; ++s) issue(row + s * step, s);
+  }
+  if (a.weight != nullptr)
+    stage_param(sw, a.weight, a.wtype, 1.f, d, g * tpr + t, tpr * blockDim.y);
+  __syncthreads();
+
+  float dw[CH][8], db[DB ? CH : 1][8];
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      dw[c][j] = 0.f;
+      if (DB) db[DB ? c : 0][j] = 0.f;
+    }
+  const float inv_d = 1.f / static_cast<float>(d);
+  int phase = 0, slot = 0;
+  uint32_t parity = 0;
+  bool ok = true;
+  bool live = row_live(a.mask, row, a.n);
+  float rstd1 = live ? a.rstd[row] : 0.f;
+  float mean1 = live && a.kind != GRPO_NORM_RMS ? a.mean[row] : 0.f;
+  for (; row < a.n; row += step) {
+    const long long next = row + step;
+    const bool live1 = row_live(a.mask, next, a.n);
+    const float rstd = rstd1, mean = mean1;
+    rstd1 = live1 ? a.rstd[next] : 0.f;
+    mean1 = live1 && a.kind != GRPO_NORM_RMS ? a.mean[next] : 0.f;
+    if (!live) {
+      const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (t == 0 && ok) issue(row + ring.slots * step, slot);
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+        store_chunk<T, true>(dx + row * a.lddx, narrow<T>(zero), c, t, tpr, d);
+    } else {
+      ok = ok && row_wait(&bars[slot], (parity >> slot) & 1u);
+      if (ok) {
+        parity ^= 1u << slot;
+        pending &= ~(1u << slot);
+      }
+      const uint32_t src = rows0 + slot * ring.row_bytes;
+      float u[CH][8], h[CH][8];
+      Raw8<T> rr[CH];
+      float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        widen(lds_chunk<T>(src, c, t, tpr, d), u[c]);
+        if (CK) {
+          RawCkpt<true> q;
+          const int i = c * tpr + t;
+          q.w = make_uint2(0, 0);
+          q.ex[0] = kCkptBias;
+          if (8 * i < d) {
+            q.w = lds_v2(src + t_bytes + 8 * i);
+            q.ex[0] = static_cast<uint8_t>(
+                lds_u8(src + t_bytes + static_cast<uint32_t>(a.ck.ldq) + i / 4));
+          }
+          ckpt_widen<true>(q, h[c]);
+        } else {
+          widen(lds_chunk<T>(src + t_bytes, c, t, tpr, d), h[c]);
+        }
+        if (dres != nullptr) rr[c] = lds_chunk<T>(src + t_bytes + x_bytes, c, t, tpr, d);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          h[c][j] = (h[c][j] - mean) * rstd;
+          dw[c][j] += u[c][j] * h[c][j];
+          if (DB) db[DB ? c : 0][j] += u[c][j];
+        }
+        if (a.weight != nullptr) {
+          float w[8];
+          read_param(sw, c, t, tpr, d, w);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) u[c][j] *= w[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          s.x += u[c][j];
+          s.y += u[c][j] * h[c][j];
+        }
+      }
+      s = row_sum2(s, t, tpr, g + 1, red[g], phase);
+      __syncwarp();
+      if (t == 0 && ok) issue(row + ring.slots * step, slot);
+      const float c1 = a.kind != GRPO_NORM_RMS ? s.x * inv_d : 0.f;
+      const float c2 = ok ? s.y * inv_d : __uint_as_float(0x7fc00000u);
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[c][j] = rstd * (u[c][j] - c1 - h[c][j] * c2);
+        if (dres != nullptr) {
+          float r[8];
+          widen(rr[c], r);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) u[c][j] += r[j];
+        }
+        store_chunk<T, true>(dx + row * a.lddx, narrow<T>(u[c]), c, t, tpr, d);
+      }
+      if (!ok) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) dw[c][j] = __uint_as_float(0x7fc00000u);
+      }
+    }
+    if (++slot == ring.slots) slot = 0;
+    live = live1;
+  }
+  land(bars, ring.slots, parity, pending);
+  if (a.dweight == nullptr && !DB) return;
+  // The CTA's rows in flight, added in their order; the rings have been read.
+  float* const cw = blockDim.y > 1 ? reinterpret_cast<float*>(ring0) : nullptr;
+  float* const cb = cw != nullptr ? cw + d : nullptr;
+  float* pw = a.partials + static_cast<long long>(blockIdx.x) * d;
+  float* pb = pw + static_cast<long long>(gridDim.x) * d;
+  if (cw == nullptr) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int col = chunk_col<true>(c, 0, t, tpr);
+      if (col >= d) continue;
+      store8(pw + col, dw[c]);
+      if (DB) store8(pb + col, db[DB ? c : 0]);
+    }
+    return;
+  }
+  __syncthreads();
+  for (int k = 0; k < static_cast<int>(blockDim.y); ++k) {
+    if (g == k) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int col = chunk_col<true>(c, j, t, tpr);
+          if (col < d) {
+            cw[col] = k == 0 ? dw[c][j] : cw[col] + dw[c][j];
+            if (DB) cb[col] = k == 0 ? db[DB ? c : 0][j] : cb[col] + db[DB ? c : 0][j];
+          }
+        }
+    }
+    __syncthreads();
+  }
+  for (int col = g * tpr + t; col < d; col += tpr * blockDim.y) {
+    pw[col] = cw[col];
+    if (DB) pb[col] = cb[col];
+  }
+}
+
 // Rows beyond kNormRegisterRow columns: dx in two walks over the row.
 template <typename T, bool VEC, bool CK>
 __global__ void __launch_bounds__(512) norm_bwd_long_kernel(const NormBwdArgs a) {
@@ -575,6 +893,53 @@ int resident(int threads, size_t smem, int sms) {
   return n * sms;
 }
 
+constexpr size_t kSmemMax = 227 * 1024 - 8192;  // less the kernels' static arrays
+constexpr size_t kSmemTarget = 72 * 1024;       // of a CTA: three to an SM
+
+// Rows in flight of a CTA: as many slots as fit kSmemTarget beside the
+// parameters, at most kMaxSlots and at least 2 (1 for rows that fit but once).
+Ring make_ring(uint32_t row_bytes, int rows, size_t fixed) {
+  const size_t slot = static_cast<size_t>(row_bytes) * rows;
+  const size_t room = kSmemTarget > fixed ? kSmemTarget - fixed : 0;
+  size_t slots = std::min<size_t>(kMaxSlots, std::max<size_t>(2, room / slot));
+  if (fixed + slots * slot > kSmemMax) slots = 1;
+  Ring r;
+  r.slots = static_cast<int>(slots);
+  r.row_bytes = row_bytes;
+  return r;
+}
+
+// Opts a kernel in to large shared memory, once.
+template <auto Kernel>
+bool opted_in() {
+  static const bool ok = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                              static_cast<int>(kSmemMax)) == cudaSuccess;
+  return ok;
+}
+
+template <auto Kernel>
+cudaError_t ctas_per_sm(int threads, size_t smem, int* n) {
+  if (!opted_in<Kernel>()) return cudaErrorInvalidValue;
+  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, Kernel, threads, smem);
+}
+
+template <typename T, int CH>
+cudaError_t fwd_ring(const NormFwdArgs& a, const RowShape& s, int sms, cudaStream_t st) {
+  constexpr auto kernel = norm_fwd_ring_kernel<T, CH>;
+  const size_t fixed = kRingBars + sizeof(float) * a.d *
+                                       ((a.weight != nullptr) + (a.bias != nullptr));
+  const Ring ring = make_ring(a.d * sizeof(T) * (a.res != nullptr ? 2 : 1), s.rows, fixed);
+  const size_t smem = fixed + static_cast<size_t>(ring.slots) * ring.row_bytes * s.rows;
+  int per_sm = 0;
+  cudaError_t e = ctas_per_sm<kernel>(s.tpr * s.rows, smem, &per_sm);
+  if (e != cudaSuccess) return e;
+  const long long units = (a.n + s.rows - 1) / s.rows;
+  const int grid = static_cast<int>(std::min<long long>(units, std::max(1, per_sm) * sms));
+  LaunchTimer timer("norm_fwd_kernel", st);
+  kernel<<<grid, dim3(s.tpr, s.rows), smem, st>>>(a, ring);
+  return cudaGetLastError();
+}
+
 template <typename T, bool VEC, int CH>
 cudaError_t fwd(const NormFwdArgs& a, const RowShape& s, int sms, cudaStream_t st) {
   constexpr auto kernel = norm_fwd_kernel<T, VEC, CH>;
@@ -595,7 +960,10 @@ cudaError_t fwd_any(const NormFwdArgs& a, int sms, cudaStream_t st) {
     return cudaGetLastError();
   }
   const RowShape s = row_shape(a.d);
-  return s.ch == 1 ? fwd<T, VEC, 1>(a, s, sms, st) : fwd<T, VEC, 2>(a, s, sms, st);
+  if constexpr (VEC)
+    return s.ch == 1 ? fwd_ring<T, 1>(a, s, sms, st) : fwd_ring<T, 2>(a, s, sms, st);
+  else
+    return s.ch == 1 ? fwd<T, false, 1>(a, s, sms, st) : fwd<T, false, 2>(a, s, sms, st);
 }
 
 cudaError_t finish(const NormBwdArgs& a, int rows, cudaStream_t st) {
@@ -605,6 +973,32 @@ cudaError_t finish(const NormBwdArgs& a, int rows, cudaStream_t st) {
   norm_bwd_finish_kernel<<<grid, 256, 0, st>>>(a.partials, rows, a.d, a.dweight, a.dbias,
                                                a.add_dweight, a.add_dbias);
   return cudaGetLastError();
+}
+
+template <typename T, int CH, bool CK, bool DB>
+cudaError_t bwd_ring(const NormBwdArgs& a, const RowShape& s, int sms, cudaStream_t st) {
+  constexpr auto kernel = norm_bwd_ring_kernel<T, CH, CK, DB>;
+  const size_t fixed = kRingBars + (a.weight != nullptr ? sizeof(float) * a.d : 0);
+  const uint32_t t_bytes = a.d * sizeof(T);
+  const Ring ring =
+      make_ring(t_bytes * (a.dres != nullptr ? 2 : 1) +
+                    (CK ? static_cast<uint32_t>(a.ck.ldq + a.ck.lde) : t_bytes),
+                s.rows, fixed);
+  size_t smem = static_cast<size_t>(ring.slots) * ring.row_bytes * s.rows;
+  if (s.rows > 1) smem = std::max(smem, static_cast<size_t>(a.d) * (DB ? 8 : 4));
+  smem += fixed;
+  int per_sm = 0;
+  cudaError_t e = ctas_per_sm<kernel>(s.tpr * s.rows, smem, &per_sm);
+  if (e != cudaSuccess) return e;
+  const long long units = (a.n + s.rows - 1) / s.rows;
+  const int grid = static_cast<int>(std::min<long long>(
+      std::min<long long>(units, kNormMaxPartials), std::max(1, per_sm) * sms));
+  {
+    LaunchTimer timer("norm_bwd_kernel", st);
+    kernel<<<grid, dim3(s.tpr, s.rows), smem, st>>>(a, ring);
+  }
+  e = cudaGetLastError();
+  return e != cudaSuccess ? e : finish(a, grid, st);
 }
 
 template <typename T, bool VEC, int CH, bool CK, bool DB>
@@ -644,11 +1038,18 @@ cudaError_t bwd_any(const NormBwdArgs& a, int sms, cudaStream_t st) {
     return e != cudaSuccess ? e : finish(a, groups, st);
   }
   const RowShape s = row_shape(a.d);
-  if (a.dbias != nullptr)
-    return s.ch == 1 ? bwd<T, VEC, 1, CK, true>(a, s, sms, st)
-                     : bwd<T, VEC, 2, CK, true>(a, s, sms, st);
-  return s.ch == 1 ? bwd<T, VEC, 1, CK, false>(a, s, sms, st)
-                   : bwd<T, VEC, 2, CK, false>(a, s, sms, st);
+  const bool db = a.dbias != nullptr;
+  if constexpr (VEC) {
+    if (s.ch == 1)
+      return db ? bwd_ring<T, 1, CK, true>(a, s, sms, st) : bwd_ring<T, 1, CK, false>(a, s, sms, st);
+    return db ? bwd_ring<T, 2, CK, true>(a, s, sms, st) : bwd_ring<T, 2, CK, false>(a, s, sms, st);
+  } else {
+    if (s.ch == 1)
+      return db ? bwd<T, false, 1, CK, true>(a, s, sms, st)
+                : bwd<T, false, 1, CK, false>(a, s, sms, st);
+    return db ? bwd<T, false, 2, CK, true>(a, s, sms, st)
+              : bwd<T, false, 2, CK, false>(a, s, sms, st);
+  }
 }
 
 template <typename T>

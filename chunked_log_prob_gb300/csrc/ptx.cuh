@@ -429,6 +429,12 @@ __device__ __forceinline__ uint4 lds_v4(uint32_t saddr) {
   return v;
 }
 
+__device__ __forceinline__ uint2 lds_v2(uint32_t saddr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(saddr) : "memory");
+  return v;
+}
+
 __device__ __forceinline__ uint32_t lds_u8(uint32_t saddr) {
   uint32_t v;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(saddr) : "memory");

@@ -97,6 +97,11 @@ __device__ __forceinline__ void store_chunk(T* row, const Raw8<T>& r, int c, int
   }
 }
 
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+
 template <typename T>
 __device__ __forceinline__ void widen(const Raw8<T>& r, float (&v)[8]) {
 #pragma unroll
@@ -150,6 +155,74 @@ __device__ __forceinline__ float2 row_sum2(float2 v, int t, int tpr, int bar, fl
   named_barrier(bar, tpr);
   const int lane = t & 31;
   return warp_sum2(lane < (tpr >> 5) ? s[lane] : make_float2(0.f, 0.f));
+}
+
+// ------------------------------------------------------- rows in flight ----
+// Rows on 16 bytes come to shared memory by bulk copies, several rows ahead:
+// the bytes in flight do not cost registers.
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Waits for a phase of `bar`; false after about a second (no status word here:
+// the caller then gives NaN).
+__device__ __forceinline__ bool row_wait(uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity))
+    if (clock64() - t0 > kWaitLimitCycles) return false;
+  return true;
+}
+
+// Chunk c of a row in shared memory (VEC layout).
+template <typename T>
+__device__ __forceinline__ Raw8<T> lds_chunk(uint32_t row, int c, int t, int tpr, int d) {
+  Raw8<T> r;
+  uint4* w = reinterpret_cast<uint4*>(&r);
+  const int i = c * tpr + t;
+#pragma unroll
+  for (int k = 0; k < static_cast<int>(sizeof(r) / 16); ++k)
+    w[k] = 8 * i < d ? lds_v4(row + i * sizeof(r) + 16 * k) : make_uint4(0, 0, 0, 0);
+  return r;
+}
+
+// A weight or bias vector as fp32 in shared memory: the first four columns of
+// every chunk, then the other four, so that neighbouring threads read
+// neighbouring 16 bytes. `half`: 4 times the number of chunks.
+__device__ __forceinline__ void stage_param(float* dst, const void* p, int type, float none, int d,
+                                            int thread, int threads) {
+  const int half = d / 2;
+  for (int col = thread; col < d; col += threads) {
+    const int j = col & 7;
+    dst[(j >= 4 ? half : 0) + (col >> 3) * 4 + (j & 3)] =
+        p != nullptr ? load_param(p, type, col) : none;
+  }
+}
+
+__device__ __forceinline__ void read_param(const float* s, int c, int t, int tpr, int d,
+                                           float (&w)[8]) {
+  const int i = c * tpr + t;
+  if (8 * i >= d) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = 0.f;
+    return;
+  }
+  const float4 a = *reinterpret_cast<const float4*>(s + 4 * i);
+  const float4 b = *reinterpret_cast<const float4*>(s + d / 2 + 4 * i);
+  w[0] = a.x;
+  w[1] = a.y;
+  w[2] = a.z;
+  w[3] = a.w;
+  w[4] = b.x;
+  w[5] = b.y;
+  w[6] = b.z;
+  w[7] = b.w;
 }
 
 // ---------------------------------------------------- 8-bit checkpoints ----
