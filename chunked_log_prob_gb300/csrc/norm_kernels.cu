@@ -182,14 +182,21 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormFwdArgs a) {
 // The aligned form. Each row of the CTA (threadIdx.y) has a ring of `slots`
 // rows in shared memory, filled by bulk copies; a slot is filled again as soon
 // as the row's sum has been taken, when every thread holds its values.
+// The bytes in flight come from the ring, so what is left is issue slots: a
+// thread holds up to 32 values, so that a row's fixed work (barriers, sums,
+// addresses) is shared by few warps, and works on pairs of them.
 struct Ring {
-  int slots;          // rows in flight for each row of the CTA
+  int slots;           // rows in flight for each row of the CTA
   uint32_t row_bytes;  // of a slot
 };
 
 // Shared memory: barriers, then the parameters as fp32, then the rings.
-constexpr uint32_t kRingBars = 8 * 8 * sizeof(uint64_t);  // 8 rows x 8 slots at most
 constexpr int kMaxSlots = 8;
+constexpr int kMaxRows = 8;  // rows of a CTA
+constexpr uint32_t kRingBars = kMaxRows * kMaxSlots * sizeof(uint64_t);
+
+// Threads of a CTA with 8 ch values a thread, at most (kNormRegisterRow columns).
+constexpr int ring_threads(int ch) { return ch == 4 ? 256 : ch == 3 ? 352 : 512; }
 
 // After a timeout: lets the copies still in flight land (within the same limit).
 __device__ __forceinline__ void land(uint64_t* bars, int slots, uint32_t parity, uint32_t pending) {
@@ -197,51 +204,81 @@ __device__ __forceinline__ void land(uint64_t* bars, int slots, uint32_t parity,
     if ((pending >> s) & 1u) row_wait(&bars[s], (parity >> s) & 1u);
 }
 
-template <typename T, int CH>
-__global__ void __launch_bounds__(512) norm_fwd_ring_kernel(const NormFwdArgs a, const Ring ring) {
+// Columns that warp k of a row holds (VEC layout).
+template <int CH>
+__device__ __forceinline__ float warp_columns(int k, int tpr, int d) {
+  int n = 0;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) n += max(0, min(256, d - (c * tpr + k * 32) * 8));
+  return static_cast<float>(n);
+}
+
+// Rows of the group that begins at `row`.
+__device__ __forceinline__ int row_count(long long row, long long n, long long step) {
+  return row < n ? static_cast<int>((n - 1 - row) / step) + 1 : 0;
+}
+
+template <typename T, int CH, int KIND>
+__global__ void __launch_bounds__(ring_threads(CH)) norm_fwd_ring_kernel(const NormFwdArgs a, const Ring ring) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float2 red[8][2 * 32];
-  __shared__ float cnt_all[8][32];
+  __shared__ float2 red[kMaxRows][2 * 32];
   const int t = threadIdx.x, tpr = blockDim.x, g = threadIdx.y, d = a.d;
+  const int warps = tpr >> 5;
   uint64_t* const bars = reinterpret_cast<uint64_t*>(smem) + g * kMaxSlots;
   float* const sw = reinterpret_cast<float*>(smem + kRingBars);
   float* const sb = sw + (a.weight != nullptr ? d : 0);
+  const uint32_t sw32 = smem_u32(sw), sb32 = smem_u32(sb);
   const uint32_t rows0 = smem_u32(sb + (a.bias != nullptr ? d : 0)) +
                          g * ring.slots * ring.row_bytes;
   const uint32_t x_bytes = d * sizeof(T);
-  const T* x = static_cast<const T*>(a.x);
-  const T* res = static_cast<const T*>(a.res);
-  T* y = static_cast<T*>(a.y);
-  T* z = static_cast<T*>(a.z);
+  const bool res = a.res != nullptr;
   const long long step = static_cast<long long>(gridDim.x) * blockDim.y;
-  long long row = static_cast<long long>(blockIdx.x) * blockDim.y + g;
-  uint32_t pending = 0;  // thread 0: slots whose copies have not been waited for
-  const auto issue = [&](long long r, int slot) {
-    if (!row_live(a.mask, r, a.n)) return;
+  const long long row0 = static_cast<long long>(blockIdx.x) * blockDim.y + g;
+  const int count = row_count(row0, a.n, step);
+  const uint8_t* const mask = a.mask;
+  // Thread 0: slots whose copies have not been waited for, and the next row to fetch.
+  uint32_t pending = 0;
+  int fetched = 0;
+  const auto fetch = [&](int slot) {
+    if (fetched >= count) return;
+    const long long r = row0 + step * fetched++;
+    if (mask != nullptr && mask[r] == 0) return;
     pending |= 1u << slot;
     const uint32_t dst = rows0 + slot * ring.row_bytes;
-    mbar_arrive_expect_tx(&bars[slot], res != nullptr ? 2 * x_bytes : x_bytes);
-    bulk_load(dst, x + r * a.ldx, x_bytes, &bars[slot]);
-    if (res != nullptr) bulk_load(dst + x_bytes, res + r * a.ldr, x_bytes, &bars[slot]);
+    mbar_arrive_expect_tx(&bars[slot], res ? 2 * x_bytes : x_bytes);
+    bulk_load(dst, static_cast<const T*>(a.x) + r * a.ldx, x_bytes, &bars[slot]);
+    if (res) bulk_load(dst + x_bytes, static_cast<const T*>(a.res) + r * a.ldr, x_bytes, &bars[slot]);
   };
   if (t == 0) {
     for (int s = 0; s < ring.slots; ++s) mbar_init(&bars[s], 1);
     fence_mbar_init();
-    for (int s = 0; s < ring.slots; ++s) issue(row + s * step, s);
+    for (int s = 0; s < ring.slots; ++s) fetch(s);
   }
-  if (a.weight != nullptr)
-    stage_param(sw, a.weight, a.wtype, 1.f, d, g * tpr + t, tpr * blockDim.y);
-  if (a.bias != nullptr) stage_param(sb, a.bias, a.wtype, 0.f, d, g * tpr + t, tpr * blockDim.y);
-  count_columns<CH, true>(t, tpr, d, cnt_all[g]);
+  if (a.weight != nullptr) stage_param(sw, a.weight, a.wtype, d, g * tpr + t, tpr * blockDim.y);
+  if (a.bias != nullptr) stage_param(sb, a.bias, a.wtype, d, g * tpr + t, tpr * blockDim.y);
   __syncthreads();
 
+  const float inv_d = 1.f / static_cast<float>(d);
+  // Values of this warp that are columns: its chunks before d.
+  float warp_n = 0.f;
+  if (KIND == GRPO_NORM_LAYER) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) warp_n += (c * tpr + t) * 8 < d ? 8.f : 0.f;
+    warp_n = warp_sum(warp_n);
+  }
+  const float inv_warp_n = warp_n > 0.f ? 1.f / warp_n : 0.f;
+  T* y = static_cast<T*>(a.y) + row0 * a.ldy;
+  T* z = res && a.z != nullptr ? static_cast<T*>(a.z) + row0 * a.ldz : nullptr;
+  uint8_t* q = a.ck.q != nullptr ? a.ck.q + row0 * a.ck.ldq : nullptr;
+  uint8_t* ex = a.ck.ex + row0 * a.ck.lde;
   int phase = 0, slot = 0;
   uint32_t parity = 0;  // a bit per slot
   bool ok = true;
-  bool live = row_live(a.mask, row, a.n);
-  for (; row < a.n; row += step) {
-    const bool live1 = row_live(a.mask, row + step, a.n);
-    float v[CH][8];
+  bool live = count > 0 && (mask == nullptr || mask[row0] != 0);
+  for (int i = 0; i < count; ++i) {
+    const bool live1 =
+        i + 1 < count && (mask == nullptr || mask[row0 + step * (i + 1)] != 0);
+    f32x2 v[CH][4];
     float mean = 0.f, rstd = 0.f;
     if (live) {
       ok = ok && row_wait(&bars[slot], (parity >> slot) & 1u);
@@ -249,64 +286,130 @@ __global__ void __launch_bounds__(512) norm_fwd_ring_kernel(const NormFwdArgs a,
         parity ^= 1u << slot;
         pending &= ~(1u << slot);
       }
-      const uint32_t src = rows0 + slot * ring.row_bytes;
+      const uint32_t src = rows0 + slot * ring.row_bytes + t * sizeof(Raw8<T>);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        widen(lds_chunk<T>(src, c, t, tpr, d), v[c]);
-        if (res != nullptr) {
-          float r[8];
-          widen(lds_chunk<T>(src + x_bytes, c, t, tpr, d), r);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[c][j] += r[j];
+        for (int j = 0; j < 4; ++j) v[c][j] = 0ull;
+        if ((c * tpr + t) * 8 >= d) continue;
+        const uint32_t at = src + c * tpr * sizeof(Raw8<T>);
+        widen2(lds_raw<T>(at), v[c]);
+        if (res) {
+          f32x2 r[4];
+          widen2(lds_raw<T>(at + x_bytes), r);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[c][j] = add2(v[c][j], r[j]);
           // The stream holds z rounded; the norm is taken of what it holds.
-          const Raw8<T> o = narrow<T>(v[c]);
-          if (z != nullptr) store_chunk<T, true>(z + row * a.ldz, o, c, t, tpr, d);
-          widen(o, v[c]);
+          const Raw8<T> o = narrow2<T>(v[c]);
+          if (z != nullptr) store_raw(z + (c * tpr + t) * 8, o);
+          widen2(o, v[c]);
         }
       }
-      const float2 m =
-          row_moments<CH, true>(v, a.kind, t, tpr, d, g + 1, red[g], cnt_all[g], phase);
-      mean = m.x;
-      rstd = 1.f / sqrtf(m.y / static_cast<float>(d) + a.eps);
+      if (KIND == GRPO_NORM_RMS) {
+        f32x2 s[2] = {0ull, 0ull};
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[j & 1] = fma2(v[c][j], v[c][j], s[j & 1]);
+        const float2 m = join_warps(make_float2(warp_sum(sum_of(add2(s[0], s[1]))), 0.f), t, warps,
+                                    g + 1, red[g], phase);
+        rstd = rsqrtf(m.x * inv_d + a.eps);
+      } else {
+        // Each warp centres its values on their own mean; the warps' sums are
+        // then joined as if all had been centred on the row's.
+        f32x2 s[2] = {0ull, 0ull};
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[j & 1] = add2(v[c][j], s[j & 1]);
+        const float sum = warp_sum(sum_of(add2(s[0], s[1])));
+        const float mw = sum * inv_warp_n;
+        const f32x2 nmw = pair(-mw, -mw);
+        s[0] = s[1] = 0ull;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          if ((c * tpr + t) * 8 >= d) continue;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const f32x2 e = add2(v[c][j], nmw);
+            s[j & 1] = fma2(e, e, s[j & 1]);
+          }
+        }
+        const float m2 = warp_sum(sum_of(add2(s[0], s[1])));
+        float total = sum, centred = m2;
+        if (warps > 1) {
+          float2* sh = red[g] + phase * 32;
+          phase ^= 1;
+          // (sum, m2) of a warp; its count follows from its index.
+          if ((t & 31) == 0) sh[t >> 5] = make_float2(sum, m2);
+          named_barrier(g + 1, tpr);
+          total = 0.f;
+          for (int k = 0; k < warps; ++k) total += sh[k].x;
+          const float mu = total * inv_d;
+          centred = 0.f;
+          for (int k = 0; k < warps; ++k) {
+            const float nk = warp_columns<CH>(k, tpr, d);
+            const float e = nk > 0.f ? sh[k].x / nk - mu : 0.f;
+            centred += sh[k].y + nk * e * e;
+          }
+        } else {
+          __syncwarp();
+        }
+        mean = total * inv_d;
+        rstd = rsqrtf(centred * inv_d + a.eps);
+      }
       if (!ok) rstd = __uint_as_float(0x7fc00000u);
     } else {
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[c][j] = 0.f;
-        if (z != nullptr && res != nullptr)
-          store_chunk<T, true>(z + row * a.ldz, narrow<T>(v[c]), c, t, tpr, d);
+        for (int j = 0; j < 4; ++j) v[c][j] = 0ull;
+        if (z != nullptr && (c * tpr + t) * 8 < d)
+          store_raw(z + (c * tpr + t) * 8, narrow2<T>(v[c]));
       }
     }
     // Every thread has its values (the sum's barrier, or the warp's).
-    __syncwarp();
-    if (t == 0 && ok) issue(row + ring.slots * step, slot);
+    if (t == 0 && ok) fetch(slot);
     if (++slot == ring.slots) slot = 0;
+    const f32x2 scale = pair(rstd, rstd), shift = pair(-mean, -mean);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      if (a.ck.q != nullptr)
-        ckpt_store_chunk<T, true>(v[c], a.ck.q + row * a.ck.ldq, a.ck.ex + row * a.ck.lde, c, t,
-                                  tpr, d);
+      const int at = c * tpr + t;
+      if (q != nullptr) {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) split(v[c][j], f[2 * j], f[2 * j + 1]);
+        ckpt_store_chunk<T, true>(f, q, ex, c, t, tpr, d);
+      }
+      if (8 * at >= d) continue;
       if (live) {
-        float w[8];
+        f32x2 w[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[c][j] = (v[c][j] - mean) * rstd;
+        for (int j = 0; j < 4; ++j)
+          v[c][j] = mul2(KIND == GRPO_NORM_LAYER ? add2(v[c][j], shift) : v[c][j], scale);
         if (a.weight != nullptr) {
-          read_param(sw, c, t, tpr, d, w);
+          read_param(sw32, at, 2 * d, w);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[c][j] *= w[j];
+          for (int j = 0; j < 4; ++j) v[c][j] = mul2(v[c][j], w[j]);
         }
         if (a.bias != nullptr) {
-          read_param(sb, c, t, tpr, d, w);
+          read_param(sb32, at, 2 * d, w);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[c][j] += w[j];
+          for (int j = 0; j < 4; ++j) v[c][j] = add2(v[c][j], w[j]);
         }
       }
-      store_chunk<T, true>(y + row * a.ldy, narrow<T>(v[c]), c, t, tpr, d);
+      store_raw(y + 8 * at, narrow2<T>(v[c]));
     }
     if (t == 0) {
+      const long long row = row0 + step * i;
       if (a.mean != nullptr) a.mean[row] = mean;
       if (a.rstd != nullptr) a.rstd[row] = rstd;
+    }
+    y += step * a.ldy;
+    if (z != nullptr) z += step * a.ldz;
+    if (q != nullptr) {
+      q += step * a.ck.ldq;
+      ex += step * a.ck.lde;
     }
     live = live1;
   }
@@ -544,76 +647,82 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormBwdArgs a) {
 
 // The aligned form of norm_bwd_kernel, its rows in flight as in
 // norm_fwd_ring_kernel. A slot holds dy, then x (or its bytes and exponents),
-// then dres.
-template <typename T, int CH, bool CK, bool DB>
-__global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const NormBwdArgs a, const Ring ring) {
+// then dres. FULL: layer norm, or a bias gradient; else neither.
+template <typename T, int CH, bool CK, bool FULL>
+__global__ void __launch_bounds__(ring_threads(CH)) norm_bwd_ring_kernel(const NormBwdArgs a, const Ring ring) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float2 red[8][2 * 32];
+  __shared__ float2 red[kMaxRows][2 * 32];
   const int t = threadIdx.x, tpr = blockDim.x, g = threadIdx.y, d = a.d;
+  const int warps = tpr >> 5;
   uint64_t* const bars = reinterpret_cast<uint64_t*>(smem) + g * kMaxSlots;
   float* const sw = reinterpret_cast<float*>(smem + kRingBars);
   uint8_t* const ring0 = reinterpret_cast<uint8_t*>(sw + (a.weight != nullptr ? d : 0));
+  const uint32_t sw32 = smem_u32(sw);
   const uint32_t rows0 = smem_u32(ring0) + g * ring.slots * ring.row_bytes;
   const uint32_t t_bytes = d * sizeof(T);
-  const uint32_t x_bytes =
-      CK ? static_cast<uint32_t>(a.ck.ldq + a.ck.lde) : t_bytes;  // rows of 16 bytes
-  const T* dy = static_cast<const T*>(a.dy);
-  const T* dres = static_cast<const T*>(a.dres);
-  T* dx = static_cast<T*>(a.dx);
+  const uint32_t q_bytes = static_cast<uint32_t>(a.ck.ldq), e_bytes = static_cast<uint32_t>(a.ck.lde);
+  const uint32_t x_bytes = CK ? q_bytes + e_bytes : t_bytes;  // rows of 16 bytes
+  const bool res = a.dres != nullptr, layer = FULL && a.kind == GRPO_NORM_LAYER;
   const long long step = static_cast<long long>(gridDim.x) * blockDim.y;
-  long long row = static_cast<long long>(blockIdx.x) * blockDim.y + g;
-  uint32_t pending = 0;  // thread 0: slots whose copies have not been waited for
-  const auto issue = [&](long long r, int slot) {
-    if (!row_live(a.mask, r, a.n)) return;
+  const long long row0 = static_cast<long long>(blockIdx.x) * blockDim.y + g;
+  const int count = row_count(row0, a.n, step);
+  const uint8_t* const mask = a.mask;
+  uint32_t pending = 0;
+  int fetched = 0;
+  const auto fetch = [&](int slot) {
+    if (fetched >= count) return;
+    const long long r = row0 + step * fetched++;
+    if (mask != nullptr && mask[r] == 0) return;
     pending |= 1u << slot;
     const uint32_t dst = rows0 + slot * ring.row_bytes;
-    mbar_arrive_expect_tx(&bars[slot], t_bytes + x_bytes + (dres != nullptr ? t_bytes : 0));
-    bulk_load(dst, dy + r * a.lddy, t_bytes, &bars[slot]);
+    mbar_arrive_expect_tx(&bars[slot], t_bytes + x_bytes + (res ? t_bytes : 0));
+    bulk_load(dst, static_cast<const T*>(a.dy) + r * a.lddy, t_bytes, &bars[slot]);
     if (CK) {
-      bulk_load(dst + t_bytes, a.ck.q + r * a.ck.ldq, static_cast<uint32_t>(a.ck.ldq), &bars[slot]);
-      bulk_load(dst + t_bytes + static_cast<uint32_t>(a.ck.ldq), a.ck.ex + r * a.ck.lde,
-                static_cast<uint32_t>(a.ck.lde), &bars[slot]);
+      bulk_load(dst + t_bytes, a.ck.q + r * a.ck.ldq, q_bytes, &bars[slot]);
+      bulk_load(dst + t_bytes + q_bytes, a.ck.ex + r * a.ck.lde, e_bytes, &bars[slot]);
     } else {
       bulk_load(dst + t_bytes, static_cast<const T*>(a.x) + r * a.ldx, t_bytes, &bars[slot]);
     }
-    if (dres != nullptr) bulk_load(dst + t_bytes + x_bytes, dres + r * a.lddres, t_bytes, &bars[slot]);
+    if (res)
+      bulk_load(dst + t_bytes + x_bytes, static_cast<const T*>(a.dres) + r * a.lddres, t_bytes,
+                &bars[slot]);
   };
   if (t == 0) {
     for (int s = 0; s < ring.slots; ++s) mbar_init(&bars[s], 1);
     fence_mbar_init();
-    for (int s = 0; s < ring.slots; ++s) issue(row + s * step, s);
+    for (int s = 0; s < ring.slots; ++s) fetch(s);
   }
-  if (a.weight != nullptr)
-    stage_param(sw, a.weight, a.wtype, 1.f, d, g * tpr + t, tpr * blockDim.y);
+  if (a.weight != nullptr) stage_param(sw, a.weight, a.wtype, d, g * tpr + t, tpr * blockDim.y);
   __syncthreads();
 
-  float dw[CH][8], db[DB ? CH : 1][8];
+  f32x2 dw[CH][4], db[FULL ? CH : 1][4];
 #pragma unroll
   for (int c = 0; c < CH; ++c)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      dw[c][j] = 0.f;
-      if (DB) db[DB ? c : 0][j] = 0.f;
+    for (int j = 0; j < 4; ++j) {
+      dw[c][j] = 0ull;
+      if (FULL) db[FULL ? c : 0][j] = 0ull;
     }
   const float inv_d = 1.f / static_cast<float>(d);
+  T* dx = static_cast<T*>(a.dx) + row0 * a.lddx;
   int phase = 0, slot = 0;
   uint32_t parity = 0;
   bool ok = true;
-  bool live = row_live(a.mask, row, a.n);
-  float rstd1 = live ? a.rstd[row] : 0.f;
-  float mean1 = live && a.kind != GRPO_NORM_RMS ? a.mean[row] : 0.f;
-  for (; row < a.n; row += step) {
-    const long long next = row + step;
-    const bool live1 = row_live(a.mask, next, a.n);
+  bool live = count > 0 && (mask == nullptr || mask[row0] != 0);
+  float rstd1 = live ? a.rstd[row0] : 0.f;
+  float mean1 = live && layer ? a.mean[row0] : 0.f;
+  for (int i = 0; i < count; ++i) {
+    const long long next = row0 + step * (i + 1);
+    const bool live1 = i + 1 < count && (mask == nullptr || mask[next] != 0);
     const float rstd = rstd1, mean = mean1;
     rstd1 = live1 ? a.rstd[next] : 0.f;
-    mean1 = live1 && a.kind != GRPO_NORM_RMS ? a.mean[next] : 0.f;
+    mean1 = live1 && layer ? a.mean[next] : 0.f;
     if (!live) {
-      const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (t == 0 && ok) issue(row + ring.slots * step, slot);
+      const f32x2 zero[4] = {0ull, 0ull, 0ull, 0ull};
+      if (t == 0 && ok) fetch(slot);
 #pragma unroll
       for (int c = 0; c < CH; ++c)
-        store_chunk<T, true>(dx + row * a.lddx, narrow<T>(zero), c, t, tpr, d);
+        if ((c * tpr + t) * 8 < d) store_raw(dx + (c * tpr + t) * 8, narrow2<T>(zero));
     } else {
       ok = ok && row_wait(&bars[slot], (parity >> slot) & 1u);
       if (ok) {
@@ -621,74 +730,74 @@ __global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const NormBwdArgs a,
         pending &= ~(1u << slot);
       }
       const uint32_t src = rows0 + slot * ring.row_bytes;
-      float u[CH][8], h[CH][8];
+      const f32x2 scale = pair(rstd, rstd), shift = pair(-mean, -mean);
+      f32x2 u[CH][4], h[CH][4];
       Raw8<T> rr[CH];
-      float2 s = make_float2(0.f, 0.f);
+      f32x2 su = 0ull, suh = 0ull;
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        widen(lds_chunk<T>(src, c, t, tpr, d), u[c]);
+        const int at = c * tpr + t;
+        if (8 * at >= d) continue;
+        const uint32_t off = at * sizeof(Raw8<T>);
+        widen2(lds_raw<T>(src + off), u[c]);
         if (CK) {
-          RawCkpt<true> q;
-          const int i = c * tpr + t;
-          q.w = make_uint2(0, 0);
-          q.ex[0] = kCkptBias;
-          if (8 * i < d) {
-            q.w = lds_v2(src + t_bytes + 8 * i);
-            q.ex[0] = static_cast<uint8_t>(
-                lds_u8(src + t_bytes + static_cast<uint32_t>(a.ck.ldq) + i / 4));
-          }
-          ckpt_widen<true>(q, h[c]);
+          ckpt_widen2(lds_v2(src + t_bytes + 8 * at),
+                      ckpt_factor(lds_u8(src + t_bytes + q_bytes + at / 4)), h[c]);
         } else {
-          widen(lds_chunk<T>(src + t_bytes, c, t, tpr, d), h[c]);
+          widen2(lds_raw<T>(src + t_bytes + off), h[c]);
         }
-        if (dres != nullptr) rr[c] = lds_chunk<T>(src + t_bytes + x_bytes, c, t, tpr, d);
+        if (res) rr[c] = lds_raw<T>(src + t_bytes + x_bytes + off);
+        f32x2 w[4];
+        if (a.weight != nullptr) read_param(sw32, at, 2 * d, w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          h[c][j] = (h[c][j] - mean) * rstd;
-          dw[c][j] += u[c][j] * h[c][j];
-          if (DB) db[DB ? c : 0][j] += u[c][j];
-        }
-        if (a.weight != nullptr) {
-          float w[8];
-          read_param(sw, c, t, tpr, d, w);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) u[c][j] *= w[j];
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          s.x += u[c][j];
-          s.y += u[c][j] * h[c][j];
+        for (int j = 0; j < 4; ++j) {
+          if (FULL) h[c][j] = add2(h[c][j], shift);
+          h[c][j] = mul2(h[c][j], scale);
+          dw[c][j] = fma2(u[c][j], h[c][j], dw[c][j]);
+          if (FULL) db[FULL ? c : 0][j] = add2(u[c][j], db[FULL ? c : 0][j]);
+          if (a.weight != nullptr) u[c][j] = mul2(u[c][j], w[j]);
+          if (FULL) su = add2(u[c][j], su);
+          suh = fma2(u[c][j], h[c][j], suh);
         }
       }
-      s = row_sum2(s, t, tpr, g + 1, red[g], phase);
-      __syncwarp();
-      if (t == 0 && ok) issue(row + ring.slots * step, slot);
-      const float c1 = a.kind != GRPO_NORM_RMS ? s.x * inv_d : 0.f;
+      float2 s = make_float2(FULL ? sum_of(su) : 0.f, sum_of(suh));
+      if (FULL) s = warp_sum2(s);
+      else s.y = warp_sum(s.y);
+      s = join_warps(s, t, warps, g + 1, red[g], phase);
+      if (t == 0 && ok) fetch(slot);
+      const float c1 = layer ? s.x * inv_d : 0.f;
       const float c2 = ok ? s.y * inv_d : __uint_as_float(0x7fc00000u);
+      const f32x2 n1 = pair(-c1, -c1), n2 = pair(-c2, -c2);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
+        const int at = c * tpr + t;
+        if (8 * at >= d) continue;
+        f32x2 r[4] = {0ull, 0ull, 0ull, 0ull};
+        if (res) widen2(rr[c], r);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) u[c][j] = rstd * (u[c][j] - c1 - h[c][j] * c2);
-        if (dres != nullptr) {
-          float r[8];
-          widen(rr[c], r);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) u[c][j] += r[j];
+        for (int j = 0; j < 4; ++j) {
+          if (FULL) u[c][j] = add2(u[c][j], n1);
+          u[c][j] = fma2(fma2(h[c][j], n2, u[c][j]), scale, r[j]);
         }
-        store_chunk<T, true>(dx + row * a.lddx, narrow<T>(u[c]), c, t, tpr, d);
+        store_raw(dx + 8 * at, narrow2<T>(u[c]));
       }
       if (!ok) {
 #pragma unroll
         for (int c = 0; c < CH; ++c)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) dw[c][j] = __uint_as_float(0x7fc00000u);
+          for (int j = 0; j < 4; ++j) {
+            dw[c][j] = ~0ull;  // NaN
+            if (FULL) db[FULL ? c : 0][j] = ~0ull;
+          }
       }
     }
     if (++slot == ring.slots) slot = 0;
+    dx += step * a.lddx;
     live = live1;
   }
   land(bars, ring.slots, parity, pending);
-  if (a.dweight == nullptr && !DB) return;
+  const bool want_db = FULL && a.dbias != nullptr;
+  if (a.dweight == nullptr && !want_db) return;
   // The CTA's rows in flight, added in their order; the rings have been read.
   float* const cw = blockDim.y > 1 ? reinterpret_cast<float*>(ring0) : nullptr;
   float* const cb = cw != nullptr ? cw + d : nullptr;
@@ -697,10 +806,10 @@ __global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const NormBwdArgs a,
   if (cw == nullptr) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int col = chunk_col<true>(c, 0, t, tpr);
-      if (col >= d) continue;
-      store8(pw + col, dw[c]);
-      if (DB) store8(pb + col, db[DB ? c : 0]);
+      const int at = c * tpr + t;
+      if (8 * at >= d) continue;
+      store_raw(pw + 8 * at, narrow2<float>(dw[c]));
+      if (want_db) store_raw(pb + 8 * at, narrow2<float>(db[FULL ? c : 0]));
     }
     return;
   }
@@ -708,21 +817,25 @@ __global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const NormBwdArgs a,
   for (int k = 0; k < static_cast<int>(blockDim.y); ++k) {
     if (g == k) {
 #pragma unroll
-      for (int c = 0; c < CH; ++c)
+      for (int c = 0; c < CH; ++c) {
+        const int at = c * tpr + t;
+        if (8 * at >= d) continue;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int col = chunk_col<true>(c, j, t, tpr);
-          if (col < d) {
-            cw[col] = k == 0 ? dw[c][j] : cw[col] + dw[c][j];
-            if (DB) cb[col] = k == 0 ? db[DB ? c : 0][j] : cb[col] + db[DB ? c : 0][j];
+        for (int j = 0; j < 4; ++j) {
+          f32x2* pc = reinterpret_cast<f32x2*>(cw + 8 * at + 2 * j);
+          *pc = k == 0 ? dw[c][j] : add2(*pc, dw[c][j]);
+          if (want_db) {
+            f32x2* pd = reinterpret_cast<f32x2*>(cb + 8 * at + 2 * j);
+            *pd = k == 0 ? db[FULL ? c : 0][j] : add2(*pd, db[FULL ? c : 0][j]);
           }
         }
+      }
     }
     __syncthreads();
   }
   for (int col = g * tpr + t; col < d; col += tpr * blockDim.y) {
     pw[col] = cw[col];
-    if (DB) pb[col] = cb[col];
+    if (want_db) pb[col] = cb[col];
   }
 }
 
@@ -864,11 +977,11 @@ __global__ void __launch_bounds__(256) norm_bwd_finish_kernel(const float* __res
   if (out != nullptr) out[col] = add != nullptr ? add[col] + s : s;
 }
 
-// Threads of a row and rows of a CTA for D columns held in registers: 16
-// values a thread (8 up to 256 columns).
+// Threads of a row and rows of a CTA for D columns held in registers.
 struct RowShape {
   int tpr, rows, ch;
 };
+// One by one: 16 values a thread (8 up to 256 columns).
 RowShape row_shape(int d) {
   RowShape s;
   s.ch = d <= 256 ? 1 : 2;
@@ -876,6 +989,22 @@ RowShape row_shape(int d) {
   s.tpr = (d + per * 32 - 1) / (per * 32) * 32;
   s.rows = s.tpr >= kRowThreads ? 1 : kRowThreads / s.tpr;
   return s;
+}
+// Aligned: the most values a thread, up to 8 `most`, that leave no more than a
+// tenth of the threads idle (else the fewest idle ones); CTAs of about
+// `threads` threads.
+RowShape ring_shape(int d, int most, int threads) {
+  RowShape best = {0, 0, 0};
+  int best_room = 0;
+  for (int ch = most; ch >= 1; --ch) {
+    const int tpr = (d + 256 * ch - 1) / (256 * ch) * 32;
+    const int room = tpr * 8 * ch;
+    if (tpr > 512 || (best.ch != 0 && room >= best_room)) continue;
+    best = {tpr, std::min(kMaxRows, std::max(1, threads / tpr)), ch};
+    best_room = room;
+    if (10 * room <= 11 * d) break;
+  }
+  return best;
 }
 
 // CTAs of `threads` threads resident on the device, looked up once per kernel.
@@ -923,9 +1052,9 @@ cudaError_t ctas_per_sm(int threads, size_t smem, int* n) {
   return cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, Kernel, threads, smem);
 }
 
-template <typename T, int CH>
+template <typename T, int CH, int KIND>
 cudaError_t fwd_ring(const NormFwdArgs& a, const RowShape& s, int sms, cudaStream_t st) {
-  constexpr auto kernel = norm_fwd_ring_kernel<T, CH>;
+  constexpr auto kernel = norm_fwd_ring_kernel<T, CH, KIND>;
   const size_t fixed = kRingBars + sizeof(float) * a.d *
                                        ((a.weight != nullptr) + (a.bias != nullptr));
   const Ring ring = make_ring(a.d * sizeof(T) * (a.res != nullptr ? 2 : 1), s.rows, fixed);
@@ -938,6 +1067,17 @@ cudaError_t fwd_ring(const NormFwdArgs& a, const RowShape& s, int sms, cudaStrea
   LaunchTimer timer("norm_fwd_kernel", st);
   kernel<<<grid, dim3(s.tpr, s.rows), smem, st>>>(a, ring);
   return cudaGetLastError();
+}
+
+template <typename T, int KIND>
+cudaError_t fwd_aligned(const NormFwdArgs& a, int sms, cudaStream_t st) {
+  const RowShape s = ring_shape(a.d, 4, kRowThreads);
+  switch (s.ch) {
+    case 1: return fwd_ring<T, 1, KIND>(a, s, sms, st);
+    case 2: return fwd_ring<T, 2, KIND>(a, s, sms, st);
+    case 3: return fwd_ring<T, 3, KIND>(a, s, sms, st);
+    default: return fwd_ring<T, 4, KIND>(a, s, sms, st);
+  }
 }
 
 template <typename T, bool VEC, int CH>
@@ -959,11 +1099,13 @@ cudaError_t fwd_any(const NormFwdArgs& a, int sms, cudaStream_t st) {
     norm_fwd_long_kernel<T, VEC><<<grid, 512, 0, st>>>(a);
     return cudaGetLastError();
   }
-  const RowShape s = row_shape(a.d);
-  if constexpr (VEC)
-    return s.ch == 1 ? fwd_ring<T, 1>(a, s, sms, st) : fwd_ring<T, 2>(a, s, sms, st);
-  else
+  if constexpr (VEC) {
+    return a.kind == GRPO_NORM_RMS ? fwd_aligned<T, GRPO_NORM_RMS>(a, sms, st)
+                                   : fwd_aligned<T, GRPO_NORM_LAYER>(a, sms, st);
+  } else {
+    const RowShape s = row_shape(a.d);
     return s.ch == 1 ? fwd<T, false, 1>(a, s, sms, st) : fwd<T, false, 2>(a, s, sms, st);
+  }
 }
 
 cudaError_t finish(const NormBwdArgs& a, int rows, cudaStream_t st) {
@@ -975,9 +1117,9 @@ cudaError_t finish(const NormBwdArgs& a, int rows, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-template <typename T, int CH, bool CK, bool DB>
+template <typename T, int CH, bool CK, bool FULL>
 cudaError_t bwd_ring(const NormBwdArgs& a, const RowShape& s, int sms, cudaStream_t st) {
-  constexpr auto kernel = norm_bwd_ring_kernel<T, CH, CK, DB>;
+  constexpr auto kernel = norm_bwd_ring_kernel<T, CH, CK, FULL>;
   const size_t fixed = kRingBars + (a.weight != nullptr ? sizeof(float) * a.d : 0);
   const uint32_t t_bytes = a.d * sizeof(T);
   const Ring ring =
@@ -985,7 +1127,7 @@ cudaError_t bwd_ring(const NormBwdArgs& a, const RowShape& s, int sms, cudaStrea
                     (CK ? static_cast<uint32_t>(a.ck.ldq + a.ck.lde) : t_bytes),
                 s.rows, fixed);
   size_t smem = static_cast<size_t>(ring.slots) * ring.row_bytes * s.rows;
-  if (s.rows > 1) smem = std::max(smem, static_cast<size_t>(a.d) * (DB ? 8 : 4));
+  if (s.rows > 1) smem = std::max(smem, static_cast<size_t>(a.d) * 8);
   smem += fixed;
   int per_sm = 0;
   cudaError_t e = ctas_per_sm<kernel>(s.tpr * s.rows, smem, &per_sm);
@@ -999,6 +1141,15 @@ cudaError_t bwd_ring(const NormBwdArgs& a, const RowShape& s, int sms, cudaStrea
   }
   e = cudaGetLastError();
   return e != cudaSuccess ? e : finish(a, grid, st);
+}
+
+template <typename T, bool CK, bool FULL>
+cudaError_t bwd_aligned(const NormBwdArgs& a, int sms, cudaStream_t st) {
+  const RowShape s = ring_shape(a.d, 2, kRowThreads);
+  switch (s.ch) {
+    case 1: return bwd_ring<T, 1, CK, FULL>(a, s, sms, st);
+    default: return bwd_ring<T, 2, CK, FULL>(a, s, sms, st);
+  }
 }
 
 template <typename T, bool VEC, int CH, bool CK, bool DB>
@@ -1037,13 +1188,12 @@ cudaError_t bwd_any(const NormBwdArgs& a, int sms, cudaStream_t st) {
     e = cudaGetLastError();
     return e != cudaSuccess ? e : finish(a, groups, st);
   }
-  const RowShape s = row_shape(a.d);
   const bool db = a.dbias != nullptr;
   if constexpr (VEC) {
-    if (s.ch == 1)
-      return db ? bwd_ring<T, 1, CK, true>(a, s, sms, st) : bwd_ring<T, 1, CK, false>(a, s, sms, st);
-    return db ? bwd_ring<T, 2, CK, true>(a, s, sms, st) : bwd_ring<T, 2, CK, false>(a, s, sms, st);
+    return db || a.kind == GRPO_NORM_LAYER ? bwd_aligned<T, CK, true>(a, sms, st)
+                                           : bwd_aligned<T, CK, false>(a, sms, st);
   } else {
+    const RowShape s = row_shape(a.d);
     if (s.ch == 1)
       return db ? bwd<T, false, 1, CK, true>(a, s, sms, st)
                 : bwd<T, false, 1, CK, false>(a, s, sms, st);
@@ -1067,9 +1217,8 @@ int norm_bwd_partials(long long n, int d) {
     return static_cast<int>(std::min<long long>(std::max(1, 8 * 152 / ((d + 255) / 256)),
                                                 std::max<long long>(1, (n + 7) / 8)));
   }
-  const int rows = row_shape(d).rows;
-  return static_cast<int>(
-      std::min<long long>(kNormMaxPartials, std::max<long long>(1, (n + rows - 1) / rows)));
+  // A CTA takes one row at least.
+  return static_cast<int>(std::min<long long>(kNormMaxPartials, std::max<long long>(1, n)));
 }
 
 cudaError_t launch_norm_fwd(const NormFwdArgs& a, int dtype, bool vec, int sms, cudaStream_t st) {

@@ -180,49 +180,121 @@ __device__ __forceinline__ bool row_wait(uint64_t* bar, uint32_t parity) {
   return true;
 }
 
-// Chunk c of a row in shared memory (VEC layout).
+// Two fp32 in one 64-bit register: Blackwell multiplies and adds them with one
+// instruction, and these kernels are near the issue limit.
+using f32x2 = unsigned long long;
+
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void split(f32x2 v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float sum_of(f32x2 v) {
+  float a, b;
+  split(v, a, b);
+  return a + b;
+}
+
+// 8 values of a chunk as four pairs.
+__device__ __forceinline__ void widen2(const Raw8<__nv_bfloat16>& r, f32x2 (&v)[4]) {
+  const uint32_t* u = reinterpret_cast<const uint32_t*>(&r);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    v[j] = pair(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xffff0000u));
+}
+__device__ __forceinline__ void widen2(const Raw8<__half>& r, f32x2 (&v)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = pair(to_f32(r.e[2 * j]), to_f32(r.e[2 * j + 1]));
+}
+__device__ __forceinline__ void widen2(const Raw8<float>& r, f32x2 (&v)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = pair(r.e[2 * j], r.e[2 * j + 1]);
+}
 template <typename T>
-__device__ __forceinline__ Raw8<T> lds_chunk(uint32_t row, int c, int t, int tpr, int d) {
+__device__ __forceinline__ Raw8<T> narrow2(const f32x2 (&v)[4]) {
+  Raw8<T> r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float a, b;
+    split(v[j], a, b);
+    from_f32x2(a, b, &r.e[2 * j]);
+  }
+  return r;
+}
+
+// A chunk in shared or global memory, 16 bytes at a time.
+template <typename T>
+__device__ __forceinline__ Raw8<T> lds_raw(uint32_t p) {
   Raw8<T> r;
   uint4* w = reinterpret_cast<uint4*>(&r);
-  const int i = c * tpr + t;
 #pragma unroll
-  for (int k = 0; k < static_cast<int>(sizeof(r) / 16); ++k)
-    w[k] = 8 * i < d ? lds_v4(row + i * sizeof(r) + 16 * k) : make_uint4(0, 0, 0, 0);
+  for (int k = 0; k < static_cast<int>(sizeof(r) / 16); ++k) w[k] = lds_v4(p + 16 * k);
   return r;
+}
+template <typename T>
+__device__ __forceinline__ void store_raw(T* p, const Raw8<T>& r) {
+  const uint4* w = reinterpret_cast<const uint4*>(&r);
+#pragma unroll
+  for (int k = 0; k < static_cast<int>(sizeof(r) / 16); ++k) reinterpret_cast<uint4*>(p)[k] = w[k];
 }
 
 // A weight or bias vector as fp32 in shared memory: the first four columns of
 // every chunk, then the other four, so that neighbouring threads read
-// neighbouring 16 bytes. `half`: 4 times the number of chunks.
-__device__ __forceinline__ void stage_param(float* dst, const void* p, int type, float none, int d,
-                                            int thread, int threads) {
+// neighbouring 16 bytes.
+__device__ __forceinline__ void stage_param(float* dst, const void* p, int type, int d, int thread,
+                                            int threads) {
   const int half = d / 2;
   for (int col = thread; col < d; col += threads) {
     const int j = col & 7;
-    dst[(j >= 4 ? half : 0) + (col >> 3) * 4 + (j & 3)] =
-        p != nullptr ? load_param(p, type, col) : none;
+    dst[(j >= 4 ? half : 0) + (col >> 3) * 4 + (j & 3)] = load_param(p, type, col);
   }
 }
+// Chunk i of it; `half_bytes`: 2 d.
+__device__ __forceinline__ void read_param(uint32_t s, int i, uint32_t half_bytes, f32x2 (&w)[4]) {
+  const uint32_t p = s + 16 * i;
+  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(w[0]), "=l"(w[1]) : "r"(p) : "memory");
+  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];"
+               : "=l"(w[2]), "=l"(w[3])
+               : "r"(p + half_bytes)
+               : "memory");
+}
 
-__device__ __forceinline__ void read_param(const float* s, int c, int t, int tpr, int d,
-                                           float (&w)[8]) {
-  const int i = c * tpr + t;
-  if (8 * i >= d) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = 0.f;
-    return;
+// Joins the warps' sums of a row (after warp sums): every thread gets the total,
+// added in warp order. As row_sum2, with the join by plain loads.
+__device__ __forceinline__ float2 join_warps(float2 v, int t, int warps, int bar, float2* sh,
+                                             int& phase) {
+  if (warps == 1) {
+    __syncwarp();
+    return v;
   }
-  const float4 a = *reinterpret_cast<const float4*>(s + 4 * i);
-  const float4 b = *reinterpret_cast<const float4*>(s + d / 2 + 4 * i);
-  w[0] = a.x;
-  w[1] = a.y;
-  w[2] = a.z;
-  w[3] = a.w;
-  w[4] = b.x;
-  w[5] = b.y;
-  w[6] = b.z;
-  w[7] = b.w;
+  float2* s = sh + phase * 32;
+  phase ^= 1;
+  if ((t & 31) == 0) s[t >> 5] = v;
+  named_barrier(bar, warps * 32);
+  float2 r = s[0];
+  for (int k = 1; k < warps; ++k) {
+    r.x += s[k].x;
+    r.y += s[k].y;
+  }
+  return r;
 }
 
 // ---------------------------------------------------- 8-bit checkpoints ----
@@ -402,6 +474,15 @@ __device__ __forceinline__ void ckpt_widen(const RawCkpt<VEC>& r, float (&v)[8])
     const float2 f = unpack_e4m3x2(w & 0xffffu);
     v[2 * h] = f.x * ckpt_factor(r.ex[VEC ? 0 : 2 * h]);
     v[2 * h + 1] = f.y * ckpt_factor(r.ex[VEC ? 0 : 2 * h + 1]);
+  }
+}
+
+__device__ __forceinline__ void ckpt_widen2(uint2 q, float f, f32x2 (&v)[4]) {
+  const f32x2 ff = pair(f, f);
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    const float2 x = unpack_e4m3x2((h < 2 ? q.x : q.y) >> (16 * (h & 1)));
+    v[h] = mul2(pair(x.x, x.y), ff);
   }
 }
 
