@@ -221,7 +221,7 @@ __device__ __forceinline__ int row_count(long long row, long long n, long long s
 template <typename T, int CH, int KIND>
 __global__ void __launch_bounds__(ring_threads(CH)) norm_fwd_ring_kernel(const NormFwdArgs a, const Ring ring) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float2 red[kMaxRows][2 * 32];
+  __shared__ __align__(16) float red[kMaxRows][2 * 2 * 16];
   const int t = threadIdx.x, tpr = blockDim.x, g = threadIdx.y, d = a.d;
   const int warps = tpr >> 5;
   uint64_t* const bars = reinterpret_cast<uint64_t*>(smem) + g * kMaxSlots;
@@ -254,6 +254,7 @@ __global__ void __launch_bounds__(ring_threads(CH)) norm_fwd_ring_kernel(const N
     fence_mbar_init();
     for (int s = 0; s < ring.slots; ++s) fetch(s);
   }
+  for (int k = t; k < 2 * 2 * 16; k += tpr) red[g][k] = 0.f;
   if (a.weight != nullptr) stage_param(sw, a.weight, a.wtype, d, g * tpr + t, tpr * blockDim.y);
   if (a.bias != nullptr) stage_param(sb, a.bias, a.wtype, d, g * tpr + t, tpr * blockDim.y);
   __syncthreads();
@@ -311,9 +312,9 @@ __global__ void __launch_bounds__(ring_threads(CH)) norm_fwd_ring_kernel(const N
         for (int c = 0; c < CH; ++c)
 #pragma unroll
           for (int j = 0; j < 4; ++j) s[j & 1] = fma2(v[c][j], v[c][j], s[j & 1]);
-        const float2 m = join_warps(make_float2(warp_sum(sum_of(add2(s[0], s[1]))), 0.f), t, warps,
-                                    g + 1, red[g], phase);
-        rstd = rsqrtf(m.x * inv_d + a.eps);
+        float m[1] = {warp_sum(sum_of(add2(s[0], s[1])))};
+        join_warps(m, t, warps, g + 1, red[g], phase);
+        rstd = rsqrtf(m[0] * inv_d + a.eps);
       } else {
         // Each warp centres its values on their own mean; the warps' sums are
         // then joined as if all had been centred on the row's.
@@ -338,19 +339,21 @@ __global__ void __launch_bounds__(ring_threads(CH)) norm_fwd_ring_kernel(const N
         const float m2 = warp_sum(sum_of(add2(s[0], s[1])));
         float total = sum, centred = m2;
         if (warps > 1) {
-          float2* sh = red[g] + phase * 32;
+          float* sh = red[g] + phase * 2 * 16;
           phase ^= 1;
-          // (sum, m2) of a warp; its count follows from its index.
-          if ((t & 31) == 0) sh[t >> 5] = make_float2(sum, m2);
+          if ((t & 31) == 0) {
+            sh[t >> 5] = sum;
+            sh[16 + (t >> 5)] = m2;
+          }
           named_barrier(g + 1, tpr);
           total = 0.f;
-          for (int k = 0; k < warps; ++k) total += sh[k].x;
+          for (int k = 0; k < warps; ++k) total += sh[k];
           const float mu = total * inv_d;
           centred = 0.f;
           for (int k = 0; k < warps; ++k) {
             const float nk = warp_columns<CH>(k, tpr, d);
-            const float e = nk > 0.f ? sh[k].x / nk - mu : 0.f;
-            centred += sh[k].y + nk * e * e;
+            const float e = nk > 0.f ? sh[k] / nk - mu : 0.f;
+            centred += sh[16 + k] + nk * e * e;
           }
         } else {
           __syncwarp();
@@ -651,7 +654,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormBwdArgs a) {
 template <typename T, int CH, bool CK, bool FULL>
 __global__ void __launch_bounds__(ring_threads(CH)) norm_bwd_ring_kernel(const NormBwdArgs a, const Ring ring) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float2 red[kMaxRows][2 * 32];
+  __shared__ __align__(16) float red[kMaxRows][2 * 2 * 16];
   const int t = threadIdx.x, tpr = blockDim.x, g = threadIdx.y, d = a.d;
   const int warps = tpr >> 5;
   uint64_t* const bars = reinterpret_cast<uint64_t*>(smem) + g * kMaxSlots;
@@ -692,6 +695,8 @@ __global__ void __launch_bounds__(ring_threads(CH)) norm_bwd_ring_kernel(const N
     fence_mbar_init();
     for (int s = 0; s < ring.slots; ++s) fetch(s);
   }
+  for (int k = t; k < 2 * 2 * 16; k += tpr) red[g][k] = 0.f;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (a.weight != nullptr) stage_param(sw, a.weight, a.wtype, d, g * tpr + t, tpr * blockDim.y);
   __syncthreads();
 
@@ -760,13 +765,13 @@ __global__ void __launch_bounds__(ring_threads(CH)) norm_bwd_ring_kernel(const N
           suh = fma2(u[c][j], h[c][j], suh);
         }
       }
-      float2 s = make_float2(FULL ? sum_of(su) : 0.f, sum_of(suh));
-      if (FULL) s = warp_sum2(s);
-      else s.y = warp_sum(s.y);
-      s = join_warps(s, t, warps, g + 1, red[g], phase);
+      float s[FULL ? 2 : 1];
+      s[0] = warp_sum(sum_of(suh));
+      if (FULL) s[FULL ? 1 : 0] = warp_sum(sum_of(su));
+      join_warps(s, t, warps, g + 1, red[g], phase);
       if (t == 0 && ok) fetch(slot);
-      const float c1 = layer ? s.x * inv_d : 0.f;
-      const float c2 = ok ? s.y * inv_d : __uint_as_float(0x7fc00000u);
+      const float c1 = layer ? s[FULL ? 1 : 0] * inv_d : 0.f;
+      const float c2 = ok ? s[0] * inv_d : __uint_as_float(0x7fc00000u);
       const f32x2 n1 = pair(-c1, -c1), n2 = pair(-c2, -c2);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
@@ -953,25 +958,27 @@ __global__ void __launch_bounds__(256) norm_bwd_cols_kernel(const NormBwdArgs a)
 }
 
 // dw and db from the CTAs' partial sums: 32 columns a CTA, the partial rows
-// dealt to its 8 warps, whose sums are added in warp order.
-__global__ void __launch_bounds__(256) norm_bwd_finish_kernel(const float* __restrict__ partials,
+// dealt to its 16 warps, whose sums are added in warp order. Launched while the
+// backward kernel still runs (it waits for its end here): 3 us less a call.
+__global__ void __launch_bounds__(512) norm_bwd_finish_kernel(const float* __restrict__ partials,
                                                               int rows, int d, float* dweight,
                                                               float* dbias, const float* add_dw,
                                                               const float* add_db) {
-  __shared__ float sh[8][33];
+  __shared__ float sh[16][33];
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + lane;
   const bool bias = blockIdx.y == 1;
   const float* p = partials + (bias ? static_cast<long long>(rows) * d : 0);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float s = 0.f;
   if (col < d) {
 #pragma unroll 8
-    for (int r = g; r < rows; r += 8) s += p[static_cast<long long>(r) * d + col];
+    for (int r = g; r < rows; r += 16) s += p[static_cast<long long>(r) * d + col];
   }
   sh[g][lane] = s;
   __syncthreads();
   if (g != 0 || col >= d) return;
-  for (int k = 1; k < 8; ++k) s += sh[k][lane];
+  for (int k = 1; k < 16; ++k) s += sh[k][lane];
   const float* add = bias ? add_db : add_dw;
   float* out = bias ? dbias : dweight;
   if (out != nullptr) out[col] = add != nullptr ? add[col] + s : s;
@@ -1111,10 +1118,18 @@ cudaError_t fwd_any(const NormFwdArgs& a, int sms, cudaStream_t st) {
 cudaError_t finish(const NormBwdArgs& a, int rows, cudaStream_t st) {
   if (a.dweight == nullptr && a.dbias == nullptr) return cudaSuccess;
   const dim3 grid((a.d + 31) / 32, a.dbias != nullptr ? 2 : 1);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(512);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   LaunchTimer timer("norm_bwd_finish_kernel", st);
-  norm_bwd_finish_kernel<<<grid, 256, 0, st>>>(a.partials, rows, a.d, a.dweight, a.dbias,
-                                               a.add_dweight, a.add_dbias);
-  return cudaGetLastError();
+  return cudaLaunchKernelEx(&cfg, norm_bwd_finish_kernel, static_cast<const float*>(a.partials), rows,
+                            a.d, a.dweight, a.dbias, a.add_dweight, a.add_dbias);
 }
 
 template <typename T, int CH, bool CK, bool FULL>

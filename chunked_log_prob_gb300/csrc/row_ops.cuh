@@ -277,24 +277,33 @@ __device__ __forceinline__ void read_param(uint32_t s, int i, uint32_t half_byte
                : "memory");
 }
 
-// Joins the warps' sums of a row (after warp sums): every thread gets the total,
-// added in warp order. As row_sum2, with the join by plain loads.
-__device__ __forceinline__ float2 join_warps(float2 v, int t, int warps, int bar, float2* sh,
-                                             int& phase) {
+// Joins NV sums of a row's warps (each after warp_sum): every thread gets the
+// totals, added in warp order. One named barrier; `sh` holds 2 x NV x 16 sums,
+// used in turn (`phase`), those beyond the last warp 0.
+template <int NV>
+__device__ __forceinline__ void join_warps(float (&v)[NV], int t, int warps, int bar, float* sh,
+                                           int& phase) {
   if (warps == 1) {
     __syncwarp();
-    return v;
+    return;
   }
-  float2* s = sh + phase * 32;
+  float* s = sh + phase * NV * 16;
   phase ^= 1;
-  if ((t & 31) == 0) s[t >> 5] = v;
-  named_barrier(bar, warps * 32);
-  float2 r = s[0];
-  for (int k = 1; k < warps; ++k) {
-    r.x += s[k].x;
-    r.y += s[k].y;
+  if ((t & 31) == 0) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) s[k * 16 + (t >> 5)] = v[k];
   }
-  return r;
+  named_barrier(bar, warps * 32);
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    v[k] = 0.f;
+#pragma unroll
+    for (int w = 0; w < 16; w += 4) {
+      if (w >= warps) break;
+      const float4 x = *reinterpret_cast<const float4*>(s + k * 16 + w);
+      v[k] += (x.x + x.y) + (x.z + x.w);
+    }
+  }
 }
 
 // ---------------------------------------------------- 8-bit checkpoints ----
