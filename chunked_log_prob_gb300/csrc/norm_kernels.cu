@@ -26,162 +26,11 @@ __device__ __forceinline__ bool row_live(const uint8_t* mask, long long row, lon
   return row < n && (mask == nullptr || mask[row] != 0);
 }
 
-// Mean and centred sum of squares of a row. Layer norm: each warp centres its
-// values on their own mean, then the warps' sums are joined exactly as if one
-// had centred on the row's (no difference of large squares). `cnt`: valid
-// values of this warp, shared by all warps in cnt_sh.
-template <int CH, bool VEC>
-__device__ __forceinline__ float2 row_moments(const float (&v)[CH][8], int kind, int t, int tpr,
-                                              int d, int bar, float2* sh, const float* cnt_sh,
-                                              int& phase) {
-  float s = 0.f;
-  if (kind == GRPO_NORM_RMS) {
-#pragma unroll
-    for (int c = 0; c < CH; ++c)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s += v[c][j] * v[c][j];
-    return make_float2(0.f, row_sum2(make_float2(s, 0.f), t, tpr, bar, sh, phase).x);
-  }
-#pragma unroll
-  for (int c = 0; c < CH; ++c)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s += v[c][j];
-  s = warp_sum(s);
-  const int warp = t >> 5, lane = t & 31;
-  const float cnt = cnt_sh[warp];
-  const float mw = cnt > 0.f ? s / cnt : 0.f;
-  float m2 = 0.f;
-#pragma unroll
-  for (int c = 0; c < CH; ++c)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float e = v[c][j] - mw;
-      if (chunk_col<VEC>(c, j, t, tpr) < d) m2 += e * e;
-    }
-  m2 = warp_sum(m2);
-  if (tpr == 32) return make_float2(mw, m2);
-  float2* p = sh + phase * 32;
-  phase ^= 1;
-  if (lane == 0) p[warp] = make_float2(s, m2);
-  named_barrier(bar, tpr);
-  const bool in = lane < (tpr >> 5);
-  const float2 o = in ? p[lane] : make_float2(0.f, 0.f);
-  const float n = in ? cnt_sh[lane] : 0.f;
-  const float mean = warp_sum(o.x) / static_cast<float>(d);
-  const float e = n > 0.f ? o.x / n - mean : 0.f;
-  return make_float2(mean, warp_sum(o.y + n * e * e));
-}
-
-// Valid columns of each warp of a row into cnt_sh; followed by a barrier.
-template <int CH, bool VEC>
-__device__ __forceinline__ void count_columns(int t, int tpr, int d, float* cnt_sh) {
-  float n = 0.f;
-#pragma unroll
-  for (int c = 0; c < CH; ++c)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) n += chunk_col<VEC>(c, j, t, tpr) < d ? 1.f : 0.f;
-  n = warp_sum(n);
-  if ((t & 31) == 0) cnt_sh[t >> 5] = n;
-}
-
-// blockDim = (tpr, rows of the CTA). The next row's loads are issued before
-// this row's sums, so that they are in flight during its barrier and stores.
-template <typename T, bool VEC, int CH>
-__global__ void __launch_bounds__(512) norm_fwd_kernel(const NormFwdArgs a) {
-  __shared__ float2 red[8][2 * 32];
-  __shared__ float cnt_all[8][32];
-  const int t = threadIdx.x, tpr = blockDim.x, g = threadIdx.y, d = a.d;
-  int phase = 0;
-  float w[CH][8], b[CH][8];
-#pragma unroll
-  for (int c = 0; c < CH; ++c)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int col = chunk_col<VEC>(c, j, t, tpr);
-      w[c][j] = a.weight != nullptr && col < d ? load_param(a.weight, a.wtype, col) : 1.f;
-      b[c][j] = a.bias != nullptr && col < d ? load_param(a.bias, a.wtype, col) : 0.f;
-    }
-  count_columns<CH, VEC>(t, tpr, d, cnt_all[g]);
-  __syncthreads();
-
-  const T* x = static_cast<const T*>(a.x);
-  const T* res = static_cast<const T*>(a.res);
-  T* y = static_cast<T*>(a.y);
-  T* z = static_cast<T*>(a.z);
-  const long long step = static_cast<long long>(gridDim.x) * blockDim.y;
-  long long row = static_cast<long long>(blockIdx.x) * blockDim.y + g;
-  bool live = row_live(a.mask, row, a.n);
-  bool live1 = row_live(a.mask, row + step, a.n);
-  Raw8<T> rx[CH], rr[CH];
-#pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    if (live) rx[c] = load_chunk<T, VEC>(x + row * a.ldx, c, t, tpr, d);
-    if (live && res != nullptr) rr[c] = load_chunk<T, VEC>(res + row * a.ldr, c, t, tpr, d);
-  }
-  for (; row < a.n; row += step) {
-    const bool live2 = row_live(a.mask, row + 2 * step, a.n);
-    const long long next = row + step;
-    float v[CH][8];
-    if (live) {
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        widen(rx[c], v[c]);
-        if (res != nullptr) {
-          float r[8];
-          widen(rr[c], r);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[c][j] += r[j];
-          // The stream holds z rounded; the norm is taken of what it holds.
-          const Raw8<T> o = narrow<T>(v[c]);
-          if (z != nullptr) store_chunk<T, VEC>(z + row * a.ldz, o, c, t, tpr, d);
-          widen(o, v[c]);
-        }
-      }
-    }
-    if (live1) {
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        rx[c] = load_chunk<T, VEC>(x + next * a.ldx, c, t, tpr, d);
-        if (res != nullptr) rr[c] = load_chunk<T, VEC>(res + next * a.ldr, c, t, tpr, d);
-      }
-    }
-    float mean = 0.f, rstd = 0.f;
-    if (live) {
-      const float2 m = row_moments<CH, VEC>(v, a.kind, t, tpr, d, g + 1, red[g], cnt_all[g], phase);
-      mean = m.x;
-      rstd = 1.f / sqrtf(m.y / static_cast<float>(d) + a.eps);
-    } else {
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[c][j] = 0.f;
-        if (z != nullptr && res != nullptr)
-          store_chunk<T, VEC>(z + row * a.ldz, narrow<T>(v[c]), c, t, tpr, d);
-      }
-    }
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      if (a.ck.q != nullptr)
-        ckpt_store_chunk<T, VEC>(v[c], a.ck.q + row * a.ck.ldq, a.ck.ex + row * a.ck.lde, c, t, tpr,
-                                 d);
-      if (live) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[c][j] = (v[c][j] - mean) * rstd * w[c][j] + b[c][j];
-      }
-      store_chunk<T, VEC>(y + row * a.ldy, narrow<T>(v[c]), c, t, tpr, d);
-    }
-    if (t == 0) {
-      if (a.mean != nullptr) a.mean[row] = mean;
-      if (a.rstd != nullptr) a.rstd[row] = rstd;
-    }
-    live = live1;
-    live1 = live2;
-  }
-}
-
-// The aligned form. Each row of the CTA (threadIdx.y) has a ring of `slots`
-// rows in shared memory, filled by bulk copies; a slot is filled again as soon
-// as the row's sum has been taken, when every thread holds its values.
+// Each row of the CTA (threadIdx.y) has a ring of `slots` rows in shared memory,
+// filled by bulk copies; a slot is filled again as soon as the row's sum has
+// been taken, when every thread holds its values. Bulk copies start and end on
+// 16 bytes: of a row that does not, the 16 bytes around its ends come too, and
+// its values are read one by one (VEC false).
 // The bytes in flight come from the ring, so what is left is issue slots: a
 // thread holds up to 32 values, so that a row's fixed work (barriers, sums,
 // addresses) is shared by few warps, and works on pairs of them.
@@ -204,33 +53,25 @@ __device__ __forceinline__ void land(uint64_t* bars, int slots, uint32_t parity,
     if ((pending >> s) & 1u) row_wait(&bars[s], (parity >> s) & 1u);
 }
 
-// Columns that warp k of a row holds (VEC layout).
-template <int CH>
-__device__ __forceinline__ float warp_columns(int k, int tpr, int d) {
-  int n = 0;
-#pragma unroll
-  for (int c = 0; c < CH; ++c) n += max(0, min(256, d - (c * tpr + k * 32) * 8));
-  return static_cast<float>(n);
-}
-
 // Rows of the group that begins at `row`.
 __device__ __forceinline__ int row_count(long long row, long long n, long long step) {
   return row < n ? static_cast<int>((n - 1 - row) / step) + 1 : 0;
 }
 
-template <typename T, int CH, int KIND>
-__global__ void __launch_bounds__(ring_threads(CH)) norm_fwd_ring_kernel(const NormFwdArgs a, const Ring ring) {
+template <typename T, bool VEC, int CH, int KIND>
+__global__ void __launch_bounds__(ring_threads(CH)) norm_fwd_kernel(const NormFwdArgs a, const Ring ring) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(16) float red[kMaxRows][2 * 2 * 16];
+  __shared__ float warp_n[2][16];
   const int t = threadIdx.x, tpr = blockDim.x, g = threadIdx.y, d = a.d;
   const int warps = tpr >> 5;
   uint64_t* const bars = reinterpret_cast<uint64_t*>(smem) + g * kMaxSlots;
   float* const sw = reinterpret_cast<float*>(smem + kRingBars);
-  float* const sb = sw + (a.weight != nullptr ? d : 0);
+  float* const sb = sw + (a.weight != nullptr ? param_bytes(d) / 4 : 0);
   const uint32_t sw32 = smem_u32(sw), sb32 = smem_u32(sb);
-  const uint32_t rows0 = smem_u32(sb + (a.bias != nullptr ? d : 0)) +
+  const uint32_t rows0 = smem_u32(sb + (a.bias != nullptr ? param_bytes(d) / 4 : 0)) +
                          g * ring.slots * ring.row_bytes;
-  const uint32_t x_bytes = d * sizeof(T);
+  const uint32_t x_bytes = row_slot<T, VEC>(d);
   const bool res = a.res != nullptr;
   const long long step = static_cast<long long>(gridDim.x) * blockDim.y;
   const long long row0 = static_cast<long long>(blockIdx.x) * blockDim.y + g;
@@ -245,9 +86,12 @@ __global__ void __launch_bounds__(ring_threads(CH)) norm_fwd_ring_kernel(const N
     if (mask != nullptr && mask[r] == 0) return;
     pending |= 1u << slot;
     const uint32_t dst = rows0 + slot * ring.row_bytes;
-    mbar_arrive_expect_tx(&bars[slot], res ? 2 * x_bytes : x_bytes);
-    bulk_load(dst, static_cast<const T*>(a.x) + r * a.ldx, x_bytes, &bars[slot]);
-    if (res) bulk_load(dst + x_bytes, static_cast<const T*>(a.res) + r * a.ldr, x_bytes, &bars[slot]);
+    const T* px = static_cast<const T*>(a.x) + r * a.ldx;
+    const T* pr = static_cast<const T*>(a.res) + r * a.ldr;
+    mbar_arrive_expect_tx(&bars[slot],
+                          row_span<T, VEC>(px, d) + (res ? row_span<T, VEC>(pr, d) : 0));
+    bulk_row<T, VEC>(dst, px, d, &bars[slot]);
+    if (res) bulk_row<T, VEC>(dst + x_bytes, pr, d, &bars[slot]);
   };
   if (t == 0) {
     for (int s = 0; s < ring.slots; ++s) mbar_init(&bars[s], 1);
@@ -255,19 +99,24 @@ __global__ void __launch_bounds__(ring_threads(CH)) norm_fwd_ring_kernel(const N
     for (int s = 0; s < ring.slots; ++s) fetch(s);
   }
   for (int k = t; k < 2 * 2 * 16; k += tpr) red[g][k] = 0.f;
-  if (a.weight != nullptr) stage_param(sw, a.weight, a.wtype, d, g * tpr + t, tpr * blockDim.y);
-  if (a.bias != nullptr) stage_param(sb, a.bias, a.wtype, d, g * tpr + t, tpr * blockDim.y);
+  if (a.weight != nullptr)
+    stage_param<VEC>(sw, a.weight, a.wtype, d, g * tpr + t, tpr * blockDim.y);
+  if (a.bias != nullptr) stage_param<VEC>(sb, a.bias, a.wtype, d, g * tpr + t, tpr * blockDim.y);
+  // Columns that each warp of a row holds, and their inverse.
+  if (KIND == GRPO_NORM_LAYER) {
+    float n = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8 * CH; ++k) n += chunk_col<VEC>(k >> 3, k & 7, t, tpr) < d ? 1.f : 0.f;
+    n = warp_sum(n);
+    if ((t & 31) == 0) {
+      warp_n[0][t >> 5] = n;
+      warp_n[1][t >> 5] = n > 0.f ? 1.f / n : 0.f;
+    }
+  }
   __syncthreads();
 
   const float inv_d = 1.f / static_cast<float>(d);
-  // Values of this warp that are columns: its chunks before d.
-  float warp_n = 0.f;
-  if (KIND == GRPO_NORM_LAYER) {
-#pragma unroll
-    for (int c = 0; c < CH; ++c) warp_n += (c * tpr + t) * 8 < d ? 8.f : 0.f;
-    warp_n = warp_sum(warp_n);
-  }
-  const float inv_warp_n = warp_n > 0.f ? 1.f / warp_n : 0.f;
+  const float inv_warp_n = KIND == GRPO_NORM_LAYER ? warp_n[1][t >> 5] : 0.f;
   T* y = static_cast<T*>(a.y) + row0 * a.ldy;
   T* z = res && a.z != nullptr ? static_cast<T*>(a.z) + row0 * a.ldz : nullptr;
   uint8_t* q = a.ck.q != nullptr ? a.ck.q + row0 * a.ck.ldq : nullptr;
@@ -287,22 +136,22 @@ __global__ void __launch_bounds__(ring_threads(CH)) norm_fwd_ring_kernel(const N
         parity ^= 1u << slot;
         pending &= ~(1u << slot);
       }
-      const uint32_t src = rows0 + slot * ring.row_bytes + t * sizeof(Raw8<T>);
+      const long long row = row0 + step * i;
+      const uint32_t src =
+          rows0 + slot * ring.row_bytes + row_shift<T, VEC>(static_cast<const T*>(a.x) + row * a.ldx);
+      const uint32_t src_r = rows0 + slot * ring.row_bytes + x_bytes +
+                             row_shift<T, VEC>(static_cast<const T*>(a.res) + row * a.ldr);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[c][j] = 0ull;
-        if ((c * tpr + t) * 8 >= d) continue;
-        const uint32_t at = src + c * tpr * sizeof(Raw8<T>);
-        widen2(lds_raw<T>(at), v[c]);
+        lds_values<T, VEC>(src, c, t, tpr, d, v[c]);
         if (res) {
           f32x2 r[4];
-          widen2(lds_raw<T>(at + x_bytes), r);
+          lds_values<T, VEC>(src_r, c, t, tpr, d, r);
 #pragma unroll
           for (int j = 0; j < 4; ++j) v[c][j] = add2(v[c][j], r[j]);
           // The stream holds z rounded; the norm is taken of what it holds.
           const Raw8<T> o = narrow2<T>(v[c]);
-          if (z != nullptr) store_raw(z + (c * tpr + t) * 8, o);
+          if (z != nullptr) store_chunk<T, VEC>(z, o, c, t, tpr, d);
           widen2(o, v[c]);
         }
       }
@@ -329,10 +178,16 @@ __global__ void __launch_bounds__(ring_threads(CH)) norm_fwd_ring_kernel(const N
         s[0] = s[1] = 0ull;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-          if ((c * tpr + t) * 8 >= d) continue;
+          if (VEC ? (c * tpr + t) * 8 >= d : 8 * c * tpr >= d) continue;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const f32x2 e = add2(v[c][j], nmw);
+            f32x2 e = add2(v[c][j], nmw);
+            if (!VEC) {
+              float lo, hi;
+              split(e, lo, hi);
+              e = pair(chunk_col<false>(c, 2 * j, t, tpr) < d ? lo : 0.f,
+                       chunk_col<false>(c, 2 * j + 1, t, tpr) < d ? hi : 0.f);
+            }
             s[j & 1] = fma2(e, e, s[j & 1]);
           }
         }
@@ -351,9 +206,8 @@ __global__ void __launch_bounds__(ring_threads(CH)) norm_fwd_ring_kernel(const N
           const float mu = total * inv_d;
           centred = 0.f;
           for (int k = 0; k < warps; ++k) {
-            const float nk = warp_columns<CH>(k, tpr, d);
-            const float e = nk > 0.f ? sh[k] / nk - mu : 0.f;
-            centred += sh[16 + k] + nk * e * e;
+            const float e = sh[k] * warp_n[1][k] - mu;
+            centred += sh[16 + k] + warp_n[0][k] * e * e;
           }
         } else {
           __syncwarp();
@@ -367,8 +221,7 @@ __global__ void __launch_bounds__(ring_threads(CH)) norm_fwd_ring_kernel(const N
       for (int c = 0; c < CH; ++c) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[c][j] = 0ull;
-        if (z != nullptr && (c * tpr + t) * 8 < d)
-          store_raw(z + (c * tpr + t) * 8, narrow2<T>(v[c]));
+        if (z != nullptr) store_chunk<T, VEC>(z, narrow2<T>(v[c]), c, t, tpr, d);
       }
     }
     // Every thread has its values (the sum's barrier, or the warp's).
@@ -377,31 +230,30 @@ __global__ void __launch_bounds__(ring_threads(CH)) norm_fwd_ring_kernel(const N
     const f32x2 scale = pair(rstd, rstd), shift = pair(-mean, -mean);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int at = c * tpr + t;
       if (q != nullptr) {
         float f[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) split(v[c][j], f[2 * j], f[2 * j + 1]);
-        ckpt_store_chunk<T, true>(f, q, ex, c, t, tpr, d);
+        ckpt_store_chunk<T, VEC>(f, q, ex, c, t, tpr, d);
       }
-      if (8 * at >= d) continue;
+      if (VEC ? (c * tpr + t) * 8 >= d : 8 * c * tpr >= d) continue;
       if (live) {
         f32x2 w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           v[c][j] = mul2(KIND == GRPO_NORM_LAYER ? add2(v[c][j], shift) : v[c][j], scale);
         if (a.weight != nullptr) {
-          read_param(sw32, at, 2 * d, w);
+          read_param<VEC>(sw32, c, t, tpr, d, w);
 #pragma unroll
           for (int j = 0; j < 4; ++j) v[c][j] = mul2(v[c][j], w[j]);
         }
         if (a.bias != nullptr) {
-          read_param(sb32, at, 2 * d, w);
+          read_param<VEC>(sb32, c, t, tpr, d, w);
 #pragma unroll
           for (int j = 0; j < 4; ++j) v[c][j] = add2(v[c][j], w[j]);
         }
       }
-      store_raw(y + 8 * at, narrow2<T>(v[c]));
+      store_chunk<T, VEC>(y, narrow2<T>(v[c]), c, t, tpr, d);
     }
     if (t == 0) {
       const long long row = row0 + step * i;
@@ -519,150 +371,22 @@ struct RawStream<T, VEC, true> {
 
 // dx, and this CTA's sums over its rows for dw (and db), which each thread
 // keeps in registers for its own columns: the rows' order is fixed by the grid,
-// so the sums are the same on every run.
-template <typename T, bool VEC, int CH, bool CK, bool DB>
-__global__ void __launch_bounds__(512) norm_bwd_kernel(const NormBwdArgs a) {
-  __shared__ float2 red[8][2 * 32];
-  extern __shared__ float col_sums[];  // [d], [d] when the CTA has several rows in flight
-  const int t = threadIdx.x, tpr = blockDim.x, g = threadIdx.y, d = a.d;
-  int phase = 0;
-  float w[CH][8], dw[CH][8], db[DB ? CH : 1][8];
-#pragma unroll
-  for (int c = 0; c < CH; ++c)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int col = chunk_col<VEC>(c, j, t, tpr);
-      w[c][j] = a.weight != nullptr && col < d ? load_param(a.weight, a.wtype, col) : 1.f;
-      dw[c][j] = 0.f;
-      if (DB) db[DB ? c : 0][j] = 0.f;
-    }
-  const T* dy = static_cast<const T*>(a.dy);
-  const T* dres = static_cast<const T*>(a.dres);
-  T* dx = static_cast<T*>(a.dx);
-  const long long step = static_cast<long long>(gridDim.x) * blockDim.y;
-  long long row = static_cast<long long>(blockIdx.x) * blockDim.y + g;
-  bool live = row_live(a.mask, row, a.n);
-  bool live1 = row_live(a.mask, row + step, a.n);
-  const float inv_d = 1.f / static_cast<float>(d);
-  Raw8<T> ry[CH], rr[CH];
-  RawStream<T, VEC, CK> rx[CH];
-  float mean = 0.f, rstd = 0.f;
-  const auto fetch = [&](long long r) {
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      ry[c] = load_chunk<T, VEC>(dy + r * a.lddy, c, t, tpr, d);
-      rx[c].load(a, r, c, t, tpr);
-      if (dres != nullptr) rr[c] = load_chunk<T, VEC>(dres + r * a.lddres, c, t, tpr, d);
-    }
-    rstd = a.rstd[r];
-    mean = a.kind != GRPO_NORM_RMS ? a.mean[r] : 0.f;
-  };
-  if (live) fetch(row);
-  for (; row < a.n; row += step) {
-    const bool live2 = row_live(a.mask, row + 2 * step, a.n);
-    if (!live) {
-      const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < CH; ++c)
-        store_chunk<T, VEC>(dx + row * a.lddx, narrow<T>(zero), c, t, tpr, d);
-      if (live1) fetch(row + step);
-    } else {
-      float u[CH][8], h[CH][8];
-      Raw8<T> cur_res[CH];
-      float2 s = make_float2(0.f, 0.f);
-      const float rs = rstd;
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        widen(ry[c], u[c]);
-        rx[c].get(h[c]);
-        if (dres != nullptr) cur_res[c] = rr[c];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          h[c][j] = (h[c][j] - mean) * rs;
-          dw[c][j] += u[c][j] * h[c][j];
-          if (DB) db[DB ? c : 0][j] += u[c][j];
-          u[c][j] *= w[c][j];
-          s.x += u[c][j];
-          s.y += u[c][j] * h[c][j];
-        }
-      }
-      if (live1) fetch(row + step);
-      s = row_sum2(s, t, tpr, g + 1, red[g], phase);
-      const float c1 = a.kind != GRPO_NORM_RMS ? s.x * inv_d : 0.f;
-      const float c2 = s.y * inv_d;
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) u[c][j] = rs * (u[c][j] - c1 - h[c][j] * c2);
-        if (dres != nullptr) {
-          float r[8];
-          widen(cur_res[c], r);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) u[c][j] += r[j];
-        }
-        store_chunk<T, VEC>(dx + row * a.lddx, narrow<T>(u[c]), c, t, tpr, d);
-      }
-    }
-    live = live1;
-    live1 = live2;
-  }
-  if (a.dweight == nullptr && !DB) return;
-  // The CTA's rows in flight, added in their order.
-  if (blockDim.y > 1) {
-    float* sw = col_sums;
-    float* sb = col_sums + d;
-    for (int k = 0; k < static_cast<int>(blockDim.y); ++k) {
-      if (g == k) {
-#pragma unroll
-        for (int c = 0; c < CH; ++c)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int col = chunk_col<VEC>(c, j, t, tpr);
-            if (col < d) {
-              sw[col] = k == 0 ? dw[c][j] : sw[col] + dw[c][j];
-              if (DB) sb[col] = k == 0 ? db[DB ? c : 0][j] : sb[col] + db[DB ? c : 0][j];
-            }
-          }
-      }
-      __syncthreads();
-    }
-    float* pw = a.partials + static_cast<long long>(blockIdx.x) * d;
-    float* pb = pw + static_cast<long long>(gridDim.x) * d;
-    for (int col = g * tpr + t; col < d; col += tpr * blockDim.y) {
-      pw[col] = sw[col];
-      if (DB) pb[col] = sb[col];
-    }
-  } else {
-    float* pw = a.partials + static_cast<long long>(blockIdx.x) * d;
-    float* pb = pw + static_cast<long long>(gridDim.x) * d;
-#pragma unroll
-    for (int c = 0; c < CH; ++c)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int col = chunk_col<VEC>(c, j, t, tpr);
-        if (col < d) {
-          pw[col] = dw[c][j];
-          if (DB) pb[col] = db[DB ? c : 0][j];
-        }
-      }
-  }
-}
-
-// The aligned form of norm_bwd_kernel, its rows in flight as in
-// norm_fwd_ring_kernel. A slot holds dy, then x (or its bytes and exponents),
-// then dres. FULL: layer norm, or a bias gradient; else neither.
-template <typename T, int CH, bool CK, bool FULL>
-__global__ void __launch_bounds__(ring_threads(CH)) norm_bwd_ring_kernel(const NormBwdArgs a, const Ring ring) {
+// so the sums are the same on every run. Rows in flight as in norm_fwd_kernel; a
+// slot holds dy, then x (or its bytes and exponents), then dres. FULL: layer
+// norm, or a bias gradient; else neither. 16 values a thread: with 32 the sums
+// alone take 64 to 128 registers (131072 x 2880 layer norm: 789 us against 545).
+template <typename T, bool VEC, int CH, bool CK, bool FULL>
+__global__ void __launch_bounds__(ring_threads(CH)) norm_bwd_kernel(const NormBwdArgs a, const Ring ring) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(16) float red[kMaxRows][2 * 2 * 16];
   const int t = threadIdx.x, tpr = blockDim.x, g = threadIdx.y, d = a.d;
   const int warps = tpr >> 5;
   uint64_t* const bars = reinterpret_cast<uint64_t*>(smem) + g * kMaxSlots;
   float* const sw = reinterpret_cast<float*>(smem + kRingBars);
-  uint8_t* const ring0 = reinterpret_cast<uint8_t*>(sw + (a.weight != nullptr ? d : 0));
+  uint8_t* const ring0 = reinterpret_cast<uint8_t*>(sw + (a.weight != nullptr ? param_bytes(d) / 4 : 0));
   const uint32_t sw32 = smem_u32(sw);
   const uint32_t rows0 = smem_u32(ring0) + g * ring.slots * ring.row_bytes;
-  const uint32_t t_bytes = d * sizeof(T);
+  const uint32_t t_bytes = row_slot<T, VEC>(d);
   const uint32_t q_bytes = static_cast<uint32_t>(a.ck.ldq), e_bytes = static_cast<uint32_t>(a.ck.lde);
   const uint32_t x_bytes = CK ? q_bytes + e_bytes : t_bytes;  // rows of 16 bytes
   const bool res = a.dres != nullptr, layer = FULL && a.kind == GRPO_NORM_LAYER;
@@ -678,17 +402,20 @@ __global__ void __launch_bounds__(ring_threads(CH)) norm_bwd_ring_kernel(const N
     if (mask != nullptr && mask[r] == 0) return;
     pending |= 1u << slot;
     const uint32_t dst = rows0 + slot * ring.row_bytes;
-    mbar_arrive_expect_tx(&bars[slot], t_bytes + x_bytes + (res ? t_bytes : 0));
-    bulk_load(dst, static_cast<const T*>(a.dy) + r * a.lddy, t_bytes, &bars[slot]);
+    const T* py = static_cast<const T*>(a.dy) + r * a.lddy;
+    const T* px = static_cast<const T*>(a.x) + r * a.ldx;
+    const T* pr = static_cast<const T*>(a.dres) + r * a.lddres;
+    mbar_arrive_expect_tx(&bars[slot], row_span<T, VEC>(py, d) +
+                                           (CK ? x_bytes : row_span<T, VEC>(px, d)) +
+                                           (res ? row_span<T, VEC>(pr, d) : 0));
+    bulk_row<T, VEC>(dst, py, d, &bars[slot]);
     if (CK) {
       bulk_load(dst + t_bytes, a.ck.q + r * a.ck.ldq, q_bytes, &bars[slot]);
       bulk_load(dst + t_bytes + q_bytes, a.ck.ex + r * a.ck.lde, e_bytes, &bars[slot]);
     } else {
-      bulk_load(dst + t_bytes, static_cast<const T*>(a.x) + r * a.ldx, t_bytes, &bars[slot]);
+      bulk_row<T, VEC>(dst + t_bytes, px, d, &bars[slot]);
     }
-    if (res)
-      bulk_load(dst + t_bytes + x_bytes, static_cast<const T*>(a.dres) + r * a.lddres, t_bytes,
-                &bars[slot]);
+    if (res) bulk_row<T, VEC>(dst + t_bytes + x_bytes, pr, d, &bars[slot]);
   };
   if (t == 0) {
     for (int s = 0; s < ring.slots; ++s) mbar_init(&bars[s], 1);
@@ -697,7 +424,8 @@ __global__ void __launch_bounds__(ring_threads(CH)) norm_bwd_ring_kernel(const N
   }
   for (int k = t; k < 2 * 2 * 16; k += tpr) red[g][k] = 0.f;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (a.weight != nullptr) stage_param(sw, a.weight, a.wtype, d, g * tpr + t, tpr * blockDim.y);
+  if (a.weight != nullptr)
+    stage_param<VEC>(sw, a.weight, a.wtype, d, g * tpr + t, tpr * blockDim.y);
   __syncthreads();
 
   f32x2 dw[CH][4], db[FULL ? CH : 1][4];
@@ -726,34 +454,36 @@ __global__ void __launch_bounds__(ring_threads(CH)) norm_bwd_ring_kernel(const N
       const f32x2 zero[4] = {0ull, 0ull, 0ull, 0ull};
       if (t == 0 && ok) fetch(slot);
 #pragma unroll
-      for (int c = 0; c < CH; ++c)
-        if ((c * tpr + t) * 8 < d) store_raw(dx + (c * tpr + t) * 8, narrow2<T>(zero));
+      for (int c = 0; c < CH; ++c) store_chunk<T, VEC>(dx, narrow2<T>(zero), c, t, tpr, d);
     } else {
       ok = ok && row_wait(&bars[slot], (parity >> slot) & 1u);
       if (ok) {
         parity ^= 1u << slot;
         pending &= ~(1u << slot);
       }
+      const long long row = row0 + step * i;
       const uint32_t src = rows0 + slot * ring.row_bytes;
+      const uint32_t src_y = src + row_shift<T, VEC>(static_cast<const T*>(a.dy) + row * a.lddy);
+      const uint32_t src_x =
+          src + t_bytes +
+          (CK ? 0 : row_shift<T, VEC>(static_cast<const T*>(a.x) + row * a.ldx));
+      const uint32_t src_r = src + t_bytes + x_bytes +
+                             row_shift<T, VEC>(static_cast<const T*>(a.dres) + row * a.lddres);
       const f32x2 scale = pair(rstd, rstd), shift = pair(-mean, -mean);
       f32x2 u[CH][4], h[CH][4];
       Raw8<T> rr[CH];
       f32x2 su = 0ull, suh = 0ull;
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        const int at = c * tpr + t;
-        if (8 * at >= d) continue;
-        const uint32_t off = at * sizeof(Raw8<T>);
-        widen2(lds_raw<T>(src + off), u[c]);
-        if (CK) {
-          ckpt_widen2(lds_v2(src + t_bytes + 8 * at),
-                      ckpt_factor(lds_u8(src + t_bytes + q_bytes + at / 4)), h[c]);
-        } else {
-          widen2(lds_raw<T>(src + t_bytes + off), h[c]);
-        }
-        if (res) rr[c] = lds_raw<T>(src + t_bytes + x_bytes + off);
+        if (VEC ? (c * tpr + t) * 8 >= d : 8 * c * tpr >= d) continue;
+        lds_values<T, VEC>(src_y, c, t, tpr, d, u[c]);
+        if (CK)
+          lds_ckpt<VEC>(src_x, src_x + q_bytes, c, t, tpr, d, h[c]);
+        else
+          lds_values<T, VEC>(src_x, c, t, tpr, d, h[c]);
+        if (res) rr[c] = lds_chunk<T, VEC>(src_r, c, t, tpr, d);
         f32x2 w[4];
-        if (a.weight != nullptr) read_param(sw32, at, 2 * d, w);
+        if (a.weight != nullptr) read_param<VEC>(sw32, c, t, tpr, d, w);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (FULL) h[c][j] = add2(h[c][j], shift);
@@ -775,8 +505,7 @@ __global__ void __launch_bounds__(ring_threads(CH)) norm_bwd_ring_kernel(const N
       const f32x2 n1 = pair(-c1, -c1), n2 = pair(-c2, -c2);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        const int at = c * tpr + t;
-        if (8 * at >= d) continue;
+        if (VEC ? (c * tpr + t) * 8 >= d : 8 * c * tpr >= d) continue;
         f32x2 r[4] = {0ull, 0ull, 0ull, 0ull};
         if (res) widen2(rr[c], r);
 #pragma unroll
@@ -784,7 +513,7 @@ __global__ void __launch_bounds__(ring_threads(CH)) norm_bwd_ring_kernel(const N
           if (FULL) u[c][j] = add2(u[c][j], n1);
           u[c][j] = fma2(fma2(h[c][j], n2, u[c][j]), scale, r[j]);
         }
-        store_raw(dx + 8 * at, narrow2<T>(u[c]));
+        store_chunk<T, VEC>(dx, narrow2<T>(u[c]), c, t, tpr, d);
       }
       if (!ok) {
 #pragma unroll
@@ -804,17 +533,15 @@ __global__ void __launch_bounds__(ring_threads(CH)) norm_bwd_ring_kernel(const N
   const bool want_db = FULL && a.dbias != nullptr;
   if (a.dweight == nullptr && !want_db) return;
   // The CTA's rows in flight, added in their order; the rings have been read.
-  float* const cw = blockDim.y > 1 ? reinterpret_cast<float*>(ring0) : nullptr;
-  float* const cb = cw != nullptr ? cw + d : nullptr;
+  float* const cw = reinterpret_cast<float*>(ring0);
+  float* const cb = cw + d;
   float* pw = a.partials + static_cast<long long>(blockIdx.x) * d;
   float* pb = pw + static_cast<long long>(gridDim.x) * d;
-  if (cw == nullptr) {
+  if (blockDim.y == 1) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int at = c * tpr + t;
-      if (8 * at >= d) continue;
-      store_raw(pw + 8 * at, narrow2<float>(dw[c]));
-      if (want_db) store_raw(pb + 8 * at, narrow2<float>(db[FULL ? c : 0]));
+      store_sums<VEC>(pw, dw[c], c, t, tpr, d);
+      if (want_db) store_sums<VEC>(pb, db[FULL ? c : 0], c, t, tpr, d);
     }
     return;
   }
@@ -822,19 +549,20 @@ __global__ void __launch_bounds__(ring_threads(CH)) norm_bwd_ring_kernel(const N
   for (int k = 0; k < static_cast<int>(blockDim.y); ++k) {
     if (g == k) {
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const int at = c * tpr + t;
-        if (8 * at >= d) continue;
+      for (int c = 0; c < CH; ++c)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          f32x2* pc = reinterpret_cast<f32x2*>(cw + 8 * at + 2 * j);
-          *pc = k == 0 ? dw[c][j] : add2(*pc, dw[c][j]);
+          const int c0 = chunk_col<VEC>(c, 2 * j, t, tpr), c1 = chunk_col<VEC>(c, 2 * j + 1, t, tpr);
+          float lo, hi;
+          split(dw[c][j], lo, hi);
+          if (c0 < d) cw[c0] = k == 0 ? lo : cw[c0] + lo;
+          if (c1 < d) cw[c1] = k == 0 ? hi : cw[c1] + hi;
           if (want_db) {
-            f32x2* pd = reinterpret_cast<f32x2*>(cb + 8 * at + 2 * j);
-            *pd = k == 0 ? db[FULL ? c : 0][j] : add2(*pd, db[FULL ? c : 0][j]);
+            split(db[FULL ? c : 0][j], lo, hi);
+            if (c0 < d) cb[c0] = k == 0 ? lo : cb[c0] + lo;
+            if (c1 < d) cb[c1] = k == 0 ? hi : cb[c1] + hi;
           }
         }
-      }
     }
     __syncthreads();
   }
@@ -988,16 +716,7 @@ __global__ void __launch_bounds__(512) norm_bwd_finish_kernel(const float* __res
 struct RowShape {
   int tpr, rows, ch;
 };
-// One by one: 16 values a thread (8 up to 256 columns).
-RowShape row_shape(int d) {
-  RowShape s;
-  s.ch = d <= 256 ? 1 : 2;
-  const int per = 8 * s.ch;
-  s.tpr = (d + per * 32 - 1) / (per * 32) * 32;
-  s.rows = s.tpr >= kRowThreads ? 1 : kRowThreads / s.tpr;
-  return s;
-}
-// Aligned: the most values a thread, up to 8 `most`, that leave no more than a
+// The most values a thread, up to 8 `most`, that leave no more than a
 // tenth of the threads idle (else the fewest idle ones); CTAs of about
 // `threads` threads.
 RowShape ring_shape(int d, int most, int threads) {
@@ -1012,21 +731,6 @@ RowShape ring_shape(int d, int most, int threads) {
     if (10 * room <= 11 * d) break;
   }
   return best;
-}
-
-// CTAs of `threads` threads resident on the device, looked up once per kernel.
-template <auto Kernel>
-int resident(int threads, size_t smem, int sms) {
-  static std::atomic<int> known[33];
-  std::atomic<int>& k = known[threads / 32];
-  int n = k.load(std::memory_order_relaxed);
-  if (n == 0) {
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, Kernel, threads, smem) != cudaSuccess ||
-        n < 1)
-      n = 1;
-    k.store(n, std::memory_order_relaxed);
-  }
-  return n * sms;
 }
 
 constexpr size_t kSmemMax = 227 * 1024 - 8192;  // less the kernels' static arrays
@@ -1059,12 +763,12 @@ cudaError_t ctas_per_sm(int threads, size_t smem, int* n) {
   return cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, Kernel, threads, smem);
 }
 
-template <typename T, int CH, int KIND>
+template <typename T, bool VEC, int CH, int KIND>
 cudaError_t fwd_ring(const NormFwdArgs& a, const RowShape& s, int sms, cudaStream_t st) {
-  constexpr auto kernel = norm_fwd_ring_kernel<T, CH, KIND>;
-  const size_t fixed = kRingBars + sizeof(float) * a.d *
-                                       ((a.weight != nullptr) + (a.bias != nullptr));
-  const Ring ring = make_ring(a.d * sizeof(T) * (a.res != nullptr ? 2 : 1), s.rows, fixed);
+  constexpr auto kernel = norm_fwd_kernel<T, VEC, CH, KIND>;
+  const size_t fixed =
+      kRingBars + param_bytes(a.d) * ((a.weight != nullptr) + (a.bias != nullptr));
+  const Ring ring = make_ring(row_slot<T, VEC>(a.d) * (a.res != nullptr ? 2 : 1), s.rows, fixed);
   const size_t smem = fixed + static_cast<size_t>(ring.slots) * ring.row_bytes * s.rows;
   int per_sm = 0;
   cudaError_t e = ctas_per_sm<kernel>(s.tpr * s.rows, smem, &per_sm);
@@ -1076,26 +780,15 @@ cudaError_t fwd_ring(const NormFwdArgs& a, const RowShape& s, int sms, cudaStrea
   return cudaGetLastError();
 }
 
-template <typename T, int KIND>
-cudaError_t fwd_aligned(const NormFwdArgs& a, int sms, cudaStream_t st) {
+template <typename T, bool VEC, int KIND>
+cudaError_t fwd_kind(const NormFwdArgs& a, int sms, cudaStream_t st) {
   const RowShape s = ring_shape(a.d, 4, kRowThreads);
   switch (s.ch) {
-    case 1: return fwd_ring<T, 1, KIND>(a, s, sms, st);
-    case 2: return fwd_ring<T, 2, KIND>(a, s, sms, st);
-    case 3: return fwd_ring<T, 3, KIND>(a, s, sms, st);
-    default: return fwd_ring<T, 4, KIND>(a, s, sms, st);
+    case 1: return fwd_ring<T, VEC, 1, KIND>(a, s, sms, st);
+    case 2: return fwd_ring<T, VEC, 2, KIND>(a, s, sms, st);
+    case 3: return fwd_ring<T, VEC, 3, KIND>(a, s, sms, st);
+    default: return fwd_ring<T, VEC, 4, KIND>(a, s, sms, st);
   }
-}
-
-template <typename T, bool VEC, int CH>
-cudaError_t fwd(const NormFwdArgs& a, const RowShape& s, int sms, cudaStream_t st) {
-  constexpr auto kernel = norm_fwd_kernel<T, VEC, CH>;
-  const long long units = (a.n + s.rows - 1) / s.rows;
-  const int grid = static_cast<int>(
-      std::min<long long>(units, resident<kernel>(s.tpr * s.rows, 0, sms)));
-  LaunchTimer timer("norm_fwd_kernel", st);
-  kernel<<<grid, dim3(s.tpr, s.rows), 0, st>>>(a);
-  return cudaGetLastError();
 }
 
 template <typename T, bool VEC>
@@ -1106,13 +799,8 @@ cudaError_t fwd_any(const NormFwdArgs& a, int sms, cudaStream_t st) {
     norm_fwd_long_kernel<T, VEC><<<grid, 512, 0, st>>>(a);
     return cudaGetLastError();
   }
-  if constexpr (VEC) {
-    return a.kind == GRPO_NORM_RMS ? fwd_aligned<T, GRPO_NORM_RMS>(a, sms, st)
-                                   : fwd_aligned<T, GRPO_NORM_LAYER>(a, sms, st);
-  } else {
-    const RowShape s = row_shape(a.d);
-    return s.ch == 1 ? fwd<T, false, 1>(a, s, sms, st) : fwd<T, false, 2>(a, s, sms, st);
-  }
+  return a.kind == GRPO_NORM_RMS ? fwd_kind<T, VEC, GRPO_NORM_RMS>(a, sms, st)
+                                 : fwd_kind<T, VEC, GRPO_NORM_LAYER>(a, sms, st);
 }
 
 cudaError_t finish(const NormBwdArgs& a, int rows, cudaStream_t st) {
@@ -1132,11 +820,11 @@ cudaError_t finish(const NormBwdArgs& a, int rows, cudaStream_t st) {
                             a.d, a.dweight, a.dbias, a.add_dweight, a.add_dbias);
 }
 
-template <typename T, int CH, bool CK, bool FULL>
+template <typename T, bool VEC, int CH, bool CK, bool FULL>
 cudaError_t bwd_ring(const NormBwdArgs& a, const RowShape& s, int sms, cudaStream_t st) {
-  constexpr auto kernel = norm_bwd_ring_kernel<T, CH, CK, FULL>;
-  const size_t fixed = kRingBars + (a.weight != nullptr ? sizeof(float) * a.d : 0);
-  const uint32_t t_bytes = a.d * sizeof(T);
+  constexpr auto kernel = norm_bwd_kernel<T, VEC, CH, CK, FULL>;
+  const size_t fixed = kRingBars + (a.weight != nullptr ? param_bytes(a.d) : 0);
+  const uint32_t t_bytes = row_slot<T, VEC>(a.d);
   const Ring ring =
       make_ring(t_bytes * (a.dres != nullptr ? 2 : 1) +
                     (CK ? static_cast<uint32_t>(a.ck.ldq + a.ck.lde) : t_bytes),
@@ -1158,30 +846,13 @@ cudaError_t bwd_ring(const NormBwdArgs& a, const RowShape& s, int sms, cudaStrea
   return e != cudaSuccess ? e : finish(a, grid, st);
 }
 
-template <typename T, bool CK, bool FULL>
-cudaError_t bwd_aligned(const NormBwdArgs& a, int sms, cudaStream_t st) {
+template <typename T, bool VEC, bool CK, bool FULL>
+cudaError_t bwd_kind(const NormBwdArgs& a, int sms, cudaStream_t st) {
   const RowShape s = ring_shape(a.d, 2, kRowThreads);
   switch (s.ch) {
-    case 1: return bwd_ring<T, 1, CK, FULL>(a, s, sms, st);
-    default: return bwd_ring<T, 2, CK, FULL>(a, s, sms, st);
+    case 1: return bwd_ring<T, VEC, 1, CK, FULL>(a, s, sms, st);
+    default: return bwd_ring<T, VEC, 2, CK, FULL>(a, s, sms, st);
   }
-}
-
-template <typename T, bool VEC, int CH, bool CK, bool DB>
-cudaError_t bwd(const NormBwdArgs& a, const RowShape& s, int sms, cudaStream_t st) {
-  constexpr auto kernel = norm_bwd_kernel<T, VEC, CH, CK, DB>;
-  const long long units = (a.n + s.rows - 1) / s.rows;
-  const size_t smem = s.rows > 1 ? static_cast<size_t>(a.d) * (DB ? 8 : 4) : 0;
-  // Occupancy is asked for the largest such buffer (rows > 1: at most 2048 columns).
-  const int grid = static_cast<int>(std::min<long long>(
-      std::min<long long>(units, kNormMaxPartials),
-      resident<kernel>(s.tpr * s.rows, s.rows > 1 ? 2048 * 8 : 0, sms)));
-  {
-    LaunchTimer timer("norm_bwd_kernel", st);
-    kernel<<<grid, dim3(s.tpr, s.rows), smem, st>>>(a);
-  }
-  const cudaError_t e = cudaGetLastError();
-  return e != cudaSuccess ? e : finish(a, grid, st);
 }
 
 template <typename T, bool VEC, bool CK>
@@ -1203,18 +874,9 @@ cudaError_t bwd_any(const NormBwdArgs& a, int sms, cudaStream_t st) {
     e = cudaGetLastError();
     return e != cudaSuccess ? e : finish(a, groups, st);
   }
-  const bool db = a.dbias != nullptr;
-  if constexpr (VEC) {
-    return db || a.kind == GRPO_NORM_LAYER ? bwd_aligned<T, CK, true>(a, sms, st)
-                                           : bwd_aligned<T, CK, false>(a, sms, st);
-  } else {
-    const RowShape s = row_shape(a.d);
-    if (s.ch == 1)
-      return db ? bwd<T, false, 1, CK, true>(a, s, sms, st)
-                : bwd<T, false, 1, CK, false>(a, s, sms, st);
-    return db ? bwd<T, false, 2, CK, true>(a, s, sms, st)
-              : bwd<T, false, 2, CK, false>(a, s, sms, st);
-  }
+  return a.dbias != nullptr || a.kind == GRPO_NORM_LAYER
+             ? bwd_kind<T, VEC, CK, true>(a, sms, st)
+             : bwd_kind<T, VEC, CK, false>(a, sms, st);
 }
 
 template <typename T>

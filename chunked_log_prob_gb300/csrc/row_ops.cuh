@@ -240,41 +240,106 @@ __device__ __forceinline__ Raw8<T> narrow2(const f32x2 (&v)[4]) {
   return r;
 }
 
-// A chunk in shared or global memory, 16 bytes at a time.
-template <typename T>
-__device__ __forceinline__ Raw8<T> lds_raw(uint32_t p) {
-  Raw8<T> r;
-  uint4* w = reinterpret_cast<uint4*>(&r);
-#pragma unroll
-  for (int k = 0; k < static_cast<int>(sizeof(r) / 16); ++k) w[k] = lds_v4(p + 16 * k);
-  return r;
+// A row of d values in a slot of shared memory: its bytes, or (VEC false) those
+// of the 16-byte pieces that it touches; where in them it begins; the slot.
+template <typename T, bool VEC>
+__device__ __forceinline__ uint32_t row_shift(const T* p) {
+  return VEC ? 0u : static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u;
 }
-template <typename T>
-__device__ __forceinline__ void store_raw(T* p, const Raw8<T>& r) {
-  const uint4* w = reinterpret_cast<const uint4*>(&r);
-#pragma unroll
-  for (int k = 0; k < static_cast<int>(sizeof(r) / 16); ++k) reinterpret_cast<uint4*>(p)[k] = w[k];
+template <typename T, bool VEC>
+__device__ __forceinline__ uint32_t row_span(const T* p, int d) {
+  const uint32_t bytes = d * static_cast<uint32_t>(sizeof(T));
+  return VEC ? bytes : (row_shift<T, false>(p) + bytes + 15u) & ~15u;
+}
+template <typename T, bool VEC>
+__host__ __device__ constexpr uint32_t row_slot(int d) {
+  const uint32_t bytes = d * static_cast<uint32_t>(sizeof(T));
+  return VEC ? bytes : ((bytes + 15u) & ~15u) + 16u;
+}
+// Every 16 bytes that are read hold at least one byte of the row.
+template <typename T, bool VEC>
+__device__ __forceinline__ void bulk_row(uint32_t dst, const T* p, int d, uint64_t* bar) {
+  bulk_load(dst, reinterpret_cast<const uint8_t*>(p) - row_shift<T, VEC>(p), row_span<T, VEC>(p, d),
+            bar);
 }
 
-// A weight or bias vector as fp32 in shared memory: the first four columns of
-// every chunk, then the other four, so that neighbouring threads read
+__device__ __forceinline__ __nv_bfloat16 lds_value(uint32_t p, __nv_bfloat16) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(p) : "memory");
+  return __ushort_as_bfloat16(v);
+}
+__device__ __forceinline__ __half lds_value(uint32_t p, __half) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(p) : "memory");
+  return __ushort_as_half(v);
+}
+__device__ __forceinline__ float lds_value(uint32_t p, float) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(p) : "memory");
+  return v;
+}
+
+// Chunk c of a row in shared memory; zeros past column d.
+template <typename T, bool VEC>
+__device__ __forceinline__ Raw8<T> lds_chunk(uint32_t row, int c, int t, int tpr, int d) {
+  Raw8<T> r;
+  if (VEC) {
+    uint4* w = reinterpret_cast<uint4*>(&r);
+    const int i = c * tpr + t;
+#pragma unroll
+    for (int k = 0; k < static_cast<int>(sizeof(r) / 16); ++k)
+      w[k] = 8 * i < d ? lds_v4(row + i * sizeof(r) + 16 * k) : make_uint4(0, 0, 0, 0);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int col = chunk_col<false>(c, j, t, tpr);
+      r.e[j] = col < d ? lds_value(row + col * sizeof(T), T()) : T(0.f);
+    }
+  }
+  return r;
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void lds_values(uint32_t row, int c, int t, int tpr, int d,
+                                           f32x2 (&v)[4]) {
+  widen2(lds_chunk<T, VEC>(row, c, t, tpr, d), v);
+}
+
+// fp32 sums of a chunk to a row of fp32 (VEC: on 16 bytes, d % 8 == 0).
+template <bool VEC>
+__device__ __forceinline__ void store_sums(float* row, const f32x2 (&v)[4], int c, int t, int tpr,
+                                           int d) {
+  store_chunk<float, VEC>(row, narrow2<float>(v), c, t, tpr, d);
+}
+
+// A weight or bias vector as fp32 in shared memory. VEC: the first four columns
+// of every chunk, then the other four, so that neighbouring threads read
 // neighbouring 16 bytes.
+__host__ __device__ constexpr uint32_t param_bytes(int d) {
+  return (4u * static_cast<uint32_t>(d) + 15u) & ~15u;
+}
+template <bool VEC>
 __device__ __forceinline__ void stage_param(float* dst, const void* p, int type, int d, int thread,
                                             int threads) {
   const int half = d / 2;
   for (int col = thread; col < d; col += threads) {
     const int j = col & 7;
-    dst[(j >= 4 ? half : 0) + (col >> 3) * 4 + (j & 3)] = load_param(p, type, col);
+    const int at = VEC ? (j >= 4 ? half : 0) + (col >> 3) * 4 + (j & 3) : col;
+    dst[at] = load_param(p, type, col);
   }
 }
-// Chunk i of it; `half_bytes`: 2 d.
-__device__ __forceinline__ void read_param(uint32_t s, int i, uint32_t half_bytes, f32x2 (&w)[4]) {
-  const uint32_t p = s + 16 * i;
-  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(w[0]), "=l"(w[1]) : "r"(p) : "memory");
-  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];"
-               : "=l"(w[2]), "=l"(w[3])
-               : "r"(p + half_bytes)
-               : "memory");
+template <bool VEC>
+__device__ __forceinline__ void read_param(uint32_t s, int c, int t, int tpr, int d,
+                                           f32x2 (&w)[4]) {
+  if (VEC) {
+    const uint32_t p = s + 16 * (c * tpr + t);
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(w[0]), "=l"(w[1]) : "r"(p) : "memory");
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];"
+                 : "=l"(w[2]), "=l"(w[3])
+                 : "r"(p + 2 * d)
+                 : "memory");
+  } else {
+    widen2(lds_chunk<float, false>(s, c, t, tpr, d), w);
+  }
 }
 
 // Joins NV sums of a row's warps (each after warp_sum): every thread gets the
@@ -486,12 +551,35 @@ __device__ __forceinline__ void ckpt_widen(const RawCkpt<VEC>& r, float (&v)[8])
   }
 }
 
-__device__ __forceinline__ void ckpt_widen2(uint2 q, float f, f32x2 (&v)[4]) {
-  const f32x2 ff = pair(f, f);
+// The same of a checkpoint row in shared memory.
+template <bool VEC>
+__device__ __forceinline__ void lds_ckpt(uint32_t q, uint32_t ex, int c, int t, int tpr, int d,
+                                         f32x2 (&v)[4]) {
+  if (VEC) {
+    const int i = c * tpr + t;
+    if (8 * i >= d) {
 #pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    const float2 x = unpack_e4m3x2((h < 2 ? q.x : q.y) >> (16 * (h & 1)));
-    v[h] = mul2(pair(x.x, x.y), ff);
+      for (int h = 0; h < 4; ++h) v[h] = 0ull;
+      return;
+    }
+    const uint2 w = lds_v2(q + 8 * i);
+    const float f = ckpt_factor(lds_u8(ex + i / 4));
+    const f32x2 ff = pair(f, f);
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      const float2 x = unpack_e4m3x2((h < 2 ? w.x : w.y) >> (16 * (h & 1)));
+      v[h] = mul2(pair(x.x, x.y), ff);
+    }
+  } else {
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int col = chunk_col<false>(c, j, t, tpr);
+      x[j] = col < d ? unpack_e4m3x2(lds_u8(q + col)).x * ckpt_factor(lds_u8(ex + col / kCkptBlock))
+                     : 0.f;
+    }
+#pragma unroll
+    for (int h = 0; h < 4; ++h) v[h] = pair(x[2 * h], x[2 * h + 1]);
   }
 }
 
