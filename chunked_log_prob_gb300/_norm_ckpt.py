@@ -3,51 +3,62 @@ include/grpo_gb300.h (argument marshalling only, like ``_binding``).
 
 Tensors are 2-D with the last dimension contiguous; rows may be any distance
 apart. Outputs are allocated when not given.
+
+The calls are short (a decoded token's norm takes the GPU 3 us), so the common
+case of every check is one expression; what it refuses is looked at again for
+the message.
 """
 
 from __future__ import annotations
 
 import ctypes
-from dataclasses import dataclass
+from functools import lru_cache
 from typing import NamedTuple
 
 import torch
 
-from ._binding import GRPO_OK, GrpoError, GrpoNormDesc, _check, _ptr, _stream, lib
+from ._binding import GRPO_OK, GrpoError, GrpoNormDesc, lib
 
+_F32 = torch.float32
+_U8 = torch.uint8
+_BF16 = torch.bfloat16
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _KINDS = {"layer": 0, "rms": 1}
+_byref = ctypes.byref
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_empty, _empty_like = torch.empty, torch.empty_like
 
 
-@dataclass(frozen=True)
 class Checkpoint8:
     """An activation [n_tokens, hidden] in 8 bits: e4m3 values, one power of two
     per 32 columns of a row. ``data`` is the library's buffer (uint8); ``q`` and
     ``exponents`` are views of it: x is about q * 2^(exponents - 127)."""
 
-    data: torch.Tensor
-    n_tokens: int
-    hidden: int
+    __slots__ = ("data", "n_tokens", "hidden")
+
+    def __init__(self, data: torch.Tensor, n_tokens: int, hidden: int):
+        self.data, self.n_tokens, self.hidden = data, n_tokens, hidden
+
+    def __repr__(self):
+        return f"Checkpoint8(n_tokens={self.n_tokens}, hidden={self.hidden}, data={self.data.device})"
 
     def _layout(self):
-        out = [ctypes.c_int64() for _ in range(3)]
-        _raise(lib.grpo_ckpt_layout(self.n_tokens, self.hidden, *map(ctypes.byref, out)),
-               "grpo_ckpt_layout")
-        return [int(v.value) for v in out]
+        return _ckpt_layout(self.n_tokens, self.hidden)[:3]
 
     @property
     def q(self) -> torch.Tensor:
         """float8_e4m3fn [n_tokens, hidden]."""
-        ldq, _, _ = self._layout()
-        return self.data.view(torch.float8_e4m3fn).as_strided((self.n_tokens, self.hidden),
-                                                              (ldq, 1))
+        n, d = self.n_tokens, self.hidden
+        ldq = _ckpt_layout(n, d)[0]
+        return self.data.view(torch.float8_e4m3fn).as_strided((n, d), (ldq, 1))
 
     @property
     def exponents(self) -> torch.Tensor:
         """uint8 [n_tokens, ceil(hidden / 32)]: k + 127."""
-        _, off, lde = self._layout()
-        return self.data.as_strided((self.n_tokens, -(-self.hidden // 32)), (lde, 1),
-                                    self.data.storage_offset() + off)
+        n, d = self.n_tokens, self.hidden
+        _, off, lde, _ = _ckpt_layout(n, d)
+        data = self.data
+        return data.as_strided((n, -(-d // 32)), (lde, 1), data.storage_offset() + off)
 
 
 class NormForward(NamedTuple):
@@ -69,78 +80,115 @@ def _raise(rc, where):
         raise GrpoError(rc, where)
 
 
-def _check_rows(t, name, dtype, shape, device):
-    """Like ``_check``, for a tensor whose rows may be apart."""
+# ------------------------------------------------------------------ checks ----
+
+
+def _type_of_rows(t, name):
+    """The library's code for the type of a 2-D tensor."""
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected 2 dimensions, got {t.dim()}")
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: expected bfloat16, float16 or float32, got {t.dtype}")
+    return code
+
+
+def _rows(t, name, dtype, shape, device):
+    """Checks a tensor whose rows may be apart; its row stride (0: packed)."""
+    if t.dtype is dtype and t.shape == shape and t.device == device:
+        if t.is_contiguous():
+            return 0
+        n, d = shape
+        if n <= 1 and (d <= 1 or t.stride(1) == 1):
+            return 0  # a single row has no distance to the next
+        if d <= 1 or t.stride(1) == 1:
+            s = t.stride(0)
+            if s >= d:
+                return s
+            raise ValueError(f"{name}: rows overlap (stride {s} < {d} columns)")
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    _refuse(t, name, dtype, shape, device)
+
+
+def _packed(t, name, dtype, shape, device):
+    """Checks a contiguous tensor; its address."""
+    if (t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
+        return t.data_ptr()
+    _refuse(t, name, dtype, shape, device)
+
+
+def _refuse(t, name, dtype, shape, device):
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name}: expected device {device}, got {t.device}")
-    if t.numel() and t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        raise ValueError(f"{name}: rows overlap (stride {t.stride(0)} < {t.shape[1]} columns)")
-
-
-def _row_stride(t):
-    # A single row has no distance to the next; torch may report any.
-    return 0 if t is None or t.shape[0] <= 1 else t.stride(0)
-
-
-def _need_cuda(device):
-    if device.type != "cuda":
-        raise ValueError(f"expected tensors on a CUDA device, got {device}")
-
-
-def _rows_shape(t, name):
-    if t.dim() != 2:
-        raise ValueError(f"{name}: expected 2 dimensions, got {t.dim()}")
-    if t.dtype not in _DTYPES:
-        raise TypeError(f"{name}: expected bfloat16, float16 or float32, got {t.dtype}")
-    return t.shape
+    raise ValueError(f"{name}: must be contiguous")
 
 
 def _kind(kind):
-    if kind not in _KINDS:
+    k = _KINDS.get(kind)
+    if k is None:
         raise ValueError(f"kind: expected 'layer' or 'rms', got {kind!r}")
-    return _KINDS[kind]
+    return k
 
 
-def _check_weight(weight, bias, x):
-    for t, name in ((weight, "weight"), (bias, "bias")):
-        if t is not None:
-            if t.dtype not in (x.dtype, torch.float32):
-                raise TypeError(f"{name}: expected {x.dtype} or torch.float32, got {t.dtype}")
-            _check(t, name, t.dtype, (x.shape[1],), x.device)
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
-        raise TypeError(f"bias: expected weight's type {weight.dtype}, got {bias.dtype}")
-    p = weight if weight is not None else bias
-    return _DTYPES[p.dtype if p is not None else torch.float32]
+def _param(t, name, dtype, d, device):
+    """Checks a weight or bias (of the rows' type or fp32); its address."""
+    wt = t.dtype
+    if wt is not dtype and wt is not _F32:
+        raise TypeError(f"{name}: expected {dtype} or torch.float32, got {wt}")
+    return _packed(t, name, wt, (d,), device)
 
 
-def _check_ckpt(ckpt, n, d, device):
+def _like(t, stride):
+    """A packed tensor of the shape and type of `t`, whose row stride is known."""
+    return _empty_like(t) if stride == 0 else _empty(t.shape, dtype=t.dtype, device=t.device)
+
+
+def _stream_of(device):
+    if device.type != "cuda":
+        raise ValueError(f"expected tensors on a CUDA device, got {device}")
+    return _raw_stream(device.index)
+
+
+@lru_cache(maxsize=512)
+def _ckpt_layout(n, d):
+    """(bytes from row to row of q, where the exponents begin, bytes from row to
+    row of them, bytes in all)."""
+    out = [ctypes.c_int64() for _ in range(3)]
+    _raise(lib.grpo_ckpt_layout(n, d, *map(_byref, out)), "grpo_ckpt_layout")
+    return (*(v.value for v in out), grpo_ckpt_size(n, d))
+
+
+def _ckpt(ckpt, n, d, device):
+    """Checks a checkpoint; its address."""
     if not isinstance(ckpt, Checkpoint8):
         raise TypeError(f"ckpt: expected Checkpoint8, got {type(ckpt).__name__}")
-    if (ckpt.n_tokens, ckpt.hidden) != (n, d):
+    if ckpt.n_tokens != n or ckpt.hidden != d:
         raise ValueError(f"ckpt: expected shape {(n, d)}, got {(ckpt.n_tokens, ckpt.hidden)}")
-    need = grpo_ckpt_size(n, d)
     t = ckpt.data
-    if t.dtype != torch.uint8 or t.dim() != 1 or not t.is_contiguous() or t.numel() < need:
+    need = _ckpt_layout(n, d)[3]
+    if t.dtype is not _U8 or t.dim() != 1 or not t.is_contiguous() or t.numel() < need:
         raise ValueError(f"ckpt: data must be contiguous uint8 of at least {need} bytes")
     if t.device != device:
         raise ValueError(f"ckpt: expected device {device}, got {t.device}")
+    return t.data_ptr()
+
+
+# ------------------------------------------------------------------- calls ----
 
 
 def grpo_ckpt_size(n_tokens, hidden) -> int:
     out = ctypes.c_size_t(0)
-    _raise(lib.grpo_ckpt_size(int(n_tokens), int(hidden), ctypes.byref(out)), "grpo_ckpt_size")
+    _raise(lib.grpo_ckpt_size(int(n_tokens), int(hidden), _byref(out)), "grpo_ckpt_size")
     return int(out.value)
 
 
 def alloc_ckpt(n_tokens, hidden, device=None) -> Checkpoint8:
-    data = torch.empty(grpo_ckpt_size(n_tokens, hidden), dtype=torch.uint8, device=device)
-    return Checkpoint8(data, int(n_tokens), int(hidden))
+    n, d = int(n_tokens), int(hidden)
+    return Checkpoint8(torch.empty(_ckpt_layout(n, d)[3], dtype=_U8, device=device), n, d)
 
 
 def grpo_norm_fwd(x, weight=None, bias=None, *, residual=None, kind="rms", eps=1e-6, mask=None,
@@ -150,55 +198,76 @@ def grpo_norm_fwd(x, weight=None, bias=None, *, residual=None, kind="rms", eps=1
 
     Returns (y, z, mean, rstd, ckpt): mean and rstd (fp32 [N], mean for layer
     norm only) are what ``grpo_norm_bwd`` needs; ckpt is z's 8-bit checkpoint.
+    Masked rows (mask 0) are not read; their outputs are zeros.
     """
-    n, d = _rows_shape(x, "x")
-    dev, dt = x.device, x.dtype
+    code = _type_of_rows(x, "x")
+    shape, dt, dev = x.shape, x.dtype, x.device
+    n, d = shape
     k = _kind(kind)
-    wt = _check_weight(weight, bias, x)
+    sx = _rows(x, "x", dt, shape, dev)
+    pw = pb = pr = pz = pm = ps = pmask = pc = None
+    wt = 2
+    sr = sz = 0
+    if weight is not None:
+        pw = _param(weight, "weight", dt, d, dev)
+        wt = _DTYPES[weight.dtype]
+    if bias is not None:
+        pb = _param(bias, "bias", dt, d, dev)
+        if weight is not None and weight.dtype is not bias.dtype:
+            raise TypeError(f"bias: expected weight's type {weight.dtype}, got {bias.dtype}")
+        wt = _DTYPES[bias.dtype]
     if residual is not None:
-        _check_rows(residual, "residual", dt, (n, d), dev)
+        sr = _rows(residual, "residual", dt, shape, dev)
+        pr = residual.data_ptr()
         if z is None:
-            z = torch.empty((n, d), dtype=dt, device=dev)
+            z = _like(x, sx)
         else:
-            _check_rows(z, "z", dt, (n, d), dev)
+            sz = _rows(z, "z", dt, shape, dev)
+        pz = z.data_ptr()
     elif z is not None:
         raise ValueError("z: is x itself without a residual")
     if mask is not None:
-        _check(mask, "mask", torch.uint8, (n,), dev)
+        pmask = _packed(mask, "mask", _U8, (n,), dev)
+    sy = 0
     if y is None:
-        y = torch.empty((n, d), dtype=dt, device=dev)
+        y = _like(x, sx)
     else:
-        _check_rows(y, "y", dt, (n, d), dev)
+        sy = _rows(y, "y", dt, shape, dev)
     if mean is not None:
         if k:
             raise ValueError("mean: RMS norm has none")
-        _check(mean, "mean", torch.float32, (n,), dev)
+        pm = _packed(mean, "mean", _F32, (n,), dev)
     elif want_stats and not k:
-        mean = torch.empty(n, dtype=torch.float32, device=dev)
+        mean = _empty(n, dtype=_F32, device=dev)
+        pm = mean.data_ptr()
     if rstd is not None:
-        _check(rstd, "rstd", torch.float32, (n,), dev)
+        ps = _packed(rstd, "rstd", _F32, (n,), dev)
     elif want_stats:
-        rstd = torch.empty(n, dtype=torch.float32, device=dev)
-    if ckpt is not None:
-        _check_ckpt(ckpt, n, d, dev)
-    elif want_ckpt:
-        ckpt = alloc_ckpt(n, d, dev)
-    _need_cuda(dev)
-    desc = GrpoNormDesc(n, d, _DTYPES[dt], wt, k, eps, 0, _row_stride(x), _row_stride(residual),
-                        _row_stride(y), _row_stride(z), 0, 0, 0)
-    _raise(lib.grpo_norm_fwd(_ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), _ptr(mask),
-                             _ptr(y), _ptr(z), _ptr(mean), _ptr(rstd),
-                             _ptr(ckpt.data) if ckpt is not None else None,
-                             ctypes.byref(desc), _stream(dev)), "grpo_norm_fwd")
+        rstd = _empty(n, dtype=_F32, device=dev)
+        ps = rstd.data_ptr()
+    if ckpt is None and want_ckpt:
+        ckpt = Checkpoint8(_empty(_ckpt_layout(n, d)[3], dtype=_U8, device=dev), n, d)
+        pc = ckpt.data.data_ptr()
+    elif ckpt is not None:
+        pc = _ckpt(ckpt, n, d, dev)
+    desc = GrpoNormDesc(n, d, code, wt, k, eps, 0, sx, sr, sy, sz)
+    rc = lib.grpo_norm_fwd(x.data_ptr(), pr, pw, pb, pmask, y.data_ptr(), pz, pm, ps, pc,
+                           _byref(desc), _stream_of(dev))
+    if rc:
+        raise GrpoError(rc, "grpo_norm_fwd")
     return NormForward(y, x if residual is None else z, mean, rstd, ckpt)
 
 
-def grpo_norm_workspace_size(n_tokens, hidden) -> int:
+@lru_cache(maxsize=512)
+def _norm_workspace(n, d):
     out = ctypes.c_size_t(0)
-    desc = GrpoNormDesc(int(n_tokens), int(hidden), 0, 0, 0, 0.0, 0, 0, 0, 0, 0, 0, 0, 0)
-    _raise(lib.grpo_norm_workspace_size(ctypes.byref(desc), ctypes.byref(out)),
-           "grpo_norm_workspace_size")
+    desc = GrpoNormDesc(n, d)
+    _raise(lib.grpo_norm_workspace_size(_byref(desc), _byref(out)), "grpo_norm_workspace_size")
     return int(out.value)
+
+
+def grpo_norm_workspace_size(n_tokens, hidden) -> int:
+    return _norm_workspace(int(n_tokens), int(hidden))
 
 
 def grpo_norm_bwd(dy, x, weight, mean, rstd, *, dres=None, kind="rms", mask=None,
@@ -211,91 +280,120 @@ def grpo_norm_bwd(dy, x, weight, mean, rstd, *, dres=None, kind="rms", mask=None
     dweight and dbias are fp32 [D], added to add_dweight and add_dbias (which
     may be the outputs themselves). dweight is left out without a weight.
     """
-    n, d = _rows_shape(dy, "dy")
-    dev, dt = dy.device, dy.dtype
+    code = _type_of_rows(dy, "dy")
+    shape, dt, dev = dy.shape, dy.dtype, dy.device
+    n, d = shape
     k = _kind(kind)
-    wt = _check_weight(weight, None, dy)
-    from_ckpt = isinstance(x, Checkpoint8)
-    if from_ckpt:
-        _check_ckpt(x, n, d, dev)
+    sdy = _rows(dy, "dy", dt, shape, dev)
+    px = pc = pw = pmean = pmask = pr = pdw = pdb = paw = pab = pws = None
+    wt = 2
+    sx = sr = sdx = ws_bytes = 0
+    if weight is not None:
+        pw = _param(weight, "weight", dt, d, dev)
+        wt = _DTYPES[weight.dtype]
+    if isinstance(x, Checkpoint8):
+        pc = _ckpt(x, n, d, dev)
     else:
-        _check_rows(x, "x", dt, (n, d), dev)
-    if k and mean is not None:
-        raise ValueError("mean: RMS norm has none")
-    if not k:
-        if mean is None:
-            raise ValueError("mean: needed by layer norm")
-        _check(mean, "mean", torch.float32, (n,), dev)
-    _check(rstd, "rstd", torch.float32, (n,), dev)
+        sx = _rows(x, "x", dt, shape, dev)
+        px = x.data_ptr()
+    if mean is not None:
+        if k:
+            raise ValueError("mean: RMS norm has none")
+        pmean = _packed(mean, "mean", _F32, (n,), dev)
+    elif not k:
+        raise ValueError("mean: needed by layer norm")
+    ps = _packed(rstd, "rstd", _F32, (n,), dev)
     if mask is not None:
-        _check(mask, "mask", torch.uint8, (n,), dev)
+        pmask = _packed(mask, "mask", _U8, (n,), dev)
     if dres is not None:
-        _check_rows(dres, "dres", dt, (n, d), dev)
+        sr = _rows(dres, "dres", dt, shape, dev)
+        pr = dres.data_ptr()
     if dx is None:
-        dx = torch.empty((n, d), dtype=dt, device=dev)
+        dx = _like(dy, sdy)
     else:
-        _check_rows(dx, "dx", dt, (n, d), dev)
+        sdx = _rows(dx, "dx", dt, shape, dev)
     if want_dweight is None:
         want_dweight = weight is not None
-    if dweight is None and (want_dweight or add_dweight is not None):
-        dweight = torch.empty(d, dtype=torch.float32, device=dev)
-    if dbias is None and (want_dbias or add_dbias is not None):
-        dbias = torch.empty(d, dtype=torch.float32, device=dev)
-    for t, name in ((dweight, "dweight"), (dbias, "dbias"), (add_dweight, "add_dweight"),
-                    (add_dbias, "add_dbias")):
-        if t is not None:
-            _check(t, name, torch.float32, (d,), dev)
-    if workspace is None and (dweight is not None or dbias is not None):
-        workspace = torch.empty(grpo_norm_workspace_size(n, d), dtype=torch.uint8, device=dev)
-    _need_cuda(dev)
-    desc = GrpoNormDesc(n, d, _DTYPES[dt], wt, k, 0.0, 0, 0 if from_ckpt else _row_stride(x), 0, 0,
-                        0, _row_stride(dy), _row_stride(dres), _row_stride(dx))
-    _raise(lib.grpo_norm_bwd(_ptr(dy), None if from_ckpt else _ptr(x),
-                             _ptr(x.data) if from_ckpt else None, _ptr(weight), _ptr(mean),
-                             _ptr(rstd), _ptr(mask), _ptr(dres), _ptr(dx), _ptr(dweight),
-                             _ptr(dbias), _ptr(add_dweight), _ptr(add_dbias), ctypes.byref(desc),
-                             _ptr(workspace), workspace.numel() if workspace is not None else 0,
-                             _stream(dev)), "grpo_norm_bwd")
+    vec = (d,)
+    if dweight is not None:
+        pdw = _packed(dweight, "dweight", _F32, vec, dev)
+    elif want_dweight or add_dweight is not None:
+        dweight = _empty(d, dtype=_F32, device=dev)
+        pdw = dweight.data_ptr()
+    if dbias is not None:
+        pdb = _packed(dbias, "dbias", _F32, vec, dev)
+    elif want_dbias or add_dbias is not None:
+        dbias = _empty(d, dtype=_F32, device=dev)
+        pdb = dbias.data_ptr()
+    if add_dweight is not None:
+        paw = _packed(add_dweight, "add_dweight", _F32, vec, dev)
+    if add_dbias is not None:
+        pab = _packed(add_dbias, "add_dbias", _F32, vec, dev)
+    if workspace is None:
+        if pdw is not None or pdb is not None:
+            workspace = _empty(_norm_workspace(n, d), dtype=_U8, device=dev)
+    if workspace is not None:
+        if workspace.device != dev:
+            raise ValueError(f"workspace: expected device {dev}, got {workspace.device}")
+        pws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    desc = GrpoNormDesc(n, d, code, wt, k, 0.0, 0, sx, 0, 0, 0, sdy, sr, sdx)
+    rc = lib.grpo_norm_bwd(dy.data_ptr(), px, pc, pw, pmean, ps, pmask, pr, dx.data_ptr(), pdw, pdb,
+                           paw, pab, _byref(desc), pws, ws_bytes, _stream_of(dev))
+    if rc:
+        raise GrpoError(rc, "grpo_norm_bwd")
     return NormBackward(dx, dweight, dbias)
 
 
 def grpo_ckpt_pack(x, *, mask=None, ckpt=None) -> Checkpoint8:
     """The 8-bit checkpoint of x [N, D]; masked rows are kept as zeros, unread."""
-    n, d = _rows_shape(x, "x")
-    _check_rows(x, "x", x.dtype, (n, d), x.device)
-    if mask is not None:
-        _check(mask, "mask", torch.uint8, (n,), x.device)
+    code = _type_of_rows(x, "x")
+    shape, dev = x.shape, x.device
+    n, d = shape
+    sx = _rows(x, "x", x.dtype, shape, dev)
+    pmask = None if mask is None else _packed(mask, "mask", _U8, (n,), dev)
     if ckpt is None:
-        ckpt = alloc_ckpt(n, d, x.device)
+        ckpt = Checkpoint8(_empty(_ckpt_layout(n, d)[3], dtype=_U8, device=dev), n, d)
+        pc = ckpt.data.data_ptr()
     else:
-        _check_ckpt(ckpt, n, d, x.device)
-    _need_cuda(x.device)
-    _raise(lib.grpo_ckpt_pack(_ptr(x), _ptr(mask), _ptr(ckpt.data), n, d, _DTYPES[x.dtype],
-                              _row_stride(x), _stream(x.device)), "grpo_ckpt_pack")
+        pc = _ckpt(ckpt, n, d, dev)
+    rc = lib.grpo_ckpt_pack(x.data_ptr(), pmask, pc, n, d, code, sx, _stream_of(dev))
+    if rc:
+        raise GrpoError(rc, "grpo_ckpt_pack")
     return ckpt
 
 
 def grpo_ckpt_unpack(ckpt, dtype=torch.bfloat16, *, out=None) -> torch.Tensor:
     """The values a checkpoint stands for, rounded once to ``dtype``."""
-    dev = ckpt.data.device
-    n, d = ckpt.n_tokens, ckpt.hidden
-    _check_ckpt(ckpt, n, d, dev)
+    if not isinstance(ckpt, Checkpoint8):
+        raise TypeError(f"ckpt: expected Checkpoint8, got {type(ckpt).__name__}")
+    data = ckpt.data
+    dev = data.device
+    n, d = shape = ckpt.n_tokens, ckpt.hidden
+    pc = _ckpt(ckpt, n, d, dev)
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"dtype: expected bfloat16, float16 or float32, got {dtype}")
+    so = 0
     if out is None:
-        out = torch.empty((n, d), dtype=dtype, device=dev)
-    _rows_shape(out, "out")
-    _check_rows(out, "out", dtype, (n, d), dev)
-    _need_cuda(dev)
-    _raise(lib.grpo_ckpt_unpack(_ptr(ckpt.data), _ptr(out), n, d, _DTYPES[out.dtype],
-                                _row_stride(out), _stream(dev)), "grpo_ckpt_unpack")
+        out = _empty(shape, dtype=dtype, device=dev)
+    else:
+        so = _rows(out, "out", dtype, shape, dev)
+    rc = lib.grpo_ckpt_unpack(pc, out.data_ptr(), n, d, code, so, _stream_of(dev))
+    if rc:
+        raise GrpoError(rc, "grpo_ckpt_unpack")
     return out
 
 
-def grpo_ckpt_wgrad_workspace_size(n_tokens, out_features, in_features) -> int:
+@lru_cache(maxsize=512)
+def _wgrad_workspace(n, out_features, in_features):
     out = ctypes.c_size_t(0)
-    _raise(lib.grpo_ckpt_wgrad_workspace_size(int(n_tokens), int(out_features), int(in_features),
-                                              ctypes.byref(out)),
+    _raise(lib.grpo_ckpt_wgrad_workspace_size(n, out_features, in_features, _byref(out)),
            "grpo_ckpt_wgrad_workspace_size")
     return int(out.value)
+
+
+def grpo_ckpt_wgrad_workspace_size(n_tokens, out_features, in_features) -> int:
+    return _wgrad_workspace(int(n_tokens), int(out_features), int(in_features))
 
 
 def grpo_ckpt_wgrad(dy, ckpt, *, add=None, dW=None, workspace=None) -> torch.Tensor:
@@ -305,24 +403,26 @@ def grpo_ckpt_wgrad(dy, ckpt, *, add=None, dW=None, workspace=None) -> torch.Ten
     """
     if dy.dim() != 2:
         raise ValueError(f"dy: expected 2 dimensions, got {dy.dim()}")
-    n, out = dy.shape
     dev = dy.device
-    _check_rows(dy, "dy", torch.bfloat16, (n, out), dev)
+    n, out = dy.shape
+    sdy = _rows(dy, "dy", _BF16, dy.shape, dev)
     if not isinstance(ckpt, Checkpoint8):
         raise TypeError(f"ckpt: expected Checkpoint8, got {type(ckpt).__name__}")
     d = ckpt.hidden
-    _check_ckpt(ckpt, n, d, dev)
+    pc = _ckpt(ckpt, n, d, dev)
+    shape = (out, d)
     if dW is None:
-        dW = torch.empty((out, d), dtype=torch.float32, device=dev)
+        dW = _empty(shape, dtype=_F32, device=dev)
+        pdw = dW.data_ptr()
     else:
-        _check(dW, "dW", torch.float32, (out, d), dev)
-    if add is not None:
-        _check(add, "add", torch.float32, (out, d), dev)
+        pdw = _packed(dW, "dW", _F32, shape, dev)
+    pa = None if add is None else _packed(add, "add", _F32, shape, dev)
     if workspace is None:
-        workspace = torch.empty(grpo_ckpt_wgrad_workspace_size(n, out, d), dtype=torch.uint8,
-                                device=dev)
-    _need_cuda(dev)
-    _raise(lib.grpo_ckpt_wgrad(_ptr(dy), _ptr(ckpt.data), _ptr(add), _ptr(dW), n, out, d,
-                               _row_stride(dy), _ptr(workspace), workspace.numel(), _stream(dev)),
-           "grpo_ckpt_wgrad")
+        workspace = _empty(_wgrad_workspace(n, out, d), dtype=_U8, device=dev)
+    elif workspace.device != dev:
+        raise ValueError(f"workspace: expected device {dev}, got {workspace.device}")
+    rc = lib.grpo_ckpt_wgrad(dy.data_ptr(), pc, pa, pdw, n, out, d, sdy, workspace.data_ptr(),
+                             workspace.numel() * workspace.element_size(), _stream_of(dev))
+    if rc:
+        raise GrpoError(rc, "grpo_ckpt_wgrad")
     return dW

@@ -231,7 +231,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int pair = static_cast<int>(blockIdx.x) / 2, pairs = static_cast<int>(gridDim.x) / 2;
   volatile int* abort_flag = &abort_sh;
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
+    // The status word of this call. Nothing writes it before a wait runs out.
+    if (blockIdx.x == 0) *args.status = GRPO_OK;
     for (int s = 0; s < kDy; ++s) {
       mbar_init(&full_bar[s], 2 + 2 * kConvertGroup);  // dY's TMA threads, converter warps
       mbar_init(&done_bar[s], 1);
@@ -558,6 +561,7 @@ __global__ void __launch_bounds__(kTileM) ckpt_wgrad_join_kernel(const WgradArgs
   const int c0 = static_cast<int>(blockIdx.y) * 16;  // column of the tile
   const int i0 = tn * kTileN + c0;
   if (row >= args.out || i0 >= args.in) return;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces are there
   float4 v[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -662,9 +666,17 @@ cudaError_t launch_ckpt_wgrad(const WgradArgs& a, int sms, cudaStream_t st) {
     e = cudaLaunchKernelEx(&cfg, ckpt_wgrad_kernel, map_dy, map_q, map_ex, map_dw, a, plan);
   }
   if (e != cudaSuccess || plan.cut == 0) return e;
+  // Its launch overlaps the end of the other (it waits for that itself).
+  cudaLaunchConfig_t join = {};
+  join.gridDim = dim3(plan.cut, kTileN / 16);
+  join.blockDim = dim3(kTileM);
+  join.stream = st;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  join.attrs = attr;
+  join.numAttrs = 1;
   LaunchTimer timer("ckpt_wgrad_join_kernel", st);
-  ckpt_wgrad_join_kernel<<<dim3(plan.cut, kTileN / 16), kTileM, 0, st>>>(a, plan);
-  return cudaGetLastError();
+  return cudaLaunchKernelEx(&join, ckpt_wgrad_join_kernel, a, plan);
 }
 
 }  // namespace grpo

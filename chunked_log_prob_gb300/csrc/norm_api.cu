@@ -280,9 +280,9 @@ int grpo_ckpt_wgrad(const void* dy, const void* ckpt, const float* add, float* d
   int sms = 0;
   if ((r = setup_device(&sms)) != GRPO_OK) return r;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(workspace, 0, 64, st) != cudaSuccess) return GRPO_ERR_CUDA;
   const size_t bytes = static_cast<size_t>(out) * in * sizeof(float);
   if (n_tokens == 0) {  // an empty sum
+    if (cudaMemsetAsync(workspace, 0, 64, st) != cudaSuccess) return GRPO_ERR_CUDA;
     const cudaError_t e = add == nullptr ? cudaMemsetAsync(dW, 0, bytes, st)
                           : add != dW    ? cudaMemcpyAsync(dW, add, bytes, cudaMemcpyDeviceToDevice, st)
                                          : cudaSuccess;

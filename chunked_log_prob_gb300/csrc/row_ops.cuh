@@ -321,6 +321,21 @@ template <bool VEC>
 __device__ __forceinline__ void stage_param(float* dst, const void* p, int type, int d, int thread,
                                             int threads) {
   const int half = d / 2;
+  if (VEC && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+    for (int i = thread; 8 * i < d; i += threads) {
+      float v[8];
+      if (type == GRPO_DTYPE_FP32)
+        widen(load_chunk<float, true>(static_cast<const float*>(p), 0, i, 0, d), v);
+      else if (type == GRPO_DTYPE_BF16)
+        widen(load_chunk<__nv_bfloat16, true>(static_cast<const __nv_bfloat16*>(p), 0, i, 0, d), v);
+      else
+        widen(load_chunk<__half, true>(static_cast<const __half*>(p), 0, i, 0, d), v);
+      *reinterpret_cast<float4*>(dst + 4 * i) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4*>(dst + half + 4 * i) = make_float4(v[4], v[5], v[6], v[7]);
+    }
+    return;
+  }
+#pragma unroll 4
   for (int col = thread; col < d; col += threads) {
     const int j = col & 7;
     const int at = VEC ? (j >= 4 ? half : 0) + (col >> 3) * 4 + (j & 3) : col;
