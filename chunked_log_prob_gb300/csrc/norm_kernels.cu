@@ -231,10 +231,7 @@ __global__ void __launch_bounds__(ring_threads(CH)) norm_fwd_kernel(const NormFw
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       if (q != nullptr) {
-        float f[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) split(v[c][j], f[2 * j], f[2 * j + 1]);
-        ckpt_store_chunk<T, VEC>(f, q, ex, c, t, tpr, d);
+        ckpt_store_chunk<T, VEC>(v[c], q, ex, c, t, tpr, d);
       }
       if (VEC ? (c * tpr + t) * 8 >= d : 8 * c * tpr >= d) continue;
       if (live) {
@@ -330,8 +327,8 @@ __global__ void __launch_bounds__(512) norm_fwd_long_kernel(const NormFwdArgs a)
       stream(c, v);
       if (z != nullptr) store_chunk<T, VEC>(z, narrow<T>(v), c, t, tpr, d);
       if (a.ck.q != nullptr)
-        ckpt_store_chunk<T, VEC>(v, a.ck.q + row * a.ck.ldq, a.ck.ex + row * a.ck.lde, c, t, tpr,
-                                 d);
+        ckpt_store_chunk<T, VEC>({pair(v[0], v[1]), pair(v[2], v[3]), pair(v[4], v[5]), pair(v[6], v[7])},
+                                 a.ck.q + row * a.ck.ldq, a.ck.ex + row * a.ck.lde, c, t, tpr, d);
       if (live) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {

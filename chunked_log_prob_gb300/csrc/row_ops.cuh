@@ -263,6 +263,13 @@ __device__ __forceinline__ void bulk_row(uint32_t dst, const T* p, int d, uint64
             bar);
 }
 
+template <typename T>
+__device__ __forceinline__ void store_raw(T* p, const Raw8<T>& r) {
+  const uint4* w = reinterpret_cast<const uint4*>(&r);
+#pragma unroll
+  for (int k = 0; k < static_cast<int>(sizeof(r) / 16); ++k) reinterpret_cast<uint4*>(p)[k] = w[k];
+}
+
 __device__ __forceinline__ __nv_bfloat16 lds_value(uint32_t p, __nv_bfloat16) {
   uint16_t v;
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(p) : "memory");
@@ -423,9 +430,9 @@ __device__ __forceinline__ float pow2(int k) {
 }
 
 // |v| maxima that keep a NaN.
-__device__ __forceinline__ float max_abs_nan(float m, float v) {
+__device__ __forceinline__ float max_abs_nan(float a, float b, float c) {
   float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 
@@ -454,58 +461,83 @@ __device__ __forceinline__ float ckpt_scaled(float v, float inv, int k) {
   return v;
 }
 
+// 8 columns of a block, of which 4 neighbouring lanes hold one, as e4m3, and the
+// block's exponent byte. Every lane of the warp calls this (0 where there is no
+// column).
+template <typename T>
+__device__ __forceinline__ uint2 ckpt_encode(const f32x2 (&p)[4], int& ex) {
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) split(p[j], v[2 * j], v[2 * j + 1]);
+  float a = max_abs_nan(v[0], v[1], v[2]);
+  a = max_abs_nan(a, v[3], v[4]);
+  a = max_abs_nan(max_abs_nan(a, v[5], v[6]), v[7], v[7]);
+  const float b = __shfl_xor_sync(0xffffffffu, a, 1);
+  a = max_abs_nan(a, b, b);
+  const float c = __shfl_xor_sync(0xffffffffu, a, 2);
+  a = max_abs_nan(a, c, c);
+  uint2 w;
+  int k = ckpt_exponent(a);
+  // Nothing in the warp's blocks is special (the usual case): scale and round.
+  // The branch keeps some ten instructions per value out of the path.
+  if (__all_sync(0xffffffffu, a <= FLT_MAX && k < CkptTop<T>::k)) {
+    const float inv = pow2(-k);
+    const f32x2 ii = pair(inv, inv);
+    uint32_t h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float lo, hi;
+      split(mul2(p[j], ii), lo, hi);
+      h[j] = pack_e4m3x2(lo, hi);
+    }
+    w.x = __byte_perm(h[0], h[1], 0x5410);
+    w.y = __byte_perm(h[2], h[3], 0x5410);
+  } else {
+    a = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float m = fabsf(v[j]);
+      if (m <= FLT_MAX) a = fmaxf(a, m);
+    }
+    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+    k = ckpt_exponent(a);
+    const float inv = pow2(-k);
+    uint32_t h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      h[j] = pack_e4m3x2(ckpt_scaled<T>(v[2 * j], inv, k), ckpt_scaled<T>(v[2 * j + 1], inv, k));
+    w.x = __byte_perm(h[0], h[1], 0x5410);
+    w.y = __byte_perm(h[2], h[3], 0x5410);
+  }
+  ex = k + kCkptBias;
+  return w;
+}
+
 // Writes chunk c of a row to its checkpoint. Every lane of the warp calls this
 // (values past column d are 0). q: the row's bytes; ex: its exponents.
 template <typename T, bool VEC>
-__device__ __forceinline__ void ckpt_store_chunk(const float (&v)[8], uint8_t* q, uint8_t* ex,
+__device__ __forceinline__ void ckpt_store_chunk(const f32x2 (&v)[4], uint8_t* q, uint8_t* ex,
                                                  int c, int t, int tpr, int d) {
   if (VEC) {
     const int col = chunk_col<true>(c, 0, t, tpr);
-    float a = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) a = max_abs_nan(a, v[j]);
-    a = max_abs_nan(a, __shfl_xor_sync(0xffffffffu, a, 1));
-    a = max_abs_nan(a, __shfl_xor_sync(0xffffffffu, a, 2));
-    uint2 w;
-    int k;
-    // No value of the warp's blocks is special (the usual case): scale and
-    // round. The branch keeps some ten instructions per value out of the path.
-    const bool plain = a <= FLT_MAX && ckpt_exponent(a) < CkptTop<T>::k;
-    if (__all_sync(0xffffffffu, plain)) {
-      k = ckpt_exponent(a);
-      const float inv = pow2(-k);
-      w.x = pack_e4m3x2(v[0] * inv, v[1] * inv) | pack_e4m3x2(v[2] * inv, v[3] * inv) << 16;
-      w.y = pack_e4m3x2(v[4] * inv, v[5] * inv) | pack_e4m3x2(v[6] * inv, v[7] * inv) << 16;
-    } else {
-      a = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float m = fabsf(v[j]);
-        if (m <= FLT_MAX) a = fmaxf(a, m);
-      }
-      a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
-      a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
-      k = ckpt_exponent(a);
-      const float inv = pow2(-k);
-      uint32_t h[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        h[j] = pack_e4m3x2(ckpt_scaled<T>(v[2 * j], inv, k), ckpt_scaled<T>(v[2 * j + 1], inv, k));
-      w.x = h[0] | h[1] << 16;
-      w.y = h[2] | h[3] << 16;
-    }
+    int e;
+    const uint2 w = ckpt_encode<T>(v, e);
     if (col < d) {
       *reinterpret_cast<uint2*>(q + col) = w;
-      if ((t & 3) == 0) ex[col / kCkptBlock] = static_cast<uint8_t>(k + kCkptBias);
+      if ((t & 3) == 0) ex[col / kCkptBlock] = static_cast<uint8_t>(e);
     }
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int col = chunk_col<false>(c, j, t, tpr);
-      const uint32_t u = __float_as_uint(v[j]) & 0x7fffffffu;
+      float lo, hi;
+      split(v[j >> 1], lo, hi);
+      const float x = (j & 1) ? hi : lo;
+      const uint32_t u = __float_as_uint(x) & 0x7fffffffu;
       const uint32_t a = __reduce_max_sync(0xffffffffu, u < 0x7f800000u ? u : 0u);
       const int k = ckpt_exponent(__uint_as_float(a));
-      const float s = ckpt_scaled<T>(v[j], pow2(-k), k);
+      const float s = ckpt_scaled<T>(x, pow2(-k), k);
       if (col < d) {
         q[col] = static_cast<uint8_t>(pack_e4m3x2(s, 0.f) & 0xffu);
         if ((t & 31) == 0) ex[col / kCkptBlock] = static_cast<uint8_t>(k + kCkptBias);
