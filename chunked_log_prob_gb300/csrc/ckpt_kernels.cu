@@ -134,12 +134,7 @@ __global__ void __launch_bounds__(kThreads) ckpt_pack_kernel(const CkptArgs a, c
       const int col = at[k].block * kCkptBlock + sub * 8;
       if (at[k].row < a.n && col < a.d) {
         uint8_t* q = a.ck.q + at[k].row * a.ck.ldq + col;
-        if (VEC || col + 8 <= a.d) {
-          *reinterpret_cast<uint2*>(q) = w;
-        } else {
-          for (int j = 0; j < a.d - col; ++j)
-            q[j] = static_cast<uint8_t>((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
-        }
+        *reinterpret_cast<uint2*>(q) = w;  // zeros into the padding behind d
         if (sub == 0) a.ck.ex[at[k].row * a.ck.lde + at[k].block] = static_cast<uint8_t>(e);
       }
     }

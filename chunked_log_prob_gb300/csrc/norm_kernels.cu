@@ -63,8 +63,10 @@ __global__ void __launch_bounds__(ring_threads(CH)) norm_fwd_kernel(const NormFw
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(16) float red[kMaxRows][2 * 2 * 16];
   __shared__ float warp_n[2][16];
+  __shared__ BlockTurn turns[VEC ? 1 : ring_threads(CH) / 32];
   const int t = threadIdx.x, tpr = blockDim.x, g = threadIdx.y, d = a.d;
   const int warps = tpr >> 5;
+  BlockTurn* const turn = turns + (VEC ? 0 : g * warps + (t >> 5));
   uint64_t* const bars = reinterpret_cast<uint64_t*>(smem) + g * kMaxSlots;
   float* const sw = reinterpret_cast<float*>(smem + kRingBars);
   float* const sb = sw + (a.weight != nullptr ? param_bytes(d) / 4 : 0);
@@ -231,7 +233,7 @@ __global__ void __launch_bounds__(ring_threads(CH)) norm_fwd_kernel(const NormFw
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       if (q != nullptr) {
-        ckpt_store_chunk<T, VEC>(v[c], q, ex, c, t, tpr, d);
+        ckpt_store_chunk<T, VEC>(v[c], q, ex, c, t, tpr, d, turn);
       }
       if (VEC ? (c * tpr + t) * 8 >= d : 8 * c * tpr >= d) continue;
       if (live) {
@@ -274,7 +276,9 @@ __global__ void __launch_bounds__(ring_threads(CH)) norm_fwd_kernel(const NormFw
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(512) norm_fwd_long_kernel(const NormFwdArgs a) {
   __shared__ float2 red[2 * 32];
+  __shared__ BlockTurn turns[VEC ? 1 : 16];
   const int t = threadIdx.x, tpr = blockDim.x, d = a.d;
+  BlockTurn* const turn = turns + (VEC ? 0 : t >> 5);
   const int chunks = (d + 8 * tpr - 1) / (8 * tpr);
   int phase = 0;
   for (long long row = blockIdx.x; row < a.n; row += gridDim.x) {
@@ -328,7 +332,7 @@ __global__ void __launch_bounds__(512) norm_fwd_long_kernel(const NormFwdArgs a)
       if (z != nullptr) store_chunk<T, VEC>(z, narrow<T>(v), c, t, tpr, d);
       if (a.ck.q != nullptr)
         ckpt_store_chunk<T, VEC>({pair(v[0], v[1]), pair(v[2], v[3]), pair(v[4], v[5]), pair(v[6], v[7])},
-                                 a.ck.q + row * a.ck.ldq, a.ck.ex + row * a.ck.lde, c, t, tpr, d);
+                                 a.ck.q + row * a.ck.ldq, a.ck.ex + row * a.ck.lde, c, t, tpr, d, turn);
       if (live) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -730,7 +734,7 @@ RowShape ring_shape(int d, int most, int threads) {
   return best;
 }
 
-constexpr size_t kSmemMax = 227 * 1024 - 8192;  // less the kernels' static arrays
+constexpr size_t kSmemMax = 227 * 1024 - 22528;  // less the kernels' static arrays
 constexpr size_t kSmemTarget = 72 * 1024;       // of a CTA: three to an SM
 
 // Rows in flight of a CTA: as many slots as fit kSmemTarget beside the
@@ -789,7 +793,7 @@ cudaError_t fwd_ring(const NormFwdArgs& a, const RowShape& s, int sms, cudaStrea
 
 template <typename T, bool VEC, int KIND>
 cudaError_t fwd_kind(const NormFwdArgs& a, int sms, cudaStream_t st) {
-  const RowShape s = ring_shape(a.d, 4, kRowThreads);
+  const RowShape s = ring_shape(a.d, VEC ? 4 : 2, kRowThreads);
   switch (s.ch) {
     case 1: return fwd_ring<T, VEC, 1, KIND>(a, s, sms, st);
     case 2: return fwd_ring<T, VEC, 2, KIND>(a, s, sms, st);

@@ -88,6 +88,10 @@ __device__ __forceinline__ void store_chunk(T* row, const Raw8<T>& r, int c, int
 #pragma unroll
       for (int i = 0; i < static_cast<int>(sizeof(r) / 16); ++i) p[i] = w[i];
     }
+  } else if (8 * (c + 1) * tpr <= d) {  // the whole row's chunk
+    T* p = row + 8 * c * tpr + t;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p[j * tpr] = r.e[j];
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -296,6 +300,10 @@ __device__ __forceinline__ Raw8<T> lds_chunk(uint32_t row, int c, int t, int tpr
 #pragma unroll
     for (int k = 0; k < static_cast<int>(sizeof(r) / 16); ++k)
       w[k] = 8 * i < d ? lds_v4(row + i * sizeof(r) + 16 * k) : make_uint4(0, 0, 0, 0);
+  } else if (8 * (c + 1) * tpr <= d) {
+    const uint32_t p = row + (8 * c * tpr + t) * sizeof(T);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r.e[j] = lds_value(p + j * tpr * static_cast<int>(sizeof(T)), T());
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -514,35 +522,43 @@ __device__ __forceinline__ uint2 ckpt_encode(const f32x2 (&p)[4], int& ex) {
   return w;
 }
 
+// 1 KB of shared memory a warp, for blocks between a column to a lane and 8
+// columns to a lane.
+struct BlockTurn {
+  float at[8][33];
+};
+
 // Writes chunk c of a row to its checkpoint. Every lane of the warp calls this
-// (values past column d are 0). q: the row's bytes; ex: its exponents.
+// (values past column d are 0, and so is what the padding behind d gets). q: the
+// row's bytes; ex: its exponents; turn: VEC false only, this warp's.
 template <typename T, bool VEC>
 __device__ __forceinline__ void ckpt_store_chunk(const f32x2 (&v)[4], uint8_t* q, uint8_t* ex,
-                                                 int c, int t, int tpr, int d) {
+                                                 int c, int t, int tpr, int d, BlockTurn* turn) {
+  int e, col;
+  uint2 w;
   if (VEC) {
-    const int col = chunk_col<true>(c, 0, t, tpr);
-    int e;
-    const uint2 w = ckpt_encode<T>(v, e);
-    if (col < d) {
-      *reinterpret_cast<uint2*>(q + col) = w;
-      if ((t & 3) == 0) ex[col / kCkptBlock] = static_cast<uint8_t>(e);
-    }
+    col = chunk_col<true>(c, 0, t, tpr);
+    w = ckpt_encode<T>(v, e);
   } else {
+    // The warp holds 8 blocks, one to each j.
+    const int lane = t & 31;
+    __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int col = chunk_col<false>(c, j, t, tpr);
+    for (int j = 0; j < 4; ++j) {
       float lo, hi;
-      split(v[j >> 1], lo, hi);
-      const float x = (j & 1) ? hi : lo;
-      const uint32_t u = __float_as_uint(x) & 0x7fffffffu;
-      const uint32_t a = __reduce_max_sync(0xffffffffu, u < 0x7f800000u ? u : 0u);
-      const int k = ckpt_exponent(__uint_as_float(a));
-      const float s = ckpt_scaled<T>(x, pow2(-k), k);
-      if (col < d) {
-        q[col] = static_cast<uint8_t>(pack_e4m3x2(s, 0.f) & 0xffu);
-        if ((t & 31) == 0) ex[col / kCkptBlock] = static_cast<uint8_t>(k + kCkptBias);
-      }
+      split(v[j], lo, hi);
+      turn->at[2 * j][lane] = lo;
+      turn->at[2 * j + 1][lane] = hi;
     }
+    __syncwarp();
+    const float* const b = turn->at[lane >> 2] + 8 * (lane & 3);
+    const f32x2 p[4] = {pair(b[0], b[1]), pair(b[2], b[3]), pair(b[4], b[5]), pair(b[6], b[7])};
+    w = ckpt_encode<T>(p, e);
+    col = (8 * c + (lane >> 2)) * tpr + (t - lane) + 8 * (lane & 3);
+  }
+  if (col < d) {
+    *reinterpret_cast<uint2*>(q + col) = w;
+    if ((t & 3) == 0) ex[col / kCkptBlock] = static_cast<uint8_t>(e);
   }
 }
 

@@ -446,7 +446,7 @@ int grpo_norm_bwd(const void* dy, const void* x_or_null, const void* ckpt_or_nul
  *
  * Buffer of a checkpoint: n_tokens rows of q, hidden rounded up to 16 bytes
  * each; from the next multiple of 256 on, rows of exponents, one byte k + 127
- * per 32 columns, rounded up to 16 bytes each. Padding bytes are not written.
+ * per 32 columns, rounded up to 16 bytes each. Padding bytes mean nothing.
  * hidden: 1 to 2^27. 1.03 bytes a value. */
 int grpo_ckpt_size(int64_t n_tokens, int32_t hidden, size_t* bytes);
 
