@@ -44,8 +44,8 @@ constexpr int kMaxSlots = 8;
 constexpr int kMaxRows = 8;  // rows of a CTA
 constexpr uint32_t kRingBars = kMaxRows * kMaxSlots * sizeof(uint64_t);
 
-// Threads of a CTA with 8 ch values a thread, at most (kNormRegisterRow columns).
-constexpr int ring_threads(int ch) { return ch == 4 ? 256 : ch == 3 ? 352 : 512; }
+// Threads of a CTA at most.
+constexpr int kRingThreads = 512;
 
 // After a timeout: lets the copies still in flight land (within the same limit).
 __device__ __forceinline__ void land(uint64_t* bars, int slots, uint32_t parity, uint32_t pending) {
@@ -59,11 +59,11 @@ __device__ __forceinline__ int row_count(long long row, long long n, long long s
 }
 
 template <typename T, bool VEC, int CH, int KIND>
-__global__ void __launch_bounds__(ring_threads(CH)) norm_fwd_kernel(const NormFwdArgs a, const Ring ring) {
+__global__ void __launch_bounds__(kRingThreads) norm_fwd_kernel(const NormFwdArgs a, const Ring ring) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(16) float red[kMaxRows][2 * 2 * 16];
   __shared__ float warp_n[2][16];
-  __shared__ BlockTurn turns[VEC ? 1 : ring_threads(CH) / 32];
+  __shared__ BlockTurn turns[VEC ? 1 : kRingThreads / 32];
   const int t = threadIdx.x, tpr = blockDim.x, g = threadIdx.y, d = a.d;
   const int warps = tpr >> 5;
   BlockTurn* const turn = turns + (VEC ? 0 : g * warps + (t >> 5));
@@ -377,7 +377,7 @@ struct RawStream<T, VEC, true> {
 // norm, or a bias gradient; else neither. 16 values a thread: with 32 the sums
 // alone take 64 to 128 registers (131072 x 2880 layer norm: 789 us against 545).
 template <typename T, bool VEC, int CH, bool CK, bool FULL>
-__global__ void __launch_bounds__(ring_threads(CH)) norm_bwd_kernel(const NormBwdArgs a, const Ring ring) {
+__global__ void __launch_bounds__(kRingThreads) norm_bwd_kernel(const NormBwdArgs a, const Ring ring) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(16) float red[kMaxRows][2 * 2 * 16];
   const int t = threadIdx.x, tpr = blockDim.x, g = threadIdx.y, d = a.d;
@@ -601,6 +601,7 @@ __global__ void __launch_bounds__(512) norm_bwd_long_kernel(const NormBwdArgs a)
       }
     };
     if (live) {
+#pragma unroll 4
       for (int c = 0; c < chunks; ++c) {
         terms(c);
 #pragma unroll
@@ -651,20 +652,33 @@ __global__ void __launch_bounds__(256) norm_bwd_cols_kernel(const NormBwdArgs a)
   } else {
     s.x = static_cast<const T*>(a.x) + first;
   }
-  for (long long row = static_cast<long long>(blockIdx.y) * 8 + g; row < a.n;
-       row += static_cast<long long>(gridDim.y) * 8) {
-    if (!row_live(a.mask, row, a.n)) continue;
-    float u[8], h[8];
-    widen(load_chunk<T, VEC>(dy + row * a.lddy, 0, t, 32, dd), u);
-    RawStream<T, VEC, CK> rx;
-    rx.load(s, row, 0, t, 32);
-    rx.get(h);
-    const float rs = a.rstd[row];
-    const float mean = a.kind != GRPO_NORM_RMS ? a.mean[row] : 0.f;
+  // Four rows' loads at a time, in flight together.
+  const long long step = static_cast<long long>(gridDim.y) * 8;
+  for (long long row = static_cast<long long>(blockIdx.y) * 8 + g; row < a.n; row += 4 * step) {
+    Raw8<T> ry[4];
+    RawStream<T, VEC, CK> rx[4];
+    float rs[4], mean[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      dw[j] += u[j] * ((h[j] - mean) * rs);
-      db[j] += u[j];
+    for (int k = 0; k < 4; ++k) {
+      const long long r = row + k * step;
+      rs[k] = mean[k] = 0.f;
+      if (!row_live(a.mask, r, a.n)) continue;
+      ry[k] = load_chunk<T, VEC>(dy + r * a.lddy, 0, t, 32, dd);
+      rx[k].load(s, r, 0, t, 32);
+      rs[k] = a.rstd[r];
+      if (a.kind != GRPO_NORM_RMS) mean[k] = a.mean[r];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (!row_live(a.mask, row + k * step, a.n)) continue;
+      float u[8], h[8];
+      widen(ry[k], u);
+      rx[k].get(h);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        dw[j] += u[j] * ((h[j] - mean[k]) * rs[k]);
+        db[j] += u[j];
+      }
     }
   }
 #pragma unroll
@@ -726,7 +740,7 @@ RowShape ring_shape(int d, int most, int threads) {
   for (int ch = most; ch >= 1; --ch) {
     const int tpr = (d + 256 * ch - 1) / (256 * ch) * 32;
     const int room = tpr * 8 * ch;
-    if (tpr > 512 || (best.ch != 0 && room >= best_room)) continue;
+    if (tpr > kRingThreads || (best.ch != 0 && room >= best_room)) continue;
     best = {tpr, std::min(kMaxRows, std::max(1, threads / tpr)), ch};
     best_room = room;
     if (10 * room <= 11 * d) break;
@@ -774,6 +788,14 @@ cudaError_t ctas_per_sm(int threads, size_t smem, int* n) {
   return e;
 }
 
+template <typename T, bool VEC>
+cudaError_t fwd_long(const NormFwdArgs& a, int sms, cudaStream_t st) {
+  const int grid = static_cast<int>(std::min<long long>(a.n, 3LL * sms));
+  LaunchTimer timer("norm_fwd_long_kernel", st);
+  norm_fwd_long_kernel<T, VEC><<<grid, 512, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
 template <typename T, bool VEC, int CH, int KIND>
 cudaError_t fwd_ring(const NormFwdArgs& a, const RowShape& s, int sms, cudaStream_t st) {
   constexpr auto kernel = norm_fwd_kernel<T, VEC, CH, KIND>;
@@ -781,6 +803,7 @@ cudaError_t fwd_ring(const NormFwdArgs& a, const RowShape& s, int sms, cudaStrea
       kRingBars + param_bytes(a.d) * ((a.weight != nullptr) + (a.bias != nullptr));
   const Ring ring = make_ring(row_slot<T, VEC>(a.d) * (a.res != nullptr ? 2 : 1), s.rows, fixed);
   const size_t smem = fixed + static_cast<size_t>(ring.slots) * ring.row_bytes * s.rows;
+  if (smem > kSmemMax) return fwd_long<T, VEC>(a, sms, st);
   int per_sm = 0;
   cudaError_t e = ctas_per_sm<kernel>(s.tpr * s.rows, smem, &per_sm);
   if (e != cudaSuccess) return e;
@@ -793,23 +816,21 @@ cudaError_t fwd_ring(const NormFwdArgs& a, const RowShape& s, int sms, cudaStrea
 
 template <typename T, bool VEC, int KIND>
 cudaError_t fwd_kind(const NormFwdArgs& a, int sms, cudaStream_t st) {
+  // One by one, 16 values a thread: 32 take 228 registers.
   const RowShape s = ring_shape(a.d, VEC ? 4 : 2, kRowThreads);
   switch (s.ch) {
     case 1: return fwd_ring<T, VEC, 1, KIND>(a, s, sms, st);
     case 2: return fwd_ring<T, VEC, 2, KIND>(a, s, sms, st);
-    case 3: return fwd_ring<T, VEC, 3, KIND>(a, s, sms, st);
-    default: return fwd_ring<T, VEC, 4, KIND>(a, s, sms, st);
+    case 3:
+      if constexpr (VEC) return fwd_ring<T, VEC, 3, KIND>(a, s, sms, st);
+    case 4:
+      if constexpr (VEC) return fwd_ring<T, VEC, 4, KIND>(a, s, sms, st);
+    default: return fwd_long<T, VEC>(a, sms, st);
   }
 }
 
 template <typename T, bool VEC>
 cudaError_t fwd_any(const NormFwdArgs& a, int sms, cudaStream_t st) {
-  if (a.d > kNormRegisterRow) {
-    const int grid = static_cast<int>(std::min<long long>(a.n, 3LL * sms));
-    LaunchTimer timer("norm_fwd_long_kernel", st);
-    norm_fwd_long_kernel<T, VEC><<<grid, 512, 0, st>>>(a);
-    return cudaGetLastError();
-  }
   return a.kind == GRPO_NORM_RMS ? fwd_kind<T, VEC, GRPO_NORM_RMS>(a, sms, st)
                                  : fwd_kind<T, VEC, GRPO_NORM_LAYER>(a, sms, st);
 }
