@@ -69,7 +69,7 @@ struct CkptArgs {
 };
 
 // Largest D of the kernels that hold a whole row in registers.
-constexpr int kNormRegisterRow = 8192;
+constexpr int kNormRegisterRow = 16384;
 // Rows of partial weight gradients of one backward call: at most this many.
 constexpr int kNormMaxPartials = 608;
 

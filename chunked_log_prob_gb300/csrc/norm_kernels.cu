@@ -37,6 +37,8 @@ __device__ __forceinline__ bool row_live(const uint8_t* mask, long long row, lon
 struct Ring {
   int slots;           // rows in flight for each row of the CTA
   uint32_t row_bytes;  // of a slot
+  int split;           // backward: CTAs of a row (a cluster of 2 beyond 8192 columns)
+  int part;            // and columns of the first
 };
 
 // Shared memory: barriers, then the parameters as fp32, then the rings.
@@ -52,6 +54,19 @@ __device__ __forceinline__ void land(uint64_t* bars, int slots, uint32_t parity,
   for (int s = 0; s < slots; ++s)
     if ((pending >> s) & 1u) row_wait(&bars[s], (parity >> s) & 1u);
 }
+
+// Two sums into the peer CTA's shared memory, counted on its barrier there.
+// `at`, `bar`: addresses in this CTA of what is meant in the peer's.
+__device__ __forceinline__ void send_sums(uint32_t at, uint32_t bar, uint32_t peer, float a,
+                                          float b) {
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%2, %3}, [%1];" ::"r"(
+          mapa_shared(at, peer)),
+      "r"(mapa_shared(bar, peer)), "f"(a), "f"(b)
+      : "memory");
+}
+
+__device__ __forceinline__ int param_width(int type) { return type == GRPO_DTYPE_FP32 ? 4 : 2; }
 
 // Rows of the group that begins at `row`.
 __device__ __forceinline__ int row_count(long long row, long long n, long long step) {
@@ -380,19 +395,36 @@ template <typename T, bool VEC, int CH, bool CK, bool FULL>
 __global__ void __launch_bounds__(kRingThreads) norm_bwd_kernel(const NormBwdArgs a, const Ring ring) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(16) float red[kMaxRows][2 * 2 * 16];
-  const int t = threadIdx.x, tpr = blockDim.x, g = threadIdx.y, d = a.d;
+  __shared__ __align__(8) uint64_t sums_bar[2];
+  __shared__ __align__(8) float peer_sums[2][2];
+  const int t = threadIdx.x, tpr = blockDim.x, g = threadIdx.y;
+  // This CTA's columns [col0, col0 + d) of the row.
+  const bool halved = ring.split == 2;
+  const uint32_t rank = halved ? cluster_ctarank() : 0u;
+  const int col0 = rank != 0 ? ring.part : 0;
+  const int d = halved ? (rank != 0 ? a.d - ring.part : ring.part) : a.d;
+  const int blk = static_cast<int>(blockIdx.x) / ring.split;
+  const int blks = static_cast<int>(gridDim.x) / ring.split;
   const int warps = tpr >> 5;
   uint64_t* const bars = reinterpret_cast<uint64_t*>(smem) + g * kMaxSlots;
   float* const sw = reinterpret_cast<float*>(smem + kRingBars);
-  uint8_t* const ring0 = reinterpret_cast<uint8_t*>(sw + (a.weight != nullptr ? param_bytes(d) / 4 : 0));
+  uint8_t* const ring0 =
+      reinterpret_cast<uint8_t*>(sw + (a.weight != nullptr ? param_bytes(d) / 4 : 0));
   const uint32_t sw32 = smem_u32(sw);
   const uint32_t rows0 = smem_u32(ring0) + g * ring.slots * ring.row_bytes;
   const uint32_t t_bytes = row_slot<T, VEC>(d);
-  const uint32_t q_bytes = static_cast<uint32_t>(a.ck.ldq), e_bytes = static_cast<uint32_t>(a.ck.lde);
+  // Of a checkpoint's row up to its padding, or (first of two CTAs) to `part`.
+  const bool ends = !halved || rank != 0;
+  const uint32_t q_bytes = static_cast<uint32_t>(ends ? a.ck.ldq - col0 : d);
+  const uint32_t e_bytes =
+      static_cast<uint32_t>(ends ? a.ck.lde - col0 / kCkptBlock : d / kCkptBlock);
   const uint32_t x_bytes = CK ? q_bytes + e_bytes : t_bytes;  // rows of 16 bytes
+  const T* const g_dy = static_cast<const T*>(a.dy) + col0;
+  const T* const g_x = static_cast<const T*>(a.x) + col0;
+  const T* const g_res = static_cast<const T*>(a.dres) + col0;
   const bool res = a.dres != nullptr, layer = FULL && a.kind == GRPO_NORM_LAYER;
-  const long long step = static_cast<long long>(gridDim.x) * blockDim.y;
-  const long long row0 = static_cast<long long>(blockIdx.x) * blockDim.y + g;
+  const long long step = static_cast<long long>(blks) * blockDim.y;
+  const long long row0 = static_cast<long long>(blk) * blockDim.y + g;
   const int count = row_count(row0, a.n, step);
   const uint8_t* const mask = a.mask;
   uint32_t pending = 0;
@@ -403,16 +435,17 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_kernel(const NormBwdArg
     if (mask != nullptr && mask[r] == 0) return;
     pending |= 1u << slot;
     const uint32_t dst = rows0 + slot * ring.row_bytes;
-    const T* py = static_cast<const T*>(a.dy) + r * a.lddy;
-    const T* px = static_cast<const T*>(a.x) + r * a.ldx;
-    const T* pr = static_cast<const T*>(a.dres) + r * a.lddres;
+    const T* py = g_dy + r * a.lddy;
+    const T* px = g_x + r * a.ldx;
+    const T* pr = g_res + r * a.lddres;
     mbar_arrive_expect_tx(&bars[slot], row_span<T, VEC>(py, d) +
                                            (CK ? x_bytes : row_span<T, VEC>(px, d)) +
                                            (res ? row_span<T, VEC>(pr, d) : 0));
     bulk_row<T, VEC>(dst, py, d, &bars[slot]);
     if (CK) {
-      bulk_load(dst + t_bytes, a.ck.q + r * a.ck.ldq, q_bytes, &bars[slot]);
-      bulk_load(dst + t_bytes + q_bytes, a.ck.ex + r * a.ck.lde, e_bytes, &bars[slot]);
+      bulk_load(dst + t_bytes, a.ck.q + r * a.ck.ldq + col0, q_bytes, &bars[slot]);
+      bulk_load(dst + t_bytes + q_bytes, a.ck.ex + r * a.ck.lde + col0 / kCkptBlock, e_bytes,
+                &bars[slot]);
     } else {
       bulk_row<T, VEC>(dst + t_bytes, px, d, &bars[slot]);
     }
@@ -424,9 +457,17 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_kernel(const NormBwdArg
     for (int s = 0; s < ring.slots; ++s) fetch(s);
   }
   for (int k = t; k < 2 * 2 * 16; k += tpr) red[g][k] = 0.f;
+  if (t == 0 && g == 0 && halved) {
+    mbar_init(&sums_bar[0], 1);
+    mbar_init(&sums_bar[1], 1);
+    fence_mbar_init();
+  }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (a.weight != nullptr)
-    stage_param<VEC>(sw, a.weight, a.wtype, d, g * tpr + t, tpr * blockDim.y);
+    stage_param<VEC>(sw, static_cast<const uint8_t*>(a.weight) + col0 * param_width(a.wtype),
+                     a.wtype, d, g * tpr + t, tpr * blockDim.y);
+  __syncwarp();
+  if (halved) cluster_sync();  // the peer's barriers are there
   __syncthreads();
 
   f32x2 dw[CH][4], db[FULL ? CH : 1][4];
@@ -437,8 +478,9 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_kernel(const NormBwdArg
       dw[c][j] = 0ull;
       if (FULL) db[FULL ? c : 0][j] = 0ull;
     }
-  const float inv_d = 1.f / static_cast<float>(d);
-  T* dx = static_cast<T*>(a.dx) + row0 * a.lddx;
+  const float inv_d = 1.f / static_cast<float>(a.d);
+  T* dx = static_cast<T*>(a.dx) + row0 * a.lddx + col0;
+  uint32_t swaps = 0;  // rows whose sums the two CTAs have told each other
   int phase = 0, slot = 0;
   uint32_t parity = 0;
   bool ok = true;
@@ -464,12 +506,9 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_kernel(const NormBwdArg
       }
       const long long row = row0 + step * i;
       const uint32_t src = rows0 + slot * ring.row_bytes;
-      const uint32_t src_y = src + row_shift<T, VEC>(static_cast<const T*>(a.dy) + row * a.lddy);
-      const uint32_t src_x =
-          src + t_bytes +
-          (CK ? 0 : row_shift<T, VEC>(static_cast<const T*>(a.x) + row * a.ldx));
-      const uint32_t src_r = src + t_bytes + x_bytes +
-                             row_shift<T, VEC>(static_cast<const T*>(a.dres) + row * a.lddres);
+      const uint32_t src_y = src + row_shift<T, VEC>(g_dy + row * a.lddy);
+      const uint32_t src_x = src + t_bytes + (CK ? 0 : row_shift<T, VEC>(g_x + row * a.ldx));
+      const uint32_t src_r = src + t_bytes + x_bytes + row_shift<T, VEC>(g_res + row * a.lddres);
       const f32x2 scale = pair(rstd, rstd), shift = pair(-mean, -mean);
       f32x2 u[CH][4], h[CH][4];
       Raw8<T> rr[CH];
@@ -501,6 +540,22 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_kernel(const NormBwdArg
       if (FULL) s[FULL ? 1 : 0] = warp_sum(sum_of(su));
       join_warps(s, t, warps, g + 1, red[g], phase);
       if (t == 0 && ok) fetch(slot);
+      __syncwarp();
+      if (halved) {
+        // Tell the peer, and wait for its part (two places in turn: it cannot
+        // be two rows ahead). Both add in the same order.
+        const uint32_t b = swaps & 1u;
+        if (t == 0) {
+          mbar_arrive_expect_tx(&sums_bar[b], 8);
+          send_sums(smem_u32(&peer_sums[b][0]), smem_u32(&sums_bar[b]), rank ^ 1u, s[0],
+                    FULL ? s[FULL ? 1 : 0] : 0.f);
+        }
+        ok = ok && row_wait(&sums_bar[b], (swaps >> 1) & 1u);
+        ++swaps;
+#pragma unroll
+        for (int k = 0; k < (FULL ? 2 : 1); ++k)
+          s[k] = rank == 0 ? s[k] + peer_sums[b][k] : peer_sums[b][k] + s[k];
+      }
       const float c1 = layer ? s[FULL ? 1 : 0] * inv_d : 0.f;
       const float c2 = ok ? s[0] * inv_d : __uint_as_float(0x7fc00000u);
       const f32x2 n1 = pair(-c1, -c1), n2 = pair(-c2, -c2);
@@ -531,13 +586,15 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_kernel(const NormBwdArg
     live = live1;
   }
   land(bars, ring.slots, parity, pending);
+  __syncwarp();
+  if (halved) cluster_sync();  // nothing more arrives from the peer
   const bool want_db = FULL && a.dbias != nullptr;
   if (a.dweight == nullptr && !want_db) return;
   // The CTA's rows in flight, added in their order; the rings have been read.
   float* const cw = reinterpret_cast<float*>(ring0);
   float* const cb = cw + d;
-  float* pw = a.partials + static_cast<long long>(blockIdx.x) * d;
-  float* pb = pw + static_cast<long long>(gridDim.x) * d;
+  float* pw = a.partials + static_cast<long long>(blk) * a.d + col0;
+  float* pb = pw + static_cast<long long>(blks) * a.d;
   if (blockDim.y == 1) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
@@ -761,6 +818,8 @@ Ring make_ring(uint32_t row_bytes, int rows, size_t fixed) {
   Ring r;
   r.slots = static_cast<int>(slots);
   r.row_bytes = row_bytes;
+  r.split = 1;
+  r.part = 0;
   return r;
 }
 
@@ -853,38 +912,54 @@ cudaError_t finish(const NormBwdArgs& a, int rows, cudaStream_t st) {
 }
 
 template <typename T, bool VEC, int CH, bool CK, bool FULL>
-cudaError_t bwd_ring(const NormBwdArgs& a, const RowShape& s, int sms, cudaStream_t st) {
+cudaError_t bwd_ring(const NormBwdArgs& a, const RowShape& s, int part, int sms, cudaStream_t st) {
   constexpr auto kernel = norm_bwd_kernel<T, VEC, CH, CK, FULL>;
-  const size_t fixed = kRingBars + (a.weight != nullptr ? param_bytes(a.d) : 0);
-  const uint32_t t_bytes = row_slot<T, VEC>(a.d);
-  const Ring ring =
-      make_ring(t_bytes * (a.dres != nullptr ? 2 : 1) +
-                    (CK ? static_cast<uint32_t>(a.ck.ldq + a.ck.lde) : t_bytes),
-                s.rows, fixed);
+  const int d = part != 0 ? part : a.d;  // columns of a CTA
+  const size_t fixed = kRingBars + (a.weight != nullptr ? param_bytes(d) : 0);
+  const uint32_t t_bytes = row_slot<T, VEC>(d);
+  const uint32_t ck_bytes = static_cast<uint32_t>(
+      part != 0 ? part + part / 32 : a.ck.ldq + a.ck.lde);
+  Ring ring = make_ring(t_bytes * (a.dres != nullptr ? 2 : 1) + (CK ? ck_bytes : t_bytes), s.rows,
+                        fixed);
+  ring.split = part != 0 ? 2 : 1;
+  ring.part = part;
   size_t smem = static_cast<size_t>(ring.slots) * ring.row_bytes * s.rows;
-  if (s.rows > 1) smem = std::max(smem, static_cast<size_t>(a.d) * 8);
+  if (s.rows > 1) smem = std::max(smem, static_cast<size_t>(d) * 8);
   smem += fixed;
   int per_sm = 0;
   cudaError_t e = ctas_per_sm<kernel>(s.tpr * s.rows, smem, &per_sm);
   if (e != cudaSuccess) return e;
   const long long units = (a.n + s.rows - 1) / s.rows;
-  const int grid = static_cast<int>(std::min<long long>(
-      std::min<long long>(units, kNormMaxPartials), std::max(1, per_sm) * sms));
+  const int groups = static_cast<int>(
+      std::min<long long>(std::min<long long>(units, kNormMaxPartials),
+                          std::max(1, per_sm) * (sms / ring.split)));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(groups * ring.split);
+  cfg.blockDim = dim3(s.tpr, s.rows);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ring.split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = ring.split == 2 ? 1 : 0;
   {
     LaunchTimer timer("norm_bwd_kernel", st);
-    kernel<<<grid, dim3(s.tpr, s.rows), smem, st>>>(a, ring);
+    e = cudaLaunchKernelEx(&cfg, kernel, a, ring);
   }
-  e = cudaGetLastError();
-  return e != cudaSuccess ? e : finish(a, grid, st);
+  return e != cudaSuccess ? e : finish(a, groups, st);
 }
 
 template <typename T, bool VEC, bool CK, bool FULL>
 cudaError_t bwd_kind(const NormBwdArgs& a, int sms, cudaStream_t st) {
-  const RowShape s = ring_shape(a.d, 2, kRowThreads);
-  switch (s.ch) {
-    case 1: return bwd_ring<T, VEC, 1, CK, FULL>(a, s, sms, st);
-    default: return bwd_ring<T, VEC, 2, CK, FULL>(a, s, sms, st);
-  }
+  // Beyond 8192 columns two CTAs share a row, at a multiple of 512 columns (16
+  // exponents: 16 bytes).
+  const int part = a.d > kRingThreads * 16 ? ((a.d + 1) / 2 + 511) / 512 * 512 : 0;
+  const RowShape s = ring_shape(part != 0 ? part : a.d, 2, kRowThreads);
+  if (s.ch == 1) return bwd_ring<T, VEC, 1, CK, FULL>(a, s, part, sms, st);
+  return bwd_ring<T, VEC, 2, CK, FULL>(a, s, part, sms, st);
 }
 
 template <typename T, bool VEC, bool CK>

@@ -31,7 +31,7 @@ DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
 # every path: one warp (8 and 16 values a thread), several rows a CTA, one row
 # a CTA, rows longer than registers; odd sizes take the one-by-one path.
 WIDTHS = [1, 7, 31, 32, 33, 64, 100, 256, 257, 264, 512, 520, 1000, 1001, 1536, 2047, 2880, 4096,
-          8192, 8193, 8200, 16384]
+          8192, 8193, 8200, 12001, 16384, 16385, 16392, 20000]
 
 
 @pytest.fixture(scope="module")
