@@ -21,8 +21,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_NAME = "libgrpo_gb300.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 
-SOURCES = ["api.cu", "fwd_kernels.cu", "bwd_gemm_launch.cu", "norm_api.cu", "norm_kernels.cu",
-           "ckpt_kernels.cu", "ckpt_wgrad.cu"]
+SOURCES = ["api.cu", "fwd_kernels.cu", "bwd_gemm_launch.cu", "norm_api.cu", "norm_fwd.cu",
+           "norm_bwd.cu", "ckpt_kernels.cu", "ckpt_wgrad.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
               "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

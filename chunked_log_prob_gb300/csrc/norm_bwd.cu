@@ -1,371 +1,8 @@
-// Layer norm and RMS norm, forward and backward, with the residual add, the
-// row mask and the 8-bit checkpoint of the normed stream fused in.
-//
-//   z = round(x + r);  mu = mean z (layer), 0 (rms);
-//   rstd = (mean (z - mu)^2 + eps)^-1/2;  y = (z - mu) rstd w + b
-//   h = (z - mu) rstd, u = dy w:
-//   dx = rstd (u - mean u - h mean(u h)) + dres   (rms: without mean u)
-//   dw = sum_t dy h, db = sum_t dy
-//
-// Memory bound: about 10 operations per value against 4 to 9 bytes. A row is
-// read once and held in registers (up to 8192 columns); statistics are fp32.
-#include <algorithm>
-#include <atomic>
-
-#include "launch.h"
-#include "norm.h"
-#include "row_ops.cuh"
+// Layer norm and RMS norm, backward (formulas in norm_fwd.cu).
+#include "norm_ring.cuh"
 
 namespace grpo {
-
 namespace {
-
-constexpr int kRowThreads = 256;  // threads of a CTA whose rows are short
-
-__device__ __forceinline__ bool row_live(const uint8_t* mask, long long row, long long n) {
-  return row < n && (mask == nullptr || mask[row] != 0);
-}
-
-// Each row of the CTA (threadIdx.y) has a ring of `slots` rows in shared memory,
-// filled by bulk copies; a slot is filled again as soon as the row's sum has
-// been taken, when every thread holds its values. Bulk copies start and end on
-// 16 bytes: of a row that does not, the 16 bytes around its ends come too, and
-// its values are read one by one (VEC false).
-// The bytes in flight come from the ring, so what is left is issue slots: a
-// thread holds up to 32 values, so that a row's fixed work (barriers, sums,
-// addresses) is shared by few warps, and works on pairs of them.
-struct Ring {
-  int slots;           // rows in flight for each row of the CTA
-  uint32_t row_bytes;  // of a slot
-  int split;           // backward: CTAs of a row (a cluster of 2 beyond 8192 columns)
-  int part;            // and columns of the first
-};
-
-// Shared memory: barriers, then the parameters as fp32, then the rings.
-constexpr int kMaxSlots = 8;
-constexpr int kMaxRows = 8;  // rows of a CTA
-constexpr uint32_t kRingBars = kMaxRows * kMaxSlots * sizeof(uint64_t);
-
-// Threads of a CTA at most.
-constexpr int kRingThreads = 512;
-
-// After a timeout: lets the copies still in flight land (within the same limit).
-__device__ __forceinline__ void land(uint64_t* bars, int slots, uint32_t parity, uint32_t pending) {
-  for (int s = 0; s < slots; ++s)
-    if ((pending >> s) & 1u) row_wait(&bars[s], (parity >> s) & 1u);
-}
-
-// Two sums into the peer CTA's shared memory, counted on its barrier there.
-// `at`, `bar`: addresses in this CTA of what is meant in the peer's.
-__device__ __forceinline__ void send_sums(uint32_t at, uint32_t bar, uint32_t peer, float a,
-                                          float b) {
-  asm volatile(
-      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%2, %3}, [%1];" ::"r"(
-          mapa_shared(at, peer)),
-      "r"(mapa_shared(bar, peer)), "f"(a), "f"(b)
-      : "memory");
-}
-
-__device__ __forceinline__ int param_width(int type) { return type == GRPO_DTYPE_FP32 ? 4 : 2; }
-
-// Rows of the group that begins at `row`.
-__device__ __forceinline__ int row_count(long long row, long long n, long long step) {
-  return row < n ? static_cast<int>((n - 1 - row) / step) + 1 : 0;
-}
-
-template <typename T, bool VEC, int CH, int KIND>
-__global__ void __launch_bounds__(kRingThreads) norm_fwd_kernel(const NormFwdArgs a, const Ring ring) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(16) float red[kMaxRows][2 * 2 * 16];
-  __shared__ float warp_n[2][16];
-  __shared__ BlockTurn turns[VEC ? 1 : kRingThreads / 32];
-  const int t = threadIdx.x, tpr = blockDim.x, g = threadIdx.y, d = a.d;
-  const int warps = tpr >> 5;
-  BlockTurn* const turn = turns + (VEC ? 0 : g * warps + (t >> 5));
-  uint64_t* const bars = reinterpret_cast<uint64_t*>(smem) + g * kMaxSlots;
-  float* const sw = reinterpret_cast<float*>(smem + kRingBars);
-  float* const sb = sw + (a.weight != nullptr ? param_bytes(d) / 4 : 0);
-  const uint32_t sw32 = smem_u32(sw), sb32 = smem_u32(sb);
-  const uint32_t rows0 = smem_u32(sb + (a.bias != nullptr ? param_bytes(d) / 4 : 0)) +
-                         g * ring.slots * ring.row_bytes;
-  const uint32_t x_bytes = row_slot<T, VEC>(d);
-  const bool res = a.res != nullptr;
-  const long long step = static_cast<long long>(gridDim.x) * blockDim.y;
-  const long long row0 = static_cast<long long>(blockIdx.x) * blockDim.y + g;
-  const int count = row_count(row0, a.n, step);
-  const uint8_t* const mask = a.mask;
-  // Thread 0: slots whose copies have not been waited for, and the next row to fetch.
-  uint32_t pending = 0;
-  int fetched = 0;
-  const auto fetch = [&](int slot) {
-    if (fetched >= count) return;
-    const long long r = row0 + step * fetched++;
-    if (mask != nullptr && mask[r] == 0) return;
-    pending |= 1u << slot;
-    const uint32_t dst = rows0 + slot * ring.row_bytes;
-    const T* px = static_cast<const T*>(a.x) + r * a.ldx;
-    const T* pr = static_cast<const T*>(a.res) + r * a.ldr;
-    mbar_arrive_expect_tx(&bars[slot],
-                          row_span<T, VEC>(px, d) + (res ? row_span<T, VEC>(pr, d) : 0));
-    bulk_row<T, VEC>(dst, px, d, &bars[slot]);
-    if (res) bulk_row<T, VEC>(dst + x_bytes, pr, d, &bars[slot]);
-  };
-  if (t == 0) {
-    for (int s = 0; s < ring.slots; ++s) mbar_init(&bars[s], 1);
-    fence_mbar_init();
-    for (int s = 0; s < ring.slots; ++s) fetch(s);
-  }
-  for (int k = t; k < 2 * 2 * 16; k += tpr) red[g][k] = 0.f;
-  if (a.weight != nullptr)
-    stage_param<VEC>(sw, a.weight, a.wtype, d, g * tpr + t, tpr * blockDim.y);
-  if (a.bias != nullptr) stage_param<VEC>(sb, a.bias, a.wtype, d, g * tpr + t, tpr * blockDim.y);
-  // Columns that each warp of a row holds, and their inverse.
-  if (KIND == GRPO_NORM_LAYER) {
-    float n = 0.f;
-#pragma unroll
-    for (int k = 0; k < 8 * CH; ++k) n += chunk_col<VEC>(k >> 3, k & 7, t, tpr) < d ? 1.f : 0.f;
-    n = warp_sum(n);
-    if ((t & 31) == 0) {
-      warp_n[0][t >> 5] = n;
-      warp_n[1][t >> 5] = n > 0.f ? 1.f / n : 0.f;
-    }
-  }
-  __syncthreads();
-
-  const float inv_d = 1.f / static_cast<float>(d);
-  const float inv_warp_n = KIND == GRPO_NORM_LAYER ? warp_n[1][t >> 5] : 0.f;
-  T* y = static_cast<T*>(a.y) + row0 * a.ldy;
-  T* z = res && a.z != nullptr ? static_cast<T*>(a.z) + row0 * a.ldz : nullptr;
-  uint8_t* q = a.ck.q != nullptr ? a.ck.q + row0 * a.ck.ldq : nullptr;
-  uint8_t* ex = a.ck.ex + row0 * a.ck.lde;
-  int phase = 0, slot = 0;
-  uint32_t parity = 0;  // a bit per slot
-  bool ok = true;
-  bool live = count > 0 && (mask == nullptr || mask[row0] != 0);
-  for (int i = 0; i < count; ++i) {
-    const bool live1 =
-        i + 1 < count && (mask == nullptr || mask[row0 + step * (i + 1)] != 0);
-    f32x2 v[CH][4];
-    float mean = 0.f, rstd = 0.f;
-    if (live) {
-      ok = ok && row_wait(&bars[slot], (parity >> slot) & 1u);
-      if (ok) {
-        parity ^= 1u << slot;
-        pending &= ~(1u << slot);
-      }
-      const long long row = row0 + step * i;
-      const uint32_t src =
-          rows0 + slot * ring.row_bytes + row_shift<T, VEC>(static_cast<const T*>(a.x) + row * a.ldx);
-      const uint32_t src_r = rows0 + slot * ring.row_bytes + x_bytes +
-                             row_shift<T, VEC>(static_cast<const T*>(a.res) + row * a.ldr);
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        lds_values<T, VEC>(src, c, t, tpr, d, v[c]);
-        if (res) {
-          f32x2 r[4];
-          lds_values<T, VEC>(src_r, c, t, tpr, d, r);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[c][j] = add2(v[c][j], r[j]);
-          // The stream holds z rounded; the norm is taken of what it holds.
-          const Raw8<T> o = narrow2<T>(v[c]);
-          if (z != nullptr) store_chunk<T, VEC>(z, o, c, t, tpr, d);
-          widen2(o, v[c]);
-        }
-      }
-      if (KIND == GRPO_NORM_RMS) {
-        f32x2 s[2] = {0ull, 0ull};
-#pragma unroll
-        for (int c = 0; c < CH; ++c)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) s[j & 1] = fma2(v[c][j], v[c][j], s[j & 1]);
-        float m[1] = {warp_sum(sum_of(add2(s[0], s[1])))};
-        join_warps(m, t, warps, g + 1, red[g], phase);
-        rstd = rsqrtf(m[0] * inv_d + a.eps);
-      } else {
-        // Each warp centres its values on their own mean; the warps' sums are
-        // then joined as if all had been centred on the row's.
-        f32x2 s[2] = {0ull, 0ull};
-#pragma unroll
-        for (int c = 0; c < CH; ++c)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) s[j & 1] = add2(v[c][j], s[j & 1]);
-        const float sum = warp_sum(sum_of(add2(s[0], s[1])));
-        const float mw = sum * inv_warp_n;
-        const f32x2 nmw = pair(-mw, -mw);
-        s[0] = s[1] = 0ull;
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          if (VEC ? (c * tpr + t) * 8 >= d : 8 * c * tpr >= d) continue;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            f32x2 e = add2(v[c][j], nmw);
-            if (!VEC) {
-              float lo, hi;
-              split(e, lo, hi);
-              e = pair(chunk_col<false>(c, 2 * j, t, tpr) < d ? lo : 0.f,
-                       chunk_col<false>(c, 2 * j + 1, t, tpr) < d ? hi : 0.f);
-            }
-            s[j & 1] = fma2(e, e, s[j & 1]);
-          }
-        }
-        const float m2 = warp_sum(sum_of(add2(s[0], s[1])));
-        float total = sum, centred = m2;
-        if (warps > 1) {
-          float* sh = red[g] + phase * 2 * 16;
-          phase ^= 1;
-          if ((t & 31) == 0) {
-            sh[t >> 5] = sum;
-            sh[16 + (t >> 5)] = m2;
-          }
-          named_barrier(g + 1, tpr);
-          total = 0.f;
-          for (int k = 0; k < warps; ++k) total += sh[k];
-          const float mu = total * inv_d;
-          centred = 0.f;
-          for (int k = 0; k < warps; ++k) {
-            const float e = sh[k] * warp_n[1][k] - mu;
-            centred += sh[16 + k] + warp_n[0][k] * e * e;
-          }
-        } else {
-          __syncwarp();
-        }
-        mean = total * inv_d;
-        rstd = rsqrtf(centred * inv_d + a.eps);
-      }
-      if (!ok) rstd = __uint_as_float(0x7fc00000u);
-    } else {
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[c][j] = 0ull;
-        if (z != nullptr) store_chunk<T, VEC>(z, narrow2<T>(v[c]), c, t, tpr, d);
-      }
-    }
-    // Every thread has its values (the sum's barrier, or the warp's).
-    if (t == 0 && ok) fetch(slot);
-    if (++slot == ring.slots) slot = 0;
-    const f32x2 scale = pair(rstd, rstd), shift = pair(-mean, -mean);
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      if (q != nullptr) {
-        ckpt_store_chunk<T, VEC>(v[c], q, ex, c, t, tpr, d, turn);
-      }
-      if (VEC ? (c * tpr + t) * 8 >= d : 8 * c * tpr >= d) continue;
-      if (live) {
-        f32x2 w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          v[c][j] = mul2(KIND == GRPO_NORM_LAYER ? add2(v[c][j], shift) : v[c][j], scale);
-        if (a.weight != nullptr) {
-          read_param<VEC>(sw32, c, t, tpr, d, w);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[c][j] = mul2(v[c][j], w[j]);
-        }
-        if (a.bias != nullptr) {
-          read_param<VEC>(sb32, c, t, tpr, d, w);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[c][j] = add2(v[c][j], w[j]);
-        }
-      }
-      store_chunk<T, VEC>(y, narrow2<T>(v[c]), c, t, tpr, d);
-    }
-    if (t == 0) {
-      const long long row = row0 + step * i;
-      if (a.mean != nullptr) a.mean[row] = mean;
-      if (a.rstd != nullptr) a.rstd[row] = rstd;
-    }
-    y += step * a.ldy;
-    if (z != nullptr) z += step * a.ldz;
-    if (q != nullptr) {
-      q += step * a.ck.ldq;
-      ex += step * a.ck.lde;
-    }
-    live = live1;
-  }
-  land(bars, ring.slots, parity, pending);
-}
-
-// Rows beyond kNormRegisterRow columns: the CTA walks over the row three times
-// (sum, centred squares, output); the second and third walk find it in L2. A
-// thread rereads only what it stored itself, so outputs may lie on the inputs.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(512) norm_fwd_long_kernel(const NormFwdArgs a) {
-  __shared__ float2 red[2 * 32];
-  __shared__ BlockTurn turns[VEC ? 1 : 16];
-  const int t = threadIdx.x, tpr = blockDim.x, d = a.d;
-  BlockTurn* const turn = turns + (VEC ? 0 : t >> 5);
-  const int chunks = (d + 8 * tpr - 1) / (8 * tpr);
-  int phase = 0;
-  for (long long row = blockIdx.x; row < a.n; row += gridDim.x) {
-    const bool live = row_live(a.mask, row, a.n);
-    const T* x = static_cast<const T*>(a.x) + row * a.ldx;
-    const T* res = a.res != nullptr ? static_cast<const T*>(a.res) + row * a.ldr : nullptr;
-    T* z = a.z != nullptr && res != nullptr ? static_cast<T*>(a.z) + row * a.ldz : nullptr;
-    T* y = static_cast<T*>(a.y) + row * a.ldy;
-    const auto stream = [&](int c, float(&v)[8]) {
-      if (!live) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 0.f;
-        return;
-      }
-      widen(load_chunk<T, VEC>(x, c, t, tpr, d), v);
-      if (res != nullptr) {
-        float r[8];
-        widen(load_chunk<T, VEC>(res, c, t, tpr, d), r);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] += r[j];
-        widen(narrow<T>(v), v);
-      }
-    };
-    float mean = 0.f, rstd = 0.f;
-    if (live) {
-      float v[8];
-      if (a.kind != GRPO_NORM_RMS) {
-        float s = 0.f;
-        for (int c = 0; c < chunks; ++c) {
-          stream(c, v);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) s += v[j];
-        }
-        mean = row_sum2(make_float2(s, 0.f), t, tpr, 1, red, phase).x / static_cast<float>(d);
-      }
-      float m2 = 0.f;
-      for (int c = 0; c < chunks; ++c) {
-        stream(c, v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float e = v[j] - mean;
-          if (chunk_col<VEC>(c, j, t, tpr) < d) m2 += e * e;
-        }
-      }
-      m2 = row_sum2(make_float2(m2, 0.f), t, tpr, 1, red, phase).x;
-      rstd = 1.f / sqrtf(m2 / static_cast<float>(d) + a.eps);
-    }
-    for (int c = 0; c < chunks; ++c) {
-      float v[8];
-      stream(c, v);
-      if (z != nullptr) store_chunk<T, VEC>(z, narrow<T>(v), c, t, tpr, d);
-      if (a.ck.q != nullptr)
-        ckpt_store_chunk<T, VEC>({pair(v[0], v[1]), pair(v[2], v[3]), pair(v[4], v[5]), pair(v[6], v[7])},
-                                 a.ck.q + row * a.ck.ldq, a.ck.ex + row * a.ck.lde, c, t, tpr, d, turn);
-      if (live) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int col = chunk_col<VEC>(c, j, t, tpr);
-          if (col >= d) continue;
-          const float w = a.weight != nullptr ? load_param(a.weight, a.wtype, col) : 1.f;
-          const float b = a.bias != nullptr ? load_param(a.bias, a.wtype, col) : 0.f;
-          v[j] = (v[j] - mean) * rstd * w + b;
-        }
-      }
-      store_chunk<T, VEC>(y, narrow<T>(v), c, t, tpr, d);
-    }
-    if (t == 0) {
-      if (a.mean != nullptr) a.mean[row] = mean;
-      if (a.rstd != nullptr) a.rstd[row] = rstd;
-    }
-  }
-}
 
 // One chunk of the stream for the backward pass, as loaded.
 template <typename T, bool VEC, bool CK>
@@ -391,7 +28,7 @@ struct RawStream<T, VEC, true> {
 // slot holds dy, then x (or its bytes and exponents), then dres. FULL: layer
 // norm, or a bias gradient; else neither. 16 values a thread: with 32 the sums
 // alone take 64 to 128 registers (131072 x 2880 layer norm: 789 us against 545).
-template <typename T, bool VEC, int CH, bool CK, bool FULL>
+template <typename T, bool VEC, int CH, bool CK, bool FULL, int SPLIT>
 __global__ void __launch_bounds__(kRingThreads) norm_bwd_kernel(const NormBwdArgs a, const Ring ring) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(16) float red[kMaxRows][2 * 2 * 16];
@@ -399,12 +36,12 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_kernel(const NormBwdArg
   __shared__ __align__(8) float peer_sums[2][2];
   const int t = threadIdx.x, tpr = blockDim.x, g = threadIdx.y;
   // This CTA's columns [col0, col0 + d) of the row.
-  const bool halved = ring.split == 2;
+  constexpr bool halved = SPLIT == 2;
   const uint32_t rank = halved ? cluster_ctarank() : 0u;
   const int col0 = rank != 0 ? ring.part : 0;
   const int d = halved ? (rank != 0 ? a.d - ring.part : ring.part) : a.d;
-  const int blk = static_cast<int>(blockIdx.x) / ring.split;
-  const int blks = static_cast<int>(gridDim.x) / ring.split;
+  const int blk = static_cast<int>(blockIdx.x) / SPLIT;
+  const int blks = static_cast<int>(gridDim.x) / SPLIT;
   const int warps = tpr >> 5;
   uint64_t* const bars = reinterpret_cast<uint64_t*>(smem) + g * kMaxSlots;
   float* const sw = reinterpret_cast<float*>(smem + kRingBars);
@@ -784,116 +421,6 @@ __global__ void __launch_bounds__(512) norm_bwd_finish_kernel(const float* __res
   if (out != nullptr) out[col] = add != nullptr ? add[col] + s : s;
 }
 
-// Threads of a row and rows of a CTA for D columns held in registers.
-struct RowShape {
-  int tpr, rows, ch;
-};
-// The most values a thread, up to 8 `most`, that leave no more than a
-// tenth of the threads idle (else the fewest idle ones); CTAs of about
-// `threads` threads.
-RowShape ring_shape(int d, int most, int threads) {
-  RowShape best = {0, 0, 0};
-  int best_room = 0;
-  for (int ch = most; ch >= 1; --ch) {
-    const int tpr = (d + 256 * ch - 1) / (256 * ch) * 32;
-    const int room = tpr * 8 * ch;
-    if (tpr > kRingThreads || (best.ch != 0 && room >= best_room)) continue;
-    best = {tpr, std::min(kMaxRows, std::max(1, threads / tpr)), ch};
-    best_room = room;
-    if (10 * room <= 11 * d) break;
-  }
-  return best;
-}
-
-constexpr size_t kSmemMax = 227 * 1024 - 22528;  // less the kernels' static arrays
-constexpr size_t kSmemTarget = 72 * 1024;       // of a CTA: three to an SM
-
-// Rows in flight of a CTA: as many slots as fit kSmemTarget beside the
-// parameters, at most kMaxSlots and at least 2 (1 for rows that fit but once).
-Ring make_ring(uint32_t row_bytes, int rows, size_t fixed) {
-  const size_t slot = static_cast<size_t>(row_bytes) * rows;
-  const size_t room = kSmemTarget > fixed ? kSmemTarget - fixed : 0;
-  size_t slots = std::min<size_t>(kMaxSlots, std::max<size_t>(2, room / slot));
-  if (fixed + slots * slot > kSmemMax) slots = 1;
-  Ring r;
-  r.slots = static_cast<int>(slots);
-  r.row_bytes = row_bytes;
-  r.split = 1;
-  r.part = 0;
-  return r;
-}
-
-// Opts a kernel in to large shared memory, once.
-template <auto Kernel>
-bool opted_in() {
-  static const bool ok = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                              static_cast<int>(kSmemMax)) == cudaSuccess;
-  return ok;
-}
-
-// CTAs of a kernel that fit an SM; the last answer is kept for calls of one shape.
-template <auto Kernel>
-cudaError_t ctas_per_sm(int threads, size_t smem, int* n) {
-  static std::atomic<uint64_t> last{0};
-  const uint64_t key = (static_cast<uint64_t>(smem) << 24) | (static_cast<uint64_t>(threads) << 8);
-  const uint64_t seen = last.load(std::memory_order_relaxed);
-  if (seen != 0 && (seen & ~uint64_t{0xff}) == key) {
-    *n = static_cast<int>(seen & 0xff);
-    return cudaSuccess;
-  }
-  if (!opted_in<Kernel>()) return cudaErrorInvalidValue;
-  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, Kernel, threads, smem);
-  if (e == cudaSuccess) last.store(key | static_cast<uint64_t>(*n), std::memory_order_relaxed);
-  return e;
-}
-
-template <typename T, bool VEC>
-cudaError_t fwd_long(const NormFwdArgs& a, int sms, cudaStream_t st) {
-  const int grid = static_cast<int>(std::min<long long>(a.n, 3LL * sms));
-  LaunchTimer timer("norm_fwd_long_kernel", st);
-  norm_fwd_long_kernel<T, VEC><<<grid, 512, 0, st>>>(a);
-  return cudaGetLastError();
-}
-
-template <typename T, bool VEC, int CH, int KIND>
-cudaError_t fwd_ring(const NormFwdArgs& a, const RowShape& s, int sms, cudaStream_t st) {
-  constexpr auto kernel = norm_fwd_kernel<T, VEC, CH, KIND>;
-  const size_t fixed =
-      kRingBars + param_bytes(a.d) * ((a.weight != nullptr) + (a.bias != nullptr));
-  const Ring ring = make_ring(row_slot<T, VEC>(a.d) * (a.res != nullptr ? 2 : 1), s.rows, fixed);
-  const size_t smem = fixed + static_cast<size_t>(ring.slots) * ring.row_bytes * s.rows;
-  if (smem > kSmemMax) return fwd_long<T, VEC>(a, sms, st);
-  int per_sm = 0;
-  cudaError_t e = ctas_per_sm<kernel>(s.tpr * s.rows, smem, &per_sm);
-  if (e != cudaSuccess) return e;
-  const long long units = (a.n + s.rows - 1) / s.rows;
-  const int grid = static_cast<int>(std::min<long long>(units, std::max(1, per_sm) * sms));
-  LaunchTimer timer("norm_fwd_kernel", st);
-  kernel<<<grid, dim3(s.tpr, s.rows), smem, st>>>(a, ring);
-  return cudaGetLastError();
-}
-
-template <typename T, bool VEC, int KIND>
-cudaError_t fwd_kind(const NormFwdArgs& a, int sms, cudaStream_t st) {
-  // One by one, 16 values a thread: 32 take 228 registers.
-  const RowShape s = ring_shape(a.d, VEC ? 4 : 2, kRowThreads);
-  switch (s.ch) {
-    case 1: return fwd_ring<T, VEC, 1, KIND>(a, s, sms, st);
-    case 2: return fwd_ring<T, VEC, 2, KIND>(a, s, sms, st);
-    case 3:
-      if constexpr (VEC) return fwd_ring<T, VEC, 3, KIND>(a, s, sms, st);
-    case 4:
-      if constexpr (VEC) return fwd_ring<T, VEC, 4, KIND>(a, s, sms, st);
-    default: return fwd_long<T, VEC>(a, sms, st);
-  }
-}
-
-template <typename T, bool VEC>
-cudaError_t fwd_any(const NormFwdArgs& a, int sms, cudaStream_t st) {
-  return a.kind == GRPO_NORM_RMS ? fwd_kind<T, VEC, GRPO_NORM_RMS>(a, sms, st)
-                                 : fwd_kind<T, VEC, GRPO_NORM_LAYER>(a, sms, st);
-}
-
 cudaError_t finish(const NormBwdArgs& a, int rows, cudaStream_t st) {
   if (a.dweight == nullptr && a.dbias == nullptr) return cudaSuccess;
   const dim3 grid((a.d + 31) / 32, a.dbias != nullptr ? 2 : 1);
@@ -911,9 +438,9 @@ cudaError_t finish(const NormBwdArgs& a, int rows, cudaStream_t st) {
                             a.d, a.dweight, a.dbias, a.add_dweight, a.add_dbias);
 }
 
-template <typename T, bool VEC, int CH, bool CK, bool FULL>
+template <typename T, bool VEC, int CH, bool CK, bool FULL, int SPLIT>
 cudaError_t bwd_ring(const NormBwdArgs& a, const RowShape& s, int part, int sms, cudaStream_t st) {
-  constexpr auto kernel = norm_bwd_kernel<T, VEC, CH, CK, FULL>;
+  constexpr auto kernel = norm_bwd_kernel<T, VEC, CH, CK, FULL, SPLIT>;
   const int d = part != 0 ? part : a.d;  // columns of a CTA
   const size_t fixed = kRingBars + (a.weight != nullptr ? param_bytes(d) : 0);
   const uint32_t t_bytes = row_slot<T, VEC>(d);
@@ -921,7 +448,6 @@ cudaError_t bwd_ring(const NormBwdArgs& a, const RowShape& s, int part, int sms,
       part != 0 ? part + part / 32 : a.ck.ldq + a.ck.lde);
   Ring ring = make_ring(t_bytes * (a.dres != nullptr ? 2 : 1) + (CK ? ck_bytes : t_bytes), s.rows,
                         fixed);
-  ring.split = part != 0 ? 2 : 1;
   ring.part = part;
   size_t smem = static_cast<size_t>(ring.slots) * ring.row_bytes * s.rows;
   if (s.rows > 1) smem = std::max(smem, static_cast<size_t>(d) * 8);
@@ -932,19 +458,19 @@ cudaError_t bwd_ring(const NormBwdArgs& a, const RowShape& s, int part, int sms,
   const long long units = (a.n + s.rows - 1) / s.rows;
   const int groups = static_cast<int>(
       std::min<long long>(std::min<long long>(units, kNormMaxPartials),
-                          std::max(1, per_sm) * (sms / ring.split)));
+                          std::max(1, per_sm) * (sms / SPLIT)));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(groups * ring.split);
+  cfg.gridDim = dim3(groups * SPLIT);
   cfg.blockDim = dim3(s.tpr, s.rows);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ring.split;
+  attr[0].val.clusterDim.x = SPLIT;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = ring.split == 2 ? 1 : 0;
+  cfg.numAttrs = SPLIT == 2 ? 1 : 0;
   {
     LaunchTimer timer("norm_bwd_kernel", st);
     e = cudaLaunchKernelEx(&cfg, kernel, a, ring);
@@ -958,8 +484,9 @@ cudaError_t bwd_kind(const NormBwdArgs& a, int sms, cudaStream_t st) {
   // exponents: 16 bytes).
   const int part = a.d > kRingThreads * 16 ? ((a.d + 1) / 2 + 511) / 512 * 512 : 0;
   const RowShape s = ring_shape(part != 0 ? part : a.d, 2, kRowThreads);
-  if (s.ch == 1) return bwd_ring<T, VEC, 1, CK, FULL>(a, s, part, sms, st);
-  return bwd_ring<T, VEC, 2, CK, FULL>(a, s, part, sms, st);
+  if (part != 0) return bwd_ring<T, VEC, 2, CK, FULL, 2>(a, s, part, sms, st);
+  if (s.ch == 1) return bwd_ring<T, VEC, 1, CK, FULL, 1>(a, s, part, sms, st);
+  return bwd_ring<T, VEC, 2, CK, FULL, 1>(a, s, part, sms, st);
 }
 
 template <typename T, bool VEC, bool CK>
@@ -1003,18 +530,6 @@ int norm_bwd_partials(long long n, int d) {
   }
   // A CTA takes one row at least.
   return static_cast<int>(std::min<long long>(kNormMaxPartials, std::max<long long>(1, n)));
-}
-
-cudaError_t launch_norm_fwd(const NormFwdArgs& a, int dtype, bool vec, int sms, cudaStream_t st) {
-  switch (dtype) {
-    case GRPO_DTYPE_BF16:
-      return vec ? fwd_any<__nv_bfloat16, true>(a, sms, st)
-                 : fwd_any<__nv_bfloat16, false>(a, sms, st);
-    case GRPO_DTYPE_FP16:
-      return vec ? fwd_any<__half, true>(a, sms, st) : fwd_any<__half, false>(a, sms, st);
-    default:
-      return vec ? fwd_any<float, true>(a, sms, st) : fwd_any<float, false>(a, sms, st);
-  }
 }
 
 cudaError_t launch_norm_bwd(const NormBwdArgs& a, int dtype, bool vec, int sms, cudaStream_t st) {
