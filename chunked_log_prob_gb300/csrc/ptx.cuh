@@ -251,6 +251,11 @@ __device__ __forceinline__ void cluster_sync() {
                ::: "memory");
 }
 
+// The same for warps whose threads may come one after the other.
+__device__ __forceinline__ void cluster_sync_threads() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
 // Arrive (with an expected byte count) on an mbarrier that may sit in the
 // peer CTA. CTA-scope release: the data it announces arrives through the TMA
 // unit's complete_tx, so no cluster-wide fence is needed on this hot path.
