@@ -274,101 +274,105 @@ __global__ void __launch_bounds__(kThreads, 1)
   // follows to the new count only where the instruction dominates it.
   if (warp < kFirstEpilogue) {
     give_registers<kControlRegs>();
+    // Whole warps walk through the work and wait; one lane issues.
     if (warp == 0) {
-      // ---------------------------------------------------- dY's tiles by TMA --
-      if (elect_one()) {
-        uint32_t n = 0;  // stages issued
-        while (ok && work.next(plan, pair, pairs, it)) {
-          int tm, tn;
-          tile_place(plan, it.tile, tm, tn);
-          const int o0 = tm * kTileM + static_cast<int>(rank) * (kTileM / 2);
-          for (int k = it.kb; k < it.ke; ++k, ++n) {
-            const uint32_t s = n % kDy;
-            if (!mbar_wait(&done_bar[s], ((n / kDy) & 1u) ^ 1u, abort_flag, args.status)) {
-              ok = false;
-              break;
-            }
+      // -------------------------------------------------- dY's tiles by TMA --
+      uint32_t n = 0;  // stages issued
+      while (ok && work.next(plan, pair, pairs, it)) {
+        int tm, tn;
+        tile_place(plan, it.tile, tm, tn);
+        const int o0 = tm * kTileM + static_cast<int>(rank) * (kTileM / 2);
+        for (int k = it.kb; k < it.ke; ++k, ++n) {
+          const uint32_t s = n % kDy;
+          if (!mbar_wait(&done_bar[s], ((n / kDy) & 1u) ^ 1u, abort_flag, args.status)) {
+            ok = false;
+            break;
+          }
+          if (elect_one()) {
             const uint32_t lead = mapa_shared(smem_u32(&full_bar[s]), 0);
             mbar_arrive_expect_tx_cluster(lead, kOperand);
             uint8_t* a = ring + s * kOperand;
             tma_load_2d_pair_nohint(a, &map_dy, lead, o0, k * kTok);
             tma_load_2d_pair_nohint(a + kBoxBytes, &map_dy, lead, o0 + 64, k * kTok);
           }
+          __syncwarp();
         }
-        // After a timeout: let the copies in flight land before the CTA exits (the
-        // peer passes the closing cluster barrier only after this). Their barriers
-        // also wait for converters that may have given up: the drain ends by its
-        // own limit then, long after any copy.
-        if (!ok && rank == 0)
-          for (uint32_t j = n >= kDy ? n - kDy : 0; j < n; ++j)
-            drain(&full_bar[j % kDy], (j / kDy) & 1u);
       }
+      // After a timeout: let the copies in flight land before the CTA exits (the
+      // peer passes the closing cluster barrier only after this). Their barriers
+      // also wait for converters that may have given up: the drain ends by its
+      // own limit then, long after any copy.
+      if (!ok && rank == 0)
+        for (uint32_t j = n >= kDy ? n - kDy : 0; j < n; ++j)
+          drain(&full_bar[j % kDy], (j / kDy) & 1u);
     } else if (warp == 2) {
-      // ---------------------------------------------- checkpoint tiles by TMA --
-      if (elect_one()) {
-        uint32_t n = 0;
-        while (ok && work.next(plan, pair, pairs, it)) {
-          int tm, tn;
-          tile_place(plan, it.tile, tm, tn);
-          const int i0 = tn * kTileN + static_cast<int>(rank) * (tile_cols(args.in, tn) / 2);
-          // Exponents come 16 at a time (a TMA copy starts on 16 bytes).
-          const int x0 = (i0 / kCkptBlock) & ~15;
-          for (int k = it.kb; k < it.ke; ++k, ++n) {
-            const uint32_t r = n % kRaw;
-            if (!mbar_wait(&raw_empty[r], ((n / kRaw) & 1u) ^ 1u, abort_flag, args.status)) {
-              ok = false;
-              break;
-            }
+      // -------------------------------------------- checkpoint tiles by TMA --
+      uint32_t n = 0;
+      while (ok && work.next(plan, pair, pairs, it)) {
+        int tm, tn;
+        tile_place(plan, it.tile, tm, tn);
+        const int i0 = tn * kTileN + static_cast<int>(rank) * (tile_cols(args.in, tn) / 2);
+        // Exponents come 16 at a time (a TMA copy starts on 16 bytes).
+        const int x0 = (i0 / kCkptBlock) & ~15;
+        for (int k = it.kb; k < it.ke; ++k, ++n) {
+          const uint32_t r = n % kRaw;
+          if (!mbar_wait(&raw_empty[r], ((n / kRaw) & 1u) ^ 1u, abort_flag, args.status)) {
+            ok = false;
+            break;
+          }
+          if (elect_one()) {
             mbar_arrive_expect_tx(&raw_full[r], kRawBytes);
             tma_load_2d(raw + r * kRawBytes, &map_q, &raw_full[r], i0, k * kTok);
             tma_load_2d(raw + r * kRawBytes + kRawQ, &map_ex, &raw_full[r], x0, k * kTok);
           }
+          __syncwarp();
         }
-        if (!ok)
-          for (uint32_t j = n >= kRaw ? n - kRaw : 0; j < n; ++j)
-            drain(&raw_full[j % kRaw], (j / kRaw) & 1u);
       }
-    } else if (warp == 1) {
-      // -------------------------------------------------------- MMA issuer --
-      if (rank == 0 && elect_one()) {
-        uint32_t n = 0, seg = 0;  // stages, segments issued
-        while (ok && work.next(plan, pair, pairs, it)) {
-          int tm, tn;
-          tile_place(plan, it.tile, tm, tn);
-          const uint32_t idesc = idesc_bf16(kTileM, tile_cols(args.in, tn), true, true);
-          for (int k = it.kb; k < it.ke; ++k, ++n) {
-            const bool first = (k - it.kb) % kSegment == 0;
-            const uint32_t buf = seg & 1u;
-            if (first &&
-                !mbar_wait(&tempty_bar[buf], ((seg >> 1) & 1u) ^ 1u, abort_flag, args.status)) {
-              ok = false;
-              break;
-            }
+      if (!ok)
+        for (uint32_t j = n >= kRaw ? n - kRaw : 0; j < n; ++j)
+          drain(&raw_full[j % kRaw], (j / kRaw) & 1u);
+    } else if (warp == 1 && rank == 0) {
+      // ------------------------------------------------------ MMA issuer --
+      uint32_t n = 0, seg = 0;  // stages, segments issued
+      while (ok && work.next(plan, pair, pairs, it)) {
+        int tm, tn;
+        tile_place(plan, it.tile, tm, tn);
+        const uint32_t idesc = idesc_bf16(kTileM, tile_cols(args.in, tn), true, true);
+        for (int k = it.kb; k < it.ke; ++k, ++n) {
+          const bool first = (k - it.kb) % kSegment == 0;
+          const bool last = (k - it.kb) % kSegment == kSegment - 1 || k == it.ke - 1;
+          const uint32_t buf = seg & 1u;
+          if (first &&
+              !mbar_wait(&tempty_bar[buf], ((seg >> 1) & 1u) ^ 1u, abort_flag, args.status)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sa = n % kDy;
+          if (!mbar_wait(&full_bar[sa], (n / kDy) & 1u, abort_flag, args.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (elect_one()) {
             const uint32_t d = tmem_base + buf * kTileN;
-            const uint32_t sa = n % kDy;
-            if (!mbar_wait(&full_bar[sa], (n / kDy) & 1u, abort_flag, args.status)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
             const uint32_t a = smem_u32(ring + sa * kOperand);
             const uint32_t b = smem_u32(xring + n % kX * kOperand);
-  #pragma unroll
+#pragma unroll
             for (int kk = 0; kk < kTok / 16; ++kk)
               // 64-wide blocks of outputs or inputs 8 KB apart, 8 tokens 1 KB.
               tc_mma_bf16_pair(d, sdesc_sw128(a + kk * 2048, kBoxBytes, 1024),
                                sdesc_sw128(b + kk * 2048, kBoxBytes, 1024), idesc,
                                first && kk == 0 ? 0u : 1u);
             tc_commit_pair_multicast(&done_bar[sa], 0x3);
-            if ((k - it.kb) % kSegment == kSegment - 1 || k == it.ke - 1) {
-              tc_commit_pair_multicast(&tfull_bar[buf], 0x3);
-              ++seg;
-            }
+            if (last) tc_commit_pair_multicast(&tfull_bar[buf], 0x3);
           }
+          __syncwarp();
+          seg += last ? 1 : 0;
         }
-        tc_commit_pair(&drain_bar);
-        drain(&drain_bar, 0);
       }
+      if (elect_one()) tc_commit_pair(&drain_bar);
+      __syncwarp();
+      drain(&drain_bar, 0);
     }
   } else if (warp >= kFirstConvert) {
     // -------------------------------------------------------- converters --
@@ -541,9 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   // Neither CTA may leave while the other's tensor core reads its shared memory
-  // or an arrival is on its way to it. Every thread arrives for itself here: the
-  // warps of the elected lanes come in two parts, and a barrier of whole warps
-  // (.aligned) that counts such a warp twice would let a CTA go too early.
+  // or an arrival is on its way to it: every thread arrives for itself here.
   __syncwarp();
   tc_fence_before();
   cluster_sync_threads();
