@@ -78,9 +78,10 @@ struct Item {
   int slot;  // partial tile to write, -1: the tile itself
 };
 
+// 32 bits hold every count: fewer than kRefPairs tiles are cut, of at most 2^24
+// stages each.
 struct WorkList {
-  int i = 0;
-  long long pos = -1, end = 0;
+  int i = 0, pos = -1, end = 0;
   __device__ __forceinline__ bool next(const WgradPlan& p, int pair, int pairs, Item& it) {
     if (pos < 0) {
       it.tile = pair + i++ * pairs;
@@ -90,16 +91,16 @@ struct WorkList {
         it.slot = -1;
         return true;
       }
-      const long long all = static_cast<long long>(p.cut) * p.kt;
-      pos = min(static_cast<long long>(pair) * p.per_pair, all);
+      const int all = p.cut * p.kt;
+      pos = min(pair * p.per_pair, all);
       end = min(pos + p.per_pair, all);
       i = 0;
     }
     if (pos >= end) return false;
-    const int t = static_cast<int>(pos / p.kt);
+    const int t = static_cast<int>(static_cast<unsigned>(pos) / static_cast<unsigned>(p.kt));
     it.tile = p.whole + t;
-    it.kb = static_cast<int>(pos - static_cast<long long>(t) * p.kt);
-    it.ke = static_cast<int>(min(static_cast<long long>(p.kt), it.kb + (end - pos)));
+    it.kb = pos - t * p.kt;
+    it.ke = min(p.kt, it.kb + (end - pos));
     it.slot = it.ke - it.kb == p.kt ? -1 : 2 * pair + i;
     ++i;
     pos += it.ke - it.kb;

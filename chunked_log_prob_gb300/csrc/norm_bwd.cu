@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(256) norm_bwd_cols_kernel(const NormBwdArgs a)
 // dw and db from the CTAs' partial sums: 32 columns a CTA, the partial rows
 // dealt to its 16 warps, whose sums are added in warp order. Launched while the
 // backward kernel still runs (it waits for its end here): 3 us less a call.
-__global__ void __launch_bounds__(512) norm_bwd_finish_kernel(const float* __restrict__ partials,
+__global__ void __launch_bounds__(512) norm_bwd_finish_kernel(const float* partials,
                                                               int rows, int d, float* dweight,
                                                               float* dbias, const float* add_dw,
                                                               const float* add_db) {
