@@ -29,9 +29,13 @@ constexpr int kTileN = 256;        // inputs of a pair's tile
 constexpr int kTok = 64;           // tokens of a stage
 // Rings: a slot's way round (barrier to barrier, TMA or widening, the MMAs)
 // takes several stages' MMA time, so each of them is as deep as memory allows.
-constexpr int kDy = 6;             // dY tiles
+constexpr int kDy = 5;             // dY tiles
 constexpr int kX = 4;              // widened X tiles
-constexpr int kRaw = 5;            // e4m3 tiles with their exponents
+constexpr int kRaw = 6;            // e4m3 tiles with their exponents
+// The converters' two groups take turns with the stages. A slot must stay with
+// one of them: a group that waits for a phase of its barrier has then seen the
+// phase before (a parity alone cannot tell that one apart from the one after).
+static_assert(kRaw % 2 == 0, "a raw slot belongs to one converter group");
 constexpr int kBoxBytes = kTok * 128;      // 64 tokens x 64 bf16 columns
 constexpr int kOperand = 2 * kBoxBytes;    // a CTA's 128 outputs, or 128 inputs
 constexpr int kRawQ = kTok * 128;          // 64 tokens x 128 e4m3

@@ -554,6 +554,20 @@ def test_wgrad_exponents_of_every_size(clp):
     check("dW", got, f64(dy).T @ x64, 8 * 2 * E * mag)  # 6 terms
 
 
+def test_wgrad_repeats_on_cold_inputs(clp):
+    # 28 of the 256 tiles are cut, and their tokens come from memory late and out
+    # of step: every launch gives the same bits.
+    g = torch.Generator(device=DEV).manual_seed(11)
+    x = torch.randn(16384, 4096, device=DEV, generator=g).bfloat16()
+    dy = torch.randn(16384, 4096, device=DEV, generator=g).bfloat16()
+    c = clp.grpo_ckpt_pack(x)
+    cold = torch.empty(256 << 20, dtype=torch.uint8, device=DEV)
+    first = clp.grpo_ckpt_wgrad(dy, c)
+    for _ in range(200):
+        cold.zero_()
+        assert torch.equal(clp.grpo_ckpt_wgrad(dy, c), first)
+
+
 def test_wgrad_nan_reaches_only_its_columns(clp):
     x = rand(torch.Generator().manual_seed(0), 100, 64, torch.bfloat16).to(DEV)
     x[50, 9] = float("nan")
