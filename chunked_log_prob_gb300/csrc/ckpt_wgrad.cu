@@ -13,7 +13,13 @@
 // off instead of rounding, which bends a long sum towards zero in proportion to
 // its length (measured against fp64: 3.1e-6 at 5541 tokens, 1.1e-5 at 16384), so
 // TMEM holds the sum of kSegment stages at a time (two buffers in turn), and the
-// epilogue warps add each to the tile's running sum in their registers, rounded.
+// epilogue warps add each to the tile's running sum in their registers, rounded
+// (4.2e-7 at 16384 tokens).
+//
+// 16384 x 4096 x 4096: 326 us, 1685 TFLOP/s (0.88 of cuBLAS's measured burst), 365
+// us in a row under the power cap. Bound by the tensor cores and, close behind,
+// by the widening (a stage of 64 tokens takes the former 512 cycles, measured
+// about 640).
 #include <algorithm>
 #include <cstring>
 

@@ -8,7 +8,11 @@
 //   dw = sum_t dy h, db = sum_t dy
 //
 // Memory bound: about 10 operations per value against 4 to 9 bytes. A row is
-// read once and held in registers (up to 8192 columns); statistics are fp32.
+// read once and held in registers (up to 16384 columns); statistics are fp32.
+// What it took, at 131072 x 2880 in bf16 with residual and checkpoint (3.41 GB):
+// loads into registers one row ahead 1615 us; rows in flight in shared memory
+// 610; pairs of values and 32 of them a thread 520 to 575 (5.9 to 6.6 TB/s, of
+// 6.8 measured for a copy; it follows how the five streams meet in DRAM).
 #include "norm_ring.cuh"
 
 namespace grpo {

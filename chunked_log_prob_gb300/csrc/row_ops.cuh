@@ -101,11 +101,6 @@ __device__ __forceinline__ void store_chunk(T* row, const Raw8<T>& r, int c, int
   }
 }
 
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-}
-
 template <typename T>
 __device__ __forceinline__ void widen(const Raw8<T>& r, float (&v)[8]) {
 #pragma unroll
@@ -127,9 +122,6 @@ __device__ __forceinline__ float load_param(const void* p, int type, int col) {
   return to_f32(static_cast<const __half*>(p)[col]);
 }
 
-// Sum of a pair over the `tpr` threads of a row, given to all of them, in a
-// fixed order. tpr == 32: shuffles alone. Otherwise one named barrier (`bar`,
-// 1-15) of the row's threads; `sh` holds 2 x 32 pairs, used in turn (`phase`).
 __device__ __forceinline__ float2 warp_sum2(float2 v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -149,6 +141,9 @@ __device__ __forceinline__ void named_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+// Sum of a pair over the `tpr` threads of a row, given to all of them, in a
+// fixed order. tpr == 32: shuffles alone. Otherwise one named barrier (`bar`,
+// 1-15) of the row's threads; `sh` holds 2 x 32 pairs, used in turn (`phase`).
 __device__ __forceinline__ float2 row_sum2(float2 v, int t, int tpr, int bar, float2* sh,
                                            int& phase) {
   v = warp_sum2(v);
@@ -162,8 +157,8 @@ __device__ __forceinline__ float2 row_sum2(float2 v, int t, int tpr, int bar, fl
 }
 
 // ------------------------------------------------------- rows in flight ----
-// Rows on 16 bytes come to shared memory by bulk copies, several rows ahead:
-// the bytes in flight do not cost registers.
+// Rows come to shared memory by bulk copies, several rows ahead: the bytes in
+// flight do not cost registers.
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
                                           uint64_t* bar) {

@@ -379,6 +379,9 @@ int grpo_launch_timing_read(grpo_kernel_time* out, int capacity, int* count);
  * Outputs may lie on inputs of the same type and stride (y on x, z on
  * residual, dx on dy, dres or x); other overlaps are not. Calls are
  * asynchronous on `stream`, allocate nothing, and can be captured in a graph.
+ * Rows that do not start on 16 bytes are read with the 16 bytes around their
+ * ends. A wait for a copy that runs out (about a second) leaves NaN in the row
+ * and in the weight gradients.
  * ------------------------------------------------------------------------- */
 #define GRPO_DTYPE_BF16 0
 #define GRPO_DTYPE_FP16 1
