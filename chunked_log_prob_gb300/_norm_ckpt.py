@@ -233,20 +233,14 @@ def grpo_norm_fwd(x, weight=None, bias=None, *, residual=None, kind="rms", eps=1
         y = _like(x, sx)
     else:
         sy = _rows(y, "y", dt, shape, dev)
-    if want_stats and mean is None and rstd is None and not k:
-        mean, rstd = _empty((2, n), dtype=_F32, device=dev).unbind()
-        pm = mean.data_ptr()
-        ps = rstd.data_ptr()
-    elif mean is not None:
+    if mean is not None:
         if k:
             raise ValueError("mean: RMS norm has none")
         pm = _packed(mean, "mean", _F32, (n,), dev)
     elif want_stats and not k:
         mean = _empty(n, dtype=_F32, device=dev)
         pm = mean.data_ptr()
-    if ps is not None:
-        pass
-    elif rstd is not None:
+    if rstd is not None:
         ps = _packed(rstd, "rstd", _F32, (n,), dev)
     elif want_stats:
         rstd = _empty(n, dtype=_F32, device=dev)
@@ -321,19 +315,12 @@ def grpo_norm_bwd(dy, x, weight, mean, rstd, *, dres=None, kind="rms", mask=None
     if want_dweight is None:
         want_dweight = weight is not None
     vec = (d,)
-    if (dweight is None and dbias is None and (want_dweight or add_dweight is not None) and
-            (want_dbias or add_dbias is not None)):
-        dweight, dbias = _empty((2, d), dtype=_F32, device=dev).unbind()
-        pdw = dweight.data_ptr()
-        pdb = dbias.data_ptr()
-    elif dweight is not None:
+    if dweight is not None:
         pdw = _packed(dweight, "dweight", _F32, vec, dev)
     elif want_dweight or add_dweight is not None:
         dweight = _empty(d, dtype=_F32, device=dev)
         pdw = dweight.data_ptr()
-    if pdb is not None:
-        pass
-    elif dbias is not None:
+    if dbias is not None:
         pdb = _packed(dbias, "dbias", _F32, vec, dev)
     elif want_dbias or add_dbias is not None:
         dbias = _empty(d, dtype=_F32, device=dev)
