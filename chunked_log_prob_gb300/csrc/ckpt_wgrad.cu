@@ -565,42 +565,69 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc_pair(tmem_base, kTmemCols);
 }
 
-// dW of the cut tiles: each tile's pieces added in the order of their tokens,
-// then `add`. Grid: cut tiles x 16 column chunks; a thread per row of the tile.
+// dW of the cut tiles: the sum of each tile's pieces, and `add`. A CTA takes 16
+// columns and 256 / G rows of a tile; thread (row, g) adds the pieces g, g + G, ...
+// in their order, and the G sums are then added in theirs: always the same order,
+// so the result does not change from call to call. G = 8 where a tile may have
+// more than 4 pieces, which one thread would wait for in a row. Whole calls, tokens
+// x out x in, with G = 1 and with G = 8: 32768 x 256 x 512 59 and 27 us, 4096 x 256 x
+// 256 20 and 17, 2000 x 512 x 512 (5 pieces) 19.1 and 17.1; but 8192 x 1536 x 1536
+// (36 tiles of up to 4 pieces, most of the 8 threads idle) 48 and 53.
+template <int G>
 __global__ void __launch_bounds__(kTileM) ckpt_wgrad_join_kernel(const WgradArgs args,
                                                                  const WgradPlan plan) {
+  constexpr int kRows = kTileM / G;
+  __shared__ float4 part[G > 1 ? G : 1][G > 1 ? 4 : 1][G > 1 ? kRows : 1];
   const int t = static_cast<int>(blockIdx.x);
-  const long long first = static_cast<long long>(t) * plan.kt;
-  const int qa = static_cast<int>(first / plan.per_pair);
-  const int qb = static_cast<int>((first + plan.kt - 1) / plan.per_pair);
-  if (qa == qb) return;  // one piece covered the tile
+  const int first = t * plan.kt;
+  const int qa = first / plan.per_pair;
+  const int qb = (first + plan.kt - 1) / plan.per_pair;  // > qa: a part is shorter than a tile
   int tm, tn;
   tile_place(plan, plan.whole + t, tm, tn);
-  const int lrow = static_cast<int>(threadIdx.x);
+  const int r = static_cast<int>(threadIdx.x) % kRows, g = static_cast<int>(threadIdx.x) / kRows;
+  const int lrow = static_cast<int>(blockIdx.z) * kRows + r;
   const int row = tm * kTileM + lrow;
   const int c0 = static_cast<int>(blockIdx.y) * 16;  // column of the tile
   const int i0 = tn * kTileN + c0;
-  if (row >= args.out || i0 >= args.in) return;
+  const bool valid = row < args.out && i0 < args.in;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces are there
   float4 v[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (valid) {
 #pragma unroll 4
-  for (int q = qa; q <= qb; ++q) {
-    // A pair's second piece begins with its tile; its first one does not, or
-    // is the first of the pair's part.
-    const int slot = 2 * q + (static_cast<long long>(q) * plan.per_pair < first ? 1 : 0);
-    const float* p = args.partials + static_cast<long long>(slot) * kSlotFloats +
-                     (c0 / 4 * kTileM + lrow) * 4;
+    for (int q = qa + g; q <= qb; q += G) {
+      // A pair's second piece begins with its tile; its first one does not, or
+      // is the first of the pair's part.
+      const int slot = 2 * q + (q * plan.per_pair < first ? 1 : 0);
+      const float* p = args.partials + static_cast<long long>(slot) * kSlotFloats +
+                       (c0 / 4 * kTileM + lrow) * 4;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float4 x = *reinterpret_cast<const float4*>(p + j * kTileM * 4);
-      v[j].x += x.x;
-      v[j].y += x.y;
-      v[j].z += x.z;
-      v[j].w += x.w;
+      for (int j = 0; j < 4; ++j) {
+        const float4 x = *reinterpret_cast<const float4*>(p + j * kTileM * 4);
+        v[j].x += x.x;
+        v[j].y += x.y;
+        v[j].z += x.z;
+        v[j].w += x.w;
+      }
     }
   }
+  if constexpr (G > 1) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) part[g][j][r] = v[j];
+    __syncthreads();
+    if (g != 0) return;
+    for (int k = 1; k < G; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float4 x = part[k][j][r];
+        v[j].x += x.x;
+        v[j].y += x.y;
+        v[j].z += x.z;
+        v[j].w += x.w;
+      }
+  }
+  if (!valid) return;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     if (i0 + 4 * j >= args.in) break;
@@ -687,8 +714,10 @@ cudaError_t launch_ckpt_wgrad(const WgradArgs& a, int sms, cudaStream_t st) {
   }
   if (e != cudaSuccess || plan.cut == 0) return e;
   // Its launch overlaps the end of the other (it waits for that itself).
+  const int pieces = (plan.kt + plan.per_pair - 1) / plan.per_pair + 1;  // of a tile, at most
+  const int groups = pieces > 4 ? 8 : 1;
   cudaLaunchConfig_t join = {};
-  join.gridDim = dim3(plan.cut, kTileN / 16);
+  join.gridDim = dim3(plan.cut, kTileN / 16, groups);
   join.blockDim = dim3(kTileM);
   join.stream = st;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -696,7 +725,8 @@ cudaError_t launch_ckpt_wgrad(const WgradArgs& a, int sms, cudaStream_t st) {
   join.attrs = attr;
   join.numAttrs = 1;
   LaunchTimer timer("ckpt_wgrad_join_kernel", st);
-  return cudaLaunchKernelEx(&join, ckpt_wgrad_join_kernel, a, plan);
+  return groups == 8 ? cudaLaunchKernelEx(&join, ckpt_wgrad_join_kernel<8>, a, plan)
+                     : cudaLaunchKernelEx(&join, ckpt_wgrad_join_kernel<1>, a, plan);
 }
 
 }  // namespace grpo
