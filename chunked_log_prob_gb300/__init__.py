@@ -42,4 +42,5 @@ from ._norm_ckpt import (  # noqa: F401
     grpo_norm_bwd,
     grpo_norm_fwd,
     grpo_norm_workspace_size,
+    grpo_selftest_lose_copy,
 )

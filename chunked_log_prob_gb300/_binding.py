@@ -112,6 +112,7 @@ def _load():
         "grpo_ckpt_pack": [vp, vp, vp, i64, i32, i32, i64, vp],
         "grpo_ckpt_unpack": [vp, vp, i64, i32, i32, i64, vp],
         "grpo_ckpt_wgrad_workspace_size": [i64, i32, i32, P(sz)],
+        "grpo_selftest_lose_copy": [i64],
         "grpo_ckpt_wgrad": [vp, vp, vp, vp, i64, i32, i32, i64, vp, sz, vp],
     }.items():
         fn = getattr(lib, name)
@@ -129,7 +130,7 @@ EXPORTED = ("grpo_default_params", "grpo_workspace_size", "grpo_logp_fwd",
             "grpo_launch_timing_read", "grpo_status_string",
             "grpo_norm_fwd", "grpo_norm_workspace_size", "grpo_norm_bwd", "grpo_ckpt_size",
             "grpo_ckpt_layout", "grpo_ckpt_pack", "grpo_ckpt_unpack",
-            "grpo_ckpt_wgrad_workspace_size", "grpo_ckpt_wgrad")
+            "grpo_ckpt_wgrad_workspace_size", "grpo_ckpt_wgrad", "grpo_selftest_lose_copy")
 
 FLAG_STORED_LOGITS = 1
 FLAG_SINGLE_CTA = 2

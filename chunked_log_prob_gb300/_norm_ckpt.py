@@ -426,3 +426,9 @@ def grpo_ckpt_wgrad(dy, ckpt, *, add=None, dW=None, workspace=None) -> torch.Ten
     if rc:
         raise GrpoError(rc, "grpo_ckpt_wgrad")
     return dW
+
+
+def grpo_selftest_lose_copy(index: int) -> None:
+    """This thread's next ``grpo_ckpt_wgrad`` leaves out one copy of its first CTA
+    (of the 64-token stage ``index``; -1: none) and gives up after about a second."""
+    _raise(lib.grpo_selftest_lose_copy(int(index)), "grpo_selftest_lose_copy")

@@ -139,6 +139,14 @@ __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
     if (clock64() - t0 > kWaitLimitCycles) return;
 }
 
+// A warp's wait: one answer for all lanes, before steps of the whole warp. Each
+// polls for itself, and one may give up (or see the abort flag) as another finds
+// the phase done.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                          int* status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status)) != 0;
+}
+
 // True in one lane of the (whole) warp. The compiler then knows that one thread
 // runs what follows and feeds tcgen05 and TMA their uniform operands directly;
 // behind `lane == 0` it cannot, and a stage took its issuing thread twice as
@@ -285,86 +293,88 @@ __global__ void __launch_bounds__(kThreads, 1)
   // follows to the new count only where the instruction dominates it.
   if (warp < kFirstEpilogue) {
     give_registers<kControlRegs>();
-    // Whole warps walk through the work and wait; one lane issues.
+    // One lane of each role walks through the work, waits and issues; the others
+    // are at the warp barrier before the closing cluster barrier. (No step inside
+    // is the whole warp's: lanes that waited each for itself could part at a wait
+    // that runs out, and the two halves then wait for each other without end.)
     if (warp == 0) {
       // -------------------------------------------------- dY's tiles by TMA --
-      uint32_t n = 0;  // stages issued
-      while (ok && work.next(plan, pair, pairs, it)) {
-        int tm, tn;
-        tile_place(plan, it.tile, tm, tn);
-        const int o0 = tm * kTileM + static_cast<int>(rank) * (kTileM / 2);
-        for (int k = it.kb; k < it.ke; ++k, ++n) {
-          const uint32_t s = n % kDy;
-          if (!mbar_wait(&done_bar[s], ((n / kDy) & 1u) ^ 1u, abort_flag, args.status)) {
-            ok = false;
-            break;
-          }
-          if (elect_one()) {
+      if (elect_one()) {
+        uint32_t n = 0;  // stages issued
+        while (ok && work.next(plan, pair, pairs, it)) {
+          int tm, tn;
+          tile_place(plan, it.tile, tm, tn);
+          const int o0 = tm * kTileM + static_cast<int>(rank) * (kTileM / 2);
+          for (int k = it.kb; k < it.ke; ++k, ++n) {
+            const uint32_t s = n % kDy;
+            if (!mbar_wait(&done_bar[s], ((n / kDy) & 1u) ^ 1u, abort_flag, args.status)) {
+              ok = false;
+              break;
+            }
             const uint32_t lead = mapa_shared(smem_u32(&full_bar[s]), 0);
             mbar_arrive_expect_tx_cluster(lead, kOperand);
             uint8_t* a = ring + s * kOperand;
             tma_load_2d_pair_nohint(a, &map_dy, lead, o0, k * kTok);
             tma_load_2d_pair_nohint(a + kBoxBytes, &map_dy, lead, o0 + 64, k * kTok);
           }
-          __syncwarp();
         }
+        // After a timeout: let the copies in flight land before the CTA exits (the
+        // peer passes the closing cluster barrier only after this). Their barriers
+        // also wait for converters that may have given up: the drain ends by its
+        // own limit then, long after any copy.
+        if (!ok && rank == 0)
+          for (uint32_t j = n >= kDy ? n - kDy : 0; j < n; ++j)
+            drain(&full_bar[j % kDy], (j / kDy) & 1u);
       }
-      // After a timeout: let the copies in flight land before the CTA exits (the
-      // peer passes the closing cluster barrier only after this). Their barriers
-      // also wait for converters that may have given up: the drain ends by its
-      // own limit then, long after any copy.
-      if (!ok && rank == 0)
-        for (uint32_t j = n >= kDy ? n - kDy : 0; j < n; ++j)
-          drain(&full_bar[j % kDy], (j / kDy) & 1u);
     } else if (warp == 2) {
       // -------------------------------------------- checkpoint tiles by TMA --
-      uint32_t n = 0;
-      while (ok && work.next(plan, pair, pairs, it)) {
-        int tm, tn;
-        tile_place(plan, it.tile, tm, tn);
-        const int i0 = tn * kTileN + static_cast<int>(rank) * (tile_cols(args.in, tn) / 2);
-        // Exponents come 16 at a time (a TMA copy starts on 16 bytes).
-        const int x0 = (i0 / kCkptBlock) & ~15;
-        for (int k = it.kb; k < it.ke; ++k, ++n) {
-          const uint32_t r = n % kRaw;
-          if (!mbar_wait(&raw_empty[r], ((n / kRaw) & 1u) ^ 1u, abort_flag, args.status)) {
-            ok = false;
-            break;
-          }
-          if (elect_one()) {
+      if (elect_one()) {
+        uint32_t n = 0;
+        while (ok && work.next(plan, pair, pairs, it)) {
+          int tm, tn;
+          tile_place(plan, it.tile, tm, tn);
+          const int i0 = tn * kTileN + static_cast<int>(rank) * (tile_cols(args.in, tn) / 2);
+          // Exponents come 16 at a time (a TMA copy starts on 16 bytes).
+          const int x0 = (i0 / kCkptBlock) & ~15;
+          for (int k = it.kb; k < it.ke; ++k, ++n) {
+            const uint32_t r = n % kRaw;
+            if (!mbar_wait(&raw_empty[r], ((n / kRaw) & 1u) ^ 1u, abort_flag, args.status)) {
+              ok = false;
+              break;
+            }
+            if (n == args.lost && blockIdx.x == 0) continue;
             mbar_arrive_expect_tx(&raw_full[r], kRawBytes);
             tma_load_2d(raw + r * kRawBytes, &map_q, &raw_full[r], i0, k * kTok);
             tma_load_2d(raw + r * kRawBytes + kRawQ, &map_ex, &raw_full[r], x0, k * kTok);
           }
-          __syncwarp();
         }
+        if (!ok)
+          for (uint32_t j = n >= kRaw ? n - kRaw : 0; j < n; ++j)
+            drain(&raw_full[j % kRaw], (j / kRaw) & 1u);
       }
-      if (!ok)
-        for (uint32_t j = n >= kRaw ? n - kRaw : 0; j < n; ++j)
-          drain(&raw_full[j % kRaw], (j / kRaw) & 1u);
     } else if (warp == 1 && rank == 0) {
       // ------------------------------------------------------ MMA issuer --
-      uint32_t n = 0, seg = 0;  // stages, segments issued
-      while (ok && work.next(plan, pair, pairs, it)) {
-        int tm, tn;
-        tile_place(plan, it.tile, tm, tn);
-        const uint32_t idesc = idesc_bf16(kTileM, tile_cols(args.in, tn), true, true);
-        for (int k = it.kb; k < it.ke; ++k, ++n) {
-          const bool first = (k - it.kb) % kSegment == 0;
-          const bool last = (k - it.kb) % kSegment == kSegment - 1 || k == it.ke - 1;
-          const uint32_t buf = seg & 1u;
-          if (first &&
-              !mbar_wait(&tempty_bar[buf], ((seg >> 1) & 1u) ^ 1u, abort_flag, args.status)) {
-            ok = false;
-            break;
-          }
-          const uint32_t sa = n % kDy;
-          if (!mbar_wait(&full_bar[sa], (n / kDy) & 1u, abort_flag, args.status)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          if (elect_one()) {
+      if (elect_one()) {
+        uint32_t n = 0, seg = 0;  // stages, segments issued
+        while (ok && work.next(plan, pair, pairs, it)) {
+          int tm, tn;
+          tile_place(plan, it.tile, tm, tn);
+          const uint32_t idesc = idesc_bf16(kTileM, tile_cols(args.in, tn), true, true);
+          for (int k = it.kb; k < it.ke; ++k, ++n) {
+            const bool first = (k - it.kb) % kSegment == 0;
+            const bool last = (k - it.kb) % kSegment == kSegment - 1 || k == it.ke - 1;
+            const uint32_t buf = seg & 1u;
+            if (first &&
+                !mbar_wait(&tempty_bar[buf], ((seg >> 1) & 1u) ^ 1u, abort_flag, args.status)) {
+              ok = false;
+              break;
+            }
+            const uint32_t sa = n % kDy;
+            if (!mbar_wait(&full_bar[sa], (n / kDy) & 1u, abort_flag, args.status)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
             const uint32_t d = tmem_base + buf * kTileN;
             const uint32_t a = smem_u32(ring + sa * kOperand);
             const uint32_t b = smem_u32(xring + n % kX * kOperand);
@@ -376,14 +386,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                first && kk == 0 ? 0u : 1u);
             tc_commit_pair_multicast(&done_bar[sa], 0x3);
             if (last) tc_commit_pair_multicast(&tfull_bar[buf], 0x3);
+            seg += last ? 1 : 0;
           }
-          __syncwarp();
-          seg += last ? 1 : 0;
         }
+        tc_commit_pair(&drain_bar);
+        drain(&drain_bar, 0);
       }
-      if (elect_one()) tc_commit_pair(&drain_bar);
-      __syncwarp();
-      drain(&drain_bar, 0);
     }
   } else if (warp >= kFirstConvert) {
     // -------------------------------------------------------- converters --
@@ -408,17 +416,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t n = 0, r = group, r_par = 0, f = group;
     uint32_t d = 2 * kDy - kX + group, d_par = 1;
     while (d >= kDy) d -= kDy;
-    while (ok && work.next(plan, pair, pairs, it)) {
+    while (__all_sync(0xffffffffu, ok) && work.next(plan, pair, pairs, it)) {
       int tm, tn;
       tile_place(plan, it.tile, tm, tn);
       const int i0 = tn * kTileN + static_cast<int>(rank) * (tile_cols(args.in, tn) / 2);
       const uint32_t ex = exp0 + ((i0 / kCkptBlock) & 15);  // our exponent of the 16
       const uint32_t n_end = n + (it.ke - it.kb);
+      // A lane whose wait ran out stays with its warp up to the tile's end (no
+      // vote on the way: 1 to 3 % of the whole): it waits no more, what it stores
+      // is not its values, and its CTA's abort flag is up.
       for (uint32_t m = n + ((n ^ group) & 1u); m < n_end; m += 2) {
-        if (!mbar_wait(&raw_full[r], r_par, abort_flag, args.status)) {
-          ok = false;
-          break;
-        }
+        ok = ok && mbar_wait(&raw_full[r], r_par, abort_flag, args.status);
         uint4 w[2];
         uint32_t e[2], o[2][8];
 #pragma unroll
@@ -429,10 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         widen32(w, e, o);
         // Widened before the slot is waited for: only the stores, the fence and
         // the barriers lie on the slot's way round.
-        if (m >= kX && !mbar_wait(&done_bar[d], d_par, abort_flag, args.status)) {
-          ok = false;
-          break;
-        }
+        if (m >= kX) ok = ok && mbar_wait(&done_bar[d], d_par, abort_flag, args.status);
         const uint32_t dst = dst0 + (m % kX) * kOperand;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -441,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
+        if (lane == 0 && ok) {
           mbar_arrive(&raw_empty[r]);
           mbar_arrive_cluster(full0 + f * 8u);
         }
@@ -478,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < 32; ++j) sum[c][j] = 0.f;
       for (int k = it.kb; k < it.ke; k += kSegment, ++seg) {
         const uint32_t buf = seg & 1u;
-        if (!mbar_wait(&tfull_bar[buf], (seg >> 1) & 1u, abort_flag, args.status)) {
+        if (!warp_wait(&tfull_bar[buf], (seg >> 1) & 1u, abort_flag, args.status)) {
           ok = false;
           break;
         }

@@ -68,6 +68,9 @@ struct CkptArgs {
   int d;
 };
 
+// No copy is left out (grpo_selftest_lose_copy).
+constexpr uint32_t kNoneLost = 0xffffffffu;
+
 // Largest D of the kernels that hold a whole row in registers.
 constexpr int kNormRegisterRow = 16384;
 // Rows of partial weight gradients of one backward call: at most this many.
@@ -88,6 +91,7 @@ struct WgradArgs {
   int* status;
   long long n, lddy, lddw, ldadd;
   int out, in;
+  uint32_t lost;  // self-test: the first CTA's stage whose copy is left out, or kNoneLost
 };
 size_t ckpt_wgrad_workspace(long long n, int out, int in);
 cudaError_t launch_ckpt_wgrad(const WgradArgs& a, int sms, cudaStream_t st);

@@ -64,6 +64,14 @@ int check_wgrad(int64_t n, int32_t out, int32_t in, int64_t dy_stride) {
   return GRPO_OK;
 }
 
+// What grpo_selftest_lose_copy asked of this thread's next call.
+thread_local uint32_t t_lost = kNoneLost;
+uint32_t take_lost() {
+  const uint32_t v = t_lost;
+  t_lost = kNoneLost;
+  return v;
+}
+
 int64_t stride_or(int64_t s, int64_t hidden) { return s != 0 ? s : hidden; }
 
 size_t norm_workspace(const grpo_norm_desc* d) {
@@ -255,6 +263,12 @@ int grpo_ckpt_unpack(const void* ckpt, void* x, int64_t n_tokens, int32_t hidden
   return ckpt_call(x, false, nullptr, ckpt, n_tokens, hidden, dtype, x_stride, stream);
 }
 
+int grpo_selftest_lose_copy(int64_t index) {
+  if (index < -1 || index >= kMaxRows) return GRPO_ERR_INVALID_ARG;
+  t_lost = index < 0 ? kNoneLost : static_cast<uint32_t>(index);
+  return GRPO_OK;
+}
+
 int grpo_ckpt_wgrad_workspace_size(int64_t n_tokens, int32_t out, int32_t in, size_t* bytes) {
   if (bytes == nullptr) return GRPO_ERR_INVALID_ARG;
   const int r = check_wgrad(n_tokens, out, in, 0);
@@ -301,6 +315,7 @@ int grpo_ckpt_wgrad(const void* dy, const void* ckpt, const float* add, float* d
   a.ldadd = in;
   a.out = out;
   a.in = in;
+  a.lost = take_lost();
   return launch_ckpt_wgrad(a, sms, st) == cudaSuccess ? GRPO_OK : GRPO_ERR_CUDA;
 }
 

@@ -481,6 +481,14 @@ int grpo_ckpt_wgrad(const void* dy, const void* ckpt, const float* add_or_null, 
                     int64_t n_tokens, int32_t out_features, int32_t in_features,
                     int64_t dy_stride, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Self-test of what these calls do when a copy never arrives: the calling
+ * thread's next grpo_ckpt_wgrad does not issue its first CTA's copy of the
+ * 64-token stage `index` (counted over the stages of that CTA's tiles). The wait
+ * for it runs out after about a second, the kernel gives up the work that
+ * depends on it, lets the copies in flight land and returns; the context stays
+ * usable. -1: nothing is left out. */
+int grpo_selftest_lose_copy(int64_t index);
+
 /* Static text for a status code. */
 const char* grpo_status_string(int status);
 
