@@ -399,7 +399,8 @@ def grpo_ckpt_wgrad_workspace_size(n_tokens, out_features, in_features) -> int:
 def grpo_ckpt_wgrad(dy, ckpt, *, add=None, dW=None, workspace=None) -> torch.Tensor:
     """dW = add + dy^T X of a linear layer whose input X was kept as ``ckpt``.
 
-    dy is bf16 [N, out]; dW and add are fp32 [out, in] and may be the same.
+    dy is bf16 [N, out]; dW and add are fp32 [out, in] and may be the same. A wait
+    on the device that runs out leaves NaN (and its status in the workspace).
     """
     if dy.dim() != 2:
         raise ValueError(f"dy: expected 2 dimensions, got {dy.dim()}")

@@ -474,7 +474,9 @@ int grpo_ckpt_unpack(const void* ckpt, void* x, int64_t n_tokens, int32_t hidden
  * start on 16 bytes. X is exact in bf16, products are exact, sums are fp32 in
  * an order fixed by the sizes. Masked tokens: pack with the mask and let dY be
  * 0 there. The first bytes of the workspace (grpo_ckpt_wgrad_workspace_size,
- * 256-byte aligned) are a status word for grpo_read_device_status. */
+ * 256-byte aligned) are a status word for grpo_read_device_status. A wait that
+ * runs out (about a second) leaves GRPO_ERR_DEVICE_TIMEOUT there, and NaN in the
+ * 256 x 256 tiles of dW that its CTA pair had not yet written. */
 int grpo_ckpt_wgrad_workspace_size(int64_t n_tokens, int32_t out_features, int32_t in_features,
                                    size_t* bytes);
 int grpo_ckpt_wgrad(const void* dy, const void* ckpt, const float* add_or_null, float* dW,
@@ -485,8 +487,8 @@ int grpo_ckpt_wgrad(const void* dy, const void* ckpt, const float* add_or_null, 
  * thread's next grpo_ckpt_wgrad does not issue its first CTA's copy of the
  * 64-token stage `index` (counted over the stages of that CTA's tiles). The wait
  * for it runs out after about a second, the kernel gives up the work that
- * depends on it, lets the copies in flight land and returns; the context stays
- * usable. -1: nothing is left out. */
+ * depends on it (NaN in its place), lets the copies in flight land and returns;
+ * the context stays usable. -1: nothing is left out. */
 int grpo_selftest_lose_copy(int64_t index);
 
 /* Static text for a status code. */

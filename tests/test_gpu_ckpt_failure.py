@@ -54,3 +54,31 @@ def test_wgrad_ends_and_reports(clp, n, out, d, stage):
     again = clp.grpo_ckpt_wgrad(dy, c, workspace=ws)
     assert clp.grpo_read_device_status(ws) == 0
     assert torch.equal(again, want)
+
+
+def _tiles(t):
+    o, i = t.shape
+    return t.reshape(o // 256, 256, i // 256, 256).transpose(1, 2).reshape(-1, 256 * 256)
+
+
+# Tiles that the pair of the lost copy had not yet written. 4096 x 4096 outputs:
+# pair 0 of 76 has three of the 228 whole tiles of 64 stages each, then 24 stages
+# of the first of the 28 cut ones.
+@pytest.mark.parametrize("n,out,d,stage,lost,add", [
+    (512, 256, 256, 2, 1, "none"), (4096, 256, 256, 7, 1, "same"), (4096, 4096, 4096, 2, 4, "none"),
+    (4096, 4096, 4096, 2, 4, "same"), (4096, 4096, 4096, 70, 3, "other"),
+    (4096, 4096, 4096, 200, 1, "same")])
+def test_wgrad_leaves_nan_and_nothing_stale(clp, n, out, d, stage, lost, add):
+    dy, c, ws = _wgrad_case(clp, n, out, d)
+    grad = None if add == "none" else torch.ones(out, d, device=DEV)
+    want = _tiles(clp.grpo_ckpt_wgrad(dy, c, add=grad, workspace=ws))
+    dW = grad if add == "same" else torch.full((out, d), 7.0, device=DEV)
+    ws.zero_()  # the pieces of cut tiles would be plausible ones
+    clp.grpo_selftest_lose_copy(stage)
+    got = _tiles(clp.grpo_ckpt_wgrad(dy, c, add=grad, dW=dW, workspace=ws))
+    assert clp.grpo_read_device_status(ws) == TIMEOUT
+    nan = torch.isnan(got)
+    assert torch.equal(nan.any(1), nan.all(1))  # a tile is whole or NaN
+    assert int(nan.all(1).sum()) == lost
+    keep = ~nan.any(1)
+    assert torch.equal(got[keep], want[keep])
