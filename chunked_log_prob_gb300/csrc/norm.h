@@ -38,6 +38,7 @@ struct NormFwdArgs {
   long long n, ldx, ldr, ldy, ldz;
   int d, wtype, kind;
   float eps;
+  uint32_t lost;  // self-test: the row from which on its CTA copies none, or kNoneLost
 };
 
 struct NormBwdArgs {

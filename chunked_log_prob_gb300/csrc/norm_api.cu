@@ -127,6 +127,7 @@ int grpo_norm_fwd(const void* x, const void* residual, const void* weight, const
   a.wtype = desc->weight_dtype;
   a.kind = desc->kind;
   a.eps = desc->eps;
+  a.lost = take_lost();
   const bool vec = rows_on_16(rows, 4, desc->hidden, desc->dtype);
   return launch_norm_fwd(a, desc->dtype, vec, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? GRPO_OK

@@ -13,16 +13,47 @@
 // loads into registers one row ahead 1615 us; rows in flight in shared memory
 // 610; pairs of values and 32 of them a thread 520 to 575 (5.9 to 6.6 TB/s, of
 // 6.8 measured for a copy; it follows how the five streams meet in DRAM).
+#include <climits>
+
 #include "norm_ring.cuh"
 
 namespace grpo {
 namespace {
+
+// `lost` holds each warp's first row whose copy did not come, and one of them all.
+__device__ __forceinline__ void gave_up(int* lost, int i) {
+  atomicMin(&lost[(threadIdx.y * blockDim.x + threadIdx.x) >> 5], i);
+  lost[kRingThreads / 32] = i;
+}
+
+// After the rows: a warp whose wait ran out has stored into z and the checkpoint
+// what its copies did not bring, in that row and in all since. NaN over it, here:
+// a branch for it in each row, or its state in registers, cost 3 to 5 % (131072
+// x 2880 without a residual).
+template <typename T, bool VEC, int CH>
+__device__ __forceinline__ void lost_rows(const NormFwdArgs& a, const int* lost) {
+  const int first = lost[(threadIdx.y * blockDim.x + threadIdx.x) >> 5];
+  if (first == INT_MAX) return;
+  const long long step = static_cast<long long>(gridDim.x) * blockDim.y;
+  for (long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y + step * first;
+       row < a.n; row += step) {
+    if (!row_live(a.mask, row, a.n)) continue;
+#pragma unroll 1
+    for (int k = 0; k < 8 * CH; ++k) {
+      const int col = chunk_col<VEC>(k >> 3, k & 7, threadIdx.x, blockDim.x);
+      if (col >= a.d) continue;
+      if (a.res != nullptr && a.z != nullptr) static_cast<T*>(a.z)[row * a.ldz + col] = T(kNaN);
+      if (a.ck.q != nullptr) a.ck.q[row * a.ck.ldq + col] = kCkptNaN;
+    }
+  }
+}
 
 template <typename T, bool VEC, int CH, int KIND>
 __global__ void __launch_bounds__(kRingThreads) norm_fwd_kernel(const NormFwdArgs a, const Ring ring) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(16) float red[kMaxRows][2 * 2 * 16];
   __shared__ float warp_n[2][16];
+  __shared__ int lost[kRingThreads / 32 + 1];
   __shared__ BlockTurn turns[VEC ? 1 : kRingThreads / 32];
   const int t = threadIdx.x, tpr = blockDim.x, g = threadIdx.y, d = a.d;
   const int warps = tpr >> 5;
@@ -38,12 +69,13 @@ __global__ void __launch_bounds__(kRingThreads) norm_fwd_kernel(const NormFwdArg
   const long long step = static_cast<long long>(gridDim.x) * blockDim.y;
   const long long row0 = static_cast<long long>(blockIdx.x) * blockDim.y + g;
   const int count = row_count(row0, a.n, step);
+  const int fetches = fetch_count(count, row0, step, a.lost);
   const uint8_t* const mask = a.mask;
   // Thread 0: slots whose copies have not been waited for, and the next row to fetch.
   uint32_t pending = 0;
   int fetched = 0;
   const auto fetch = [&](int slot) {
-    if (fetched >= count) return;
+    if (fetched >= fetches) return;
     const long long r = row0 + step * fetched++;
     if (mask != nullptr && mask[r] == 0) return;
     pending |= 1u << slot;
@@ -61,6 +93,7 @@ __global__ void __launch_bounds__(kRingThreads) norm_fwd_kernel(const NormFwdArg
     for (int s = 0; s < ring.slots; ++s) fetch(s);
   }
   for (int k = t; k < 2 * 2 * 16; k += tpr) red[g][k] = 0.f;
+  for (int k = g * tpr + t; k <= kRingThreads / 32; k += tpr * blockDim.y) lost[k] = INT_MAX;
   if (a.weight != nullptr)
     stage_param<VEC>(sw, a.weight, a.wtype, d, g * tpr + t, tpr * blockDim.y);
   if (a.bias != nullptr) stage_param<VEC>(sb, a.bias, a.wtype, d, g * tpr + t, tpr * blockDim.y);
@@ -93,7 +126,8 @@ __global__ void __launch_bounds__(kRingThreads) norm_fwd_kernel(const NormFwdArg
     f32x2 v[CH][4];
     float mean = 0.f, rstd = 0.f;
     if (live) {
-      ok = ok && row_wait(&bars[slot], (parity >> slot) & 1u);
+      ok = ok && row_wait(&bars[slot], (parity >> slot) & 1u,
+                          [&] { gave_up(lost, i); });
       if (ok) {
         parity ^= 1u << slot;
         pending &= ~(1u << slot);
@@ -123,7 +157,8 @@ __global__ void __launch_bounds__(kRingThreads) norm_fwd_kernel(const NormFwdArg
         for (int c = 0; c < CH; ++c)
 #pragma unroll
           for (int j = 0; j < 4; ++j) s[j & 1] = fma2(v[c][j], v[c][j], s[j & 1]);
-        float m[1] = {warp_sum(sum_of(add2(s[0], s[1])))};
+        // A thread whose copy did not come has NaN: so has then all of the row.
+        float m[1] = {warp_sum(ok ? sum_of(add2(s[0], s[1])) : kNaN)};
         join_warps(m, t, warps, g + 1, red[g], phase);
         rstd = rsqrtf(m[0] * inv_d + a.eps);
       } else {
@@ -134,7 +169,7 @@ __global__ void __launch_bounds__(kRingThreads) norm_fwd_kernel(const NormFwdArg
         for (int c = 0; c < CH; ++c)
 #pragma unroll
           for (int j = 0; j < 4; ++j) s[j & 1] = add2(v[c][j], s[j & 1]);
-        const float sum = warp_sum(sum_of(add2(s[0], s[1])));
+        const float sum = warp_sum(ok ? sum_of(add2(s[0], s[1])) : kNaN);
         const float mw = sum * inv_warp_n;
         const f32x2 nmw = pair(-mw, -mw);
         s[0] = s[1] = 0ull;
@@ -177,7 +212,6 @@ __global__ void __launch_bounds__(kRingThreads) norm_fwd_kernel(const NormFwdArg
         mean = total * inv_d;
         rstd = rsqrtf(centred * inv_d + a.eps);
       }
-      if (!ok) rstd = __uint_as_float(0x7fc00000u);
     } else {
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
@@ -228,6 +262,8 @@ __global__ void __launch_bounds__(kRingThreads) norm_fwd_kernel(const NormFwdArg
     live = live1;
   }
   land(bars, ring.slots, parity, pending);
+  __syncwarp();
+  if (lost[kRingThreads / 32] != INT_MAX) lost_rows<T, VEC, CH>(a, lost);
 }
 
 // Rows beyond kNormRegisterRow columns: the CTA walks over the row three times

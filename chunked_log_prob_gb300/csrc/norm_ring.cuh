@@ -64,6 +64,15 @@ __device__ __forceinline__ int row_count(long long row, long long n, long long s
   return row < n ? static_cast<int>((n - 1 - row) / step) + 1 : 0;
 }
 
+// How many of them are fetched: up to the self-test's lost row.
+__device__ __forceinline__ int fetch_count(int count, long long row0, long long step,
+                                           uint32_t lost) {
+  if (lost == kNoneLost) return count;
+  const long long past = static_cast<long long>(lost) - row0;
+  return past >= 0 && past % step == 0 && past / step < count ? static_cast<int>(past / step)
+                                                              : count;
+}
+
 // Threads of a row and rows of a CTA for D columns held in registers.
 struct RowShape {
   int tpr, rows, ch;

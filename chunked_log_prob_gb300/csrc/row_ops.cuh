@@ -25,6 +25,9 @@ constexpr int kCkptMinExp = -117;  // 2^-117 2^-9 is a normal bf16: every value
                                    // of the format expands to bf16 exactly
 constexpr int kCkptBias = 127;
 
+constexpr uint8_t kCkptNaN = 0x7f;  // an e4m3 NaN
+constexpr float kNaN = __builtin_nanf("");
+
 template <typename T>
 struct alignas(16) Raw8 {
   T e[8];
@@ -169,14 +172,22 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
-// Waits for a phase of `bar`; false after about a second (no status word here:
-// the caller then gives NaN).
-__device__ __forceinline__ bool row_wait(uint64_t* bar, uint32_t parity) {
+// Waits for a phase of `bar`; false after about a second, then after `gave_up()`
+// (no status word here: the caller gives NaN).
+template <typename F>
+__device__ __forceinline__ bool row_wait(uint64_t* bar, uint32_t parity, F gave_up) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity))
-    if (clock64() - t0 > kWaitLimitCycles) return false;
+  while (!mbar_try_wait(bar, parity)) {
+    if (clock64() - t0 > kWaitLimitCycles) {
+      gave_up();
+      return false;
+    }
+  }
   return true;
+}
+__device__ __forceinline__ bool row_wait(uint64_t* bar, uint32_t parity) {
+  return row_wait(bar, parity, [] {});
 }
 
 // Two fp32 in one 64-bit register: Blackwell multiplies and adds them with one

@@ -381,7 +381,8 @@ int grpo_launch_timing_read(grpo_kernel_time* out, int capacity, int* count);
  * asynchronous on `stream`, allocate nothing, and can be captured in a graph.
  * Rows that do not start on 16 bytes are read with the 16 bytes around their
  * ends. A wait for a copy that runs out (about a second) leaves NaN in the row
- * and in the weight gradients.
+ * and in the rows that its CTA has still to do: in y, mean and rstd, in what did
+ * not arrive of z and its checkpoint, in dx and in the weight gradients.
  * ------------------------------------------------------------------------- */
 #define GRPO_DTYPE_BF16 0
 #define GRPO_DTYPE_FP16 1
@@ -484,9 +485,10 @@ int grpo_ckpt_wgrad(const void* dy, const void* ckpt, const float* add_or_null, 
                     int64_t dy_stride, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Self-test of what these calls do when a copy never arrives: the calling
- * thread's next grpo_ckpt_wgrad does not issue its first CTA's copy of the
- * 64-token stage `index` (counted over the stages of that CTA's tiles). The wait
- * for it runs out after about a second, the kernel gives up the work that
+ * thread's next grpo_norm_fwd copies neither row `index` nor what its CTA has to
+ * do after it, or its next grpo_ckpt_wgrad does not copy the 64-token stage
+ * `index` (counted over the stages of the first CTA's tiles) to that CTA. The
+ * wait for it runs out after about a second, the kernel gives up the work that
  * depends on it (NaN in its place), lets the copies in flight land and returns;
  * the context stays usable. -1: nothing is left out. */
 int grpo_selftest_lose_copy(int64_t index);

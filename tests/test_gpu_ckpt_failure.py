@@ -82,3 +82,38 @@ def test_wgrad_leaves_nan_and_nothing_stale(clp, n, out, d, stage, lost, add):
     assert int(nan.all(1).sum()) == lost
     keep = ~nan.any(1)
     assert torch.equal(got[keep], want[keep])
+
+
+def _rows_or_nan(got, want, lost):
+    """Every row is `want`'s or NaN throughout, row `lost` NaN; which are NaN."""
+    got, want = got.float().reshape(len(got), -1), want.float().reshape(len(want), -1)
+    nan = torch.isnan(got)
+    assert torch.equal(nan.any(1), nan.all(1))
+    keep = ~nan.all(1)
+    assert torch.equal(got[keep], want[keep])
+    assert not keep[lost]
+    return nan.all(1)
+
+
+# Several rows a CTA, one row a CTA, and rows that do not start on 16 bytes.
+@pytest.mark.parametrize("d", [512, 1001, 4096, 8200, 16384])
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+def test_norm_forward_leaves_nan(clp, d, kind):
+    n, lost = 2000, 5
+    g = torch.Generator().manual_seed(d)
+    x, r = (torch.randn(n, d, generator=g).to(DEV, torch.bfloat16) for _ in range(2))
+    w = torch.ones(d, dtype=torch.bfloat16, device=DEV)
+    want = clp.grpo_norm_fwd(x, w, residual=r, kind=kind, want_ckpt=True)
+    z = torch.full_like(x, 7.0)
+    ckpt = clp.Checkpoint8(torch.zeros_like(want.ckpt.data), n, d)
+    clp.grpo_selftest_lose_copy(lost)
+    got = clp.grpo_norm_fwd(x, w, residual=r, kind=kind, z=z, ckpt=ckpt)
+    torch.cuda.synchronize()
+    nan = _rows_or_nan(got.y, want.y, lost)
+    assert int(nan.sum()) < n // 20  # one CTA's rows
+    for a, b in ((got.z, want.z), (got.rstd, want.rstd), (ckpt.q.float(), want.ckpt.q.float())):
+        assert torch.equal(_rows_or_nan(a, b, lost), nan)
+    if kind == "layer":
+        assert torch.equal(_rows_or_nan(got.mean, want.mean, lost), nan)
+    again = clp.grpo_norm_fwd(x, w, residual=r, kind=kind)
+    assert torch.equal(again.y, want.y) and torch.equal(again.z, want.z)
