@@ -430,7 +430,8 @@ def grpo_ckpt_wgrad(dy, ckpt, *, add=None, dW=None, workspace=None) -> torch.Ten
 
 
 def grpo_selftest_lose_copy(index: int) -> None:
-    """This thread's next ``grpo_norm_fwd`` leaves out the copies of row ``index`` and
-    of its CTA's later rows, or its next ``grpo_ckpt_wgrad`` that of its first CTA's
-    64-token stage ``index`` (-1: none); the call gives up after about a second."""
+    """This thread's next ``grpo_norm_fwd`` or ``grpo_norm_bwd`` leaves out the copies
+    of row ``index`` and of its CTA's later rows, or its next ``grpo_ckpt_wgrad``
+    that of its first CTA's 64-token stage ``index`` (-1: none). The call gives up
+    after about a second."""
     _raise(lib.grpo_selftest_lose_copy(int(index)), "grpo_selftest_lose_copy")

@@ -58,6 +58,7 @@ struct NormBwdArgs {
   float* partials;  // [rows of partials][d], those of dbias behind them
   long long n, lddy, ldx, lddres, lddx;
   int d, wtype, kind;
+  uint32_t lost;  // as above (where two CTAs share a row: the first)
 };
 
 struct CkptArgs {

@@ -194,6 +194,7 @@ int grpo_norm_bwd(const void* dy, const void* x, const void* ckpt, const void* w
   a.d = desc->hidden;
   a.wtype = desc->weight_dtype;
   a.kind = desc->kind;
+  a.lost = take_lost();
   const bool vec = rows_on_16(rows, 4, desc->hidden, desc->dtype);
   return launch_norm_bwd(a, desc->dtype, vec, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? GRPO_OK

@@ -70,11 +70,12 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_kernel(const NormBwdArg
   const long long step = static_cast<long long>(blks) * blockDim.y;
   const long long row0 = static_cast<long long>(blk) * blockDim.y + g;
   const int count = row_count(row0, a.n, step);
+  const int fetches = fetch_count(count, row0, step, rank == 0 ? a.lost : kNoneLost);
   const uint8_t* const mask = a.mask;
   uint32_t pending = 0;
   int fetched = 0;
   const auto fetch = [&](int slot) {
-    if (fetched >= count) return;
+    if (fetched >= fetches) return;
     const long long r = row0 + step * fetched++;
     if (mask != nullptr && mask[r] == 0) return;
     pending |= 1u << slot;
@@ -128,6 +129,7 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_kernel(const NormBwdArg
   int phase = 0, slot = 0;
   uint32_t parity = 0;
   bool ok = true;
+  bool heard = true;  // the peer's sums have come so far
   bool live = count > 0 && (mask == nullptr || mask[row0] != 0);
   float rstd1 = live ? a.rstd[row0] : 0.f;
   float mean1 = live && layer ? a.mean[row0] : 0.f;
@@ -180,28 +182,31 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_kernel(const NormBwdArg
         }
       }
       float s[FULL ? 2 : 1];
-      s[0] = warp_sum(sum_of(suh));
+      // A thread whose copy did not come has NaN: so has then all of the row's dx.
+      s[0] = warp_sum(ok ? sum_of(suh) : kNaN);
       if (FULL) s[FULL ? 1 : 0] = warp_sum(sum_of(su));
       join_warps(s, t, warps, g + 1, red[g], phase);
       if (t == 0 && ok) fetch(slot);
       __syncwarp();
       if (halved) {
         // Tell the peer, and wait for its part (two places in turn: it cannot
-        // be two rows ahead). Both add in the same order.
+        // be two rows ahead). Both add in the same order. This goes on when a
+        // copy did not come, or the CTAs would lose count of each other: a row
+        // then takes the peer up to kWaitLimitCycles, and this waits longer.
         const uint32_t b = swaps & 1u;
         if (t == 0) {
-          mbar_arrive_expect_tx(&sums_bar[b], 8);
+          if (heard) mbar_arrive_expect_tx(&sums_bar[b], 8);
           send_sums(smem_u32(&peer_sums[b][0]), smem_u32(&sums_bar[b]), rank ^ 1u, s[0],
                     FULL ? s[FULL ? 1 : 0] : 0.f);
         }
-        ok = ok && row_wait(&sums_bar[b], (swaps >> 1) & 1u);
+        heard = heard && row_wait(&sums_bar[b], (swaps >> 1) & 1u, [] {}, 4 * kWaitLimitCycles);
         ++swaps;
 #pragma unroll
         for (int k = 0; k < (FULL ? 2 : 1); ++k)
           s[k] = rank == 0 ? s[k] + peer_sums[b][k] : peer_sums[b][k] + s[k];
       }
       const float c1 = layer ? s[FULL ? 1 : 0] * inv_d : 0.f;
-      const float c2 = ok ? s[0] * inv_d : __uint_as_float(0x7fc00000u);
+      const float c2 = heard ? s[0] * inv_d : kNaN;
       const f32x2 n1 = pair(-c1, -c1), n2 = pair(-c2, -c2);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
@@ -215,15 +220,6 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_kernel(const NormBwdArg
         }
         store_chunk<T, VEC>(dx, narrow2<T>(u[c]), c, t, tpr, d);
       }
-      if (!ok) {
-#pragma unroll
-        for (int c = 0; c < CH; ++c)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            dw[c][j] = ~0ull;  // NaN
-            if (FULL) db[FULL ? c : 0][j] = ~0ull;
-          }
-      }
     }
     if (++slot == ring.slots) slot = 0;
     dx += step * a.lddx;
@@ -231,7 +227,21 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_kernel(const NormBwdArg
   }
   land(bars, ring.slots, parity, pending);
   __syncwarp();
-  if (halved) cluster_sync();  // nothing more arrives from the peer
+  if (halved) {
+    cluster_sync();  // nothing more arrives from the peer
+    if (!heard)      // or what it sent last is on its way: half a millisecond
+      for (const long long t0 = clock64(); clock64() - t0 < (1 << 20);) {
+      }
+  }
+  if (!ok) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        dw[c][j] = ~0ull;  // NaN
+        if (FULL) db[FULL ? c : 0][j] = ~0ull;
+      }
+  }
   const bool want_db = FULL && a.dbias != nullptr;
   if (a.dweight == nullptr && !want_db) return;
   // The CTA's rows in flight, added in their order; the rings have been read.

@@ -175,11 +175,12 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 // Waits for a phase of `bar`; false after about a second, then after `gave_up()`
 // (no status word here: the caller gives NaN).
 template <typename F>
-__device__ __forceinline__ bool row_wait(uint64_t* bar, uint32_t parity, F gave_up) {
+__device__ __forceinline__ bool row_wait(uint64_t* bar, uint32_t parity, F gave_up,
+                                         long long limit = kWaitLimitCycles) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   while (!mbar_try_wait(bar, parity)) {
-    if (clock64() - t0 > kWaitLimitCycles) {
+    if (clock64() - t0 > limit) {
       gave_up();
       return false;
     }

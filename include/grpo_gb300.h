@@ -382,7 +382,8 @@ int grpo_launch_timing_read(grpo_kernel_time* out, int capacity, int* count);
  * Rows that do not start on 16 bytes are read with the 16 bytes around their
  * ends. A wait for a copy that runs out (about a second) leaves NaN in the row
  * and in the rows that its CTA has still to do: in y, mean and rstd, in what did
- * not arrive of z and its checkpoint, in dx and in the weight gradients.
+ * not arrive of z and its checkpoint, in dx, and in the columns of the weight
+ * gradients that lack them.
  * ------------------------------------------------------------------------- */
 #define GRPO_DTYPE_BF16 0
 #define GRPO_DTYPE_FP16 1
@@ -485,8 +486,8 @@ int grpo_ckpt_wgrad(const void* dy, const void* ckpt, const float* add_or_null, 
                     int64_t dy_stride, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Self-test of what these calls do when a copy never arrives: the calling
- * thread's next grpo_norm_fwd copies neither row `index` nor what its CTA has to
- * do after it, or its next grpo_ckpt_wgrad does not copy the 64-token stage
+ * thread's next grpo_norm_fwd or grpo_norm_bwd copies neither row `index` nor what
+ * its CTA has to do after it (where two CTAs share a row: the first of them), or its next grpo_ckpt_wgrad does not copy the 64-token stage
  * `index` (counted over the stages of the first CTA's tiles) to that CTA. The
  * wait for it runs out after about a second, the kernel gives up the work that
  * depends on it (NaN in its place), lets the copies in flight land and returns;
