@@ -207,8 +207,20 @@ def _check(t, name, dtype, shape, device):
         raise ValueError(f"{name}: must be contiguous")
 
 
-def _stream(device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def call_on(device, fn, *args):
+    """fn(*args, stream) with the tensors' device current, and the stream that is
+    current on it: the library launches on the device that it finds current."""
+    index = device.index
+    if index is None:  # a tensor's CUDA device has one
+        raise ValueError(f"expected tensors on a CUDA device, got {device}")
+    if index == _current_device():
+        return fn(*args, _raw_stream(index))
+    with torch.cuda.device(device):
+        return fn(*args, _raw_stream(index))
 
 
 def alloc_workspace(n_tokens, hidden, vocab, seq_len=1, params=None, device=None) -> torch.Tensor:
@@ -232,10 +244,9 @@ def grpo_logp_fwd(hidden, W, ids, *, params: GrpoParams | None = None, workspace
     if workspace is None:
         workspace = alloc_workspace(N, D, V, 1, params, dev)
     shape = make_shape(N, 1, D, V)
-    rc = lib.grpo_logp_fwd(_ptr(hidden), _ptr(W), _ptr(ids), _ptr(logp), _ptr(lse),
-                           ctypes.byref(shape),
-                           ctypes.byref(params) if params is not None else None,
-                           _ptr(workspace), workspace.numel(), _stream(dev))
+    rc = call_on(dev, lib.grpo_logp_fwd, _ptr(hidden), _ptr(W), _ptr(ids), _ptr(logp), _ptr(lse),
+                 ctypes.byref(shape), ctypes.byref(params) if params is not None else None,
+                 _ptr(workspace), workspace.numel())
     if rc != GRPO_OK:
         raise GrpoError(rc, "grpo_logp_fwd")
     return logp, lse
@@ -275,11 +286,11 @@ def grpo_loss_fwd_bwd(hidden, W, ids, mask, old_logp, ref_logp, adv, seq_len, *,
     if workspace is None:
         workspace = alloc_workspace(N, D, V, seq_len, params, dev)
     shape = make_shape(N, seq_len, D, V)
-    rc = lib.grpo_loss_fwd_bwd(_ptr(hidden), _ptr(W), _ptr(ids), _ptr(mask), _ptr(old_logp),
-                               _ptr(ref_logp), _ptr(adv), _ptr(loss), _ptr(logp), _ptr(dH),
-                               _ptr(dW), ctypes.byref(shape),
-                               ctypes.byref(params) if params is not None else None,
-                               _ptr(workspace), workspace.numel(), _stream(dev))
+    rc = call_on(dev, lib.grpo_loss_fwd_bwd, _ptr(hidden), _ptr(W), _ptr(ids), _ptr(mask),
+                 _ptr(old_logp), _ptr(ref_logp), _ptr(adv), _ptr(loss), _ptr(logp), _ptr(dH),
+                 _ptr(dW), ctypes.byref(shape),
+                 ctypes.byref(params) if params is not None else None,
+                 _ptr(workspace), workspace.numel())
     if rc != GRPO_OK:
         raise GrpoError(rc, "grpo_loss_fwd_bwd")
     if dW is not None:
@@ -289,8 +300,7 @@ def grpo_loss_fwd_bwd(hidden, W, ids, mask, old_logp, ref_logp, adv, seq_len, *,
 
 def grpo_read_device_status(workspace) -> int:
     st = ctypes.c_int(0)
-    rc = lib.grpo_read_device_status(_ptr(workspace), ctypes.byref(st),
-                                     _stream(workspace.device))
+    rc = call_on(workspace.device, lib.grpo_read_device_status, _ptr(workspace), ctypes.byref(st))
     if rc != GRPO_OK:
         raise GrpoError(rc, "grpo_read_device_status")
     return int(st.value)
@@ -313,8 +323,8 @@ def grpo_logp_fwd_noalloc(hidden, W, ids, logp, lse=None):
     if lse is not None:
         _check(lse, "lse", torch.float32, (N,), dev)
     shape = make_shape(N, 1, D, V)
-    rc = lib.grpo_logp_fwd_noalloc(_ptr(hidden), _ptr(W), _ptr(ids), _ptr(logp), _ptr(lse),
-                                   ctypes.byref(shape), _stream(dev))
+    rc = call_on(dev, lib.grpo_logp_fwd_noalloc, _ptr(hidden), _ptr(W), _ptr(ids), _ptr(logp),
+                 _ptr(lse), ctypes.byref(shape))
     if rc != GRPO_OK:
         raise GrpoError(rc, "grpo_logp_fwd_noalloc")
     return logp, lse
@@ -322,8 +332,8 @@ def grpo_logp_fwd_noalloc(hidden, W, ids, logp, lse=None):
 
 def grpo_selftest_bounded_wait(workspace) -> int:
     """Runs the bounded-wait self-test; returns the device status it left (-7 expected)."""
-    rc = lib.grpo_selftest_bounded_wait(_ptr(workspace), workspace.numel(),
-                                        _stream(workspace.device))
+    rc = call_on(workspace.device, lib.grpo_selftest_bounded_wait, _ptr(workspace),
+                 workspace.numel())
     if rc != GRPO_OK:
         raise GrpoError(rc, "grpo_selftest_bounded_wait")
     return grpo_read_device_status(workspace)

@@ -17,7 +17,7 @@ from typing import NamedTuple
 
 import torch
 
-from ._binding import GRPO_OK, GrpoError, GrpoNormDesc, lib
+from ._binding import GRPO_OK, GrpoError, GrpoNormDesc, call_on, lib
 
 _F32 = torch.float32
 _U8 = torch.uint8
@@ -25,7 +25,6 @@ _BF16 = torch.bfloat16
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _KINDS = {"layer": 0, "rms": 1}
 _byref = ctypes.byref
-_raw_stream = torch._C._cuda_getCurrentRawStream
 _empty, _empty_like = torch.empty, torch.empty_like
 
 
@@ -147,12 +146,6 @@ def _like(t, stride):
     return _empty_like(t) if stride == 0 else _empty(t.shape, dtype=t.dtype, device=t.device)
 
 
-def _stream_of(device):
-    if device.type != "cuda":
-        raise ValueError(f"expected tensors on a CUDA device, got {device}")
-    return _raw_stream(device.index)
-
-
 @lru_cache(maxsize=512)
 def _ckpt_layout(n, d):
     """(bytes from row to row of q, where the exponents begin, bytes from row to
@@ -251,8 +244,8 @@ def grpo_norm_fwd(x, weight=None, bias=None, *, residual=None, kind="rms", eps=1
     elif ckpt is not None:
         pc = _ckpt(ckpt, n, d, dev)
     desc = GrpoNormDesc(n, d, code, wt, k, eps, 0, sx, sr, sy, sz)
-    rc = lib.grpo_norm_fwd(x.data_ptr(), pr, pw, pb, pmask, y.data_ptr(), pz, pm, ps, pc,
-                           _byref(desc), _stream_of(dev))
+    rc = call_on(dev, lib.grpo_norm_fwd, x.data_ptr(), pr, pw, pb, pmask, y.data_ptr(), pz, pm, ps,
+                 pc, _byref(desc))
     if rc:
         raise GrpoError(rc, "grpo_norm_fwd")
     return NormForward(y, x if residual is None else z, mean, rstd, ckpt)
@@ -337,8 +330,8 @@ def grpo_norm_bwd(dy, x, weight, mean, rstd, *, dres=None, kind="rms", mask=None
             raise ValueError(f"workspace: expected device {dev}, got {workspace.device}")
         pws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     desc = GrpoNormDesc(n, d, code, wt, k, 0.0, 0, sx, 0, 0, 0, sdy, sr, sdx)
-    rc = lib.grpo_norm_bwd(dy.data_ptr(), px, pc, pw, pmean, ps, pmask, pr, dx.data_ptr(), pdw, pdb,
-                           paw, pab, _byref(desc), pws, ws_bytes, _stream_of(dev))
+    rc = call_on(dev, lib.grpo_norm_bwd, dy.data_ptr(), px, pc, pw, pmean, ps, pmask, pr,
+                 dx.data_ptr(), pdw, pdb, paw, pab, _byref(desc), pws, ws_bytes)
     if rc:
         raise GrpoError(rc, "grpo_norm_bwd")
     return NormBackward(dx, dweight, dbias)
@@ -356,7 +349,7 @@ def grpo_ckpt_pack(x, *, mask=None, ckpt=None) -> Checkpoint8:
         pc = ckpt.data.data_ptr()
     else:
         pc = _ckpt(ckpt, n, d, dev)
-    rc = lib.grpo_ckpt_pack(x.data_ptr(), pmask, pc, n, d, code, sx, _stream_of(dev))
+    rc = call_on(dev, lib.grpo_ckpt_pack, x.data_ptr(), pmask, pc, n, d, code, sx)
     if rc:
         raise GrpoError(rc, "grpo_ckpt_pack")
     return ckpt
@@ -378,7 +371,7 @@ def grpo_ckpt_unpack(ckpt, dtype=torch.bfloat16, *, out=None) -> torch.Tensor:
         out = _empty(shape, dtype=dtype, device=dev)
     else:
         so = _rows(out, "out", dtype, shape, dev)
-    rc = lib.grpo_ckpt_unpack(pc, out.data_ptr(), n, d, code, so, _stream_of(dev))
+    rc = call_on(dev, lib.grpo_ckpt_unpack, pc, out.data_ptr(), n, d, code, so)
     if rc:
         raise GrpoError(rc, "grpo_ckpt_unpack")
     return out
@@ -422,8 +415,8 @@ def grpo_ckpt_wgrad(dy, ckpt, *, add=None, dW=None, workspace=None) -> torch.Ten
         workspace = _empty(_wgrad_workspace(n, out, d), dtype=_U8, device=dev)
     elif workspace.device != dev:
         raise ValueError(f"workspace: expected device {dev}, got {workspace.device}")
-    rc = lib.grpo_ckpt_wgrad(dy.data_ptr(), pc, pa, pdw, n, out, d, sdy, workspace.data_ptr(),
-                             workspace.numel() * workspace.element_size(), _stream_of(dev))
+    rc = call_on(dev, lib.grpo_ckpt_wgrad, dy.data_ptr(), pc, pa, pdw, n, out, d, sdy,
+                 workspace.data_ptr(), workspace.numel() * workspace.element_size())
     if rc:
         raise GrpoError(rc, "grpo_ckpt_wgrad")
     return dW
