@@ -14,6 +14,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "grpo_gb300.h"
+#include "kernel_fit.h"
 #include "launch.h"
 
 namespace grpo {
@@ -40,7 +41,6 @@ constexpr int kSplitsTarget = 8;        // forward vocab splits per raster group
 // the sizing without a device and for the call's own plan.
 constexpr int kRefSms = 152;
 constexpr size_t kHeaderBytes = 16384;   // status, counters, loss partials
-constexpr int kMaxDevices = 64;
 
 // Workspace header layout.
 constexpr size_t kOffStatus = 0;       // int

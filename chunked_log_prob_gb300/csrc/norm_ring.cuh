@@ -3,8 +3,8 @@
 #pragma once
 
 #include <algorithm>
-#include <atomic>
 
+#include "kernel_fit.h"
 #include "launch.h"
 #include "norm.h"
 #include "row_ops.cuh"
@@ -111,27 +111,22 @@ Ring make_ring(uint32_t row_bytes, int rows, size_t fixed) {
   return r;
 }
 
-// Opts a kernel in to large shared memory, once.
-template <auto Kernel>
-bool opted_in() {
-  static const bool ok = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                              static_cast<int>(kSmemMax)) == cudaSuccess;
-  return ok;
-}
-
-// CTAs of a kernel that fit an SM; the last answer is kept for calls of one shape.
+// CTAs of a kernel that fit an SM of the current device, which is opted in to
+// large shared memory for it first. What was found is kept for each device.
 template <auto Kernel>
 cudaError_t ctas_per_sm(int threads, size_t smem, int* n) {
-  static std::atomic<uint64_t> last{0};
-  const uint64_t key = (static_cast<uint64_t>(smem) << 24) | (static_cast<uint64_t>(threads) << 8);
-  const uint64_t seen = last.load(std::memory_order_relaxed);
-  if (seen != 0 && (seen & ~uint64_t{0xff}) == key) {
-    *n = static_cast<int>(seen & 0xff);
-    return cudaSuccess;
+  static KernelFit fit;
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess || fit.find(device, threads, smem, n)) return e;
+  if (!fit.opted_in(device)) {
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kSmemMax));
+    if (e != cudaSuccess) return e;
+    fit.set_opted_in(device);
   }
-  if (!opted_in<Kernel>()) return cudaErrorInvalidValue;
-  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, Kernel, threads, smem);
-  if (e == cudaSuccess) last.store(key | static_cast<uint64_t>(*n), std::memory_order_relaxed);
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, Kernel, threads, smem);
+  if (e == cudaSuccess) fit.keep(device, threads, smem, *n);
   return e;
 }
 

@@ -1,6 +1,8 @@
 """Host-side checks of the norm and checkpoint calls' bookkeeping (CPU)."""
 
 import contextlib
+import os
+import subprocess
 
 import pytest
 import torch
@@ -104,3 +106,68 @@ def test_every_launching_call_goes_to_the_tensors_device(clp, monkeypatch):
         call()
         assert seen.pop() == ("cpu", name)
         assert not seen
+
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                    "chunked_log_prob_gb300", "csrc")
+
+
+def run_cpp(tmp_path, source):
+    """Compiles and runs a program of the host headers; fails on a nonzero exit."""
+    src, exe = tmp_path / "t.cpp", tmp_path / "t"
+    src.write_text(source)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-pthread", "-I", CSRC,
+                    str(src), "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+    return r.stdout
+
+
+def test_what_is_kept_of_a_kernel_holds_for_its_device_only(tmp_path):
+    run_cpp(tmp_path, r"""
+#include <cstdio>
+#include <thread>
+#include "kernel_fit.h"
+using grpo::KernelFit;
+#define NEED(x) do { if (!(x)) { std::printf("line %d: %s\n", __LINE__, #x); return 1; } } while (0)
+int main() {
+  static KernelFit f;
+  int n = -1;
+  NEED(!f.opted_in(0) && !f.find(0, 512, 65536, &n));
+  f.set_opted_in(0);
+  f.keep(0, 512, 65536, 3);
+  NEED(f.opted_in(0) && f.find(0, 512, 65536, &n) && n == 3);
+  // Another device: neither the opt-in nor the answer.
+  NEED(!f.opted_in(1) && !f.find(1, 512, 65536, &n));
+  f.keep(1, 512, 65536, 2);
+  NEED(f.find(0, 512, 65536, &n) && n == 3);
+  NEED(f.find(1, 512, 65536, &n) && n == 2);
+  NEED(!f.opted_in(1));
+  // Another shape of the launch.
+  NEED(!f.find(0, 256, 65536, &n) && !f.find(0, 512, 65552, &n));
+  f.keep(0, 1024, 232448, 0);
+  NEED(f.find(0, 1024, 232448, &n) && n == 0 && !f.find(0, 512, 65536, &n));
+  // Devices out of range keep nothing; a count too large for its byte neither.
+  f.keep(-1, 512, 65536, 3);
+  f.keep(grpo::kMaxDevices, 512, 65536, 3);
+  f.set_opted_in(grpo::kMaxDevices);
+  f.keep(2, 512, 65536, 256);
+  NEED(!f.find(-1, 512, 65536, &n) && !f.find(grpo::kMaxDevices, 512, 65536, &n));
+  NEED(!f.opted_in(grpo::kMaxDevices) && !f.find(2, 512, 65536, &n));
+  // Threads that keep different shapes: what is found belongs to its shape.
+  int wrong[4] = {};
+  std::thread t[4];
+  for (int k = 0; k < 4; ++k)
+    t[k] = std::thread([&, k] {
+      for (int i = 0; i < 200000; ++i) {
+        const int threads = 32 * (1 + (i + k) % 5);
+        int got = 0;
+        f.keep(3, threads, 1024, threads / 32);
+        if (f.find(3, 32 * (1 + i % 5), 1024, &got) && got != 1 + i % 5) ++wrong[k];
+      }
+    });
+  for (auto& x : t) x.join();
+  NEED(wrong[0] + wrong[1] + wrong[2] + wrong[3] == 0);
+  return 0;
+}
+""")
