@@ -26,13 +26,11 @@
 #include "launch.h"
 #include "norm.h"
 #include "row_ops.cuh"
+#include "wgrad_plan.h"
 
 namespace grpo {
 namespace {
 
-constexpr int kTileM = 256;        // outputs of a pair's tile, 128 per CTA
-constexpr int kTileN = 256;        // inputs of a pair's tile
-constexpr int kTok = 64;           // tokens of a stage
 // Rings: a slot's way round (barrier to barrier, TMA or widening, the MMAs)
 // takes several stages' MMA time, so each of them is as deep as memory allows.
 constexpr int kDy = 5;             // dY tiles
@@ -68,70 +66,7 @@ constexpr int kSmem = 1024 + (kDy + kX) * kOperand + kRaw * kRawBytes +
                       kEpilogueWarps * kStoreBuf;
 constexpr uint32_t kTmemCols = 512;
 static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
-constexpr int kGroupM = 8;         // tiles are walked 8 row tiles at a time
 constexpr int kSlotFloats = kTileM * kTileN;
-constexpr int kRefPairs = 76;      // GB300's SM pairs
-
-// The work of a launch, in stages of kTok tokens. Tiles are dealt whole, one to
-// a pair and round, except the last round's `cut` tiles when they fill it
-// badly: their stages are dealt evenly, `per_pair` in a row to each pair, and
-// a second kernel adds the pieces of a tile in the order of its tokens.
-struct WgradPlan {
-  int n_m, n_n, kt;
-  int whole;     // tiles dealt whole
-  int cut;       // tiles dealt in pieces
-  int per_pair;  // stages of a pair's part of them
-};
-
-struct Item {
-  int tile, kb, ke;
-  int slot;  // partial tile to write, -1: the tile itself
-};
-
-// 32 bits hold every count: fewer than kRefPairs tiles are cut, of at most 2^24
-// stages each.
-struct WorkList {
-  int i = 0, pos = -1, end = 0;
-  __device__ __forceinline__ bool next(const WgradPlan& p, int pair, int pairs, Item& it) {
-    if (pos < 0) {
-      it.tile = pair + i++ * pairs;
-      if (it.tile < p.whole) {
-        it.kb = 0;
-        it.ke = p.kt;
-        it.slot = -1;
-        return true;
-      }
-      const int all = p.cut * p.kt;
-      pos = min(pair * p.per_pair, all);
-      end = min(pos + p.per_pair, all);
-      i = 0;
-    }
-    if (pos >= end) return false;
-    const int t = static_cast<int>(static_cast<unsigned>(pos) / static_cast<unsigned>(p.kt));
-    it.tile = p.whole + t;
-    it.kb = pos - t * p.kt;
-    it.ke = min(p.kt, it.kb + (end - pos));
-    it.slot = it.ke - it.kb == p.kt ? -1 : 2 * pair + i;
-    ++i;
-    pos += it.ke - it.kb;
-    return true;
-  }
-};
-
-// Row and column of a tile: column by column within kGroupM row tiles, so that
-// the tiles of a round share both operands in L2.
-__device__ __forceinline__ void tile_place(const WgradPlan& p, int tile, int& m, int& n) {
-  const int per_group = kGroupM * p.n_n;
-  const int g = tile / per_group, r = tile - g * per_group;
-  const int rows = min(kGroupM, p.n_m - g * kGroupM);
-  n = r / rows;
-  m = g * kGroupM + (r - n * rows);
-}
-
-// Inputs of a tile: 256, or 128 where no more are left.
-__device__ __forceinline__ int tile_cols(int in, int n) {
-  return in - n * kTileN <= kTileN / 2 ? kTileN / 2 : kTileN;
-}
 
 __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
   const long long t0 = clock64();
@@ -285,8 +220,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = tmem_base_sh;
 
-  WorkList work;
-  Item it;
+  WgradWork work;
+  WgradItem it;
   bool ok = true;
 
   // Each role moves its registers inside its own branch: the compiler holds what
@@ -603,9 +538,7 @@ __global__ void __launch_bounds__(kTileM) ckpt_wgrad_join_kernel(const WgradArgs
   constexpr int kRows = kTileM / G;
   __shared__ float4 part[G > 1 ? G : 1][G > 1 ? 4 : 1][G > 1 ? kRows : 1];
   const int t = static_cast<int>(blockIdx.x);
-  const int first = t * plan.kt;
-  const int qa = first / plan.per_pair;
-  const int qb = (first + plan.kt - 1) / plan.per_pair;  // > qa: a part is shorter than a tile
+  const int qa = first_piece(plan, t), qb = last_piece(plan, t);
   int tm, tn;
   tile_place(plan, plan.whole + t, tm, tn);
   const int r = static_cast<int>(threadIdx.x) % kRows, g = static_cast<int>(threadIdx.x) / kRows;
@@ -621,9 +554,7 @@ __global__ void __launch_bounds__(kTileM) ckpt_wgrad_join_kernel(const WgradArgs
   if (valid) {
 #pragma unroll 4
     for (int q = qa + g; q <= qb; q += G) {
-      // A pair's second piece begins with its tile; its first one does not, or
-      // is the first of the pair's part.
-      const int slot = 2 * q + (q * plan.per_pair < first ? 1 : 0);
+      const int slot = piece_slot(plan, t, q);
       const float* p = args.partials + static_cast<long long>(slot) * kSlotFloats +
                        (c0 / 4 * kTileM + lrow) * 4;
 #pragma unroll
@@ -666,33 +597,10 @@ __global__ void __launch_bounds__(kTileM) ckpt_wgrad_join_kernel(const WgradArgs
   }
 }
 
-// A launch on `pairs` SM pairs.
-WgradPlan make_plan(long long n, int out, int in, int pairs) {
-  WgradPlan p;
-  p.n_m = (out + kTileM - 1) / kTileM;
-  p.n_n = (in + kTileN - 1) / kTileN;
-  p.kt = static_cast<int>((n + kTok - 1) / kTok);
-  const int tiles = p.n_m * p.n_n;
-  p.cut = tiles % pairs;
-  // Cut the last round's tiles when that saves at least kMinSaved stages of
-  // its length, in pieces of at least kMinPiece.
-  constexpr int kMinSaved = 24, kMinPiece = 8;
-  p.per_pair = 0;
-  if (p.cut > 0) {
-    const long long stages = static_cast<long long>(p.cut) * p.kt;
-    p.per_pair = static_cast<int>(std::max<long long>(kMinPiece, (stages + pairs - 1) / pairs));
-    if (p.kt - p.per_pair < kMinSaved) p.cut = 0;
-  }
-  if (p.cut == 0) p.per_pair = 0;
-  p.whole = tiles - p.cut;
-  return p;
-}
-
 }  // namespace
 
 size_t ckpt_wgrad_workspace(long long n, int out, int in) {
-  const WgradPlan p = make_plan(n, out, in, kRefPairs);
-  return 256 + (p.cut > 0 ? static_cast<size_t>(2) * kRefPairs * kSlotFloats * sizeof(float) : 0);
+  return 256 + partial_tiles(n, out, in) * kSlotFloats * sizeof(float);
 }
 
 cudaError_t prepare_ckpt_wgrad() {
@@ -702,7 +610,6 @@ cudaError_t prepare_ckpt_wgrad() {
 
 cudaError_t launch_ckpt_wgrad(const WgradArgs& a, int sms, cudaStream_t st) {
   const int pairs = std::min(sms / 2, kRefPairs);
-  if (pairs < kRefPairs) return cudaErrorNotSupported;  // the workspace's plan is for 76 pairs
   CUtensorMap map_dy, map_q, map_ex, map_dw;
   if (!encode_map_2d(&map_dy, a.dy, a.out, a.n, a.lddy * 2, 64, kTok,
                      CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B) ||
@@ -714,13 +621,8 @@ cudaError_t launch_ckpt_wgrad(const WgradArgs& a, int sms, cudaStream_t st) {
                      CU_TENSOR_MAP_DATA_TYPE_FLOAT32, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
   const WgradPlan plan = make_plan(a.n, a.out, a.in, pairs);
-  const long long stages = static_cast<long long>(plan.cut) * plan.kt;
-  const int busy = std::max(
-      std::min(plan.whole, pairs),
-      plan.per_pair > 0 ? static_cast<int>((stages + plan.per_pair - 1) / plan.per_pair) : 0);
   cudaLaunchConfig_t cfg = {};
-  // Whole tiles are dealt to `pairs` pairs: fewer only when one round holds all.
-  cfg.gridDim = dim3(2 * (plan.whole > pairs ? pairs : busy));
+  cfg.gridDim = dim3(2 * launch_pairs(plan, pairs));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;

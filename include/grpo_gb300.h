@@ -474,7 +474,7 @@ int grpo_ckpt_unpack(const void* ckpt, void* x, int64_t n_tokens, int32_t hidden
  *   add_or_null: fp32, like dW, may be dW itself; NULL = 0
  * out_features, in_features and dy_stride are multiples of 8; dY, dW and add
  * start on 16 bytes. X is exact in bf16, products are exact, sums are fp32 in
- * an order fixed by the sizes. Masked tokens: pack with the mask and let dY be
+ * an order fixed by the sizes and the device's SM pairs (at most 76). Masked tokens: pack with the mask and let dY be
  * 0 there. The first bytes of the workspace (grpo_ckpt_wgrad_workspace_size,
  * 256-byte aligned) are a status word for grpo_read_device_status. A wait that
  * runs out (about a second) leaves GRPO_ERR_DEVICE_TIMEOUT there, and NaN in the

@@ -171,3 +171,73 @@ int main() {
   return 0;
 }
 """)
+
+
+def test_wgrad_work_is_dealt_once_on_any_number_of_pairs(tmp_path):
+    # Every stage of every tile is some pair's, once; the pieces of a cut tile lie
+    # in their own partial tiles of the workspace, where the join looks for them.
+    out = run_cpp(tmp_path, r"""
+#include <cstdio>
+#include <random>
+#include <set>
+#include <vector>
+#include "wgrad_plan.h"
+using namespace grpo;
+static int check(long long n, int out, int in, int pairs, int& cuts) {
+  const WgradPlan p = make_plan(n, out, in, pairs);
+  const int tiles = p.n_m * p.n_n, grid = launch_pairs(p, pairs);
+  if (p.whole + p.cut != tiles || grid < 1 || grid > pairs) return 1;
+  cuts += p.cut > 0;
+  std::vector<std::vector<int>> seen(tiles, std::vector<int>(p.kt, 0));
+  std::vector<std::set<int>> slots(tiles);
+  std::set<int> used;
+  for (int q = 0; q < grid; ++q) {
+    WgradWork w;
+    WgradItem it;
+    while (w.next(p, q, grid, it)) {
+      if (it.tile < 0 || it.tile >= tiles || it.kb < 0 || it.kb >= it.ke || it.ke > p.kt) return 2;
+      for (int k = it.kb; k < it.ke; ++k) seen[it.tile][k]++;
+      if (it.slot < 0) {
+        if (it.kb != 0 || it.ke != p.kt) return 3;
+      } else {
+        if (it.tile < p.whole || !used.insert(it.slot).second) return 4;
+        if (static_cast<size_t>(it.slot) >= partial_tiles(n, out, in)) return 5;
+        slots[it.tile].insert(it.slot);
+      }
+    }
+  }
+  std::set<long long> places;
+  for (int t = 0; t < tiles; ++t) {
+    for (int c : seen[t])
+      if (c != 1) return 6;
+    int m, nn;
+    tile_place(p, t, m, nn);
+    if (m < 0 || m >= p.n_m || nn < 0 || nn >= p.n_n) return 7;
+    if (!places.insert(static_cast<long long>(m) * p.n_n + nn).second) return 8;
+  }
+  for (int t = 0; t < p.cut; ++t) {
+    std::set<int> joined;
+    for (int q = first_piece(p, t); q <= last_piece(p, t); ++q) joined.insert(piece_slot(p, t, q));
+    if (joined != slots[p.whole + t] || joined.size() < 2) return 9;
+  }
+  return 0;
+}
+int main() {
+  std::mt19937 r(1);
+  auto log_int = [&](int bits) { return 1 + static_cast<int>(r() >> (32 - 1 - r() % bits)); };
+  int cuts = 0, cases = 0;
+  for (int pairs : {1, 2, 3, 16, 37, 64, 66, 70, 74, 75, 76})
+    for (int k = 0; k < 300; ++k, ++cases) {
+      const long long n = log_int(17);
+      const int out = log_int(13), in = log_int(13);
+      const int e = check(n, out, in, pairs, cuts);
+      if (e) {
+        std::printf("%d: n %lld out %d in %d pairs %d\n", e, n, out, in, pairs);
+        return 1;
+      }
+    }
+  std::printf("%d %d\n", cases, cuts);
+  return cuts > cases / 20 ? 0 : 2;
+}
+""")
+    assert out.split()[0] == "3300"
