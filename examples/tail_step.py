@@ -8,8 +8,11 @@
     dWp = dz^T a            grpo_ckpt_wgrad, from the checkpoint of a
     da = dz Wp              into the block
 
-Between the forward and the backward pass the step keeps z and a as 1.03 bytes a
-value instead of 2. Run: python examples/tail_step.py (one GB300).
+What the backward passes of the norm and of the linear layer read, z and a, is kept
+as 1.03 bytes a value instead of 2. h stays in bf16 until the loss has read it (that
+call is the head's forward and backward pass in one).
+
+Run: python examples/tail_step.py (one GB300).
 """
 
 from __future__ import annotations
@@ -44,14 +47,15 @@ class StepResult:
     da: torch.Tensor      # gradient of the last block's activation
     dproj: torch.Tensor   # fp32 [D, F]
     dnorm: torch.Tensor   # fp32 [D]
-    kept_bytes: int       # activations held from the forward to the backward pass
+    kept_bytes: int       # checkpoints of z and a, and rstd; h is held besides, up to the loss
 
 
 def tail_step(tail: Tail, x, a, ids, mask, old_logp, ref_logp, adv, seq_len, *, params=None,
               dproj=None, dnorm=None) -> StepResult:
     """Loss and gradients of one batch; dproj and dnorm, where given, are added to
     (in place)."""
-    # Forward: what is kept is a's and z's checkpoints, one rstd a row, and h.
+    # Forward: what is kept is a's and z's checkpoints and one rstd a row; and h,
+    # for the loss.
     keep_a = clp.grpo_ckpt_pack(a, mask=mask)
     fwd = clp.grpo_norm_fwd(x, tail.norm, residual=a @ tail.proj.t(), eps=tail.eps, mask=mask,
                             want_ckpt=True)
@@ -61,6 +65,7 @@ def tail_step(tail: Tail, x, a, ids, mask, old_logp, ref_logp, adv, seq_len, *, 
 
     loss, _, dh = clp.grpo_loss_fwd_bwd(h, tail.head, ids, mask, old_logp, ref_logp, adv, seq_len,
                                         params=params, want_logp=False)
+    del h
     # Backward, from the checkpoints.
     back = clp.grpo_norm_bwd(dh, keep_z, tail.norm, None, rstd, mask=mask, add_dweight=dnorm,
                              dweight=dnorm)
@@ -85,7 +90,7 @@ def main():
     old, _ = clp.grpo_logp_fwd(h, tail.head, ids)
     r = tail_step(tail, x, a, ids, mask, old, old - 0.05, p.adv.to(dev), p.seq_len)
     print(f"loss {r.loss.item():.6f}  |dproj| {r.dproj.norm().item():.4e}  "
-          f"|dnorm| {r.dnorm.norm().item():.4e}  kept {r.kept_bytes / 2**20:.2f} MiB "
+          f"|dnorm| {r.dnorm.norm().item():.4e}  z and a kept in {r.kept_bytes / 2**20:.2f} MiB "
           f"(in bf16 {2 * n * (d + f) / 2**20:.2f})")
 
 
