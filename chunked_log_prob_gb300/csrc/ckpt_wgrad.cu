@@ -16,8 +16,8 @@
 // epilogue warps add each to the tile's running sum in their registers, rounded
 // (4.2e-7 at 16384 tokens).
 //
-// 16384 x 4096 x 4096: 326 us, 1685 TFLOP/s (0.88 of cuBLAS's measured burst), 365
-// us in a row under the power cap. Bound by the tensor cores and, close behind,
+// 16384 x 4096 x 4096: 322 us, 1707 TFLOP/s (0.89 of cuBLAS's measured burst), 353
+// to 368 us in a row under the power cap. Bound by the tensor cores and, close behind,
 // by the widening (a stage of 64 tokens takes the former 512 cycles, measured
 // about 640).
 #include <algorithm>

@@ -73,7 +73,8 @@ struct CkptArgs {
 // No copy is left out (grpo_selftest_lose_copy).
 constexpr uint32_t kNoneLost = 0xffffffffu;
 
-// Largest D of the kernels that hold a whole row in registers.
+// Largest D of the kernels that hold a whole row in registers (forward: of rows on
+// 16 bytes; others up to 8192).
 constexpr int kNormRegisterRow = 16384;
 // Rows of partial weight gradients of one backward call: at most this many.
 constexpr int kNormMaxPartials = 608;

@@ -8,10 +8,13 @@
 //   dw = sum_t dy h, db = sum_t dy
 //
 // Memory bound: about 10 operations per value against 4 to 9 bytes. A row is
-// read once and held in registers (up to 16384 columns); statistics are fp32.
+// read once and held in registers: up to 16384 columns where rows start on 16
+// bytes and shared memory holds one of them beside the parameters (not fp32 of
+// 16384 columns with residual, weight and bias), else up to 8192; longer rows are
+// walked three times. Statistics are fp32.
 // What it took, at 131072 x 2880 in bf16 with residual and checkpoint (3.41 GB):
 // loads into registers one row ahead 1615 us; rows in flight in shared memory
-// 610; pairs of values and 32 of them a thread 520 to 575 (5.9 to 6.6 TB/s, of
+// 610; pairs of values and 32 of them a thread 568 to 580 (5.9 to 6.0 TB/s, of
 // 6.8 measured for a copy; it follows how the five streams meet in DRAM).
 #include <climits>
 
@@ -266,9 +269,12 @@ __global__ void __launch_bounds__(kRingThreads) norm_fwd_kernel(const NormFwdArg
   if (lost[kRingThreads / 32] != INT_MAX) lost_rows<T, VEC, CH>(a, lost);
 }
 
-// Rows beyond kNormRegisterRow columns: the CTA walks over the row three times
-// (sum, centred squares, output); the second and third walk find it in L2. A
-// thread rereads only what it stored itself, so outputs may lie on the inputs.
+// Rows that leave registers (unaligned ones beyond 8192 columns, others beyond
+// kNormRegisterRow, and those that shared memory has no room for): the CTA walks
+// over the row three times (sum, centred squares, output); the second and third
+// walk find it in L2. A thread rereads only what it stored itself, so outputs may
+// lie on the inputs. With residual and checkpoint in bf16: 4096 x 20480 203 us
+// (3.7 TB/s), 4096 x 9001 160 us (2.1), 4096 x 16384 in registers 107 (5.7).
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(512) norm_fwd_long_kernel(const NormFwdArgs a) {
   __shared__ float2 red[2 * 32];
