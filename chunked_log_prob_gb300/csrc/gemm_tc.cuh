@@ -1256,24 +1256,25 @@ __global__ void __launch_bounds__(PairCfg<MODE, CTAS>::kThreads, 1)
         float zc[kPre], zn[kPre];
 #pragma unroll
         for (int j = 0; j < kPre; ++j) zc[j] = box_max_of(wk.kb + j);
-        for (int k0 = wk.kb; k0 < wk.ke && ok; k0 += kPre) {
+        // A lane whose wait ran out stays with its warp up to the unit's end: it
+        // waits no more, and what it converts is not its stage's (the status
+        // word is set). Lanes that left would wait at the closing barrier for
+        // the others, and those at the next __syncwarp for them.
+        for (int k0 = wk.kb; k0 < wk.ke; k0 += kPre) {
 #pragma unroll
           for (int j = 0; j < kPre; ++j) zn[j] = box_max_of(k0 + kPre + j);
 #pragma unroll
           for (int j = 0; j < kPre; ++j) {
             const int k = k0 + j;
-            if (k >= wk.ke || !ok) break;
+            if (k >= wk.ke) break;
             const int s = static_cast<int>(cit % kStages);
-            if (!mbar_wait(&afull_bar[s], (cit / kStages) & 1u, abort_flag, args.status)) {
-              ok = false;
-              break;
-            }
+            ok = ok && mbar_wait(&afull_bar[s], (cit / kStages) & 1u, abort_flag, args.status);
             constexpr int kNch = 8 / C::kCvtGroups;
             stage_row_to_bf16<kNch>(args, smem + s * C::kStageBytes, lrow_in_tile, part * kNch,
                                     args.v0 + k * BK, rc, zc[j]);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) {
+            if (lane == 0 && ok) {
               if (CTAS == 2) mbar_arrive_cluster(cvt_addr0 + static_cast<uint32_t>(s) * 8u);
               else mbar_arrive(&cvt_bar[s]);
             }
@@ -1282,6 +1283,7 @@ __global__ void __launch_bounds__(PairCfg<MODE, CTAS>::kThreads, 1)
 #pragma unroll
           for (int j = 0; j < kPre; ++j) zc[j] = zn[j];
         }
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (part != 0) continue;  // converter-only warps: no epilogue
       }
@@ -1289,7 +1291,9 @@ __global__ void __launch_bounds__(PairCfg<MODE, CTAS>::kThreads, 1)
       for (int t = t0; t < t1; ++t, ++tile_it) {
         const uint32_t buf = tile_it % C::kNBuf;
         const uint32_t use = tile_it / C::kNBuf;
-        if (!mbar_wait(&tfull_bar[buf], use & 1u, abort_flag, args.status)) {
+        // One answer for the warp: what follows are steps of all its lanes.
+        if (!__all_sync(0xffffffffu,
+                        mbar_wait(&tfull_bar[buf], use & 1u, abort_flag, args.status))) {
           ok = false;
           break;
         }
