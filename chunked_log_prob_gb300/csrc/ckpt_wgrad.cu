@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_base + (static_cast<uint32_t>(q * 32) << 16) + half * (kTileN / 2);
     uint32_t seg = 0;
     const uint32_t peer_abort = mapa_shared(smem_u32(&abort_sh), rank ^ 1u);
-    while (work.next(plan, pair, pairs, it)) {
+    while (ok && work.next(plan, pair, pairs, it)) {
       int tm, tn;
       tile_place(plan, it.tile, tm, tn);
       float sum[4][32];
@@ -417,11 +417,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < 4; ++c)
 #pragma unroll
         for (int j = 0; j < 32; ++j) sum[c][j] = 0.f;
-      // A tile, or a piece of one, is whole or NaN. Where a wait of either CTA ran
-      // out, X may hold what a converter lane did not widen; its CTA's abort flag
-      // was up before that stage reached the tensor core.
+      // Where a wait of either CTA ran out, X may hold what a converter lane did
+      // not widen; its CTA's abort flag was up before that stage reached the
+      // tensor core.
       uint32_t gave_up = 0;
-      for (int k = it.kb; ok && k < it.ke; k += kSegment, ++seg) {
+      for (int k = it.kb; k < it.ke; k += kSegment, ++seg) {
         const uint32_t buf = seg & 1u;
         if (!warp_wait(&tfull_bar[buf], (seg >> 1) & 1u, abort_flag, args.status)) {
           ok = false;
@@ -444,22 +444,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(tempty0 + buf * 8u);
       }
+      if (__any_sync(0xffffffffu, !ok || gave_up != 0)) {
+        ok = false;
+        break;
+      }
       const int lrow = static_cast<int>(rank) * 128 + q * 32 + lane;  // row of the tile
       const int row0 = tm * kTileM + static_cast<int>(rank) * 128 + q * 32;
       const int row = row0 + lane;
-      if (__any_sync(0xffffffffu, !ok || gave_up != 0)) {
-#pragma unroll 1
-        for (int c4 = half * 32; c4 < half * 32 + 32; ++c4) {
-          const int i0 = tn * kTileN + 4 * c4;
-          float* p = it.slot >= 0
-                         ? args.partials + static_cast<long long>(it.slot) * kSlotFloats +
-                               (c4 * kTileM + lrow) * 4
-                     : row < args.out && i0 < args.in ? args.dw + row * args.lddw + i0
-                                                      : nullptr;
-          if (p != nullptr) st_global_v4(p, 0x7fc00000u, 0x7fc00000u, 0x7fc00000u, 0x7fc00000u);
-        }
-        continue;
-      }
       if (row0 >= args.out) continue;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -510,6 +501,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+    }
+    // A tile, or a piece of one, is whole or NaN: so are this one and the rest.
+    if (!ok) {
+      do {
+        int tm, tn;
+        tile_place(plan, it.tile, tm, tn);
+        const int lrow = static_cast<int>(rank) * 128 + q * 32 + lane;
+        const int row = tm * kTileM + lrow;
+#pragma unroll 1
+        for (int c4 = half * 32; c4 < half * 32 + 32; ++c4) {
+          const int i0 = tn * kTileN + 4 * c4;
+          float* p = it.slot >= 0
+                         ? args.partials + static_cast<long long>(it.slot) * kSlotFloats +
+                               (c4 * kTileM + lrow) * 4
+                     : row < args.out && i0 < args.in ? args.dw + row * args.lddw + i0
+                                                      : nullptr;
+          if (p != nullptr) st_global_v4(p, 0x7fc00000u, 0x7fc00000u, 0x7fc00000u, 0x7fc00000u);
+        }
+      } while (work.next(plan, pair, pairs, it));
     }
     if (lane == 0) bulk_wait_group<0>();
   }
