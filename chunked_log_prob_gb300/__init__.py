@@ -29,6 +29,22 @@ from ._binding import (  # noqa: F401
     make_shape,
     status_string,
 )
+from ._adamw import (  # noqa: F401
+    AdamState,
+    AdamW,
+    GradNorm,
+    alloc_adam_state,
+    grpo_grad_norm,
+    grpo_grad_norm_workspace_size,
+)
+from ._glu import (  # noqa: F401
+    GluBackward,
+    GluForward,
+    grpo_glu_bwd,
+    grpo_glu_fwd,
+    grpo_glu_wgrad,
+    grpo_glu_wgrad_workspace_size,
+)
 from ._norm_ckpt import (  # noqa: F401
     Checkpoint8,
     NormBackward,

@@ -62,6 +62,37 @@ class GrpoNormDesc(ctypes.Structure):
                 ("dx_stride", ctypes.c_int64)]
 
 
+class GrpoGluDesc(ctypes.Structure):
+    _fields_ = [("n_tokens", ctypes.c_int64), ("hidden", ctypes.c_int32),
+                ("inner", ctypes.c_int32), ("dtype", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("x_stride", ctypes.c_int64), ("w_gate_stride", ctypes.c_int64),
+                ("w_up_stride", ctypes.c_int64), ("h_stride", ctypes.c_int64),
+                ("gate_stride", ctypes.c_int64), ("up_stride", ctypes.c_int64),
+                ("dh_stride", ctypes.c_int64), ("dgate_stride", ctypes.c_int64),
+                ("dup_stride", ctypes.c_int64), ("dx_stride", ctypes.c_int64)]
+
+
+class GrpoGrad(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class GrpoAdamwTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("copy", ctypes.c_void_p),
+                ("numel", ctypes.c_int64), ("lr", ctypes.c_float),
+                ("weight_decay", ctypes.c_float), ("param_dtype", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32), ("copy_dtype", ctypes.c_int32),
+                ("state_bits", ctypes.c_int32)]
+
+
+class GrpoAdamwParams(ctypes.Structure):
+    _fields_ = [("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+                ("step", ctypes.c_int64), ("seed", ctypes.c_uint64), ("scale", ctypes.c_void_p),
+                ("lr_factor", ctypes.c_void_p), ("step_on_device", ctypes.c_void_p)]
+
+
 class GrpoError(RuntimeError):
     def __init__(self, code: int, where: str):
         self.code = code
@@ -114,6 +145,13 @@ def _load():
         "grpo_ckpt_wgrad_workspace_size": [i64, i32, i32, P(sz)],
         "grpo_selftest_lose_copy": [i64],
         "grpo_ckpt_wgrad": [vp, vp, vp, vp, i64, i32, i32, i64, vp, sz, vp],
+        "grpo_glu_fwd": [vp] * 8 + [P(GrpoGluDesc), vp],
+        "grpo_glu_bwd": [vp] * 11 + [P(GrpoGluDesc), vp],
+        "grpo_glu_wgrad_workspace_size": [i64, i32, i32, P(sz)],
+        "grpo_glu_wgrad": [vp] * 7 + [P(GrpoGluDesc), vp, sz, vp],
+        "grpo_grad_norm_workspace_size": [i32, P(sz)],
+        "grpo_grad_norm": [P(GrpoGrad), i32, ctypes.c_float, vp, vp, sz, vp],
+        "grpo_adamw_step": [P(GrpoAdamwTensor), i32, P(GrpoAdamwParams), vp],
     }.items():
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, ctypes.c_int
@@ -130,7 +168,9 @@ EXPORTED = ("grpo_default_params", "grpo_workspace_size", "grpo_logp_fwd",
             "grpo_launch_timing_read", "grpo_status_string",
             "grpo_norm_fwd", "grpo_norm_workspace_size", "grpo_norm_bwd", "grpo_ckpt_size",
             "grpo_ckpt_layout", "grpo_ckpt_pack", "grpo_ckpt_unpack",
-            "grpo_ckpt_wgrad_workspace_size", "grpo_ckpt_wgrad", "grpo_selftest_lose_copy")
+            "grpo_ckpt_wgrad_workspace_size", "grpo_ckpt_wgrad", "grpo_selftest_lose_copy",
+            "grpo_glu_fwd", "grpo_glu_bwd", "grpo_glu_wgrad_workspace_size", "grpo_glu_wgrad",
+            "grpo_grad_norm_workspace_size", "grpo_grad_norm", "grpo_adamw_step")
 
 FLAG_STORED_LOGITS = 1
 FLAG_SINGLE_CTA = 2

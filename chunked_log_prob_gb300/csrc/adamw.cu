@@ -1,0 +1,733 @@
+// One AdamW step over many tensors, and the norm of all their gradients.
+//
+// Memory bound: every value is read and written once (fp32 moments: 28 bytes a
+// parameter with fp32 gradients and parameters; 8-bit moments: 16), so many tensors
+// share a launch and their table travels in the kernel's parameters: no copy to the
+// device, nothing kept from one call for the next, and a captured launch holds it.
+// A CTA takes a chunk of one tensor, which it finds by bisection; a warp takes 256
+// consecutive values at a time, 8 to a lane in 16-byte loads.
+//
+// Moments in 8 bits: 128 consecutive values share a scale, and 16 lanes hold them, so
+// the largest is four shuffles away. With round to nearest, a second moment that
+// changes by a thousandth a step would stand still (e4m3's neighbours are a sixteenth
+// to an eighth apart); rounded at random it is right in the mean.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "launch.h"
+#include "norm.h"
+#include "row_ops.cuh"
+
+namespace grpo {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kGroup = 256;  // values of a warp's step
+constexpr int kBlock = 128;  // values that share a scale
+constexpr float kTop = 448.f;              // the largest e4m3
+constexpr float kLeast = 3.0092655e-36f;   // 2^-118: blocks below it are kept as zeros
+constexpr int kSmallTable = 24, kLargeTable = 256;
+
+struct AdamwEntry {
+  void* param;
+  const void* grad;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  void* copy;
+  long long numel;
+  long long place;  // of its first value in the random numbers' count
+  float lr, decay;
+  int chunk;        // its first chunk of the launch
+  uint8_t ptype, gtype, ctype, bits;
+};
+
+template <int N>
+struct AdamwTable {
+  AdamwEntry e[N];
+};
+
+struct AdamwArgs {
+  int count;
+  int chunk;  // values of a chunk, a multiple of kGroup
+  float beta1, beta2, rest1, rest2, eps;
+  float log1, log2;  // of the betas
+  float fix1, fix2;  // 1 / (1 - beta1^step), 1 / sqrt(1 - beta2^step)
+  uint64_t seed;
+  long long step;
+  const float* scale;
+  const float* lr_factor;
+  const int64_t* step_on_device;
+};
+
+// ------------------------------------------------------- random numbers ----
+
+// A 32-bit number to another, all bits mixed (multiply and fold; the multipliers are
+// the fractions of the roots of 2 and 3).
+__device__ __forceinline__ uint32_t mix(uint32_t x) {
+  x ^= x >> 16;
+  x *= 0x6A09E667u;
+  x ^= x >> 15;
+  x *= 0xBB67AE85u;
+  return x ^ (x >> 16);
+}
+
+struct Keys {
+  uint32_t k0, k1;
+};
+__device__ __forceinline__ Keys keys_of(uint64_t seed, uint64_t step) {
+  const uint32_t a =
+      mix(static_cast<uint32_t>(seed) ^ mix(static_cast<uint32_t>(seed >> 32) + 0x3C6EF372u));
+  const uint32_t b =
+      mix(static_cast<uint32_t>(step) ^ mix(static_cast<uint32_t>(step >> 32) + a));
+  return {b, mix(b + 0x510E527Fu)};
+}
+
+// The first hash of a place: 16 bits for either moment.
+__device__ __forceinline__ uint32_t bits_at(const Keys& k, uint64_t i) {
+  uint32_t x = static_cast<uint32_t>(i) ^ k.k0;
+  x ^= x >> 16;
+  x *= 0x6A09E667u;
+  x ^= x >> 15;
+  x += k.k1 + static_cast<uint32_t>(i >> 32) * 0x1F83D9ABu;
+  x *= 0xBB67AE85u;
+  return x ^ (x >> 16);
+}
+// And the second, from the first: 16 bits for the parameter.
+__device__ __forceinline__ uint32_t more_bits(const Keys& k, uint32_t x) {
+  const uint32_t y = (x ^ k.k1) * 0x5BE0CD19u;
+  return y ^ (y >> 16);
+}
+
+// ----------------------------------------------------------- conversions ----
+
+// a (0 <= a <= 448) to an e4m3 code: to the lower neighbour lo, or to the upper one
+// hi = lo + step with probability (a - lo) / step, SQUARE: (a^2 - lo^2) / (hi^2 -
+// lo^2). u: 0 to 65535. From 2^-6 on the code's bits are those of the fp32; below,
+// the neighbours are 2^-9 apart.
+template <bool SQUARE>
+__device__ __forceinline__ uint32_t to_e4m3(float a, float u) {
+  const uint32_t w = __float_as_uint(a);
+  const bool small = a < 0.015625f;
+  const float count = floorf(a * 512.f);
+  const float lo = small ? count * 0.001953125f : __uint_as_float(w & 0xfff00000u);
+  const float step = small ? 0.001953125f : __uint_as_float((w & 0x7f800000u) - (3u << 23));
+  const uint32_t code = small ? static_cast<uint32_t>(count) : (w >> 20) - (120u << 3);
+  const bool up = SQUARE ? u * ((2.f * lo + step) * step) < 65536.f * ((a - lo) * (a + lo))
+                         : u * step < 65536.f * (a - lo);
+  return code + (up ? 1u : 0u);
+}
+
+template <typename T>
+__device__ __forceinline__ float load1(const void* p, long long i) {
+  return to_f32(static_cast<const T*>(p)[i]);
+}
+
+// 8 consecutive values from 16-byte loads.
+template <typename T>
+__device__ __forceinline__ void load8(const void* p, long long i, float (&v)[8]) {
+  Raw8<T> r;
+  const uint4* s = reinterpret_cast<const uint4*>(static_cast<const T*>(p) + i);
+  uint4* w = reinterpret_cast<uint4*>(&r);
+#pragma unroll
+  for (int k = 0; k < static_cast<int>(sizeof(r) / 16); ++k) w[k] = __ldcs(s + k);
+  widen(r, v);
+}
+template <typename T>
+__device__ __forceinline__ void store8(void* p, long long i, const float (&v)[8]) {
+  const Raw8<T> r = narrow<T>(v);
+  uint4* d = reinterpret_cast<uint4*>(static_cast<T*>(p) + i);
+  const uint4* w = reinterpret_cast<const uint4*>(&r);
+#pragma unroll
+  for (int k = 0; k < static_cast<int>(sizeof(r) / 16); ++k) __stcs(d + k, w[k]);
+}
+
+// fp32 to bf16 rounded at random: 16 random bits below the kept ones, then cut off.
+__device__ __forceinline__ float random_bf16(float p, uint32_t bits) {
+  const uint32_t w = __float_as_uint(p);
+  const uint32_t r = (w + (bits & 0xffffu)) & 0xffff0000u;
+  // Infinities and NaN as they are (a NaN of low bits alone made a whole one).
+  if ((w & 0x7f800000u) == 0x7f800000u)
+    return __uint_as_float((w & 0x7fffffu) != 0 ? 0x7fc00000u : w);
+  return __uint_as_float(r);
+}
+
+// ------------------------------------------------------------------ step ----
+
+// What a chunk's threads share.
+struct StepOf {
+  float scale, shrink, rate, beta1, beta2, rest1, rest2, fix2, eps;
+  Keys keys;
+};
+
+// The largest finite |y| over the 16 lanes of a block; 0 below kLeast.
+__device__ __forceinline__ float block_top(const float (&y)[8]) {
+  float a = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float m = fabsf(y[j]);
+    a = m <= FLT_MAX ? fmaxf(a, m) : a;
+  }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+  return a >= kLeast ? a : 0.f;
+}
+
+// A lane's 8 values: consecutive from `first` on (VEC, all there), or every 16th of
+// their block (the `have` lowest bits of mask say which are there).
+template <int BITS, typename P, typename G, bool VEC>
+__device__ __forceinline__ void step8(const AdamwEntry& e, const StepOf& s, long long first,
+                                      int lane) {
+  constexpr int kEvery = VEC ? 1 : 16;
+  float p[8], g[8], m[8], v[8];
+  bool have[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) have[j] = VEC || first + j * kEvery < e.numel;
+  const long long block = first / kBlock;  // BITS 8: of this lane's values
+  float ms = 0.f, vs = 0.f;
+  if (BITS == 8 && have[0]) {
+    ms = e.m_scale[block];
+    vs = e.v_scale[block];
+  }
+  if constexpr (VEC) {
+    load8<P>(e.param, first, p);
+    load8<G>(e.grad, first, g);
+    if constexpr (BITS == 32) {
+      load8<float>(e.m, first, m);
+      load8<float>(e.v, first, v);
+    } else {
+      const uint2 mq = __ldcs(reinterpret_cast<const uint2*>(static_cast<uint8_t*>(e.m) + first));
+      const uint2 vq = __ldcs(reinterpret_cast<const uint2*>(static_cast<uint8_t*>(e.v) + first));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 a = unpack_e4m3x2((j < 2 ? mq.x : mq.y) >> (16 * (j & 1)));
+        const float2 b = unpack_e4m3x2((j < 2 ? vq.x : vq.y) >> (16 * (j & 1)));
+        m[2 * j] = a.x;
+        m[2 * j + 1] = a.y;
+        v[2 * j] = b.x;
+        v[2 * j + 1] = b.y;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const long long i = first + j * kEvery;
+      p[j] = g[j] = m[j] = v[j] = 0.f;
+      if (have[j]) {
+        p[j] = load1<P>(e.param, i);
+        g[j] = load1<G>(e.grad, i);
+        if constexpr (BITS == 32) {
+          m[j] = static_cast<const float*>(e.m)[i];
+          v[j] = static_cast<const float*>(e.v)[i];
+        } else {
+          m[j] = unpack_e4m3x2(static_cast<const uint8_t*>(e.m)[i]).x;
+          v[j] = unpack_e4m3x2(static_cast<const uint8_t*>(e.v)[i]).x;
+        }
+      }
+    }
+  }
+  float root[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (BITS == 8) {
+      m[j] *= ms;
+      const float r = v[j] * vs;
+      v[j] = r * r;
+    }
+    const float x = g[j] * s.scale;
+    m[j] = s.beta1 * m[j] + s.rest1 * x;
+    v[j] = s.beta2 * v[j] + s.rest2 * (x * x);
+    root[j] = sqrtf(v[j]);
+    p[j] = p[j] * s.shrink - s.rate * m[j] / (root[j] * s.fix2 + s.eps);
+  }
+  if constexpr (BITS == 32 && VEC) {
+    store8<float>(e.m, first, m);
+    store8<float>(e.v, first, v);
+  } else if constexpr (BITS == 32) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (have[j]) {
+        static_cast<float*>(e.m)[first + j * kEvery] = m[j];
+        static_cast<float*>(e.v)[first + j * kEvery] = v[j];
+      }
+  }
+  uint32_t x[8];
+  constexpr bool kRandom = BITS == 8 || sizeof(P) == 2;
+  if constexpr (kRandom) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      x[j] = bits_at(s.keys, static_cast<uint64_t>(e.place + first + j * kEvery));
+  }
+  if constexpr (BITS == 8) {
+    const float mt = block_top(m), vt = block_top(root);
+    const float mi = mt > 0.f ? kTop / mt : 0.f, vi = vt > 0.f ? kTop / vt : 0.f;
+    uint32_t mq[8], vq[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float am = fabsf(m[j]);
+      mq[j] = to_e4m3<false>(fminf(am * mi, kTop), static_cast<float>(x[j] & 0xffffu));
+      mq[j] |= m[j] < 0.f ? 0x80u : 0u;
+      if (!(am <= FLT_MAX)) mq[j] = kCkptNaN;
+      vq[j] = to_e4m3<true>(fminf(root[j] * vi, kTop), static_cast<float>(x[j] >> 16));
+      if (vt > 0.f && root[j] > 0.f) vq[j] = max(vq[j], 1u);
+      if (!(root[j] <= FLT_MAX)) vq[j] = kCkptNaN;
+    }
+    if constexpr (VEC) {
+      uint2 a, b;
+      a.x = mq[0] | mq[1] << 8 | mq[2] << 16 | mq[3] << 24;
+      a.y = mq[4] | mq[5] << 8 | mq[6] << 16 | mq[7] << 24;
+      b.x = vq[0] | vq[1] << 8 | vq[2] << 16 | vq[3] << 24;
+      b.y = vq[4] | vq[5] << 8 | vq[6] << 16 | vq[7] << 24;
+      __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(e.m) + first), a);
+      __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(e.v) + first), b);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (have[j]) {
+          static_cast<uint8_t*>(e.m)[first + j * kEvery] = static_cast<uint8_t>(mq[j]);
+          static_cast<uint8_t*>(e.v)[first + j * kEvery] = static_cast<uint8_t>(vq[j]);
+        }
+    }
+    if ((lane & 15) == 0 && have[0]) {
+      e.m_scale[block] = mt / kTop;
+      e.v_scale[block] = vt / kTop;
+    }
+  }
+  if constexpr (sizeof(P) == 2) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p[j] = random_bf16(p[j], more_bits(s.keys, x[j]));
+  }
+  if constexpr (VEC) {
+    store8<P>(e.param, first, p);
+    if (e.copy != nullptr) {
+      if (e.ctype == GRPO_DTYPE_BF16)
+        store8<__nv_bfloat16>(e.copy, first, p);
+      else
+        store8<__half>(e.copy, first, p);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (!have[j]) continue;
+      const long long i = first + j * kEvery;
+      static_cast<P*>(e.param)[i] = static_cast<P>(p[j]);
+      if (e.copy != nullptr) {
+        if (e.ctype == GRPO_DTYPE_BF16)
+          static_cast<__nv_bfloat16*>(e.copy)[i] = __float2bfloat16_rn(p[j]);
+        else
+          static_cast<__half*>(e.copy)[i] = __float2half_rn(p[j]);
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ bool on(const void* p, int a) {
+  return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+
+template <int BITS, typename P, typename G>
+__device__ __forceinline__ void step_chunk(const AdamwEntry& e, const StepOf& s, long long begin,
+                                           int chunk) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long end = min(begin + chunk, e.numel);
+  constexpr int kState = BITS == 8 ? 8 : 16;
+  const bool vec = on(e.param, 16) && on(e.grad, 16) && on(e.m, kState) && on(e.v, kState) &&
+                   on(e.copy, 16);
+  for (long long at = begin + warp * kGroup; at < end; at += kWarps * kGroup) {
+    if (vec && at + kGroup <= e.numel)
+      step8<BITS, P, G, true>(e, s, at + lane * 8, lane);
+    else
+      step8<BITS, P, G, false>(e, s, at + (lane >> 4) * kBlock + (lane & 15), lane);
+  }
+}
+
+template <int BITS, typename P>
+__device__ __forceinline__ void step_grad(const AdamwEntry& e, const StepOf& s, long long begin,
+                                          int chunk) {
+  if (e.gtype == GRPO_DTYPE_FP32)
+    step_chunk<BITS, P, float>(e, s, begin, chunk);
+  else if (e.gtype == GRPO_DTYPE_BF16)
+    step_chunk<BITS, P, __nv_bfloat16>(e, s, begin, chunk);
+  else
+    step_chunk<BITS, P, __half>(e, s, begin, chunk);
+}
+
+// The last entry whose first chunk is at most c.
+template <typename E>
+__device__ __forceinline__ int find_entry(const E* e, int count, int c) {
+  int lo = 0, hi = count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (e[mid].chunk <= c)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads)
+    adamw_kernel(const __grid_constant__ AdamwTable<N> table, const AdamwArgs args) {
+  const float scale = args.scale != nullptr ? *args.scale : 1.f;
+  if (!(fabsf(scale) <= FLT_MAX)) return;  // the step is skipped
+  const int c = static_cast<int>(blockIdx.x);
+  const AdamwEntry& e = table.e[find_entry(table.e, args.count, c)];
+  StepOf s;
+  float fix1 = args.fix1;
+  s.fix2 = args.fix2;
+  long long step = args.step;
+  if (args.step_on_device != nullptr) {
+    step = max(static_cast<long long>(*args.step_on_device), 1LL);
+    // 1 - beta^t without its cancellation.
+    const float t = static_cast<float>(step);
+    fix1 = 1.f / -expm1f(t * args.log1);
+    s.fix2 = rsqrtf(-expm1f(t * args.log2));
+  }
+  const float lr = e.lr * (args.lr_factor != nullptr ? *args.lr_factor : 1.f);
+  s.scale = scale;
+  s.shrink = 1.f - lr * e.decay;
+  s.rate = lr * fix1;
+  s.beta1 = args.beta1;
+  s.beta2 = args.beta2;
+  s.rest1 = args.rest1;
+  s.rest2 = args.rest2;
+  s.eps = args.eps;
+  s.keys = keys_of(args.seed, static_cast<uint64_t>(step));
+  const long long begin = static_cast<long long>(c - e.chunk) * args.chunk;
+  if (e.bits == 32) {
+    if (e.ptype == GRPO_DTYPE_FP32)
+      step_grad<32, float>(e, s, begin, args.chunk);
+    else
+      step_grad<32, __nv_bfloat16>(e, s, begin, args.chunk);
+  } else {
+    if (e.ptype == GRPO_DTYPE_FP32)
+      step_grad<8, float>(e, s, begin, args.chunk);
+    else
+      step_grad<8, __nv_bfloat16>(e, s, begin, args.chunk);
+  }
+}
+
+// ------------------------------------------------------------------ norm ----
+
+constexpr int kNormTable = 1024;
+constexpr int kNormCtas = 1216;  // 8 an SM
+constexpr int kNormChunk = 16384;
+
+struct NormEntry {
+  const void* grad;
+  long long numel;
+  int chunk;
+  int type;
+};
+template <int N>
+struct NormTable {
+  NormEntry e[N];
+};
+
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// The sum over the CTA, in thread 0.
+__device__ __forceinline__ double cta_sum(double v) {
+  __shared__ double part[kWarps];
+  v = warp_sum(v);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.0;
+  if (threadIdx.x == 0)
+    for (int w = 0; w < kWarps; ++w) v += part[w];
+  return v;
+}
+
+// A thread's squares of a chunk: fp32 sums of 32 at most, added in fp64.
+template <typename T>
+__device__ __forceinline__ double squares(const void* p, long long begin, long long end) {
+  double sum = 0.0;
+  long long at = begin;
+  if (on(p, 16)) {  // begin is a multiple of the chunk
+    constexpr int kStep = kThreads * 8;
+    for (; at + 4 * kStep <= end; at += 4 * kStep) {
+      float v[4][8], q = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) load8<T>(p, at + k * kStep + threadIdx.x * 8, v[k]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q += v[k][j] * v[k][j];
+      sum += static_cast<double>(q);
+    }
+  }
+  for (; at < end; at += 32 * kThreads) {
+    float q = 0.f;
+#pragma unroll 8
+    for (int k = 0; k < 32; ++k) {
+      const long long i = at + k * kThreads + threadIdx.x;
+      if (i < end) {
+        const float v = load1<T>(p, i);
+        q += v * v;
+      }
+    }
+    sum += static_cast<double>(q);
+  }
+  return sum;
+}
+
+// One partial sum a CTA; CTAs take the chunks round robin.
+template <int N>
+__global__ void __launch_bounds__(kThreads)
+    grad_norm_kernel(const __grid_constant__ NormTable<N> table, int count, int chunks,
+                     double* partials) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  double sum = 0.0;
+  for (int c = static_cast<int>(blockIdx.x); c < chunks; c += static_cast<int>(gridDim.x)) {
+    const NormEntry& e = table.e[find_entry(table.e, count, c)];
+    const long long begin = static_cast<long long>(c - e.chunk) * kNormChunk;
+    const long long end = min(begin + kNormChunk, e.numel);
+    if (e.type == GRPO_DTYPE_FP32)
+      sum += squares<float>(e.grad, begin, end);
+    else if (e.type == GRPO_DTYPE_BF16)
+      sum += squares<__nv_bfloat16>(e.grad, begin, end);
+    else
+      sum += squares<__half>(e.grad, begin, end);
+  }
+  sum = cta_sum(sum);
+  if (threadIdx.x == 0) partials[blockIdx.x] = sum;
+}
+
+// norm and scale from the partial sums, in their order.
+__global__ void __launch_bounds__(kThreads)
+    grad_norm_finish_kernel(const double* partials, int count, float max_norm, float* out) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial sums are there
+  double sum = 0.0;
+  for (int i = static_cast<int>(threadIdx.x); i < count; i += kThreads) sum += partials[i];
+  sum = cta_sum(sum);
+  if (threadIdx.x != 0) return;
+  const float norm = static_cast<float>(sqrt(sum));
+  out[0] = norm;
+  float scale = 1.f;
+  if (!(norm <= FLT_MAX))
+    scale = kNaN;
+  else if (max_norm > 0.f)
+    scale = fminf(1.f, max_norm / (norm + 1e-6f));
+  out[1] = scale;
+}
+
+template <int N>
+cudaError_t launch_adamw(const AdamwEntry* e, const AdamwArgs& a, int chunks, cudaStream_t st) {
+  AdamwTable<N> table;
+  std::copy(e, e + a.count, table.e);
+  std::fill(table.e + a.count, table.e + N, AdamwEntry());
+  LaunchTimer timer("adamw_kernel", st);
+  adamw_kernel<N><<<chunks, kThreads, 0, st>>>(table, a);
+  return cudaGetLastError();
+}
+
+template <int N>
+cudaError_t launch_norm(const NormEntry* e, int count, int chunks, double* partials,
+                        cudaStream_t st) {
+  NormTable<N> table;
+  std::copy(e, e + count, table.e);
+  std::fill(table.e + count, table.e + N, NormEntry());
+  LaunchTimer timer("grad_norm_kernel", st);
+  grad_norm_kernel<N><<<std::min(chunks, kNormCtas), kThreads, 0, st>>>(table, count, chunks,
+                                                                       partials);
+  return cudaGetLastError();
+}
+
+bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+size_t dtype_bytes(int t) { return t == GRPO_DTYPE_FP32 ? 4 : 2; }
+bool known_dtype(int t) { return t >= GRPO_DTYPE_BF16 && t <= GRPO_DTYPE_FP32; }
+constexpr int64_t kMaxValues = 1LL << 44;
+
+size_t norm_workspace(int32_t count) {
+  const size_t launches = (static_cast<size_t>(count) + kNormTable - 1) / kNormTable;
+  return std::max<size_t>(1, launches) * ((kNormCtas * sizeof(double) + 255) / 256 * 256);
+}
+
+int check_tensor(const grpo_adamw_tensor& t) {
+  if (t.numel < 0) return GRPO_ERR_INVALID_ARG;
+  if (t.numel > kMaxValues) return GRPO_ERR_UNSUPPORTED_SHAPE;
+  if ((t.param_dtype != GRPO_DTYPE_FP32 && t.param_dtype != GRPO_DTYPE_BF16) ||
+      !known_dtype(t.grad_dtype) || (t.state_bits != 8 && t.state_bits != 32) ||
+      !(std::fabs(t.lr) <= 3e38f) || !(std::fabs(t.weight_decay) <= 3e38f))
+    return GRPO_ERR_INVALID_ARG;
+  if (t.copy_or_null != nullptr &&
+      (t.param_dtype != GRPO_DTYPE_FP32 ||
+       (t.copy_dtype != GRPO_DTYPE_BF16 && t.copy_dtype != GRPO_DTYPE_FP16)))
+    return GRPO_ERR_INVALID_ARG;
+  if (t.numel == 0 || t.grad == nullptr) return GRPO_OK;
+  if (t.param == nullptr || t.m == nullptr || t.v == nullptr ||
+      (t.state_bits == 8 && (t.m_scale == nullptr || t.v_scale == nullptr)))
+    return GRPO_ERR_INVALID_ARG;
+  const size_t state = t.state_bits == 8 ? 1 : 4;
+  if (!aligned(t.param, dtype_bytes(t.param_dtype)) || !aligned(t.grad, dtype_bytes(t.grad_dtype)) ||
+      !aligned(t.m, state) || !aligned(t.v, state) || !aligned(t.m_scale, 4) ||
+      !aligned(t.v_scale, 4) || !aligned(t.copy_or_null, 2))
+    return GRPO_ERR_MISALIGNED;
+  return GRPO_OK;
+}
+
+}  // namespace
+}  // namespace grpo
+
+using namespace grpo;
+
+extern "C" {
+
+int grpo_grad_norm_workspace_size(int32_t count, size_t* bytes) {
+  if (bytes == nullptr || count < 0) return GRPO_ERR_INVALID_ARG;
+  *bytes = norm_workspace(count);
+  return GRPO_OK;
+}
+
+int grpo_grad_norm(const grpo_grad* grads, int32_t count, float max_norm, float* out,
+                   void* workspace, size_t workspace_bytes, void* stream) {
+  const CallRange range("grpo_grad_norm");
+  if (count < 0 || (count > 0 && grads == nullptr) || out == nullptr || workspace == nullptr ||
+      max_norm != max_norm)
+    return GRPO_ERR_INVALID_ARG;
+  for (int i = 0; i < count; ++i) {
+    if (grads[i].numel < 0 || grads[i].reserved != 0 || !known_dtype(grads[i].dtype))
+      return GRPO_ERR_INVALID_ARG;
+    if (grads[i].numel > kMaxValues) return GRPO_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned(grads[i].data, dtype_bytes(grads[i].dtype))) return GRPO_ERR_MISALIGNED;
+  }
+  if (!aligned(out, 4) || !aligned(workspace, 256)) return GRPO_ERR_MISALIGNED;
+  if (workspace_bytes < norm_workspace(count)) return GRPO_ERR_WORKSPACE_TOO_SMALL;
+  int sms = 0;
+  const int r = setup_device(&sms);
+  if (r != GRPO_OK) return r;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  double* partials = static_cast<double*>(workspace);
+  NormEntry e[kNormTable];
+  int used = 0, sums = 0;
+  int64_t chunks = 0;
+  auto flush = [&]() {
+    if (used == 0) return cudaSuccess;
+    const int c = static_cast<int>(chunks);
+    const cudaError_t err = used <= 64 ? launch_norm<64>(e, used, c, partials + sums, st)
+                                       : launch_norm<kNormTable>(e, used, c, partials + sums, st);
+    sums += std::min(c, kNormCtas);
+    used = 0;
+    chunks = 0;
+    return err;
+  };
+  for (int i = 0; i < count; ++i) {
+    if (grads[i].numel == 0 || grads[i].data == nullptr) continue;
+    const int64_t more = (grads[i].numel + kNormChunk - 1) / kNormChunk;
+    if (used == kNormTable && flush() != cudaSuccess) return GRPO_ERR_CUDA;
+    e[used++] = {grads[i].data, grads[i].numel, static_cast<int>(chunks), grads[i].dtype};
+    chunks += more;
+    if (chunks > (1LL << 30)) return GRPO_ERR_UNSUPPORTED_SHAPE;
+  }
+  if (flush() != cudaSuccess) return GRPO_ERR_CUDA;
+  // Its launch overlaps the end of the other (it waits for that itself).
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  LaunchTimer timer("grad_norm_finish_kernel", st);
+  return cudaLaunchKernelEx(&cfg, grad_norm_finish_kernel,
+                            static_cast<const double*>(partials), sums, max_norm,
+                            out) == cudaSuccess
+             ? GRPO_OK
+             : GRPO_ERR_CUDA;
+}
+
+int grpo_adamw_step(const grpo_adamw_tensor* tensors, int32_t count,
+                    const grpo_adamw_params* params, void* stream) {
+  const CallRange range("grpo_adamw_step");
+  if (count < 0 || (count > 0 && tensors == nullptr) || params == nullptr)
+    return GRPO_ERR_INVALID_ARG;
+  const grpo_adamw_params& q = *params;
+  if (!(q.beta1 >= 0.0 && q.beta1 < 1.0) || !(q.beta2 >= 0.0 && q.beta2 < 1.0) ||
+      !(q.eps >= 0.0) || (q.step_on_device == nullptr && q.step < 1))
+    return GRPO_ERR_INVALID_ARG;
+  if (!aligned(q.scale, 4) || !aligned(q.lr_factor, 4) || !aligned(q.step_on_device, 8))
+    return GRPO_ERR_MISALIGNED;
+  int64_t values = 0;
+  for (int i = 0; i < count; ++i) {
+    const int r = check_tensor(tensors[i]);
+    if (r != GRPO_OK) return r;
+    if (tensors[i].grad != nullptr) values += tensors[i].numel;
+  }
+  int sms = 0;
+  const int r = setup_device(&sms);
+  if (r != GRPO_OK) return r;
+  AdamwArgs a;
+  // The largest chunk that still gives every SM eight CTAs: long chunks find their
+  // tensor and work out the step less often, short ones fill the device.
+  a.chunk = 16384;
+  while (a.chunk > 8 * kGroup && values / a.chunk < 8LL * sms) a.chunk /= 2;
+  a.beta1 = static_cast<float>(q.beta1);
+  a.beta2 = static_cast<float>(q.beta2);
+  a.rest1 = static_cast<float>(1.0 - q.beta1);
+  a.rest2 = static_cast<float>(1.0 - q.beta2);
+  a.eps = static_cast<float>(q.eps);
+  // beta 0: its power is 0 (the logarithm a number that expm1 takes to -1).
+  a.log1 = q.beta1 > 0.0 ? static_cast<float>(std::log(q.beta1)) : -200.f;
+  a.log2 = q.beta2 > 0.0 ? static_cast<float>(std::log(q.beta2)) : -200.f;
+  const double t = static_cast<double>(q.step_on_device == nullptr ? q.step : 1);
+  a.fix1 = static_cast<float>(1.0 / (1.0 - std::pow(q.beta1, t)));
+  a.fix2 = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(q.beta2, t)));
+  a.seed = q.seed;
+  a.step = q.step;
+  a.scale = q.scale;
+  a.lr_factor = q.lr_factor;
+  a.step_on_device = q.step_on_device;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  AdamwEntry e[kLargeTable];
+  int64_t chunks = 0, place = 0;
+  a.count = 0;
+  auto flush = [&]() {
+    if (a.count == 0) return cudaSuccess;
+    const int c = static_cast<int>(chunks);
+    const cudaError_t err = a.count <= kSmallTable ? launch_adamw<kSmallTable>(e, a, c, st)
+                                                   : launch_adamw<kLargeTable>(e, a, c, st);
+    a.count = 0;
+    chunks = 0;
+    return err;
+  };
+  for (int i = 0; i < count; ++i) {
+    const grpo_adamw_tensor& x = tensors[i];
+    const int64_t at = place;
+    place += (x.numel + kBlock - 1) / kBlock * kBlock;
+    if (x.numel == 0 || x.grad == nullptr) continue;
+    const int64_t more = (x.numel + a.chunk - 1) / a.chunk;
+    if ((a.count == kLargeTable || chunks + more > (1LL << 30)) && flush() != cudaSuccess)
+      return GRPO_ERR_CUDA;
+    AdamwEntry& d = e[a.count++];
+    d.param = x.param;
+    d.grad = x.grad;
+    d.m = x.m;
+    d.v = x.v;
+    d.m_scale = x.m_scale;
+    d.v_scale = x.v_scale;
+    d.copy = x.copy_or_null;
+    d.numel = x.numel;
+    d.place = at;
+    d.lr = x.lr;
+    d.decay = x.weight_decay;
+    d.chunk = static_cast<int>(chunks);
+    d.ptype = static_cast<uint8_t>(x.param_dtype);
+    d.gtype = static_cast<uint8_t>(x.grad_dtype);
+    d.ctype = static_cast<uint8_t>(x.copy_dtype);
+    d.bits = static_cast<uint8_t>(x.state_bits);
+    chunks += more;
+  }
+  return flush() == cudaSuccess ? GRPO_OK : GRPO_ERR_CUDA;
+}
+
+}  // extern "C"

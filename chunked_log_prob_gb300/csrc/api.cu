@@ -15,6 +15,7 @@
 
 #include "grpo_gb300.h"
 #include "kernel_fit.h"
+#include "glu.h"
 #include "launch.h"
 
 namespace grpo {
@@ -693,7 +694,8 @@ int device_setup(int* sms) {
     } else if (major != 10 || minor != 3) {
       d.status = GRPO_ERR_UNSUPPORTED_DEVICE;
     } else if (prepare_fwd_gemm() != cudaSuccess || prepare_bwd_gemms() != cudaSuccess ||
-               prepare_fwds_gemm() != cudaSuccess || prepare_ckpt_wgrad() != cudaSuccess) {
+               prepare_fwds_gemm() != cudaSuccess || prepare_ckpt_wgrad() != cudaSuccess ||
+               prepare_glu_gemm() != cudaSuccess || prepare_glu_wgrad() != cudaSuccess) {
       d.status = GRPO_ERR_CUDA;
     }
     if (d.status == GRPO_OK) {

@@ -1,0 +1,573 @@
+// The gated feed-forward block's matrix products, with what belongs to them in the
+// epilogue:
+//   forward   h = act(x Wg^T) * (x Wu^T)
+//   again     dgate = dh u act'(g), dup = dh act(g) from g = x Wg^T, u = x Wu^T
+//   dx        dgate Wg + dup Wu
+//
+// One tcgen05 GEMM. A CTA pair computes 256 rows x 256 accumulator columns: of the
+// first two, 128 columns of the gate and the same 128 of the other projection. Each
+// CTA of a pair brings half of the second operand, so one loads Wg's rows and the
+// other Wu's, and both projections of a value end up in the same thread's TMEM
+// lane. They leave TMEM once, as h (or as the gradients): against two GEMMs and an
+// elementwise pass, x is read once and the fp32 projections are never written. dx
+// is one sum over 2 f columns, its first half from (dgate, Wg) and its second from
+// (dup, Wu). TMEM holds two tiles, so an epilogue runs beside the next tile's MMAs.
+#include <algorithm>
+#include <type_traits>
+
+#include "glu.h"
+#include "glu_act.cuh"
+#include "launch.h"
+#include "row_ops.cuh"
+#include "wgrad_plan.h"
+
+namespace grpo {
+namespace {
+
+constexpr int kFwd = 0, kAgain = 1, kDx = 2;
+
+constexpr int kStages = 6;
+constexpr int kBK = 64;                  // columns of a stage: 128 bytes
+constexpr int kOperand = 128 * kBK * 2;  // a CTA's 128 rows of either operand
+constexpr int kBox = kBK * 128;          // 64 rows x 64 columns of an MN-major operand
+constexpr int kEpilogueWarps = 8;
+constexpr int kFirstEpilogue = 4;  // warps 0 TMA, 1 MMA, 2 and 3 idle
+constexpr int kThreads = 32 * (kFirstEpilogue + kEpilogueWarps);
+constexpr int kSmem = 1024 + 2 * kStages * kOperand;
+constexpr uint32_t kTmemCols = 512;
+
+// The launch's tiles: 256 rows x 128 columns of f (256 of d for dx), dealt round
+// robin to the pairs, column by column within groups of row tiles.
+struct GluPlan {
+  int n_m, n_n, tiles;
+  int kt, kt2;  // stages of the first operand pair, and of both
+  int group;    // row tiles of a group
+};
+
+__device__ __forceinline__ void place(const GluPlan& p, int tile, int& m, int& n) {
+  const int per_group = p.group * p.n_n;
+  const int g = tile / per_group, r = tile - g * per_group;
+  const int rows = least(p.group, p.n_m - g * p.group);
+  n = r / rows;
+  m = g * p.group + (r - n * rows);
+}
+
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity))
+    if (clock64() - t0 > kWaitLimitCycles) return;
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                          int* status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status)) != 0;
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\t"
+      "elect.sync _|P, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, P;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  return std::is_same_v<T, __half> ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
+}
+template <typename T>
+__device__ __forceinline__ void unpack16(uint32_t w, float& lo, float& hi) {
+  if constexpr (std::is_same_v<T, __half>) {
+    unpack_f16x2(w, lo, hi);
+  } else {
+    lo = __uint_as_float(w << 16);
+    hi = __uint_as_float(w & 0xffff0000u);
+  }
+}
+
+// 32 columns of a row, rounded: as many whole groups of 8 as the row has left.
+template <typename T>
+__device__ __forceinline__ void store32(void* base, long long at, const uint32_t (&w)[16],
+                                        int left) {
+  T* p = static_cast<T*>(base) + at;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (8 * j < left) st_global_v4(p + 8 * j, w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+}
+
+// A checkpoint block that one thread holds: 32 values as stored.
+template <typename T>
+__device__ __forceinline__ void ckpt_store32(const uint32_t (&w)[16], uint8_t* q, uint8_t* ex,
+                                             int left) {
+  float a = 0.f;
+  bool special = false;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    float lo, hi;
+    unpack16<T>(w[j], lo, hi);
+    const float m0 = fabsf(lo), m1 = fabsf(hi);
+    if (m0 <= FLT_MAX) a = fmaxf(a, m0);
+    if (m1 <= FLT_MAX) a = fmaxf(a, m1);
+    special = special || !(m0 <= FLT_MAX) || !(m1 <= FLT_MAX);
+  }
+  const int k = ckpt_exponent(a);
+  const float inv = pow2(-k);
+  special = special || k >= CkptTop<T>::k;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float lo, hi;
+      unpack16<T>(w[4 * j + i], lo, hi);
+      o[i] = special ? pack_e4m3x2(ckpt_scaled<T>(lo, inv, k), ckpt_scaled<T>(hi, inv, k))
+                     : pack_e4m3x2(lo * inv, hi * inv);
+    }
+    if (8 * j < left)
+      *reinterpret_cast<uint2*>(q + 8 * j) =
+          make_uint2(__byte_perm(o[0], o[1], 0x5410), __byte_perm(o[2], o[3], 0x5410));
+  }
+  *ex = static_cast<uint8_t>(k + kCkptBias);
+}
+
+template <int MODE, typename T>
+__global__ void __launch_bounds__(kThreads, 1)
+    glu_gemm_kernel(const __grid_constant__ CUtensorMap map_a0,
+                    const __grid_constant__ CUtensorMap map_a1,
+                    const __grid_constant__ CUtensorMap map_b0,
+                    const __grid_constant__ CUtensorMap map_b1, const GluArgs args,
+                    const GluPlan plan) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full_bar[kStages];  // leader: both CTAs' tiles are there
+  __shared__ __align__(8) uint64_t done_bar[kStages];  // the stage's MMAs are done
+  __shared__ __align__(8) uint64_t tfull_bar[2], tempty_bar[2];
+  __shared__ __align__(8) uint64_t drain_bar;
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int abort_sh, status_sh;
+
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* const ring = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = static_cast<int>(blockIdx.x) / 2, pairs = static_cast<int>(gridDim.x) / 2;
+  volatile int* abort_flag = &abort_sh;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full_bar[s], 2);
+      mbar_init(&done_bar[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull_bar[b], 1);
+      mbar_init(&tempty_bar[b], 2 * kEpilogueWarps);  // both CTAs' epilogue warps
+    }
+    mbar_init(&drain_bar, 1);
+    abort_sh = 0;
+    status_sh = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&map_a0);
+    tma_prefetch_desc(rank == 0 ? &map_b0 : &map_b1);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(&tmem_base_sh, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = tmem_base_sh;
+  const int stages = MODE == kDx ? plan.kt2 : plan.kt;
+
+  bool ok = true;
+  // One lane of each role walks through the work, waits and issues; the others are
+  // at the warp barrier before the closing cluster barrier.
+  if (warp == 0) {
+    // ------------------------------------------------------ tiles by TMA --
+    if (elect_one()) {
+      uint32_t n = 0;  // stages issued
+      for (int tile = pair; ok && tile < plan.tiles; tile += pairs) {
+        int tm, tn;
+        place(plan, tile, tm, tn);
+        const int m0 = tm * kTileM + static_cast<int>(rank) * 128;
+        const int n0 = MODE == kDx ? tn * kTileN + static_cast<int>(rank) * (tile_cols(args.d, tn) / 2)
+                                   : tn * 128;
+        for (int k = 0; k < stages; ++k, ++n) {
+          const uint32_t s = n % kStages;
+          if (!mbar_wait(&done_bar[s], ((n / kStages) & 1u) ^ 1u, abort_flag, &status_sh)) {
+            ok = false;
+            break;
+          }
+          if (n == args.lost && blockIdx.x == 0) continue;
+          const uint32_t lead = mapa_shared(smem_u32(&full_bar[s]), 0);
+          mbar_arrive_expect_tx_cluster(lead, 2 * kOperand);
+          uint8_t* a = ring + s * 2 * kOperand;
+          uint8_t* b = a + kOperand;
+          if constexpr (MODE == kDx) {
+            const bool second = k >= plan.kt;
+            const int k0 = (second ? k - plan.kt : k) * kBK;
+            const CUtensorMap* ma = second ? &map_a1 : &map_a0;
+            const CUtensorMap* mb = second ? &map_b1 : &map_b0;
+            tma_load_2d_pair_nohint(a, ma, lead, k0, m0);
+            tma_load_2d_pair_nohint(b, mb, lead, n0, k0);
+            tma_load_2d_pair_nohint(b + kBox, mb, lead, n0 + 64, k0);
+          } else {
+            tma_load_2d_pair_nohint(a, &map_a0, lead, k * kBK, m0);
+            tma_load_2d_pair_nohint(b, rank == 0 ? &map_b0 : &map_b1, lead, k * kBK, n0);
+          }
+        }
+      }
+      // After a timeout: let the copies in flight land before the CTA exits.
+      if (!ok && rank == 0)
+        for (uint32_t j = n >= kStages ? n - kStages : 0; j < n; ++j)
+          drain(&full_bar[j % kStages], (j / kStages) & 1u);
+    }
+  } else if (warp == 1 && rank == 0) {
+    // -------------------------------------------------------- MMA issuer --
+    if (elect_one()) {
+      uint32_t n = 0, t = 0;  // stages, tiles issued
+      const uint32_t type_bits = args.fp16 ? (1u << 7) | (1u << 10) : 0u;
+      for (int tile = pair; ok && tile < plan.tiles; tile += pairs, ++t) {
+        int tm, tn;
+        place(plan, tile, tm, tn);
+        const uint32_t idesc =
+            idesc_bf16(kTileM, MODE == kDx ? tile_cols(args.d, tn) : kTileN, false, MODE == kDx) &
+            ~type_bits;
+        const uint32_t buf = t & 1u;
+        if (!mbar_wait(&tempty_bar[buf], ((t >> 1) & 1u) ^ 1u, abort_flag, &status_sh)) {
+          ok = false;
+          break;
+        }
+        const uint32_t dcol = tmem_base + buf * kTileN;
+        for (int k = 0; k < stages; ++k, ++n) {
+          const uint32_t s = n % kStages;
+          if (!mbar_wait(&full_bar[s], (n / kStages) & 1u, abort_flag, &status_sh)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a = smem_u32(ring + s * 2 * kOperand), b = a + kOperand;
+#pragma unroll
+          for (int kk = 0; kk < kBK / 16; ++kk)
+            tc_mma_bf16_pair(dcol, sdesc_sw128(a + kk * 32, 16, 1024),
+                             MODE == kDx ? sdesc_sw128(b + kk * 2048, kBox, 1024)
+                                         : sdesc_sw128(b + kk * 32, 16, 1024),
+                             idesc, k == 0 && kk == 0 ? 0u : 1u);
+          tc_commit_pair_multicast(&done_bar[s], 0x3);
+        }
+        if (ok) tc_commit_pair_multicast(&tfull_bar[buf], 0x3);
+      }
+      tc_commit_pair(&drain_bar);
+      drain(&drain_bar, 0);
+    }
+  } else if (warp >= kFirstEpilogue) {
+    // ---------------------------------------------------------- epilogue --
+    // A thread holds one row's half of the tile's columns.
+    const int q = warp & 3;  // TMEM lane quarter of this warp
+    const int half = (warp - kFirstEpilogue) >> 2;
+    const uint32_t tempty0 = mapa_shared(smem_u32(&tempty_bar[0]), 0);
+    const uint32_t t0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+    uint32_t t = 0;
+    int tile = pair;
+    for (; tile < plan.tiles; tile += pairs, ++t) {
+      int tm, tn;
+      place(plan, tile, tm, tn);
+      const long long row =
+          static_cast<long long>(tm) * kTileM + static_cast<int>(rank) * 128 + q * 32 + lane;
+      const uint32_t buf = t & 1u;
+      const bool there = row < args.n;
+      const bool live = there && (args.mask == nullptr || args.mask[row] != 0);
+      if (!warp_wait(&tfull_bar[buf], (t >> 1) & 1u, abort_flag, &status_sh)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t acc = t0 + buf * kTileN;
+      if constexpr (MODE == kDx) {
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          const int col = half * 128 + c * 32;
+          const int left = args.d - (tn * kTileN + col);
+          float v[32];
+          tmem_ld32(acc + col, v);
+          if (there && left > 0) {
+            uint32_t w[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              w[j] = live ? pack16<T>(v[2 * j], v[2 * j + 1]) : 0u;
+            store32<T>(args.dx, row * args.lddx + tn * kTileN + col, w, left);
+          }
+          __syncwarp();  // the next load is the whole warp's
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          const int col = half * 64 + c * 32;
+          const int f0 = tn * 128 + col;
+          const int left = args.f - f0;
+          float g[32], u[32];
+          tmem_ld32(acc + col, g);
+          tmem_ld32(acc + 128 + col, u);
+          if (!there || left <= 0) {
+          } else if constexpr (MODE == kFwd) {
+            uint32_t w[16];
+            if (args.gate != nullptr) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                w[j] = live ? pack16<T>(g[2 * j], g[2 * j + 1]) : 0u;
+              store32<T>(args.gate, row * args.ldg + f0, w, left);
+            }
+            if (args.up != nullptr) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                w[j] = live ? pack16<T>(u[2 * j], u[2 * j + 1]) : 0u;
+              store32<T>(args.up, row * args.ldu + f0, w, left);
+            }
+            with_act(args.act, [&](auto tag) {
+              float s;
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const float h0 = activate<decltype(tag)::value, false>(g[2 * j], s) * u[2 * j];
+                const float h1 =
+                    activate<decltype(tag)::value, false>(g[2 * j + 1], s) * u[2 * j + 1];
+                w[j] = live ? pack16<T>(h0, h1) : 0u;
+              }
+            });
+            store32<T>(args.h, row * args.ldh + f0, w, left);
+            if (args.ck.q != nullptr)
+              ckpt_store32<T>(w, args.ck.q + row * args.ck.ldq + f0,
+                              args.ck.ex + row * args.ck.lde + f0 / kCkptBlock, left);
+          } else {
+            uint32_t dg[16], du[16];
+            {
+              const T* p = static_cast<const T*>(args.dh) + row * args.lddh + f0;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (live && 8 * j < left) x = *reinterpret_cast<const uint4*>(p + 8 * j);
+                dg[4 * j] = x.x;
+                dg[4 * j + 1] = x.y;
+                dg[4 * j + 2] = x.z;
+                dg[4 * j + 3] = x.w;
+              }
+            }
+            with_act(args.act, [&](auto tag) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                float d0, d1, s0, s1;
+                unpack16<T>(dg[j], d0, d1);
+                const float a0 = activate<decltype(tag)::value, true>(g[2 * j], s0);
+                const float a1 = activate<decltype(tag)::value, true>(g[2 * j + 1], s1);
+                dg[j] = live ? pack16<T>(d0 * u[2 * j] * s0, d1 * u[2 * j + 1] * s1) : 0u;
+                du[j] = live ? pack16<T>(d0 * a0, d1 * a1) : 0u;
+                // h in the projections' place, should it be wanted
+                u[2 * j] *= a0;
+                u[2 * j + 1] *= a1;
+              }
+            });
+            store32<T>(args.gate, row * args.ldg + f0, dg, left);
+            store32<T>(args.up, row * args.ldu + f0, du, left);
+            if (args.h != nullptr) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                du[j] = live ? pack16<T>(u[2 * j], u[2 * j + 1]) : 0u;
+              store32<T>(args.h, row * args.ldh + f0, du, left);
+            }
+          }
+          __syncwarp();  // the next load is the whole warp's
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(tempty0 + buf * 8u);
+    }
+    // A tile is whole or NaN: so are this one and the rest after a wait that ran out.
+    if (!ok) {
+      for (; tile < plan.tiles; tile += pairs) {
+        int tm, tn;
+        place(plan, tile, tm, tn);
+        const long long row =
+            static_cast<long long>(tm) * kTileM + static_cast<int>(rank) * 128 + q * 32 + lane;
+        if (row >= args.n) continue;
+        const uint32_t w = pack16<T>(kNaN, kNaN);
+        const int width = MODE == kDx ? args.d : args.f, cols = MODE == kDx ? 128 : 64;
+        const int c0 = (MODE == kDx ? tn * kTileN : tn * 128) + half * cols;
+#pragma unroll 1
+        for (int c = c0; c < least(c0 + cols, width); c += 8) {
+          if (MODE == kDx) {
+            st_global_v4(static_cast<T*>(args.dx) + row * args.lddx + c, w, w, w, w);
+            continue;
+          }
+          if (args.h != nullptr)
+            st_global_v4(static_cast<T*>(args.h) + row * args.ldh + c, w, w, w, w);
+          if (args.gate != nullptr)
+            st_global_v4(static_cast<T*>(args.gate) + row * args.ldg + c, w, w, w, w);
+          if (args.up != nullptr)
+            st_global_v4(static_cast<T*>(args.up) + row * args.ldu + c, w, w, w, w);
+          if (args.ck.q != nullptr) {
+            *reinterpret_cast<uint2*>(args.ck.q + row * args.ck.ldq + c) =
+                make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+            args.ck.ex[row * args.ck.lde + c / kCkptBlock] = kCkptBias;
+          }
+        }
+      }
+    }
+  }
+
+  // Neither CTA may leave while the other's tensor core reads its shared memory
+  // or an arrival is on its way to it: every thread arrives for itself here.
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync_threads();
+  tc_fence_after();
+  __syncwarp();
+  if (warp == 1) tmem_dealloc_pair(tmem_base, kTmemCols);
+}
+
+template <int MODE, typename T>
+cudaError_t launch(const CUtensorMap (&a)[2], const CUtensorMap (&b)[2], const GluArgs& args,
+                   const GluPlan& plan, int sms, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * std::min(plan.tiles, sms / 2));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  LaunchTimer timer(MODE == kFwd     ? "glu_gemm_kernel<fwd>"
+                    : MODE == kAgain ? "glu_gemm_kernel<again>"
+                                     : "glu_gemm_kernel<dx>",
+                    st);
+  return cudaLaunchKernelEx(&cfg, glu_gemm_kernel<MODE, T>, a[0], a[1], b[0], b[1], args, plan);
+}
+
+bool map16(CUtensorMap* map, const void* base, int cols, long long rows, long long ld,
+           uint32_t box_rows) {
+  return encode_map_2d(map, base, static_cast<uint64_t>(cols), static_cast<uint64_t>(rows),
+                       static_cast<uint64_t>(ld) * 2, kBK, box_rows,
+                       CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int MODE>
+cudaError_t launch_mode(const GluArgs& args, int sms, cudaStream_t st) {
+  CUtensorMap a[2], b[2];
+  GluPlan plan;
+  plan.n_m = static_cast<int>((args.n + kTileM - 1) / kTileM);
+  if (MODE == kDx) {
+    plan.n_n = (args.d + kTileN - 1) / kTileN;
+    plan.kt = (args.f + kBK - 1) / kBK;
+    if (!map16(&a[0], args.gate, args.f, args.n, args.ldg, 128) ||
+        !map16(&a[1], args.up, args.f, args.n, args.ldu, 128) ||
+        !map16(&b[0], args.w_gate, args.d, args.f, args.ldwg, kBK) ||
+        !map16(&b[1], args.w_up, args.d, args.f, args.ldwu, kBK))
+      return cudaErrorInvalidValue;
+  } else {
+    plan.n_n = (args.f + 127) / 128;
+    plan.kt = (args.d + kBK - 1) / kBK;
+    if (!map16(&a[0], args.x, args.d, args.n, args.ldx, 128) ||
+        !map16(&b[0], args.w_gate, args.d, args.f, args.ldwg, 128) ||
+        !map16(&b[1], args.w_up, args.d, args.f, args.ldwu, 128))
+      return cudaErrorInvalidValue;
+    a[1] = a[0];
+  }
+  plan.kt2 = 2 * plan.kt;
+  plan.tiles = plan.n_m * plan.n_n;
+  plan.group = kGroupM;
+  return args.fp16 ? launch<MODE, __half>(a, b, args, plan, sms, st)
+                   : launch<MODE, __nv_bfloat16>(a, b, args, plan, sms, st);
+}
+
+// ---------------------------------------- from the projections as kept ----
+
+constexpr int kRowThreads = 256;
+
+// dgate = dh u act'(g), dup = dh act(g), h = act(g) u: memory bound, 8 values of a
+// row a thread.
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads) glu_bwd_kept_kernel(const GluArgs a) {
+  const int per_row = a.f / 8;
+  const long long all = a.n * per_row;
+  for (long long i = static_cast<long long>(blockIdx.x) * kRowThreads + threadIdx.x; i < all;
+       i += static_cast<long long>(gridDim.x) * kRowThreads) {
+    const long long row = i / per_row;
+    const int col = static_cast<int>(i - row * per_row) * 8;
+    const bool live = a.mask == nullptr || a.mask[row] != 0;
+    uint4 d = make_uint4(0, 0, 0, 0), g = d, u = d;
+    if (live) {
+      d = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.dh) + row * a.lddh + col);
+      g = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.gate_in) + row * a.ldgi + col);
+      u = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.up_in) + row * a.ldui + col);
+    }
+    const uint32_t dw[4] = {d.x, d.y, d.z, d.w}, gw[4] = {g.x, g.y, g.z, g.w},
+                   uw[4] = {u.x, u.y, u.z, u.w};
+    uint32_t og[4], ou[4], oh[4];
+    with_act(a.act, [&](auto tag) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float d0, d1, g0, g1, u0, u1, s0, s1;
+        unpack16<T>(dw[j], d0, d1);
+        unpack16<T>(gw[j], g0, g1);
+        unpack16<T>(uw[j], u0, u1);
+        const float a0 = activate<decltype(tag)::value, true>(g0, s0);
+        const float a1 = activate<decltype(tag)::value, true>(g1, s1);
+        og[j] = pack16<T>(d0 * u0 * s0, d1 * u1 * s1);
+        ou[j] = pack16<T>(d0 * a0, d1 * a1);
+        oh[j] = pack16<T>(a0 * u0, a1 * u1);
+      }
+    });
+    st_global_v4(static_cast<T*>(a.gate) + row * a.ldg + col, og[0], og[1], og[2], og[3]);
+    st_global_v4(static_cast<T*>(a.up) + row * a.ldu + col, ou[0], ou[1], ou[2], ou[3]);
+    if (a.h != nullptr)
+      st_global_v4(static_cast<T*>(a.h) + row * a.ldh + col, oh[0], oh[1], oh[2], oh[3]);
+  }
+}
+
+}  // namespace
+
+cudaError_t prepare_glu_gemm() {
+  const void* all[] = {
+      reinterpret_cast<const void*>(glu_gemm_kernel<kFwd, __nv_bfloat16>),
+      reinterpret_cast<const void*>(glu_gemm_kernel<kFwd, __half>),
+      reinterpret_cast<const void*>(glu_gemm_kernel<kAgain, __nv_bfloat16>),
+      reinterpret_cast<const void*>(glu_gemm_kernel<kAgain, __half>),
+      reinterpret_cast<const void*>(glu_gemm_kernel<kDx, __nv_bfloat16>),
+      reinterpret_cast<const void*>(glu_gemm_kernel<kDx, __half>)};
+  for (const void* k : all) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_glu_fwd(const GluArgs& a, int sms, cudaStream_t st) {
+  return launch_mode<kFwd>(a, sms, st);
+}
+cudaError_t launch_glu_bwd_again(const GluArgs& a, int sms, cudaStream_t st) {
+  return launch_mode<kAgain>(a, sms, st);
+}
+cudaError_t launch_glu_dx(const GluArgs& a, int sms, cudaStream_t st) {
+  return launch_mode<kDx>(a, sms, st);
+}
+
+cudaError_t launch_glu_bwd_kept(const GluArgs& a, int sms, cudaStream_t st) {
+  const long long all = a.n * (a.f / 8);
+  const unsigned grid = static_cast<unsigned>(
+      std::min<long long>((all + kRowThreads - 1) / kRowThreads, 8LL * sms));
+  LaunchTimer timer("glu_bwd_kept_kernel", st);
+  if (a.fp16)
+    glu_bwd_kept_kernel<__half><<<grid, kRowThreads, 0, st>>>(a);
+  else
+    glu_bwd_kept_kernel<__nv_bfloat16><<<grid, kRowThreads, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace grpo

@@ -72,6 +72,8 @@ struct CkptArgs {
 
 // No copy is left out (grpo_selftest_lose_copy).
 constexpr uint32_t kNoneLost = 0xffffffffu;
+// What it asked of this thread's next call, once.
+uint32_t take_lost();
 
 // Largest D of the kernels that hold a whole row in registers (forward: of rows on
 // 16 bytes; others up to 8192).

@@ -64,13 +64,7 @@ int check_wgrad(int64_t n, int32_t out, int32_t in, int64_t dy_stride) {
   return GRPO_OK;
 }
 
-// What grpo_selftest_lose_copy asked of this thread's next call.
 thread_local uint32_t t_lost = kNoneLost;
-uint32_t take_lost() {
-  const uint32_t v = t_lost;
-  t_lost = kNoneLost;
-  return v;
-}
 
 int64_t stride_or(int64_t s, int64_t hidden) { return s != 0 ? s : hidden; }
 
@@ -80,6 +74,13 @@ size_t norm_workspace(const grpo_norm_desc* d) {
 }
 
 }  // namespace
+
+uint32_t take_lost() {
+  const uint32_t v = t_lost;
+  t_lost = kNoneLost;
+  return v;
+}
+
 }  // namespace grpo
 
 using namespace grpo;

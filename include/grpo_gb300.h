@@ -485,11 +485,153 @@ int grpo_ckpt_wgrad(const void* dy, const void* ckpt, const float* add_or_null, 
                     int64_t n_tokens, int32_t out_features, int32_t in_features,
                     int64_t dy_stride, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The gated feed-forward block below the tail: both projections, the activation
+ * and the product in one kernel, and its backward pass. grpo_norm_fwd's y is its
+ * x; its h is the input of the block's last linear layer, and grpo_norm_bwd takes
+ * its dx.
+ *
+ *   g = x Wg^T, u = x Wu^T, h = act(g) u
+ *   dgate = dh u act'(g), dup = dh act(g), dx = dgate Wg + dup Wu
+ *   dWg = dgate^T x, dWu = dup^T x
+ *
+ * x, dx: [n_tokens][hidden]; h, the projections and their gradients: [n_tokens]
+ * [inner]; Wg, Wu: [inner][hidden] (halves of one matrix, or two). All are bf16 or
+ * all fp16, start on 16 bytes, and have row strides of their own, in elements;
+ * hidden, inner and the strides are multiples of 8. Sums are fp32; g, u and what is
+ * made of them are rounded where they are stored and nowhere before. `mask` (uint8
+ * [n_tokens] or NULL): a row with mask 0 has no influence, whatever it holds, and
+ * its output rows are exact zeros. n_tokens = 0 is allowed. Calls are asynchronous
+ * on `stream`, allocate nothing, can be captured in a graph, and give the same bits
+ * each time. A wait on the device that runs out (about a second) leaves NaN in the
+ * tiles of the outputs that were still to be written.
+ * ------------------------------------------------------------------------- */
+#define GRPO_ACT_SILU 0      /* g / (1 + e^-g)                                     */
+#define GRPO_ACT_GELU 1      /* g Phi(g)                                           */
+#define GRPO_ACT_GELU_TANH 2 /* g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2  */
+#define GRPO_ACT_RELU 3      /* max(g, 0), its derivative at 0 is 0                */
+
+typedef struct grpo_glu_desc {
+  int64_t n_tokens;
+  int32_t hidden, inner;
+  int32_t dtype; /* GRPO_DTYPE_BF16 or GRPO_DTYPE_FP16 of every tensor              */
+  int32_t act;   /* GRPO_ACT_*                                                      */
+  /* Elements from one row to the next; 0 = packed. gate and up: the projections
+   * (written by the forward pass, read by the backward pass). */
+  int64_t x_stride, w_gate_stride, w_up_stride, h_stride, gate_stride, up_stride;
+  int64_t dh_stride, dgate_stride, dup_stride, dx_stride;
+} grpo_glu_desc;
+
+/* h and, where given, the projections as the backward pass reads them.
+ *   gate_or_null, up_or_null: both or neither
+ *   ckpt_or_null: checkpoint of h as stored (grpo_ckpt_size bytes, 256-byte
+ *     aligned), what grpo_ckpt_pack would make of it */
+int grpo_glu_fwd(const void* x, const void* w_gate, const void* w_up, const uint8_t* mask_or_null,
+                 void* h, void* gate_or_null, void* up_or_null, void* ckpt_or_null,
+                 const grpo_glu_desc* desc, void* stream);
+
+/* The gradients of the projections, and of x where dx is given.
+ *   gate_or_null, up_or_null: the projections as the forward pass kept them; with
+ *     both NULL they are computed again from x (which may be NULL otherwise)
+ *   h_or_null: h again, for the weight gradient of the layer that it went into
+ * dx is that of dgate and dup as stored. dgate may lie on gate or on dh, dup on up or
+ * on dh, h on whichever of the three is left, with the same stride (dh and the
+ * projections are lost then); other overlaps are not allowed. */
+int grpo_glu_bwd(const void* dh, const void* x_or_null, const void* w_gate, const void* w_up,
+                 const void* gate_or_null, const void* up_or_null, const uint8_t* mask_or_null,
+                 void* dgate, void* dup, void* dx_or_null, void* h_or_null,
+                 const grpo_glu_desc* desc, void* stream);
+
+/* The weight gradients, fp32 [inner][hidden], packed, starting on 16 bytes:
+ *   dw_gate = add_gate + dgate^T x,  dw_up = add_up + dup^T x
+ *   add_gate_or_null, add_up_or_null: may be the outputs themselves; NULL = 0
+ * Products are exact, sums are fp32 in an order fixed by the sizes and the device's
+ * SM pairs. Masked tokens: dgate and dup are 0 there (grpo_glu_bwd leaves them so),
+ * and x must be finite (grpo_norm_fwd leaves 0). x kept as a checkpoint:
+ * grpo_ckpt_wgrad. The first bytes of the workspace (256-byte aligned) are a status
+ * word for grpo_read_device_status. */
+int grpo_glu_wgrad_workspace_size(int64_t n_tokens, int32_t inner, int32_t hidden, size_t* bytes);
+int grpo_glu_wgrad(const void* dgate, const void* dup, const void* x, const float* add_gate_or_null,
+                   const float* add_up_or_null, float* dw_gate, float* dw_up,
+                   const grpo_glu_desc* desc, void* workspace, size_t workspace_bytes,
+                   void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The optimizer's step at the end of a training step: AdamW over many tensors in
+ * one launch per 256 tensors, and the norm of all gradients.
+ * ------------------------------------------------------------------------- */
+typedef struct grpo_grad {
+  const void* data;
+  int64_t numel;
+  int32_t dtype; /* GRPO_DTYPE_*                                                    */
+  int32_t reserved;
+} grpo_grad;
+
+/* norm = sqrt(sum over all tensors of g^2), scale = min(1, max_norm / (norm + 1e-6))
+ * (max_norm <= 0: 1). out: fp32 [2] on the device, norm and scale; where the norm is
+ * not finite the scale is NaN. Squares, and sums of 32 of them, are fp32 (a gradient
+ * beyond 1.8e19 counts as not finite), further sums fp64 in an order fixed by the
+ * sizes. Tensors are packed and start on an element; NULL ones add nothing. grads: on
+ * the host, read during the call. */
+int grpo_grad_norm_workspace_size(int32_t count, size_t* bytes);
+int grpo_grad_norm(const grpo_grad* grads, int32_t count, float max_norm, float* out,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* One tensor of the optimizer: packed, each part starting on an element. A NULL grad
+ * or numel 0 leaves the tensor as it is.
+ *   param: fp32 or bf16; copy_or_null: bf16 or fp16, the new parameters rounded to
+ *     nearest (fp32 parameters only)
+ *   state_bits 32: m and v are fp32 [numel]
+ *   state_bits 8: m and v are e4m3 [numel]; m_scale and v_scale fp32
+ *     [ceil(numel / 128)]: m is m_q m_scale, v is (v_q v_scale)^2 */
+typedef struct grpo_adamw_tensor {
+  void* param;
+  const void* grad;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  void* copy_or_null;
+  int64_t numel;
+  float lr, weight_decay;
+  int32_t param_dtype, grad_dtype, copy_dtype, state_bits;
+} grpo_adamw_tensor;
+
+typedef struct grpo_adamw_params {
+  double beta1, beta2, eps; /* 0 <= beta < 1, eps >= 0                               */
+  int64_t step;             /* of this call, from 1 on                               */
+  uint64_t seed;            /* of the random rounding                                */
+  /* On the device, or NULL: */
+  const float* scale;     /* [1] multiplies the gradients (grpo_grad_norm's); a scale
+                             that is not finite leaves everything as it is           */
+  const float* lr_factor; /* [1] multiplies every lr                                 */
+  const int64_t* step_on_device; /* [1] read in place of `step` (below 1: 1)          */
+} grpo_adamw_params;
+
+/* g = grad scale, p = param (1 - lr weight_decay),
+ *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2,
+ *   param = p - lr / (1 - beta1^step) m / (sqrt(v / (1 - beta2^step)) + eps),
+ * in fp32. What is kept in fewer bits is rounded at random, so that steps far below
+ * its spacing are not lost: a value between two neighbours lo < hi goes to hi with
+ * the probability that makes the mean right (of v, where its root is kept). The
+ * random numbers are a hash of seed, step and the value's place, where the tensors
+ * are counted through in their order, each from the next multiple of 128 on; so
+ * results repeat bit for bit. bf16 parameters: u < 2^16 is added below the kept bits,
+ * which are then cut off. Moments in 8 bits: of each 128 consecutive values the
+ * scale is the largest / 448; a v above 0 never becomes 0. Moments of a block whose
+ * largest is below 2^-118 are kept as 0; a value that is not finite is kept as NaN.
+ * tensors: on the host, read during the call; of a tensor, param, m, v and the
+ * rest overlap nothing. A captured call repeats its step and its lr unless
+ * step_on_device and lr_factor give others. */
+int grpo_adamw_step(const grpo_adamw_tensor* tensors, int32_t count,
+                    const grpo_adamw_params* params, void* stream);
+
 /* Self-test of what these calls do when a copy never arrives: the calling
  * thread's next grpo_norm_fwd or grpo_norm_bwd copies neither row `index` nor what
- * its CTA has to do after it (where two CTAs share a row: the first of them), or its next grpo_ckpt_wgrad does not copy the 64-token stage
- * `index` (counted over the stages of the first CTA's tiles) to that CTA. The
- * wait for it runs out after about a second, the kernel gives up the work that
+ * its CTA has to do after it (where two CTAs share a row: the first of them), or its
+ * next grpo_ckpt_wgrad or grpo_glu_wgrad does not copy the 64-token stage `index`,
+ * its next grpo_glu_fwd or grpo_glu_bwd (the first of its products) the 64-column
+ * stage (counted over the stages of the first CTA's tiles), to that CTA. The wait for it runs out after about a second, the kernel gives up the work that
  * depends on it (NaN in its place), lets the copies in flight land and returns;
  * the context stays usable. -1: nothing is left out. */
 int grpo_selftest_lose_copy(int64_t index);
