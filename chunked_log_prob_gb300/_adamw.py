@@ -6,8 +6,10 @@ from __future__ import annotations
 
 import ctypes
 from functools import lru_cache
+from operator import attrgetter
 from typing import NamedTuple, Sequence
 
+import numpy as np
 import torch
 
 from ._binding import GRPO_OK, GrpoAdamwParams, GrpoAdamwTensor, GrpoError, GrpoGrad, call_on, lib
@@ -17,7 +19,11 @@ _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _PARAMS = (torch.float32, torch.bfloat16)
 _COPIES = (torch.bfloat16, torch.float16)
 _BLOCK = 128
+_GRAD = np.dtype(GrpoGrad)
 _byref = ctypes.byref
+_data_ptr, _numel = torch.Tensor.data_ptr, torch.Tensor.numel
+_packed, _device_index = torch.Tensor.is_contiguous, torch.Tensor.get_device
+_dtype, _shape = attrgetter("dtype"), attrgetter("shape")
 
 
 class GradNorm(NamedTuple):
@@ -86,6 +92,21 @@ def _grad_type(g, i, device):
     return code
 
 
+def _quick(view, field, grads, device):
+    """The gradients' addresses, with their types' codes put into the table, where all
+    of them are what is expected; None otherwise: they are then looked at one by one.
+    (A set of adapters has hundreds, at a few us each one by one.)"""
+    try:
+        codes = [_DTYPES[t] for t in map(_dtype, grads)]
+        if set(map(_device_index, grads)) != {device.index} or not all(map(_packed, grads)):
+            return None
+        data = list(map(_data_ptr, grads))
+    except (AttributeError, KeyError, TypeError):  # None among them, or another type
+        return None
+    view[field] = codes
+    return data
+
+
 def grpo_grad_norm(grads: Sequence[torch.Tensor | None], *, max_norm=None, out=None,
                    workspace=None) -> GradNorm:
     """The 2-norm over all gradients (None ones add nothing), and what to scale them
@@ -107,9 +128,14 @@ def grpo_grad_norm(grads: Sequence[torch.Tensor | None], *, max_norm=None, out=N
         raise ValueError(f"max_norm: expected a positive number, got {max_norm!r}")
     n = len(live)
     table = (GrpoGrad * n)()
-    for i, (e, g) in enumerate(zip(table, live)):
-        e.dtype = _grad_type(g, i, dev)
-        e.data, e.numel = g.data_ptr(), g.numel()
+    if n:
+        view = np.frombuffer(table, dtype=_GRAD)
+        data = _quick(view, "dtype", live, dev)
+        if data is None:
+            view["dtype"] = [_grad_type(g, i, dev) for i, g in enumerate(live)]
+            data = list(map(_data_ptr, live))
+        view["data"] = data
+        view["numel"] = list(map(_numel, live))
     if workspace is None:
         workspace = torch.empty(_norm_workspace(n), dtype=_U8, device=dev)
     elif workspace.device != dev:
@@ -190,8 +216,28 @@ class AdamW:
         if step_tensor is not None:
             _device_scalar(step_tensor, "step_tensor", torch.int64, self.device)
         self._table = (GrpoAdamwTensor * n)()
-        for i in range(n):
+        self._view = np.frombuffer(self._table, dtype=GrpoAdamwTensor)
+        self._describe()
+
+    def _now(self):
+        """Where the parameters are, and how many values they have."""
+        return list(map(_data_ptr, self.params)), list(map(_numel, self.params))
+
+    def _describe(self):
+        for i in range(len(self.params)):
             self._fill(i)
+        self._seen = self._now()
+        self._shapes = list(map(_shape, self.params))
+
+    def _grad(self, i, g):
+        """Checks one gradient; its address (0: none)."""
+        if g is None:
+            return 0
+        self._table[i].grad_dtype = _grad_type(g, i, self.device)
+        if g.shape != self._shapes[i]:
+            raise ValueError(f"grads[{i}]: expected shape {tuple(self._shapes[i])}, "
+                             f"got {tuple(g.shape)}")
+        return g.data_ptr()
 
     def _fill(self, i):
         """Checks a tensor, its moments and its copy, and describes them."""
@@ -233,28 +279,21 @@ class AdamW:
         tensor as it is); by default their ``.grad``. scale: fp32 on the device,
         multiplies the gradients; where it is not finite the step changes nothing. lr:
         from this step on. lr_factor: fp32 on the device, multiplies it."""
-        params, table, dev = self.params, self._table, self.device
+        params, dev = self.params, self.device
         if grads is None:
             grads = [p.grad for p in params]
         if len(grads) != len(params):
             raise ValueError(f"grads: expected {len(params)} of them, got {len(grads)}")
         if lr is not None:
             self.lr = _per_tensor(lr, len(params), "lr")
-        types = _DTYPES
-        for i, (e, p, g, rate, decay) in enumerate(
-                zip(table, params, grads, self.lr, self.weight_decay)):
-            if p.data_ptr() != e.param:  # its storage was exchanged
-                self._fill(i)
-            e.lr, e.weight_decay = rate, decay
-            if g is None:
-                e.grad = None
-                continue
-            code = types.get(g.dtype)
-            if code is None or g.device != dev or not g.is_contiguous():
-                _grad_type(g, i, dev)
-            if g.shape != p.shape:
-                raise ValueError(f"grads[{i}]: expected shape {tuple(p.shape)}, got {tuple(g.shape)}")
-            e.grad, e.grad_dtype = g.data_ptr(), code
+        if self._now() != self._seen:  # a parameter's storage was exchanged
+            self._describe()
+        view = self._view
+        view["lr"], view["weight_decay"] = self.lr, self.weight_decay
+        data = _quick(view, "grad_dtype", grads, dev)
+        if data is None or list(map(_shape, grads)) != self._shapes:
+            data = [self._grad(i, g) for i, g in enumerate(grads)]
+        view["grad"] = data
         q = GrpoAdamwParams(*self.betas, self.eps, self.steps_done + 1, self.seed)
         if scale is not None:
             q.scale = _device_scalar(scale, "scale", _F32, dev)
@@ -262,7 +301,7 @@ class AdamW:
             q.lr_factor = _device_scalar(lr_factor, "lr_factor", _F32, dev)
         if self.step_tensor is not None:
             q.step_on_device = _device_scalar(self.step_tensor, "step_tensor", torch.int64, dev)
-        rc = call_on(dev, lib.grpo_adamw_step, table, len(params), _byref(q))
+        rc = call_on(dev, lib.grpo_adamw_step, self._table, len(params), _byref(q))
         if rc:
             raise GrpoError(rc, "grpo_adamw_step")
         self.steps_done += 1

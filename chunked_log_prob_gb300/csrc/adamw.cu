@@ -86,14 +86,20 @@ __device__ __forceinline__ Keys keys_of(uint64_t seed, uint64_t step) {
   return {b, mix(b + 0x510E527Fu)};
 }
 
+// The keys of the 2^32 places that begin at a multiple of it: the step's own for the
+// first of them (mix(0) is 0).
+__device__ __forceinline__ Keys keys_at(const Keys& k, uint32_t high) {
+  const uint32_t far = mix(high);
+  return {k.k0 ^ far, k.k1 + mix(far * 0x1F83D9ABu)};
+}
+
 // The first hash of a place: 16 bits for either moment.
-__device__ __forceinline__ uint32_t bits_at(const Keys& k, uint64_t i) {
-  uint32_t x = static_cast<uint32_t>(i) ^ k.k0;
+__device__ __forceinline__ uint32_t bits_at(const Keys& k, uint32_t i) {
+  uint32_t x = i ^ k.k0;
   x ^= x >> 16;
   x *= 0x6A09E667u;
   x ^= x >> 15;
-  x += k.k1 + static_cast<uint32_t>(i >> 32) * 0x1F83D9ABu;
-  x *= 0xBB67AE85u;
+  x = x * 0xBB67AE85u + k.k1 * 0xBB67AE85u;
   return x ^ (x >> 16);
 }
 // And the second, from the first: 16 bits for the parameter.
@@ -104,21 +110,44 @@ __device__ __forceinline__ uint32_t more_bits(const Keys& k, uint32_t x) {
 
 // ----------------------------------------------------------- conversions ----
 
-// a (0 <= a <= 448) to an e4m3 code: to the lower neighbour lo, or to the upper one
-// hi = lo + step with probability (a - lo) / step, SQUARE: (a^2 - lo^2) / (hi^2 -
-// lo^2). u: 0 to 65535. From 2^-6 on the code's bits are those of the fp32; below,
-// the neighbours are 2^-9 apart.
-template <bool SQUARE>
-__device__ __forceinline__ uint32_t to_e4m3(float a, float u) {
-  const uint32_t w = __float_as_uint(a);
-  const bool small = a < 0.015625f;
-  const float count = floorf(a * 512.f);
-  const float lo = small ? count * 0.001953125f : __uint_as_float(w & 0xfff00000u);
-  const float step = small ? 0.001953125f : __uint_as_float((w & 0x7f800000u) - (3u << 23));
-  const uint32_t code = small ? static_cast<uint32_t>(count) : (w >> 20) - (120u << 3);
-  const bool up = SQUARE ? u * ((2.f * lo + step) * step) < 65536.f * ((a - lo) * (a + lo))
-                         : u * step < 65536.f * (a - lo);
-  return code + (up ? 1u : 0u);
+// To e4m3 at random: a (0 <= a <= 448) goes to its lower neighbour lo, or to the upper
+// one hi = lo + step where u < 2^16 (a - lo) / step; u: 0 to 65535. From 2^-6 on the
+// code's bits are those of the fp32, and the 20 bits below them are (a - lo) / step;
+// below, 2^-6 is added, which puts the neighbours, 2^-9 apart, in the same bits.
+struct Scaled {
+  uint32_t w;     // the bits of a, or of a + 2^-6
+  uint32_t zero;  // the code's offset in them
+  bool small;
+};
+__device__ __forceinline__ Scaled scaled(float a) {
+  Scaled s;
+  s.small = a < 0.015625f;
+  s.w = __float_as_uint(s.small ? a + 0.015625f : a);
+  s.zero = s.small ? 121u << 3 : 120u << 3;
+  return s;
+}
+__device__ __forceinline__ uint32_t to_e4m3(float a, uint32_t u) {
+  const Scaled s = scaled(a);
+  // The low bits are more than 16 u where this carries out of them.
+  return ((s.w + (((u ^ 0xffffu) << 4) | 15u)) >> 20) - s.zero;
+}
+// The same by the squares: u < 2^16 (a^2 - lo^2) / (hi^2 - lo^2). In units of step,
+// z = a and k = lo: u (2 k + 1) < 2^16 (z - k) (z + k).
+__device__ __forceinline__ uint32_t to_e4m3_square(float a, uint32_t u) {
+  const Scaled s = scaled(a);
+  const float off = s.small ? 8.f : 0.f;
+  const float z = __uint_as_float((s.w & 0x007fffffu) | 0x41000000u) - off;  // 8 to 16
+  const float k = __uint_as_float((s.w & 0x00700000u) | 0x41000000u) - off;
+  const float q = __uint_as_float((u << 7) | 0x3f800000u) - 1.f;  // u / 2^16
+  const bool up = q * fmaf(2.f, k, 1.f) < (z - k) * (z + k);
+  return (s.w >> 20) - s.zero + (up ? 1u : 0u);
+}
+
+// Off by 2^-23 of itself at most; where v is subnormal too.
+__device__ __forceinline__ float quick_root(float v) {
+  float r;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
 }
 
 template <typename T>
@@ -163,17 +192,28 @@ struct StepOf {
   Keys keys;
 };
 
-// The largest finite |y| over the 16 lanes of a block; 0 below kLeast.
+// The largest |y| over the 16 lanes of a block; NaN where one of them is.
 __device__ __forceinline__ float block_top(const float (&y)[8]) {
+  float a = max_abs_nan(y[0], y[1], y[2]);
+  a = max_abs_nan(a, y[3], y[4]);
+  a = max_abs_nan(max_abs_nan(a, y[5], y[6]), y[7], y[7]);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    const float b = __shfl_xor_sync(0xffffffffu, a, o);
+    a = max_abs_nan(a, b, b);
+  }
+  return a;
+}
+// The largest finite one.
+__device__ __noinline__ float block_top_finite(float y0, float y1, float y2, float y3, float y4,
+                                               float y5, float y6, float y7) {
+  const float y[8] = {y0, y1, y2, y3, y4, y5, y6, y7};
   float a = 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float m = fabsf(y[j]);
-    a = m <= FLT_MAX ? fmaxf(a, m) : a;
-  }
+  for (int j = 0; j < 8; ++j) a = fabsf(y[j]) <= FLT_MAX ? fmaxf(a, fabsf(y[j])) : a;
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-  return a >= kLeast ? a : 0.f;
+  return a;
 }
 
 // A lane's 8 values: consecutive from `first` on (VEC, all there), or every 16th of
@@ -240,8 +280,9 @@ __device__ __forceinline__ void step8(const AdamwEntry& e, const StepOf& s, long
     const float x = g[j] * s.scale;
     m[j] = s.beta1 * m[j] + s.rest1 * x;
     v[j] = s.beta2 * v[j] + s.rest2 * (x * x);
-    root[j] = sqrtf(v[j]);
-    p[j] = p[j] * s.shrink - s.rate * m[j] / (root[j] * s.fix2 + s.eps);
+    root[j] = quick_root(v[j]);
+    // the quick division: off by 2 units at most, of the step alone
+    p[j] = p[j] * s.shrink - __fdividef(s.rate * m[j], root[j] * s.fix2 + s.eps);
   }
   if constexpr (BITS == 32 && VEC) {
     store8<float>(e.m, first, m);
@@ -256,24 +297,41 @@ __device__ __forceinline__ void step8(const AdamwEntry& e, const StepOf& s, long
   }
   uint32_t x[8];
   constexpr bool kRandom = BITS == 8 || sizeof(P) == 2;
+  Keys keys = {};
   if constexpr (kRandom) {
+    // A lane's values lie in one block, which no multiple of 2^32 parts.
+    const uint64_t place = static_cast<uint64_t>(e.place + first);
+    keys = keys_at(s.keys, static_cast<uint32_t>(place >> 32));
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      x[j] = bits_at(s.keys, static_cast<uint64_t>(e.place + first + j * kEvery));
+      x[j] = bits_at(keys, static_cast<uint32_t>(place) + j * kEvery);
   }
   if constexpr (BITS == 8) {
-    const float mt = block_top(m), vt = block_top(root);
+    float mt = block_top(m), vt = block_top(root);
+    // Nothing in the warp's blocks is special (the usual case).
+    const bool plain = __all_sync(0xffffffffu, mt <= FLT_MAX && vt <= FLT_MAX);
+    if (!plain) {
+      mt = block_top_finite(m[0], m[1], m[2], m[3], m[4], m[5], m[6], m[7]);
+      vt = block_top_finite(root[0], root[1], root[2], root[3], root[4], root[5], root[6], root[7]);
+    }
+    mt = mt >= kLeast ? mt : 0.f;
+    vt = vt >= kLeast ? vt : 0.f;
     const float mi = mt > 0.f ? kTop / mt : 0.f, vi = vt > 0.f ? kTop / vt : 0.f;
+    const float some = vt > 0.f ? 0.f : FLT_MAX;  // a root beyond it never becomes 0
     uint32_t mq[8], vq[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float am = fabsf(m[j]);
-      mq[j] = to_e4m3<false>(fminf(am * mi, kTop), static_cast<float>(x[j] & 0xffffu));
-      mq[j] |= m[j] < 0.f ? 0x80u : 0u;
-      if (!(am <= FLT_MAX)) mq[j] = kCkptNaN;
-      vq[j] = to_e4m3<true>(fminf(root[j] * vi, kTop), static_cast<float>(x[j] >> 16));
-      if (vt > 0.f && root[j] > 0.f) vq[j] = max(vq[j], 1u);
-      if (!(root[j] <= FLT_MAX)) vq[j] = kCkptNaN;
+      mq[j] = to_e4m3(fminf(fabsf(m[j]) * mi, kTop), x[j] & 0xffffu);
+      mq[j] |= (__float_as_uint(m[j]) >> 24) & 0x80u;
+      const float a = fminf(root[j] * vi, kTop);
+      vq[j] = to_e4m3_square(root[j] > some ? fmaxf(a, 0.001953125f) : a, x[j] >> 16);
+    }
+    if (!plain) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (!(fabsf(m[j]) <= FLT_MAX)) mq[j] = kCkptNaN;
+        if (!(root[j] <= FLT_MAX)) vq[j] = kCkptNaN;
+      }
     }
     if constexpr (VEC) {
       uint2 a, b;
@@ -298,7 +356,7 @@ __device__ __forceinline__ void step8(const AdamwEntry& e, const StepOf& s, long
   }
   if constexpr (sizeof(P) == 2) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) p[j] = random_bf16(p[j], more_bits(s.keys, x[j]));
+    for (int j = 0; j < 8; ++j) p[j] = random_bf16(p[j], more_bits(keys, x[j]));
   }
   if constexpr (VEC) {
     store8<P>(e.param, first, p);

@@ -6,7 +6,7 @@
 // token's row holds 64 outputs or inputs in 128 bytes. A CTA pair computes 256
 // outputs x 256 inputs. The tensor core's fp32 sums cut off instead of rounding,
 // which bends a long sum towards zero in proportion to its length, so TMEM holds the
-// sum of 1024 tokens at a time (two buffers in turn), and the epilogue warps add
+// sum of at most 512 tokens at a time (two buffers in turn), and the epilogue warps add
 // each to the tile's running sum in their registers, rounded. The last round's tiles
 // are cut into ranges of tokens where they fill it badly (wgrad_plan.h).
 #include <algorithm>
@@ -22,7 +22,13 @@ namespace {
 constexpr int kStages = 6;
 constexpr int kBox = kTok * 128;     // 64 tokens x 64 columns
 constexpr int kOperand = 2 * kBox;   // a CTA's 128 outputs, or 128 inputs
-constexpr int kSegment = 16;         // stages summed in TMEM: 1024 tokens
+// Stages summed in TMEM: 512 tokens of bf16, 256 of fp16, whose products have 22
+// significant bits against 16, so that more of each is cut off (512 tokens of one sign:
+// bf16 9e-7 off, fp16 2.8e-6; 256 of them in bf16 cost 5541 x 1536 x 8960 262 us
+// against 250).
+__host__ __device__ __forceinline__ int segment_of(const GluWgradArgs& a) {
+  return a.fp16 ? 4 : 8;
+}
 constexpr int kEpilogueWarps = 8;
 constexpr int kFirstEpilogue = 4;  // warps 0 TMA, 1 MMA, 2 and 3 idle
 constexpr int kThreads = 32 * (kFirstEpilogue + kEpilogueWarps);
@@ -118,6 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   WgradWork work;
   WgradItem it;
   bool ok = true;
+  const int segment = segment_of(args);
   // One lane of each role walks through the work, waits and issues; the others are
   // at the warp barrier before the closing cluster barrier.
   if (warp == 0) {
@@ -162,8 +169,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tile_place(plan, it.tile, tm, tn);
         const uint32_t idesc = idesc_bf16(kTileM, tile_cols(args.d, tn), true, true) & ~type_bits;
         for (int k = it.kb; k < it.ke; ++k, ++n) {
-          const bool first = (k - it.kb) % kSegment == 0;
-          const bool last = (k - it.kb) % kSegment == kSegment - 1 || k == it.ke - 1;
+          const bool first = ((k - it.kb) & (segment - 1)) == 0;
+          const bool last = ((k - it.kb + 1) & (segment - 1)) == 0 || k == it.ke - 1;
           const uint32_t buf = seg & 1u;
           if (first &&
               !mbar_wait(&tempty_bar[buf], ((seg >> 1) & 1u) ^ 1u, abort_flag, args.status)) {
@@ -209,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < 4; ++c)
 #pragma unroll
         for (int j = 0; j < 32; ++j) sum[c][j] = 0.f;
-      for (int k = it.kb; k < it.ke; k += kSegment, ++seg) {
+      for (int k = it.kb; k < it.ke; k += segment, ++seg) {
         const uint32_t buf = seg & 1u;
         if (!warp_wait(&tfull_bar[buf], (seg >> 1) & 1u, abort_flag, args.status)) {
           ok = false;
