@@ -23,7 +23,7 @@ LIB_PATH = os.path.join(PKG, LIB_NAME)
 
 SOURCES = ["api.cu", "fwd_kernels.cu", "bwd_gemm_launch.cu", "norm_api.cu", "norm_fwd.cu",
            "norm_bwd.cu", "ckpt_kernels.cu", "ckpt_wgrad.cu", "glu_api.cu", "glu_gemm.cu",
-           "glu_wgrad.cu", "adamw.cu"]
+           "glu_small.cu", "glu_wgrad.cu", "adamw.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
               "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

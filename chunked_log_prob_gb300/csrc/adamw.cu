@@ -42,7 +42,7 @@ struct AdamwEntry {
   long long place;  // of its first value in the random numbers' count
   float lr, decay;
   int chunk;        // its first chunk of the launch
-  uint8_t ptype, gtype, ctype, bits;
+  uint8_t ptype, gtype, ctype;
 };
 
 template <int N>
@@ -94,59 +94,94 @@ __device__ __forceinline__ Keys keys_at(const Keys& k, uint32_t high) {
 }
 
 // The first hash of a place: 16 bits for either moment.
-__device__ __forceinline__ uint32_t bits_at(const Keys& k, uint32_t i) {
-  uint32_t x = i ^ k.k0;
-  x ^= x >> 16;
+__device__ __forceinline__ uint32_t bits_after(const Keys& k, uint32_t x) {
   x *= 0x6A09E667u;
   x ^= x >> 15;
   x = x * 0xBB67AE85u + k.k1 * 0xBB67AE85u;
   return x ^ (x >> 16);
 }
+__device__ __forceinline__ uint32_t bits_at(const Keys& k, uint32_t i) {
+  const uint32_t x = i ^ k.k0;
+  return bits_after(k, x ^ (x >> 16));
+}
 // And the second, from the first: 16 bits for the parameter.
 __device__ __forceinline__ uint32_t more_bits(const Keys& k, uint32_t x) {
   const uint32_t y = (x ^ k.k1) * 0x5BE0CD19u;
-  return y ^ (y >> 16);
+  return (y ^ (y >> 16)) & 0xffffu;
 }
 
 // ----------------------------------------------------------- conversions ----
 
-// To e4m3 at random: a (0 <= a <= 448) goes to its lower neighbour lo, or to the upper
-// one hi = lo + step where u < 2^16 (a - lo) / step; u: 0 to 65535. From 2^-6 on the
-// code's bits are those of the fp32, and the 20 bits below them are (a - lo) / step;
-// below, 2^-6 is added, which puts the neighbours, 2^-9 apart, in the same bits.
-struct Scaled {
-  uint32_t w;     // the bits of a, or of a + 2^-6
-  uint32_t zero;  // the code's offset in them
-  bool small;
-};
-__device__ __forceinline__ Scaled scaled(float a) {
-  Scaled s;
-  s.small = a < 0.015625f;
-  s.w = __float_as_uint(s.small ? a + 0.015625f : a);
-  s.zero = s.small ? 121u << 3 : 120u << 3;
-  return s;
+// The high bytes of four words, the first one's lowest.
+__device__ __forceinline__ uint32_t high_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
 }
-__device__ __forceinline__ uint32_t to_e4m3(float a, uint32_t u) {
-  const Scaled s = scaled(a);
-  // The low bits are more than 16 u where this carries out of them.
-  return ((s.w + (((u ^ 0xffffu) << 4) | 15u)) >> 20) - s.zero;
+
+// Eight values y scaled by f (|y f| <= 448) to e4m3 at random: a = |y f| goes to its
+// lower neighbour lo, or to the upper one hi where u < 2^16 (a - lo) / (hi - lo), u
+// the low 16 bits of x.
+//
+// 2^-120 takes e4m3's normal range to fp32's, and its subnormals to fp32's: bits 20 to
+// 26 of the word are lo's code and the 20 below them (a - lo) / (hi - lo), for every
+// a, and the sign is where it was. Adding 2^20 - 1 - 16 u carries into the code where
+// those are more than 16 u.
+__device__ __forceinline__ uint2 codes_of(const float (&y)[8], float f, const uint32_t (&x)[8]) {
+  uint32_t s[8], t[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t w = __float_as_uint((y[j] * f) * 0x1p-120f);
+    s[j] = (w + 0xfffffu) - 16u * (x[j] & 0xffffu);
+    t[j] = s[j] * 16u;
+  }
+  constexpr uint32_t kSigns = 0x80808080u;
+  return make_uint2(high_bytes(t[0], t[1], t[2], t[3]) | (high_bytes(s[0], s[1], s[2], s[3]) & kSigns),
+                    high_bytes(t[4], t[5], t[6], t[7]) | (high_bytes(s[4], s[5], s[6], s[7]) & kSigns));
 }
-// The same by the squares: u < 2^16 (a^2 - lo^2) / (hi^2 - lo^2). In units of step,
-// z = a and k = lo: u (2 k + 1) < 2^16 (z - k) (z + k).
-__device__ __forceinline__ uint32_t to_e4m3_square(float a, uint32_t u) {
-  const Scaled s = scaled(a);
-  const float off = s.small ? 8.f : 0.f;
-  const float z = __uint_as_float((s.w & 0x007fffffu) | 0x41000000u) - off;  // 8 to 16
-  const float k = __uint_as_float((s.w & 0x00700000u) | 0x41000000u) - off;
-  const float q = __uint_as_float((u << 7) | 0x3f800000u) - 1.f;  // u / 2^16
-  const bool up = q * fmaf(2.f, k, 1.f) < (z - k) * (z + k);
-  return (s.w >> 20) - s.zero + (up ? 1u : 0u);
+
+// The same of roots (y >= 0) by their squares: u < 2^16 (a^2 - lo^2) / (hi^2 - lo^2), u
+// the high 16 bits of x. A y beyond `some` never becomes 0.
+__device__ __forceinline__ uint2 codes_of_roots(const float (&y)[8], float f,
+                                                const uint32_t (&x)[8], float some) {
+  uint32_t t[8], least = 0xffffffffu;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float a = y[j] * f;
+    const uint32_t w = __float_as_uint(a * 0x1p-120f);
+    const uint32_t lo = w & 0xfff00000u, hi = lo + 0x100000u;
+    const float l = __uint_as_float(lo) * 0x1p120f, h = __uint_as_float(hi) * 0x1p120f;
+    const float q = __uint_as_float(((x[j] >> 9) & 0x007fff80u) | 0x3f800000u) - 1.f;  // u / 2^16
+    t[j] = (q * ((h - l) * (h + l)) < (a - l) * (a + l) ? hi : lo) * 16u;
+    least = min(least, w);
+  }
+  if (least < 0x100000u) {  // rare: a value, or a zero, below the least code
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (y[j] > some) t[j] = max(t[j], 0x1000000u);
+  }
+  return make_uint2(high_bytes(t[0], t[1], t[2], t[3]), high_bytes(t[4], t[5], t[6], t[7]));
+}
+
+// Codes whose values are not finite, as NaN.
+__device__ __forceinline__ void lose(const float (&y)[8], uint2& q) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    uint32_t& w = j < 4 ? q.x : q.y;
+    const int at = 8 * (j & 3);
+    if (!(fabsf(y[j]) <= FLT_MAX))
+      w = (w & ~(0xffu << at)) | static_cast<uint32_t>(kCkptNaN) << at;
+  }
 }
 
 // Off by 2^-23 of itself at most; where v is subnormal too.
 __device__ __forceinline__ float quick_root(float v) {
   float r;
   asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+// Off by 2^-23 of itself at most, for 0 and 2^-126 to 2^126.
+__device__ __forceinline__ float quick_inverse(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
 
@@ -172,16 +207,6 @@ __device__ __forceinline__ void store8(void* p, long long i, const float (&v)[8]
   const uint4* w = reinterpret_cast<const uint4*>(&r);
 #pragma unroll
   for (int k = 0; k < static_cast<int>(sizeof(r) / 16); ++k) __stcs(d + k, w[k]);
-}
-
-// fp32 to bf16 rounded at random: 16 random bits below the kept ones, then cut off.
-__device__ __forceinline__ float random_bf16(float p, uint32_t bits) {
-  const uint32_t w = __float_as_uint(p);
-  const uint32_t r = (w + (bits & 0xffffu)) & 0xffff0000u;
-  // Infinities and NaN as they are (a NaN of low bits alone made a whole one).
-  if ((w & 0x7f800000u) == 0x7f800000u)
-    return __uint_as_float((w & 0x7fffffu) != 0 ? 0x7fc00000u : w);
-  return __uint_as_float(r);
 }
 
 // ------------------------------------------------------------------ step ----
@@ -270,19 +295,33 @@ __device__ __forceinline__ void step8(const AdamwEntry& e, const StepOf& s, long
     }
   }
   float root[8];
+  {
+    const f32x2 scale = pair(s.scale, s.scale), beta1 = pair(s.beta1, s.beta1),
+                beta2 = pair(s.beta2, s.beta2), rest1 = pair(s.rest1, s.rest1),
+                rest2 = pair(s.rest2, s.rest2), fix2 = pair(s.fix2, s.fix2),
+                eps = pair(s.eps, s.eps), rate = pair(-s.rate, -s.rate),
+                shrink = pair(s.shrink, s.shrink), ms2 = pair(ms, ms), vs2 = pair(vs, vs);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if (BITS == 8) {
-      m[j] *= ms;
-      const float r = v[j] * vs;
-      v[j] = r * r;
+    for (int j = 0; j < 8; j += 2) {
+      f32x2 m2 = pair(m[j], m[j + 1]), v2 = pair(v[j], v[j + 1]);
+      if (BITS == 8) {
+        m2 = mul2(m2, ms2);
+        v2 = mul2(v2, vs2);
+        v2 = mul2(v2, v2);
+      }
+      const f32x2 x2 = mul2(pair(g[j], g[j + 1]), scale);
+      m2 = fma2(beta1, m2, mul2(rest1, x2));
+      v2 = fma2(beta2, v2, mul2(rest2, mul2(x2, x2)));
+      split(m2, m[j], m[j + 1]);
+      split(v2, v[j], v[j + 1]);
+      root[j] = quick_root(v[j]);
+      root[j + 1] = quick_root(v[j + 1]);
+      float d0, d1;
+      split(fma2(pair(root[j], root[j + 1]), fix2, eps), d0, d1);
+      // d is 0 or normal: a root of at least 2^-75, or eps
+      const f32x2 step = mul2(mul2(rate, m2), pair(quick_inverse(d0), quick_inverse(d1)));
+      split(fma2(pair(p[j], p[j + 1]), shrink, step), p[j], p[j + 1]);
     }
-    const float x = g[j] * s.scale;
-    m[j] = s.beta1 * m[j] + s.rest1 * x;
-    v[j] = s.beta2 * v[j] + s.rest2 * (x * x);
-    root[j] = quick_root(v[j]);
-    // the quick division: off by 2 units at most, of the step alone
-    p[j] = p[j] * s.shrink - __fdividef(s.rate * m[j], root[j] * s.fix2 + s.eps);
   }
   if constexpr (BITS == 32 && VEC) {
     store8<float>(e.m, first, m);
@@ -302,51 +341,51 @@ __device__ __forceinline__ void step8(const AdamwEntry& e, const StepOf& s, long
     // A lane's values lie in one block, which no multiple of 2^32 parts.
     const uint64_t place = static_cast<uint64_t>(e.place + first);
     keys = keys_at(s.keys, static_cast<uint32_t>(place >> 32));
+    // Consecutive places, from a multiple of 8 on, differ below what the first fold
+    // moves.
+    const uint32_t head = static_cast<uint32_t>(place) ^ keys.k0;
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      x[j] = bits_at(keys, static_cast<uint32_t>(place) + j * kEvery);
+      x[j] = VEC ? bits_after(keys, (head ^ (head >> 16)) ^ j)
+                 : bits_at(keys, static_cast<uint32_t>(place) + j * kEvery);
   }
   if constexpr (BITS == 8) {
     float mt = block_top(m), vt = block_top(root);
-    // Nothing in the warp's blocks is special (the usual case).
-    const bool plain = __all_sync(0xffffffffu, mt <= FLT_MAX && vt <= FLT_MAX);
-    if (!plain) {
+    float mi, vi;
+    // Nothing in the warp's blocks is special (the usual case). The quick factor and
+    // its product are off by 2^-22 at most, so it is taken 3 2^-23 lower: no value
+    // passes 448, and the largest, 9 of its word's units below at most, goes there.
+    constexpr float kLow = 1.f - 3 * 0x1p-23f, kMost = 0x1p125f;
+    const bool plain = __all_sync(0xffffffffu, mt >= kLeast && mt <= kMost && vt >= kLeast &&
+                                                   vt <= kMost);
+    if (plain) {
+      mi = kTop * kLow * quick_inverse(mt);
+      vi = kTop * kLow * quick_inverse(vt);
+    } else {
       mt = block_top_finite(m[0], m[1], m[2], m[3], m[4], m[5], m[6], m[7]);
       vt = block_top_finite(root[0], root[1], root[2], root[3], root[4], root[5], root[6], root[7]);
+      mt = mt >= kLeast ? mt : 0.f;
+      vt = vt >= kLeast ? vt : 0.f;
+      mi = mt > 0.f ? __fdiv_rz(kTop, mt) : 0.f;
+      vi = vt > 0.f ? __fdiv_rz(kTop, vt) : 0.f;
     }
-    mt = mt >= kLeast ? mt : 0.f;
-    vt = vt >= kLeast ? vt : 0.f;
-    const float mi = mt > 0.f ? kTop / mt : 0.f, vi = vt > 0.f ? kTop / vt : 0.f;
-    const float some = vt > 0.f ? 0.f : FLT_MAX;  // a root beyond it never becomes 0
-    uint32_t mq[8], vq[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      mq[j] = to_e4m3(fminf(fabsf(m[j]) * mi, kTop), x[j] & 0xffffu);
-      mq[j] |= (__float_as_uint(m[j]) >> 24) & 0x80u;
-      const float a = fminf(root[j] * vi, kTop);
-      vq[j] = to_e4m3_square(root[j] > some ? fmaxf(a, 0.001953125f) : a, x[j] >> 16);
-    }
+    uint2 mq = codes_of(m, mi, x);
+    uint2 vq = codes_of_roots(root, vi, x, vt > 0.f ? 0.f : FLT_MAX);
     if (!plain) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (!(fabsf(m[j]) <= FLT_MAX)) mq[j] = kCkptNaN;
-        if (!(root[j] <= FLT_MAX)) vq[j] = kCkptNaN;
-      }
+      lose(m, mq);
+      lose(root, vq);
     }
     if constexpr (VEC) {
-      uint2 a, b;
-      a.x = mq[0] | mq[1] << 8 | mq[2] << 16 | mq[3] << 24;
-      a.y = mq[4] | mq[5] << 8 | mq[6] << 16 | mq[7] << 24;
-      b.x = vq[0] | vq[1] << 8 | vq[2] << 16 | vq[3] << 24;
-      b.y = vq[4] | vq[5] << 8 | vq[6] << 16 | vq[7] << 24;
-      __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(e.m) + first), a);
-      __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(e.v) + first), b);
+      __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(e.m) + first), mq);
+      __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(e.v) + first), vq);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (have[j]) {
-          static_cast<uint8_t*>(e.m)[first + j * kEvery] = static_cast<uint8_t>(mq[j]);
-          static_cast<uint8_t*>(e.v)[first + j * kEvery] = static_cast<uint8_t>(vq[j]);
+          static_cast<uint8_t*>(e.m)[first + j * kEvery] =
+              static_cast<uint8_t>((j < 4 ? mq.x : mq.y) >> (8 * (j & 3)));
+          static_cast<uint8_t*>(e.v)[first + j * kEvery] =
+              static_cast<uint8_t>((j < 4 ? vq.x : vq.y) >> (8 * (j & 3)));
         }
     }
     if ((lane & 15) == 0 && have[0]) {
@@ -355,11 +394,33 @@ __device__ __forceinline__ void step8(const AdamwEntry& e, const StepOf& s, long
     }
   }
   if constexpr (sizeof(P) == 2) {
+    // To bf16 at random: 16 random bits below the kept ones, then cut off; infinities
+    // and NaN as they are.
+    float top = max_abs_nan(p[0], p[1], p[2]);
+    top = max_abs_nan(max_abs_nan(top, p[3], p[4]), max_abs_nan(p[5], p[6], p[7]), p[0]);
+    uint32_t w[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) p[j] = random_bf16(p[j], more_bits(keys, x[j]));
+    for (int j = 0; j < 8; ++j)
+      w[j] = (__float_as_uint(p[j]) + more_bits(keys, x[j])) & 0xffff0000u;
+    if (!(top <= FLT_MAX)) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (!(fabsf(p[j]) <= FLT_MAX)) w[j] = __float_as_uint(p[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p[j] = __uint_as_float(w[j]);
   }
   if constexpr (VEC) {
-    store8<P>(e.param, first, p);
+    if constexpr (sizeof(P) == 2) {  // already bf16s
+      uint4 w;
+      w.x = __byte_perm(__float_as_uint(p[0]), __float_as_uint(p[1]), 0x7632);
+      w.y = __byte_perm(__float_as_uint(p[2]), __float_as_uint(p[3]), 0x7632);
+      w.z = __byte_perm(__float_as_uint(p[4]), __float_as_uint(p[5]), 0x7632);
+      w.w = __byte_perm(__float_as_uint(p[6]), __float_as_uint(p[7]), 0x7632);
+      __stcs(reinterpret_cast<uint4*>(static_cast<P*>(e.param) + first), w);
+    } else {
+      store8<P>(e.param, first, p);
+    }
     if (e.copy != nullptr) {
       if (e.ctype == GRPO_DTYPE_BF16)
         store8<__nv_bfloat16>(e.copy, first, p);
@@ -427,8 +488,8 @@ __device__ __forceinline__ int find_entry(const E* e, int count, int c) {
   return lo;
 }
 
-template <int N>
-__global__ void __launch_bounds__(kThreads)
+template <int N, int BITS>
+__global__ void __launch_bounds__(kThreads, 4)
     adamw_kernel(const __grid_constant__ AdamwTable<N> table, const AdamwArgs args) {
   const float scale = args.scale != nullptr ? *args.scale : 1.f;
   if (!(fabsf(scale) <= FLT_MAX)) return;  // the step is skipped
@@ -456,17 +517,10 @@ __global__ void __launch_bounds__(kThreads)
   s.eps = args.eps;
   s.keys = keys_of(args.seed, static_cast<uint64_t>(step));
   const long long begin = static_cast<long long>(c - e.chunk) * args.chunk;
-  if (e.bits == 32) {
-    if (e.ptype == GRPO_DTYPE_FP32)
-      step_grad<32, float>(e, s, begin, args.chunk);
-    else
-      step_grad<32, __nv_bfloat16>(e, s, begin, args.chunk);
-  } else {
-    if (e.ptype == GRPO_DTYPE_FP32)
-      step_grad<8, float>(e, s, begin, args.chunk);
-    else
-      step_grad<8, __nv_bfloat16>(e, s, begin, args.chunk);
-  }
+  if (e.ptype == GRPO_DTYPE_FP32)
+    step_grad<BITS, float>(e, s, begin, args.chunk);
+  else
+    step_grad<BITS, __nv_bfloat16>(e, s, begin, args.chunk);
 }
 
 // ------------------------------------------------------------------ norm ----
@@ -577,13 +631,13 @@ __global__ void __launch_bounds__(kThreads)
   out[1] = scale;
 }
 
-template <int N>
+template <int N, int BITS>
 cudaError_t launch_adamw(const AdamwEntry* e, const AdamwArgs& a, int chunks, cudaStream_t st) {
   AdamwTable<N> table;
   std::copy(e, e + a.count, table.e);
   std::fill(table.e + a.count, table.e + N, AdamwEntry());
   LaunchTimer timer("adamw_kernel", st);
-  adamw_kernel<N><<<chunks, kThreads, 0, st>>>(table, a);
+  adamw_kernel<N, BITS><<<chunks, kThreads, 0, st>>>(table, a);
   return cudaGetLastError();
 }
 
@@ -746,46 +800,52 @@ int grpo_adamw_step(const grpo_adamw_tensor* tensors, int32_t count,
   a.lr_factor = q.lr_factor;
   a.step_on_device = q.step_on_device;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // Tensors with moments of either kind have launches of their own.
   AdamwEntry e[kLargeTable];
-  int64_t chunks = 0, place = 0;
-  a.count = 0;
-  auto flush = [&]() {
-    if (a.count == 0) return cudaSuccess;
-    const int c = static_cast<int>(chunks);
-    const cudaError_t err = a.count <= kSmallTable ? launch_adamw<kSmallTable>(e, a, c, st)
-                                                   : launch_adamw<kLargeTable>(e, a, c, st);
+  for (const int bits : {32, 8}) {
+    int64_t chunks = 0, place = 0;
     a.count = 0;
-    chunks = 0;
-    return err;
-  };
-  for (int i = 0; i < count; ++i) {
-    const grpo_adamw_tensor& x = tensors[i];
-    const int64_t at = place;
-    place += (x.numel + kBlock - 1) / kBlock * kBlock;
-    if (x.numel == 0 || x.grad == nullptr) continue;
-    const int64_t more = (x.numel + a.chunk - 1) / a.chunk;
-    if ((a.count == kLargeTable || chunks + more > (1LL << 30)) && flush() != cudaSuccess)
-      return GRPO_ERR_CUDA;
-    AdamwEntry& d = e[a.count++];
-    d.param = x.param;
-    d.grad = x.grad;
-    d.m = x.m;
-    d.v = x.v;
-    d.m_scale = x.m_scale;
-    d.v_scale = x.v_scale;
-    d.copy = x.copy_or_null;
-    d.numel = x.numel;
-    d.place = at;
-    d.lr = x.lr;
-    d.decay = x.weight_decay;
-    d.chunk = static_cast<int>(chunks);
-    d.ptype = static_cast<uint8_t>(x.param_dtype);
-    d.gtype = static_cast<uint8_t>(x.grad_dtype);
-    d.ctype = static_cast<uint8_t>(x.copy_dtype);
-    d.bits = static_cast<uint8_t>(x.state_bits);
-    chunks += more;
+    auto flush = [&]() {
+      if (a.count == 0) return cudaSuccess;
+      const int c = static_cast<int>(chunks);
+      const bool few = a.count <= kSmallTable;
+      const cudaError_t err = bits == 32 ? (few ? launch_adamw<kSmallTable, 32>(e, a, c, st)
+                                                : launch_adamw<kLargeTable, 32>(e, a, c, st))
+                                         : (few ? launch_adamw<kSmallTable, 8>(e, a, c, st)
+                                                : launch_adamw<kLargeTable, 8>(e, a, c, st));
+      a.count = 0;
+      chunks = 0;
+      return err;
+    };
+    for (int i = 0; i < count; ++i) {
+      const grpo_adamw_tensor& x = tensors[i];
+      const int64_t at = place;
+      place += (x.numel + kBlock - 1) / kBlock * kBlock;
+      if (x.numel == 0 || x.grad == nullptr || x.state_bits != bits) continue;
+      const int64_t more = (x.numel + a.chunk - 1) / a.chunk;
+      if ((a.count == kLargeTable || chunks + more > (1LL << 30)) && flush() != cudaSuccess)
+        return GRPO_ERR_CUDA;
+      AdamwEntry& d = e[a.count++];
+      d.param = x.param;
+      d.grad = x.grad;
+      d.m = x.m;
+      d.v = x.v;
+      d.m_scale = x.m_scale;
+      d.v_scale = x.v_scale;
+      d.copy = x.copy_or_null;
+      d.numel = x.numel;
+      d.place = at;
+      d.lr = x.lr;
+      d.decay = x.weight_decay;
+      d.chunk = static_cast<int>(chunks);
+      d.ptype = static_cast<uint8_t>(x.param_dtype);
+      d.gtype = static_cast<uint8_t>(x.grad_dtype);
+      d.ctype = static_cast<uint8_t>(x.copy_dtype);
+      chunks += more;
+    }
+    if (flush() != cudaSuccess) return GRPO_ERR_CUDA;
   }
-  return flush() == cudaSuccess ? GRPO_OK : GRPO_ERR_CUDA;
+  return GRPO_OK;
 }
 
 }  // extern "C"

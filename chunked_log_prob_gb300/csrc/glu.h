@@ -34,6 +34,9 @@ struct GluArgs {
 
 // act(x Wg^T) * (x Wu^T) for any number of rows.
 cudaError_t launch_glu_fwd(const GluArgs& a, int sms, cudaStream_t st);
+// The same (but no checkpoint) for up to kGluSmallRows of them.
+constexpr int kGluSmallRows = 8;
+cudaError_t launch_glu_small(const GluArgs& a, int sms, cudaStream_t st);
 // The gradients of the projections, which are computed again.
 cudaError_t launch_glu_bwd_again(const GluArgs& a, int sms, cudaStream_t st);
 // The same from the projections as they were kept.

@@ -96,8 +96,20 @@ int grpo_glu_fwd(const void* x, const void* w_gate, const void* w_up, const uint
   a.ldu = stride_or(desc->up_stride, desc->inner);
   a.ck = ckpt_view(ckpt, desc->n_tokens, desc->inner);
   a.lost = take_lost();
-  return launch_glu_fwd(a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GRPO_OK
-                                                                                  : GRPO_ERR_CUDA;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (a.n > kGluSmallRows)
+    return launch_glu_fwd(a, sms, st) == cudaSuccess ? GRPO_OK : GRPO_ERR_CUDA;
+  if (launch_glu_small(a, sms, st) != cudaSuccess) return GRPO_ERR_CUDA;
+  if (ckpt == nullptr) return GRPO_OK;
+  CkptArgs c;  // few rows are seldom kept: a launch of its own
+  c.x = h;
+  c.out = h;
+  c.mask = mask;
+  c.ck = a.ck;
+  c.n = a.n;
+  c.ld = a.ldh;
+  c.d = a.f;
+  return launch_ckpt_pack(c, desc->dtype, true, sms, st) == cudaSuccess ? GRPO_OK : GRPO_ERR_CUDA;
 }
 
 int grpo_glu_bwd(const void* dh, const void* x, const void* w_gate, const void* w_up,

@@ -31,25 +31,79 @@ constexpr int kBK = 64;                  // columns of a stage: 128 bytes
 constexpr int kOperand = 128 * kBK * 2;  // a CTA's 128 rows of either operand
 constexpr int kBox = kBK * 128;          // 64 rows x 64 columns of an MN-major operand
 constexpr int kEpilogueWarps = 8;
-constexpr int kFirstEpilogue = 4;  // warps 0 TMA, 1 MMA, 2 and 3 idle
+constexpr int kFirstEpilogue = 4;  // warps 0 TMA, 1 MMA, 2 and 3 zeros of masked segments
 constexpr int kThreads = 32 * (kFirstEpilogue + kEpilogueWarps);
-constexpr int kSmem = 1024 + 2 * kStages * kOperand;
+constexpr int kSeg = 16;               // rows of a segment
+constexpr int kTileSegs = 256 / kSeg;
+// Segments that a CTA lists (2 bytes each): 131072 rows. Beyond them masked rows are
+// computed like the others, and their zeros written in the epilogue.
+constexpr int kMostSegs = 8192;
+constexpr int kSmem = 1024 + 2 * kStages * kOperand + 2 * kMostSegs;
+static_assert(kSmem <= 227 * 1024 - 1024, "shared memory of a CTA");
 constexpr uint32_t kTmemCols = 512;
 
-// The launch's tiles: 256 rows x 128 columns of f (256 of d for dx), dealt round
-// robin to the pairs, column by column within groups of row tiles.
+// The launch's tiles: 256 rows x `cols` columns of f (of d for dx), dealt round robin
+// to the pairs, column by column within groups of row tiles.
 struct GluPlan {
-  int n_m, n_n, tiles;
+  int n_m, n_n;
   int kt, kt2;  // stages of the first operand pair, and of both
   int group;    // row tiles of a group
+  int cols;     // forward and again: 128 or 64; dx: 256 or 128
+  int segs;     // segments to list, 0: tiles are of consecutive rows
 };
 
-__device__ __forceinline__ void place(const GluPlan& p, int tile, int& m, int& n) {
+__device__ __forceinline__ void place(const GluPlan& p, int n_m, int tile, int& m, int& n) {
   const int per_group = p.group * p.n_n;
   const int g = tile / per_group, r = tile - g * per_group;
-  const int rows = least(p.group, p.n_m - g * p.group);
+  const int rows = least(p.group, n_m - g * p.group);
   n = r / rows;
   m = g * p.group + (r - n * rows);
+}
+
+// Whether a segment holds a row that counts.
+__device__ __forceinline__ bool segment_lives(const uint8_t* mask, long long n, int seg) {
+  const long long r0 = static_cast<long long>(seg) * kSeg;
+  const uint8_t* p = mask + r0;
+  if (r0 + kSeg <= n && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    return (v.x | v.y | v.z | v.w) != 0;
+  }
+  bool any = false;
+  for (int i = 0; i < kSeg && r0 + i < n; ++i) any = any || p[i] != 0;
+  return any;
+}
+
+// Lists the segments of all rows: those that live first, in order, then the others.
+// All threads of the CTA call this. Returns how many live.
+__device__ __forceinline__ int list_segments(const uint8_t* mask, long long n, int segs,
+                                             uint16_t* list, int* scratch) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int each = (segs + kThreads - 1) / kThreads;
+  const int a = least(static_cast<int>(threadIdx.x) * each, segs), b = least(a + each, segs);
+  int mine = 0;
+  for (int s = a; s < b; ++s) mine += segment_lives(mask, n, s) ? 1 : 0;
+  int before = mine;  // inclusive sums, of the warp and then of the warps
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += v;
+  }
+  if (lane == 31) scratch[warp] = before;
+  __syncthreads();
+  int live = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w == warp) before += live - mine;
+    live += scratch[w];
+  }
+  int other = live + a - before;  // where this thread's first dead one goes
+  for (int s = a; s < b; ++s) {
+    if (segment_lives(mask, n, s))
+      list[before++] = static_cast<uint16_t>(s);
+    else
+      list[other++] = static_cast<uint16_t>(s);
+  }
+  __syncthreads();
+  return live;
 }
 
 __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
@@ -97,6 +151,44 @@ __device__ __forceinline__ void store32(void* base, long long at, const uint32_t
     if (8 * j < left) st_global_v4(p + 8 * j, w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
 }
 
+// The same of 16 columns, and their loads (zeros past `left`).
+template <typename T>
+__device__ __forceinline__ void store16(void* base, long long at, const uint32_t (&w)[8],
+                                        int left) {
+  T* p = static_cast<T*>(base) + at;
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    if (8 * j < left) st_global_v4(p + 8 * j, w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+}
+template <typename T>
+__device__ __forceinline__ void load16(const T* p, uint32_t (&w)[8], int left) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (8 * j < left) x = *reinterpret_cast<const uint4*>(p + 8 * j);
+    w[4 * j] = x.x;
+    w[4 * j + 1] = x.y;
+    w[4 * j + 2] = x.z;
+    w[4 * j + 3] = x.w;
+  }
+}
+
+// 16 TMEM columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
 // A checkpoint block that one thread holds: 32 values as stored.
 template <typename T>
 __device__ __forceinline__ void ckpt_store32(const uint32_t (&w)[16], uint8_t* q, uint8_t* ex,
@@ -132,10 +224,17 @@ __device__ __forceinline__ void ckpt_store32(const uint32_t (&w)[16], uint8_t* q
   *ex = static_cast<uint8_t>(k + kCkptBias);
 }
 
+// Columns of a dx tile's MMAs: half of them where no more are left.
+__device__ __forceinline__ int dx_cols(const GluPlan& p, int d, int tn) {
+  return p.cols == kTileN ? tile_cols(d, tn) : p.cols;
+}
+
 template <int MODE, typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     glu_gemm_kernel(const __grid_constant__ CUtensorMap map_a0,
                     const __grid_constant__ CUtensorMap map_a1,
+                    const __grid_constant__ CUtensorMap map_s0,
+                    const __grid_constant__ CUtensorMap map_s1,
                     const __grid_constant__ CUtensorMap map_b0,
                     const __grid_constant__ CUtensorMap map_b1, const GluArgs args,
                     const GluPlan plan) {
@@ -146,9 +245,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t drain_bar;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh, status_sh;
+  __shared__ int scratch[kThreads / 32];
 
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* const ring = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+  uint16_t* const list = reinterpret_cast<uint16_t*>(ring + 2 * kStages * kOperand);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int pair = static_cast<int>(blockIdx.x) / 2, pairs = static_cast<int>(gridDim.x) / 2;
@@ -176,11 +277,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc_pair(&tmem_base_sh, kTmemCols);
     tmem_relinquish_pair();
   }
+  const int live_segs =
+      plan.segs > 0 ? list_segments(args.mask, args.n, plan.segs, list, scratch) : 0;
+  const int n_m = plan.segs > 0 ? (live_segs + kTileSegs - 1) / kTileSegs : plan.n_m;
+  const int tiles = n_m * plan.n_n;
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
+  if constexpr (MODE == kDx)
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // dgate and dup are there
+  else
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem_base = tmem_base_sh;
   const int stages = MODE == kDx ? plan.kt2 : plan.kt;
+  // Row of this CTA's row i of a row tile; args.n where there is none.
+  auto row_of = [&](int tm, int i) -> long long {
+    if (plan.segs == 0)
+      return min(static_cast<long long>(tm) * kTileM + static_cast<int>(rank) * 128 + i, args.n);
+    const int s = tm * kTileSegs + static_cast<int>(rank) * (kTileSegs / 2) + i / kSeg;
+    return s < live_segs
+               ? min(static_cast<long long>(list[s]) * kSeg + (i & (kSeg - 1)), args.n)
+               : args.n;
+  };
 
   bool ok = true;
   // One lane of each role walks through the work, waits and issues; the others are
@@ -189,12 +307,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------ tiles by TMA --
     if (elect_one()) {
       uint32_t n = 0;  // stages issued
-      for (int tile = pair; ok && tile < plan.tiles; tile += pairs) {
+      // dx: half a tile's columns are a box of 64, or two
+      const bool two = MODE == kDx && plan.cols == kTileN;
+      const uint32_t b_bytes =
+          MODE == kDx ? (two ? kOperand : kBox) : static_cast<uint32_t>(plan.cols) * kBK * 2;
+      for (int tile = pair; ok && tile < tiles; tile += pairs) {
         int tm, tn;
-        place(plan, tile, tm, tn);
-        const int m0 = tm * kTileM + static_cast<int>(rank) * 128;
-        const int n0 = MODE == kDx ? tn * kTileN + static_cast<int>(rank) * (tile_cols(args.d, tn) / 2)
-                                   : tn * 128;
+        place(plan, n_m, tile, tm, tn);
+        int rows[kTileSegs / 2];  // where the tile's segments begin
+#pragma unroll
+        for (int j = 0; j < kTileSegs / 2; ++j) rows[j] = static_cast<int>(row_of(tm, j * kSeg));
+        const bool together =
+            plan.segs == 0 || rows[kTileSegs / 2 - 1] - rows[0] == 128 - kSeg;
+        const int n0 = tn * plan.cols + (MODE == kDx ? static_cast<int>(rank) *
+                                                           (dx_cols(plan, args.d, tn) / 2)
+                                                     : 0);
         for (int k = 0; k < stages; ++k, ++n) {
           const uint32_t s = n % kStages;
           if (!mbar_wait(&done_bar[s], ((n / kStages) & 1u) ^ 1u, abort_flag, &status_sh)) {
@@ -203,20 +330,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (n == args.lost && blockIdx.x == 0) continue;
           const uint32_t lead = mapa_shared(smem_u32(&full_bar[s]), 0);
-          mbar_arrive_expect_tx_cluster(lead, 2 * kOperand);
+          mbar_arrive_expect_tx_cluster(lead, kOperand + b_bytes);
           uint8_t* a = ring + s * 2 * kOperand;
           uint8_t* b = a + kOperand;
-          if constexpr (MODE == kDx) {
-            const bool second = k >= plan.kt;
-            const int k0 = (second ? k - plan.kt : k) * kBK;
-            const CUtensorMap* ma = second ? &map_a1 : &map_a0;
-            const CUtensorMap* mb = second ? &map_b1 : &map_b0;
-            tma_load_2d_pair_nohint(a, ma, lead, k0, m0);
-            tma_load_2d_pair_nohint(b, mb, lead, n0, k0);
-            tma_load_2d_pair_nohint(b + kBox, mb, lead, n0 + 64, k0);
+          const bool second = MODE == kDx && k >= plan.kt;
+          const int k0 = (second ? k - plan.kt : k) * kBK;
+          if (together) {
+            tma_load_2d_pair_nohint(a, second ? &map_a1 : &map_a0, lead, k0, rows[0]);
           } else {
-            tma_load_2d_pair_nohint(a, &map_a0, lead, k * kBK, m0);
-            tma_load_2d_pair_nohint(b, rank == 0 ? &map_b0 : &map_b1, lead, k * kBK, n0);
+            const CUtensorMap* ms = second ? &map_s1 : &map_s0;
+#pragma unroll
+            for (int j = 0; j < kTileSegs / 2; ++j)
+              tma_load_2d_pair_nohint(a + j * kSeg * kBK * 2, ms, lead, k0, rows[j]);
+          }
+          if constexpr (MODE == kDx) {
+            const CUtensorMap* mb = second ? &map_b1 : &map_b0;
+            tma_load_2d_pair_nohint(b, mb, lead, n0, k0);
+            if (two) tma_load_2d_pair_nohint(b + kBox, mb, lead, n0 + 64, k0);
+          } else {
+            tma_load_2d_pair_nohint(b, rank == 0 ? &map_b0 : &map_b1, lead, k0, n0);
           }
         }
       }
@@ -230,11 +362,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elect_one()) {
       uint32_t n = 0, t = 0;  // stages, tiles issued
       const uint32_t type_bits = args.fp16 ? (1u << 7) | (1u << 10) : 0u;
-      for (int tile = pair; ok && tile < plan.tiles; tile += pairs, ++t) {
+      for (int tile = pair; ok && tile < tiles; tile += pairs, ++t) {
         int tm, tn;
-        place(plan, tile, tm, tn);
+        place(plan, n_m, tile, tm, tn);
         const uint32_t idesc =
-            idesc_bf16(kTileM, MODE == kDx ? tile_cols(args.d, tn) : kTileN, false, MODE == kDx) &
+            idesc_bf16(kTileM, MODE == kDx ? dx_cols(plan, args.d, tn) : 2 * plan.cols, false,
+                       MODE == kDx) &
             ~type_bits;
         const uint32_t buf = t & 1u;
         if (!mbar_wait(&tempty_bar[buf], ((t >> 1) & 1u) ^ 1u, abort_flag, &status_sh)) {
@@ -263,6 +396,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_commit_pair(&drain_bar);
       drain(&drain_bar, 0);
     }
+  } else if (warp < kFirstEpilogue && warp > 1) {
+    // ------------------------------------- zeros of the masked segments --
+    const int width = MODE == kDx ? args.d : args.f;
+    for (int i = live_segs + static_cast<int>(blockIdx.x); i < plan.segs;
+         i += static_cast<int>(gridDim.x)) {
+#pragma unroll 1
+      for (int r = 0; r < kSeg; ++r) {
+        const long long row = static_cast<long long>(list[i]) * kSeg + r;
+        if (row >= args.n) break;
+        for (int c = (static_cast<int>(threadIdx.x) - 64) * 8; c < width; c += 64 * 8) {
+          if (MODE == kDx) {
+            st_global_v4(static_cast<T*>(args.dx) + row * args.lddx + c, 0u, 0u, 0u, 0u);
+            continue;
+          }
+          if (args.h != nullptr)
+            st_global_v4(static_cast<T*>(args.h) + row * args.ldh + c, 0u, 0u, 0u, 0u);
+          if (args.gate != nullptr)
+            st_global_v4(static_cast<T*>(args.gate) + row * args.ldg + c, 0u, 0u, 0u, 0u);
+          if (args.up != nullptr)
+            st_global_v4(static_cast<T*>(args.up) + row * args.ldu + c, 0u, 0u, 0u, 0u);
+          if (args.ck.q != nullptr) {
+            *reinterpret_cast<uint2*>(args.ck.q + row * args.ck.ldq + c) = make_uint2(0u, 0u);
+            args.ck.ex[row * args.ck.lde + c / kCkptBlock] =
+                static_cast<uint8_t>(kCkptMinExp + kCkptBias);
+          }
+        }
+      }
+    }
   } else if (warp >= kFirstEpilogue) {
     // ---------------------------------------------------------- epilogue --
     // A thread holds one row's half of the tile's columns.
@@ -272,14 +433,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t t0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
     uint32_t t = 0;
     int tile = pair;
-    for (; tile < plan.tiles; tile += pairs, ++t) {
+    for (; tile < tiles; tile += pairs, ++t) {
       int tm, tn;
-      place(plan, tile, tm, tn);
-      const long long row =
-          static_cast<long long>(tm) * kTileM + static_cast<int>(rank) * 128 + q * 32 + lane;
+      place(plan, n_m, tile, tm, tn);
+      const long long row = row_of(tm, q * 32 + lane);
       const uint32_t buf = t & 1u;
       const bool there = row < args.n;
       const bool live = there && (args.mask == nullptr || args.mask[row] != 0);
+      // The first of dh comes while the tile's sums do, each next one a step ahead.
+      uint32_t ahead[8];
+      if constexpr (MODE == kAgain) {
+        const int f0 = tn * plan.cols + half * (plan.cols / 2);
+        load16<T>(static_cast<const T*>(args.dh) + row * args.lddh + f0, ahead,
+                  live ? args.f - f0 : 0);
+      }
       if (!warp_wait(&tfull_bar[buf], (t >> 1) & 1u, abort_flag, &status_sh)) {
         ok = false;
         break;
@@ -288,9 +455,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t acc = t0 + buf * kTileN;
       if constexpr (MODE == kDx) {
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          const int col = half * 128 + c * 32;
-          const int left = args.d - (tn * kTileN + col);
+        for (int c = 0; c < plan.cols / 64; ++c) {
+          const int col = half * (plan.cols / 2) + c * 32;
+          const int left = args.d - (tn * plan.cols + col);
           float v[32];
           tmem_ld32(acc + col, v);
           if (there && left > 0) {
@@ -298,21 +465,56 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 16; ++j)
               w[j] = live ? pack16<T>(v[2 * j], v[2 * j + 1]) : 0u;
-            store32<T>(args.dx, row * args.lddx + tn * kTileN + col, w, left);
+            store32<T>(args.dx, row * args.lddx + tn * plan.cols + col, w, left);
+          }
+          __syncwarp();  // the next load is the whole warp's
+        }
+      } else if constexpr (MODE == kAgain) {
+        const int first = half * (plan.cols / 2), chunks = plan.cols / 32;
+        const int left = args.f - (tn * plan.cols + first);
+        const long long f0 = tn * plan.cols + first;
+        const T* const dh = static_cast<const T*>(args.dh) + row * args.lddh + f0;
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+          float g[16], u[16];
+          tmem_ld16(acc + first + 16 * c, g);
+          tmem_ld16(acc + plan.cols + first + 16 * c, u);
+          uint32_t d[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) d[j] = ahead[j];
+          load16<T>(dh + 16 * (c + 1), ahead, live && c + 1 < chunks ? left - 16 * (c + 1) : 0);
+          if (there && 16 * c < left) {
+            uint32_t dg[8], du[8], hw[8];
+            with_act(args.act, [&](auto tag) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                float d0, d1, s0, s1;
+                unpack16<T>(d[j], d0, d1);
+                const float a0 = activate<decltype(tag)::value, true>(g[2 * j], s0);
+                const float a1 = activate<decltype(tag)::value, true>(g[2 * j + 1], s1);
+                const float u0 = u[2 * j], u1 = u[2 * j + 1];
+                dg[j] = live ? pack16<T>(d0 * u0 * s0, d1 * u1 * s1) : 0u;
+                du[j] = live ? pack16<T>(d0 * a0, d1 * a1) : 0u;
+                hw[j] = live ? pack16<T>(a0 * u0, a1 * u1) : 0u;
+              }
+            });
+            store16<T>(args.gate, row * args.ldg + f0 + 16 * c, dg, left - 16 * c);
+            store16<T>(args.up, row * args.ldu + f0 + 16 * c, du, left - 16 * c);
+            if (args.h != nullptr)
+              store16<T>(args.h, row * args.ldh + f0 + 16 * c, hw, left - 16 * c);
           }
           __syncwarp();  // the next load is the whole warp's
         }
       } else {
 #pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          const int col = half * 64 + c * 32;
-          const int f0 = tn * 128 + col;
+        for (int c = 0; c < plan.cols / 64; ++c) {
+          const int col = half * (plan.cols / 2) + c * 32;
+          const int f0 = tn * plan.cols + col;
           const int left = args.f - f0;
           float g[32], u[32];
           tmem_ld32(acc + col, g);
-          tmem_ld32(acc + 128 + col, u);
-          if (!there || left <= 0) {
-          } else if constexpr (MODE == kFwd) {
+          tmem_ld32(acc + plan.cols + col, u);
+          if (there && left > 0) {
             uint32_t w[16];
             if (args.gate != nullptr) {
 #pragma unroll
@@ -340,42 +542,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (args.ck.q != nullptr)
               ckpt_store32<T>(w, args.ck.q + row * args.ck.ldq + f0,
                               args.ck.ex + row * args.ck.lde + f0 / kCkptBlock, left);
-          } else {
-            uint32_t dg[16], du[16];
-            {
-              const T* p = static_cast<const T*>(args.dh) + row * args.lddh + f0;
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (live && 8 * j < left) x = *reinterpret_cast<const uint4*>(p + 8 * j);
-                dg[4 * j] = x.x;
-                dg[4 * j + 1] = x.y;
-                dg[4 * j + 2] = x.z;
-                dg[4 * j + 3] = x.w;
-              }
-            }
-            with_act(args.act, [&](auto tag) {
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                float d0, d1, s0, s1;
-                unpack16<T>(dg[j], d0, d1);
-                const float a0 = activate<decltype(tag)::value, true>(g[2 * j], s0);
-                const float a1 = activate<decltype(tag)::value, true>(g[2 * j + 1], s1);
-                dg[j] = live ? pack16<T>(d0 * u[2 * j] * s0, d1 * u[2 * j + 1] * s1) : 0u;
-                du[j] = live ? pack16<T>(d0 * a0, d1 * a1) : 0u;
-                // h in the projections' place, should it be wanted
-                u[2 * j] *= a0;
-                u[2 * j + 1] *= a1;
-              }
-            });
-            store32<T>(args.gate, row * args.ldg + f0, dg, left);
-            store32<T>(args.up, row * args.ldu + f0, du, left);
-            if (args.h != nullptr) {
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                du[j] = live ? pack16<T>(u[2 * j], u[2 * j + 1]) : 0u;
-              store32<T>(args.h, row * args.ldh + f0, du, left);
-            }
           }
           __syncwarp();  // the next load is the whole warp's
         }
@@ -386,15 +552,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // A tile is whole or NaN: so are this one and the rest after a wait that ran out.
     if (!ok) {
-      for (; tile < plan.tiles; tile += pairs) {
+      for (; tile < tiles; tile += pairs) {
         int tm, tn;
-        place(plan, tile, tm, tn);
-        const long long row =
-            static_cast<long long>(tm) * kTileM + static_cast<int>(rank) * 128 + q * 32 + lane;
+        place(plan, n_m, tile, tm, tn);
+        const long long row = row_of(tm, q * 32 + lane);
         if (row >= args.n) continue;
         const uint32_t w = pack16<T>(kNaN, kNaN);
-        const int width = MODE == kDx ? args.d : args.f, cols = MODE == kDx ? 128 : 64;
-        const int c0 = (MODE == kDx ? tn * kTileN : tn * 128) + half * cols;
+        const int width = MODE == kDx ? args.d : args.f, cols = plan.cols / 2;
+        const int c0 = tn * plan.cols + half * cols;
 #pragma unroll 1
         for (int c = c0; c < least(c0 + cols, width); c += 8) {
           if (MODE == kDx) {
@@ -428,25 +593,29 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int MODE, typename T>
-cudaError_t launch(const CUtensorMap (&a)[2], const CUtensorMap (&b)[2], const GluArgs& args,
+cudaError_t launch(const CUtensorMap (&a)[4], const CUtensorMap (&b)[2], const GluArgs& args,
                    const GluPlan& plan, int sms, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * std::min(plan.tiles, sms / 2));
+  cfg.gridDim = dim3(2 * std::min(plan.n_m * plan.n_n, sms / 2));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  // dx starts while the kernel before it ends (and waits for that itself).
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = MODE == kDx ? 2 : 1;
   LaunchTimer timer(MODE == kFwd     ? "glu_gemm_kernel<fwd>"
                     : MODE == kAgain ? "glu_gemm_kernel<again>"
                                      : "glu_gemm_kernel<dx>",
                     st);
-  return cudaLaunchKernelEx(&cfg, glu_gemm_kernel<MODE, T>, a[0], a[1], b[0], b[1], args, plan);
+  return cudaLaunchKernelEx(&cfg, glu_gemm_kernel<MODE, T>, a[0], a[1], a[2], a[3], b[0], b[1], args,
+                            plan);
 }
 
 bool map16(CUtensorMap* map, const void* base, int cols, long long rows, long long ld,
@@ -456,30 +625,43 @@ bool map16(CUtensorMap* map, const void* base, int cols, long long rows, long lo
                        CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// Columns of a tile: half where one round of the SM pairs then holds them all, and a
+// tile's stages take half the time (2880 x 2880, 33 rows: 23 -> 21 us a call). Not
+// otherwise: as many rows of the first operand for half the products (16384 x 4096 x
+// 14336 forward 2193 -> 3076 us; 33 rows, which the weights bound, 62 -> 68).
+int tile_columns(int n_m, int width, int most, int pairs) {
+  const long long halves = static_cast<long long>(n_m) * ((width + most / 2 - 1) / (most / 2));
+  return halves <= pairs ? most / 2 : most;
+}
+
 template <int MODE>
 cudaError_t launch_mode(const GluArgs& args, int sms, cudaStream_t st) {
-  CUtensorMap a[2], b[2];
+  CUtensorMap a[4], b[2];
   GluPlan plan;
+  const long long segs = (args.n + kSeg - 1) / kSeg;
+  plan.segs = args.mask != nullptr && segs <= kMostSegs ? static_cast<int>(segs) : 0;
   plan.n_m = static_cast<int>((args.n + kTileM - 1) / kTileM);
-  if (MODE == kDx) {
-    plan.n_n = (args.d + kTileN - 1) / kTileN;
-    plan.kt = (args.f + kBK - 1) / kBK;
-    if (!map16(&a[0], args.gate, args.f, args.n, args.ldg, 128) ||
-        !map16(&a[1], args.up, args.f, args.n, args.ldu, 128) ||
-        !map16(&b[0], args.w_gate, args.d, args.f, args.ldwg, kBK) ||
-        !map16(&b[1], args.w_up, args.d, args.f, args.ldwu, kBK))
+  const int width = MODE == kDx ? args.d : args.f, depth = MODE == kDx ? args.f : args.d;
+  plan.cols = tile_columns(plan.n_m, width, MODE == kDx ? kTileN : 128, sms / 2);
+  plan.kt = (depth + kBK - 1) / kBK;
+  // The first operand's rows by 128 and by segments; the weights' by columns of f.
+  const void* first[2] = {MODE == kDx ? args.gate : args.x, MODE == kDx ? args.up : args.x};
+  const long long ld[2] = {MODE == kDx ? args.ldg : args.ldx, MODE == kDx ? args.ldu : args.ldx};
+  const uint32_t b_rows = MODE == kDx ? kBK : static_cast<uint32_t>(plan.cols);
+  for (int i = 0; i < 2; ++i) {
+    if (MODE != kDx && i == 1) {
+      a[1] = a[0];
+      a[3] = a[2];
+    } else if (!map16(&a[i], first[i], depth, args.n, ld[i], 128) ||
+               !map16(&a[2 + i], first[i], depth, args.n, ld[i], kSeg)) {
       return cudaErrorInvalidValue;
-  } else {
-    plan.n_n = (args.f + 127) / 128;
-    plan.kt = (args.d + kBK - 1) / kBK;
-    if (!map16(&a[0], args.x, args.d, args.n, args.ldx, 128) ||
-        !map16(&b[0], args.w_gate, args.d, args.f, args.ldwg, 128) ||
-        !map16(&b[1], args.w_up, args.d, args.f, args.ldwu, 128))
-      return cudaErrorInvalidValue;
-    a[1] = a[0];
+    }
   }
+  if (!map16(&b[0], args.w_gate, args.d, args.f, args.ldwg, b_rows) ||
+      !map16(&b[1], args.w_up, args.d, args.f, args.ldwu, b_rows))
+    return cudaErrorInvalidValue;
+  plan.n_n = (width + plan.cols - 1) / plan.cols;
   plan.kt2 = 2 * plan.kt;
-  plan.tiles = plan.n_m * plan.n_n;
   plan.group = kGroupM;
   return args.fp16 ? launch<MODE, __half>(a, b, args, plan, sms, st)
                    : launch<MODE, __nv_bfloat16>(a, b, args, plan, sms, st);
@@ -493,6 +675,7 @@ constexpr int kRowThreads = 256;
 // row a thread.
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads) glu_bwd_kept_kernel(const GluArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int per_row = a.f / 8;
   const long long all = a.n * per_row;
   for (long long i = static_cast<long long>(blockIdx.x) * kRowThreads + threadIdx.x; i < all;
