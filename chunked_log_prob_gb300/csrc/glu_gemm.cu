@@ -26,7 +26,7 @@ namespace {
 
 constexpr int kFwd = 0, kAgain = 1, kDx = 2;
 
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kBK = 64;                  // columns of a stage: 128 bytes
 constexpr int kOperand = 128 * kBK * 2;  // a CTA's 128 rows of either operand
 constexpr int kBox = kBK * 128;          // 64 rows x 64 columns of an MN-major operand
@@ -38,7 +38,12 @@ constexpr int kTileSegs = 256 / kSeg;
 // Segments that a CTA lists (2 bytes each): 131072 rows. Beyond them masked rows are
 // computed like the others, and their zeros written in the epilogue.
 constexpr int kMostSegs = 8192;
-constexpr int kSmem = 1024 + 2 * kStages * kOperand + 2 * kMostSegs;
+// Outputs leave by TMA from boxes of 32 rows x 32 columns, three a warp in turn: a
+// thread's own stores, 16 bytes of a row each, took longer than a tile's MMAs
+// (8192 x 1536 x 8960 padded, h and the projections: 254 us).
+constexpr int kOutBox = 32 * 64, kOutBoxes = 3;
+constexpr int kSmem = 1024 + 2 * kStages * kOperand + kEpilogueWarps * kOutBoxes * kOutBox +
+                      2 * kMostSegs;
 static_assert(kSmem <= 227 * 1024 - 1024, "shared memory of a CTA");
 constexpr uint32_t kTmemCols = 512;
 
@@ -141,25 +146,37 @@ __device__ __forceinline__ void unpack16(uint32_t w, float& lo, float& hi) {
   }
 }
 
-// 32 columns of a row, rounded: as many whole groups of 8 as the row has left.
-template <typename T>
-__device__ __forceinline__ void store32(void* base, long long at, const uint32_t (&w)[16],
-                                        int left) {
-  T* p = static_cast<T*>(base) + at;
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (8 * j < left) st_global_v4(p + 8 * j, w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-}
+// A warp's boxes on their way out, through the 64-byte swizzle: the lane's row of 32
+// columns, 16 at a time. The rows are two segments, of 16 lanes each.
+struct OutBoxes {
+  uint8_t* base;
+  uint32_t turn;
+  int lane;
 
-// The same of 16 columns, and their loads (zeros past `left`).
-template <typename T>
-__device__ __forceinline__ void store16(void* base, long long at, const uint32_t (&w)[8],
-                                        int left) {
-  T* p = static_cast<T*>(base) + at;
-#pragma unroll
-  for (int j = 0; j < 2; ++j)
-    if (8 * j < left) st_global_v4(p + 8 * j, w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-}
+  // The next box, free again.
+  __device__ __forceinline__ uint32_t begin() {
+    if (lane == 0) bulk_wait_group_read<kOutBoxes - 1>();
+    __syncwarp();
+    return smem_u32(base + turn * kOutBox);
+  }
+  __device__ __forceinline__ void put16(uint32_t box, int half, const uint32_t* w) const {
+    const uint32_t row = box + lane * 64, x = (lane >> 1) & 3;
+    sts_v4(row + (((2 * half) ^ x) << 4), w[0], w[1], w[2], w[3]);
+    sts_v4(row + (((2 * half + 1) ^ x) << 4), w[4], w[5], w[6], w[7]);
+  }
+  // Sends it to column `col`, rows r0 and r1 on (n: not there).
+  __device__ __forceinline__ void end(const CUtensorMap* map, int col, int r0, int r1, int n) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      if (r0 < n) tma_store_2d(map, base + turn * kOutBox, col, r0);
+      if (r1 < n) tma_store_2d(map, base + turn * kOutBox + kOutBox / 2, col, r1);
+      bulk_commit_group();
+    }
+    turn = turn == kOutBoxes - 1 ? 0 : turn + 1;
+  }
+};
+
 template <typename T>
 __device__ __forceinline__ void load16(const T* p, uint32_t (&w)[8], int left) {
 #pragma unroll
@@ -208,18 +225,19 @@ __device__ __forceinline__ void ckpt_store32(const uint32_t (&w)[16], uint8_t* q
   const float inv = pow2(-k);
   special = special || k >= CkptTop<T>::k;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    uint32_t o[4];
+  for (int j = 0; j < 2; ++j) {
+    uint32_t o[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
       float lo, hi;
-      unpack16<T>(w[4 * j + i], lo, hi);
+      unpack16<T>(w[8 * j + i], lo, hi);
       o[i] = special ? pack_e4m3x2(ckpt_scaled<T>(lo, inv, k), ckpt_scaled<T>(hi, inv, k))
                      : pack_e4m3x2(lo * inv, hi * inv);
     }
-    if (8 * j < left)
-      *reinterpret_cast<uint2*>(q + 8 * j) =
-          make_uint2(__byte_perm(o[0], o[1], 0x5410), __byte_perm(o[2], o[3], 0x5410));
+    // A row's bytes are padded to 16.
+    if (16 * j < left)
+      st_global_v4(q + 16 * j, __byte_perm(o[0], o[1], 0x5410), __byte_perm(o[2], o[3], 0x5410),
+                   __byte_perm(o[4], o[5], 0x5410), __byte_perm(o[6], o[7], 0x5410));
   }
   *ex = static_cast<uint8_t>(k + kCkptBias);
 }
@@ -236,7 +254,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ CUtensorMap map_s0,
                     const __grid_constant__ CUtensorMap map_s1,
                     const __grid_constant__ CUtensorMap map_b0,
-                    const __grid_constant__ CUtensorMap map_b1, const GluArgs args,
+                    const __grid_constant__ CUtensorMap map_b1,
+                    const __grid_constant__ CUtensorMap map_o0,
+                    const __grid_constant__ CUtensorMap map_o1,
+                    const __grid_constant__ CUtensorMap map_o2, const GluArgs args,
                     const GluPlan plan) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full_bar[kStages];  // leader: both CTAs' tiles are there
@@ -249,7 +270,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* const ring = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
-  uint16_t* const list = reinterpret_cast<uint16_t*>(ring + 2 * kStages * kOperand);
+  uint8_t* const boxes = ring + 2 * kStages * kOperand;
+  uint16_t* const list =
+      reinterpret_cast<uint16_t*>(boxes + kEpilogueWarps * kOutBoxes * kOutBox);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int pair = static_cast<int>(blockIdx.x) / 2, pairs = static_cast<int>(gridDim.x) / 2;
@@ -433,19 +456,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t t0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
     uint32_t t = 0;
     int tile = pair;
+    OutBoxes out = {boxes + (warp - kFirstEpilogue) * kOutBoxes * kOutBox, 0u, lane};
+    const int n = static_cast<int>(args.n);
     for (; tile < tiles; tile += pairs, ++t) {
       int tm, tn;
       place(plan, n_m, tile, tm, tn);
       const long long row = row_of(tm, q * 32 + lane);
+      const int r0 = static_cast<int>(row_of(tm, q * 32)),
+                r1 = static_cast<int>(row_of(tm, q * 32 + 16));
       const uint32_t buf = t & 1u;
       const bool there = row < args.n;
       const bool live = there && (args.mask == nullptr || args.mask[row] != 0);
       // The first of dh comes while the tile's sums do, each next one a step ahead.
       uint32_t ahead[8];
+      const T* dh = nullptr;
       if constexpr (MODE == kAgain) {
         const int f0 = tn * plan.cols + half * (plan.cols / 2);
-        load16<T>(static_cast<const T*>(args.dh) + row * args.lddh + f0, ahead,
-                  live ? args.f - f0 : 0);
+        dh = static_cast<const T*>(args.dh) + row * args.lddh + f0;
+        load16<T>(dh, ahead, live ? args.f - f0 : 0);
       }
       if (!warp_wait(&tfull_bar[buf], (t >> 1) & 1u, abort_flag, &status_sh)) {
         ok = false;
@@ -453,38 +481,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_after();
       const uint32_t acc = t0 + buf * kTileN;
-      if constexpr (MODE == kDx) {
+      const int width = MODE == kDx ? args.d : args.f;
+      const int chunks = plan.cols / 64;  // of 32 columns
 #pragma unroll 1
-        for (int c = 0; c < plan.cols / 64; ++c) {
-          const int col = half * (plan.cols / 2) + c * 32;
-          const int left = args.d - (tn * plan.cols + col);
+      for (int c = 0; c < chunks; ++c) {
+        const int col = half * (plan.cols / 2) + c * 32;
+        const int at = tn * plan.cols + col, left = width - at;
+        if (left <= 0) break;
+        if constexpr (MODE == kDx) {
           float v[32];
           tmem_ld32(acc + col, v);
-          if (there && left > 0) {
-            uint32_t w[16];
+          uint32_t w[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              w[j] = live ? pack16<T>(v[2 * j], v[2 * j + 1]) : 0u;
-            store32<T>(args.dx, row * args.lddx + tn * plan.cols + col, w, left);
-          }
-          __syncwarp();  // the next load is the whole warp's
-        }
-      } else if constexpr (MODE == kAgain) {
-        const int first = half * (plan.cols / 2), chunks = plan.cols / 32;
-        const int left = args.f - (tn * plan.cols + first);
-        const long long f0 = tn * plan.cols + first;
-        const T* const dh = static_cast<const T*>(args.dh) + row * args.lddh + f0;
+          for (int j = 0; j < 16; ++j) w[j] = live ? pack16<T>(v[2 * j], v[2 * j + 1]) : 0u;
+          const uint32_t box = out.begin();
+          out.put16(box, 0, w);
+          out.put16(box, 1, w + 8);
+          out.end(&map_o0, at, r0, r1, n);
+        } else if constexpr (MODE == kAgain) {
+          // Three boxes at once: dgate, dup and (should it be wanted) h.
+          const int outs = args.h != nullptr ? 3 : 2;
+          if (lane == 0) bulk_wait_group_read<0>();
+          __syncwarp();
+          const uint32_t box = smem_u32(out.base);
 #pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
-          float g[16], u[16];
-          tmem_ld16(acc + first + 16 * c, g);
-          tmem_ld16(acc + plan.cols + first + 16 * c, u);
-          uint32_t d[8];
+          for (int s = 0; s < 2; ++s) {
+            float g[16], u[16];
+            tmem_ld16(acc + col + 16 * s, g);
+            tmem_ld16(acc + plan.cols + col + 16 * s, u);
+            uint32_t d[8], dg[8], du[8], hw[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) d[j] = ahead[j];
-          load16<T>(dh + 16 * (c + 1), ahead, live && c + 1 < chunks ? left - 16 * (c + 1) : 0);
-          if (there && 16 * c < left) {
-            uint32_t dg[8], du[8], hw[8];
+            for (int j = 0; j < 8; ++j) d[j] = ahead[j];
+            const int next = 32 * c + 16 * (s + 1);  // of this thread's columns
+            load16<T>(dh + next, ahead,
+                      live && next < plan.cols / 2 ? left - 16 * (s + 1) : 0);
             with_act(args.act, [&](auto tag) {
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
@@ -498,53 +528,59 @@ __global__ void __launch_bounds__(kThreads, 1)
                 hw[j] = live ? pack16<T>(a0 * u0, a1 * u1) : 0u;
               }
             });
-            store16<T>(args.gate, row * args.ldg + f0 + 16 * c, dg, left - 16 * c);
-            store16<T>(args.up, row * args.ldu + f0 + 16 * c, du, left - 16 * c);
-            if (args.h != nullptr)
-              store16<T>(args.h, row * args.ldh + f0 + 16 * c, hw, left - 16 * c);
+            out.put16(box, s, dg);
+            out.put16(box + kOutBox, s, du);
+            if (outs == 3) out.put16(box + 2 * kOutBox, s, hw);
+            __syncwarp();  // the next load is the whole warp's
           }
-          __syncwarp();  // the next load is the whole warp's
-        }
-      } else {
-#pragma unroll 1
-        for (int c = 0; c < plan.cols / 64; ++c) {
-          const int col = half * (plan.cols / 2) + c * 32;
-          const int f0 = tn * plan.cols + col;
-          const int left = args.f - f0;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            const CUtensorMap* const to[3] = {&map_o0, &map_o1, &map_o2};
+            for (int o = 0; o < outs; ++o) {
+              if (r0 < n) tma_store_2d(to[o], out.base + o * kOutBox, at, r0);
+              if (r1 < n) tma_store_2d(to[o], out.base + o * kOutBox + kOutBox / 2, at, r1);
+            }
+            bulk_commit_group();
+          }
+        } else {
           float g[32], u[32];
           tmem_ld32(acc + col, g);
           tmem_ld32(acc + plan.cols + col, u);
-          if (there && left > 0) {
-            uint32_t w[16];
-            if (args.gate != nullptr) {
+          uint32_t w[16];
+          if (args.gate != nullptr) {
+            uint32_t box = out.begin();
 #pragma unroll
-              for (int j = 0; j < 16; ++j)
-                w[j] = live ? pack16<T>(g[2 * j], g[2 * j + 1]) : 0u;
-              store32<T>(args.gate, row * args.ldg + f0, w, left);
-            }
-            if (args.up != nullptr) {
+            for (int j = 0; j < 16; ++j) w[j] = live ? pack16<T>(g[2 * j], g[2 * j + 1]) : 0u;
+            out.put16(box, 0, w);
+            out.put16(box, 1, w + 8);
+            out.end(&map_o1, at, r0, r1, n);
+            box = out.begin();
 #pragma unroll
-              for (int j = 0; j < 16; ++j)
-                w[j] = live ? pack16<T>(u[2 * j], u[2 * j + 1]) : 0u;
-              store32<T>(args.up, row * args.ldu + f0, w, left);
-            }
-            with_act(args.act, [&](auto tag) {
-              float s;
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const float h0 = activate<decltype(tag)::value, false>(g[2 * j], s) * u[2 * j];
-                const float h1 =
-                    activate<decltype(tag)::value, false>(g[2 * j + 1], s) * u[2 * j + 1];
-                w[j] = live ? pack16<T>(h0, h1) : 0u;
-              }
-            });
-            store32<T>(args.h, row * args.ldh + f0, w, left);
-            if (args.ck.q != nullptr)
-              ckpt_store32<T>(w, args.ck.q + row * args.ck.ldq + f0,
-                              args.ck.ex + row * args.ck.lde + f0 / kCkptBlock, left);
+            for (int j = 0; j < 16; ++j) w[j] = live ? pack16<T>(u[2 * j], u[2 * j + 1]) : 0u;
+            out.put16(box, 0, w);
+            out.put16(box, 1, w + 8);
+            out.end(&map_o2, at, r0, r1, n);
           }
-          __syncwarp();  // the next load is the whole warp's
+          with_act(args.act, [&](auto tag) {
+            float s;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float h0 = activate<decltype(tag)::value, false>(g[2 * j], s) * u[2 * j];
+              const float h1 =
+                  activate<decltype(tag)::value, false>(g[2 * j + 1], s) * u[2 * j + 1];
+              w[j] = live ? pack16<T>(h0, h1) : 0u;
+            }
+          });
+          const uint32_t box = out.begin();
+          out.put16(box, 0, w);
+          out.put16(box, 1, w + 8);
+          out.end(&map_o0, at, r0, r1, n);
+          if (args.ck.q != nullptr && there)
+            ckpt_store32<T>(w, args.ck.q + row * args.ck.ldq + at,
+                            args.ck.ex + row * args.ck.lde + at / kCkptBlock, left);
         }
+        __syncwarp();  // the next load is the whole warp's
       }
       tc_fence_before();
       __syncwarp();
@@ -580,6 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    if (lane == 0) bulk_wait_group<0>();
   }
 
   // Neither CTA may leave while the other's tensor core reads its shared memory
@@ -593,7 +630,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int MODE, typename T>
-cudaError_t launch(const CUtensorMap (&a)[4], const CUtensorMap (&b)[2], const GluArgs& args,
+cudaError_t launch(const CUtensorMap (&a)[4], const CUtensorMap (&b)[2],
+                   const CUtensorMap (&o)[3], const GluArgs& args,
                    const GluPlan& plan, int sms, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * std::min(plan.n_m * plan.n_n, sms / 2));
@@ -614,8 +652,8 @@ cudaError_t launch(const CUtensorMap (&a)[4], const CUtensorMap (&b)[2], const G
                     : MODE == kAgain ? "glu_gemm_kernel<again>"
                                      : "glu_gemm_kernel<dx>",
                     st);
-  return cudaLaunchKernelEx(&cfg, glu_gemm_kernel<MODE, T>, a[0], a[1], a[2], a[3], b[0], b[1], args,
-                            plan);
+  return cudaLaunchKernelEx(&cfg, glu_gemm_kernel<MODE, T>, a[0], a[1], a[2], a[3], b[0], b[1],
+                            o[0], o[1], o[2], args, plan);
 }
 
 bool map16(CUtensorMap* map, const void* base, int cols, long long rows, long long ld,
@@ -660,11 +698,25 @@ cudaError_t launch_mode(const GluArgs& args, int sms, cudaStream_t st) {
   if (!map16(&b[0], args.w_gate, args.d, args.f, args.ldwg, b_rows) ||
       !map16(&b[1], args.w_up, args.d, args.f, args.ldwu, b_rows))
     return cudaErrorInvalidValue;
+  // What leaves: dx; or h, gate and up; or dgate, dup and h.
+  CUtensorMap o[3];
+  void* const out[3] = {MODE == kDx ? args.dx : MODE == kFwd ? args.h : args.gate,
+                        MODE == kFwd ? args.gate : args.up, MODE == kFwd ? args.up : args.h};
+  const long long ldo[3] = {MODE == kDx ? args.lddx : MODE == kFwd ? args.ldh : args.ldg,
+                            MODE == kFwd ? args.ldg : args.ldu, MODE == kFwd ? args.ldu : args.ldh};
+  for (int i = 0; i < 3; ++i) {
+    if (i > 0 && (MODE == kDx || out[i] == nullptr))
+      o[i] = o[0];
+    else if (!encode_map_2d(&o[i], out[i], static_cast<uint64_t>(width),
+                            static_cast<uint64_t>(args.n), static_cast<uint64_t>(ldo[i]) * 2, 32,
+                            kSeg, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_64B))
+      return cudaErrorInvalidValue;
+  }
   plan.n_n = (width + plan.cols - 1) / plan.cols;
   plan.kt2 = 2 * plan.kt;
   plan.group = kGroupM;
-  return args.fp16 ? launch<MODE, __half>(a, b, args, plan, sms, st)
-                   : launch<MODE, __nv_bfloat16>(a, b, args, plan, sms, st);
+  return args.fp16 ? launch<MODE, __half>(a, b, o, args, plan, sms, st)
+                   : launch<MODE, __nv_bfloat16>(a, b, o, args, plan, sms, st);
 }
 
 // ---------------------------------------- from the projections as kept ----
@@ -676,12 +728,20 @@ constexpr int kRowThreads = 256;
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads) glu_bwd_kept_kernel(const GluArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // Steps of all threads' groups of 8; the place moves on without a division.
   const int per_row = a.f / 8;
-  const long long all = a.n * per_row;
-  for (long long i = static_cast<long long>(blockIdx.x) * kRowThreads + threadIdx.x; i < all;
-       i += static_cast<long long>(gridDim.x) * kRowThreads) {
-    const long long row = i / per_row;
-    const int col = static_cast<int>(i - row * per_row) * 8;
+  const long long step = static_cast<long long>(gridDim.x) * kRowThreads;
+  const long long rows = step / per_row;
+  const int more = static_cast<int>(step - rows * per_row);
+  const long long first = static_cast<long long>(blockIdx.x) * kRowThreads + threadIdx.x;
+  long long row = first / per_row;
+  int group = static_cast<int>(first - row * per_row);
+  for (; row < a.n; row += rows, group += more) {
+    if (group >= per_row) {
+      group -= per_row;
+      if (++row >= a.n) break;
+    }
+    const int col = group * 8;
     const bool live = a.mask == nullptr || a.mask[row] != 0;
     uint4 d = make_uint4(0, 0, 0, 0), g = d, u = d;
     if (live) {

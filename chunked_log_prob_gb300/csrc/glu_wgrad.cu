@@ -19,7 +19,7 @@
 namespace grpo {
 namespace {
 
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kBox = kTok * 128;     // 64 tokens x 64 columns
 constexpr int kOperand = 2 * kBox;   // a CTA's 128 outputs, or 128 inputs
 // Stages summed in TMEM: 512 tokens of bf16, 256 of fp16, whose products have 22
@@ -32,7 +32,13 @@ __host__ __device__ __forceinline__ int segment_of(const GluWgradArgs& a) {
 constexpr int kEpilogueWarps = 8;
 constexpr int kFirstEpilogue = 4;  // warps 0 TMA, 1 MMA, 2 and 3 idle
 constexpr int kThreads = 32 * (kFirstEpilogue + kEpilogueWarps);
-constexpr int kSmem = 1024 + 2 * kStages * kOperand;
+// dW leaves, and what is added to it comes, by TMA in boxes of 32 outputs x 16 inputs,
+// four a warp in turn: a thread's own accesses, 16 bytes of a row each, held the next
+// tile's sums up (4096 tokens x 4096 x 14336: 672 us without `add`, 862 with it).
+constexpr int kBoxBytes = 32 * 64, kBoxes = 4, kBoxesOfTile = kTileN / 2 / 16;
+constexpr int kSmem = 1024 + 2 * kStages * kOperand + kEpilogueWarps * kBoxes * kBoxBytes;
+static_assert(kSmem <= 227 * 1024 - 1024, "shared memory of a CTA");
+static_assert(kBoxesOfTile == 2 * kBoxes, "each box is loaded twice a tile");
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSlotFloats = kTileM * kTileN;
 
@@ -74,18 +80,24 @@ __device__ __forceinline__ Side side_of(const GluWgradArgs& a, int tm) {
 __global__ void __launch_bounds__(kThreads, 1)
     glu_wgrad_kernel(const __grid_constant__ CUtensorMap map_gate,
                      const __grid_constant__ CUtensorMap map_up,
-                     const __grid_constant__ CUtensorMap map_x, const GluWgradArgs args,
+                     const __grid_constant__ CUtensorMap map_x,
+                     const __grid_constant__ CUtensorMap map_dw0,
+                     const __grid_constant__ CUtensorMap map_dw1,
+                     const __grid_constant__ CUtensorMap map_add0,
+                     const __grid_constant__ CUtensorMap map_add1, const GluWgradArgs args,
                      const WgradPlan plan) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full_bar[kStages];  // leader: both CTAs' tiles are there
   __shared__ __align__(8) uint64_t done_bar[kStages];  // the stage's MMAs are done
   __shared__ __align__(8) uint64_t tfull_bar[2], tempty_bar[2];
+  __shared__ __align__(8) uint64_t add_bar[kEpilogueWarps][kBoxes];  // a box to add landed
   __shared__ __align__(8) uint64_t drain_bar;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
 
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* const ring = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+  uint8_t* const boxes = ring + 2 * kStages * kOperand;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int pair = static_cast<int>(blockIdx.x) / 2, pairs = static_cast<int>(gridDim.x) / 2;
@@ -103,6 +115,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&tfull_bar[b], 1);
       mbar_init(&tempty_bar[b], 2 * kEpilogueWarps);  // both CTAs' epilogue warps
     }
+    for (int w = 0; w < kEpilogueWarps; ++w)
+      for (int b = 0; b < kBoxes; ++b) mbar_init(&add_bar[w][b], 1);
     mbar_init(&drain_bar, 1);
     abort_sh = 0;
     fence_mbar_init();
@@ -208,9 +222,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t t0 =
         tmem_base + (static_cast<uint32_t>(q * 32) << 16) + half * (kTileN / 2);
     uint32_t seg = 0;
+    const int wid = warp - kFirstEpilogue;
+    uint8_t* const box0 = boxes + wid * kBoxes * kBoxBytes;
+    const uint32_t lane_row = smem_u32(box0) + lane * 64, swizzle = (lane >> 1) & 3;
+    // Of the current tile: boxes of `add` asked for, and waited for. Each tile has all
+    // of its boxes loaded, so a box's first load of a tile ends phase 0, its second 1.
+    int asked = 0, had = 0;
     while (ok && work.next(plan, pair, pairs, it)) {
       int tm, tn;
       tile_place(plan, it.tile, tm, tn);
+      const Side side = side_of(args, tm);
+      const int row0 = side.o0 + static_cast<int>(rank) * 128 + q * 32;
+      const int col0 = tn * kTileN + half * (kTileN / 2);
+      const CUtensorMap* const map_add = side.up ? &map_add1 : &map_add0;
+      const bool whole = it.slot < 0 && row0 < args.f && col0 < args.d;
+      const bool adds = whole && (side.up ? args.add_up : args.add_gate) != nullptr;
+      auto ask = [&](int b) {
+        if (lane == 0) {
+          uint64_t* bar = &add_bar[wid][b % kBoxes];
+          mbar_arrive_expect_tx(bar, kBoxBytes);
+          tma_load_2d(box0 + (b % kBoxes) * kBoxBytes, map_add, bar, col0 + 16 * b, row0);
+        }
+      };
+      asked = had = 0;
+      if (adds) {  // the first boxes come while the tile's sums do
+        if (lane == 0) bulk_wait_group_read<0>();
+        __syncwarp();
+        for (; asked < kBoxes; ++asked) ask(asked);
+      }
       float sum[4][32];
 #pragma unroll
       for (int c = 0; c < 4; ++c)
@@ -238,43 +277,64 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive_cluster(tempty0 + buf * 8u);
       }
       if (!ok) break;
-      const Side side = side_of(args, tm);
-      const int lrow = static_cast<int>(rank) * 128 + q * 32 + lane;  // row of the tile
-      const int row = side.o0 + lrow;
-      const float* add = side.up ? args.add_up : args.add_gate;
-      float* dw = side.up ? args.dw_up : args.dw_gate;
-      const long long at = static_cast<long long>(row) * args.d;
+      if (it.slot >= 0) {
+        const int lrow = static_cast<int>(rank) * 128 + q * 32 + lane;  // row of the tile
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int cb = half * 4 + c;
-        const int i0 = tn * kTileN + cb * 32;
-        if (i0 >= args.d) break;
-        if (it.slot >= 0) {
+        for (int c = 0; c < 4; ++c) {
+          if (col0 + c * 32 >= args.d) break;
           float* p = args.partials + static_cast<long long>(it.slot) * kSlotFloats +
-                     (cb * 8 * kTileM + lrow) * 4;
+                     ((half * 4 + c) * 8 * kTileM + lrow) * 4;
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             *reinterpret_cast<float4*>(p + j * kTileM * 4) = make_float4(
                 sum[c][4 * j], sum[c][4 * j + 1], sum[c][4 * j + 2], sum[c][4 * j + 3]);
-        } else if (row < args.f) {
+        }
+        __syncwarp();
+        continue;
+      }
+      if (!whole) continue;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (i0 + 4 * j >= args.d) break;
-            float4 v = make_float4(sum[c][4 * j], sum[c][4 * j + 1], sum[c][4 * j + 2],
-                                   sum[c][4 * j + 3]);
-            if (add != nullptr) {
-              const float4 x = *reinterpret_cast<const float4*>(add + at + i0 + 4 * j);
-              v.x += x.x;
-              v.y += x.y;
-              v.z += x.z;
-              v.w += x.w;
-            }
-            *reinterpret_cast<float4*>(dw + at + i0 + 4 * j) = v;
+      for (int b = 0; b < kBoxesOfTile; ++b) {
+        float* const v = &sum[b / 2][16 * (b % 2)];
+        const uint32_t at = lane_row + (b % kBoxes) * kBoxBytes;
+        if (adds) {
+          ok = ok && warp_wait(&add_bar[wid][b % kBoxes], b / kBoxes, abort_flag, args.status);
+          if (ok) had = b + 1;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint4 x = lds_v4(at + ((j ^ swizzle) << 4));
+            v[4 * j] += __uint_as_float(x.x);
+            v[4 * j + 1] += __uint_as_float(x.y);
+            v[4 * j + 2] += __uint_as_float(x.z);
+            v[4 * j + 3] += __uint_as_float(x.w);
           }
+        } else {
+          if (lane == 0) bulk_wait_group_read<kBoxes - 1>();
+          __syncwarp();
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          sts_v4(at + ((j ^ swizzle) << 4), __float_as_uint(v[4 * j]),
+                 __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]),
+                 __float_as_uint(v[4 * j + 3]));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (ok && col0 + 16 * b < args.d)
+            tma_store_2d(side.up ? &map_dw1 : &map_dw0, box0 + (b % kBoxes) * kBoxBytes,
+                         col0 + 16 * b, row0);
+          bulk_commit_group();
+        }
+        if (adds && ok && b > 0 && asked < kBoxesOfTile) {  // into the box before this one
+          if (lane == 0) bulk_wait_group_read<1>();
+          ask(asked++);
         }
       }
-      __syncwarp();
+      if (!ok) break;
     }
+    // Copies in flight land before the CTA exits.
+    if (!ok && lane == 0)
+      for (; had < asked; ++had) drain(&add_bar[wid][had % kBoxes], had / kBoxes);
     // A tile, or a piece of one, is whole or NaN: so are this one and the rest.
     if (!ok) {
       do {
@@ -297,6 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } while (work.next(plan, pair, pairs, it));
     }
+    if (lane == 0) bulk_wait_group<0>();
   }
 
   // Neither CTA may leave while the other's tensor core reads its shared memory
@@ -403,6 +464,17 @@ cudaError_t launch_glu_wgrad(const GluWgradArgs& a, int sms, cudaStream_t st) {
   if (!map(&map_gate, a.dgate, a.f, a.ldg) || !map(&map_up, a.dup, a.f, a.ldu) ||
       !map(&map_x, a.x, a.d, a.ldx))
     return cudaErrorInvalidValue;
+  // dW and what is added to it, by 16 inputs.
+  CUtensorMap out[4];
+  const float* const base[4] = {a.dw_gate, a.dw_up, a.add_gate, a.add_up};
+  for (int i = 0; i < 4; ++i) {
+    if (base[i] == nullptr)
+      out[i] = out[0];
+    else if (!encode_map_2d(&out[i], base[i], static_cast<uint64_t>(a.d),
+                            static_cast<uint64_t>(a.f), static_cast<uint64_t>(a.d) * 4, 16, 32,
+                            CU_TENSOR_MAP_DATA_TYPE_FLOAT32, CU_TENSOR_MAP_SWIZZLE_64B))
+      return cudaErrorInvalidValue;
+  }
   const WgradPlan plan = make_plan(a.n, 2 * half_tiles(a.f) * kTileM, a.d, pairs);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * launch_pairs(plan, pairs));
@@ -419,7 +491,8 @@ cudaError_t launch_glu_wgrad(const GluWgradArgs& a, int sms, cudaStream_t st) {
   cudaError_t e;
   {
     LaunchTimer timer("glu_wgrad_kernel", st);
-    e = cudaLaunchKernelEx(&cfg, glu_wgrad_kernel, map_gate, map_up, map_x, a, plan);
+    e = cudaLaunchKernelEx(&cfg, glu_wgrad_kernel, map_gate, map_up, map_x, out[0], out[1], out[2],
+                           out[3], a, plan);
   }
   if (e != cudaSuccess || plan.cut == 0) return e;
   // Its launch overlaps the end of the other (it waits for that itself).

@@ -464,3 +464,23 @@ def test_a_lost_copy_of_the_weight_gradient_is_reported(clp):
         assert torch.equal(p[fine], q[fine])
     for p, q in zip(clp.grpo_glu_wgrad(dg, du, x, workspace=ws), want):
         assert torch.equal(p, q)
+
+
+def test_a_lost_copy_with_something_to_add(clp):
+    # More tiles than pairs, so that tiles are whole and their boxes in flight.
+    g = _gen(3)
+    n, d, f = 1000, 2560, 2560
+    x, dg, du = _randn(g, n, d), _randn(g, n, f), _randn(g, n, f)
+    add = torch.randn(f, d, generator=g, device=DEV)
+    ws = torch.empty(clp.grpo_glu_wgrad_workspace_size(n, f, d), dtype=torch.uint8, device=DEV)
+    want = clp.grpo_glu_wgrad(dg, du, x, add_gate=add, add_up=add, workspace=ws)
+    for stage in (0, 20):
+        clp.grpo_selftest_lose_copy(stage)
+        got = clp.grpo_glu_wgrad(dg, du, x, add_gate=add, add_up=add, workspace=ws)
+        assert clp.grpo_read_device_status(ws) == -7
+        assert torch.isnan(got[0]).any() or torch.isnan(got[1]).any()
+        for p, q in zip(got, want):
+            fine = ~torch.isnan(p)
+            assert torch.equal(p[fine], q[fine])
+    for p, q in zip(clp.grpo_glu_wgrad(dg, du, x, add_gate=add, add_up=add, workspace=ws), want):
+        assert torch.equal(p, q)
