@@ -22,8 +22,13 @@
 namespace grpo {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;  // of the norm's kernels
 constexpr int kWarps = kThreads / 32;
+// Of the step's: 2^28 values with moments in 8 bits, which the instructions bound, 720
+// us with CTAs of 256 threads and 676 with 128 (bf16 parameters; fp32 791 and 735), as
+// each gives its place up sooner; in 32 bits, which memory bounds, 1023 and 1036.
+template <int BITS>
+constexpr int kStepThreads = BITS == 8 ? 128 : 256;
 constexpr int kGroup = 256;  // values of a warp's step
 constexpr int kBlock = 128;  // values that share a scale
 constexpr float kTop = 448.f;              // the largest e4m3
@@ -214,7 +219,8 @@ __device__ __forceinline__ void store8(void* p, long long i, const float (&v)[8]
 // What a chunk's threads share.
 struct StepOf {
   float scale, shrink, rate, beta1, beta2, rest1, rest2, fix2, eps;
-  Keys keys;
+  Keys keys;  // of the chunk's places where they are all `near` one another, or the step's
+  bool near;
 };
 
 // The largest |y| over the 16 lanes of a block; NaN where one of them is.
@@ -251,7 +257,7 @@ __device__ __forceinline__ void step8(const AdamwEntry& e, const StepOf& s, long
   bool have[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) have[j] = VEC || first + j * kEvery < e.numel;
-  const long long block = first / kBlock;  // BITS 8: of this lane's values
+  const uint64_t block = static_cast<uint64_t>(first) / kBlock;  // BITS 8: this lane's
   float ms = 0.f, vs = 0.f;
   if (BITS == 8 && have[0]) {
     ms = e.m_scale[block];
@@ -336,11 +342,11 @@ __device__ __forceinline__ void step8(const AdamwEntry& e, const StepOf& s, long
   }
   uint32_t x[8];
   constexpr bool kRandom = BITS == 8 || sizeof(P) == 2;
-  Keys keys = {};
+  Keys keys = s.keys;
   if constexpr (kRandom) {
     // A lane's values lie in one block, which no multiple of 2^32 parts.
     const uint64_t place = static_cast<uint64_t>(e.place + first);
-    keys = keys_at(s.keys, static_cast<uint32_t>(place >> 32));
+    if (!s.near) keys = keys_at(s.keys, static_cast<uint32_t>(place >> 32));
     // Consecutive places, from a multiple of 8 on, differ below what the first fold
     // moves.
     const uint32_t head = static_cast<uint32_t>(place) ^ keys.k0;
@@ -389,8 +395,8 @@ __device__ __forceinline__ void step8(const AdamwEntry& e, const StepOf& s, long
         }
     }
     if ((lane & 15) == 0 && have[0]) {
-      e.m_scale[block] = mt / kTop;
-      e.v_scale[block] = vt / kTop;
+      e.m_scale[block] = mt * (1.f / kTop);
+      e.v_scale[block] = vt * (1.f / kTop);
     }
   }
   if constexpr (sizeof(P) == 2) {
@@ -455,7 +461,8 @@ __device__ __forceinline__ void step_chunk(const AdamwEntry& e, const StepOf& s,
   constexpr int kState = BITS == 8 ? 8 : 16;
   const bool vec = on(e.param, 16) && on(e.grad, 16) && on(e.m, kState) && on(e.v, kState) &&
                    on(e.copy, 16);
-  for (long long at = begin + warp * kGroup; at < end; at += kWarps * kGroup) {
+  constexpr int kStep = kStepThreads<BITS> / 32 * kGroup;
+  for (long long at = begin + warp * kGroup; at < end; at += kStep) {
     if (vec && at + kGroup <= e.numel)
       step8<BITS, P, G, true>(e, s, at + lane * 8, lane);
     else
@@ -489,7 +496,7 @@ __device__ __forceinline__ int find_entry(const E* e, int count, int c) {
 }
 
 template <int N, int BITS>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kStepThreads<BITS>, 1024 / kStepThreads<BITS>)
     adamw_kernel(const __grid_constant__ AdamwTable<N> table, const AdamwArgs args) {
   const float scale = args.scale != nullptr ? *args.scale : 1.f;
   if (!(fabsf(scale) <= FLT_MAX)) return;  // the step is skipped
@@ -517,6 +524,9 @@ __global__ void __launch_bounds__(kThreads, 4)
   s.eps = args.eps;
   s.keys = keys_of(args.seed, static_cast<uint64_t>(step));
   const long long begin = static_cast<long long>(c - e.chunk) * args.chunk;
+  const uint64_t place = static_cast<uint64_t>(e.place + begin);
+  s.near = (place >> 32) == ((place + static_cast<uint64_t>(args.chunk) - 1) >> 32);
+  if (s.near) s.keys = keys_at(s.keys, static_cast<uint32_t>(place >> 32));
   if (e.ptype == GRPO_DTYPE_FP32)
     step_grad<BITS, float>(e, s, begin, args.chunk);
   else
@@ -637,7 +647,7 @@ cudaError_t launch_adamw(const AdamwEntry* e, const AdamwArgs& a, int chunks, cu
   std::copy(e, e + a.count, table.e);
   std::fill(table.e + a.count, table.e + N, AdamwEntry());
   LaunchTimer timer("adamw_kernel", st);
-  adamw_kernel<N, BITS><<<chunks, kThreads, 0, st>>>(table, a);
+  adamw_kernel<N, BITS><<<chunks, kStepThreads<BITS>, 0, st>>>(table, a);
   return cudaGetLastError();
 }
 
