@@ -53,7 +53,7 @@ struct GluPlan {
   int n_m, n_n;
   int kt, kt2;  // stages of the first operand pair, and of both
   int group;    // row tiles of a group
-  int cols;     // forward and again: 128 or 64; dx: 256 or 128
+  int cols;     // forward and again: 128, 96 or 64; dx: 256 or 128
   int segs;     // segments to list, 0: tiles are of consecutive rows
 };
 
@@ -471,9 +471,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t ahead[8];
       const T* dh = nullptr;
       if constexpr (MODE == kAgain) {
-        const int f0 = tn * plan.cols + half * (plan.cols / 2);
+        const int f0 = tn * plan.cols;
         dh = static_cast<const T*>(args.dh) + row * args.lddh + f0;
-        load16<T>(dh, ahead, live ? args.f - f0 : 0);
+        load16<T>(dh + half * 32, ahead,
+                  live && half * 32 < plan.cols ? args.f - f0 - half * 32 : 0);
       }
       if (!warp_wait(&tfull_bar[buf], (t >> 1) & 1u, abort_flag, &status_sh)) {
         ok = false;
@@ -482,10 +483,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const uint32_t acc = t0 + buf * kTileN;
       const int width = MODE == kDx ? args.d : args.f;
-      const int chunks = plan.cols / 64;  // of 32 columns
+      // The two halves of the warps take turns with the tile's 32 columns each.
 #pragma unroll 1
-      for (int c = 0; c < chunks; ++c) {
-        const int col = half * (plan.cols / 2) + c * 32;
+      for (int col = half * 32; col < plan.cols; col += 64) {
         const int at = tn * plan.cols + col, left = width - at;
         if (left <= 0) break;
         if constexpr (MODE == kDx) {
@@ -501,8 +501,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if constexpr (MODE == kAgain) {
           // Three boxes at once: dgate, dup and (should it be wanted) h.
           const int outs = args.h != nullptr ? 3 : 2;
-          if (lane == 0) bulk_wait_group_read<0>();
-          __syncwarp();
           const uint32_t box = smem_u32(out.base);
 #pragma unroll 1
           for (int s = 0; s < 2; ++s) {
@@ -512,9 +510,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t d[8], dg[8], du[8], hw[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) d[j] = ahead[j];
-            const int next = 32 * c + 16 * (s + 1);  // of this thread's columns
-            load16<T>(dh + next, ahead,
-                      live && next < plan.cols / 2 ? left - 16 * (s + 1) : 0);
+            const int next = s == 0 ? 16 : 64;  // columns on
+            load16<T>(dh + col + next, ahead,
+                      live && col + next < plan.cols ? left - next : 0);
             with_act(args.act, [&](auto tag) {
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
@@ -528,6 +526,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 hw[j] = live ? pack16<T>(a0 * u0, a1 * u1) : 0u;
               }
             });
+            if (s == 0) {  // the boxes before them have been read
+              if (lane == 0) bulk_wait_group_read<0>();
+              __syncwarp();
+            }
             out.put16(box, s, dg);
             out.put16(box + kOutBox, s, du);
             if (outs == 3) out.put16(box + 2 * kOutBox, s, hw);
@@ -595,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (row >= args.n) continue;
         const uint32_t w = pack16<T>(kNaN, kNaN);
         const int width = MODE == kDx ? args.d : args.f, cols = plan.cols / 2;
-        const int c0 = tn * plan.cols + half * cols;
+        const int c0 = tn * plan.cols + half * cols;  // any half: a multiple of 8
 #pragma unroll 1
         for (int c = c0; c < least(c0 + cols, width); c += 8) {
           if (MODE == kDx) {
@@ -663,13 +665,25 @@ bool map16(CUtensorMap* map, const void* base, int cols, long long rows, long lo
                        CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Columns of a tile: half where one round of the SM pairs then holds them all, and a
-// tile's stages take half the time (2880 x 2880, 33 rows: 23 -> 21 us a call). Not
-// otherwise: as many rows of the first operand for half the products (16384 x 4096 x
-// 14336 forward 2193 -> 3076 us; 33 rows, which the weights bound, 62 -> 68).
+// Columns of a tile: fewer where the rounds of the SM pairs then come out shorter. A
+// stage of fewer columns brings as many rows of the first operand, so a tile of half
+// the columns takes 0.70 to 0.73 of the time (16384 x 4096 x 14336 forward 2193 us with
+// 128, 3076 with 64; 33 rows, which the weights bound, 62 in two rounds, 68 in three).
 int tile_columns(int n_m, int width, int most, int pairs) {
-  const long long halves = static_cast<long long>(n_m) * ((width + most / 2 - 1) / (most / 2));
-  return halves <= pairs ? most / 2 : most;
+  const int choice[3] = {most, most / 4 * 3, most / 2};
+  const int cost[3] = {100, 86, 72};
+  int best = most;
+  long long least = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (choice[i] == 192) continue;  // dx: its weights come in boxes of 64 columns
+    const long long tiles = static_cast<long long>(n_m) * ((width + choice[i] - 1) / choice[i]);
+    const long long time = (tiles + pairs - 1) / pairs * cost[i];
+    if (i == 0 || time < least) {
+      best = choice[i];
+      least = time;
+    }
+  }
+  return best;
 }
 
 template <int MODE>
@@ -724,7 +738,8 @@ cudaError_t launch_mode(const GluArgs& args, int sms, cudaStream_t st) {
 constexpr int kRowThreads = 256;
 
 // dgate = dh u act'(g), dup = dh act(g), h = act(g) u: memory bound, 8 values of a
-// row a thread.
+// row a thread. 4096 x 14336: 90 us, 6.5 TB/s, with 32 CTAs an SM, four rounds of them
+// (110 with 8, which all run at once, 101 with a thread for each 8 values).
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads) glu_bwd_kept_kernel(const GluArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -804,7 +819,7 @@ cudaError_t launch_glu_dx(const GluArgs& a, int sms, cudaStream_t st) {
 cudaError_t launch_glu_bwd_kept(const GluArgs& a, int sms, cudaStream_t st) {
   const long long all = a.n * (a.f / 8);
   const unsigned grid = static_cast<unsigned>(
-      std::min<long long>((all + kRowThreads - 1) / kRowThreads, 8LL * sms));
+      std::min<long long>((all + kRowThreads - 1) / kRowThreads, 32LL * sms));
   LaunchTimer timer("glu_bwd_kept_kernel", st);
   if (a.fp16)
     glu_bwd_kept_kernel<__half><<<grid, kRowThreads, 0, st>>>(a);
