@@ -181,6 +181,10 @@ class AdamW:
 
     ``step_tensor`` (int64, one value, on the device) takes the count's place, for
     steps that are captured in a graph: the program adds 1 to it before each.
+
+    Parameters, moments and copies are written in place on the current stream, which
+    autograd does not see. To go on later, keep ``states``, ``steps_done``, ``seed`` and
+    the parameters, and make an AdamW of them.
     """
 
     def __init__(self, params: Sequence[torch.Tensor], *, lr, betas=(0.9, 0.999), eps=1e-8,
@@ -226,6 +230,12 @@ class AdamW:
     def _describe(self):
         for i in range(len(self.params)):
             self._fill(i)
+        # One value in two tensors would be stepped twice at once.
+        spans = sorted((p.data_ptr(), p.numel() * p.element_size(), i)
+                       for i, p in enumerate(self.params) if p.numel())
+        for (a, size, i), (b, _, j) in zip(spans, spans[1:]):
+            if a + size > b:
+                raise ValueError(f"params[{i}] and params[{j}] overlap")
         self._seen = self._now()
         self._shapes = list(map(_shape, self.params))
 

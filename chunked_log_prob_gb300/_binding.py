@@ -150,7 +150,7 @@ def _load():
         "grpo_glu_wgrad_workspace_size": [i64, i32, i32, P(sz)],
         "grpo_glu_wgrad": [vp] * 7 + [P(GrpoGluDesc), vp, sz, vp],
         "grpo_grad_norm_workspace_size": [i32, P(sz)],
-        "grpo_grad_norm": [P(GrpoGrad), i32, ctypes.c_float, vp, vp, sz, vp],
+        "grpo_grad_norm": [P(GrpoGrad), i32, ctypes.c_double, vp, vp, sz, vp],
         "grpo_adamw_step": [P(GrpoAdamwTensor), i32, P(GrpoAdamwParams), vp],
     }.items():
         fn = getattr(lib, name)

@@ -24,11 +24,15 @@ namespace {
 
 constexpr int kThreads = 256;  // of the norm's kernels
 constexpr int kWarps = kThreads / 32;
-// Of the step's: 2^28 values with moments in 8 bits, which the instructions bound, 720
-// us with CTAs of 256 threads and 676 with 128 (bf16 parameters; fp32 791 and 735), as
-// each gives its place up sooner; in 32 bits, which memory bounds, 1023 and 1036.
+// Of the step's, and the most values that a CTA takes. 2^28 values with moments in 8
+// bits, which the instructions bound: 751 us with CTAs of 256 threads, 676 with 128, 673
+// with 64 (bf16 parameters; fp32 791, 735 and 687), as each gives its place up sooner.
+// In 32 bits, which memory bounds: 1023, 1017 and 997 us with 16384, 8192 and 4096
+// values.
 template <int BITS>
-constexpr int kStepThreads = BITS == 8 ? 128 : 256;
+constexpr int kStepThreads = BITS == 8 ? 64 : 256;
+template <int BITS>
+constexpr int kStepChunk = BITS == 8 ? 16384 : 4096;
 constexpr int kGroup = 256;  // values of a warp's step
 constexpr int kBlock = 128;  // values that share a scale
 constexpr float kTop = 448.f;              // the largest e4m3
@@ -122,21 +126,20 @@ __device__ __forceinline__ uint32_t high_bytes(uint32_t a, uint32_t b, uint32_t 
   return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
 }
 
-// Eight values y scaled by f (|y f| <= 448) to e4m3 at random: a = |y f| goes to its
+// Eight values y scaled by f to e4m3 at random: a = |y f| (448 at most) goes to its
 // lower neighbour lo, or to the upper one hi where u < 2^16 (a - lo) / (hi - lo), u
-// the low 16 bits of x.
+// the low 16 bits of x. The comparison is exact.
 //
 // 2^-120 takes e4m3's normal range to fp32's, and its subnormals to fp32's: bits 20 to
 // 26 of the word are lo's code and the 20 below them (a - lo) / (hi - lo), for every
-// a, and the sign is where it was. Adding 2^20 - 1 - 16 u carries into the code where
-// those are more than 16 u.
+// a. Adding 2^20 - 1 - 16 u carries into the code where those are more than 16 u.
 __device__ __forceinline__ uint2 codes_of(const float (&y)[8], float f, const uint32_t (&x)[8]) {
   uint32_t s[8], t[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const uint32_t w = __float_as_uint((y[j] * f) * 0x1p-120f);
-    s[j] = (w + 0xfffffu) - 16u * (x[j] & 0xffffu);
-    t[j] = s[j] * 16u;
+    const uint32_t w = __float_as_uint(fminf(fabsf(y[j] * f), kTop) * 0x1p-120f);
+    t[j] = ((w + 0xfffffu) - 16u * (x[j] & 0xffffu)) * 16u;
+    s[j] = __float_as_uint(y[j]);
   }
   constexpr uint32_t kSigns = 0x80808080u;
   return make_uint2(high_bytes(t[0], t[1], t[2], t[3]) | (high_bytes(s[0], s[1], s[2], s[3]) & kSigns),
@@ -150,7 +153,7 @@ __device__ __forceinline__ uint2 codes_of_roots(const float (&y)[8], float f,
   uint32_t t[8], least = 0xffffffffu;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float a = y[j] * f;
+    const float a = fminf(y[j] * f, kTop);
     const uint32_t w = __float_as_uint(a * 0x1p-120f);
     const uint32_t lo = w & 0xfff00000u, hi = lo + 0x100000u;
     const float l = __uint_as_float(lo) * 0x1p120f, h = __uint_as_float(hi) * 0x1p120f;
@@ -181,6 +184,12 @@ __device__ __forceinline__ void lose(const float (&y)[8], uint2& q) {
 __device__ __forceinline__ float quick_root(float v) {
   float r;
   asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+// Off by 2^-22 of itself at most, for 2^-126 and more.
+__device__ __forceinline__ float quick_inverse_root(float v) {
+  float r;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
 // Off by 2^-23 of itself at most, for 0 and 2^-126 to 2^126.
@@ -223,11 +232,14 @@ struct StepOf {
   bool near;
 };
 
-// The largest |y| over the 16 lanes of a block; NaN where one of them is.
-__device__ __forceinline__ float block_top(const float (&y)[8]) {
+// The largest |y| of a lane, and over the 16 lanes of a block; NaN where one of them is.
+__device__ __forceinline__ float lane_top(const float (&y)[8]) {
   float a = max_abs_nan(y[0], y[1], y[2]);
   a = max_abs_nan(a, y[3], y[4]);
-  a = max_abs_nan(max_abs_nan(a, y[5], y[6]), y[7], y[7]);
+  return max_abs_nan(max_abs_nan(a, y[5], y[6]), y[7], y[7]);
+}
+__device__ __forceinline__ float block_top(const float (&y)[8]) {
+  float a = lane_top(y);
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) {
     const float b = __shfl_xor_sync(0xffffffffu, a, o);
@@ -316,16 +328,47 @@ __device__ __forceinline__ void step8(const AdamwEntry& e, const StepOf& s, long
         v2 = mul2(v2, v2);
       }
       const f32x2 x2 = mul2(pair(g[j], g[j + 1]), scale);
-      m2 = fma2(beta1, m2, mul2(rest1, x2));
-      v2 = fma2(beta2, v2, mul2(rest2, mul2(x2, x2)));
+      const f32x2 dm = mul2(rest1, x2), dv = mul2(rest2, mul2(x2, x2));
+      if (BITS == 8) {
+        // Each product and sum rounded (and the root below): which of two neighbours a
+        // moment goes to then follows from the formula's own fp32 values. (The
+        // assembler makes one fused step of a product and a sum of pairs.)
+        float a, b, c, d;
+        split(m2, a, b);
+        split(dm, c, d);
+        m2 = pair(__fadd_rn(__fmul_rn(s.beta1, a), c), __fadd_rn(__fmul_rn(s.beta1, b), d));
+        split(v2, a, b);
+        split(dv, c, d);
+        v2 = pair(__fadd_rn(__fmul_rn(s.beta2, a), c), __fadd_rn(__fmul_rn(s.beta2, b), d));
+      } else {
+        m2 = fma2(beta1, m2, dm);
+        v2 = fma2(beta2, v2, dv);
+      }
       split(m2, m[j], m[j + 1]);
       split(v2, v[j], v[j + 1]);
-      root[j] = quick_root(v[j]);
-      root[j + 1] = quick_root(v[j + 1]);
+      if (BITS == 8) {
+        // y about v^-1/2 to 2^-22, g = v y; then Newton's step for the root, g + (v -
+        // g^2) y / 2, which is right to the last bit but for one in a million.
+        const f32x2 y = pair(quick_inverse_root(v[j]), quick_inverse_root(v[j + 1]));
+        const f32x2 minus = pair(-1.f, -1.f), half = pair(-0.5f, -0.5f);
+        const f32x2 g2 = mul2(v2, y);
+        split(fma2(fma2(g2, g2, mul2(v2, minus)), mul2(y, half), g2), root[j], root[j + 1]);
+      } else {
+        root[j] = quick_root(v[j]);
+        root[j + 1] = quick_root(v[j + 1]);
+      }
+    }
+    if (BITS == 8 && !(lane_top(root) <= FLT_MAX)) {  // 0, subnormal or not finite: no y
+#pragma unroll
+      for (int j = 0; j < 8; ++j) root[j] = __fsqrt_rn(v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
       float d0, d1;
       split(fma2(pair(root[j], root[j + 1]), fix2, eps), d0, d1);
       // d is 0 or normal: a root of at least 2^-75, or eps
-      const f32x2 step = mul2(mul2(rate, m2), pair(quick_inverse(d0), quick_inverse(d1)));
+      const f32x2 step =
+          mul2(mul2(rate, pair(m[j], m[j + 1])), pair(quick_inverse(d0), quick_inverse(d1)));
       split(fma2(pair(p[j], p[j + 1]), shrink, step), p[j], p[j + 1]);
     }
   }
@@ -357,24 +400,20 @@ __device__ __forceinline__ void step8(const AdamwEntry& e, const StepOf& s, long
   }
   if constexpr (BITS == 8) {
     float mt = block_top(m), vt = block_top(root);
-    float mi, vi;
-    // Nothing in the warp's blocks is special (the usual case). The quick factor and
-    // its product are off by 2^-22 at most, so it is taken 3 2^-23 lower: no value
-    // passes 448, and the largest, 9 of its word's units below at most, goes there.
-    constexpr float kLow = 1.f - 3 * 0x1p-23f, kMost = 0x1p125f;
-    const bool plain = __all_sync(0xffffffffu, mt >= kLeast && mt <= kMost && vt >= kLeast &&
-                                                   vt <= kMost);
-    if (plain) {
-      mi = kTop * kLow * quick_inverse(mt);
-      vi = kTop * kLow * quick_inverse(vt);
-    } else {
+    // Nothing in the warp's blocks is special (the usual case).
+    const bool plain = __all_sync(0xffffffffu, mt <= FLT_MAX && vt <= FLT_MAX);
+    if (!plain) {
       mt = block_top_finite(m[0], m[1], m[2], m[3], m[4], m[5], m[6], m[7]);
       vt = block_top_finite(root[0], root[1], root[2], root[3], root[4], root[5], root[6], root[7]);
-      mt = mt >= kLeast ? mt : 0.f;
-      vt = vt >= kLeast ? vt : 0.f;
-      mi = mt > 0.f ? __fdiv_rz(kTop, mt) : 0.f;
-      vi = vt > 0.f ? __fdiv_rz(kTop, vt) : 0.f;
     }
+    mt = mt >= kLeast ? mt : 0.f;
+    vt = vt >= kLeast ? vt : 0.f;
+    // 448 / top: of m in the even lanes, of the root in the odd ones, and then for all.
+    // The top of a block of zeros is 0, and so is its factor.
+    const float top = (lane & 1) == 0 ? mt : vt;
+    const float factor = top > 0.f ? __frcp_rn(top) * kTop : 0.f;
+    const float mi = __shfl_sync(0xffffffffu, factor, lane & 16);
+    const float vi = __shfl_sync(0xffffffffu, factor, (lane & 16) + 1);
     uint2 mq = codes_of(m, mi, x);
     uint2 vq = codes_of_roots(root, vi, x, vt > 0.f ? 0.f : FLT_MAX);
     if (!plain) {
@@ -394,10 +433,8 @@ __device__ __forceinline__ void step8(const AdamwEntry& e, const StepOf& s, long
               static_cast<uint8_t>((j < 4 ? vq.x : vq.y) >> (8 * (j & 3)));
         }
     }
-    if ((lane & 15) == 0 && have[0]) {
-      e.m_scale[block] = mt * (1.f / kTop);
-      e.v_scale[block] = vt * (1.f / kTop);
-    }
+    if ((lane & 14) == 0 && static_cast<long long>(block) * kBlock < e.numel)
+      ((lane & 1) == 0 ? e.m_scale : e.v_scale)[block] = top * (1.f / kTop);
   }
   if constexpr (sizeof(P) == 2) {
     // To bf16 at random: 16 random bits below the kept ones, then cut off; infinities
@@ -568,37 +605,65 @@ __device__ __forceinline__ double cta_sum(double v) {
   return v;
 }
 
-// A thread's squares of a chunk: fp32 sums of 32 at most, added in fp64.
+// A sum of fp32 values in two parts, two such sums side by side: what the sum's
+// rounding leaves is found exactly and kept (the sum of two floating-point numbers and
+// its error: Knuth), so that the norm is right to fp32's last bit however many there are;
+// fp64 for every value would take three times as long as reading it.
+struct Squares {
+  f32x2 sum = 0ull, rest = 0ull;
+
+  __device__ __forceinline__ void add(f32x2 q) {
+    const f32x2 minus = pair(-1.f, -1.f);
+    const f32x2 t = add2(sum, q);
+    const f32x2 b = fma2(sum, minus, t);                           // t - sum
+    const f32x2 c = add2(fma2(b, minus, q), fma2(fma2(b, minus, t), minus, sum));
+    sum = t;
+    rest = add2(rest, c);
+  }
+  // Two values' squares; EXACT: they are fp32 numbers themselves (16-bit values').
+  template <bool EXACT>
+  __device__ __forceinline__ void square(float x, float y) {
+    const f32x2 v = pair(x, y), q = pair(__fmul_rn(x, x), __fmul_rn(y, y));
+    add(q);
+    if (!EXACT) rest = add2(rest, fma2(v, v, mul2(q, pair(-1.f, -1.f))));
+  }
+  __device__ __forceinline__ double total() const {
+    float a, b, c, d;
+    split(sum, a, b);
+    split(rest, c, d);
+    return (static_cast<double>(a) + static_cast<double>(c)) +
+           (static_cast<double>(b) + static_cast<double>(d));
+  }
+};
+
+// A thread's squares of a chunk.
 template <typename T>
-__device__ __forceinline__ double squares(const void* p, long long begin, long long end) {
-  double sum = 0.0;
+__device__ __forceinline__ void squares(const void* p, long long begin, long long end,
+                                        Squares& s) {
+  constexpr bool kExact = sizeof(T) == 2;
   long long at = begin;
   if (on(p, 16)) {  // begin is a multiple of the chunk
     constexpr int kStep = kThreads * 8;
     for (; at + 4 * kStep <= end; at += 4 * kStep) {
-      float v[4][8], q = 0.f;
+      float v[4][8];
 #pragma unroll
       for (int k = 0; k < 4; ++k) load8<T>(p, at + k * kStep + threadIdx.x * 8, v[k]);
 #pragma unroll
       for (int k = 0; k < 4; ++k)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) q += v[k][j] * v[k][j];
-      sum += static_cast<double>(q);
+        for (int j = 0; j < 8; j += 2) s.square<kExact>(v[k][j], v[k][j + 1]);
     }
   }
-  for (; at < end; at += 32 * kThreads) {
-    float q = 0.f;
-#pragma unroll 8
-    for (int k = 0; k < 32; ++k) {
+  for (; at < end; at += 8 * kThreads) {
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
       const long long i = at + k * kThreads + threadIdx.x;
-      if (i < end) {
-        const float v = load1<T>(p, i);
-        q += v * v;
-      }
+      v[k] = i < end ? load1<T>(p, i) : 0.f;
     }
-    sum += static_cast<double>(q);
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) s.square<kExact>(v[k], v[k + 1]);
   }
-  return sum;
 }
 
 // One partial sum a CTA; CTAs take the chunks round robin.
@@ -607,37 +672,37 @@ __global__ void __launch_bounds__(kThreads)
     grad_norm_kernel(const __grid_constant__ NormTable<N> table, int count, int chunks,
                      double* partials) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  double sum = 0.0;
+  Squares s;
   for (int c = static_cast<int>(blockIdx.x); c < chunks; c += static_cast<int>(gridDim.x)) {
     const NormEntry& e = table.e[find_entry(table.e, count, c)];
     const long long begin = static_cast<long long>(c - e.chunk) * kNormChunk;
     const long long end = min(begin + kNormChunk, e.numel);
     if (e.type == GRPO_DTYPE_FP32)
-      sum += squares<float>(e.grad, begin, end);
+      squares<float>(e.grad, begin, end, s);
     else if (e.type == GRPO_DTYPE_BF16)
-      sum += squares<__nv_bfloat16>(e.grad, begin, end);
+      squares<__nv_bfloat16>(e.grad, begin, end, s);
     else
-      sum += squares<__half>(e.grad, begin, end);
+      squares<__half>(e.grad, begin, end, s);
   }
-  sum = cta_sum(sum);
+  const double sum = cta_sum(s.total());
   if (threadIdx.x == 0) partials[blockIdx.x] = sum;
 }
 
 // norm and scale from the partial sums, in their order.
 __global__ void __launch_bounds__(kThreads)
-    grad_norm_finish_kernel(const double* partials, int count, float max_norm, float* out) {
+    grad_norm_finish_kernel(const double* partials, int count, double max_norm, float* out) {
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial sums are there
   double sum = 0.0;
   for (int i = static_cast<int>(threadIdx.x); i < count; i += kThreads) sum += partials[i];
   sum = cta_sum(sum);
   if (threadIdx.x != 0) return;
-  const float norm = static_cast<float>(sqrt(sum));
-  out[0] = norm;
+  const double norm = sqrt(sum);
+  out[0] = static_cast<float>(norm);
   float scale = 1.f;
-  if (!(norm <= FLT_MAX))
+  if (!(out[0] <= FLT_MAX))
     scale = kNaN;
-  else if (max_norm > 0.f)
-    scale = fminf(1.f, max_norm / (norm + 1e-6f));
+  else if (max_norm > 0.0)
+    scale = static_cast<float>(fmin(1.0, max_norm / (norm + 1e-6)));
   out[1] = scale;
 }
 
@@ -666,7 +731,7 @@ cudaError_t launch_norm(const NormEntry* e, int count, int chunks, double* parti
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 size_t dtype_bytes(int t) { return t == GRPO_DTYPE_FP32 ? 4 : 2; }
 bool known_dtype(int t) { return t >= GRPO_DTYPE_BF16 && t <= GRPO_DTYPE_FP32; }
-constexpr int64_t kMaxValues = 1LL << 44;
+constexpr int64_t kMaxValues = 1LL << 40;
 
 size_t norm_workspace(int32_t count) {
   const size_t launches = (static_cast<size_t>(count) + kNormTable - 1) / kNormTable;
@@ -709,7 +774,7 @@ int grpo_grad_norm_workspace_size(int32_t count, size_t* bytes) {
   return GRPO_OK;
 }
 
-int grpo_grad_norm(const grpo_grad* grads, int32_t count, float max_norm, float* out,
+int grpo_grad_norm(const grpo_grad* grads, int32_t count, double max_norm, float* out,
                    void* workspace, size_t workspace_bytes, void* stream) {
   const CallRange range("grpo_grad_norm");
   if (count < 0 || (count > 0 && grads == nullptr) || out == nullptr || workspace == nullptr ||
@@ -789,10 +854,6 @@ int grpo_adamw_step(const grpo_adamw_tensor* tensors, int32_t count,
   const int r = setup_device(&sms);
   if (r != GRPO_OK) return r;
   AdamwArgs a;
-  // The largest chunk that still gives every SM eight CTAs: long chunks find their
-  // tensor and work out the step less often, short ones fill the device.
-  a.chunk = 16384;
-  while (a.chunk > 8 * kGroup && values / a.chunk < 8LL * sms) a.chunk /= 2;
   a.beta1 = static_cast<float>(q.beta1);
   a.beta2 = static_cast<float>(q.beta2);
   a.rest1 = static_cast<float>(1.0 - q.beta1);
@@ -813,6 +874,10 @@ int grpo_adamw_step(const grpo_adamw_tensor* tensors, int32_t count,
   // Tensors with moments of either kind have launches of their own.
   AdamwEntry e[kLargeTable];
   for (const int bits : {32, 8}) {
+    // The largest chunk that still gives every SM eight CTAs: long chunks find their
+    // tensor and work out the step less often, short ones fill the device.
+    a.chunk = bits == 8 ? kStepChunk<8> : kStepChunk<32>;
+    while (a.chunk > (bits == 8 ? 4 : 8) * kGroup && values / a.chunk < 8LL * sms) a.chunk /= 2;
     int64_t chunks = 0, place = 0;
     a.count = 0;
     auto flush = [&]() {

@@ -14,8 +14,8 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "grpo_gb300.h"
-#include "kernel_fit.h"
 #include "glu.h"
+#include "kernel_fit.h"
 #include "launch.h"
 
 namespace grpo {

@@ -25,6 +25,7 @@
 
 #include "launch.h"
 #include "norm.h"
+#include "pair_roles.cuh"
 #include "row_ops.cuh"
 #include "wgrad_plan.h"
 
@@ -67,34 +68,6 @@ constexpr int kSmem = 1024 + (kDy + kX) * kOperand + kRaw * kRawBytes +
 constexpr uint32_t kTmemCols = 512;
 static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 constexpr int kSlotFloats = kTileM * kTileN;
-
-__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity))
-    if (clock64() - t0 > kWaitLimitCycles) return;
-}
-
-// A warp's wait: one answer for all lanes, before steps of the whole warp. Each
-// polls for itself, and one may give up (or see the abort flag) as another finds
-// the phase done.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                          int* status) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status)) != 0;
-}
-
-// True in one lane of the (whole) warp. The compiler then knows that one thread
-// runs what follows and feeds tcgen05 and TMA their uniform operands directly;
-// behind `lane == 0` it cannot, and a stage took its issuing thread twice as
-// long as the tensor core (16384 x 4096 x 4096: 518 us against 407).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred P;\n\t"
-      "elect.sync _|P, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, P;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
 
 template <int N>
 __device__ __forceinline__ void take_registers() {

@@ -18,6 +18,7 @@
 #include "glu.h"
 #include "glu_act.cuh"
 #include "launch.h"
+#include "pair_roles.cuh"
 #include "row_ops.cuh"
 #include "wgrad_plan.h"
 
@@ -109,27 +110,6 @@ __device__ __forceinline__ int list_segments(const uint8_t* mask, long long n, i
   }
   __syncthreads();
   return live;
-}
-
-__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity))
-    if (clock64() - t0 > kWaitLimitCycles) return;
-}
-
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                          int* status) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status)) != 0;
-}
-
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred P;\n\t"
-      "elect.sync _|P, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, P;\n\t}"
-      : "=r"(p));
-  return p != 0;
 }
 
 template <typename T>
@@ -704,10 +684,12 @@ cudaError_t launch_mode(const GluArgs& args, int sms, cudaStream_t st) {
     if (MODE != kDx && i == 1) {
       a[1] = a[0];
       a[3] = a[2];
-    } else if (!map16(&a[i], first[i], depth, args.n, ld[i], 128) ||
-               !map16(&a[2 + i], first[i], depth, args.n, ld[i], kSeg)) {
-      return cudaErrorInvalidValue;
+      continue;
     }
+    if (!map16(&a[i], first[i], depth, args.n, ld[i], 128)) return cudaErrorInvalidValue;
+    a[2 + i] = a[i];
+    if (plan.segs > 0 && !map16(&a[2 + i], first[i], depth, args.n, ld[i], kSeg))
+      return cudaErrorInvalidValue;
   }
   if (!map16(&b[0], args.w_gate, args.d, args.f, args.ldwg, b_rows) ||
       !map16(&b[1], args.w_up, args.d, args.f, args.ldwu, b_rows))

@@ -13,6 +13,7 @@
 
 #include "glu.h"
 #include "launch.h"
+#include "pair_roles.cuh"
 #include "row_ops.cuh"
 #include "wgrad_plan.h"
 
@@ -41,27 +42,6 @@ static_assert(kSmem <= 227 * 1024 - 1024, "shared memory of a CTA");
 static_assert(kBoxesOfTile == 2 * kBoxes, "each box is loaded twice a tile");
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSlotFloats = kTileM * kTileN;
-
-__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity))
-    if (clock64() - t0 > kWaitLimitCycles) return;
-}
-
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                          int* status) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status)) != 0;
-}
-
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred P;\n\t"
-      "elect.sync _|P, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, P;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
 
 // Row tiles of one weight: the first half of the plan's are the gate's.
 __host__ __device__ __forceinline__ int half_tiles(int f) { return (f + kTileM - 1) / kTileM; }

@@ -569,12 +569,13 @@ typedef struct grpo_grad {
 
 /* norm = sqrt(sum over all tensors of g^2), scale = min(1, max_norm / (norm + 1e-6))
  * (max_norm <= 0: 1). out: fp32 [2] on the device, norm and scale; where the norm is
- * not finite the scale is NaN. Squares, and sums of 32 of them, are fp32 (a gradient
- * beyond 1.8e19 counts as not finite), further sums fp64 in an order fixed by the
- * sizes. Tensors are packed and start on an element; NULL ones add nothing. grads: on
- * the host, read during the call. */
+ * not finite the scale is NaN. Squares are fp32 (a gradient beyond 1.8e19 counts as not
+ * finite, one below 1e-23 as 0), what their sums round off is kept, so both results
+ * are right to the last bit or so; the order is fixed by the sizes. Tensors are packed
+ * and start on an element; NULL ones add nothing. grads: on the host, read during the
+ * call. */
 int grpo_grad_norm_workspace_size(int32_t count, size_t* bytes);
-int grpo_grad_norm(const grpo_grad* grads, int32_t count, float max_norm, float* out,
+int grpo_grad_norm(const grpo_grad* grads, int32_t count, double max_norm, float* out,
                    void* workspace, size_t workspace_bytes, void* stream);
 
 /* One tensor of the optimizer: packed, each part starting on an element. A NULL grad
@@ -631,9 +632,10 @@ int grpo_adamw_step(const grpo_adamw_tensor* tensors, int32_t count,
  * its CTA has to do after it (where two CTAs share a row: the first of them), or its
  * next grpo_ckpt_wgrad or grpo_glu_wgrad does not copy the 64-token stage `index`,
  * its next grpo_glu_fwd or grpo_glu_bwd (the first of its products) the 64-column
- * stage (counted over the stages of the first CTA's tiles), to that CTA. The wait for it runs out after about a second, the kernel gives up the work that
- * depends on it (NaN in its place), lets the copies in flight land and returns;
- * the context stays usable. -1: nothing is left out. */
+ * stage (counted over the stages of the first CTA's tiles), to that CTA. The wait for
+ * it runs out after about a second, the kernel gives up the work that depends on it
+ * (NaN in its place), lets the copies in flight land and returns; the context stays
+ * usable. A forward pass of up to 8 rows waits for nothing. -1: nothing is left out. */
 int grpo_selftest_lose_copy(int64_t index);
 
 /* Static text for a status code. */

@@ -331,6 +331,12 @@ def test_shapes_gradients_and_exchanged_storage(clp):
         clp.AdamW([q], lr=LR, states=[])
     with pytest.raises(ValueError, match="lr"):
         clp.AdamW([q], lr=[1.0, 2.0])
+    r = torch.zeros(20, device=DEV)
+    with pytest.raises(ValueError, match="overlap"):
+        clp.AdamW([q, r, q], lr=LR)
+    with pytest.raises(ValueError, match="overlap"):
+        clp.AdamW([r[4:12], q, r[11:]], lr=LR)
+    clp.AdamW([r[:4], r[4:4], r[4:]], lr=LR)
     with pytest.raises(ValueError, match="step_tensor"):
         clp.AdamW([q], lr=LR, step_tensor=torch.zeros(1, device=DEV))
 
@@ -378,3 +384,41 @@ def test_results_repeat(clp):
         runs.append(p + [z for s in opt.states for z in s.moments()])
     for a, b in zip(*runs):
         assert torch.equal(a, b)
+
+
+def test_going_on_from_kept_states_is_the_same(clp):
+    g = _gen(10)
+    sizes = [1000, 257]
+    base = _tensors(g, sizes)
+    grads = [_tensors(g, sizes, F32, 0.1) for _ in range(4)]
+    a, b = [x.clone() for x in base], [x.clone() for x in base]
+    one = clp.AdamW(a, lr=LR, state_bits=8, seed=3)
+    two = clp.AdamW(b, lr=LR, state_bits=8, seed=3)
+    for x in grads[:2]:
+        one.step(x)
+        two.step(x)
+    kept = [clp.AdamState(*(z.clone() for z in s)) for s in two.states]
+    two = clp.AdamW(b, lr=LR, states=kept, steps_done=two.steps_done, seed=3)
+    for x in grads[2:]:
+        one.step(x)
+        two.step(x)
+    for p, q in zip(a, b):
+        assert torch.equal(p, q)
+    for s, t in zip(one.states, two.states):
+        for p, q in zip(s.moments(), t.moments()):
+            assert torch.equal(p, q)
+
+
+def test_on_another_stream(clp):
+    g = _gen(11)
+    p, gr = torch.randn(50_000, generator=g).to(DEV), torch.randn(50_000, generator=g).to(DEV)
+    q = p.clone()
+    one, two = clp.AdamW([p], lr=LR), clp.AdamW([q], lr=LR)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        one.step([gr], scale=clp.grpo_grad_norm([gr], max_norm=1.0).scale)
+        with torch.cuda.stream(side):
+            two.step([gr], scale=clp.grpo_grad_norm([gr], max_norm=1.0).scale)
+    torch.cuda.synchronize()
+    assert torch.equal(p, q)

@@ -484,3 +484,33 @@ def test_a_lost_copy_with_something_to_add(clp):
             assert torch.equal(p[fine], q[fine])
     for p, q in zip(clp.grpo_glu_wgrad(dg, du, x, add_gate=add, add_up=add, workspace=ws), want):
         assert torch.equal(p, q)
+
+
+def test_more_masked_rows_than_are_listed(clp):
+    # Beyond 131072 rows the tiles are of consecutive rows, masked ones among them.
+    g = _gen(12)
+    n, d, f = 131_100, 16, 24
+    x, (wg, wu), dh = _randn(g, n, d), _weights(g, f, d, BF), _randn(g, n, f)
+    m = _mask("some", n, g)
+    m[1000:3000] = 0
+    off = m == 0
+    want = clp.grpo_glu_fwd(x, wg, wu), clp.grpo_glu_bwd(dh, x, wg, wu, want_h=True)
+    x[off], dh[off] = float("nan"), float("nan")
+    got = (clp.grpo_glu_fwd(x, wg, wu, mask=m),
+           clp.grpo_glu_bwd(dh, x, wg, wu, mask=m, want_h=True))
+    for a, b in zip(got, want):
+        for p, q in zip(a, b):
+            if p is not None:
+                assert (p[off] == 0).all() and torch.equal(p[~off], q[~off])
+
+
+@pytest.mark.parametrize("n", [16 * 8192, 16 * 8192 - 5])
+def test_as_many_masked_rows_as_are_listed(clp, n):
+    g = _gen(13)
+    d, f = 8, 16
+    x, (wg, wu) = _randn(g, n, d), _weights(g, f, d, BF)
+    m = torch.zeros(n + 3, dtype=torch.uint8, device=DEV)[3:]  # off 16 bytes
+    m[-1] = m[77] = 1
+    h = clp.grpo_glu_fwd(x, wg, wu, mask=m).h
+    want = clp.grpo_glu_fwd(x, wg, wu).h
+    assert torch.equal(h[m != 0], want[m != 0]) and not h[m == 0].any()
