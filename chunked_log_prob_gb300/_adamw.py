@@ -97,11 +97,12 @@ def _quick(view, field, grads, device):
     of them are what is expected; None otherwise: they are then looked at one by one.
     (A set of adapters has hundreds, at a few us each one by one.)"""
     try:
-        codes = [_DTYPES[t] for t in map(_dtype, grads)]
+        types = list(map(_dtype, grads))
+        codes = _DTYPES[types[0]] if len(set(types)) == 1 else [_DTYPES[t] for t in types]
         if set(map(_device_index, grads)) != {device.index} or not all(map(_packed, grads)):
             return None
         data = list(map(_data_ptr, grads))
-    except (AttributeError, KeyError, TypeError):  # None among them, or another type
+    except (AttributeError, KeyError, TypeError, IndexError):  # None, or another type
         return None
     view[field] = codes
     return data
@@ -190,7 +191,7 @@ class AdamW:
     def __init__(self, params: Sequence[torch.Tensor], *, lr, betas=(0.9, 0.999), eps=1e-8,
                  weight_decay=0.01, state_bits=32, states=None, copies=None, steps_done=0, seed=0,
                  step_tensor=None):
-        self.params = list(params)
+        self.params = tuple(params)
         n = len(self.params)
         if n == 0:
             raise ValueError("params: none given")
@@ -207,8 +208,8 @@ class AdamW:
         self.weight_decay = _per_tensor(weight_decay, n, "weight_decay")
         if states is None:
             states = [alloc_adam_state(p, state_bits) for p in self.params]
-        self.states = [s if isinstance(s, AdamState) else AdamState(*s) for s in states]
-        self.copies = [None] * n if copies is None else list(copies)
+        self.states = tuple(s if isinstance(s, AdamState) else AdamState(*s) for s in states)
+        self.copies = (None,) * n if copies is None else tuple(copies)
         if len(self.states) != n or len(self.copies) != n:
             raise ValueError(f"states and copies: expected {n} of them, got {len(self.states)} "
                              f"and {len(self.copies)}")
@@ -223,10 +224,6 @@ class AdamW:
         self._view = np.frombuffer(self._table, dtype=GrpoAdamwTensor)
         self._describe()
 
-    def _now(self):
-        """Where the parameters are, and how many values they have."""
-        return list(map(_data_ptr, self.params)), list(map(_numel, self.params))
-
     def _describe(self):
         for i in range(len(self.params)):
             self._fill(i)
@@ -236,7 +233,7 @@ class AdamW:
         for (a, size, i), (b, _, j) in zip(spans, spans[1:]):
             if a + size > b:
                 raise ValueError(f"params[{i}] and params[{j}] overlap")
-        self._seen = self._now()
+        self._at = list(map(_data_ptr, self.params))
         self._shapes = list(map(_shape, self.params))
 
     def _grad(self, i, g):
@@ -287,8 +284,8 @@ class AdamW:
              lr_factor=None) -> None:
         """One step. grads: one for each parameter, bf16, fp16 or fp32 (None leaves the
         tensor as it is); by default their ``.grad``. scale: fp32 on the device,
-        multiplies the gradients; where it is not finite the step changes nothing. lr:
-        from this step on. lr_factor: fp32 on the device, multiplies it."""
+        multiplies the gradients; where it is not finite the step changes nothing (and
+        is counted all the same). lr: from this step on. lr_factor: fp32 on the device, multiplies it."""
         params, dev = self.params, self.device
         if grads is None:
             grads = [p.grad for p in params]
@@ -296,12 +293,14 @@ class AdamW:
             raise ValueError(f"grads: expected {len(params)} of them, got {len(grads)}")
         if lr is not None:
             self.lr = _per_tensor(lr, len(params), "lr")
-        if self._now() != self._seen:  # a parameter's storage was exchanged
+        if list(map(_data_ptr, params)) != self._at:  # a parameter's storage was exchanged
             self._describe()
         view = self._view
         view["lr"], view["weight_decay"] = self.lr, self.weight_decay
         data = _quick(view, "grad_dtype", grads, dev)
         if data is None or list(map(_shape, grads)) != self._shapes:
+            if list(map(_shape, params)) != self._shapes:  # or other values of it taken
+                self._describe()
             data = [self._grad(i, g) for i, g in enumerate(grads)]
         view["grad"] = data
         q = GrpoAdamwParams(*self.betas, self.eps, self.steps_done + 1, self.seed)

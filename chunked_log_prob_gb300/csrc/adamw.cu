@@ -260,7 +260,7 @@ __device__ __noinline__ float block_top_finite(float y0, float y1, float y2, flo
 }
 
 // A lane's 8 values: consecutive from `first` on (VEC, all there), or every 16th of
-// their block (the `have` lowest bits of mask say which are there).
+// their block, as far as the tensor goes.
 template <int BITS, typename P, typename G, bool VEC>
 __device__ __forceinline__ void step8(const AdamwEntry& e, const StepOf& s, long long first,
                                       int lane) {

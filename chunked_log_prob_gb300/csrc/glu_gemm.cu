@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   if constexpr (MODE == kDx)
     asm volatile("griddepcontrol.wait;" ::: "memory");  // dgate and dup are there
-  else
+  else if constexpr (MODE == kAgain)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem_base = tmem_base_sh;
   const int stages = MODE == kDx ? plan.kt2 : plan.kt;
@@ -320,8 +320,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         int rows[kTileSegs / 2];  // where the tile's segments begin
 #pragma unroll
         for (int j = 0; j < kTileSegs / 2; ++j) rows[j] = static_cast<int>(row_of(tm, j * kSeg));
-        const bool together =
-            plan.segs == 0 || rows[kTileSegs / 2 - 1] - rows[0] == 128 - kSeg;
+        // One box holds them where the last one is there, and that far from the first.
+        const int last = rows[kTileSegs / 2 - 1];
+        const bool together = plan.segs == 0 || (last < args.n && last - rows[0] == 128 - kSeg);
         const int n0 = tn * plan.cols + (MODE == kDx ? static_cast<int>(rank) *
                                                            (dx_cols(plan, args.d, tn) / 2)
                                                      : 0);

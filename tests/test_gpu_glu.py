@@ -514,3 +514,22 @@ def test_as_many_masked_rows_as_are_listed(clp, n):
     h = clp.grpo_glu_fwd(x, wg, wu, mask=m).h
     want = clp.grpo_glu_fwd(x, wg, wu).h
     assert torch.equal(h[m != 0], want[m != 0]) and not h[m == 0].any()
+
+
+@pytest.mark.parametrize("n", [112, 368, 240, 256, 111, 113])
+def test_segments_apart_in_the_last_tile(clp, n):
+    # Every second segment of a tile whose rows end 112 behind its first: the places
+    # that hold none must not look like the eighth of eight in a row.
+    g = _gen(n)
+    d, f = 72, 136
+    x, (wg, wu), dh = _randn(g, n, d), _weights(g, f, d, BF), _randn(g, n, f)
+    want = clp.grpo_glu_fwd(x, wg, wu), clp.grpo_glu_bwd(dh, x, wg, wu, want_h=True)
+    at = torch.arange(n, device=DEV) // 16
+    for keep in (at % 2 == 0, at % 3 == 0, at >= at.max() - 1, at != at.max() // 2):
+        m = keep.to(torch.uint8)
+        got = (clp.grpo_glu_fwd(x, wg, wu, mask=m),
+               clp.grpo_glu_bwd(dh, x, wg, wu, mask=m, want_h=True))
+        for a, b in zip(got, want):
+            for p, q in zip(a, b):
+                if p is not None:
+                    assert torch.equal(p[keep], q[keep]) and not p[~keep].any()
