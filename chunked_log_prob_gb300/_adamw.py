@@ -145,7 +145,7 @@ def grpo_grad_norm(grads: Sequence[torch.Tensor | None], *, max_norm=None, out=N
                  workspace.data_ptr(), workspace.numel() * workspace.element_size())
     if rc:
         raise GrpoError(rc, "grpo_grad_norm")
-    return GradNorm(out[0], out[1])
+    return GradNorm(*out.unbind())
 
 
 # --------------------------------------------------------------------- AdamW ----
