@@ -41,6 +41,7 @@ from ._glu import (  # noqa: F401
     GluBackward,
     GluForward,
     grpo_glu_bwd,
+    grpo_glu_bwd_workspace_size,
     grpo_glu_fwd,
     grpo_glu_wgrad,
     grpo_glu_wgrad_workspace_size,

@@ -146,7 +146,8 @@ def _load():
         "grpo_selftest_lose_copy": [i64],
         "grpo_ckpt_wgrad": [vp, vp, vp, vp, i64, i32, i32, i64, vp, sz, vp],
         "grpo_glu_fwd": [vp] * 8 + [P(GrpoGluDesc), vp],
-        "grpo_glu_bwd": [vp] * 11 + [P(GrpoGluDesc), vp],
+        "grpo_glu_bwd": [vp] * 11 + [P(GrpoGluDesc), vp, sz, vp],
+        "grpo_glu_bwd_workspace_size": [i64, i32, i32, P(sz)],
         "grpo_glu_wgrad_workspace_size": [i64, i32, i32, P(sz)],
         "grpo_glu_wgrad": [vp] * 7 + [P(GrpoGluDesc), vp, sz, vp],
         "grpo_grad_norm_workspace_size": [i32, P(sz)],
@@ -169,7 +170,8 @@ EXPORTED = ("grpo_default_params", "grpo_workspace_size", "grpo_logp_fwd",
             "grpo_norm_fwd", "grpo_norm_workspace_size", "grpo_norm_bwd", "grpo_ckpt_size",
             "grpo_ckpt_layout", "grpo_ckpt_pack", "grpo_ckpt_unpack",
             "grpo_ckpt_wgrad_workspace_size", "grpo_ckpt_wgrad", "grpo_selftest_lose_copy",
-            "grpo_glu_fwd", "grpo_glu_bwd", "grpo_glu_wgrad_workspace_size", "grpo_glu_wgrad",
+            "grpo_glu_fwd", "grpo_glu_bwd", "grpo_glu_bwd_workspace_size",
+            "grpo_glu_wgrad_workspace_size", "grpo_glu_wgrad",
             "grpo_grad_norm_workspace_size", "grpo_grad_norm", "grpo_adamw_step")
 
 FLAG_STORED_LOGITS = 1

@@ -112,13 +112,14 @@ def grpo_glu_fwd(x, w_gate, w_up, *, act="silu", mask=None, want_gates=False, wa
 
 
 def grpo_glu_bwd(dh, x, w_gate, w_up, *, gate=None, up=None, act="silu", mask=None, want_dx=True,
-                 want_h=False, dgate=None, dup=None, dx=None, h=None) -> GluBackward:
+                 want_h=False, dgate=None, dup=None, dx=None, h=None, workspace=None) -> GluBackward:
     """Gradients of ``grpo_glu_fwd``: dgate, dup [N, F] of the projections, dx [N, D].
 
     ``gate`` and ``up`` are the projections that the forward pass kept (x may be None
     then); without them they are computed again from x. want_h: h again, for the
     weight gradient of the layer that it went into. dgate and dup may be given as dh,
-    gate and up themselves, whose contents are lost then.
+    gate and up themselves, whose contents are lost then. The workspace
+    (``grpo_glu_bwd_workspace_size`` bytes) is allocated when not given.
     """
     code, k = _type_of(dh, "dh"), _act(act)
     shape, dt, dev = dh.shape, dh.dtype, dh.device
@@ -161,12 +162,36 @@ def grpo_glu_bwd(dh, x, w_gate, w_up, *, gate=None, up=None, act="silu", mask=No
     elif want_h:
         h = _empty(shape, dtype=dt, device=dev)
         ph = h.data_ptr()
+    pw, nw = None, 0
+    if pdx is not None:
+        if workspace is None:
+            nw = _bwd_workspace(n, f, d)
+            if nw:
+                workspace = _empty(nw, dtype=_U8, device=dev)
+                pw = workspace.data_ptr()
+        elif workspace.device != dev:
+            raise ValueError(f"workspace: expected device {dev}, got {workspace.device}")
+        else:
+            pw, nw = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     desc = GrpoGluDesc(n, d, f, code, k, sx, swg, swu, sh, sg, su, sdh, sdg, sdu, sdx)
     rc = call_on(dev, lib.grpo_glu_bwd, dh.data_ptr(), px, w_gate.data_ptr(), w_up.data_ptr(), pg,
-                 pu, pm, dgate.data_ptr(), dup.data_ptr(), pdx, ph, _byref(desc))
+                 pu, pm, dgate.data_ptr(), dup.data_ptr(), pdx, ph, _byref(desc), pw, nw)
     if rc:
         raise GrpoError(rc, "grpo_glu_bwd")
     return GluBackward(dgate, dup, dx, h)
+
+
+@lru_cache(maxsize=512)
+def _bwd_workspace(n, f, d):
+    out = ctypes.c_size_t(0)
+    rc = lib.grpo_glu_bwd_workspace_size(n, f, d, _byref(out))
+    if rc != GRPO_OK:
+        raise GrpoError(rc, "grpo_glu_bwd_workspace_size")
+    return int(out.value)
+
+
+def grpo_glu_bwd_workspace_size(n_tokens, inner, hidden) -> int:
+    return _bwd_workspace(int(n_tokens), int(inner), int(hidden))
 
 
 @lru_cache(maxsize=512)

@@ -29,6 +29,7 @@ struct GluArgs {
   int d, f;
   int fp16;  // the 16-bit type: 0 bf16, 1 fp16
   int act;
+  float* partials;  // dx: pieces of cut tiles, or null (nothing is cut)
   uint32_t lost;  // self-test: the first CTA's stage whose copies are left out, or kNoneLost
 };
 
@@ -41,7 +42,8 @@ cudaError_t launch_glu_small(const GluArgs& a, int sms, cudaStream_t st);
 cudaError_t launch_glu_bwd_again(const GluArgs& a, int sms, cudaStream_t st);
 // The same from the projections as they were kept.
 cudaError_t launch_glu_bwd_kept(const GluArgs& a, int sms, cudaStream_t st);
-// dx = a.gate Wg + a.up Wu.
+// dx = a.gate Wg + a.up Wu. Bytes of partials that help it (host only; 0: none).
+size_t glu_dx_workspace(long long n, int f, int d);
 cudaError_t launch_glu_dx(const GluArgs& a, int sms, cudaStream_t st);
 cudaError_t prepare_glu_gemm();
 

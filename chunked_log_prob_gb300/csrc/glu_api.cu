@@ -114,7 +114,8 @@ int grpo_glu_fwd(const void* x, const void* w_gate, const void* w_up, const uint
 
 int grpo_glu_bwd(const void* dh, const void* x, const void* w_gate, const void* w_up,
                  const void* gate, const void* up, const uint8_t* mask, void* dgate, void* dup,
-                 void* dx, void* h, const grpo_glu_desc* desc, void* stream) {
+                 void* dx, void* h, const grpo_glu_desc* desc, void* workspace,
+                 size_t workspace_bytes, void* stream) {
   const CallRange range("grpo_glu_bwd");
   int r = check_desc(desc);
   if (r != GRPO_OK) return r;
@@ -127,6 +128,10 @@ int grpo_glu_bwd(const void* dh, const void* x, const void* w_gate, const void* 
                         static_cast<const void*>(dup), static_cast<const void*>(dx),
                         static_cast<const void*>(h)})
     if (!on16(p)) return GRPO_ERR_MISALIGNED;
+  if (!on(workspace, 256)) return GRPO_ERR_MISALIGNED;
+  const size_t need = glu_dx_workspace(desc->n_tokens, desc->inner, desc->hidden);
+  if (workspace != nullptr && dx != nullptr && workspace_bytes < need)
+    return GRPO_ERR_WORKSPACE_TOO_SMALL;
   int sms = 0;
   if ((r = setup_device(&sms)) != GRPO_OK) return r;
   if (desc->n_tokens == 0) return GRPO_OK;
@@ -146,6 +151,7 @@ int grpo_glu_bwd(const void* dh, const void* x, const void* w_gate, const void* 
   a.ldg = stride_or(desc->dgate_stride, desc->inner);
   a.ldu = stride_or(desc->dup_stride, desc->inner);
   a.dx = dx;
+  a.partials = need > 0 ? static_cast<float*>(workspace) : nullptr;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const uint32_t lost = take_lost();
   if (!kept) a.lost = lost;
@@ -154,6 +160,14 @@ int grpo_glu_bwd(const void* dh, const void* x, const void* w_gate, const void* 
   if (dx == nullptr) return GRPO_OK;
   a.lost = kept ? lost : kNoneLost;
   return launch_glu_dx(a, sms, st) == cudaSuccess ? GRPO_OK : GRPO_ERR_CUDA;
+}
+
+int grpo_glu_bwd_workspace_size(int64_t n_tokens, int32_t inner, int32_t hidden, size_t* bytes) {
+  if (bytes == nullptr) return GRPO_ERR_INVALID_ARG;
+  const int r = check_sizes(n_tokens, inner, hidden);
+  if (r != GRPO_OK) return r;
+  *bytes = glu_dx_workspace(n_tokens, inner, hidden);
+  return GRPO_OK;
 }
 
 int grpo_glu_wgrad_workspace_size(int64_t n_tokens, int32_t inner, int32_t hidden, size_t* bytes) {

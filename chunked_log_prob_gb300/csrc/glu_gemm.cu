@@ -11,7 +11,8 @@
 // lane. They leave TMEM once, as h (or as the gradients): against two GEMMs and an
 // elementwise pass, x is read once and the fp32 projections are never written. dx
 // is one sum over 2 f columns, its first half from (dgate, Wg) and its second from
-// (dup, Wu). TMEM holds two tiles, so an epilogue runs beside the next tile's MMAs.
+// (dup, Wu); where its tiles fill no round of the SM pairs, or the last one badly, they
+// are cut along that sum, and a second kernel adds the pieces. TMEM holds two tiles, so an epilogue runs beside the next tile's MMAs.
 #include <algorithm>
 #include <type_traits>
 
@@ -47,24 +48,16 @@ constexpr int kSmem = 1024 + 2 * kStages * kOperand + kEpilogueWarps * kOutBoxes
                       2 * kMostSegs;
 static_assert(kSmem <= 227 * 1024 - 1024, "shared memory of a CTA");
 constexpr uint32_t kTmemCols = 512;
+constexpr int kSlotFloats = kTileM * kTileN;  // of a piece of a cut tile
 
-// The launch's tiles: 256 rows x `cols` columns of f (of d for dx), dealt round robin
-// to the pairs, column by column within groups of row tiles.
+// The launch's tiles: 256 rows x `cols` columns of f (of d for dx), dealt to the pairs
+// by `work`; its kt counts the stages of a tile, for dx those of both operand pairs.
 struct GluPlan {
-  int n_m, n_n;
-  int kt, kt2;  // stages of the first operand pair, and of both
-  int group;    // row tiles of a group
-  int cols;     // forward and again: 128, 96 or 64; dx: 256 or 128
-  int segs;     // segments to list, 0: tiles are of consecutive rows
+  WgradPlan work;
+  int half;  // dx: stages of the first operand pair
+  int cols;  // forward and again: 128, 96 or 64; dx: 256 or 128
+  int segs;  // segments to list, 0: tiles are of consecutive rows
 };
-
-__device__ __forceinline__ void place(const GluPlan& p, int n_m, int tile, int& m, int& n) {
-  const int per_group = p.group * p.n_n;
-  const int g = tile / per_group, r = tile - g * per_group;
-  const int rows = least(p.group, n_m - g * p.group);
-  n = r / rows;
-  m = g * p.group + (r - n * rows);
-}
 
 // Whether a segment holds a row that counts.
 __device__ __forceinline__ bool segment_lives(const uint8_t* mask, long long n, int seg) {
@@ -282,17 +275,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int live_segs =
       plan.segs > 0 ? list_segments(args.mask, args.n, plan.segs, list, scratch) : 0;
-  const int n_m = plan.segs > 0 ? (live_segs + kTileSegs - 1) / kTileSegs : plan.n_m;
-  const int tiles = n_m * plan.n_n;
+  WgradPlan wp = plan.work;
+  if (plan.segs > 0) {  // nothing is cut then
+    wp.n_m = (live_segs + kTileSegs - 1) / kTileSegs;
+    wp.whole = wp.n_m * wp.n_n;
+  }
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
   if constexpr (MODE == kDx)
     asm volatile("griddepcontrol.wait;" ::: "memory");  // dgate and dup are there
-  else if constexpr (MODE == kAgain)
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if constexpr (MODE != kFwd) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem_base = tmem_base_sh;
-  const int stages = MODE == kDx ? plan.kt2 : plan.kt;
+  WgradWork work;
+  WgradItem it;
   // Row of this CTA's row i of a row tile; args.n where there is none.
   auto row_of = [&](int tm, int i) -> long long {
     if (plan.segs == 0)
@@ -314,9 +310,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool two = MODE == kDx && plan.cols == kTileN;
       const uint32_t b_bytes =
           MODE == kDx ? (two ? kOperand : kBox) : static_cast<uint32_t>(plan.cols) * kBK * 2;
-      for (int tile = pair; ok && tile < tiles; tile += pairs) {
+      while (ok && work.next(wp, pair, pairs, it)) {
         int tm, tn;
-        place(plan, n_m, tile, tm, tn);
+        tile_place(wp, it.tile, tm, tn);
         int rows[kTileSegs / 2];  // where the tile's segments begin
 #pragma unroll
         for (int j = 0; j < kTileSegs / 2; ++j) rows[j] = static_cast<int>(row_of(tm, j * kSeg));
@@ -326,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n0 = tn * plan.cols + (MODE == kDx ? static_cast<int>(rank) *
                                                            (dx_cols(plan, args.d, tn) / 2)
                                                      : 0);
-        for (int k = 0; k < stages; ++k, ++n) {
+        for (int k = it.kb; k < it.ke; ++k, ++n) {
           const uint32_t s = n % kStages;
           if (!mbar_wait(&done_bar[s], ((n / kStages) & 1u) ^ 1u, abort_flag, &status_sh)) {
             ok = false;
@@ -337,8 +333,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx_cluster(lead, kOperand + b_bytes);
           uint8_t* a = ring + s * 2 * kOperand;
           uint8_t* b = a + kOperand;
-          const bool second = MODE == kDx && k >= plan.kt;
-          const int k0 = (second ? k - plan.kt : k) * kBK;
+          const bool second = MODE == kDx && k >= plan.half;
+          const int k0 = (second ? k - plan.half : k) * kBK;
           if (together) {
             tma_load_2d_pair_nohint(a, second ? &map_a1 : &map_a0, lead, k0, rows[0]);
           } else {
@@ -366,9 +362,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elect_one()) {
       uint32_t n = 0, t = 0;  // stages, tiles issued
       const uint32_t type_bits = args.fp16 ? (1u << 7) | (1u << 10) : 0u;
-      for (int tile = pair; ok && tile < tiles; tile += pairs, ++t) {
+      for (; ok && work.next(wp, pair, pairs, it); ++t) {
         int tm, tn;
-        place(plan, n_m, tile, tm, tn);
+        tile_place(wp, it.tile, tm, tn);
         const uint32_t idesc =
             idesc_bf16(kTileM, MODE == kDx ? dx_cols(plan, args.d, tn) : 2 * plan.cols, false,
                        MODE == kDx) &
@@ -379,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         const uint32_t dcol = tmem_base + buf * kTileN;
-        for (int k = 0; k < stages; ++k, ++n) {
+        for (int k = it.kb; k < it.ke; ++k, ++n) {
           const uint32_t s = n % kStages;
           if (!mbar_wait(&full_bar[s], (n / kStages) & 1u, abort_flag, &status_sh)) {
             ok = false;
@@ -392,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_mma_bf16_pair(dcol, sdesc_sw128(a + kk * 32, 16, 1024),
                              MODE == kDx ? sdesc_sw128(b + kk * 2048, kBox, 1024)
                                          : sdesc_sw128(b + kk * 32, 16, 1024),
-                             idesc, k == 0 && kk == 0 ? 0u : 1u);
+                             idesc, k == it.kb && kk == 0 ? 0u : 1u);
           tc_commit_pair_multicast(&done_bar[s], 0x3);
         }
         if (ok) tc_commit_pair_multicast(&tfull_bar[buf], 0x3);
@@ -436,12 +432,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tempty0 = mapa_shared(smem_u32(&tempty_bar[0]), 0);
     const uint32_t t0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
     uint32_t t = 0;
-    int tile = pair;
     OutBoxes out = {boxes + (warp - kFirstEpilogue) * kOutBoxes * kOutBox, 0u, lane};
     const int n = static_cast<int>(args.n);
-    for (; tile < tiles; tile += pairs, ++t) {
+    for (; work.next(wp, pair, pairs, it); ++t) {
       int tm, tn;
-      place(plan, n_m, tile, tm, tn);
+      tile_place(wp, it.tile, tm, tn);
       const long long row = row_of(tm, q * 32 + lane);
       const int r0 = static_cast<int>(row_of(tm, q * 32)),
                 r1 = static_cast<int>(row_of(tm, q * 32 + 16));
@@ -472,13 +467,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (MODE == kDx) {
           float v[32];
           tmem_ld32(acc + col, v);
-          uint32_t w[16];
+          if (it.slot >= 0) {  // a piece of a cut tile
+            float* p = args.partials + static_cast<long long>(it.slot) * kSlotFloats +
+                       (col / 4 * kTileM + static_cast<int>(rank) * 128 + q * 32 + lane) * 4;
 #pragma unroll
-          for (int j = 0; j < 16; ++j) w[j] = live ? pack16<T>(v[2 * j], v[2 * j + 1]) : 0u;
-          const uint32_t box = out.begin();
-          out.put16(box, 0, w);
-          out.put16(box, 1, w + 8);
-          out.end(&map_o0, at, r0, r1, n);
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<float4*>(p + j * kTileM * 4) =
+                  make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          } else {
+            uint32_t w[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) w[j] = live ? pack16<T>(v[2 * j], v[2 * j + 1]) : 0u;
+            const uint32_t box = out.begin();
+            out.put16(box, 0, w);
+            out.put16(box, 1, w + 8);
+            out.end(&map_o0, at, r0, r1, n);
+          }
         } else if constexpr (MODE == kAgain) {
           // Three boxes at once: dgate, dup and (should it be wanted) h.
           const int outs = args.h != nullptr ? 3 : 2;
@@ -571,9 +575,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // A tile is whole or NaN: so are this one and the rest after a wait that ran out.
     if (!ok) {
-      for (; tile < tiles; tile += pairs) {
+      do {
         int tm, tn;
-        place(plan, n_m, tile, tm, tn);
+        tile_place(wp, it.tile, tm, tn);
+        if (MODE == kDx && it.slot >= 0) {
+          float* p = args.partials + static_cast<long long>(it.slot) * kSlotFloats +
+                     (static_cast<int>(rank) * 128 + q * 32 + lane) * 4;
+#pragma unroll 1
+          for (int c4 = half * 32; c4 < half * 32 + 32; ++c4)
+            *reinterpret_cast<float4*>(p + c4 * kTileM * 4) = make_float4(kNaN, kNaN, kNaN, kNaN);
+          continue;
+        }
         const long long row = row_of(tm, q * 32 + lane);
         if (row >= args.n) continue;
         const uint32_t w = pack16<T>(kNaN, kNaN);
@@ -597,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             args.ck.ex[row * args.ck.lde + c / kCkptBlock] = kCkptBias;
           }
         }
-      }
+      } while (work.next(wp, pair, pairs, it));
     }
     if (lane == 0) bulk_wait_group<0>();
   }
@@ -612,12 +624,95 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc_pair(tmem_base, kTmemCols);
 }
 
+// dx of the cut tiles: the sum of each tile's pieces in their order. A CTA takes 16
+// columns and 256 / G rows of a tile; thread (row, g) adds the pieces g, g + G, ..., and
+// the G sums are then added in their order.
+template <typename T, int G>
+__global__ void __launch_bounds__(kTileM) glu_dx_join_kernel(const GluArgs args,
+                                                             const WgradPlan plan) {
+  constexpr int kRows = kTileM / G;
+  __shared__ float4 part[G > 1 ? G : 1][G > 1 ? 4 : 1][G > 1 ? kRows : 1];
+  const int t = static_cast<int>(blockIdx.x);
+  int tm, tn;
+  tile_place(plan, plan.whole + t, tm, tn);
+  const int r = static_cast<int>(threadIdx.x) % kRows, g = static_cast<int>(threadIdx.x) / kRows;
+  const int lrow = static_cast<int>(blockIdx.z) * kRows + r;
+  const long long row = static_cast<long long>(tm) * kTileM + lrow;
+  const int c0 = static_cast<int>(blockIdx.y) * 16;  // column of the tile
+  const int i0 = tn * kTileN + c0;
+  const bool valid = row < args.n && i0 < args.d;
+  const bool live = valid && (args.mask == nullptr || args.mask[row] != 0);
+  const int qa = first_piece(plan, t), qb = last_piece(plan, t);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces are there
+  float v[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) v[j] = 0.f;
+  if (live) {
+#pragma unroll 4
+    for (int q = qa + g; q <= qb; q += G) {
+      const float* p = args.partials +
+                       static_cast<long long>(piece_slot(plan, t, q)) * kSlotFloats +
+                       (c0 / 4 * kTileM + lrow) * 4;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float4 x = *reinterpret_cast<const float4*>(p + j * kTileM * 4);
+        v[4 * j] += x.x;
+        v[4 * j + 1] += x.y;
+        v[4 * j + 2] += x.z;
+        v[4 * j + 3] += x.w;
+      }
+    }
+  }
+  if constexpr (G > 1) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      part[g][j][r] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    __syncthreads();
+    if (g != 0) return;
+    for (int k = 1; k < G; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float4 x = part[k][j][r];
+        v[4 * j] += x.x;
+        v[4 * j + 1] += x.y;
+        v[4 * j + 2] += x.z;
+        v[4 * j + 3] += x.w;
+      }
+  }
+  if (!valid) return;
+  T* const out = static_cast<T*>(args.dx) + row * args.lddx + i0;
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    if (i0 + 8 * j < args.d)
+      st_global_v4(out + 8 * j, pack16<T>(v[8 * j], v[8 * j + 1]),
+                   pack16<T>(v[8 * j + 2], v[8 * j + 3]), pack16<T>(v[8 * j + 4], v[8 * j + 5]),
+                   pack16<T>(v[8 * j + 6], v[8 * j + 7]));
+}
+
+template <typename T>
+cudaError_t launch_dx_join(const GluArgs& args, const WgradPlan& plan, cudaStream_t st) {
+  const int pieces = (plan.kt + plan.per_pair - 1) / plan.per_pair + 1;  // of a tile, at most
+  const int groups = pieces > 4 ? 8 : 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(plan.cut, kTileN / 16, groups);
+  cfg.blockDim = dim3(kTileM);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  LaunchTimer timer("glu_dx_join_kernel", st);
+  return groups == 8 ? cudaLaunchKernelEx(&cfg, glu_dx_join_kernel<T, 8>, args, plan)
+                     : cudaLaunchKernelEx(&cfg, glu_dx_join_kernel<T, 1>, args, plan);
+}
+
 template <int MODE, typename T>
 cudaError_t launch(const CUtensorMap (&a)[4], const CUtensorMap (&b)[2],
                    const CUtensorMap (&o)[3], const GluArgs& args,
                    const GluPlan& plan, int sms, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * std::min(plan.n_m * plan.n_n, sms / 2));
+  cfg.gridDim = dim3(2 * launch_pairs(plan.work, std::min(sms / 2, kRefPairs)));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;
@@ -631,12 +726,17 @@ cudaError_t launch(const CUtensorMap (&a)[4], const CUtensorMap (&b)[2],
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = MODE == kDx ? 2 : 1;
-  LaunchTimer timer(MODE == kFwd     ? "glu_gemm_kernel<fwd>"
-                    : MODE == kAgain ? "glu_gemm_kernel<again>"
-                                     : "glu_gemm_kernel<dx>",
-                    st);
-  return cudaLaunchKernelEx(&cfg, glu_gemm_kernel<MODE, T>, a[0], a[1], a[2], a[3], b[0], b[1],
-                            o[0], o[1], o[2], args, plan);
+  cudaError_t e;
+  {
+    LaunchTimer timer(MODE == kFwd     ? "glu_gemm_kernel<fwd>"
+                      : MODE == kAgain ? "glu_gemm_kernel<again>"
+                                       : "glu_gemm_kernel<dx>",
+                      st);
+    e = cudaLaunchKernelEx(&cfg, glu_gemm_kernel<MODE, T>, a[0], a[1], a[2], a[3], b[0], b[1],
+                           o[0], o[1], o[2], args, plan);
+  }
+  if (MODE != kDx || e != cudaSuccess || plan.work.cut == 0) return e;
+  return launch_dx_join<T>(args, plan.work, st);
 }
 
 bool map16(CUtensorMap* map, const void* base, int cols, long long rows, long long ld,
@@ -667,16 +767,51 @@ int tile_columns(int n_m, int width, int most, int pairs) {
   return best;
 }
 
+// dx as a sum over the columns of dgate and of dup, dealt like that of a weight gradient
+// over its tokens. Pieces of different tiles share no operands while they run, and a stage
+// of them takes some 1.6 times as long, so tiles are cut only where that and the join (25
+// stages) still save 24 of them, which the host's part of the join costs. Uncut and cut, with the pass before it: 64 rows x 4096 x 14336 126
+// and 55 us, 512 rows 135 and 117, 3 x 48 x 12800 100 and 11; not cut by this rule: 5888
+// x 1536 x 8960 255 and 312, 2048 rows 121 and 120, 1024 x 2880 x 2880 41 and 43.
+WgradPlan dx_plan(long long n, int f, int d, int pairs) {
+  const long long stages = 2LL * ((f + kBK - 1) / kBK);
+  WgradPlan p = make_plan(stages * kTok, static_cast<int>(n), d, pairs);
+  if (p.cut > 0 && (8LL * p.per_pair + 5 * (25 + 24) > 5LL * p.kt ||
+                    // the workspace is sized for kRefPairs
+                    (pairs < kRefPairs && dx_plan(n, f, d, kRefPairs).cut == 0)))
+    p.cut = 0;
+  return p;
+}
+
 template <int MODE>
 cudaError_t launch_mode(const GluArgs& args, int sms, cudaStream_t st) {
   CUtensorMap a[4], b[2];
   GluPlan plan;
+  const int pairs = std::min(sms / 2, kRefPairs);
   const long long segs = (args.n + kSeg - 1) / kSeg;
   plan.segs = args.mask != nullptr && segs <= kMostSegs ? static_cast<int>(segs) : 0;
-  plan.n_m = static_cast<int>((args.n + kTileM - 1) / kTileM);
+  const int n_m = static_cast<int>((args.n + kTileM - 1) / kTileM);
   const int width = MODE == kDx ? args.d : args.f, depth = MODE == kDx ? args.f : args.d;
-  plan.cols = tile_columns(plan.n_m, width, MODE == kDx ? kTileN : 128, sms / 2);
-  plan.kt = (depth + kBK - 1) / kBK;
+  plan.half = (depth + kBK - 1) / kBK;
+  const int stages = MODE == kDx ? 2 * plan.half : plan.half;
+  plan.work = {};
+  if (MODE == kDx && args.partials != nullptr) {
+    // Tiles that fill no round, or the last one badly, are cut along their long sum.
+    // Segments are not listed then (masked rows are zeros already, and few).
+    plan.work = dx_plan(args.n, args.f, args.d, pairs);
+    if (plan.work.cut > 0 && plan.segs > 0 && plan.work.whole > 0) plan.work.cut = 0;
+  }
+  if (plan.work.cut > 0) {
+    plan.cols = kTileN;
+    plan.segs = 0;
+  } else {
+    plan.cols = tile_columns(n_m, width, MODE == kDx ? kTileN : 128, pairs);
+    plan.work = {};
+    plan.work.n_m = n_m;
+    plan.work.n_n = (width + plan.cols - 1) / plan.cols;
+    plan.work.kt = stages;
+    plan.work.whole = n_m * plan.work.n_n;
+  }
   // The first operand's rows by 128 and by segments; the weights' by columns of f.
   const void* first[2] = {MODE == kDx ? args.gate : args.x, MODE == kDx ? args.up : args.x};
   const long long ld[2] = {MODE == kDx ? args.ldg : args.ldx, MODE == kDx ? args.ldu : args.ldx};
@@ -709,9 +844,6 @@ cudaError_t launch_mode(const GluArgs& args, int sms, cudaStream_t st) {
                             kSeg, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_64B))
       return cudaErrorInvalidValue;
   }
-  plan.n_n = (width + plan.cols - 1) / plan.cols;
-  plan.kt2 = 2 * plan.kt;
-  plan.group = kGroupM;
   return args.fp16 ? launch<MODE, __half>(a, b, o, args, plan, sms, st)
                    : launch<MODE, __nv_bfloat16>(a, b, o, args, plan, sms, st);
 }
@@ -787,6 +919,11 @@ cudaError_t prepare_glu_gemm() {
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
+}
+
+size_t glu_dx_workspace(long long n, int f, int d) {
+  if (n == 0 || dx_plan(n, f, d, kRefPairs).cut == 0) return 0;
+  return 2 * kRefPairs * kSlotFloats * sizeof(float);
 }
 
 cudaError_t launch_glu_fwd(const GluArgs& a, int sms, cudaStream_t st) {

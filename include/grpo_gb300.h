@@ -503,7 +503,7 @@ int grpo_ckpt_wgrad(const void* dy, const void* ckpt, const float* add_or_null, 
  * [n_tokens] or NULL): a row with mask 0 has no influence, whatever it holds, and
  * its output rows are exact zeros. n_tokens = 0 is allowed. Calls are asynchronous
  * on `stream`, allocate nothing, can be captured in a graph, and give the same bits
- * each time. A wait on the device that runs out (about a second) leaves NaN in the
+ * each time (dx: with and without a workspace they may differ). A wait on the device that runs out (about a second) leaves NaN in the
  * tiles of the outputs that were still to be written.
  * ------------------------------------------------------------------------- */
 #define GRPO_ACT_SILU 0      /* g / (1 + e^-g)                                     */
@@ -540,7 +540,8 @@ int grpo_glu_fwd(const void* x, const void* w_gate, const void* w_up, const uint
 int grpo_glu_bwd(const void* dh, const void* x_or_null, const void* w_gate, const void* w_up,
                  const void* gate_or_null, const void* up_or_null, const uint8_t* mask_or_null,
                  void* dgate, void* dup, void* dx_or_null, void* h_or_null,
-                 const grpo_glu_desc* desc, void* stream);
+                 const grpo_glu_desc* desc, void* workspace_or_null, size_t workspace_bytes,
+                 void* stream);
 
 /* The weight gradients, fp32 [inner][hidden], packed, starting on 16 bytes:
  *   dw_gate = add_gate + dgate^T x,  dw_up = add_up + dup^T x

@@ -46,8 +46,9 @@ def _fwd(clp, desc, **kw):
 def _bwd(clp, desc, **kw):
     a = Buf().a
     p = dict(dh=a, x=a, wg=a, wu=a, gate=None, up=None, mask=None, dgate=a, dup=a, dx=a, h=None)
+    ws, size = kw.pop("ws", None), kw.pop("size", 0)
     p.update(kw)
-    return clp.lib.grpo_glu_bwd(*p.values(), _ref(desc), None)
+    return clp.lib.grpo_glu_bwd(*p.values(), _ref(desc), ws, size, None)
 
 
 def _wgrad(clp, desc, ws=1 << 30, **kw):
@@ -91,6 +92,9 @@ def test_glu_calls_refuse_bad_pointers(clp):
     assert _bwd(clp, d, gate=a) == -1
     assert _bwd(clp, d, dx=a + 2) == -2
     assert _bwd(clp, d, h=a + 2) == -2
+    assert _bwd(clp, d, ws=a + 16, size=1 << 30) == -2
+    long = _desc(clp, f=4096)  # one tile of 128 stages: cut
+    assert _bwd(clp, long, ws=a, size=256) == -4
     for name in ("dgate", "dup", "x", "dwg", "dwu"):
         assert _wgrad(clp, d, **{name: None}) == -1
         assert _wgrad(clp, d, **{name: a + 4}) == -2
@@ -105,6 +109,11 @@ def test_glu_workspace(clp):
     assert lib.grpo_glu_wgrad_workspace_size(4, 24, 16, None) == -1
     assert lib.grpo_glu_wgrad_workspace_size(-1, 24, 16, ctypes.byref(out)) == -1
     assert lib.grpo_glu_wgrad_workspace_size(4, 20, 16, ctypes.byref(out)) == -3
+    assert lib.grpo_glu_bwd_workspace_size(4, 24, 16, None) == -1
+    assert lib.grpo_glu_bwd_workspace_size(4, 24, -8, ctypes.byref(out)) == -1
+    assert clp.grpo_glu_bwd_workspace_size(4, 24, 16) == 0
+    assert clp.grpo_glu_bwd_workspace_size(0, 4096, 16) == 0
+    assert clp.grpo_glu_bwd_workspace_size(4, 4096, 16) == 152 * 65536 * 4
     assert clp.grpo_glu_wgrad_workspace_size(4, 24, 16) == 256
     # Long sums over few tiles are cut into pieces: two tiles a pair at most.
     assert clp.grpo_glu_wgrad_workspace_size(1 << 20, 256, 256) == 256 + 152 * 65536 * 4
@@ -146,6 +155,8 @@ def test_python_glu_refuses(clp):
         clp.grpo_glu_bwd(dh, x, w, w, gate=dh)
     with pytest.raises(ValueError, match="w_gate"):
         clp.grpo_glu_bwd(dh, x, _t(16, 16), w)
+    with pytest.raises(ValueError, match="workspace"):
+        clp.grpo_glu_bwd(dh, x, w, w, workspace=torch.empty(8, device="meta"))
     with pytest.raises(ValueError, match="dup: expected shape"):
         clp.grpo_glu_bwd(dh, x, w, w, dup=x)
     with pytest.raises(ValueError, match="x: expected shape"):

@@ -533,3 +533,55 @@ def test_segments_apart_in_the_last_tile(clp, n):
             for p, q in zip(a, b):
                 if p is not None:
                     assert torch.equal(p[keep], q[keep]) and not p[~keep].any()
+
+
+# Rows, hidden, inner: one tile in 50 pieces; a tile to a few pairs each; whole rounds
+# and a cut one (80 tiles on 76 pairs); columns and rows that end inside tiles.
+CUT = [(3, 48, 12800), (64, 2048, 4096), (35, 496, 6976), (600, 776, 4096), (2500, 2048, 4096),
+       (300, 264, 4096)]
+
+
+@pytest.mark.parametrize("n,d,f", CUT)
+@pytest.mark.parametrize("t", [BF, HF])
+def test_dx_in_pieces(clp, n, d, f, t):
+    g = _gen(n)
+    (wg, wu), dh = _weights(g, f, d, t), _randn(g, n, f, t=t, scale=0.1)
+    gate, up = _randn(g, n, f, t=t), _randn(g, n, f, t=t)
+    need = clp.grpo_glu_bwd_workspace_size(n, f, d)
+    assert need > 0
+    ws = torch.full((need // 4,), float("nan"), device=DEV)
+    none = torch.empty(0, device=DEV)
+    m = _mask("blocks", n, g)
+    m[0] = 1
+    off = m == 0
+    big = torch.cat([wg.double(), wu.double()])
+    for mask in (None, m):
+        if mask is not None:
+            dh[off] = float("nan")
+        kw = dict(gate=gate, up=up, mask=mask)
+        r = clp.grpo_glu_bwd(dh, None, wg, wu, workspace=ws, **kw)
+        both = torch.cat([r.dgate.double(), r.dup.double()], 1)
+        want, err = both @ big, _sum_error(both, big.t())
+        _check(r.dx, want, err, t)
+        _check(clp.grpo_glu_bwd(dh, None, wg, wu, workspace=none, **kw).dx, want, err, t)
+        again = clp.grpo_glu_bwd(dh, None, wg, wu, **kw)
+        assert torch.equal(again.dx, r.dx)
+        if mask is not None:
+            assert not r.dx[off].any()
+    dx, wide = _wide(t, n, d, g)
+    assert torch.equal(clp.grpo_glu_bwd(dh, None, wg, wu, gate=gate, up=up, mask=m, dx=dx).dx, r.dx)
+    wide[1:-1, 8:-16] = 7.0
+    assert (wide == 7.0).all()
+
+
+def test_a_lost_copy_of_dx_in_pieces(clp):
+    g = _gen(21)
+    n, d, f = 64, 512, 8192
+    (wg, wu), dh = _weights(g, f, d, BF), _randn(g, n, f)
+    gate, up = _randn(g, n, f), _randn(g, n, f)
+    want = clp.grpo_glu_bwd(dh, None, wg, wu, gate=gate, up=up).dx
+    clp.grpo_selftest_lose_copy(3)
+    got = clp.grpo_glu_bwd(dh, None, wg, wu, gate=gate, up=up).dx
+    fine = ~torch.isnan(got)
+    assert not fine.all() and torch.equal(got[fine], want[fine])
+    assert torch.equal(clp.grpo_glu_bwd(dh, None, wg, wu, gate=gate, up=up).dx, want)
