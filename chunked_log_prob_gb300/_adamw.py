@@ -152,10 +152,10 @@ def grpo_grad_norm(grads: Sequence[torch.Tensor | None], *, max_norm=None, out=N
 
 
 def _per_tensor(value, n, name):
-    """A number for all tensors, or one for each."""
+    """A number for all tensors, or one for each, as an array."""
     if isinstance(value, (int, float)):
-        return [float(value)] * n
-    value = [float(v) for v in value]
+        return np.full(n, value, np.float32)
+    value = np.array([float(v) for v in value], np.float32)
     if len(value) != n:
         raise ValueError(f"{name}: expected {n} numbers, got {len(value)}")
     return value
