@@ -503,8 +503,9 @@ int grpo_ckpt_wgrad(const void* dy, const void* ckpt, const float* add_or_null, 
  * [n_tokens] or NULL): a row with mask 0 has no influence, whatever it holds, and
  * its output rows are exact zeros. n_tokens = 0 is allowed. Calls are asynchronous
  * on `stream`, allocate nothing, can be captured in a graph, and give the same bits
- * each time (dx: with and without a workspace they may differ). A wait on the device that runs out (about a second) leaves NaN in the
- * tiles of the outputs that were still to be written.
+ * each time (dx: with and without a workspace they may differ). A wait on the device
+ * that runs out (about a second) leaves NaN in the tiles of the outputs that were still
+ * to be written.
  * ------------------------------------------------------------------------- */
 #define GRPO_ACT_SILU 0      /* g / (1 + e^-g)                                     */
 #define GRPO_ACT_GELU 1      /* g Phi(g)                                           */

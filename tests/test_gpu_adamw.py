@@ -422,3 +422,31 @@ def test_on_another_stream(clp):
             two.step([gr], scale=clp.grpo_grad_norm([gr], max_norm=1.0).scale)
     torch.cuda.synchronize()
     assert torch.equal(p, q)
+
+
+def test_places_beyond_32_bits(clp):
+    # One tensor of 2^32 + 1000 bf16 values, its moments in 8 bits: the last 1300 values,
+    # on both sides of the border, as the formulas have them there.
+    n, k = (1 << 32) + 1000, 1300
+    first = n - k
+    first -= first % 128  # whole blocks
+    p = torch.zeros(n, dtype=BF, device=DEV)
+    gr = torch.zeros(n, dtype=BF, device=DEV)
+    g = _gen(12)
+    p[first:] = torch.randn(n - first, generator=g).to(DEV, BF)
+    gr[first:] = (0.1 * torch.randn(n - first, generator=g)).to(DEV, BF)
+    opt = clp.AdamW([p], lr=LR, weight_decay=0.0, state_bits=8, seed=9)
+    before = f64(p[first:])
+    opt.step([gr], scale=clp.grpo_grad_norm([gr]).scale)
+    (p1, m1, v1), _ = _fp32_step(before, f64(gr[first:]), 0 * before, 0 * before, 1, 0.0)
+    um, uv, up = o.random_bits(np.arange(first, n), 9, 1)
+    s = opt.states[0]
+    _check_8(s.m[first:], s.m_scale[first // 128:], m1, 1, um, 1e-6)
+    _check_8(s.v[first:], s.v_scale[first // 128:], np.sqrt(v1), 2, uv, 1e-6)
+    step = 2.0 ** (np.floor(np.log2(np.abs(p1))) - 7)
+    low = np.floor(np.abs(p1) / step) * step
+    part = (np.abs(p1) - low) / step
+    want = np.sign(p1) * np.where(part + up / 65536 >= 1, low + step, low)
+    clear = (np.abs(part + up / 65536 - 1) > 1e-3) & (part > 1e-3) & (part < 1 - 1e-3)
+    assert (f64(p[first:]) == want)[clear].all() and clear.mean() > 0.9
+    assert not p[:first].any() and not s.m.view(torch.uint8)[:first:4099].any()

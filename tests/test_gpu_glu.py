@@ -585,3 +585,22 @@ def test_a_lost_copy_of_dx_in_pieces(clp):
     fine = ~torch.isnan(got)
     assert not fine.all() and torch.equal(got[fine], want[fine])
     assert torch.equal(clp.grpo_glu_bwd(dh, None, wg, wu, gate=gate, up=up).dx, want)
+
+
+def test_offsets_beyond_32_bits(clp):
+    # 2.3e9 values of h: the last rows are what they are on their own.
+    g = _gen(30)
+    n, d, f = 140_000, 64, 16384
+    x, (wg, wu) = _randn(g, n, d), _weights(g, f, d, BF)
+    last = slice(n - 200, n)
+    r = clp.grpo_glu_fwd(x, wg, wu)
+    want = clp.grpo_glu_fwd(x[last], wg, wu)
+    assert torch.equal(r.h[last], want.h)
+    dg = r.h  # any gradient will do, in place
+    b = clp.grpo_glu_bwd(dg, x, wg, wu, dgate=dg, workspace=torch.empty(0, device=DEV))
+    wb = clp.grpo_glu_bwd(want.h, x[last], wg, wu, workspace=torch.empty(0, device=DEV))
+    for p, q in zip(b[:3], wb[:3]):
+        assert torch.equal(p[last], q)
+    k = clp.grpo_glu_bwd(b.dup, None, wg, wu, gate=b.dgate, up=b.dup, dgate=b.dgate, want_dx=False)
+    kw = clp.grpo_glu_bwd(wb.dup, None, wg, wu, gate=wb.dgate, up=wb.dup, want_dx=False)
+    assert torch.equal(k.dgate[last], kw.dgate) and torch.equal(k.dup[last], kw.dup)
