@@ -505,7 +505,7 @@ int grpo_ckpt_wgrad(const void* dy, const void* ckpt, const float* add_or_null, 
  * on `stream`, allocate nothing, can be captured in a graph, and give the same bits
  * each time (dx: with and without a workspace they may differ). A wait on the device
  * that runs out (about a second) leaves NaN in the tiles of the outputs that were still
- * to be written.
+ * to be written. Calls that may overlap on the GPU need workspaces of their own.
  * ------------------------------------------------------------------------- */
 #define GRPO_ACT_SILU 0      /* g / (1 + e^-g)                                     */
 #define GRPO_ACT_GELU 1      /* g Phi(g)                                           */

@@ -316,7 +316,10 @@ def test_infinities_and_nan_stay_where_they_are(clp, n):
     want = clp.grpo_glu_fwd(x, wg, wu)
     back = clp.grpo_glu_bwd(dh, x, wg, wu)
     x[1, 3], dh[0, 5] = float("inf"), float("nan")
-    got = clp.grpo_glu_fwd(x, wg, wu)
+    got = clp.grpo_glu_fwd(x, wg, wu, want_ckpt=True)
+    c = clp.grpo_ckpt_pack(got.h)
+    assert torch.equal(got.ckpt.q.view(torch.uint8), c.q.view(torch.uint8))
+    assert torch.equal(got.ckpt.exponents, c.exponents)
     keep = torch.arange(n, device=DEV) != 1
     assert torch.equal(got.h[keep], want.h[keep]) and not torch.isfinite(got.h[1]).all()
     gb = clp.grpo_glu_bwd(dh, x, wg, wu)
@@ -380,6 +383,20 @@ def test_captured_and_replayed_beside_other_calls(clp, n):
         torch.cuda.current_stream().wait_stream(side)
         for p, q in zip(out, want):
             assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("t", [BF, HF])
+def test_checkpoints_of_any_size_of_value(clp, t):
+    # Blocks from the type's least to its largest numbers, and beyond it.
+    g = _gen(31)
+    n, d, f = 300, 64, 320
+    x, (wg, wu) = _randn(g, n, d, t=t), _weights(g, f, d, t)
+    span = torch.linspace(-24, 16 if t is HF else 60, n, device=DEV)
+    x = (x.double() * (2.0 ** span.double())[:, None]).to(t)
+    r = clp.grpo_glu_fwd(x, wg, wu, act="relu", want_ckpt=True)
+    c = clp.grpo_ckpt_pack(r.h)
+    assert torch.equal(r.ckpt.q.view(torch.uint8), c.q.view(torch.uint8))
+    assert torch.equal(r.ckpt.exponents, c.exponents)
 
 
 def test_two_host_threads(clp):
