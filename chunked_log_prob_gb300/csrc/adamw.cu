@@ -14,6 +14,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "launch.h"
 #include "norm.h"
@@ -24,13 +25,16 @@ namespace {
 
 constexpr int kThreads = 256;  // of the norm's kernels
 constexpr int kWarps = kThreads / 32;
-// Of the step's, and the most values that a CTA takes. 2^28 values with moments in 8
-// bits, which the instructions bound: 751 us with CTAs of 256 threads, 676 with 128, 673
-// with 64 (bf16 parameters; fp32 791, 735 and 687), as each gives its place up sooner.
-// In 32 bits, which memory bounds: 1023, 1017 and 997 us with 16384, 8192 and 4096
-// values.
+// Of the step's, its CTAs of an SM (which set its registers), and the most values that
+// one takes. With moments in 8 bits the instructions bound it, and short CTAs give their
+// places up sooner: 2^28 values in 720 us with CTAs of 256 threads, 676 with 128, 673 with
+// 64 (bf16 parameters, before the roundings were made exact; fp32 791, 735 and 687); exact,
+// 14 of them an SM 739 and 718, 16 738 and 786, 12 745 and 736. In 32 bits, which memory
+// bounds: 1023, 1017 and 997 us with 16384, 8192 and 4096 values.
 template <int BITS>
 constexpr int kStepThreads = BITS == 8 ? 64 : 256;
+template <int BITS>
+constexpr int kStepCtas = BITS == 8 ? 14 : 4;
 template <int BITS>
 constexpr int kStepChunk = BITS == 8 ? 16384 : 4096;
 constexpr int kGroup = 256;  // values of a warp's step
@@ -259,17 +263,47 @@ __device__ __noinline__ float block_top_finite(float y0, float y1, float y2, flo
   return a;
 }
 
+// A chunk of a tensor: its values' parts, how many they are, and the place of the first.
+template <int BITS, typename P, typename G>
+struct Chunk {
+  using M = std::conditional_t<BITS == 8, uint8_t, float>;
+  P* param;
+  const G* grad;
+  M* m;
+  M* v;
+  float* m_scale;
+  float* v_scale;
+  void* copy;  // 2 bytes a value
+  int count;
+  uint32_t place;  // its low 32 bits
+  uint32_t high;   // the others, of the first value
+  int ctype;
+
+  __device__ __forceinline__ Chunk(const AdamwEntry& e, long long begin, int chunk)
+      : param(static_cast<P*>(e.param) + begin),
+        grad(static_cast<const G*>(e.grad) + begin),
+        m(static_cast<M*>(e.m) + begin),
+        v(static_cast<M*>(e.v) + begin),
+        m_scale(BITS == 8 ? e.m_scale + begin / kBlock : nullptr),
+        v_scale(BITS == 8 ? e.v_scale + begin / kBlock : nullptr),
+        copy(e.copy == nullptr ? nullptr : static_cast<uint16_t*>(e.copy) + begin),
+        count(static_cast<int>(min(static_cast<long long>(chunk), e.numel - begin))),
+        place(static_cast<uint32_t>(e.place + begin)),
+        high(static_cast<uint32_t>(static_cast<uint64_t>(e.place + begin) >> 32)),
+        ctype(e.ctype) {}
+};
+
 // A lane's 8 values: consecutive from `first` on (VEC, all there), or every 16th of
-// their block, as far as the tensor goes.
+// their block, as far as the chunk goes.
 template <int BITS, typename P, typename G, bool VEC>
-__device__ __forceinline__ void step8(const AdamwEntry& e, const StepOf& s, long long first,
+__device__ __forceinline__ void step8(const Chunk<BITS, P, G>& e, const StepOf& s, int first,
                                       int lane) {
   constexpr int kEvery = VEC ? 1 : 16;
   float p[8], g[8], m[8], v[8];
   bool have[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) have[j] = VEC || first + j * kEvery < e.numel;
-  const uint64_t block = static_cast<uint64_t>(first) / kBlock;  // BITS 8: this lane's
+  for (int j = 0; j < 8; ++j) have[j] = VEC || first + j * kEvery < e.count;
+  const int block = first / kBlock;  // BITS 8: this lane's
   float ms = 0.f, vs = 0.f;
   if (BITS == 8 && have[0]) {
     ms = e.m_scale[block];
@@ -282,8 +316,8 @@ __device__ __forceinline__ void step8(const AdamwEntry& e, const StepOf& s, long
       load8<float>(e.m, first, m);
       load8<float>(e.v, first, v);
     } else {
-      const uint2 mq = __ldcs(reinterpret_cast<const uint2*>(static_cast<uint8_t*>(e.m) + first));
-      const uint2 vq = __ldcs(reinterpret_cast<const uint2*>(static_cast<uint8_t*>(e.v) + first));
+      const uint2 mq = __ldcs(reinterpret_cast<const uint2*>(e.m + first));
+      const uint2 vq = __ldcs(reinterpret_cast<const uint2*>(e.v + first));
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 a = unpack_e4m3x2((j < 2 ? mq.x : mq.y) >> (16 * (j & 1)));
@@ -297,17 +331,17 @@ __device__ __forceinline__ void step8(const AdamwEntry& e, const StepOf& s, long
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const long long i = first + j * kEvery;
+      const int i = first + j * kEvery;
       p[j] = g[j] = m[j] = v[j] = 0.f;
       if (have[j]) {
-        p[j] = load1<P>(e.param, i);
-        g[j] = load1<G>(e.grad, i);
+        p[j] = to_f32(e.param[i]);
+        g[j] = to_f32(e.grad[i]);
         if constexpr (BITS == 32) {
-          m[j] = static_cast<const float*>(e.m)[i];
-          v[j] = static_cast<const float*>(e.v)[i];
+          m[j] = e.m[i];
+          v[j] = e.v[i];
         } else {
-          m[j] = unpack_e4m3x2(static_cast<const uint8_t*>(e.m)[i]).x;
-          v[j] = unpack_e4m3x2(static_cast<const uint8_t*>(e.v)[i]).x;
+          m[j] = unpack_e4m3x2(e.m[i]).x;
+          v[j] = unpack_e4m3x2(e.v[i]).x;
         }
       }
     }
@@ -379,8 +413,8 @@ __device__ __forceinline__ void step8(const AdamwEntry& e, const StepOf& s, long
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (have[j]) {
-        static_cast<float*>(e.m)[first + j * kEvery] = m[j];
-        static_cast<float*>(e.v)[first + j * kEvery] = v[j];
+        e.m[first + j * kEvery] = m[j];
+        e.v[first + j * kEvery] = v[j];
       }
   }
   uint32_t x[8];
@@ -388,15 +422,15 @@ __device__ __forceinline__ void step8(const AdamwEntry& e, const StepOf& s, long
   Keys keys = s.keys;
   if constexpr (kRandom) {
     // A lane's values lie in one block, which no multiple of 2^32 parts.
-    const uint64_t place = static_cast<uint64_t>(e.place + first);
-    if (!s.near) keys = keys_at(s.keys, static_cast<uint32_t>(place >> 32));
+    const uint32_t place = e.place + static_cast<uint32_t>(first);
+    if (!s.near) keys = keys_at(s.keys, e.high + (place < e.place ? 1u : 0u));
     // Consecutive places, from a multiple of 8 on, differ below what the first fold
     // moves.
-    const uint32_t head = static_cast<uint32_t>(place) ^ keys.k0;
+    const uint32_t head = place ^ keys.k0;
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       x[j] = VEC ? bits_after(keys, (head ^ (head >> 16)) ^ j)
-                 : bits_at(keys, static_cast<uint32_t>(place) + j * kEvery);
+                 : bits_at(keys, place + j * kEvery);
   }
   if constexpr (BITS == 8) {
     float mt = block_top(m), vt = block_top(root);
@@ -421,19 +455,19 @@ __device__ __forceinline__ void step8(const AdamwEntry& e, const StepOf& s, long
       lose(root, vq);
     }
     if constexpr (VEC) {
-      __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(e.m) + first), mq);
-      __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(e.v) + first), vq);
+      __stcs(reinterpret_cast<uint2*>(e.m + first), mq);
+      __stcs(reinterpret_cast<uint2*>(e.v + first), vq);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (have[j]) {
-          static_cast<uint8_t*>(e.m)[first + j * kEvery] =
+          e.m[first + j * kEvery] =
               static_cast<uint8_t>((j < 4 ? mq.x : mq.y) >> (8 * (j & 3)));
-          static_cast<uint8_t*>(e.v)[first + j * kEvery] =
+          e.v[first + j * kEvery] =
               static_cast<uint8_t>((j < 4 ? vq.x : vq.y) >> (8 * (j & 3)));
         }
     }
-    if ((lane & 14) == 0 && static_cast<long long>(block) * kBlock < e.numel)
+    if ((lane & 14) == 0 && block * kBlock < e.count)
       ((lane & 1) == 0 ? e.m_scale : e.v_scale)[block] = top * (1.f / kTop);
   }
   if constexpr (sizeof(P) == 2) {
@@ -460,7 +494,7 @@ __device__ __forceinline__ void step8(const AdamwEntry& e, const StepOf& s, long
       w.y = __byte_perm(__float_as_uint(p[2]), __float_as_uint(p[3]), 0x7632);
       w.z = __byte_perm(__float_as_uint(p[4]), __float_as_uint(p[5]), 0x7632);
       w.w = __byte_perm(__float_as_uint(p[6]), __float_as_uint(p[7]), 0x7632);
-      __stcs(reinterpret_cast<uint4*>(static_cast<P*>(e.param) + first), w);
+      __stcs(reinterpret_cast<uint4*>(e.param + first), w);
     } else {
       store8<P>(e.param, first, p);
     }
@@ -474,8 +508,8 @@ __device__ __forceinline__ void step8(const AdamwEntry& e, const StepOf& s, long
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       if (!have[j]) continue;
-      const long long i = first + j * kEvery;
-      static_cast<P*>(e.param)[i] = static_cast<P>(p[j]);
+      const int i = first + j * kEvery;
+      e.param[i] = static_cast<P>(p[j]);
       if (e.copy != nullptr) {
         if (e.ctype == GRPO_DTYPE_BF16)
           static_cast<__nv_bfloat16*>(e.copy)[i] = __float2bfloat16_rn(p[j]);
@@ -494,16 +528,16 @@ template <int BITS, typename P, typename G>
 __device__ __forceinline__ void step_chunk(const AdamwEntry& e, const StepOf& s, long long begin,
                                            int chunk) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long end = min(begin + chunk, e.numel);
   constexpr int kState = BITS == 8 ? 8 : 16;
+  constexpr int kStep = kStepThreads<BITS> / 32 * kGroup;
   const bool vec = on(e.param, 16) && on(e.grad, 16) && on(e.m, kState) && on(e.v, kState) &&
                    on(e.copy, 16);
-  constexpr int kStep = kStepThreads<BITS> / 32 * kGroup;
-  for (long long at = begin + warp * kGroup; at < end; at += kStep) {
-    if (vec && at + kGroup <= e.numel)
-      step8<BITS, P, G, true>(e, s, at + lane * 8, lane);
+  const Chunk<BITS, P, G> c(e, begin, chunk);
+  for (int at = warp * kGroup; at < c.count; at += kStep) {
+    if (vec && at + kGroup <= c.count)
+      step8<BITS, P, G, true>(c, s, at + lane * 8, lane);
     else
-      step8<BITS, P, G, false>(e, s, at + (lane >> 4) * kBlock + (lane & 15), lane);
+      step8<BITS, P, G, false>(c, s, at + (lane >> 4) * kBlock + (lane & 15), lane);
   }
 }
 
@@ -533,7 +567,7 @@ __device__ __forceinline__ int find_entry(const E* e, int count, int c) {
 }
 
 template <int N, int BITS>
-__global__ void __launch_bounds__(kStepThreads<BITS>, 1024 / kStepThreads<BITS>)
+__global__ void __launch_bounds__(kStepThreads<BITS>, kStepCtas<BITS>)
     adamw_kernel(const __grid_constant__ AdamwTable<N> table, const AdamwArgs args) {
   const float scale = args.scale != nullptr ? *args.scale : 1.f;
   if (!(fabsf(scale) <= FLT_MAX)) return;  // the step is skipped
