@@ -10,6 +10,12 @@
 
 namespace grpo {
 
+// Row tiles that the block's GEMMs walk together. 16384 x 4096 x 14336, forward / backward
+// again / weight gradients (us, under the power cap, two boxes): 4 2348 / 4829 / 2377, 8
+// 2231 / 4667 / 2335, 16 2174 / 4636 / 2325; 16 2118 / 4513 / 2270, 20 2110 / 4579 / 2346,
+// 32 2227 / 4751 / 2424.
+constexpr int kGluGroup = 16;
+
 // One call's tensors, [n][d] and [n][f] with row strides in elements; the weights
 // are [f][d]. Which of them a launch reads and writes depends on it.
 struct GluArgs {

@@ -813,6 +813,7 @@ cudaError_t launch_mode(const GluArgs& args, int sms, cudaStream_t st) {
     plan.work.kt = stages;
     plan.work.whole = n_m * plan.work.n_n;
   }
+  plan.work.group = kGluGroup;
   // The first operand's rows by 128 and by segments; the weights' by columns of f.
   const void* first[2] = {MODE == kDx ? args.gate : args.x, MODE == kDx ? args.up : args.x};
   const long long ld[2] = {MODE == kDx ? args.ldg : args.ldx, MODE == kDx ? args.ldu : args.ldx};

@@ -455,7 +455,8 @@ cudaError_t launch_glu_wgrad(const GluWgradArgs& a, int sms, cudaStream_t st) {
                             CU_TENSOR_MAP_DATA_TYPE_FLOAT32, CU_TENSOR_MAP_SWIZZLE_64B))
       return cudaErrorInvalidValue;
   }
-  const WgradPlan plan = make_plan(a.n, 2 * half_tiles(a.f) * kTileM, a.d, pairs);
+  WgradPlan plan = make_plan(a.n, 2 * half_tiles(a.f) * kTileM, a.d, pairs);
+  plan.group = kGluGroup;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * launch_pairs(plan, pairs));
   cfg.blockDim = dim3(kThreads);

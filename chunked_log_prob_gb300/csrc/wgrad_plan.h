@@ -16,7 +16,7 @@ namespace grpo {
 constexpr int kTileM = 256;    // outputs of a pair's tile, 128 per CTA
 constexpr int kTileN = 256;    // inputs of a pair's tile
 constexpr int kTok = 64;       // tokens of a stage
-constexpr int kGroupM = 8;     // tiles are walked 8 row tiles at a time
+constexpr int kGroupM = 8;     // tiles are walked 8 row tiles at a time, where not said otherwise
 constexpr int kRefPairs = 76;  // GB300's SM pairs
 
 GRPO_HD int least(int a, int b) { return a < b ? a : b; }
@@ -30,6 +30,7 @@ struct WgradPlan {
   int whole;     // tiles dealt whole
   int cut;       // tiles dealt in pieces
   int per_pair;  // stages of a pair's part of them
+  int group = kGroupM;  // row tiles that are walked together
 };
 
 struct WgradItem {
@@ -76,14 +77,14 @@ GRPO_HD int piece_slot(const WgradPlan& p, int t, int q) {
   return 2 * q + (q * p.per_pair < t * p.kt ? 1 : 0);
 }
 
-// Row and column of a tile: column by column within kGroupM row tiles, so that
+// Row and column of a tile: column by column within `group` row tiles, so that
 // the tiles of a round share both operands in L2.
 GRPO_HD void tile_place(const WgradPlan& p, int tile, int& m, int& n) {
-  const int per_group = kGroupM * p.n_n;
+  const int per_group = p.group * p.n_n;
   const int g = tile / per_group, r = tile - g * per_group;
-  const int rows = least(kGroupM, p.n_m - g * kGroupM);
+  const int rows = least(p.group, p.n_m - g * p.group);
   n = r / rows;
-  m = g * kGroupM + (r - n * rows);
+  m = g * p.group + (r - n * rows);
 }
 
 // Inputs of a tile: 256, or 128 where no more are left.
