@@ -169,6 +169,12 @@ def _device_scalar(t, name, dtype, device):
     return t.data_ptr()
 
 
+def _cuda_device(t):
+    if t.device.type != "cuda":
+        raise ValueError(f"expected tensors on a CUDA device, got {t.device}")
+    return t.device
+
+
 class AdamW:
     """AdamW over many tensors, one launch per 256 of them.
 
@@ -184,7 +190,7 @@ class AdamW:
     steps that are captured in a graph: the program adds 1 to it before each.
 
     Parameters, moments and copies are written in place on the current stream, which
-    autograd does not see. To go on later, keep ``states``, ``steps_done``, ``seed`` and
+    autograd does not see; the ``.data`` of each may be exchanged between steps. To go on later, keep ``states``, ``steps_done``, ``seed`` and
     the parameters, and make an AdamW of them.
     """
 
@@ -195,9 +201,7 @@ class AdamW:
         n = len(self.params)
         if n == 0:
             raise ValueError("params: none given")
-        self.device = self.params[0].device
-        if self.device.type != "cuda":
-            raise ValueError(f"expected tensors on a CUDA device, got {self.device}")
+        self.device = _cuda_device(self.params[0])
         self.betas = (float(betas[0]), float(betas[1]))
         if not all(0.0 <= b < 1.0 for b in self.betas):
             raise ValueError(f"betas: expected numbers in [0, 1), got {betas!r}")
@@ -233,8 +237,19 @@ class AdamW:
         for (a, size, i), (b, _, j) in zip(spans, spans[1:]):
             if a + size > b:
                 raise ValueError(f"params[{i}] and params[{j}] overlap")
-        self._at = list(map(_data_ptr, self.params))
         self._shapes = list(map(_shape, self.params))
+        # All that the step writes, as the table has it.
+        written = [self.params, *zip(*self.states), self.copies]
+        self._held = [t for part in written for t in part if t is not None]
+        self._at = list(map(_data_ptr, self._held))
+        self._rounded = [c for c in self.copies if c is not None]
+        self._types = list(map(_dtype, self._rounded))
+
+    def _moved(self):
+        """Whether a tensor's storage was exchanged (`.data`) since it was described. At one
+        address may be copies of either type."""
+        return (list(map(_data_ptr, self._held)) != self._at
+                or list(map(_dtype, self._rounded)) != self._types)
 
     def _grad(self, i, g):
         """Checks one gradient; its address (0: none)."""
@@ -293,7 +308,7 @@ class AdamW:
             raise ValueError(f"grads: expected {len(params)} of them, got {len(grads)}")
         if lr is not None:
             self.lr = _per_tensor(lr, len(params), "lr")
-        if list(map(_data_ptr, params)) != self._at:  # a parameter's storage was exchanged
+        if self._moved():
             self._describe()
         view = self._view
         view["lr"], view["weight_decay"] = self.lr, self.weight_decay

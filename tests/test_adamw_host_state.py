@@ -1,0 +1,83 @@
+"""What an AdamW step hands to the library, on host tensors with the call recorded: the
+addresses that it reads and writes through are those of the tensors as they are now."""
+
+import pytest
+import torch
+
+import __graft_entry__
+
+BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
+E4M3 = torch.float8_e4m3fn
+
+
+@pytest.fixture
+def adamw(monkeypatch):
+    """(AdamW on host tensors, the list of recorded steps' tables)."""
+    __graft_entry__.build()
+    import chunked_log_prob_gb300._adamw as m
+
+    steps = []
+
+    def record(device, fn, table, count, params):
+        assert fn is m.lib.grpo_adamw_step and device.type == "cpu"
+        steps.append([{name: getattr(e, name) for name, _ in e._fields_} for e in table])
+        return 0
+
+    monkeypatch.setattr(m, "call_on", record)
+    monkeypatch.setattr(m, "_cuda_device", lambda t: t.device)
+    return m.AdamW, steps
+
+
+def _made(adamw, bits=8, ct=BF, n=3):
+    params = [torch.randn(130 + i, 4) for i in range(n)]
+    copies = [p.to(ct) if i != 1 else None for i, p in enumerate(params)]
+    opt = adamw(params, lr=1e-3, state_bits=bits, copies=copies)
+    return opt, params, copies, [torch.zeros_like(p) for p in params]
+
+
+def _as_described(opt, entry, i):
+    s, c = opt.states[i], opt.copies[i]
+    assert entry["param"] == opt.params[i].data_ptr()
+    assert entry["numel"] == opt.params[i].numel()
+    assert entry["m"] == s.m.data_ptr() and entry["v"] == s.v.data_ptr()
+    if s.m_scale is not None:
+        assert entry["m_scale"] == s.m_scale.data_ptr()
+        assert entry["v_scale"] == s.v_scale.data_ptr()
+    assert entry["copy"] == (None if c is None else c.data_ptr())
+    if c is not None:
+        assert entry["copy_dtype"] == {BF: 0, HF: 1}[c.dtype]
+
+
+@pytest.mark.parametrize("bits,part", [(32, "m"), (32, "v"), (8, "m"), (8, "v"), (8, "m_scale"),
+                                       (8, "v_scale"), (8, "param"), (32, "copy")])
+def test_exchanged_storage_is_followed(adamw, bits, part):
+    opt, params, copies, grads = _made(adamw[0], bits)
+    opt.step(grads)
+    kept = []  # so that no new storage lies where an old one did
+    for i in (0, 2):
+        t = {"param": params[i], "copy": copies[i]}.get(part)
+        t = getattr(opt.states[i], part) if t is None else t
+        kept.append(t.data)
+        t.data = t.data.clone()
+    opt.step(grads)
+    for i in range(3):
+        _as_described(opt, adamw[1][-1][i], i)
+    opt.step(grads)
+    assert adamw[1][-1] == adamw[1][-2] and opt.steps_done == 3
+
+
+def test_a_copy_of_another_type_in_the_same_place(adamw):
+    opt, _, copies, grads = _made(adamw[0])
+    opt.step(grads)
+    copies[2].data = copies[2].data.view(HF)
+    opt.step(grads)
+    _as_described(opt, adamw[1][-1][2], 2)
+
+
+def test_a_copy_of_no_type_that_is_taken(adamw):
+    opt, _, copies, grads = _made(adamw[0])
+    opt.step(grads)
+    copies[0].data = copies[0].data.double()
+    with pytest.raises(TypeError, match=r"copies\[0\]"):
+        opt.step(grads)
+    assert len(adamw[1]) == 1
