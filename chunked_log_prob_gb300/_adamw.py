@@ -23,7 +23,7 @@ _GRAD = np.dtype(GrpoGrad)
 _byref = ctypes.byref
 _data_ptr, _numel = torch.Tensor.data_ptr, torch.Tensor.numel
 _packed, _device_index = torch.Tensor.is_contiguous, torch.Tensor.get_device
-_dtype, _shape = attrgetter("dtype"), attrgetter("shape")
+_dtype, _shape, _nbytes = attrgetter("dtype"), attrgetter("shape"), attrgetter("nbytes")
 
 
 class GradNorm(NamedTuple):
@@ -242,13 +242,15 @@ class AdamW:
         written = [self.params, *zip(*self.states), self.copies]
         self._held = [t for part in written for t in part if t is not None]
         self._at = list(map(_data_ptr, self._held))
+        self._sizes = list(map(_nbytes, self._held))
         self._rounded = [c for c in self.copies if c is not None]
         self._types = list(map(_dtype, self._rounded))
 
     def _moved(self):
-        """Whether a tensor's storage was exchanged (`.data`) since it was described. At one
-        address may be copies of either type."""
-        return (list(map(_data_ptr, self._held)) != self._at
+        """Whether a tensor's storage was exchanged (`.data`), or fewer values of it taken,
+        since it was described. At one address and of one size may be copies of either type."""
+        held = self._held
+        return (list(map(_data_ptr, held)) != self._at or list(map(_nbytes, held)) != self._sizes
                 or list(map(_dtype, self._rounded)) != self._types)
 
     def _grad(self, i, g):

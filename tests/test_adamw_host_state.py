@@ -74,6 +74,29 @@ def test_a_copy_of_another_type_in_the_same_place(adamw):
     _as_described(opt, adamw[1][-1][2], 2)
 
 
+def test_fewer_values_in_the_same_place_are_refused(adamw):
+    opt, params, copies, grads = _made(adamw[0], 32)
+    opt.step(grads)
+    # A gradient of the shape that the parameter had.
+    keep, params[1].data = params[1].data, params[1].data[:7]
+    for _ in range(2):  # and again: what was refused is not taken for described
+        with pytest.raises(ValueError, match=r"states m\[1\]"):
+            opt.step(grads)
+    params[1].data = keep
+    opt.step(grads)
+    m = opt.states[0].m
+    keep, m.data = m.data, m.data[:100]
+    with pytest.raises(ValueError, match=r"states m\[0\]"):
+        opt.step(grads)
+    m.data = keep
+    keep, copies[0].data = copies[0].data, copies[0].data[:1]
+    with pytest.raises(ValueError, match=r"copies\[0\]"):
+        opt.step(grads)
+    copies[0].data = keep
+    opt.step(grads)
+    assert opt.steps_done == 3 and len(adamw[1]) == 3
+
+
 def test_a_copy_of_no_type_that_is_taken(adamw):
     opt, _, copies, grads = _made(adamw[0])
     opt.step(grads)
