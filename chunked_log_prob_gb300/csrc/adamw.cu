@@ -231,7 +231,7 @@ __device__ __forceinline__ void store8(void* p, long long i, const float (&v)[8]
 
 // What a chunk's threads share.
 struct StepOf {
-  float scale, shrink, rate, beta1, beta2, rest1, rest2, fix2, eps;
+  float scale, fade, rate, beta1, beta2, rest1, rest2, fix2, eps;
   Keys keys;  // of the chunk's places where they are all `near` one another, or the step's
   bool near;
 };
@@ -352,7 +352,7 @@ __device__ __forceinline__ void step8(const Chunk<BITS, P, G>& e, const StepOf& 
                 beta2 = pair(s.beta2, s.beta2), rest1 = pair(s.rest1, s.rest1),
                 rest2 = pair(s.rest2, s.rest2), fix2 = pair(s.fix2, s.fix2),
                 eps = pair(s.eps, s.eps), rate = pair(-s.rate, -s.rate),
-                shrink = pair(s.shrink, s.shrink), ms2 = pair(ms, ms), vs2 = pair(vs, vs);
+                fade = pair(-s.fade, -s.fade), ms2 = pair(ms, ms), vs2 = pair(vs, vs);
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
       f32x2 m2 = pair(m[j], m[j + 1]), v2 = pair(v[j], v[j + 1]);
@@ -396,14 +396,28 @@ __device__ __forceinline__ void step8(const Chunk<BITS, P, G>& e, const StepOf& 
 #pragma unroll
       for (int j = 0; j < 8; ++j) root[j] = __fsqrt_rn(v[j]);
     }
-#pragma unroll
-    for (int j = 0; j < 8; j += 2) {
+    auto step_of = [&](int j) {  // of values j and j + 1
       float d0, d1;
       split(fma2(pair(root[j], root[j + 1]), fix2, eps), d0, d1);
       // d is 0 or normal: a root of at least 2^-75, or eps
-      const f32x2 step =
-          mul2(mul2(rate, pair(m[j], m[j + 1])), pair(quick_inverse(d0), quick_inverse(d1)));
-      split(fma2(pair(p[j], p[j + 1]), shrink, step), p[j], p[j + 1]);
+      return mul2(mul2(rate, pair(m[j], m[j + 1])), pair(quick_inverse(d0), quick_inverse(d1)));
+    };
+    // Decay and step are added up before the parameter takes them: 1 - lr decay as an
+    // fp32 would round the decay itself to a multiple of 2^-24, each step the same way.
+    if (lane_top(p) <= FLT_MAX) {
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        const f32x2 q = pair(p[j], p[j + 1]);
+        split(add2(q, fma2(fade, q, step_of(j))), p[j], p[j + 1]);
+      }
+    } else {  // an infinity has no decay: it stays
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        float d0, d1;
+        split(step_of(j), d0, d1);
+        p[j] += fabsf(p[j]) <= FLT_MAX ? fmaf(-s.fade, p[j], d0) : d0;
+        p[j + 1] += fabsf(p[j + 1]) <= FLT_MAX ? fmaf(-s.fade, p[j + 1], d1) : d1;
+      }
     }
   }
   if constexpr (BITS == 32 && VEC) {
@@ -586,7 +600,7 @@ __global__ void __launch_bounds__(kStepThreads<BITS>, kStepCtas<BITS>)
   }
   const float lr = e.lr * (args.lr_factor != nullptr ? *args.lr_factor : 1.f);
   s.scale = scale;
-  s.shrink = 1.f - lr * e.decay;
+  s.fade = lr * e.decay;
   s.rate = lr * fix1;
   s.beta1 = args.beta1;
   s.beta2 = args.beta2;

@@ -54,3 +54,93 @@ def test_copies_and_moments_that_were_moved_away_and_back(clp, bits):
         assert torch.equal(a, b)
     for k in kept:
         assert (k.view(torch.uint8) == 0xEE).all()
+
+
+# lr decay = 1.5 2^-24, which 1 - lr decay as an fp32 takes for 2^-24 or 2^-23.
+FADE_LR, FADE = 1e-5, 1.5e5 * 2.0 ** -24
+
+
+def _faded(p0):
+    """The values after a step without gradients, in fp64."""
+    return p0 * (1 - float(np.float32(FADE_LR)) * float(np.float32(FADE)))
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_a_small_decay_is_the_one_that_was_asked(clp, bits):
+    # p in [1, 2) is faded by 0.75 to 1.5 of its spacing; with no step beside it, the sum
+    # is rounded once: half a spacing, 2^-24. lr decay itself is off by 2^-24 of itself,
+    # and its product with p: 4 2^-24 of 3 2^-24.
+    n = 100_000
+    p = 1 + torch.rand(n, generator=torch.Generator().manual_seed(3))
+    p0 = f64(p)
+    p = p.to(DEV)
+    opt = clp.AdamW([p], lr=FADE_LR, weight_decay=FADE, state_bits=bits)
+    opt.step([torch.zeros(n, device=DEV)])
+    assert (np.abs(f64(p) - _faded(p0)) <= 2.0 ** -24 * (1 + 12 * 2.0 ** -24)).all()
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_a_small_decay_beside_a_step(clp, bits):
+    # Steps of every size below lr: the sums' roundings are even over a spacing, so their
+    # mean over n values is 2^-23 / sqrt(12 n) at one sigma; six of them are 6e-10. The
+    # step's own error, 16 2^-24 of at most 4e-5 and of either sign, is far below. The decay
+    # taken for 2^-24 or 2^-23 would move the mean by 4e-8.
+    n = 1 << 17
+    g = torch.Generator().manual_seed(5)
+    p = (1 + torch.rand(n, generator=g)).to(DEV)
+    m, v = torch.randn(n, generator=g), 0.1 + torch.rand(n, generator=g)
+    gr = torch.randn(n, generator=g)
+    if bits == 8:
+        state = clp.alloc_adam_state(p, 8)
+        state.m.copy_((100 * m).to(state.m.dtype))
+        state.v.copy_((100 * v).to(state.v.dtype))
+        for z in (state.m_scale, state.v_scale):
+            z.fill_(0.01)
+    else:
+        state = clp.AdamState(m.to(DEV), v.to(DEV))
+    p0, m0, v0 = f64(p), *map(f64, state.moments())
+    opt = clp.AdamW([p], lr=FADE_LR, weight_decay=FADE, states=[state], steps_done=4)
+    opt.step([gr.to(DEV)])
+    want, _, _ = o.adamw(p0, f64(gr), m0, v0, 5, float(np.float32(FADE_LR)),
+                         decay=float(np.float32(FADE)))
+    off = f64(p) - want
+    assert np.abs(off).max() <= 2.0 ** -24 + 16 * 2.0 ** -24 * 4e-4
+    assert abs(off.mean()) <= 6e-10
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_a_small_decay_of_bf16_parameters(clp, bits):
+    # 127 values in (1, 2), each of which has one nearest fp32 for its faded value (none
+    # is within 2^-20 of a spacing of the middle between two, 12 2^-24 would do); of that
+    # the 16 random bits make a bf16.
+    n = 1 << 24
+    p = (1 + torch.rand(n, generator=torch.Generator().manual_seed(7))).clamp(1.01, 1.99).to(BF)
+    want = _faded(f64(p))
+    p = p.to(DEV)
+    opt = clp.AdamW([p], lr=FADE_LR, weight_decay=FADE, state_bits=bits, seed=21)
+    opt.step([torch.zeros(n, dtype=BF, device=DEV)])
+    part = want * 2.0 ** 23 % 1.0
+    assert want.min() > 1 and (np.abs(part - 0.5) > 2.0 ** -20).all()
+    _, _, u = o.random_bits(np.arange(n), 21, 1)
+    raised = want.astype(np.float32).view(np.uint32) + u.astype(np.uint32)
+    want = (raised & np.uint32(0xFFFF0000)).view(np.float32)
+    assert (p.float().cpu().numpy() == want).all()
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("t", [F32, BF])
+def test_infinite_parameters_stay_and_their_neighbours_step(clp, bits, t):
+    g = torch.Generator().manual_seed(9)
+    p = torch.randn(1000, generator=g).to(DEV, t)
+    gr = torch.randn(1000, generator=g).to(DEV)
+    q = p.clone()
+    at = torch.tensor([3, 8, 700], device=DEV)
+    bad = torch.tensor([float("inf"), float("-inf"), float("nan")], dtype=t, device=DEV)
+    q[at] = bad
+    for x in (p, q):
+        opt = clp.AdamW([x], lr=1e-3, state_bits=bits, weight_decay=0.1, seed=2)
+        for _ in range(2):
+            opt.step([gr])
+    assert torch.equal(q[at][:2], bad[:2]) and torch.isnan(q[700])
+    p[at] = q[at] = 0
+    assert torch.equal(p, q)
