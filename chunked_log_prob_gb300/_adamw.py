@@ -98,7 +98,8 @@ def _quick(view, field, grads, device):
     (A set of adapters has hundreds, at a few us each one by one.)"""
     try:
         types = list(map(_dtype, grads))
-        codes = _DTYPES[types[0]] if len(set(types)) == 1 else [_DTYPES[t] for t in types]
+        same = types.count(types[0]) == len(types)
+        codes = _DTYPES[types[0]] if same else [_DTYPES[t] for t in types]
         if set(map(_device_index, grads)) != {device.index} or not all(map(_packed, grads)):
             return None
         data = list(map(_data_ptr, grads))
@@ -190,7 +191,8 @@ class AdamW:
     steps that are captured in a graph: the program adds 1 to it before each.
 
     Parameters, moments and copies are written in place on the current stream, which
-    autograd does not see; the ``.data`` of each may be exchanged between steps. To go on later, keep ``states``, ``steps_done``, ``seed`` and
+    autograd does not see. The ``.data`` of each may be exchanged between steps, for values
+    of the same shape and type. To go on later, keep ``states``, ``steps_done``, ``seed`` and
     the parameters, and make an AdamW of them.
     """
 
@@ -242,15 +244,17 @@ class AdamW:
         written = [self.params, *zip(*self.states), self.copies]
         self._held = [t for part in written for t in part if t is not None]
         self._at = list(map(_data_ptr, self._held))
-        self._sizes = list(map(_nbytes, self._held))
         self._rounded = [c for c in self.copies if c is not None]
         self._types = list(map(_dtype, self._rounded))
+        self._model = [*self.params, *self._rounded]
+        self._sizes = list(map(_nbytes, self._model))
 
     def _moved(self):
         """Whether a tensor's storage was exchanged (`.data`), or fewer values of it taken,
-        since it was described. At one address and of one size may be copies of either type."""
-        held = self._held
-        return (list(map(_data_ptr, held)) != self._at or list(map(_nbytes, held)) != self._sizes
+        since it was described. At one address and of one size may be copies of either type;
+        of the moments, which are the optimizer's, the address is enough."""
+        return (list(map(_data_ptr, self._held)) != self._at
+                or list(map(_nbytes, self._model)) != self._sizes
                 or list(map(_dtype, self._rounded)) != self._types)
 
     def _grad(self, i, g):

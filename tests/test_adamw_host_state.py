@@ -84,11 +84,6 @@ def test_fewer_values_in_the_same_place_are_refused(adamw):
             opt.step(grads)
     params[1].data = keep
     opt.step(grads)
-    m = opt.states[0].m
-    keep, m.data = m.data, m.data[:100]
-    with pytest.raises(ValueError, match=r"states m\[0\]"):
-        opt.step(grads)
-    m.data = keep
     keep, copies[0].data = copies[0].data, copies[0].data[:1]
     with pytest.raises(ValueError, match=r"copies\[0\]"):
         opt.step(grads)
