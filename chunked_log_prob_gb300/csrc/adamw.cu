@@ -656,9 +656,12 @@ __device__ __forceinline__ double cta_sum(double v) {
 // A sum of fp32 values in two parts, two such sums side by side: what the sum's
 // rounding leaves is found exactly and kept (the sum of two floating-point numbers and
 // its error: Knuth), so that the norm is right to fp32's last bit however many there are;
-// fp64 for every value would take three times as long as reading it.
+// fp64 for every value would take three times as long as reading it. Its range is that of
+// values up to 2^50 (2^25 of their squares are below 2^126) beside one of 2^-50 at least
+// (the others' squares may be subnormal, off by 2^-149 each); the rest is summed in fp64.
 struct Squares {
   f32x2 sum = 0ull, rest = 0ull;
+  double far = 0.0;
 
   __device__ __forceinline__ void add(f32x2 q) {
     const f32x2 minus = pair(-1.f, -1.f);
@@ -675,12 +678,41 @@ struct Squares {
     add(q);
     if (!EXACT) rest = add2(rest, fma2(v, v, mul2(q, pair(-1.f, -1.f))));
   }
+  // A thread's eight values at a time, N of them: whether they are in range.
+  template <int N>
+  static __device__ __forceinline__ bool in_range(const float (&v)[N][8]) {
+    float top = 0.f;
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) top = max_abs_nan(top, v[k][j], v[k][j + 1]);
+    return (top >= 0x1p-50f && top <= 0x1p50f) || top == 0.f;
+  }
+  template <bool EXACT, int N>
+  __device__ __forceinline__ void take(const float (&v)[N][8]) {
+    if (in_range(v)) {
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) square<EXACT>(v[k][j], v[k][j + 1]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float x = v[k][j], q = __fmul_rn(x, x);
+          // beyond fp32: infinity, or NaN
+          far += q <= FLT_MAX ? static_cast<double>(x) * static_cast<double>(x)
+                              : static_cast<double>(q);
+        }
+    }
+  }
   __device__ __forceinline__ double total() const {
     float a, b, c, d;
     split(sum, a, b);
     split(rest, c, d);
     return (static_cast<double>(a) + static_cast<double>(c)) +
-           (static_cast<double>(b) + static_cast<double>(d));
+           (static_cast<double>(b) + static_cast<double>(d)) + far;
   }
 };
 
@@ -696,21 +728,17 @@ __device__ __forceinline__ void squares(const void* p, long long begin, long lon
       float v[4][8];
 #pragma unroll
       for (int k = 0; k < 4; ++k) load8<T>(p, at + k * kStep + threadIdx.x * 8, v[k]);
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) s.square<kExact>(v[k][j], v[k][j + 1]);
+      s.take<kExact>(v);
     }
   }
   for (; at < end; at += 8 * kThreads) {
-    float v[8];
+    float v[1][8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const long long i = at + k * kThreads + threadIdx.x;
-      v[k] = i < end ? load1<T>(p, i) : 0.f;
+      v[0][k] = i < end ? load1<T>(p, i) : 0.f;
     }
-#pragma unroll
-    for (int k = 0; k < 8; k += 2) s.square<kExact>(v[k], v[k + 1]);
+    s.take<kExact>(v);
   }
 }
 

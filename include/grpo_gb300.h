@@ -575,10 +575,10 @@ typedef struct grpo_grad {
 
 /* norm = sqrt(sum over all tensors of g^2), scale = min(1, max_norm / (norm + 1e-6))
  * (max_norm <= 0: 1). out: fp32 [2] on the device, norm and scale; where the norm is
- * not finite the scale is NaN. Squares are fp32 (a gradient beyond 1.8e19 counts as not
- * finite, one below 1e-23 as 0), what their sums round off is kept, so both results
- * are right to the last bit or so; the order is fixed by the sizes. Tensors are packed
- * and start on an element; NULL ones add nothing. grads: on the host, read during the
+ * not finite the scale is NaN. What the squares and their sums round off is kept, so the
+ * norm is the formula's to fp32's last bit, whatever the gradients' size; one beyond
+ * 1.8e19, whose square no fp32 holds, counts as not finite. The order is fixed by the
+ * sizes. Tensors are packed and start on an element; NULL ones add nothing. grads: on the host, read during the
  * call. */
 int grpo_grad_norm_workspace_size(int32_t count, size_t* bytes);
 int grpo_grad_norm(const grpo_grad* grads, int32_t count, double max_norm, float* out,

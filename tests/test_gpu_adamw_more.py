@@ -144,3 +144,58 @@ def test_infinite_parameters_stay_and_their_neighbours_step(clp, bits, t):
     assert torch.equal(q[at][:2], bad[:2]) and torch.isnan(q[700])
     p[at] = q[at] = 0
     assert torch.equal(p, q)
+
+
+def _norm64(grads):
+    return torch.stack([x.double().square().sum() for x in grads]).sum().sqrt().item()
+
+
+# A rounding to fp32, 2^-24, and a last bit more for what is before it: the parts that the
+# sums leave (2^-24 of them is lost of each of some 2^9 squares a thread) and fp64 sums.
+LAST_BIT = 1.01 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("t", [F32, BF, HF])
+@pytest.mark.parametrize("kind", ["even", "random"])
+def test_the_norm_of_long_tensors_to_the_last_bit(clp, t, kind):
+    # Several chunks of 16384 values for each of the 1216 CTAs: 512 squares a thread, whose
+    # plain fp32 sums of values of one size would be off by some 2^-24 each time.
+    n = 8 * 1216 * 16384 + 12345
+    x = torch.full((n,), 0.37, device=DEV, dtype=t)
+    if kind == "random":
+        x.mul_(torch.rand(n, generator=torch.Generator(DEV).manual_seed(1), device=DEV))
+    want = _norm64([x])
+    got = clp.grpo_grad_norm([x]).norm.item()
+    assert abs(got - want) <= LAST_BIT * want
+
+
+@pytest.mark.parametrize("t", [F32, BF])
+@pytest.mark.parametrize("size", [1e-44, 1e-38, 1e-30, 1e-24, 1e-22, 1e-19, 1e-16, 1e-15, 1e-14,
+                                  1e14, 2e15, 1e18, 1.7e19])
+def test_the_norm_of_very_small_and_very_large_gradients(clp, t, size):
+    g = torch.Generator(DEV).manual_seed(2)
+    for n in (1, 1001, 16384, 400_003):
+        x = (size * (0.5 + 0.5 * torch.rand(n, generator=g, device=DEV, dtype=torch.float64))).to(t)
+        y = torch.randn(n, generator=g, device=DEV).to(t)  # beside usual ones
+        for grads in ([x], [x, y], [torch.cat([x, y])], [torch.stack([x, y], 1).reshape(-1)]):
+            want = _norm64(grads)
+            got = clp.grpo_grad_norm(grads).norm.item()
+            if want < 2.0 ** -126:  # subnormals are 2^-149 apart
+                assert abs(got - want) <= 1.01 * 2.0 ** -150
+            else:
+                assert abs(got - want) <= LAST_BIT * want
+            r = clp.grpo_grad_norm(grads, max_norm=0.1)
+            assert abs(r.scale.item() - min(1.0, 0.1 / (want + 1e-6))) <= LAST_BIT * r.scale.item()
+
+
+def test_the_norm_of_zeros_and_of_what_is_not_finite(clp):
+    for t in (F32, BF, HF):
+        x = torch.zeros(100_000, device=DEV, dtype=t)
+        assert clp.grpo_grad_norm([x]).norm.item() == 0.0
+        for bad, is_nan in ((float("inf"), False), (float("-inf"), False), (float("nan"), True)):
+            for at in (0, 99_999):
+                x.fill_(0.25)
+                x[at] = bad
+                r = clp.grpo_grad_norm([x], max_norm=1.0)
+                assert torch.isnan(r.norm) if is_nan else r.norm.item() == float("inf")
+                assert torch.isnan(r.scale)
