@@ -42,6 +42,8 @@ static_assert(kSmem <= 227 * 1024 - 1024, "shared memory of a CTA");
 static_assert(kBoxesOfTile == 2 * kBoxes, "each box is loaded twice a tile");
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSlotFloats = kTileM * kTileN;
+// Self-test: from here on `lost` counts boxes to add of the first CTA's first tile.
+constexpr uint32_t kLostBox = 1u << 29;
 
 // Row tiles of one weight: the first half of the plan's are the gate's.
 __host__ __device__ __forceinline__ int half_tiles(int f) { return (f + kTileM - 1) / kTileM; }
@@ -208,6 +210,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Of the current tile: boxes of `add` asked for, and waited for. Each tile has all
     // of its boxes loaded, so a box's first load of a tile ends phase 0, its second 1.
     int asked = 0, had = 0;
+    const uint32_t lost_box =
+        args.lost != kNoneLost && args.lost >= kLostBox && blockIdx.x == 0 && wid == 0
+            ? args.lost - kLostBox
+            : kNoneLost;
     while (ok && work.next(plan, pair, pairs, it)) {
       int tm, tn;
       tile_place(plan, it.tile, tm, tn);
@@ -218,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = it.slot < 0 && row0 < args.f && col0 < args.d;
       const bool adds = whole && (side.up ? args.add_up : args.add_gate) != nullptr;
       auto ask = [&](int b) {
-        if (lane == 0) {
+        if (lane == 0 && (static_cast<uint32_t>(b) != lost_box || it.tile != 0)) {
           uint64_t* bar = &add_bar[wid][b % kBoxes];
           mbar_arrive_expect_tx(bar, kBoxBytes);
           tma_load_2d(box0 + (b % kBoxes) * kBoxBytes, map_add, bar, col0 + 16 * b, row0);
@@ -315,8 +321,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Copies in flight land before the CTA exits.
     if (!ok && lane == 0)
       for (; had < asked; ++had) drain(&add_bar[wid][had % kBoxes], had / kBoxes);
-    // A tile, or a piece of one, is whole or NaN: so are this one and the rest.
+    // A tile, or a piece of one, is whole or NaN: so are this one and the rest. Boxes of
+    // this one that are on their way out land first.
     if (!ok) {
+      if (lane == 0) bulk_wait_group<0>();
+      __syncwarp();
       do {
         int tm, tn;
         tile_place(plan, it.tile, tm, tn);

@@ -639,7 +639,9 @@ int grpo_adamw_step(const grpo_adamw_tensor* tensors, int32_t count,
  * its CTA has to do after it (where two CTAs share a row: the first of them), or its
  * next grpo_ckpt_wgrad or grpo_glu_wgrad does not copy the 64-token stage `index`,
  * its next grpo_glu_fwd or grpo_glu_bwd (the first of its products) the 64-column
- * stage (counted over the stages of the first CTA's tiles), to that CTA. The wait for
+ * stage (counted over the stages of the first CTA's tiles), to that CTA; from 2^29 on
+ * grpo_glu_wgrad leaves out box index - 2^29 (0 to 7, of 16 columns) of what the first
+ * CTA's first rows add to its first tile. The wait for
  * it runs out after about a second, the kernel gives up the work that depends on it
  * (NaN in its place), lets the copies in flight land and returns; the context stays
  * usable. A forward pass of up to 8 rows waits for nothing. -1: nothing is left out. */
