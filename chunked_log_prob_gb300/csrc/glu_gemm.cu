@@ -12,7 +12,13 @@
 // elementwise pass, x is read once and the fp32 projections are never written. dx
 // is one sum over 2 f columns, its first half from (dgate, Wg) and its second from
 // (dup, Wu); where its tiles fill no round of the SM pairs, or the last one badly, they
-// are cut along that sum, and a second kernel adds the pieces. TMEM holds two tiles, so an epilogue runs beside the next tile's MMAs.
+// are cut along that sum, and a second kernel adds the pieces. TMEM holds two tiles, so an
+// epilogue runs beside the next tile's MMAs.
+//
+// The tensor core's fp32 sums cut off instead of rounding: a unit of 2^-23 of the sum so
+// far, at most, every 16 products, which bends a long sum towards zero (2^20 products of
+// one sign: 7e-3). A sum of more than kSumStages is therefore made of sums of that many
+// stages, added with rounding by the epilogue warps.
 #include <algorithm>
 #include <type_traits>
 
@@ -49,6 +55,11 @@ constexpr int kSmem = 1024 + 2 * kStages * kOperand + kEpilogueWarps * kOutBoxes
 static_assert(kSmem <= 227 * 1024 - 1024, "shared memory of a CTA");
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSlotFloats = kTileM * kTileN;  // of a piece of a cut tile
+// Stages of one sum in TMEM: 32768 products of bf16, 2048 of fp16, whose sums are 2.4e-4
+// and 1.5e-5 off at most: an eighth and a sixteenth of the least half step of the type's
+// numbers, 2^-9 and 2^-12.
+template <typename T>
+constexpr int kSumStages = std::is_same_v<T, __half> ? 32 : 512;
 
 // The launch's tiles: 256 rows x `cols` columns of f (of d for dx), dealt to the pairs
 // by `work`; its kt counts the stages of a tile, for dx those of both operand pairs.
@@ -179,6 +190,18 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float (&v)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+      "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+      "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
 // A checkpoint block that one thread holds: 32 values as stored.
 template <typename T>
 __device__ __forceinline__ void ckpt_store32(const uint32_t (&w)[16], uint8_t* q, uint8_t* ex,
@@ -220,7 +243,8 @@ __device__ __forceinline__ int dx_cols(const GluPlan& p, int d, int tn) {
   return p.cols == kTileN ? tile_cols(d, tn) : p.cols;
 }
 
-template <int MODE, typename T>
+// LONG: tiles of more than kSumStages stages.
+template <int MODE, typename T, bool LONG>
 __global__ void __launch_bounds__(kThreads, 1)
     glu_gemm_kernel(const __grid_constant__ CUtensorMap map_a0,
                     const __grid_constant__ CUtensorMap map_a1,
@@ -287,6 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");  // dgate and dup are there
   if constexpr (MODE != kFwd) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem_base = tmem_base_sh;
+  constexpr int kSum = kSumStages<T>;
   WgradWork work;
   WgradItem it;
   // Row of this CTA's row i of a row tile; args.n where there is none.
@@ -360,38 +385,42 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1 && rank == 0) {
     // -------------------------------------------------------- MMA issuer --
     if (elect_one()) {
-      uint32_t n = 0, t = 0;  // stages, tiles issued
+      uint32_t n = 0, t = 0;  // stages, sums issued
       const uint32_t type_bits = args.fp16 ? (1u << 7) | (1u << 10) : 0u;
-      for (; ok && work.next(wp, pair, pairs, it); ++t) {
+      while (ok && work.next(wp, pair, pairs, it)) {
         int tm, tn;
         tile_place(wp, it.tile, tm, tn);
         const uint32_t idesc =
             idesc_bf16(kTileM, MODE == kDx ? dx_cols(plan, args.d, tn) : 2 * plan.cols, false,
                        MODE == kDx) &
             ~type_bits;
-        const uint32_t buf = t & 1u;
-        if (!mbar_wait(&tempty_bar[buf], ((t >> 1) & 1u) ^ 1u, abort_flag, &status_sh)) {
-          ok = false;
-          break;
-        }
-        const uint32_t dcol = tmem_base + buf * kTileN;
-        for (int k = it.kb; k < it.ke; ++k, ++n) {
-          const uint32_t s = n % kStages;
-          if (!mbar_wait(&full_bar[s], (n / kStages) & 1u, abort_flag, &status_sh)) {
+        for (int k0 = it.kb; ok && k0 < it.ke; ++t) {
+          const int k1 = LONG ? least(k0 + kSum, it.ke) : it.ke;
+          const uint32_t buf = t & 1u;
+          if (!mbar_wait(&tempty_bar[buf], ((t >> 1) & 1u) ^ 1u, abort_flag, &status_sh)) {
             ok = false;
             break;
           }
-          tc_fence_after();
-          const uint32_t a = smem_u32(ring + s * 2 * kOperand), b = a + kOperand;
+          const uint32_t dcol = tmem_base + buf * kTileN;
+          for (int k = k0; k < k1; ++k, ++n) {
+            const uint32_t s = n % kStages;
+            if (!mbar_wait(&full_bar[s], (n / kStages) & 1u, abort_flag, &status_sh)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t a = smem_u32(ring + s * 2 * kOperand), b = a + kOperand;
 #pragma unroll
-          for (int kk = 0; kk < kBK / 16; ++kk)
-            tc_mma_bf16_pair(dcol, sdesc_sw128(a + kk * 32, 16, 1024),
-                             MODE == kDx ? sdesc_sw128(b + kk * 2048, kBox, 1024)
-                                         : sdesc_sw128(b + kk * 32, 16, 1024),
-                             idesc, k == it.kb && kk == 0 ? 0u : 1u);
-          tc_commit_pair_multicast(&done_bar[s], 0x3);
+            for (int kk = 0; kk < kBK / 16; ++kk)
+              tc_mma_bf16_pair(dcol, sdesc_sw128(a + kk * 32, 16, 1024),
+                               MODE == kDx ? sdesc_sw128(b + kk * 2048, kBox, 1024)
+                                           : sdesc_sw128(b + kk * 32, 16, 1024),
+                               idesc, k == k0 && kk == 0 ? 0u : 1u);
+            tc_commit_pair_multicast(&done_bar[s], 0x3);
+          }
+          if (ok) tc_commit_pair_multicast(&tfull_bar[buf], 0x3);
+          k0 = k1;
         }
-        if (ok) tc_commit_pair_multicast(&tfull_bar[buf], 0x3);
       }
       tc_commit_pair(&drain_bar);
       drain(&drain_bar, 0);
@@ -440,23 +469,83 @@ __global__ void __launch_bounds__(kThreads, 1)
       const long long row = row_of(tm, q * 32 + lane);
       const int r0 = static_cast<int>(row_of(tm, q * 32)),
                 r1 = static_cast<int>(row_of(tm, q * 32 + 16));
-      const uint32_t buf = t & 1u;
       const bool there = row < args.n;
       const bool live = there && (args.mask == nullptr || args.mask[row] != 0);
-      // The first of dh comes while the tile's sums do, each next one a step ahead.
+      // The first of dh comes while the tile's (last) sum does, each next one a step ahead.
       uint32_t ahead[8];
       const T* dh = nullptr;
-      if constexpr (MODE == kAgain) {
+      auto bring_dh = [&] {
         const int f0 = tn * plan.cols;
         dh = static_cast<const T*>(args.dh) + row * args.lddh + f0;
         load16<T>(dh + half * 32, ahead,
                   live && half * 32 < plan.cols ? args.f - f0 - half * 32 : 0);
+      };
+      if constexpr (MODE == kAgain && !LONG) bring_dh();
+      if constexpr (LONG) {
+        // The sums before the tile's last are added up in registers, and then to that in
+        // TMEM. Chunk c of this warp's 32 columns: of dx, or of either projection.
+        float sum[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sum[c][j] = 0.f;
+        auto chunk = [&](int c) {
+          const int col = half * 32 + 64 * (MODE == kDx ? c : c & 1);
+          return MODE == kDx ? col : col + (c >> 1) * plan.cols;
+        };
+        int k = it.kb;
+        for (; ok && k + kSum < it.ke; k += kSum, ++t) {
+          const uint32_t buf = t & 1u;
+          if (!warp_wait(&tfull_bar[buf], (t >> 1) & 1u, abort_flag, &status_sh)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              float v[8];
+              tmem_ld8(t0 + buf * kTileN + chunk(c) + 8 * h, v);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) sum[c][8 * h + j] += v[j];
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(tempty0 + buf * 8u);
+        }
+        const uint32_t buf = t & 1u;
+        if (!ok || !warp_wait(&tfull_bar[buf], (t >> 1) & 1u, abort_flag, &status_sh)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (k != it.kb) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              if (half * 32 + 64 * (MODE == kDx ? c : c & 1) >= plan.cols) continue;
+              const uint32_t at = t0 + buf * kTileN + chunk(c) + 8 * h;
+              float v[8];
+              tmem_ld8(at, v);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) v[j] += sum[c][8 * h + j];
+              tmem_st8(at, v);
+            }
+          }
+          tmem_wait_st();
+        }
+        if constexpr (MODE == kAgain) bring_dh();
+      } else {
+        if (!warp_wait(&tfull_bar[t & 1u], (t >> 1) & 1u, abort_flag, &status_sh)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
       }
-      if (!warp_wait(&tfull_bar[buf], (t >> 1) & 1u, abort_flag, &status_sh)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
+      const uint32_t buf = t & 1u;
       const uint32_t acc = t0 + buf * kTileN;
       const int width = MODE == kDx ? args.d : args.f;
       // The two halves of the warps take turns with the tile's 32 columns each.
@@ -707,7 +796,7 @@ cudaError_t launch_dx_join(const GluArgs& args, const WgradPlan& plan, cudaStrea
                      : cudaLaunchKernelEx(&cfg, glu_dx_join_kernel<T, 1>, args, plan);
 }
 
-template <int MODE, typename T>
+template <int MODE, typename T, bool LONG>
 cudaError_t launch(const CUtensorMap (&a)[4], const CUtensorMap (&b)[2],
                    const CUtensorMap (&o)[3], const GluArgs& args,
                    const GluPlan& plan, int sms, cudaStream_t st) {
@@ -732,7 +821,7 @@ cudaError_t launch(const CUtensorMap (&a)[4], const CUtensorMap (&b)[2],
                       : MODE == kAgain ? "glu_gemm_kernel<again>"
                                        : "glu_gemm_kernel<dx>",
                       st);
-    e = cudaLaunchKernelEx(&cfg, glu_gemm_kernel<MODE, T>, a[0], a[1], a[2], a[3], b[0], b[1],
+    e = cudaLaunchKernelEx(&cfg, glu_gemm_kernel<MODE, T, LONG>, a[0], a[1], a[2], a[3], b[0], b[1],
                            o[0], o[1], o[2], args, plan);
   }
   if (MODE != kDx || e != cudaSuccess || plan.work.cut == 0) return e;
@@ -846,8 +935,12 @@ cudaError_t launch_mode(const GluArgs& args, int sms, cudaStream_t st) {
                             kSeg, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_64B))
       return cudaErrorInvalidValue;
   }
-  return args.fp16 ? launch<MODE, __half>(a, b, o, args, plan, sms, st)
-                   : launch<MODE, __nv_bfloat16>(a, b, o, args, plan, sms, st);
+  auto run = [&](auto type) {
+    using T = decltype(type);
+    return stages > kSumStages<T> ? launch<MODE, T, true>(a, b, o, args, plan, sms, st)
+                                  : launch<MODE, T, false>(a, b, o, args, plan, sms, st);
+  };
+  return args.fp16 ? run(__half()) : run(__nv_bfloat16());
 }
 
 // ---------------------------------------- from the projections as kept ----
@@ -907,17 +1000,21 @@ __global__ void __launch_bounds__(kRowThreads) glu_bwd_kept_kernel(const GluArgs
 
 }  // namespace
 
+template <int MODE, typename T>
+cudaError_t prepare() {
+  cudaError_t e = cudaSuccess;
+  for (const void* k : {reinterpret_cast<const void*>(glu_gemm_kernel<MODE, T, false>),
+                        reinterpret_cast<const void*>(glu_gemm_kernel<MODE, T, true>)})
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  return e;
+}
+
 cudaError_t prepare_glu_gemm() {
-  const void* all[] = {
-      reinterpret_cast<const void*>(glu_gemm_kernel<kFwd, __nv_bfloat16>),
-      reinterpret_cast<const void*>(glu_gemm_kernel<kFwd, __half>),
-      reinterpret_cast<const void*>(glu_gemm_kernel<kAgain, __nv_bfloat16>),
-      reinterpret_cast<const void*>(glu_gemm_kernel<kAgain, __half>),
-      reinterpret_cast<const void*>(glu_gemm_kernel<kDx, __nv_bfloat16>),
-      reinterpret_cast<const void*>(glu_gemm_kernel<kDx, __half>)};
-  for (const void* k : all) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  for (const auto f : {prepare<kFwd, __nv_bfloat16>, prepare<kFwd, __half>,
+                       prepare<kAgain, __nv_bfloat16>, prepare<kAgain, __half>,
+                       prepare<kDx, __nv_bfloat16>, prepare<kDx, __half>}) {
+    const cudaError_t e = f();
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -23,6 +23,7 @@ namespace grpo {
 namespace {
 
 constexpr int kBlockK = 64;  // of a warp's step: 128 bytes of a row
+constexpr int kSumSteps = 32;  // of one sum of the tensor core: 2048 products
 
 __device__ __forceinline__ uint4 stream16(const void* p) {
   uint4 v;
@@ -51,8 +52,9 @@ constexpr int kMostWarps = 16;
 constexpr int kCols = 8;                      // of f, a CTA
 constexpr int kSums = 2 * kCols * kGluSmallRows;  // of a warp
 
+// 40 registers: 12 CTAs of 4 warps an SM hold the 1792 of 4096 x 14336 at once.
 template <typename T>
-__global__ void __launch_bounds__(32 * kMostWarps) glu_small_kernel(const GluArgs a) {
+__global__ void __launch_bounds__(32 * kMostWarps, 3) glu_small_kernel(const GluArgs a) {
   __shared__ float part[kMostWarps][2][kCols][kGluSmallRows];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int r = lane >> 2, c = lane & 3;
@@ -61,27 +63,38 @@ __global__ void __launch_bounds__(32 * kMostWarps) glu_small_kernel(const GluArg
   const T* const wg = static_cast<const T*>(a.w_gate) + (f0 + r) * a.ldwg + c * 8;
   const T* const wu = static_cast<const T*>(a.w_up) + (f0 + r) * a.ldwu + c * 8;
   const T* const x = static_cast<const T*>(a.x) + r * a.ldx + c * 8;
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
   const uint4 zero = make_uint4(0, 0, 0, 0);
+  float2* const sums[2] = {reinterpret_cast<float2*>(&part[warp][0][r][2 * c]),
+                           reinterpret_cast<float2*>(&part[warp][1][r][2 * c])};
+  const int step = warps * kBlockK, most = kSumSteps * step;
+  // The tensor core's sums cut off instead of rounding, so they are kept short.
+  for (int k0 = warp * kBlockK, begin = k0; begin < a.d; begin += most) {
+    const int end = a.d - begin > most ? begin + most : a.d;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-  for (int k0 = warp * kBlockK; k0 < a.d; k0 += warps * kBlockK) {
-    uint4 g[2], u[2], b[2];
+    for (; k0 < end; k0 += step) {
+      uint4 g[2], u[2], b[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int k = k0 + 32 * h;
-      const bool in = k + c * 8 < a.d;
-      g[h] = in ? stream16(wg + k) : zero;
-      u[h] = in ? stream16(wu + k) : zero;
-      b[h] = in && r < n ? __ldg(reinterpret_cast<const uint4*>(x + k)) : zero;
+      for (int h = 0; h < 2; ++h) {
+        const int k = k0 + 32 * h;
+        const bool in = k + c * 8 < a.d;
+        g[h] = in ? stream16(wg + k) : zero;
+        u[h] = in ? stream16(wu + k) : zero;
+        b[h] = in && r < n ? __ldg(reinterpret_cast<const uint4*>(x + k)) : zero;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        mma16<T>(acc, g[h].x, u[h].x, g[h].y, u[h].y, b[h].x, b[h].y);
+        mma16<T>(acc, g[h].z, u[h].z, g[h].w, u[h].w, b[h].z, b[h].w);
+      }
     }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      mma16<T>(acc, g[h].x, u[h].x, g[h].y, u[h].y, b[h].x, b[h].y);
-      mma16<T>(acc, g[h].z, u[h].z, g[h].w, u[h].w, b[h].z, b[h].w);
+    for (int j = 0; j < 2; ++j) {
+      float2 v = make_float2(acc[2 * j], acc[2 * j + 1]);
+      if (begin != warp * kBlockK) v = make_float2(sums[j]->x + v.x, sums[j]->y + v.y);
+      *sums[j] = v;
     }
   }
-  *reinterpret_cast<float2*>(&part[warp][0][r][2 * c]) = make_float2(acc[0], acc[1]);
-  *reinterpret_cast<float2*>(&part[warp][1][r][2 * c]) = make_float2(acc[2], acc[3]);
   __syncthreads();
   // A thread finishes one value: neighbours take neighbouring columns of a row.
   for (int i = threadIdx.x; i < kCols * n; i += blockDim.x) {

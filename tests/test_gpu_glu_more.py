@@ -49,3 +49,122 @@ def test_a_tile_is_nan_as_a_whole_where_what_is_added_does_not_come(clp, box):
         assert torch.equal(parts.any(1).any(2), parts.all(1).all(2))
     for p, q in zip(clp.grpo_glu_wgrad(dg, du, x, add_gate=add, add_up=add, workspace=ws), want):
         assert torch.equal(p, q)
+
+
+def _even(g, *shape, t, scale):
+    """Values of one sign and size: what a sum cuts off adds up, and nothing cancels."""
+    return (scale * (0.5 + 0.5 * torch.rand(*shape, generator=g, device=DEV))).to(t)
+
+
+def _unbiased(got, want, t, length, terms=1):
+    """The mean relative error is that of roundings to nearest, whose size is at most half
+    a step, 2^-11 of a value (fp16) or 2^-8, of either sign: six sigma of their mean. Beside
+    it each fp32 sum of at most `length` products may be cut off by one unit of 2^-23 of
+    itself per 16 products and at four joins, and up to 512 of them are added with
+    roundings of 2^-24, half of the whole on average."""
+    off = ((got.double() - want) / want).mean().item()
+    half = torch.finfo(t).eps / 2
+    bound = 6 * half / 3 ** 0.5 / want.numel() ** 0.5 + terms * (
+        (length / 16 + 4) * 2.0 ** -23 + 512 / 2 * 2.0 ** -24)
+    assert abs(off) <= bound, f"{off:.2e} off, beyond {bound:.2e}"
+
+
+LONGEST = {HF: 2048, BF: 32768}  # products of one sum
+
+
+@pytest.mark.parametrize("t,n,d", [(HF, 300, 1 << 17), (HF, 300, 1 << 20), (HF, 3, 1 << 20),
+                                   (BF, 300, 1 << 20), (BF, 8, 1 << 20), (HF, 300, 5000)])
+def test_long_sums_of_the_forward_pass_are_not_cut_short(clp, t, n, d):
+    g = _gen(1)
+    f, s = 64, (14.0 / d) ** 0.5
+    x, wg, wu = _even(g, n, d, t=t, scale=s), _even(g, f, d, t=t, scale=s), _even(g, f, d, t=t, scale=s)
+    gate, up = x.double() @ wg.double().t(), x.double() @ wu.double().t()
+    r = clp.grpo_glu_fwd(x, wg, wu, act="relu", want_gates=True)
+    _unbiased(r.gate, gate, t, LONGEST[t])
+    _unbiased(r.up, up, t, LONGEST[t])
+    _unbiased(r.h, gate * up, t, LONGEST[t], 2)
+    if n <= 8:
+        return
+    dh = _even(g, n, f, t=t, scale=0.1)
+    b = clp.grpo_glu_bwd(dh, x, wg, wu, act="relu", want_h=True, want_dx=False)
+    _unbiased(b.dgate, dh.double() * up, t, LONGEST[t])
+    _unbiased(b.dup, dh.double() * gate, t, LONGEST[t])
+    _unbiased(b.h, gate * up, t, LONGEST[t], 2)
+
+
+@pytest.mark.parametrize("t,n,f", [(HF, 300, 1 << 17), (HF, 200, 14336), (BF, 64, 1 << 19),
+                                   (HF, 2000, 3000), (HF, 9, 1 << 20)])
+@pytest.mark.parametrize("cut", [True, False])
+def test_long_sums_of_dx_are_not_cut_short(clp, t, n, f, cut):
+    g = _gen(2)
+    d, s = 64, (7.0 / f) ** 0.5
+    wg, wu, dh = (_even(g, m, k, t=t, scale=s) for m, k in ((f, d), (f, d), (n, f)))
+    ones = torch.ones(n, f, device=DEV, dtype=t)
+    ws = None if cut else torch.empty(0, device=DEV)
+    r = clp.grpo_glu_bwd(dh, None, wg, wu, gate=ones, up=ones, act="relu", workspace=ws)
+    assert torch.equal(r.dgate, dh) and torch.equal(r.dup, dh)
+    want = dh.double() @ (wg.double() + wu.double())
+    _unbiased(r.dx, want, t, LONGEST[t])
+
+
+@pytest.mark.parametrize("t,d,f", [(HF, 2048, 328), (HF, 2056, 328), (HF, 4160, 200),
+                                   (HF, 6200, 1368), (BF, 32776, 136)])
+@pytest.mark.parametrize("n", [33, 300])
+def test_sums_about_the_longest(clp, t, d, f, n):
+    # Against fp64, tile widths and masks as they come; a tile's sum is one, two or more.
+    g = _gen(d)
+    x, wg, wu = (_randn(g, m, k, t=t, scale=c) for m, k, c in
+                 ((n, d, 1.0), (f, d, d ** -0.5), (f, d, d ** -0.5)))
+    dh = _randn(g, n, f, t=t)
+    m = (torch.rand(n, generator=g, device=DEV) < 0.7).to(torch.uint8)
+    m[0] = 1
+    live = m != 0
+    gate, up = x.double() @ wg.double().t(), x.double() @ wu.double().t()
+    half = torch.finfo(t).eps / 2
+    # One unit of 2^-23 of the partial sum per 16 products and at joins.
+    err = (d / 16 + 8) * 2.0 ** -23 * (x.double().abs() @ wg.double().abs().t())
+    plain = clp.grpo_glu_fwd(x, wg, wu, act="relu", want_gates=True, want_ckpt=True)
+    assert ((plain.gate.double() - gate).abs() <= err + half * (gate.abs() + err) + 2.0 ** -25).all()
+    x[~live], dh[~live] = float("nan"), float("nan")
+    r = clp.grpo_glu_fwd(x, wg, wu, act="relu", mask=m, want_gates=True)
+    for p, q in zip(r[:3], plain[:3]):
+        assert torch.equal(p[live], q[live]) and not p[~live].any()
+    b = clp.grpo_glu_bwd(dh, x, wg, wu, act="silu", mask=m, want_h=True)
+    both = torch.cat([b.dgate, b.dup], 1).double()
+    w2 = torch.cat([wg, wu]).double()
+    want = both @ w2
+    err = (2 * f / 16 + 8) * 2.0 ** -23 * (both.abs() @ w2.abs())
+    assert ((b.dx.double() - want).abs() <= err + half * (want.abs() + err) + 2.0 ** -25)[live].all()
+    s = torch.sigmoid(gate)
+    want = dh.double() * gate * s
+    # |silu'| <= 1.1; __expf and the quick division are off by 2 + 1.2 |g| and 2 units.
+    err = dh.double().abs() * (1.1 * (d / 16 + 8) * 2.0 ** -23 * 4 * d ** 0.5
+                               + 32 * 2.0 ** -23 * (1 + gate.abs()))
+    assert ((b.dup.double() - want).abs() <= err + half * (want.abs() + err) + 2.0 ** -25)[live].all()
+
+
+@pytest.mark.parametrize("call", ["fwd", "again", "dx"])
+@pytest.mark.parametrize("stage", [5, 40, 70])
+def test_a_lost_copy_of_a_long_sum(clp, call, stage):
+    # fp16, three sums a tile: the copy is lost in the first, the second or the last.
+    g = _gen(7)
+    n, d, f = (700, 72 * 64, 1024) if call != "dx" else (2600, 1024, 36 * 64)
+    x, wg, wu, dh = (_randn(g, a, b, t=HF, scale=c) for a, b, c in
+                     ((n, d, 1.0), (f, d, d ** -0.5), (f, d, d ** -0.5), (n, f, 1.0)))
+    none = torch.empty(0, device=DEV)
+
+    def run():
+        if call == "fwd":
+            return list(clp.grpo_glu_fwd(x, wg, wu, want_gates=True)[:3])
+        if call == "again":
+            return list(clp.grpo_glu_bwd(dh, x, wg, wu, want_dx=False)[:2])
+        return [clp.grpo_glu_bwd(dh, None, wg, wu, gate=dh, up=dh, workspace=none).dx]
+
+    want = run()
+    clp.grpo_selftest_lose_copy(stage)
+    got = run()
+    for p, q in zip(got, want):
+        fine = ~torch.isnan(p)
+        assert not fine.all() and torch.equal(p[fine], q[fine])
+    for p, q in zip(run(), want):
+        assert torch.equal(p, q)
