@@ -233,16 +233,19 @@ class AdamW:
     def _describe(self):
         for i in range(len(self.params)):
             self._fill(i)
-        # One value in two tensors would be stepped twice at once.
-        spans = sorted((p.data_ptr(), p.numel() * p.element_size(), i)
-                       for i, p in enumerate(self.params) if p.numel())
-        for (a, size, i), (b, _, j) in zip(spans, spans[1:]):
-            if a + size > b:
-                raise ValueError(f"params[{i}] and params[{j}] overlap")
-        self._shapes = list(map(_shape, self.params))
         # All that the step writes, as the table has it.
-        written = [self.params, *zip(*self.states), self.copies]
-        self._held = [t for part in written for t in part if t is not None]
+        m, v, m_scale, v_scale = zip(*self.states)
+        written = {"params": self.params, "states m": m, "states v": v,
+                   "states m_scale": m_scale, "states v_scale": v_scale, "copies": self.copies}
+        held = [(t, name, i) for name, part in written.items() for i, t in enumerate(part)
+                if t is not None]
+        # One value in two of them would be written twice at once.
+        spans = sorted((t.data_ptr(), t.nbytes, f"{name}[{i}]") for t, name, i in held if t.numel())
+        for (a, size, one), (b, _, other) in zip(spans, spans[1:]):
+            if a + size > b:
+                raise ValueError(f"{one} and {other} overlap")
+        self._shapes = list(map(_shape, self.params))
+        self._held = [t for t, _, _ in held]
         self._at = list(map(_data_ptr, self._held))
         self._rounded = [c for c in self.copies if c is not None]
         self._types = list(map(_dtype, self._rounded))

@@ -99,3 +99,26 @@ def test_a_copy_of_no_type_that_is_taken(adamw):
     with pytest.raises(TypeError, match=r"copies\[0\]"):
         opt.step(grads)
     assert len(adamw[1]) == 1
+
+
+def test_tensors_that_share_values_are_refused(adamw):
+    cls = adamw[0]
+    p, q = torch.randn(40), torch.randn(40)
+    s = [torch.zeros(40) for _ in range(4)]
+    both = torch.zeros(60, dtype=BF)
+    for kw, what in (
+            (dict(states=[(s[0], s[1]), (s[0], s[2])]), r"states m\[0\] and states m\[1\]"),
+            (dict(states=[(s[0], s[0]), (s[1], s[2])]), r"states m\[0\] and states v\[0\]"),
+            (dict(states=[(p, s[1]), (s[2], s[3])]), r"params\[0\] and states m\[0\]"),
+            (dict(copies=[both[:40], both[20:]]), r"copies\[0\] and copies\[1\]"),
+            (dict(copies=[both[:40], both[:40]]), r"copies\[0\] and copies\[1\]")):
+        with pytest.raises(ValueError, match=what + " overlap"):
+            cls([p, q], lr=1e-3, **kw)
+    scale = torch.zeros(2)
+    e = [torch.zeros(40, dtype=torch.uint8).view(E4M3) for _ in range(4)]
+    with pytest.raises(ValueError, match=r"states m_scale\[0\] and states m_scale\[1\] overlap"):
+        cls([p, q], lr=1e-3, states=[(e[0], e[1], scale[:1], scale[1:]),
+                                     (e[2], e[3], scale[:1], torch.zeros(1))])
+    # Neighbours in one buffer are not.
+    flat = torch.zeros(6, 40)
+    cls([flat[0], flat[1]], lr=1e-3, states=[(flat[2], flat[3]), (flat[4], flat[5])])
