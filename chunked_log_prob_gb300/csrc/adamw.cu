@@ -12,6 +12,7 @@
 // changes by a thousandth a step would stand still (e4m3's neighbours are a sixteenth
 // to an eighth apart); rounded at random it is right in the mean.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -934,7 +935,9 @@ int grpo_adamw_step(const grpo_adamw_tensor* tensors, int32_t count,
   a.beta2 = static_cast<float>(q.beta2);
   a.rest1 = static_cast<float>(1.0 - q.beta1);
   a.rest2 = static_cast<float>(1.0 - q.beta2);
-  a.eps = static_cast<float>(q.eps);
+  // An eps above 0 stays so, and normal (the step's quick inverse takes no subnormals); no
+  // root but 0 is that small.
+  a.eps = q.eps > 0.0 ? std::max(static_cast<float>(q.eps), FLT_MIN) : 0.f;
   // beta 0: its power is 0 (the logarithm a number that expm1 takes to -1).
   a.log1 = q.beta1 > 0.0 ? static_cast<float>(std::log(q.beta1)) : -200.f;
   a.log2 = q.beta2 > 0.0 ? static_cast<float>(std::log(q.beta2)) : -200.f;

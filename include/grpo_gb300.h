@@ -607,7 +607,7 @@ typedef struct grpo_adamw_tensor {
 } grpo_adamw_tensor;
 
 typedef struct grpo_adamw_params {
-  double beta1, beta2, eps; /* 0 <= beta < 1, eps >= 0                               */
+  double beta1, beta2, eps; /* 0 <= beta < 1, eps >= 0 (above 0: 2^-126 at least)    */
   int64_t step;             /* of this call, from 1 on                               */
   uint64_t seed;            /* of the random rounding                                */
   /* On the device, or NULL: */

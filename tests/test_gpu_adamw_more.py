@@ -199,3 +199,63 @@ def test_the_norm_of_zeros_and_of_what_is_not_finite(clp):
                 r = clp.grpo_grad_norm([x], max_norm=1.0)
                 assert torch.isnan(r.norm) if is_nan else r.norm.item() == float("inf")
                 assert torch.isnan(r.scale)
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("eps", [1e-300, 1e-45, 1e-40, 1e-38])
+def test_an_eps_above_zero_however_small(clp, bits, eps):
+    # Values without a gradient so far have no step: 0 / eps. The others' is lr.
+    p = torch.ones(300, device=DEV)
+    gr = torch.zeros(300, device=DEV)
+    gr[::3] = 0.5
+    opt = clp.AdamW([p], lr=0.25, eps=eps, weight_decay=0.0, state_bits=bits)
+    opt.step([gr])
+    assert (p[gr == 0] == 1).all()
+    assert ((p[::3] - 0.75).abs() <= 8 * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("gt", [F32, BF, HF])
+@pytest.mark.parametrize("off", [0, 1])
+def test_bf16_parameters_with_moments_in_32_bits(clp, gt, off):
+    # Moments against fp64 as for fp32 parameters; the parameter goes where its 16 random
+    # bits send the fp32 sum, which is within a few units of 2^-24 of the exact one.
+    sizes = [1, 7, 128, 129, 255, 257, 1000, 4096, 4097, 40_003]
+    g = torch.Generator().manual_seed(11)
+
+    def made(t, scale=1.0):
+        out = []
+        for n in sizes:
+            big = (scale * torch.randn(n + off, generator=g)).to(t).to(DEV)
+            out.append(big[off:])
+        return out
+
+    lr, decay, seed = 3e-3, 0.1, 77
+    params = made(BF)
+    states = [clp.AdamState(m, v.abs()) for m, v in zip(made(F32, 0.1), made(F32, 0.02))]
+    opt = clp.AdamW(params, lr=lr, weight_decay=decay, states=states, steps_done=3, seed=seed)
+    lr = float(np.float32(lr))
+    for t in (4, 5):
+        grads = made(gt, 0.1)
+        before = [(f64(p), f64(s.m), f64(s.v)) for p, s in zip(params, states)]
+        opt.step(grads)
+        at = 0
+        for (p0, m0, v0), p, gr, s in zip(before, params, grads, states):
+            q = f64(gr)
+            p1, m1, v1 = o.adamw(p0, q, m0, v0, t, lr, decay=decay)
+            # Two products and a sum each, beta's complements as fp32.
+            dm, dv = 4 * 2.0 ** -24 * (np.abs(m0) + np.abs(q)), 4 * 2.0 ** -24 * (v0 + q ** 2)
+            assert (np.abs(f64(s.m) - m1) <= dm).all()
+            assert (np.abs(f64(s.v) - v1) <= dv + 1e-45).all()
+            root = np.sqrt(v1 / (1 - 0.999 ** t)) + 1e-8
+            scale = lr / (1 - 0.9 ** t) / root
+            near = scale * dm + np.abs(scale * m1) * 16 * 2.0 ** -24 + 2.0 ** -23 * np.abs(p1)
+            _, _, u = o.random_bits(np.arange(at, at + p0.size), seed, t)
+            at += -(-p0.size // 128) * 128
+            step = 2.0 ** (np.floor(np.log2(np.abs(p1))) - 7)
+            raised = np.abs(p1) / step + u / 65536
+            want = np.sign(p1) * np.floor(raised) * step
+            clear = np.abs(raised - np.round(raised)) * step > near
+            # The power of two above p1 may be the sum's own.
+            clear &= np.abs(np.abs(p1) / step - 128) * step > near
+            assert (f64(p) == want)[clear].all() and clear.mean() > 0.99 - 3 / p0.size
+            assert (np.abs(f64(p) - p1) <= step + near).all()

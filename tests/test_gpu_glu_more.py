@@ -168,3 +168,27 @@ def test_a_lost_copy_of_a_long_sum(clp, call, stage):
         assert not fine.all() and torch.equal(p[fine], q[fine])
     for p, q in zip(run(), want):
         assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("n", [1, 8, 12, 400])
+def test_all_that_a_captured_forward_pass_writes(clp, n):
+    g = _gen(n)
+    d, f = 136, 520
+    x, wg, wu = _randn(g, n, d), _randn(g, f, d, scale=d ** -0.5), _randn(g, f, d, scale=d ** -0.5)
+    m = (torch.rand(n, generator=g, device=DEV) < 0.6).to(torch.uint8)
+    m[0] = 1
+    clp.grpo_glu_fwd(x, wg, wu, mask=m, want_gates=True, want_ckpt=True)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = clp.grpo_glu_fwd(x, wg, wu, mask=m, want_gates=True, want_ckpt=True)
+    for seed in (1, 2):
+        x.copy_(_randn(_gen(seed), n, d))
+        want = clp.grpo_glu_fwd(x, wg, wu, mask=m, want_gates=True, want_ckpt=True)
+        for z in (held.h, held.gate, held.up, held.ckpt.data):
+            z.fill_(1)
+        graph.replay()
+        for p, q in zip((held.h, held.gate, held.up), (want.h, want.gate, want.up)):
+            assert torch.equal(p, q)
+        assert torch.equal(held.ckpt.q.view(torch.uint8), want.ckpt.q.view(torch.uint8))
+        assert torch.equal(held.ckpt.exponents, want.ckpt.exponents)
