@@ -18,12 +18,15 @@
 #include "glu.h"
 #include "glu_act.cuh"
 #include "launch.h"
+#include "wgrad_plan.h"
 
 namespace grpo {
 namespace {
 
 constexpr int kBlockK = 64;  // of a warp's step: 128 bytes of a row
-constexpr int kSumSteps = 32;  // of one sum of the tensor core: 2048 products
+// Steps of one sum of the tensor core, which cuts off instead of rounding: 2048 products,
+// 1.5e-5 off at most. A warp adds longer ones up with rounding.
+constexpr int kSumSteps = 32;
 
 __device__ __forceinline__ uint4 stream16(const void* p) {
   uint4 v;
@@ -52,9 +55,9 @@ constexpr int kMostWarps = 16;
 constexpr int kCols = 8;                      // of f, a CTA
 constexpr int kSums = 2 * kCols * kGluSmallRows;  // of a warp
 
-// 40 registers: 12 CTAs of 4 warps an SM hold the 1792 of 4096 x 14336 at once.
-template <typename T>
-__global__ void __launch_bounds__(32 * kMostWarps, 3) glu_small_kernel(const GluArgs a) {
+// LONG: a warp's share of k is more than one sum (all sizes in that form: 1 to 3 % slower).
+template <typename T, bool LONG>
+__global__ void __launch_bounds__(32 * kMostWarps) glu_small_kernel(const GluArgs a) {
   __shared__ float part[kMostWarps][2][kCols][kGluSmallRows];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int r = lane >> 2, c = lane & 3;
@@ -63,38 +66,44 @@ __global__ void __launch_bounds__(32 * kMostWarps, 3) glu_small_kernel(const Glu
   const T* const wg = static_cast<const T*>(a.w_gate) + (f0 + r) * a.ldwg + c * 8;
   const T* const wu = static_cast<const T*>(a.w_up) + (f0 + r) * a.ldwu + c * 8;
   const T* const x = static_cast<const T*>(a.x) + r * a.ldx + c * 8;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  float2* const sums[2] = {reinterpret_cast<float2*>(&part[warp][0][r][2 * c]),
-                           reinterpret_cast<float2*>(&part[warp][1][r][2 * c])};
-  const int step = warps * kBlockK, most = kSumSteps * step;
-  // The tensor core's sums cut off instead of rounding, so they are kept short.
-  for (int k0 = warp * kBlockK, begin = k0; begin < a.d; begin += most) {
-    const int end = a.d - begin > most ? begin + most : a.d;
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  auto add_step = [&](int k0) {
+    uint4 g[2], u[2], b[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = k0 + 32 * h;
+      const bool in = k + c * 8 < a.d;
+      g[h] = in ? stream16(wg + k) : zero;
+      u[h] = in ? stream16(wu + k) : zero;
+      b[h] = in && r < n ? __ldg(reinterpret_cast<const uint4*>(x + k)) : zero;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      mma16<T>(acc, g[h].x, u[h].x, g[h].y, u[h].y, b[h].x, b[h].y);
+      mma16<T>(acc, g[h].z, u[h].z, g[h].w, u[h].w, b[h].z, b[h].w);
+    }
+  };
+  if constexpr (LONG) {
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    int k0 = warp * kBlockK;
+    while (k0 < a.d) {
+      const int end = least(a.d, k0 + kSumSteps * warps * kBlockK);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[j] = 0.f;
 #pragma unroll 4
-    for (; k0 < end; k0 += step) {
-      uint4 g[2], u[2], b[2];
+      for (; k0 < end; k0 += warps * kBlockK) add_step(k0);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int k = k0 + 32 * h;
-        const bool in = k + c * 8 < a.d;
-        g[h] = in ? stream16(wg + k) : zero;
-        u[h] = in ? stream16(wu + k) : zero;
-        b[h] = in && r < n ? __ldg(reinterpret_cast<const uint4*>(x + k)) : zero;
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        mma16<T>(acc, g[h].x, u[h].x, g[h].y, u[h].y, b[h].x, b[h].y);
-        mma16<T>(acc, g[h].z, u[h].z, g[h].w, u[h].w, b[h].z, b[h].w);
-      }
+      for (int j = 0; j < 4; ++j) sum[j] += acc[j];
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      float2 v = make_float2(acc[2 * j], acc[2 * j + 1]);
-      if (begin != warp * kBlockK) v = make_float2(sums[j]->x + v.x, sums[j]->y + v.y);
-      *sums[j] = v;
-    }
+    for (int j = 0; j < 4; ++j) acc[j] = sum[j];
+  } else {
+#pragma unroll 4
+    for (int k0 = warp * kBlockK; k0 < a.d; k0 += warps * kBlockK) add_step(k0);
   }
+  *reinterpret_cast<float2*>(&part[warp][0][r][2 * c]) = make_float2(acc[0], acc[1]);
+  *reinterpret_cast<float2*>(&part[warp][1][r][2 * c]) = make_float2(acc[2], acc[3]);
   __syncthreads();
   // A thread finishes one value: neighbours take neighbouring columns of a row.
   for (int i = threadIdx.x; i < kCols * n; i += blockDim.x) {
@@ -129,7 +138,10 @@ cudaError_t launch(const GluArgs& a, int sms, cudaStream_t st) {
   const int most = groups >= 6 * sms ? 4 : groups >= 3 * sms ? 8 : kMostWarps;
   const int warps = std::max(1, std::min(most, steps));
   LaunchTimer timer("glu_small_kernel", st);
-  glu_small_kernel<T><<<groups, 32 * warps, 0, st>>>(a);
+  if (a.d > warps * kSumSteps * kBlockK)
+    glu_small_kernel<T, true><<<groups, 32 * warps, 0, st>>>(a);
+  else
+    glu_small_kernel<T, false><<<groups, 32 * warps, 0, st>>>(a);
   return cudaGetLastError();
 }
 
