@@ -625,11 +625,11 @@ typedef struct grpo_adamw_params {
  * between two neighbours lo < hi goes to hi with the probability that makes the mean
  * right (of v, where its root is kept; but a v above 0 never becomes 0). The random
  * numbers are a hash of seed, step and the value's place, where the tensors are counted
- * through in their order, each from the next multiple of 128 on; so results repeat bit
- * for bit. bf16 parameters: u < 2^16 is added below the kept bits, which are then cut
- * off. Moments in 8 bits: of each 128 consecutive values the scale is the largest / 448.
- * Moments of a block whose largest is below 2^-118 are kept as 0; a value that is not
- * finite is kept as NaN.
+ * through in their order, each from the next multiple of 128 on (each 2^32 places with
+ * keys of their own); so results repeat bit for bit. bf16 parameters: u < 2^16 is added
+ * below the kept bits, which are then cut off. Moments in 8 bits: of each 128 consecutive
+ * values the scale is the largest / 448. Moments of a block whose largest is below 2^-118
+ * are kept as 0; a value that is not finite is kept as NaN.
  * tensors: on the host, read during the call; of a tensor, param, m, v and the
  * rest overlap nothing. A captured call repeats its step and its lr unless
  * step_on_device and lr_factor give others. */
