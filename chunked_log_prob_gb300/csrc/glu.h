@@ -13,7 +13,9 @@ namespace grpo {
 // Row tiles that the block's GEMMs walk together. 16384 x 4096 x 14336, forward / backward
 // again / weight gradients (us, under the power cap, two boxes): 4 2348 / 4829 / 2377, 8
 // 2231 / 4667 / 2335, 16 2174 / 4636 / 2325; 16 2118 / 4513 / 2270, 20 2110 / 4579 / 2346,
-// 32 2227 / 4751 / 2424.
+// 32 2227 / 4751 / 2424. At 8192 x 1536 x 8960, 8 241 / 549 / 282, 16 234 / 545 / 281, 20
+// 234 / 547 / 284; 4096 x 4096 x 14336, 8 536 / 1175 / 610, 16 534 / 1141 / 618, 20 528 /
+// 1140 / 620; 2048 x 2880 x 2880 all within the 5 % that runs of one differ by.
 constexpr int kGluGroup = 16;
 
 // One call's tensors, [n][d] and [n][f] with row strides in elements; the weights
