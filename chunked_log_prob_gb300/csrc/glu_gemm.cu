@@ -55,11 +55,13 @@ constexpr int kSmem = 1024 + 2 * kStages * kOperand + kEpilogueWarps * kOutBoxes
 static_assert(kSmem <= 227 * 1024 - 1024, "shared memory of a CTA");
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSlotFloats = kTileM * kTileN;  // of a piece of a cut tile
-// Stages of one sum in TMEM: 32768 products of bf16, 2048 of fp16, whose sums are 2.4e-4
-// and 1.5e-5 off at most: an eighth and a sixteenth of the least half step of the type's
-// numbers, 2^-9 and 2^-12.
-template <typename T>
-constexpr int kSumStages = std::is_same_v<T, __half> ? 32 : 512;
+// Stages of one sum in TMEM: 1024 products. Values of random sign, of which a wrong sum now
+// and then sends one to the other 16-bit neighbour: h at 16384 x 4096 x 14336 is not the
+// nearest to its value in 64 bits in 1.2e-3 of them (6.7e-4 where fp32 sums round), dx at
+// 8192 x 1536 x 8960 in 1.2e-3 (1.5e-3); with whole sums in TMEM 4.2e-3 and 7.8e-3. Stages
+// of one sum, forward / backward again there and forward padded (us, one box): all 2185 /
+// 4671 / 234, 32 2204 / 4706 / 234, 16 2214 / 4808 / 240, 8 2248 / 4895 / 252.
+constexpr int kSumStages = 16;
 
 // The launch's tiles: 256 rows x `cols` columns of f (of d for dx), dealt to the pairs
 // by `work`; its kt counts the stages of a tile, for dx those of both operand pairs.
@@ -311,7 +313,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");  // dgate and dup are there
   if constexpr (MODE != kFwd) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem_base = tmem_base_sh;
-  constexpr int kSum = kSumStages<T>;
   WgradWork work;
   WgradItem it;
   // Row of this CTA's row i of a row tile; args.n where there is none.
@@ -395,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                        MODE == kDx) &
             ~type_bits;
         for (int k0 = it.kb; ok && k0 < it.ke; ++t) {
-          const int k1 = LONG ? least(k0 + kSum, it.ke) : it.ke;
+          const int k1 = LONG ? least(k0 + kSumStages, it.ke) : it.ke;
           const uint32_t buf = t & 1u;
           if (!mbar_wait(&tempty_bar[buf], ((t >> 1) & 1u) ^ 1u, abort_flag, &status_sh)) {
             ok = false;
@@ -494,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return MODE == kDx ? col : col + (c >> 1) * plan.cols;
         };
         int k = it.kb;
-        for (; ok && k + kSum < it.ke; k += kSum, ++t) {
+        for (; ok && k + kSumStages < it.ke; k += kSumStages, ++t) {
           const uint32_t buf = t & 1u;
           if (!warp_wait(&tfull_bar[buf], (t >> 1) & 1u, abort_flag, &status_sh)) {
             ok = false;
@@ -937,7 +938,7 @@ cudaError_t launch_mode(const GluArgs& args, int sms, cudaStream_t st) {
   }
   auto run = [&](auto type) {
     using T = decltype(type);
-    return stages > kSumStages<T> ? launch<MODE, T, true>(a, b, o, args, plan, sms, st)
+    return stages > kSumStages ? launch<MODE, T, true>(a, b, o, args, plan, sms, st)
                                   : launch<MODE, T, false>(a, b, o, args, plan, sms, st);
   };
   return args.fp16 ? run(__half()) : run(__nv_bfloat16());

@@ -499,7 +499,7 @@ int grpo_ckpt_wgrad(const void* dy, const void* ckpt, const float* add_or_null, 
  * [inner]; Wg, Wu: [inner][hidden] (halves of one matrix, or two). All are bf16 or
  * all fp16, start on 16 bytes, and have row strides of their own, in elements;
  * hidden, inner and the strides are multiples of 8. Sums are fp32 (the tensor core's own
- * cut off: 32768 products of bf16 or 2048 of fp16 at most are summed there, the weight
+ * cut off: 1024 products at most are summed there, 2048 for up to eight rows, the weight
  * gradients' 512 or 256, and such sums added with rounding); g, u and what is made of
  * them are rounded where they are stored and nowhere before. `mask` (uint8
  * [n_tokens] or NULL): a row with mask 0 has no influence, whatever it holds, and
