@@ -861,9 +861,11 @@ int tile_columns(int n_m, int width, int most, int pairs) {
 // over its tokens. Pieces of different tiles share no operands while they run, and a stage
 // of them takes some 1.6 times as long, so tiles are cut only where that and the join (25
 // stages) still save 24 of them, which the host's part of the join costs, and up to
-// four whole rounds before them (16384 x 4096 x 14336, 13 rounds: 2453 and 2520 us). Uncut and cut, with the pass before it: 64 rows x 4096 x 14336 126
-// and 55 us, 512 rows 135 and 117, 3 x 48 x 12800 100 and 11; not cut by this rule: 5888
-// x 1536 x 8960 255 and 312, 2048 rows 121 and 120, 1024 x 2880 x 2880 41 and 43.
+// four whole rounds before them (16384 x 4096 x 14336, 13 rounds: 2453 and 2520 us).
+// Uncut and cut, with the pass before it: 64 rows x 4096 x 14336 132 and 59 us, 512 rows
+// 141 and 121, 35 x 496 x 6976 62 and 18, 3 x 48 x 12800 105 and 15; not cut by this rule
+// (with whole sums in TMEM): 5888 x 1536 x 8960 255 and 312, 2048 rows 121 and 120, 1024 x
+// 2880 x 2880 41 and 43.
 WgradPlan dx_plan(long long n, int f, int d, int pairs) {
   const long long stages = 2LL * ((f + kBK - 1) / kBK);
   WgradPlan p = make_plan(stages * kTok, static_cast<int>(n), d, pairs);

@@ -542,7 +542,7 @@ int grpo_glu_fwd(const void* x, const void* w_gate, const void* w_up, const uint
  * projections are lost then); other overlaps are not allowed.
  *   workspace_or_null: grpo_glu_bwd_workspace_size bytes (0 for most sizes; 256-byte
  *     aligned). With it, a dx of few rows or columns, whose long sum would keep few SMs
- *     busy, is cut into pieces (4096 x 14336, 64 rows: 55 us against 126). */
+ *     busy, is cut into pieces (4096 x 14336, 64 rows: 59 us against 132). */
 int grpo_glu_bwd_workspace_size(int64_t n_tokens, int32_t inner, int32_t hidden, size_t* bytes);
 int grpo_glu_bwd(const void* dh, const void* x_or_null, const void* w_gate, const void* w_up,
                  const void* gate_or_null, const void* up_or_null, const uint8_t* mask_or_null,
