@@ -23,6 +23,8 @@ _GRAD = np.dtype(GrpoGrad)
 _byref = ctypes.byref
 _data_ptr, _numel = torch.Tensor.data_ptr, torch.Tensor.numel
 _packed, _device_index = torch.Tensor.is_contiguous, torch.Tensor.get_device
+# (tensors, addresses, indices): whether those tensors lie there; a third faster than a map.
+_lie_at = torch._C._tensors_data_ptrs_at_indices_equal
 _dtype, _shape, _nbytes = attrgetter("dtype"), attrgetter("shape"), attrgetter("nbytes")
 
 
@@ -246,7 +248,7 @@ class AdamW:
                 raise ValueError(f"{one} and {other} overlap")
         self._shapes = list(map(_shape, self.params))
         self._held = [t for t, _, _ in held]
-        self._at = list(map(_data_ptr, self._held))
+        self._at = list(map(_data_ptr, self._held)), list(range(len(self._held)))
         self._rounded = [c for c in self.copies if c is not None]
         self._types = list(map(_dtype, self._rounded))
         self._model = [*self.params, *self._rounded]
@@ -256,7 +258,7 @@ class AdamW:
         """Whether a tensor's storage was exchanged (`.data`), or fewer values of it taken,
         since it was described. At one address and of one size may be copies of either type;
         of the moments, which are the optimizer's, the address is enough."""
-        return (list(map(_data_ptr, self._held)) != self._at
+        return (not _lie_at(self._held, *self._at)
                 or list(map(_nbytes, self._model)) != self._sizes
                 or list(map(_dtype, self._rounded)) != self._types)
 
