@@ -194,8 +194,9 @@ class AdamW:
 
     Parameters, moments and copies are written in place on the current stream, which
     autograd does not see. The ``.data`` of each may be exchanged between steps, for values
-    of the same shape and type. To go on later, keep ``states``, ``steps_done``, ``seed`` and
-    the parameters, and make an AdamW of them.
+    of the same shape and type (a captured step keeps the addresses that it had). To go on
+    later, keep ``states``, ``steps_done``, ``seed`` and the parameters, and make an AdamW
+    of them.
     """
 
     def __init__(self, params: Sequence[torch.Tensor], *, lr, betas=(0.9, 0.999), eps=1e-8,
@@ -233,6 +234,7 @@ class AdamW:
         self._describe()
 
     def _describe(self):
+        self._described = False  # until all of it is: what is refused is looked at again
         for i in range(len(self.params)):
             self._fill(i)
         # All that the step writes, as the table has it.
@@ -253,12 +255,13 @@ class AdamW:
         self._types = list(map(_dtype, self._rounded))
         self._model = [*self.params, *self._rounded]
         self._sizes = list(map(_nbytes, self._model))
+        self._described = True
 
     def _moved(self):
         """Whether a tensor's storage was exchanged (`.data`), or fewer values of it taken,
         since it was described. At one address and of one size may be copies of either type;
         of the moments, which are the optimizer's, the address is enough."""
-        return (not _lie_at(self._held, *self._at)
+        return (not self._described or not _lie_at(self._held, *self._at)
                 or list(map(_nbytes, self._model)) != self._sizes
                 or list(map(_dtype, self._rounded)) != self._types)
 

@@ -92,6 +92,20 @@ def test_fewer_values_in_the_same_place_are_refused(adamw):
     assert opt.steps_done == 3 and len(adamw[1]) == 3
 
 
+def test_what_was_read_before_a_refusal_is_read_again(adamw):
+    # One tensor lies elsewhere, a later one is refused; then both are back as they were.
+    opt, params, copies, grads = _made(adamw[0])
+    opt.step(grads)
+    there, copy = params[0].data, copies[2].data
+    params[0].data, copies[2].data = there.clone(), copy.double()
+    with pytest.raises(TypeError, match=r"copies\[2\]"):
+        opt.step(grads)
+    params[0].data, copies[2].data = there, copy
+    opt.step(grads)
+    for i in range(3):
+        _as_described(opt, adamw[1][-1][i], i)
+
+
 def test_a_copy_of_no_type_that_is_taken(adamw):
     opt, _, copies, grads = _made(adamw[0])
     opt.step(grads)
